@@ -422,6 +422,160 @@ int w12_verify_greedy_noalloc(const void *logits_dev, int dtype, int64_t R, int6
                               const int32_t *draft_dev, int32_t *accept_len_dev,
                               int32_t *next_tok_dev, void *stream);
 
+/* --------------------------------------------------------------------- */
+/* Decode step: paged key/value cache                                    */
+/* --------------------------------------------------------------------- */
+
+/*
+ * The calls from here on are the parts of a decode step between
+ * the projections (w12_gemm_batched) and the committed token: rotary
+ * positions and the cache write, attention over the cache, sampling.  The
+ * SpecPilot pages describe no layout or rule for them; they are this
+ * library's own.  They use programmatic dependent launch as the GEMM calls
+ * do: nothing in global memory is read or written before the kernel launched
+ * just before on the same stream has completed.
+ */
+
+/* Element types of a cache. */
+#define W12_KV_BF16 0
+#define W12_KV_E4M3 1 /* 8-bit codes, one fp32 scale per token and head: value = code * scale */
+
+/*
+ * A paged cache: pages of `page` tokens (16, 32, 64 or 128).
+ *   k, v: [n_pages][heads][page][head_dim] bf16 or e4m3, 16-byte aligned;
+ *   k_scale, v_scale: [n_pages][heads][page] fp32, 16-byte aligned
+ *     (W12_KV_E4M3), else NULL.
+ * head_dim is 64 or 128; n_pages * heads * page < 2^31.  Memory is the
+ * caller's; rows that were never written are never looked at.
+ */
+typedef struct w12_kv {
+    void *k, *v;
+    float *k_scale, *v_scale;
+    int64_t n_pages;
+    int32_t heads, head_dim, page, dtype;
+} w12_kv;
+
+/*
+ * Requests.  A call serves R requests of T new tokens each (T = 1: plain
+ * decoding; a draft block; a piece of a prompt), tokens ordered [R][T].
+ *   kv_len_dev: [R] int32, each request's length WITH its T new tokens:
+ *     token i of request r has position kv_len[r] - T + i.  A negative
+ *     position is a padding token (a request with fewer than T tokens).
+ *   block_table_dev: [R][blocks] int32: position p of request r lives in row
+ *     p % page of page block_table[r][p / page].
+ * Lengths and tables stay on the device; a bad entry (a page outside
+ * [0, n_pages), a position past the table) is not followed and records
+ * W12_ERR_DEVICE.
+ */
+
+/* Channel pairs of a rotated head with `rot` rotated channels. */
+#define W12_ROPE_HALF 0        /* pair j: channels j and j + rot / 2 */
+#define W12_ROPE_INTERLEAVED 1 /* pair j: channels 2 j and 2 j + 1   */
+
+/* Scaling of the rotary frequencies f_j = base^(-2 j / rot) for contexts
+ * beyond the `original` trained length. */
+#define W12_ROPE_SCALE_NONE 0
+#define W12_ROPE_SCALE_LINEAR 1 /* f_j / factor                                                  */
+#define W12_ROPE_SCALE_BASE 2   /* base * factor^(rot / (rot - 2)) in place of base              */
+#define W12_ROPE_SCALE_BANDS 3  /* f_j (g + (1 - g) / factor), g = (turns_j - low) / (high - low)
+                                   in [0, 1], turns_j = original f_j / (2 pi)                    */
+#define W12_ROPE_SCALE_YARN 4   /* as BANDS with g linear in j between the (rounded outwards)
+                                   channels that make `high` and `low` turns, and cos and sin
+                                   times `attention` (0: 0.1 ln(factor) + 1)                     */
+typedef struct w12_rope_scaling {
+    int32_t mode, reserved;
+    double factor;    /* > 0 */
+    double original;  /* > 0; BANDS, YARN */
+    double low, high; /* 0 < low < high; BANDS, YARN */
+    double attention; /* >= 0; YARN */
+} w12_rope_scaling;
+
+/*
+ * Rotary table on the host: table[p][0 .. rot/2) = cos(p f_j),
+ * table[p][rot/2 .. rot) = sin(p f_j) for p < positions, computed in double
+ * precision and rounded once.  rot: a multiple of 8; base > 1; scaling may
+ * be NULL (none).  Errors: W12_ERR_ARG, W12_ERR_SHAPE.  Multithreaded.
+ */
+int w12_rope_table(int64_t positions, int rot, double base, const w12_rope_scaling *scaling, float *table_host);
+
+/*
+ * Rotate the queries and keys of R * T new tokens and write keys and values
+ * into the cache (rounded to bf16, or quantised), in one launch.
+ *   q_dev, k_dev, v_dev: x_dtype W12_F32 or W12_BF16; token n's heads start at
+ *     q_dev + n * q_stride (elements; heads and channels contiguous), so the
+ *     three may be parts of one projection output.  16-byte (F32) or 8-byte
+ *     (BF16) aligned, strides multiples of 4.
+ *   rope_dev: fp32 [rope_positions][rot] (w12_rope_table), 16-byte aligned;
+ *     NULL with rot = 0: no rotation.  rot is a multiple of 8, at most
+ *     head_dim; the channels from rot on are left as they are.
+ *   q_out_dev: bf16, token stride q_out_stride (a multiple of 4), 8-byte
+ *     aligned.  Padding tokens write nothing, here and in the cache.
+ * W12_KV_E4M3: a row's scale is amax / 448 and its codes are
+ * round(x * (448 / amax)) (nearest even); a row whose amax is at most 1e-30
+ * is stored as zeros; one that holds a NaN or an infinity reads back as NaN.
+ * Errors: W12_ERR_ARG, W12_ERR_SHAPE, W12_ERR_ALIGN, W12_ERR_CUDA.  Device
+ * errors (also a position past rope_positions) go to *err_dev if it is not
+ * NULL; such a token writes nothing.
+ */
+int w12_kv_append(const w12_kv *kv, const void *q_dev, int64_t q_stride, const void *k_dev, int64_t k_stride,
+                  const void *v_dev, int64_t v_stride, int x_dtype, int64_t R, int64_t T, int q_heads,
+                  const int32_t *block_table_dev, int64_t blocks, const int32_t *kv_len_dev, const float *rope_dev,
+                  int64_t rope_positions, int rot, int layout, uint16_t *q_out_dev, int64_t q_out_stride,
+                  int *err_dev, void *stream);
+
+/*
+ * Read the cache back: rows 0 .. cu_len[r+1] - cu_len[r] - 1 of every
+ * request, packed, as bf16 (codes times scale, rounded once).
+ *   cu_len_dev: [R + 1] int32, cu_len[0] = 0, not decreasing, cu_len[R] = tokens.
+ *   k_out_dev, v_out_dev: [tokens][heads][head_dim] bf16, 16-byte aligned.
+ * A row whose table entry is bad reads as zeros and records W12_ERR_DEVICE
+ * in *err_dev (may be NULL).
+ * Errors: W12_ERR_ARG, W12_ERR_SHAPE, W12_ERR_ALIGN, W12_ERR_CUDA.
+ */
+int w12_kv_read(const w12_kv *kv, const int32_t *block_table_dev, int64_t blocks, const int32_t *cu_len_dev,
+                int64_t R, int64_t tokens, uint16_t *k_out_dev, uint16_t *v_out_dev, int *err_dev, void *stream);
+
+/* Most requests of one w12_attend call. */
+#define W12_ATTEND_MAX_R 512
+
+/* Bytes of workspace w12_attend needs (0 on invalid arguments; max_len and
+ * prefix_len as in the call). */
+size_t w12_attend_workspace_size(const w12_kv *kv, int64_t R, int64_t T, int q_heads, int64_t max_len,
+                                 int64_t prefix_len);
+
+/*
+ * Causal attention of R * T new tokens over the cache (their own keys and
+ * values are in it: w12_kv_append), grouped query heads:
+ *   out[n, h] = sum_j softmax_j(scale q[n, h] . k[j, h / G]) v[j, h / G],
+ *   G = q_heads / kv->heads, over the keys j <= position of token n.
+ *   q_dev: bf16, token n's heads at q_dev + n * q_stride; 16-byte aligned,
+ *     q_stride a multiple of 8.
+ *   out_dev: bf16, token stride out_stride (a multiple of 4), 8-byte aligned.
+ *   lse_dev: NULL, or fp32 [R * T][q_heads]: log(sum_j exp(scale q . k_j)).
+ *   max_len: no kv_len is above it (a longer one records W12_ERR_DEVICE and
+ *     is cut there); it only bounds the work.
+ *   prefix_len: 0, or the number of leading keys that ALL requests share:
+ *     they are read once for the whole batch, through request 0's table (so
+ *     its row must name the prefix's pages); keys from prefix_len on are each
+ *     request's own, through its own row.  Not tied to page boundaries.
+ * A token that sees no key (a padding token, kv_len = 0) gives zeros and
+ * lse = -infinity.  Keys past a token's position, rows past kv_len and pages
+ * not named by the table never reach a result, whatever they hold.  Scores,
+ * the running maximum and sums are fp32; the weights of the second product
+ * are rounded to bf16 (bf16 cache) or fp16 (e4m3 cache).  The order of every
+ * sum is fixed by the arguments, the lengths and the GPU's SM count, so
+ * repeated calls give identical bits.  head_dim 64 or 128; 1 <= R <=
+ * W12_ATTEND_MAX_R; q_heads a multiple of kv->heads.
+ * Errors: W12_ERR_ARG, W12_ERR_SHAPE, W12_ERR_ALIGN, W12_ERR_WORKSPACE,
+ * W12_ERR_CUDA.  Device errors in word 0 of ws: W12_ERR_DEVICE (a length
+ * above max_len or the table, a page outside the cache, which reads as page
+ * 0), W12_ERR_TIMEOUT.
+ */
+int w12_attend(const w12_kv *kv, const uint16_t *q_dev, int64_t q_stride, int64_t R, int64_t T, int q_heads,
+               const int32_t *block_table_dev, int64_t blocks, const int32_t *kv_len_dev, int64_t max_len,
+               int64_t prefix_len, float scale, uint16_t *out_dev, int64_t out_stride, float *lse_dev, void *ws_dev,
+               size_t ws_bytes, void *stream);
+
 /*
  * Read (and clear) the sticky device error word of a workspace: waits for
  * `stream`, copies word 0 to *err_host, then zeroes it.  Returns W12_OK or

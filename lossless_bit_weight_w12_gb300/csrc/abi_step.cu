@@ -1,0 +1,195 @@
+// abi_step.cu -- the extern "C" entry points of the decode-step calls
+// (include/w12.h: paged cache, attention, sampling): argument checks and
+// dispatch.  Host code only.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "step_internal.h"
+
+namespace w12 {
+
+namespace {
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+constexpr int kMaxDevices = 256;
+std::atomic<int> g_sms[kMaxDevices];
+
+// SM count of the current device, asked once per device.
+int current_sms(int *sms) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return W12_ERR_CUDA;
+    int v = g_sms[dev].load(std::memory_order_relaxed);
+    if (v == 0) {
+        if (device_sm_count(&v) != W12_OK) return W12_ERR_CUDA;
+        g_sms[dev].store(v, std::memory_order_relaxed);
+    }
+    *sms = v;
+    return W12_OK;
+}
+
+int log2_of(int v) {
+    int l = 0;
+    while ((1 << l) < v) ++l;
+    return l;
+}
+
+int check_kv(const w12_kv *kv) {
+    if (!kv || (kv->dtype != W12_KV_BF16 && kv->dtype != W12_KV_E4M3)) return W12_ERR_ARG;
+    if (kv->heads < 1 || kv->n_pages < 1 || (kv->head_dim != 64 && kv->head_dim != 128)) return W12_ERR_SHAPE;
+    if (kv->page != 16 && kv->page != 32 && kv->page != 64 && kv->page != 128) return W12_ERR_SHAPE;
+    if (kv->n_pages >= ((int64_t(1) << 31) / kv->page + kv->heads - 1) / kv->heads) return W12_ERR_SHAPE;
+    const bool q8 = kv->dtype == W12_KV_E4M3;
+    if (!kv->k || !kv->v || (q8 && (!kv->k_scale || !kv->v_scale))) return W12_ERR_ARG;
+    if (!aligned(kv->k, 16) || !aligned(kv->v, 16) || (q8 && (!aligned(kv->k_scale, 16) || !aligned(kv->v_scale, 16))))
+        return W12_ERR_ALIGN;
+    return W12_OK;
+}
+
+constexpr int64_t kLim31 = int64_t(1) << 31;
+
+struct AttendPlan {
+    int32_t rows, rt, pu, su;
+    int grid;
+    size_t off_plan, off_ml, off_o, total;
+};
+
+// Work split and workspace layout of an attention call.
+int plan_attend(const w12_kv *kv, int64_t R, int64_t T, int q_heads, int64_t max_len, int64_t prefix, AttendPlan *p) {
+    const int st = check_kv(kv);
+    if (st != W12_OK) return st;
+    if (R < 1 || R > W12_ATTEND_MAX_R || T < 1 || T >= kLim31 || q_heads < 1 || q_heads > (1 << 20) ||
+        q_heads % kv->heads != 0)
+        return W12_ERR_SHAPE;
+    if (max_len < 0 || max_len >= kLim31 || prefix < 0 || prefix >= kLim31) return W12_ERR_SHAPE;
+    const int64_t tg = T * (q_heads / kv->heads), rows = R * tg;
+    if (rows >= kLim31 / 2) return W12_ERR_SHAPE;
+    const int64_t most = prefix > 0 ? rows : tg;
+    p->rows = int32_t(rows);
+    p->rt = most <= 16 ? 16 : 32;
+    p->pu = prefix > 0 ? int32_t((rows + p->rt - 1) / p->rt) : 0;
+    p->su = int32_t((tg + p->rt - 1) / p->rt);
+    const int64_t own = max_len / kAttTile + 1, shared = (std::min(prefix, max_len) + kAttTile - 1) / kAttTile;
+    if (own > kLim31 / (R * p->su) || shared > kLim31 / std::max(p->pu, 1)) return W12_ERR_SHAPE;
+    if (own * R * p->su + shared * p->pu >= kLim31 / kv->heads) return W12_ERR_SHAPE;
+    const int64_t tiles = (own * R * p->su + shared * p->pu) * kv->heads;
+    int sms = 0;
+    if (current_sms(&sms) != W12_OK) return W12_ERR_CUDA;
+    p->grid = int(std::min<int64_t>(sms, tiles));
+    const int64_t slots = int64_t(kv->heads) * (p->pu + R * p->su) + p->grid;
+    size_t off = kWsHeader;
+    p->off_plan = off;
+    off += round256(uint64_t(R + 2) * 4u);
+    p->off_ml = off;
+    off += round256(uint64_t(slots) * p->rt * 8u);
+    p->off_o = off;
+    off += round256(uint64_t(slots) * p->rt * uint64_t(kv->head_dim) * 4u);
+    p->total = off;
+    return W12_OK;
+}
+
+}  // namespace
+
+}  // namespace w12
+
+using namespace w12;
+
+extern "C" int w12_kv_append(const w12_kv *kv, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                             const void *v, int64_t v_stride, int x_dtype, int64_t R, int64_t T, int q_heads,
+                             const int32_t *table, int64_t blocks, const int32_t *kv_len, const float *rope,
+                             int64_t rope_positions, int rot, int layout, uint16_t *q_out, int64_t q_out_stride,
+                             int *err, void *stream) {
+    int st = check_kv(kv);
+    if (st != W12_OK) return st;
+    if (x_dtype != W12_F32 && x_dtype != W12_BF16) return W12_ERR_ARG;
+    if (layout != W12_ROPE_HALF && layout != W12_ROPE_INTERLEAVED) return W12_ERR_ARG;
+    if (R < 0 || T < 1 || T >= kLim31 || R >= kLim31 || q_heads < 1 || q_heads > (1 << 20) ||
+        kv->heads > (1 << 20) || blocks < 0)
+        return W12_ERR_SHAPE;
+    if (rot < 0 || rot % 8 != 0 || rot > kv->head_dim || rope_positions < 0) return W12_ERR_SHAPE;
+    if (R * T >= kLim31) return W12_ERR_SHAPE;
+    if (R == 0) return W12_OK;
+    if (!q || !k || !v || !table || !kv_len || !q_out || (rot > 0 && !rope)) return W12_ERR_ARG;
+    const uintptr_t xa = x_dtype == W12_F32 ? 16 : 8;
+    if (!aligned(q, xa) || !aligned(k, xa) || !aligned(v, xa) || !aligned(q_out, 8) || !aligned(table, 4) ||
+        !aligned(kv_len, 4) || (rot > 0 && !aligned(rope, 16)) || (err && !aligned(err, 4)))
+        return W12_ERR_ALIGN;
+    if ((q_stride | k_stride | v_stride | q_out_stride) & 3) return W12_ERR_ALIGN;
+    int sms = 0;
+    if (current_sms(&sms) != W12_OK) return W12_ERR_CUDA;
+    AppendArgs a = {};
+    a.q = q, a.k = k, a.v = v;
+    a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride, a.out_stride = q_out_stride;
+    a.q_out = q_out;
+    a.kc = kv->k, a.vc = kv->v, a.ks = kv->k_scale, a.vs = kv->v_scale;
+    a.table = table, a.kv_len = kv_len, a.rope = rope;
+    a.rope_positions = rope_positions, a.tokens = R * T, a.table_cols = blocks, a.n_pages = kv->n_pages;
+    a.T = int32_t(T), a.q_heads = q_heads, a.heads = kv->heads, a.page = kv->page, a.page_log2 = log2_of(kv->page);
+    a.rot = rot, a.interleaved = layout == W12_ROPE_INTERLEAVED;
+    a.err = err;
+    return launch_append(a, x_dtype, kv->head_dim, kv->dtype, sms, stream);
+}
+
+extern "C" int w12_kv_read(const w12_kv *kv, const int32_t *table, int64_t blocks, const int32_t *cu_len, int64_t R,
+                           int64_t tokens, uint16_t *k_out, uint16_t *v_out, int *err, void *stream) {
+    int st = check_kv(kv);
+    if (st != W12_OK) return st;
+    if (R < 0 || tokens < 0 || R >= kLim31 || tokens >= kLim31 || blocks < 0 || kv->heads > (1 << 16))
+        return W12_ERR_SHAPE;
+    if (tokens == 0) return W12_OK;
+    if (R == 0) return W12_ERR_SHAPE;
+    if (!table || !cu_len || !k_out || !v_out) return W12_ERR_ARG;
+    if (!aligned(table, 4) || !aligned(cu_len, 4) || !aligned(k_out, 16) || !aligned(v_out, 16) ||
+        (err && !aligned(err, 4)))
+        return W12_ERR_ALIGN;
+    ReadArgs a = {};
+    a.kc = kv->k, a.vc = kv->v, a.ks = kv->k_scale, a.vs = kv->v_scale;
+    a.table = table, a.cu_len = cu_len, a.k_out = k_out, a.v_out = v_out;
+    a.R = R, a.tokens = tokens, a.table_cols = blocks, a.n_pages = kv->n_pages;
+    a.heads = kv->heads, a.page = kv->page, a.page_log2 = log2_of(kv->page);
+    a.err = err;
+    return launch_read(a, kv->head_dim, kv->dtype, stream);
+}
+
+extern "C" size_t w12_attend_workspace_size(const w12_kv *kv, int64_t R, int64_t T, int q_heads, int64_t max_len,
+                                            int64_t prefix_len) {
+    AttendPlan p;
+    return plan_attend(kv, R, T, q_heads, max_len, prefix_len, &p) == W12_OK ? p.total : 0;
+}
+
+extern "C" int w12_attend(const w12_kv *kv, const uint16_t *q, int64_t q_stride, int64_t R, int64_t T, int q_heads,
+                          const int32_t *table, int64_t blocks, const int32_t *kv_len, int64_t max_len,
+                          int64_t prefix_len, float scale, uint16_t *out, int64_t out_stride, float *lse, void *ws,
+                          size_t ws_bytes, void *stream) {
+    if (!kv || !q || !table || !kv_len || !out || !(scale == scale)) return W12_ERR_ARG;
+    if (blocks < 0) return W12_ERR_SHAPE;
+    if (!aligned(q, 16) || !aligned(out, 8) || !aligned(table, 4) || !aligned(kv_len, 4) || (lse && !aligned(lse, 4)) ||
+        (q_stride & 7) || (out_stride & 3))
+        return W12_ERR_ALIGN;
+    AttendPlan p;
+    int st = plan_attend(kv, R, T, q_heads, max_len, prefix_len, &p);
+    if (st != W12_OK) return st;
+    if (!ws || ws_bytes < p.total) return W12_ERR_WORKSPACE;
+    if (!aligned(ws, 256)) return W12_ERR_ALIGN;
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    AttendArgs a = {};
+    st = attend_make_maps(a, kv);
+    if (st != W12_OK) return st;
+    a.q = q, a.out = out, a.lse = lse;
+    a.ks = kv->k_scale, a.vs = kv->v_scale;
+    a.table = table, a.kv_len = kv_len;
+    a.q_stride = q_stride, a.out_stride = out_stride;
+    a.n_pages = kv->n_pages, a.table_cols = blocks;
+    a.R = int32_t(R), a.T = int32_t(T), a.G = q_heads / kv->heads, a.heads = kv->heads;
+    a.page = kv->page, a.page_log2 = log2_of(kv->page);
+    a.rows = p.rows, a.rt = p.rt, a.pu = p.pu, a.su = p.su;
+    a.prefix = int32_t(prefix_len), a.max_len = int32_t(max_len);
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.plan = reinterpret_cast<int32_t *>(w + p.off_plan);
+    a.part_ml = reinterpret_cast<float2 *>(w + p.off_ml);
+    a.part_o = reinterpret_cast<float *>(w + p.off_o);
+    a.err = reinterpret_cast<int *>(w);
+    return launch_attend(a, kv->head_dim, kv->dtype, p.grid, stream);
+}

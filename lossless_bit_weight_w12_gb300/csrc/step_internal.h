@@ -1,0 +1,93 @@
+// step_internal.h -- declarations shared by the decode-step calls (paged
+// key/value cache, attention over it, sampling): argument blocks of the
+// kernels and their launchers.  Not installed.
+#pragma once
+
+#include <cuda.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "../../include/w12.h"
+#include "w12_internal.h"
+
+namespace w12 {
+
+// Launch with programmatic stream serialization (the kernel's CTAs may start
+// while the previous kernel of the stream drains; they call pdl_wait()
+// before their first access to global memory).
+#ifdef __CUDACC__
+template <typename Args>
+int launch_step(void (*kernel)(Args), int grid, int threads, size_t smem, int cluster, void *stream, const Args &a) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(grid));
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cluster > 1) {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = unsigned(cluster);
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+    }
+    return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? W12_OK : W12_ERR_CUDA;
+}
+#endif
+
+struct AppendArgs {
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride, out_stride;  // elements per token
+    uint16_t *q_out;
+    void *kc, *vc;
+    float *ks, *vs;
+    const int32_t *table, *kv_len;
+    const float *rope;
+    int64_t rope_positions, tokens, table_cols, n_pages;
+    int32_t T, q_heads, heads, page, page_log2, rot, interleaved;
+    int *err;
+};
+int launch_append(const AppendArgs &a, int x_dtype, int head_dim, int kv_dtype, int sms, void *stream);
+
+struct ReadArgs {
+    const void *kc, *vc;
+    const float *ks, *vs;
+    const int32_t *table, *cu_len;
+    uint16_t *k_out, *v_out;
+    int64_t R, tokens, table_cols, n_pages;
+    int32_t heads, page, page_log2;
+    int *err;
+};
+int launch_read(const ReadArgs &a, int head_dim, int kv_dtype, void *stream);
+
+// Attention (kernels_attend.cu).  Work split: "attend_device.cuh".
+constexpr int kAttTile = 64;  // keys per tile
+struct AttendArgs {
+    CUtensorMap mk, mv;  // the cache as rows of head_dim channels
+    const uint16_t *q;
+    uint16_t *out;
+    float *lse;
+    const float *ks, *vs;
+    const int32_t *table, *kv_len;
+    int64_t q_stride, out_stride;
+    int64_t n_pages, table_cols;
+    int32_t R, T, G, heads, page, page_log2;
+    int32_t rows;      // R * T * G query rows per key head
+    int32_t rt;        // query rows per unit
+    int32_t pu, su;    // units per head: row tiles of all requests under the prefix, row tiles per request
+    int32_t prefix, max_len;
+    float scale_log2;  // scale * log2(e)
+    float *part_o;     // [slots][rt][head_dim]
+    float2 *part_ml;   // [slots][rt]: running maximum (log2 units) and sum
+    int32_t *plan;     // prefix tiles per unit, then the R + 1 cumulative tile counts of the requests
+    int *err;
+    uint64_t wait_ns;
+};
+int attend_make_maps(AttendArgs &a, const w12_kv *kv);
+int launch_attend(const AttendArgs &a, int head_dim, int kv_dtype, int grid, void *stream);
+
+}  // namespace w12

@@ -25,6 +25,10 @@ F32, BF16 = 0, 1
 PATH_AUTO, PATH_GEMV, PATH_MMA, PATH_TC = 0, 1, 2, 3
 OPT_EARLY_WEIGHTS = 0x100  # OR into a path: weight copies start under the previous kernel's tail
 MAX_M = 128
+ATTEND_MAX_R = 512
+KV_BF16, KV_E4M3 = 0, 1
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_SCALE_NONE, ROPE_SCALE_LINEAR, ROPE_SCALE_BASE, ROPE_SCALE_BANDS, ROPE_SCALE_YARN = 0, 1, 2, 3, 4
 
 # every symbol include/w12.h declares
 EXPORTS = (
@@ -34,7 +38,8 @@ EXPORTS = (
     "w12_verify_greedy_lmhead", "w12_get_device_error", "w12_verify_greedy_noalloc",
     "w12_gemm_batched_workspace_size", "w12_gemm_batched", "w12_gemm_batched_ex",
     "w12_encode_device_workspace_size", "w12_encode_plan_device", "w12_encode_device",
-    "w12_gemm_batched_debug",
+    "w12_gemm_batched_debug", "w12_rope_table", "w12_kv_append", "w12_kv_read",
+    "w12_attend_workspace_size", "w12_attend",
 )
 
 
@@ -55,6 +60,18 @@ class _CDesc(ctypes.Structure):
 
 class _CDebug(ctypes.Structure):
     _fields_ = [("withhold_unit", ctypes.c_int32), ("wait_limit_us", ctypes.c_uint32)]
+
+
+class _CKV(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class _CRopeScaling(ctypes.Structure):
+    _fields_ = [("mode", ctypes.c_int32), ("reserved", ctypes.c_int32), ("factor", ctypes.c_double),
+                ("original", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double),
+                ("attention", ctypes.c_double)]
 
 
 @dataclass(frozen=True)
@@ -122,6 +139,14 @@ def lib():
         L.w12_encode_plan_device.argtypes = [P, I64, I64, I, D, P, SZ, P]
         L.w12_encode_device.argtypes = [P, I64, I64, I, D, P, P, SZ, P]
         L.w12_gemm_batched_debug.argtypes = [D, P, P, I64, P, I, I, P, SZ, I, ctypes.POINTER(_CDebug), P]
+        KV = ctypes.POINTER(_CKV)
+        L.w12_rope_table.argtypes = [I64, I, ctypes.c_double, ctypes.POINTER(_CRopeScaling), P]
+        L.w12_kv_append.argtypes = [KV, P, I64, P, I64, P, I64, I, I64, I64, I, P, I64, P, P, I64, I, I, P, I64,
+                                    P, P]
+        L.w12_kv_read.argtypes = [KV, P, I64, P, I64, I64, P, P, P, P]
+        L.w12_attend_workspace_size.restype = SZ
+        L.w12_attend_workspace_size.argtypes = [KV, I64, I64, I, I64, I64]
+        L.w12_attend.argtypes = [KV, P, I64, I64, I64, I, P, I64, P, I64, I64, ctypes.c_float, P, I64, P, P, SZ, P]
         _lib = L
     return _lib
 
@@ -339,6 +364,135 @@ def get_device_error(ws_dev, stream=None) -> int:
     _check(lib().w12_get_device_error(_dptr(ws_dev), ctypes.byref(v), _stream(stream)),
            "w12_get_device_error")
     return v.value
+
+
+# ------------------------------------------------- decode step: paged cache
+
+class KVCache:
+    """A paged cache over device tensors (w12_kv): k, v [n_pages, heads, page,
+    head_dim] bfloat16 or float8_e4m3fn; for e4m3 the scales [n_pages, heads,
+    page] float32.  Holds the tensors and the marshalled descriptor."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        import torch
+        kinds = {torch.bfloat16: KV_BF16, torch.float8_e4m3fn: KV_E4M3}
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.dtype not in kinds:
+            raise ValueError("k and v: bfloat16 or float8_e4m3fn tensors [n_pages, heads, page, head_dim]")
+        self.dtype = kinds[k.dtype]
+        for t in (k_scale, v_scale):
+            if (t is None) != (self.dtype == KV_BF16):
+                raise ValueError("e4m3 caches have scales, bf16 caches have none")
+            if t is not None and (t.shape != k.shape[:3] or t.dtype != torch.float32):
+                raise ValueError("scales: float32 tensors [n_pages, heads, page]")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_pages, self.heads, self.page, self.head_dim = k.shape
+        self.c = _CKV(_dptr(k), _dptr(v), _dptr(k_scale), _dptr(v_scale), self.n_pages, self.heads,
+                      self.head_dim, self.page, self.dtype)
+        self.ref = ctypes.byref(self.c)
+
+    @staticmethod
+    def alloc(n_pages: int, heads: int, head_dim: int, page: int = 64, dtype: int = KV_BF16, device="cuda"):
+        """An empty cache of n_pages pages."""
+        import torch
+        shape = (n_pages, heads, page, head_dim)
+        if dtype == KV_BF16:
+            return KVCache(*(torch.empty(shape, dtype=torch.bfloat16, device=device) for _ in range(2)))
+        kv = [torch.empty(shape, dtype=torch.float8_e4m3fn, device=device) for _ in range(2)]
+        return KVCache(*kv, *(torch.empty(shape[:3], device=device) for _ in range(2)))
+
+
+def _heads_ptr(t, heads: int, dim: int):
+    """Device pointer of [tokens, heads, dim] rows with contiguous heads (any token stride)."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"expected [tokens, {heads}, {dim}], got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+        raise ValueError("expected contiguous heads")
+    return t.data_ptr()
+
+
+def _int32(t, what: str):
+    import torch
+    if t.dtype != torch.int32:
+        raise ValueError(f"{what}: expected int32")
+    return _dptr(t)
+
+
+def rope_table(positions: int, rot: int, base: float = 10000.0, mode: int = ROPE_SCALE_NONE, factor: float = 1.0,
+               original: float = 0.0, low: float = 1.0, high: float = 32.0, attention: float = 0.0) -> np.ndarray:
+    """w12_rope_table: float32 [positions, rot], cosines then sines (host)."""
+    table = np.empty((positions, rot), dtype=np.float32)
+    sc = _CRopeScaling(mode, 0, factor, original, low, high, attention)
+    _check(lib().w12_rope_table(positions, rot, base, ctypes.byref(sc), _np_ptr(table)), "w12_rope_table")
+    return table
+
+
+def kv_append(kv: KVCache, q, k, v, block_table, kv_len, T: int, q_out, table=None, layout: int = ROPE_HALF,
+              err_dev=None, stream=None):
+    """Rotate the new tokens' queries (into q_out, bfloat16) and keys and write
+    keys and values into the cache.  q [R*T, q_heads, head_dim], k and v
+    [R*T, heads, head_dim]: float32 or bfloat16, any token stride (parts of
+    one projection output); block_table [R, blocks] and kv_len [R] int32;
+    table: the rotary table on the device (None: no rotation)."""
+    import torch
+    n, hq, dim = q.shape
+    R = kv_len.numel()
+    if n != R * T or block_table.shape[0] != R or not (q.dtype == k.dtype == v.dtype):
+        raise ValueError("q, k, v: R * T tokens of one type; block_table: R rows")
+    if q.dtype not in (torch.float32, torch.bfloat16) or q_out.dtype != torch.bfloat16:
+        raise ValueError("q, k, v: float32 or bfloat16; q_out: bfloat16")
+    if k.shape[0] != n or v.shape[0] != n or q_out.shape[0] != n:
+        raise ValueError("q, k, v, q_out: R * T tokens each")
+    positions, rot = (0, 0) if table is None else table.shape
+    if table is not None and table.dtype != torch.float32:
+        raise ValueError("table: expected float32")
+    _check(lib().w12_kv_append(
+        kv.ref, _heads_ptr(q, hq, kv.head_dim), q.stride(0), _heads_ptr(k, kv.heads, kv.head_dim), k.stride(0),
+        _heads_ptr(v, kv.heads, kv.head_dim), v.stride(0), F32 if q.dtype == torch.float32 else BF16, R, T, hq,
+        _int32(block_table, "block_table"), block_table.shape[1], _int32(kv_len, "kv_len"), _dptr(table),
+        positions, rot, layout, _heads_ptr(q_out, hq, kv.head_dim), q_out.stride(0), _dptr(err_dev),
+        _stream(stream)), "w12_kv_append")
+
+
+def kv_read(kv: KVCache, block_table, cu_len, k_out, v_out, err_dev=None, stream=None):
+    """Read rows 0 .. cu_len[r+1] - cu_len[r] - 1 of every request back, packed
+    into k_out and v_out [tokens, heads, head_dim] bfloat16."""
+    import torch
+    R = cu_len.numel() - 1
+    if block_table.shape[0] != R or k_out.dtype != torch.bfloat16 or v_out.dtype != torch.bfloat16:
+        raise ValueError("block_table: one row per request; outputs: bfloat16")
+    if k_out.shape != v_out.shape or k_out.shape[1:] != (kv.heads, kv.head_dim):
+        raise ValueError("outputs: [tokens, heads, head_dim]")
+    _check(lib().w12_kv_read(kv.ref, _int32(block_table, "block_table"), block_table.shape[1],
+                             _int32(cu_len, "cu_len"), R, k_out.shape[0], _dptr(k_out), _dptr(v_out),
+                             _dptr(err_dev), _stream(stream)), "w12_kv_read")
+
+
+def attend_workspace_size(kv: KVCache, R: int, T: int, q_heads: int, max_len: int, prefix_len: int = 0) -> int:
+    return int(lib().w12_attend_workspace_size(kv.ref, R, T, q_heads, max_len, prefix_len))
+
+
+def attend(kv: KVCache, q, block_table, kv_len, T: int, max_len: int, out, ws_dev, scale: float | None = None,
+           prefix_len: int = 0, lse_dev=None, stream=None):
+    """Causal attention of the R * T newest tokens over the cache.  q and out
+    [R*T, q_heads, head_dim] bfloat16 (any token stride); scale: 1 /
+    sqrt(head_dim) by default; the first prefix_len keys are shared by all
+    requests; lse_dev: float32 [R*T, q_heads] or None."""
+    import torch
+    n, hq, dim = q.shape
+    R = kv_len.numel()
+    if n != R * T or out.shape != q.shape or block_table.shape[0] != R:
+        raise ValueError("q and out: R * T tokens; block_table: R rows")
+    if q.dtype != torch.bfloat16 or out.dtype != torch.bfloat16:
+        raise ValueError("q and out: bfloat16")
+    if lse_dev is not None and (lse_dev.dtype != torch.float32 or lse_dev.numel() != n * hq):
+        raise ValueError("lse: float32 [R * T, q_heads]")
+    _check(lib().w12_attend(kv.ref, _heads_ptr(q, hq, kv.head_dim), q.stride(0), R, T, hq,
+                            _int32(block_table, "block_table"), block_table.shape[1], _int32(kv_len, "kv_len"),
+                            max_len, prefix_len, dim ** -0.5 if scale is None else scale,
+                            _heads_ptr(out, hq, kv.head_dim), out.stride(0), _dptr(lse_dev), _dptr(ws_dev),
+                            ws_dev.numel() * ws_dev.element_size(), _stream(stream)), "w12_attend")
 
 
 # --------------------------------------------------------------- helpers
