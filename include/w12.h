@@ -576,6 +576,48 @@ int w12_attend(const w12_kv *kv, const uint16_t *q_dev, int64_t q_stride, int64_
                int64_t prefix_len, float scale, uint16_t *out_dev, int64_t out_stride, float *lse_dev, void *ws_dev,
                size_t ws_bytes, void *stream);
 
+/* Largest V of w12_sample. */
+#define W12_SAMPLE_MAX_V 524288
+
+/* Bytes of workspace w12_sample needs (0 on invalid arguments). */
+size_t w12_sample_workspace_size(int64_t R, int64_t T, int64_t V);
+
+/*
+ * Sample one token for each of R * T rows of logits from given random
+ * numbers, and accept drafts against the sampled tokens.
+ *   logits_dev: [R*T][V] row-major, dtype W12_F32 or W12_BF16 (4- or 2-byte
+ *     aligned; 16-byte aligned rows are read faster).
+ *   temperature_dev, top_k_dev, top_p_dev, min_p_dev: [R] per request (fp32,
+ *     top_k int32), each may be NULL (temperature 1; no cut).
+ *   u_dev: [R*T] fp32 in [0, 1), one random number per row (24 bits count).
+ * Per row, with max its largest logit and t the temperature:
+ *   w_i = round(2^31 e^((x_i - max) / t)), tokens ordered by logit, equal ones
+ *   by index; a NaN counts as -infinity (never sampled).
+ *   top_k (0 < top_k < V): the first top_k tokens stay.
+ *   top_p (< 1): of those, a token stays while the weight before it is less
+ *     than top_p (in units of 2^-24) times their whole weight; the first always.
+ *   min_p (> 0): of those, tokens with w_i >= min_p 2^31 stay.
+ *   tokens_dev[row] = the first index, in index order, at which the sum of the
+ *     staying weights W passes u W; prob_dev[row] (may be NULL) = its w / W.
+ *   t <= 0 (or NaN): the lowest index of the largest logit, probability 1.
+ *   A row without a logit above -infinity, or whose tokens min_p > 1 all
+ *   removes: token -1, probability 0.
+ * The sums are whole numbers, so a result does not depend on how a row is
+ * cut over the GPU.
+ * Acceptance (accept_len_dev NULL: none), the rule of w12_verify_greedy on
+ * the sampled tokens: accept_len[r] = first i < T - 1 with draft[r, i] !=
+ * tokens[r, i], else T - 1; next_tok[r] = tokens[r, accept_len[r]]: every
+ * committed token is the target model's own sample.
+ *   draft_dev: [R][T-1] int32 (may be NULL when T == 1).
+ * R >= 1, T >= 1, R * T < 2^27, 1 <= V <= W12_SAMPLE_MAX_V.
+ * Errors: W12_ERR_ARG, W12_ERR_SHAPE, W12_ERR_ALIGN, W12_ERR_WORKSPACE,
+ * W12_ERR_CUDA.
+ */
+int w12_sample(const void *logits_dev, int dtype, int64_t R, int64_t T, int64_t V, const float *temperature_dev,
+               const int32_t *top_k_dev, const float *top_p_dev, const float *min_p_dev, const float *u_dev,
+               int32_t *tokens_dev, float *prob_dev, const int32_t *draft_dev, int32_t *accept_len_dev,
+               int32_t *next_tok_dev, void *ws_dev, size_t ws_bytes, void *stream);
+
 /*
  * Read (and clear) the sticky device error word of a workspace: waits for
  * `stream`, copies word 0 to *err_host, then zeroes it.  Returns W12_OK or

@@ -193,3 +193,37 @@ extern "C" int w12_attend(const w12_kv *kv, const uint16_t *q, int64_t q_stride,
     a.err = reinterpret_cast<int *>(w);
     return launch_attend(a, kv->head_dim, kv->dtype, p.grid, stream);
 }
+
+extern "C" size_t w12_sample_workspace_size(int64_t R, int64_t T, int64_t V) {
+    if (R < 1 || T < 1 || V < 1 || V > W12_SAMPLE_MAX_V || R >= kLim31 || T >= kLim31 || R * T >= (int64_t(1) << 27))
+        return 0;
+    return kWsHeader + 256;
+}
+
+extern "C" int w12_sample(const void *logits, int dtype, int64_t R, int64_t T, int64_t V, const float *temperature,
+                          const int32_t *top_k, const float *top_p, const float *min_p, const float *u,
+                          int32_t *tokens, float *prob, const int32_t *draft, int32_t *accept_len, int32_t *next_tok,
+                          void *ws, size_t ws_bytes, void *stream) {
+    if (dtype != W12_F32 && dtype != W12_BF16) return W12_ERR_ARG;
+    const size_t need = w12_sample_workspace_size(R, T, V);
+    if (need == 0) return W12_ERR_SHAPE;
+    if (!logits || !u || !tokens || (!accept_len) != (!next_tok) || (accept_len && T > 1 && !draft)) return W12_ERR_ARG;
+    for (const void *p : {static_cast<const void *>(temperature), static_cast<const void *>(top_k),
+                          static_cast<const void *>(top_p), static_cast<const void *>(min_p),
+                          static_cast<const void *>(u), static_cast<const void *>(tokens),
+                          static_cast<const void *>(prob), static_cast<const void *>(draft),
+                          static_cast<const void *>(accept_len), static_cast<const void *>(next_tok)})
+        if (!aligned(p, 4)) return W12_ERR_ALIGN;
+    if (!aligned(logits, dtype == W12_F32 ? 4 : 2)) return W12_ERR_ALIGN;
+    if (!ws || ws_bytes < need) return W12_ERR_WORKSPACE;
+    if (!aligned(ws, 256)) return W12_ERR_ALIGN;
+    int sms = 0;
+    if (current_sms(&sms) != W12_OK) return W12_ERR_CUDA;
+    SampleArgs a = {};
+    a.logits = logits;
+    a.temperature = temperature, a.top_k = top_k, a.top_p = top_p, a.min_p = min_p, a.u = u;
+    a.tokens = tokens, a.prob = prob, a.draft = draft, a.accept_len = accept_len, a.next_tok = next_tok;
+    a.counter = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(ws) + kWsHeader);
+    a.V = V, a.rows = R * T, a.R = R, a.T = T;
+    return launch_sample(a, dtype, sms, stream);
+}

@@ -90,4 +90,18 @@ struct AttendArgs {
 int attend_make_maps(AttendArgs &a, const w12_kv *kv);
 int launch_attend(const AttendArgs &a, int head_dim, int kv_dtype, int grid, void *stream);
 
+struct SampleArgs {
+    const void *logits;
+    const float *temperature, *top_p, *min_p, *u;
+    const int32_t *top_k, *draft;
+    int32_t *tokens, *accept_len, *next_tok;
+    float *prob;
+    uint32_t *counter;
+    int64_t V, rows, R, T;
+    int32_t chunk;      // logits per CTA of a row's cluster
+    int32_t resident;   // the chunk fits in shared memory
+    int32_t vec;        // 16-byte loads: every chunk starts on a 16-byte boundary
+};
+int launch_sample(SampleArgs &a, int dtype, int sms, void *stream);
+
 }  // namespace w12

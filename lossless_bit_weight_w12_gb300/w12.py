@@ -26,6 +26,7 @@ PATH_AUTO, PATH_GEMV, PATH_MMA, PATH_TC = 0, 1, 2, 3
 OPT_EARLY_WEIGHTS = 0x100  # OR into a path: weight copies start under the previous kernel's tail
 MAX_M = 128
 ATTEND_MAX_R = 512
+SAMPLE_MAX_V = 524288
 KV_BF16, KV_E4M3 = 0, 1
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 ROPE_SCALE_NONE, ROPE_SCALE_LINEAR, ROPE_SCALE_BASE, ROPE_SCALE_BANDS, ROPE_SCALE_YARN = 0, 1, 2, 3, 4
@@ -39,7 +40,7 @@ EXPORTS = (
     "w12_gemm_batched_workspace_size", "w12_gemm_batched", "w12_gemm_batched_ex",
     "w12_encode_device_workspace_size", "w12_encode_plan_device", "w12_encode_device",
     "w12_gemm_batched_debug", "w12_rope_table", "w12_kv_append", "w12_kv_read",
-    "w12_attend_workspace_size", "w12_attend",
+    "w12_attend_workspace_size", "w12_attend", "w12_sample_workspace_size", "w12_sample",
 )
 
 
@@ -147,6 +148,9 @@ def lib():
         L.w12_attend_workspace_size.restype = SZ
         L.w12_attend_workspace_size.argtypes = [KV, I64, I64, I, I64, I64]
         L.w12_attend.argtypes = [KV, P, I64, I64, I64, I, P, I64, P, I64, I64, ctypes.c_float, P, I64, P, P, SZ, P]
+        L.w12_sample_workspace_size.restype = SZ
+        L.w12_sample_workspace_size.argtypes = [I64, I64, I64]
+        L.w12_sample.argtypes = [P, I, I64, I64, I64, P, P, P, P, P, P, P, P, P, P, P, SZ, P]
         _lib = L
     return _lib
 
@@ -493,6 +497,34 @@ def attend(kv: KVCache, q, block_table, kv_len, T: int, max_len: int, out, ws_de
                             max_len, prefix_len, dim ** -0.5 if scale is None else scale,
                             _heads_ptr(out, hq, kv.head_dim), out.stride(0), _dptr(lse_dev), _dptr(ws_dev),
                             ws_dev.numel() * ws_dev.element_size(), _stream(stream)), "w12_attend")
+
+
+# ---------------------------------------------------- decode step: sampling
+
+def sample_workspace_size(R: int, T: int, V: int) -> int:
+    return int(lib().w12_sample_workspace_size(R, T, V))
+
+
+def sample(logits, R: int, T: int, u, tokens_dev, ws_dev, temperature=None, top_k=None, top_p=None, min_p=None,
+           prob_dev=None, draft_dev=None, accept_dev=None, next_dev=None, stream=None):
+    """One token for each of R * T rows of logits [R*T, V] (float32 or
+    bfloat16) from the random numbers u [R*T]; temperature, top_p, min_p
+    (float32) and top_k (int32): [R] or None; with accept_dev and next_dev the
+    drafts are accepted against the sampled tokens."""
+    import torch
+    if logits.dtype not in (torch.float32, torch.bfloat16) or logits.numel() != R * T * logits.shape[-1]:
+        raise ValueError("logits: float32 or bfloat16 [R * T, V]")
+    for t, n in ((temperature, R), (top_p, R), (min_p, R), (u, R * T), (prob_dev, R * T)):
+        if t is not None and (t.dtype != torch.float32 or t.numel() != n):
+            raise ValueError("temperature, top_p, min_p [R], u, prob [R * T]: float32")
+    for t, n in ((top_k, R), (tokens_dev, R * T), (draft_dev, R * (T - 1)), (accept_dev, R), (next_dev, R)):
+        if t is not None and (t.dtype != torch.int32 or t.numel() != n):
+            raise ValueError("top_k, accept, next [R], tokens [R * T], draft [R, T - 1]: int32")
+    _check(lib().w12_sample(_dptr(logits), F32 if logits.dtype == torch.float32 else BF16, R, T, logits.shape[-1],
+                            _dptr(temperature), _dptr(top_k), _dptr(top_p), _dptr(min_p), _dptr(u),
+                            _dptr(tokens_dev), _dptr(prob_dev), _dptr(draft_dev), _dptr(accept_dev),
+                            _dptr(next_dev), _dptr(ws_dev), ws_dev.numel() * ws_dev.element_size(),
+                            _stream(stream)), "w12_sample")
 
 
 # --------------------------------------------------------------- helpers
