@@ -51,10 +51,18 @@ int check_kv(const w12_kv *kv) {
 constexpr int64_t kLim31 = int64_t(1) << 31;
 
 struct AttendPlan {
-    int32_t rows, rt, pu, su;
-    int grid;
-    size_t off_plan, off_ml, off_o, total;
+    int32_t rows;
+    struct Line {
+        int32_t pu, su, rt, halves, grid;
+        size_t off_plan, off_ml, off_o;
+    } line[kLines];
+    size_t total;
 };
+
+// Rows per key head from which the tensor-memory kernel takes a part's whole
+// tiles: its tile has 128 rows whatever their number, the register kernel
+// streams the keys once per 32 rows.
+constexpr int64_t kTcRows = 33;
 
 // Work split and workspace layout of an attention call.
 int plan_attend(const w12_kv *kv, int64_t R, int64_t T, int q_heads, int64_t max_len, int64_t prefix, AttendPlan *p) {
@@ -68,24 +76,43 @@ int plan_attend(const w12_kv *kv, int64_t R, int64_t T, int q_heads, int64_t max
     if (rows >= kLim31 / 2) return W12_ERR_SHAPE;
     const int64_t most = prefix > 0 ? rows : tg;
     p->rows = int32_t(rows);
-    p->rt = most <= 16 ? 16 : 32;
-    p->pu = prefix > 0 ? int32_t((rows + p->rt - 1) / p->rt) : 0;
-    p->su = int32_t((tg + p->rt - 1) / p->rt);
-    const int64_t own = max_len / kAttTile + 1, shared = (std::min(prefix, max_len) + kAttTile - 1) / kAttTile;
-    if (own > kLim31 / (R * p->su) || shared > kLim31 / std::max(p->pu, 1)) return W12_ERR_SHAPE;
-    if (own * R * p->su + shared * p->pu >= kLim31 / kv->heads) return W12_ERR_SHAPE;
-    const int64_t tiles = (own * R * p->su + shared * p->pu) * kv->heads;
+    const auto blocks = [](int64_t n, int64_t rt) { return int32_t((n + rt - 1) / rt); };
+    auto *l = p->line;
+    for (int i = 0; i < kLines; ++i) l[i] = {};
+    const int64_t shared = (std::min(prefix, max_len) + kAttTile - 1) / kAttTile, own = max_len / kAttTile + 1;
+    // whole tiles: at most these many of the prefix and of a request
+    const bool tc_p = rows >= kTcRows && std::min(prefix, max_len) >= kAttTile;
+    const bool tc_r = tg >= kTcRows && max_len - T + 1 >= (prefix + kAttTile - 1) / kAttTile * kAttTile + kAttTile;
+    if (tc_p) {
+        l[kLinePrefix].rt = rows <= 128 ? 128 : 256;
+        l[kLinePrefix].pu = blocks(rows, l[kLinePrefix].rt);
+    }
+    if (tc_r) {
+        l[kLineRequests].rt = tg <= 128 ? 128 : 256;
+        l[kLineRequests].su = blocks(tg, l[kLineRequests].rt);
+    }
+    l[kLineRest].rt = most <= 16 ? 16 : 32;
+    l[kLineRest].pu = prefix > 0 ? blocks(rows, l[kLineRest].rt) : 0;
+    l[kLineRest].su = blocks(tg, l[kLineRest].rt);
     int sms = 0;
     if (current_sms(&sms) != W12_OK) return W12_ERR_CUDA;
-    p->grid = int(std::min<int64_t>(sms, tiles));
-    const int64_t slots = int64_t(kv->heads) * (p->pu + R * p->su) + p->grid;
     size_t off = kWsHeader;
-    p->off_plan = off;
-    off += round256(uint64_t(R + 2) * 4u);
-    p->off_ml = off;
-    off += round256(uint64_t(slots) * p->rt * 8u);
-    p->off_o = off;
-    off += round256(uint64_t(slots) * p->rt * uint64_t(kv->head_dim) * 4u);
+    for (int i = 0; i < kLines; ++i) {
+        auto &n = l[i];
+        if (n.pu + n.su == 0) continue;
+        n.halves = i != kLineRest && n.rt == 128 ? 2 : 1;
+        if (own > kLim31 / (R * std::max(n.su, 1)) || shared > kLim31 / std::max(n.pu, 1)) return W12_ERR_SHAPE;
+        const int64_t tiles = own * R * n.su + shared * n.pu;
+        if (tiles >= kLim31 / kv->heads) return W12_ERR_SHAPE;
+        n.grid = int(std::max<int64_t>(1, std::min<int64_t>(sms, tiles * kv->heads)));
+        const uint64_t rowsets = uint64_t(kv->heads * (n.pu + R * n.su) + n.grid) * n.halves * n.rt;
+        n.off_plan = off;
+        off += round256(uint64_t(R + 2) * 4u);
+        n.off_ml = off;
+        off += round256(rowsets * 8u);
+        n.off_o = off;
+        off += round256(rowsets * uint64_t(kv->head_dim) * 4u);
+    }
     p->total = off;
     return W12_OK;
 }
@@ -184,14 +211,23 @@ extern "C" int w12_attend(const w12_kv *kv, const uint16_t *q, int64_t q_stride,
     a.n_pages = kv->n_pages, a.table_cols = blocks;
     a.R = int32_t(R), a.T = int32_t(T), a.G = q_heads / kv->heads, a.heads = kv->heads;
     a.page = kv->page, a.page_log2 = log2_of(kv->page);
-    a.rows = p.rows, a.rt = p.rt, a.pu = p.pu, a.su = p.su;
+    a.rows = p.rows;
     a.prefix = int32_t(prefix_len), a.max_len = int32_t(max_len);
     a.scale_log2 = scale * 1.4426950408889634f;
-    a.plan = reinterpret_cast<int32_t *>(w + p.off_plan);
-    a.part_ml = reinterpret_cast<float2 *>(w + p.off_ml);
-    a.part_o = reinterpret_cast<float *>(w + p.off_o);
     a.err = reinterpret_cast<int *>(w);
-    return launch_attend(a, kv->head_dim, kv->dtype, p.grid, stream);
+    for (int i = 0; i < kLines; ++i) {
+        const auto &n = p.line[i];
+        a.line[i] = {n.pu, n.su, n.rt, n.halves, n.grid, reinterpret_cast<int32_t *>(w + n.off_plan),
+                     reinterpret_cast<float *>(w + n.off_o), reinterpret_cast<float2 *>(w + n.off_ml)};
+    }
+    for (int i = 0; i < kLines; ++i) {
+        a.self = i;
+        if (!a.line[i].grid) continue;
+        st = i == kLineRest ? launch_attend_rest(a, kv->head_dim, kv->dtype, stream)
+                            : launch_attend_tc(a, kv->head_dim, kv->dtype, stream);
+        if (st != W12_OK) return st;
+    }
+    return launch_attend_join(a, kv->head_dim, stream);
 }
 
 extern "C" size_t w12_sample_workspace_size(int64_t R, int64_t T, int64_t V) {

@@ -9,7 +9,8 @@
 // second product rounded to bf16 (bf16 cache) or fp16 (e4m3 cache), as
 // tensor cores take them; l sums the unrounded ones.
 //
-// With few query rows the cache stream bounds it.  attend_kernel: one CTA
+// The register kernel, for few query rows per key head (the cache stream
+// bounds it) and for every tile that needs a mask: one CTA
 // per SM, a producer warp keeps a ring of key/value tiles full with TMA
 // boxes (a box per page and tile; 128-byte swizzle, so that the fragment
 // loads below have no bank conflicts), 8 consumer warps in two groups take
@@ -21,9 +22,11 @@
 // e4m3 tiles stay 8 bits wide up to the registers: codes are exact in fp16,
 // so both products run in fp16; the query row is scaled by a power of two to
 // below 2 (its bf16 values then lose nothing that matters: what is 2^-14 of
-// the row's largest keeps fewer bits), the key's scale multiplies the score,
-// and the value's scale, over a power of two that bounds the scales seen so
-// far, multiplies the weight.
+// the row's largest keeps fewer bits), the key's scale multiplies the score
+// and the value's scale the weight.  m only has to keep the exponentials in
+// range: with value scales below 2^e it is max - 7 + e, so that weights times
+// scales stay below 2^7 and the fp16 they are rounded to is far from both of
+// its ends.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -39,26 +42,20 @@ namespace {
 constexpr int kCW = 8;                  // consumer warps, two groups of 4
 constexpr int kCT = kCW * 32;
 constexpr int kAT = kCT + 32;           // + the producer warp
-constexpr int kMaxR = W12_ATTEND_MAX_R;
 constexpr int kJoinCols = 32;           // channels per step of the CTA's join
 constexpr int kJoinPitch = kJoinCols + 4;
 constexpr float kNegInf = -INFINITY;
 
-struct AttendJoinArgs {
-    AttendArgs a;
-    int grid;
-};
-
 template <int D, bool Q8, int MT>
 struct ACfg {
     static constexpr int RT = 16 * MT;
-    static constexpr int kTileBytes = kAttTile * D * (Q8 ? 1 : 2);  // keys or values of a tile
-    static constexpr int kScaleOff = 2 * kTileBytes;
-    static constexpr int kStage = 2 * kTileBytes + (Q8 ? 1024 : 0);
+    static constexpr int kTileBytes = AttStage<D, Q8>::kTile;
+    static constexpr int kScaleOff = AttStage<D, Q8>::kScale;
+    static constexpr int kStage = AttStage<D, Q8>::kBytes;
     static constexpr int kQ = RT * D * 2;
     static constexpr int kJoin = kCW * 16 * kJoinPitch * 4;
     static constexpr int kRowStat = kCW * RT * 8;
-    static constexpr int kLens = (2 * kMaxR + 1) * 4;
+    static constexpr int kLens = int(sizeof(AttShared));
     static constexpr int kMisc = 1024;                              // barriers, wait state, scalars
     static constexpr int kFixed = kQ + kJoin + kRowStat + kLens + kMisc;
     static constexpr int kFit = (227 * 1024 - kFixed) / kStage;
@@ -68,20 +65,6 @@ struct ACfg {
     static constexpr size_t kSmem = size_t(S) * kStage + kFixed;
     static_assert(S >= 2 && kSmem <= 227 * 1024, "shared memory");
 };
-
-__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_addr(bar))
-        : "memory");
-}
-
-__device__ __forceinline__ void bulk_bytes(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(smem_addr(bar))
-                 : "memory");
-}
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -106,12 +89,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                      "{%0,%1,%2,%3};"
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
 }
 
 __device__ __forceinline__ float2 lds_f2(uint32_t addr) {
@@ -189,13 +166,11 @@ __global__ void __launch_bounds__(kAT, 1) attend_kernel(const __grid_constant__ 
     const uint32_t qs = smem_addr(fixed);
     float *join = reinterpret_cast<float *>(fixed + C::kQ);
     float2 *rowstat = reinterpret_cast<float2 *>(fixed + C::kQ + C::kJoin);
-    int *lens = reinterpret_cast<int *>(fixed + C::kQ + C::kJoin + C::kRowStat);
-    int *cum = lens + kMaxR;
+    AttShared &sh = *reinterpret_cast<AttShared *>(fixed + C::kQ + C::kJoin + C::kRowStat);
     unsigned char *misc = fixed + C::kQ + C::kJoin + C::kRowStat + C::kLens;
     misc = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(misc) + 15) & ~uintptr_t(15));
     uint64_t *full = reinterpret_cast<uint64_t *>(misc), *empty = full + S;
     WaitCtl &ctl = *reinterpret_cast<WaitCtl *>(empty + S);
-    int &s_longest = *reinterpret_cast<int *>(reinterpret_cast<unsigned char *>(&ctl) + sizeof(WaitCtl));
     float *row_m = reinterpret_cast<float *>(misc + 512);  // [RT] the segment's maxima (RT <= 32)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (ring & 1023u) {  // the swizzled boxes need a 1024-byte aligned ring
@@ -214,120 +189,11 @@ __global__ void __launch_bounds__(kAT, 1) attend_kernel(const __grid_constant__ 
     pdl_launch_dependents();
     pdl_wait_previous();
 
-    // ---- the plan: lengths, cumulative tiles
-    for (int r = threadIdx.x; r < a.R; r += kAT) {
-        const int n = att_len(a, r);
-        if (a.kv_len[r] > n && blockIdx.x == 0) record_error(a.err, W12_ERR_DEVICE);
-        lens[r] = n;
-    }
-    __syncthreads();
-    if (warp == 0) {
-        int sum = 0, longest = 0;
-        for (int r0 = 0; r0 < a.R; r0 += 32) {
-            const int r = r0 + lane, n = r < a.R ? lens[r] : 0;
-            int x = att_req_tiles(a, n), y = x;
-            longest = max(longest, n);
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int z = __shfl_up_sync(0xFFFFFFFFu, x, o);
-                if (lane >= o) x += z;
-            }
-            if (r < a.R) cum[r] = sum + x - y;
-            sum += __shfl_sync(0xFFFFFFFFu, x, 31);
-        }
-        longest = __reduce_max_sync(0xFFFFFFFFu, longest);
-        if (lane == 0) {
-            cum[a.R] = sum;
-            s_longest = longest;
-        }
-    }
-    __syncthreads();
-    const int longest = s_longest;
-    AttPlan plan;
-    plan.cum = cum;
-    plan.np = (att_prefix_end(a, longest) + kAttTile - 1) / kAttTile;
-    plan.per_head = a.pu * plan.np + a.su * cum[a.R];
-    const int total = plan.per_head * a.heads;
-    const int t0 = att_begin(total, int(gridDim.x), int(blockIdx.x));
-    const int t1 = att_begin(total, int(gridDim.x), int(blockIdx.x) + 1);
-    if (blockIdx.x == 0) {  // for the join kernel
-        if (threadIdx.x == 0) a.plan[0] = plan.np;
-        for (int r = threadIdx.x; r <= a.R; r += kAT) a.plan[1 + r] = cum[r];
-    }
-
+    const AttPlan plan = att_plan(a, sh, kAT);
+    const AttendLine &ln = a.line[a.self];
+    const int t0 = plan.t0, t1 = plan.t1;
     if (warp == kCW) {
-        // ------------------------------------------------------- producer
-        // A lane per box row block ("chunk": the keys of one page in one
-        // tile); a batch of 32 chunks has its table entries read at once,
-        // the next batch's while this one is issued.
-        const int br = min(a.page, kAttTile), cpt = kAttTile / br, tpb = 32 / cpt;
-        const int my_tile = lane / cpt, my_chunk = lane % cpt;
-        struct Chunk {
-            int row, valid;  // first cache row; 0: nothing to load
-        };
-        const auto look = [&](int tb) {
-            Chunk c{0, 0};
-            const int t = tb + my_tile;
-            if (t >= t1) return c;
-            const AttSeg g = att_locate(a, plan, lens, longest, t);
-            const int key = g.tile * kAttTile + my_chunk * br;
-            // (keys before the prefix's end are not looked up in the request's own row)
-            if (key >= g.key_end || key + br <= g.key_begin) return c;
-            int pg = a.table[int64_t(g.req) * a.table_cols + (key >> a.page_log2)];
-            if (pg < 0 || pg >= a.n_pages) {
-                record_error(a.err, W12_ERR_DEVICE);
-                pg = 0;
-            }
-            c.row = ((pg * a.heads + g.head) << a.page_log2) + (key & (a.page - 1));
-            c.valid = 1;
-            return c;
-        };
-        int issued = 0;
-        bool stop = false;
-        Chunk cur = look(t0);
-        for (int tb = t0; tb < t1 && !stop; tb += tpb) {
-            const Chunk nxt = look(tb + tpb);
-            for (int k = 0; k < tpb && tb + k < t1; ++k) {
-                const int i = tb + k - t0, s = i % S;
-                int go = 1;
-                if (lane == 0) go = i < S || (mbar_wait(&empty[s], uint32_t(i / S - 1) & 1u, &ctl, a.err) && !aborted(&ctl));
-                go = __shfl_sync(0xFFFFFFFFu, go, 0);
-                if (!go) {
-                    stop = true;
-                    break;
-                }
-                const bool mine = my_tile == k && cur.valid;
-                const int chunks = __popc(__ballot_sync(0xFFFFFFFFu, mine));
-                const uint32_t st = ring + uint32_t(s) * uint32_t(C::kStage);
-                if (lane == 0)
-                    mbar_expect_tx(&full[s], uint32_t(chunks) * uint32_t(br) * uint32_t(D * (Q8 ? 2 : 4) + (Q8 ? 8 : 0)));
-                __syncwarp();
-                if (mine) {
-                    const uint32_t at = uint32_t(my_chunk * br);
-                    if (Q8) {
-                        const uint32_t o = st + at * uint32_t(D);
-                        tma_box(o, &a.mk, 0, cur.row, &full[s]);
-                        tma_box(o + uint32_t(C::kTileBytes), &a.mv, 0, cur.row, &full[s]);
-                        const uint32_t sc = st + uint32_t(C::kScaleOff) + at * 4u;
-                        bulk_bytes(sc, a.ks + cur.row, uint32_t(br) * 4u, &full[s]);
-                        bulk_bytes(sc + kAttTile * 4u, a.vs + cur.row, uint32_t(br) * 4u, &full[s]);
-                    } else {
-#pragma unroll
-                        for (int h = 0; h < D / 64; ++h) {
-                            const uint32_t o = st + uint32_t(h * kAttTile * 128) + at * 128u;
-                            tma_box(o, &a.mk, 64 * h, cur.row, &full[s]);
-                            tma_box(o + uint32_t(C::kTileBytes), &a.mv, 64 * h, cur.row, &full[s]);
-                        }
-                    }
-                }
-                ++issued;
-            }
-            cur = nxt;
-        }
-        // after a timeout: let the copies in flight land before the CTA ends
-        if (lane == 0 && aborted(&ctl))
-            for (int j = issued - 1; j >= 0 && j >= issued - S; --j)
-                mbar_drain(&full[j % S], uint32_t(j / S) & 1u, ctl.limit_ns);
+        att_producer<D, Q8, S>(a, plan, sh, ring, full, empty, &ctl);
         return;
     }
 
@@ -336,7 +202,7 @@ __global__ void __launch_bounds__(kAT, 1) attend_kernel(const __grid_constant__ 
     const int g8 = lane >> 2, q4 = lane & 3;
     const int r0 = lane & 7, mat = lane >> 3;         // ldmatrix: this lane's row and matrix
     for (int t = t0; t < t1;) {
-        const AttSeg seg = att_locate(a, plan, lens, longest, t);
+        const AttSeg seg = att_locate(a, plan, sh, t);
         const int n_tiles = min(seg.left, t1 - t);
         // ---- query rows into shared memory (rows past the unit: zeros)
         named_sync(kCT);  // the previous segment's copy is no longer read
@@ -387,7 +253,7 @@ __global__ void __launch_bounds__(kAT, 1) attend_kernel(const __grid_constant__ 
                 pos[m][h] = 0x7FFFFFFF;  // rows past the unit: their results are not kept
                 if (row < seg.nrows) {
                     const int tok = (seg.row0 + row) / a.G, r = tok / a.T;
-                    pos[m][h] = lens[r] - a.T + tok - r * a.T;
+                    pos[m][h] = sh.lens[r] - a.T + tok - r * a.T;
                 }
                 min_pos = min(min_pos, pos[m][h]);
             }
@@ -396,7 +262,6 @@ __global__ void __launch_bounds__(kAT, 1) attend_kernel(const __grid_constant__ 
 
         float o[MT][NT][4];
         float m_run[MT][2], l_run[MT][2];
-        float ref = 0.0f, inv_ref = 0.0f;  // e4m3: power of two above the value scales seen; 2^15 / ref
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             m_run[m][0] = m_run[m][1] = kNegInf;
@@ -410,7 +275,7 @@ __global__ void __launch_bounds__(kAT, 1) attend_kernel(const __grid_constant__ 
             const int i = i0 + k, s = i % S;
             mbar_wait(&full[s], uint32_t(i / S) & 1u, &ctl, a.err);
             const uint32_t kb = ring + uint32_t(s) * uint32_t(C::kStage), vb = kb + uint32_t(C::kTileBytes);
-            const int key0 = (seg.tile + k) * kAttTile + kw;  // this warp's first key
+            const int key0 = seg.key(k) + kw;  // this warp's first key
             const bool whole = key0 >= seg.key_begin && key0 + 16 <= seg.key_end && key0 + 15 <= min_pos;
 
             // ---- scores of 16 keys
@@ -458,6 +323,7 @@ __global__ void __launch_bounds__(kAT, 1) attend_kernel(const __grid_constant__ 
                 }
             }
             float2 kscale[2], vscale[2];
+            float lift = 0.0f;  // e4m3: e - 7 for value scales below 2^e
             if (Q8) {
                 const uint32_t sb = kb + uint32_t(C::kScaleOff) + uint32_t(kw + 2 * q4) * 4u;
                 float top = 0.0f;
@@ -473,19 +339,7 @@ __global__ void __launch_bounds__(kAT, 1) attend_kernel(const __grid_constant__ 
                 }
                 top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-                top = fmaxf(top, 1e-30f);
-                if (!(top <= ref)) {  // uniform over the warp
-                    const float next = __uint_as_float(min((__float_as_uint(top) & 0x7F800000u) + 0x00800000u, 0x7E800000u));
-                    const float down = ref / next;
-#pragma unroll
-                    for (int m = 0; m < MT; ++m)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) o[m][n][c] *= down;
-                    ref = next;
-                    inv_ref = 32768.0f / next;
-                }
+                lift = exp_above(top) - 7.0f;
             }
             // ---- mask, running maximum, weights
             uint32_t pf[MT][4];
@@ -510,7 +364,7 @@ __global__ void __launch_bounds__(kAT, 1) attend_kernel(const __grid_constant__ 
                         }
                     mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
                     mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-                    const float mn = fmaxf(m_run[m][h], mx);
+                    const float mn = fmaxf(m_run[m][h], mx + lift);
                     const float mu = mn == kNegInf ? 0.0f : mn;  // a row without keys so far
                     alpha[m][h] = ex2(m_run[m][h] - mu);
                     moved = moved || m_run[m][h] != mn;
@@ -524,7 +378,7 @@ __global__ void __launch_bounds__(kAT, 1) attend_kernel(const __grid_constant__ 
                             sum += p;
                             // a masked weight is zero whatever the key's scale holds
                             pw[m][n][2 * h + c] =
-                                !Q8 ? p : p == 0.0f ? 0.0f : p * ((c ? vscale[n].y : vscale[n].x) * inv_ref);
+                                !Q8 ? p : p == 0.0f ? 0.0f : p * (c ? vscale[n].y : vscale[n].x);
                         }
                     l_run[m][h] = l_run[m][h] * alpha[m][h] + sum;
                 }
@@ -683,7 +537,7 @@ __global__ void __launch_bounds__(kAT, 1) attend_kernel(const __grid_constant__ 
 #pragma unroll
             for (int w = 0; w < kCW; ++w) l += rowstat[w * RT + row].y * ex2(rowstat[w * RT + row].x - mu);
             row_m[row] = mu;
-            if (row < seg.nrows) a.part_ml[size_t(slot) * RT + row] = make_float2(m, l);
+            if (row < seg.nrows) ln.part_ml[size_t(slot) * RT + row] = make_float2(m, l);
         }
         named_sync(kCT);
 #pragma unroll
@@ -691,7 +545,7 @@ __global__ void __launch_bounds__(kAT, 1) attend_kernel(const __grid_constant__ 
             float f[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                f[h] = ex2(m_run[m][h] - row_m[16 * m + 8 * h + g8]) * (Q8 ? ref * (1.0f / 32768.0f) : 1.0f);
+                f[h] = ex2(m_run[m][h] - row_m[16 * m + 8 * h + g8]);
 #pragma unroll
             for (int c0 = 0; c0 < NT / 4; ++c0) {
                 // 32 channels of 16 rows per step: this warp's registers (n, c)
@@ -709,7 +563,7 @@ __global__ void __launch_bounds__(kAT, 1) attend_kernel(const __grid_constant__ 
 #pragma unroll
                     for (int w = 0; w < kCW; ++w) x += join[(w * 16 + row) * kJoinPitch + col];
                     const int d = out_channel<D, Q8>(4 * c0 + (col >> 3), (col >> 1) & 3, col & 1);
-                    if (16 * m + row < seg.nrows) a.part_o[(size_t(slot) * RT + 16 * m + row) * D + d] = x;
+                    if (16 * m + row < seg.nrows) ln.part_o[(size_t(slot) * RT + 16 * m + row) * D + d] = x;
                 }
                 named_sync(kCT);
             }
@@ -718,12 +572,10 @@ __global__ void __launch_bounds__(kAT, 1) attend_kernel(const __grid_constant__ 
     }
 }
 
-// One warp per output row: its segments under the prefix and of its request,
-// each [first CTA, last CTA], added up in that order.
+// One warp per output row: the results of its segments in every line, under
+// the prefix and of its request, each from the first CTA to the last.
 template <int D>
-__global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ AttendJoinArgs ja) {
-    const AttendArgs &a = ja.a;
-    const int grid = ja.grid;
+__global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ AttendArgs a) {
     constexpr int V = D / 32;
     const int lane = threadIdx.x & 31;
     pdl_launch_dependents();
@@ -731,49 +583,59 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     const int64_t i = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
     if (i >= int64_t(a.rows) * a.heads) return;
     const int tok = int(i / (a.G * a.heads)), hq = int(i - int64_t(tok) * (a.G * a.heads));
-    const int head = hq / a.G, rho = tok * a.G + (hq - head * a.G), r = tok / a.T;
-    const int np = a.plan[0];
-    const int c_r = a.plan[1 + r], n_r = a.plan[2 + r] - c_r;
-    const int per_head = a.pu * np + a.su * a.plan[1 + a.R], total = per_head * a.heads;
-    const int units = a.pu + a.R * a.su;
-    const int p = rho / a.rt, in_req = rho - r * a.T * a.G, s = in_req / a.rt;
-    int first[2], n[2], row[2];  // slots of the two units (consecutive), and the row in them
-    first[0] = first[1] = n[0] = n[1] = 0;
-    row[0] = rho - p * a.rt;
-    row[1] = in_req - s * a.rt;
-    if (a.pu && np) {
-        const int b = head * per_head + p * np, c = att_owner(total, grid, b);
-        first[0] = head * units + p + c;
-        n[0] = att_owner(total, grid, b + np - 1) - c + 1;
-    }
-    if (n_r) {
-        const int b = head * per_head + a.pu * np + a.su * c_r + s * n_r, c = att_owner(total, grid, b);
-        first[1] = head * units + a.pu + r * a.su + s + c;
-        n[1] = att_owner(total, grid, b + n_r - 1) - c + 1;
-    }
-    const int all = n[0] + n[1];
-    const auto at = [&](int k) {
-        return k < n[0] ? size_t(first[0] + k) * a.rt + row[0] : size_t(first[1] + k - n[0]) * a.rt + row[1];
-    };
-    float m = kNegInf;
-    for (int k = lane; k < all; k += 32) m = fmaxf(m, a.part_ml[at(k)].x);
+    const int head = hq / a.G, rho = tok * a.G + (hq - head * a.G), r = tok / a.T, in_req = rho - r * a.T * a.G;
+    // running maximum of the references, sum and output so far
+    float m = kNegInf, l = 0.0f, acc[V] = {};
+    const auto add = [&](const AttendLine &ln, int first, int n, int row) {
+        // entries (slot, half) first .. : reference and sum of up to 32 at once, a lane each
+        for (int k0 = 0; k0 < n * ln.halves; k0 += 32) {
+            const int left = min(32, n * ln.halves - k0);
+            const size_t e0 = size_t(first) * ln.halves + k0;
+            float2 ml = make_float2(kNegInf, 0.0f);
+            if (lane < left) ml = ln.part_ml[(e0 + lane) * ln.rt + row];
+            float top = ml.x;
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    const float mu = m == kNegInf ? 0.0f : m;
-    float l = 0.0f, acc[V] = {};
-#pragma unroll 4
-    for (int k = 0; k < all; ++k) {
-        const size_t x = at(k);
-        const float2 ml = a.part_ml[x];
-        const float f = ex2(ml.x - mu);
-        l += ml.y * f;
-        const float *src = a.part_o + x * D + V * lane;
-        if (V == 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(src);
-            acc[0] += v.x * f, acc[1] += v.y * f, acc[V - 2] += v.z * f, acc[V - 1] += v.w * f;
-        } else {
-            const float2 v = *reinterpret_cast<const float2 *>(src);
-            acc[0] += v.x * f, acc[1] += v.y * f;
+            for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            const float mn = fmaxf(m, top), mu = mn == kNegInf ? 0.0f : mn;
+            const float down = ex2(m - mu);
+            l *= down;
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[v] *= down;
+            m = mn;
+            const float f = ex2(ml.x - mu), lf = ml.y * f;
+#pragma unroll 8
+            for (int k = 0; k < left; ++k) {
+                const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
+                const float lk = __shfl_sync(0xFFFFFFFFu, lf, k);
+                l += lk;
+                // (an entry without keys may hold anything)
+                if (fk == 0.0f && lk == 0.0f) continue;
+                const float *src = ln.part_o + ((e0 + k) * ln.rt + row) * D + V * lane;
+                if (V == 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(src);
+                    acc[0] += x.x * fk, acc[1] += x.y * fk, acc[V - 2] += x.z * fk, acc[V - 1] += x.w * fk;
+                } else {
+                    const float2 x = *reinterpret_cast<const float2 *>(src);
+                    acc[0] += x.x * fk, acc[1] += x.y * fk;
+                }
+            }
+        }
+    };
+    for (int q = 0; q < kLines; ++q) {
+        const AttendLine &ln = a.line[q];
+        if (!ln.grid) continue;
+        const int np = ln.plan[0], c_r = ln.plan[1 + r], n_r = ln.plan[2 + r] - c_r;
+        const int per_head = ln.pu * np + ln.su * ln.plan[1 + a.R], total = per_head * a.heads;
+        const int units = ln.pu + a.R * ln.su;
+        if (ln.pu && np) {
+            const int p = rho / ln.rt, b = head * per_head + p * np, c = att_owner(total, ln.grid, b);
+            add(ln, head * units + p + c, att_owner(total, ln.grid, b + np - 1) - c + 1, rho - p * ln.rt);
+        }
+        if (ln.su && n_r) {
+            const int s = in_req / ln.rt, b = head * per_head + ln.pu * np + ln.su * c_r + s * n_r;
+            const int c = att_owner(total, ln.grid, b);
+            add(ln, head * units + ln.pu + r * ln.su + s + c, att_owner(total, ln.grid, b + n_r - 1) - c + 1,
+                in_req - s * ln.rt);
         }
     }
     const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);  // no key: zeros
@@ -784,7 +646,8 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     else
         *reinterpret_cast<uint32_t *>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
     if (a.lse && lane == 0)
-        a.lse[int64_t(tok) * (a.G * a.heads) + hq] = l == 0.0f ? kNegInf : (mu + log2f(l)) * 0.6931471805599453f;
+        a.lse[int64_t(tok) * (a.G * a.heads) + hq] =
+            l == 0.0f ? kNegInf : ((m == kNegInf ? 0.0f : m) + log2f(l)) * 0.6931471805599453f;
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -820,7 +683,7 @@ int cache_map(CUtensorMap *m, void *base, int64_t rows, int dim, bool q8, int bo
 
 // The dynamic shared-memory limit is raised once per device and variant.
 template <int D, bool Q8, int MT>
-int run(const AttendArgs &a, int grid, void *stream) {
+int run(const AttendArgs &a, void *stream) {
     using C = ACfg<D, Q8, MT>;
     static std::atomic<uint64_t> ready[4];
     int dev = 0;
@@ -832,7 +695,7 @@ int run(const AttendArgs &a, int grid, void *stream) {
             return W12_ERR_CUDA;
         ready[dev >> 6].fetch_or(bit, std::memory_order_relaxed);
     }
-    return launch_step(attend_kernel<D, Q8, MT>, grid, kAT, C::kSmem, 1, stream, a);
+    return launch_step(attend_kernel<D, Q8, MT>, a.line[a.self].grid, kAT, C::kSmem, 1, stream, a);
 }
 
 }  // namespace
@@ -846,21 +709,19 @@ int attend_make_maps(AttendArgs &a, const w12_kv *kv) {
     return st != W12_OK ? st : cache_map(&a.mv, kv->v, rows, kv->head_dim, q8, br);
 }
 
-int launch_attend(const AttendArgs &a, int dim, int kv, int grid, void *stream) {
-    const bool q8 = kv == W12_KV_E4M3, two = a.rt > 16;
-    int st;
+int launch_attend_rest(const AttendArgs &a, int dim, int kv, void *stream) {
+    const bool q8 = kv == W12_KV_E4M3, two = a.line[kLineRest].rt > 16;
     if (dim == 128)
-        st = q8 ? (two ? run<128, true, 2>(a, grid, stream) : run<128, true, 1>(a, grid, stream))
-                : (two ? run<128, false, 2>(a, grid, stream) : run<128, false, 1>(a, grid, stream));
-    else
-        st = q8 ? (two ? run<64, true, 2>(a, grid, stream) : run<64, true, 1>(a, grid, stream))
-                : (two ? run<64, false, 2>(a, grid, stream) : run<64, false, 1>(a, grid, stream));
-    if (st != W12_OK) return st;
-    const int64_t rows = int64_t(a.rows) * a.heads;
-    AttendJoinArgs j{a, grid};
-    const int blocks = int((rows + 7) / 8);
-    return dim == 128 ? launch_step(attend_join_kernel<128>, blocks, 256, 0, 1, stream, j)
-                      : launch_step(attend_join_kernel<64>, blocks, 256, 0, 1, stream, j);
+        return q8 ? (two ? run<128, true, 2>(a, stream) : run<128, true, 1>(a, stream))
+                  : (two ? run<128, false, 2>(a, stream) : run<128, false, 1>(a, stream));
+    return q8 ? (two ? run<64, true, 2>(a, stream) : run<64, true, 1>(a, stream))
+              : (two ? run<64, false, 2>(a, stream) : run<64, false, 1>(a, stream));
+}
+
+int launch_attend_join(const AttendArgs &a, int dim, void *stream) {
+    const int blocks = int((int64_t(a.rows) * a.heads + 7) / 8);
+    return dim == 128 ? launch_step(attend_join_kernel<128>, blocks, 256, 0, 1, stream, a)
+                      : launch_step(attend_join_kernel<64>, blocks, 256, 0, 1, stream, a);
 }
 
 }  // namespace w12

@@ -64,8 +64,26 @@ struct ReadArgs {
 };
 int launch_read(const ReadArgs &a, int head_dim, int kv_dtype, void *stream);
 
-// Attention (kernels_attend.cu).  Work split: "attend_device.cuh".
+// Attention (kernels_attend.cu, kernels_attend_tc.cu); the work split is
+// described in attend_device.cuh.
 constexpr int kAttTile = 64;  // keys per tile
+
+// One launch's share of the work: units, their tiles on a line, the CTAs
+// that cut it, and where the segments' results go.
+struct AttendLine {
+    int32_t pu, su;   // units per head: row blocks of all requests under the prefix, row blocks per request
+    int32_t rt;       // query rows per unit
+    int32_t halves;   // results per segment (2: its tiles in two alternating halves)
+    int32_t grid;     // CTAs; 0: the line is not used
+    int32_t *plan;    // tiles of a prefix unit, then the R + 1 cumulative tile counts of the requests
+    float *part_o;    // [slots][halves][rt][head_dim]
+    float2 *part_ml;  // [slots][halves][rt]: reference exponent (log2 units) and sum
+};
+
+// Lines: the tensor-memory kernel on the prefix's whole tiles, the same on
+// the requests' whole tiles, the register kernel on the rest.
+enum { kLinePrefix = 0, kLineRequests = 1, kLineRest = 2, kLines = 3 };
+
 struct AttendArgs {
     CUtensorMap mk, mv;  // the cache as rows of head_dim channels
     const uint16_t *q;
@@ -77,18 +95,17 @@ struct AttendArgs {
     int64_t n_pages, table_cols;
     int32_t R, T, G, heads, page, page_log2;
     int32_t rows;      // R * T * G query rows per key head
-    int32_t rt;        // query rows per unit
-    int32_t pu, su;    // units per head: row tiles of all requests under the prefix, row tiles per request
     int32_t prefix, max_len;
+    int32_t self;      // the line of this launch
     float scale_log2;  // scale * log2(e)
-    float *part_o;     // [slots][rt][head_dim]
-    float2 *part_ml;   // [slots][rt]: running maximum (log2 units) and sum
-    int32_t *plan;     // prefix tiles per unit, then the R + 1 cumulative tile counts of the requests
     int *err;
     uint64_t wait_ns;
+    AttendLine line[kLines];
 };
 int attend_make_maps(AttendArgs &a, const w12_kv *kv);
-int launch_attend(const AttendArgs &a, int head_dim, int kv_dtype, int grid, void *stream);
+int launch_attend_rest(const AttendArgs &a, int head_dim, int kv_dtype, void *stream);
+int launch_attend_tc(const AttendArgs &a, int head_dim, int kv_dtype, void *stream);
+int launch_attend_join(const AttendArgs &a, int head_dim, void *stream);
 
 struct SampleArgs {
     const void *logits;
