@@ -554,10 +554,12 @@ size_t w12_attend_workspace_size(const w12_kv *kv, int64_t R, int64_t T, int q_h
  *   lse_dev: NULL, or fp32 [R * T][q_heads]: log(sum_j exp(scale q . k_j)).
  *   max_len: no kv_len is above it (a longer one records W12_ERR_DEVICE and
  *     is cut there); it only bounds the work.
- *   prefix_len: 0, or the number of leading keys that ALL requests share:
- *     they are read once for the whole batch, through request 0's table (so
- *     its row must name the prefix's pages); keys from prefix_len on are each
- *     request's own, through its own row.  Not tied to page boundaries.
+ *   prefix_len: 0, or the number of leading keys that ALL requests share
+ *     (the same rows of the cache, or copies): as far as they fill tiles of
+ *     128 keys that every token sees, they are read once for the whole
+ *     batch, through request 0's table.  Every request's row of the table
+ *     names all of its pages, the prefix's among them.  Not tied to page
+ *     boundaries.
  * A token that sees no key (a padding token, kv_len = 0) gives zeros and
  * lse = -infinity.  Keys past a token's position, rows past kv_len and pages
  * not named by the table never reach a result, whatever they hold.  Scores,

@@ -54,14 +54,16 @@ struct AttendPlan {
     int32_t rows;
     struct Line {
         int32_t pu, su, rt, halves, grid;
-        size_t off_plan, off_ml, off_o;
+        size_t off_ml, off_o;
     } line[kLines];
-    size_t total;
+    size_t off_arrived, off_plan, total;
+    bool join;
 };
 
-// Rows per key head from which the tensor-memory kernel takes a part's whole
-// tiles: its tile has 128 rows whatever their number, the register kernel
-// streams the keys once per 32 rows.
+// Rows per key head and request from which the tensor-memory kernel takes a
+// request's whole tiles: its tile has 128 rows whatever their number, the
+// register kernel streams the keys once per 32 rows.  (The prefix of two or
+// more requests always goes there: it is what reads it once.)
 constexpr int64_t kTcRows = 33;
 
 // Work split and workspace layout of an attention call.
@@ -74,40 +76,41 @@ int plan_attend(const w12_kv *kv, int64_t R, int64_t T, int q_heads, int64_t max
     if (max_len < 0 || max_len >= kLim31 || prefix < 0 || prefix >= kLim31) return W12_ERR_SHAPE;
     const int64_t tg = T * (q_heads / kv->heads), rows = R * tg;
     if (rows >= kLim31 / 2) return W12_ERR_SHAPE;
-    const int64_t most = prefix > 0 ? rows : tg;
     p->rows = int32_t(rows);
     const auto blocks = [](int64_t n, int64_t rt) { return int32_t((n + rt - 1) / rt); };
     auto *l = p->line;
     for (int i = 0; i < kLines; ++i) l[i] = {};
-    const int64_t shared = (std::min(prefix, max_len) + kAttTile - 1) / kAttTile, own = max_len / kAttTile + 1;
-    // whole tiles: at most these many of the prefix and of a request
-    const bool tc_p = rows >= kTcRows && std::min(prefix, max_len) >= kAttTile;
-    const bool tc_r = tg >= kTcRows && max_len - T + 1 >= (prefix + kAttTile - 1) / kAttTile * kAttTile + kAttTile;
-    if (tc_p) {
+    const int64_t shared = std::min(prefix, max_len) / kAttTcTile;  // at most these many whole tiles of the prefix
+    if (R > 1 && shared > 0) {
         l[kLinePrefix].rt = rows <= 128 ? 128 : 256;
         l[kLinePrefix].pu = blocks(rows, l[kLinePrefix].rt);
     }
-    if (tc_r) {
+    if (tg >= kTcRows && max_len - T + 1 >= kAttTcTile) {
         l[kLineRequests].rt = tg <= 128 ? 128 : 256;
         l[kLineRequests].su = blocks(tg, l[kLineRequests].rt);
     }
-    l[kLineRest].rt = most <= 16 ? 16 : 32;
-    l[kLineRest].pu = prefix > 0 ? blocks(rows, l[kLineRest].rt) : 0;
+    l[kLineRest].rt = tg <= 8 ? 8 : tg <= 16 ? 16 : 32;
     l[kLineRest].su = blocks(tg, l[kLineRest].rt);
     int sms = 0;
     if (current_sms(&sms) != W12_OK) return W12_ERR_CUDA;
     size_t off = kWsHeader;
+    p->off_arrived = off;
+    off += round256(uint64_t(kv->heads) * R * l[kLineRest].su * 4u);
+    p->off_plan = off;
+    off += round256(uint64_t(2 * R + 3) * 4u);
+    p->join = l[kLinePrefix].pu + l[kLineRequests].su > 0;
     for (int i = 0; i < kLines; ++i) {
         auto &n = l[i];
         if (n.pu + n.su == 0) continue;
         n.halves = i != kLineRest && n.rt == 128 ? 2 : 1;
+        const int64_t own = max_len / kAttTile + 1;  // at most these many tiles of a request
         if (own > kLim31 / (R * std::max(n.su, 1)) || shared > kLim31 / std::max(n.pu, 1)) return W12_ERR_SHAPE;
         const int64_t tiles = own * R * n.su + shared * n.pu;
         if (tiles >= kLim31 / kv->heads) return W12_ERR_SHAPE;
-        n.grid = int(std::max<int64_t>(1, std::min<int64_t>(sms, tiles * kv->heads)));
+        // (the register kernel has two workers per CTA)
+        const int64_t per = i == kLineRest ? 2 : 1;
+        n.grid = int(per * std::max<int64_t>(1, std::min<int64_t>(sms, (tiles * kv->heads + per - 1) / per)));
         const uint64_t rowsets = uint64_t(kv->heads * (n.pu + R * n.su) + n.grid) * n.halves * n.rt;
-        n.off_plan = off;
-        off += round256(uint64_t(R + 2) * 4u);
         n.off_ml = off;
         off += round256(rowsets * 8u);
         n.off_o = off;
@@ -215,10 +218,13 @@ extern "C" int w12_attend(const w12_kv *kv, const uint16_t *q, int64_t q_stride,
     a.prefix = int32_t(prefix_len), a.max_len = int32_t(max_len);
     a.scale_log2 = scale * 1.4426950408889634f;
     a.err = reinterpret_cast<int *>(w);
+    a.arrived = reinterpret_cast<uint32_t *>(w + p.off_arrived);
+    a.plan = reinterpret_cast<int32_t *>(w + p.off_plan);
+    a.join = p.join;
     for (int i = 0; i < kLines; ++i) {
         const auto &n = p.line[i];
-        a.line[i] = {n.pu, n.su, n.rt, n.halves, n.grid, reinterpret_cast<int32_t *>(w + n.off_plan),
-                     reinterpret_cast<float *>(w + n.off_o), reinterpret_cast<float2 *>(w + n.off_ml)};
+        a.line[i] = {n.pu, n.su, n.rt, n.halves, n.grid, reinterpret_cast<float *>(w + n.off_o),
+                     reinterpret_cast<float2 *>(w + n.off_ml)};
     }
     for (int i = 0; i < kLines; ++i) {
         a.self = i;
@@ -227,7 +233,7 @@ extern "C" int w12_attend(const w12_kv *kv, const uint16_t *q, int64_t q_stride,
                             : launch_attend_tc(a, kv->head_dim, kv->dtype, stream);
         if (st != W12_OK) return st;
     }
-    return launch_attend_join(a, kv->head_dim, stream);
+    return p.join ? launch_attend_join(a, kv->head_dim, stream) : W12_OK;
 }
 
 extern "C" size_t w12_sample_workspace_size(int64_t R, int64_t T, int64_t V) {

@@ -2,26 +2,30 @@
 // what its kernels share.
 //
 // Query rows of one key head: row rho = token * G + g, token = request * T +
-// i, G = query heads per key head; a request's rows are consecutive.  Keys
-// come in tiles of kAttTile on one grid.  A unit is a block of rt query rows
-// of one head against one stretch of keys:
+// i, G = query heads per key head; a request's rows are consecutive.  A unit
+// is a block of rt query rows of one head against one stretch of keys:
 //  - prefix unit p < pu: rows [p rt, (p + 1) rt) of ALL requests against the
-//    keys [0, prefix), read once through request 0's table;
+//    keys of the prefix, read once through request 0's table;
 //  - request unit (r, s), s < su: rows s rt .. of request r against its own
-//    keys [prefix, kv_len[r]).
-// Up to three launches ("lines") share the tiles.  Where a part has enough
-// rows, its whole tiles (every key of the tile seen by every row) go to the
-// tensor-memory kernel, which then needs no masks; what is left -- the tile
-// that the prefix ends in, the tiles of the draft block and of a ragged end,
-// parts with few rows -- goes to the register kernel.
-// Within a line, units of a head are ordered prefix first, then by r and s;
-// heads in order.  All tiles of all units form one row, cut into equal
-// pieces, one per CTA: every CTA streams the same number of tiles whatever
-// the lengths are.  A CTA's share of a unit is a segment; it leaves its
-// (m, l, O) -- reference exponent, sum and unnormalised output -- in slot
-// (unit + CTA), which no other segment has: from one segment to the next
-// either the unit or the CTA goes up, never down.  The join kernel adds up
-// each row's segments in a fixed order, so results do not depend on timing.
+//    keys.
+// Up to three launches ("lines") share the keys.  Tiles of 128 keys that
+// every row of a part sees go to the tensor-memory kernel, which needs no
+// masks: the prefix's first W tiles, and, for requests with many rows, their
+// tiles from W to the last that their first new token sees whole.  The rest
+// -- what follows, and requests with few rows from W on -- goes to the
+// register kernel in tiles of 64 keys.  (The part of the prefix past W * 128
+// keys is thus read by each request through its own table.)
+// Within a line, units of a head are ordered by p, or by r and s; heads in
+// order.  All tiles of all units form one row, cut into equal pieces, one per
+// worker (a CTA; in the register kernel each half of a CTA): every worker
+// streams the same number of tiles whatever the lengths are.  A worker's
+// share of a unit is a segment; it leaves its (m, l, O) -- reference exponent,
+// sum and unnormalised output -- in slot (unit + worker), which no other
+// segment has: from one segment to the next either the unit or the worker
+// goes up, never down.  Where only the rest line has results, the worker that
+// finishes a unit's last segment adds them up (a unit of one segment is
+// written at once); else a join kernel does.  Both in a fixed order, so the
+// outputs do not depend on timing.
 #pragma once
 
 #include "async_common.cuh"
@@ -32,21 +36,21 @@ namespace w12 {
 
 constexpr int kAttMaxR = W12_ATTEND_MAX_R;
 
+// A position on the line: a unit, its first key from here on, its tiles left.
+struct AttSeg {
+    int head, req, block;  // block: of the unit's rows in its request (prefix: of all rows)
+    int unit;              // global index
+    int row0, nrows;       // query rows
+    int key, left;
+    int key_end;
+};
+
 // Shared memory of the plan that every CTA makes for itself.
 struct AttShared {
     int lens[kAttMaxR];
     int cum[kAttMaxR + 1];  // tiles of the requests before r, one row block each
-    int shortest, longest;
-};
-
-struct AttSeg {
-    int head, unit;         // unit: global index
-    int req;                // table row
-    int row0, nrows;        // query rows
-    int tile, left;         // key tile, tiles of the unit from here on
-    int skip_at, skip;      // after skip_at tiles the unit goes on `skip` tiles later
-    int key_begin, key_end;
-    __device__ __forceinline__ int key(int k) const { return (tile + k + (k >= skip_at ? skip : 0)) * kAttTile; }
+    int w;
+    AttSeg first[2];        // the CTA's workers' first positions
 };
 
 __device__ __forceinline__ int att_len(const AttendArgs &a, int n) {
@@ -55,34 +59,24 @@ __device__ __forceinline__ int att_len(const AttendArgs &a, int n) {
     return n < 0 ? 0 : n > cap ? cap : n;
 }
 
-// Whole tiles of the prefix (the tensor-memory kernel's), and the end of the
-// prefix's keys.
+// W: the prefix's tiles of 128 keys that are read once for all requests.
 __device__ __forceinline__ int att_prefix_whole(const AttendArgs &a, int shortest) {
-    return a.line[kLinePrefix].grid ? min(a.prefix, max(shortest - a.T + 1, 0)) / kAttTile : 0;
+    return a.line[kLinePrefix].grid ? min(a.prefix, max(shortest - a.T + 1, 0)) / kAttTcTile : 0;
 }
-__device__ __forceinline__ int att_prefix_end(const AttendArgs &a, int longest) { return min(a.prefix, longest); }
-
-// The tensor-memory kernel's tiles [c0, c1) of a request of len keys.
-__device__ __forceinline__ void att_req_whole(const AttendArgs &a, int len, int *c0, int *c1) {
-    *c0 = (a.prefix + kAttTile - 1) / kAttTile;
-    *c1 = a.line[kLineRequests].grid ? max(*c0, max(len - a.T + 1, 0) / kAttTile) : *c0;
+// The end of a request's tiles of 128 keys that the tensor-memory kernel takes.
+__device__ __forceinline__ int att_req_whole(const AttendArgs &a, int w, int len) {
+    return a.line[kLineRequests].grid ? max(w, max(len - a.T + 1, 0) / kAttTcTile) : w;
 }
-
-// This line's tiles of a prefix unit and of a request.
-__device__ __forceinline__ int att_prefix_tiles(const AttendArgs &a, int shortest, int longest) {
-    if (!a.line[a.self].pu) return 0;
-    const int w = att_prefix_whole(a, shortest);
-    return a.self == kLineRest ? (att_prefix_end(a, longest) + kAttTile - 1) / kAttTile - w : w;
-}
-__device__ __forceinline__ int att_req_tiles(const AttendArgs &a, int len) {
-    if (!a.line[a.self].su) return 0;
-    int c0, c1;
-    att_req_whole(a, len, &c0, &c1);
-    if (a.self != kLineRest) return c1 - c0;
-    return len > a.prefix ? (len + kAttTile - 1) / kAttTile - a.prefix / kAttTile - (c1 - c0) : 0;
+// This line's tiles of a request of len keys.
+__device__ __forceinline__ int att_req_tiles(const AttendArgs &a, int w, int len) {
+    if (a.self == kLinePrefix) return 0;
+    const int c1 = att_req_whole(a, w, len);
+    if (a.self == kLineRequests) return c1 - w;
+    return max((len + kAttTile - 1) / kAttTile - c1 * (kAttTcTile / kAttTile), 1);
 }
 
-// CTA c's tiles begin at att_begin(total, grid, c); the CTA that has tile t.
+// Worker c's tiles begin at att_begin(total, grid, c); the worker that has
+// tile t.
 __device__ __forceinline__ int att_begin(int total, int grid, int c) {
     const int per = total / grid, rem = total % grid;
     return c * per + min(c, rem);
@@ -93,33 +87,91 @@ __device__ __forceinline__ int att_owner(int total, int grid, int t) {
 }
 
 struct AttPlan {
-    int np;        // tiles of a prefix unit
+    int w;         // the prefix's shared tiles
+    int np;        // tiles of a prefix unit of this line
     int per_head;  // tiles of a head
-    int t0, t1;    // this CTA's tiles
+    int t0, t1;    // this worker's tiles
 };
 
+// Fills in what follows from (head, req, block) for the unit's tile k.
+__device__ __forceinline__ void att_unit_at(const AttendArgs &a, const AttPlan &p, const AttShared &sh, AttSeg &s, int k) {
+    const AttendLine &ln = a.line[a.self];
+    if (a.self == kLinePrefix) {
+        s.unit = s.head * ln.pu + s.block;
+        s.row0 = s.block * ln.rt;
+        s.nrows = min(ln.rt, a.rows - s.row0);
+        s.left = p.np - k;
+        s.key = k * kAttTcTile;
+        s.key_end = p.w * kAttTcTile;
+        return;
+    }
+    const int tg = a.T * a.G;
+    s.unit = (s.head * a.R + s.req) * ln.su + s.block;
+    s.row0 = s.req * tg + s.block * ln.rt;
+    s.nrows = min(ln.rt, tg - s.block * ln.rt);
+    s.left = sh.cum[s.req + 1] - sh.cum[s.req] - k;
+    s.key_end = sh.lens[s.req];
+    s.key = a.self == kLineRest ? att_req_whole(a, p.w, s.key_end) * kAttTcTile + k * kAttTile : (p.w + k) * kAttTcTile;
+}
+
+// The position of tile t of the line.
+__device__ __forceinline__ AttSeg att_locate(const AttendArgs &a, const AttPlan &p, const AttShared &sh, int t) {
+    const AttendLine &ln = a.line[a.self];
+    AttSeg s;
+    s.head = t / p.per_head;
+    int w = t - s.head * p.per_head, n = p.np;
+    s.req = 0;
+    if (a.self != kLinePrefix) {
+        int lo = 0, hi = a.R;  // the last request with cum <= w / su
+        const int x = w / ln.su;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (sh.cum[mid] <= x) lo = mid; else hi = mid;
+        }
+        s.req = lo;
+        n = sh.cum[lo + 1] - sh.cum[lo];
+        w -= sh.cum[lo] * ln.su;
+    }
+    s.block = w / n;
+    att_unit_at(a, p, sh, s, w - s.block * n);
+    return s;
+}
+
+// The start of the next unit that has tiles (there is one).
+__device__ __forceinline__ void att_next(const AttendArgs &a, const AttPlan &p, const AttShared &sh, AttSeg &s) {
+    const AttendLine &ln = a.line[a.self];
+    const bool prefix = a.self == kLinePrefix;
+    if (++s.block == (prefix ? ln.pu : ln.su)) {
+        s.block = 0;
+        do {
+            if (prefix || ++s.req == a.R) s.req = 0, ++s.head;
+        } while (!prefix && sh.cum[s.req + 1] == sh.cum[s.req]);
+    }
+    att_unit_at(a, p, sh, s, 0);
+}
+
 // Lengths and cumulative tile counts into shared memory (all threads of the
-// CTA); CTA 0 also leaves them for the join kernel.
-__device__ __forceinline__ AttPlan att_plan(const AttendArgs &a, AttShared &sh, int threads) {
+// CTA).
+__device__ __forceinline__ AttPlan att_plan(const AttendArgs &a, AttShared &sh, int workers, int worker) {
     const int lane = threadIdx.x & 31;
     const AttendLine &ln = a.line[a.self];
-    for (int r = threadIdx.x; r < a.R; r += threads) {
-        const int n0 = a.kv_len[r], n = att_len(a, n0);
-        if (n0 > n && blockIdx.x == 0) atomicCAS(a.err, 0, W12_ERR_DEVICE);
-        sh.lens[r] = n;
-    }
-    __syncthreads();
     if (threadIdx.x < 32) {
-        int sum = 0, longest = 0, shortest = 0x7FFFFFFF;
+        int longest = 0, shortest = 0x7FFFFFFF;
+        for (int r = lane; r < a.R; r += 32) {
+            const int n0 = a.kv_len[r], n = att_len(a, n0);
+            if (n0 > n && blockIdx.x == 0) atomicCAS(a.err, 0, W12_ERR_DEVICE);
+            sh.lens[r] = n;
+            longest = max(longest, n);
+            shortest = min(shortest, n);
+        }
+        shortest = __reduce_min_sync(0xFFFFFFFFu, shortest);
+        const int w = att_prefix_whole(a, shortest);
+        __syncwarp();
+        int sum = 0, sum_q = 0;
         for (int r0 = 0; r0 < a.R; r0 += 32) {
             const int r = r0 + lane;
-            int x = 0;
-            if (r < a.R) {
-                const int n = sh.lens[r];
-                longest = max(longest, n);
-                shortest = min(shortest, n);
-                x = att_req_tiles(a, n);
-            }
+            const int n = r < a.R ? sh.lens[r] : 0;
+            int x = r < a.R ? att_req_tiles(a, w, n) : 0;
             const int y = x;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -128,76 +180,47 @@ __device__ __forceinline__ AttPlan att_plan(const AttendArgs &a, AttShared &sh, 
             }
             if (r < a.R) sh.cum[r] = sum + x - y;
             sum += __shfl_sync(0xFFFFFFFFu, x, 31);
+            if (a.join && a.self == kLineRest && blockIdx.x == 0) {  // for the join kernel
+                int q = r < a.R ? att_req_whole(a, w, n) - w : 0;
+                const int p = q;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int z = __shfl_up_sync(0xFFFFFFFFu, q, o);
+                    if (lane >= o) q += z;
+                }
+                if (r < a.R) {
+                    a.plan[1 + r] = sum_q + q - p;
+                    a.plan[a.R + 2 + r] = sh.cum[r];
+                }
+                sum_q += __shfl_sync(0xFFFFFFFFu, q, 31);
+            }
         }
-        longest = __reduce_max_sync(0xFFFFFFFFu, longest);
-        shortest = __reduce_min_sync(0xFFFFFFFFu, shortest);
         if (lane == 0) {
             sh.cum[a.R] = sum;
-            sh.longest = longest;
-            sh.shortest = shortest;
+            sh.w = w;
+            if (a.join && a.self == kLineRest && blockIdx.x == 0) {
+                a.plan[0] = w;
+                a.plan[1 + a.R] = sum_q;
+                a.plan[2 * a.R + 2] = sum;
+            }
         }
     }
     __syncthreads();
     AttPlan p;
-    p.np = att_prefix_tiles(a, sh.shortest, sh.longest);
+    p.w = sh.w;
+    p.np = a.self == kLinePrefix ? p.w : 0;
     p.per_head = ln.pu * p.np + ln.su * sh.cum[a.R];
     const int total = p.per_head * a.heads;
-    p.t0 = att_begin(total, ln.grid, int(blockIdx.x));
-    p.t1 = att_begin(total, ln.grid, int(blockIdx.x) + 1);
-    if (blockIdx.x == 0) {
-        if (threadIdx.x == 0) ln.plan[0] = p.np;
-        for (int r = threadIdx.x; r <= a.R; r += threads) ln.plan[1 + r] = sh.cum[r];
+    // the CTA's `workers` workers; this thread's is number `worker` of them
+    const int c = int(blockIdx.x) * workers + worker;
+    p.t0 = att_begin(total, ln.grid, c);
+    p.t1 = att_begin(total, ln.grid, c + 1);
+    if (int(threadIdx.x) < workers) {
+        const int t = att_begin(total, ln.grid, int(blockIdx.x) * workers + int(threadIdx.x));
+        if (t < total) sh.first[threadIdx.x] = att_locate(a, p, sh, t);
     }
+    __syncthreads();
     return p;
-}
-
-// The unit and key tile of tile t of the line.
-__device__ __forceinline__ AttSeg att_locate(const AttendArgs &a, const AttPlan &p, const AttShared &sh, int t) {
-    const AttendLine &ln = a.line[a.self];
-    AttSeg s;
-    s.head = t / p.per_head;
-    s.skip_at = 0x7FFFFFFF;
-    s.skip = 0;
-    int w = t - s.head * p.per_head;
-    const int units = ln.pu + a.R * ln.su;
-    if (w < ln.pu * p.np) {
-        const int u = w / p.np;
-        s.unit = s.head * units + u;
-        s.req = 0;
-        s.row0 = u * ln.rt;
-        s.nrows = min(ln.rt, a.rows - s.row0);
-        s.left = p.np - (w - u * p.np);
-        s.tile = (a.self == kLineRest ? att_prefix_whole(a, sh.shortest) : 0) + (w - u * p.np);
-        s.key_begin = 0;
-        s.key_end = att_prefix_end(a, sh.longest);
-        return s;
-    }
-    w -= ln.pu * p.np;
-    int lo = 0, hi = a.R;  // the last request r with cum[r] <= w / su
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (sh.cum[mid] <= w / ln.su) lo = mid; else hi = mid;
-    }
-    const int r = lo, n = sh.cum[r + 1] - sh.cum[r];
-    w -= sh.cum[r] * ln.su;
-    const int u = w / n, k = w - u * n, tg = a.T * a.G;
-    s.unit = s.head * units + ln.pu + r * ln.su + u;
-    s.req = r;
-    s.row0 = r * tg + u * ln.rt;
-    s.nrows = min(ln.rt, tg - u * ln.rt);
-    s.left = n - k;
-    int c0, c1;
-    att_req_whole(a, sh.lens[r], &c0, &c1);
-    if (a.self == kLineRest) {
-        const int first = a.prefix / kAttTile, head = c1 > c0 ? c0 - first : 0x3FFFFFFF;  // tiles before the gap
-        s.tile = k < head ? first + k : c1 + (k - head);
-        if (k < head && c1 > c0) s.skip_at = head - k, s.skip = c1 - c0;
-    } else {
-        s.tile = c0 + k;
-    }
-    s.key_begin = a.prefix;
-    s.key_end = sh.lens[r];
-    return s;
 }
 
 // ---- copies into a ring stage
@@ -216,98 +239,85 @@ __device__ __forceinline__ void bulk_bytes(uint32_t dst, const void *src, uint32
                  : "memory");
 }
 
-// Bytes of the keys (or values) of a tile, and of a stage as the boxes lay
-// it: keys, values, then (e4m3) 64 key scales and 64 value scales.  bf16 rows
-// of 128 channels are two 128-byte halves (all rows of the first, then of
-// the second); all with the 128-byte swizzle but the 64-byte rows of e4m3
-// with 64 channels (64-byte swizzle).
-template <int D, bool Q8>
-struct AttStage {
-    static constexpr int kTile = kAttTile * D * (Q8 ? 1 : 2);
-    static constexpr int kScale = 2 * kTile;
-    static constexpr int kBytes = 2 * kTile + (Q8 ? 1024 : 0);
-};
-
-// The producer warp: tiles [t0, t1) of the line into a ring of S stages,
-// tile i into stage i % S once `empty` says that its last tile is done with.
-// A lane per box row block ("chunk": the keys of one page in one tile); a
-// batch of 32 chunks has its table entries read at once, the next batch's
-// while this one is issued.  full[s] is armed with the bytes of the chunks
-// that hold keys of the unit.
-template <int D, bool Q8, int S>
-__device__ __forceinline__ void att_producer(const AttendArgs &a, const AttPlan &plan, const AttShared &sh, uint32_t ring,
-                                             uint64_t *full, uint64_t *empty, WaitCtl *ctl) {
-    using St = AttStage<D, Q8>;
+// The tiles' copies by a producer warp: KT keys each, a lane per box ("chunk":
+// the keys of one page in one tile).  A batch of 32 chunks has its table
+// entries read at once, the next batch's behind the copies of this one's
+// first tile.  ready(i), by all lanes: waits until the CTA's tile i may be
+// written, false to stop; issue(i, chunks, chunk, row), on the lanes that have
+// a chunk of it (keys chunk * br ... of the tile, cache rows row ...): copies
+// it; chunks: of the tile, on its first, which arms the barrier before the
+// others' copies.
+template <int KT, typename Ready, typename Arm, typename Issue>
+__device__ __forceinline__ void att_producer(const AttendArgs &a, const AttPlan &plan, const AttShared &sh, int br,
+                                             Ready ready, Arm arm, Issue issue) {
     const int lane = threadIdx.x & 31;
-    const int br = min(a.page, kAttTile), cpt = kAttTile / br, tpb = 32 / cpt;
+    const int cpt = KT / br, tpb = 32 / cpt;
     const int my_tile = lane / cpt, my_chunk = lane % cpt;
     struct Chunk {
-        int row, valid;  // first cache row; 0: nothing to load
+        int head, key, page, chunks;  // key < 0: nothing to load; chunks: of the tile, from this one on
     };
+    // (what it loads is not looked at before the batch is issued)
     const auto look = [&](int tb) {
-        Chunk c{0, 0};
         const int t = tb + my_tile;
+        Chunk c{0, -1, 0, 0};
         if (t >= plan.t1) return c;
         const AttSeg g = att_locate(a, plan, sh, t);
-        const int key = g.key(0) + my_chunk * br;
-        // (keys before the prefix's end are not looked up in the request's own row)
-        if (key >= g.key_end || key + br <= g.key_begin) return c;
-        int pg = a.table[int64_t(g.req) * a.table_cols + (key >> a.page_log2)];
-        if (pg < 0 || pg >= a.n_pages) {
-            atomicCAS(a.err, 0, W12_ERR_DEVICE);
-            pg = 0;
-        }
-        c.row = ((pg * a.heads + g.head) << a.page_log2) + (key & (a.page - 1));
-        c.valid = 1;
+        const int key = g.key + my_chunk * br;
+        if (key >= g.key_end) return c;
+        c.head = g.head;
+        c.key = key;
+        c.chunks = min(cpt - my_chunk, (g.key_end - key + br - 1) / br);
+        c.page = a.table[int64_t(g.req) * a.table_cols + (key >> a.page_log2)];
         return c;
     };
-    int issued = 0;
-    bool stop = false;
-    Chunk cur = look(plan.t0);
-    for (int tb = plan.t0; tb < plan.t1 && !stop; tb += tpb) {
-        const Chunk nxt = look(tb + tpb);
-        for (int k = 0; k < tpb && tb + k < plan.t1; ++k) {
-            const int i = tb + k - plan.t0, s = i % S;
-            int go = 1;
-            if (lane == 0) go = i < S || (mbar_wait(&empty[s], uint32_t(i / S - 1) & 1u, ctl, a.err) && !aborted(ctl));
-            go = __shfl_sync(0xFFFFFFFFu, go, 0);
-            if (!go) {
-                stop = true;
-                break;
-            }
-            const bool mine = my_tile == k && cur.valid;
-            const int chunks = __popc(__ballot_sync(0xFFFFFFFFu, mine));
-            const uint32_t st = ring + uint32_t(s) * uint32_t(St::kBytes);
-            if (lane == 0)
-                mbar_expect_tx(&full[s], uint32_t(chunks) * uint32_t(br) * uint32_t(D * (Q8 ? 2 : 4) + (Q8 ? 8 : 0)));
-            __syncwarp();
-            if (mine) {
-                const uint32_t at = uint32_t(my_chunk * br);
-                if (Q8) {
-                    const uint32_t o = st + at * uint32_t(D);
-                    tma_box(o, &a.mk, 0, cur.row, &full[s]);
-                    tma_box(o + uint32_t(St::kTile), &a.mv, 0, cur.row, &full[s]);
-                    const uint32_t sc = st + uint32_t(St::kScale) + at * 4u;
-                    bulk_bytes(sc, a.ks + cur.row, uint32_t(br) * 4u, &full[s]);
-                    bulk_bytes(sc + kAttTile * 4u, a.vs + cur.row, uint32_t(br) * 4u, &full[s]);
-                } else {
-#pragma unroll
-                    for (int h = 0; h < D / 64; ++h) {
-                        const uint32_t o = st + uint32_t(h * kAttTile * 128) + at * 128u;
-                        tma_box(o, &a.mk, 64 * h, cur.row, &full[s]);
-                        tma_box(o + uint32_t(St::kTile), &a.mv, 64 * h, cur.row, &full[s]);
-                    }
-                }
-            }
-            ++issued;
+    Chunk cur{0, -1, 0, 0}, nxt = cur;
+    int row = 0;
+#pragma unroll 1
+    for (int tb = plan.t0 - tpb, k = tpb - 1; tb < plan.t1;) {
+        // tile tb + k (first round: of a batch before the first, of which
+        // nothing is issued)
+        if (tb >= plan.t0) {
+            if (tb + k >= plan.t1) return;
+            const int i = tb + k - plan.t0;
+            if (!ready(i)) return;
+            const bool mine = my_tile == k;
+            if (mine && my_chunk == 0) arm(i, cur.chunks);
+            if (cpt > 1) __syncwarp();
+            if (mine && cur.key >= 0) issue(i, my_chunk, row);
         }
-        cur = nxt;
+        if (k == 0 || tb < plan.t0) nxt = look(tb + tpb);
+        if (++k == tpb) {
+            k = 0;
+            tb += tpb;
+            cur = nxt;
+            int pg = cur.page;
+            if (cur.key >= 0 && (pg < 0 || pg >= a.n_pages)) {
+                atomicCAS(a.err, 0, W12_ERR_DEVICE);
+                pg = 0;
+            }
+            row = ((pg * a.heads + cur.head) << a.page_log2) + (cur.key & (a.page - 1));
+        }
     }
-    // after a timeout: let the copies in flight land before the CTA ends
-    if (lane == 0 && aborted(ctl))
-        for (int j = issued - 1; j >= 0 && j >= issued - S; --j)
-            mbar_drain(&full[j % S], uint32_t(j / S) & 1u, ctl->limit_ns);
 }
+
+// After a timeout a producer lets its copies land, at most this long for each
+// (a stage that another producer did not reach never completes).
+constexpr uint64_t kAttDrainNs = 20000000ull;
+
+// mbar_wait() that reads the clock only after some tries: the waits of these
+// kernels are short and the clock is slow.
+__device__ __forceinline__ bool att_wait(uint64_t *bar, uint32_t parity, WaitCtl *ctl, int *err) {
+#pragma unroll 1
+    for (int k = 0; k < 16; ++k)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait(bar, parity, ctl, err);
+}
+
+// Adds up n entries from `first` on of row r and channels d0 .. d0 + C - 1 in a
+// line's results; U entries are in flight.
+template <int D, int C, int U>
+__device__ __forceinline__ void att_add(const AttendLine &ln, int64_t first, int n, int r, int d0, float &m, float &l,
+                                        float (&acc)[C]);
 
 __device__ __forceinline__ float ex2(float x) {
     float r;
@@ -318,6 +328,57 @@ __device__ __forceinline__ float ex2(float x) {
 // Exponent e of the power of two 2^e above x (x is taken as at least 1e-30).
 __device__ __forceinline__ float exp_above(float x) {
     return float(int(__float_as_uint(fmaxf(x, 1e-30f)) >> 23) - 126);
+}
+
+template <int D, int C, int U>
+__device__ __forceinline__ void att_add(const AttendLine &ln, int64_t first, int n, int r, int d0, float &m, float &l,
+                                        float (&acc)[C]) {
+    const int rt = ln.rt;
+    const float2 *pm = ln.part_ml + first * rt + r;
+    const float *po = ln.part_o + (first * D + d0) * rt + r;
+#pragma unroll 1
+    for (int k0 = 0; k0 < n; k0 += U) {
+        // (past the last entry: the last one again, with weight 0)
+        float2 ml[U];
+        float x[U][C];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int e = min(k0 + k, n - 1);
+            ml[k] = __ldcg(pm + int64_t(e) * rt);
+            const float *src = po + int64_t(e) * (D * rt);
+#pragma unroll
+            for (int c = 0; c < C; ++c) x[k][c] = __ldcg(src + c * rt);
+        }
+        float mn = m;
+#pragma unroll
+        for (int k = 0; k < U; ++k) mn = fmaxf(mn, ml[k].x);
+        const float mu = mn == -INFINITY ? 0.0f : mn, down = ex2(m - mu);
+        m = mn;
+        l *= down;
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc[c] *= down;
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            // (an entry without keys may hold anything)
+            const bool none = k0 + k >= n || (ml[k].x == -INFINITY && ml[k].y == 0.0f);
+            const float f = ex2(ml[k].x - mu);
+            l += none ? 0.0f : ml[k].y * f;
+#pragma unroll
+            for (int c = 0; c < C; ++c) acc[c] += none ? 0.0f : x[k][c] * f;
+        }
+    }
+}
+
+// The output row of query row rho of a head, and its lse.
+template <int D>
+__device__ __forceinline__ uint16_t *att_out(const AttendArgs &a, int head, int rho) {
+    const int tok = rho / a.G, hq = head * a.G + rho - tok * a.G;
+    return a.out + int64_t(tok) * a.out_stride + int64_t(hq) * D;
+}
+__device__ __forceinline__ void att_store_lse(const AttendArgs &a, int head, int rho, float mu, float l) {
+    if (!a.lse) return;
+    const int tok = rho / a.G, hq = head * a.G + rho - tok * a.G;
+    a.lse[int64_t(tok) * (a.G * a.heads) + hq] = l == 0.0f ? -INFINITY : (mu + log2f(l)) * 0.6931471805599453f;
 }
 
 }  // namespace w12

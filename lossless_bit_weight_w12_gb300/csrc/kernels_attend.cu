@@ -10,14 +10,18 @@
 // tensor cores take them; l sums the unrounded ones.
 //
 // The register kernel, for few query rows per key head (the cache stream
-// bounds it) and for every tile that needs a mask: one CTA
-// per SM, a producer warp keeps a ring of key/value tiles full with TMA
-// boxes (a box per page and tile; 128-byte swizzle, so that the fragment
-// loads below have no bank conflicts), 8 consumer warps in two groups take
-// alternate tiles, and within a group warp w owns 16 of a tile's 64 keys for
-// all query rows: no warp waits for another until a segment ends, when the 8
-// (m, l, O) are added up in warp order.  Products are mma.sync m16n8k16 with
-// fp32 accumulation.
+// bounds it) and for every tile that needs a mask.  One CTA per SM with two
+// workers, each four warps with a ring of key/value tiles of its own and its
+// own piece of the work: while one finishes a segment the other streams.  A
+// warp owns 16 of a tile's 64 keys for all query rows; no warp waits for
+// another until a segment ends, when the four (m, l, O) are added up in warp
+// order.  Producer warps fill the rings with TMA boxes (a box per page and
+// tile; 128-byte swizzle, so that the fragment loads below have no bank
+// conflicts).  Products are mma.sync m16n8k16 with fp32 accumulation,
+// transposed: S^T = K Q^T has the 16 keys as its rows and the query rows as
+// its columns, O^T = V^T P^T the channels as its rows, so that a block of
+// query rows is 8 wide and not 16 (48 query heads over 8 key heads make 6
+// rows a token); P^T is turned between the two by movmatrix.
 //
 // e4m3 tiles stay 8 bits wide up to the registers: codes are exact in fp16,
 // so both products run in fp16; the query row is scaled by a power of two to
@@ -39,31 +43,43 @@ namespace w12 {
 
 namespace {
 
-constexpr int kCW = 8;                  // consumer warps, two groups of 4
-constexpr int kCT = kCW * 32;
-constexpr int kAT = kCT + 32;           // + the producer warp
-constexpr int kJoinCols = 32;           // channels per step of the CTA's join
-constexpr int kJoinPitch = kJoinCols + 4;
+constexpr int kGW = 4;                  // warps of a worker
+constexpr int kGT = kGW * 32;
+constexpr int kCW = 2 * kGW;            // consumer warps
 constexpr float kNegInf = -INFINITY;
 
-template <int D, bool Q8, int MT>
+// Bytes of the keys (or values) of a tile, and of a stage as the boxes lay
+// it: keys, values, then (e4m3) 64 key scales and 64 value scales.  bf16 rows
+// of 128 channels are two 128-byte halves (all rows of the first, then of
+// the second).
+template <int D, bool Q8, int NR>
 struct ACfg {
-    static constexpr int RT = 16 * MT;
-    static constexpr int kTileBytes = AttStage<D, Q8>::kTile;
-    static constexpr int kScaleOff = AttStage<D, Q8>::kScale;
-    static constexpr int kStage = AttStage<D, Q8>::kBytes;
+    static constexpr int RT = 8 * NR;
+    // A copy takes its issuing thread some 100 cycles, so a worker's keys,
+    // values and e4m3 scales have a warp each (with one warp for all three
+    // the stream stops at 4.4 TB/s): warpgroups 2 and, e4m3, 3.
+    static constexpr int kThreads = Q8 ? 512 : 384;
+    static constexpr int kProducers = Q8 ? 3 : 2;
+    // registers: shares of the launch's 16 x 128 or 12 x 168 per lane
+    static constexpr int kRegsConsumer = Q8 ? 200 : 216, kRegsProducer = Q8 ? 56 : 72;
+    static_assert(8 * kRegsConsumer + (kThreads / 32 - 8) * kRegsProducer <= (Q8 ? 16 * 128 : 12 * 168), "register shares");
+    static constexpr int kTileBytes = kAttTile * D * (Q8 ? 1 : 2);
+    static constexpr int kScaleOff = 2 * kTileBytes;
+    static constexpr int kStage = 2 * kTileBytes + (Q8 ? 1024 : 0);
+    // per worker, after the rings: queries, the join's step, row statistics
     static constexpr int kQ = RT * D * 2;
-    static constexpr int kJoin = kCW * 16 * kJoinPitch * 4;
-    static constexpr int kRowStat = kCW * RT * 8;
-    static constexpr int kLens = int(sizeof(AttShared));
-    static constexpr int kMisc = 1024;                              // barriers, wait state, scalars
-    static constexpr int kFixed = kQ + kJoin + kRowStat + kLens + kMisc;
-    static constexpr int kFit = (227 * 1024 - kFixed) / kStage;
-    // an even number of stages: a stage is then always the same group's, so
-    // one barrier per stage sees its phases one by one
-    static constexpr int S = (kFit > 12 ? 12 : kFit) & ~1;
-    static constexpr size_t kSmem = size_t(S) * kStage + kFixed;
-    static_assert(S >= 2 && kSmem <= 227 * 1024, "shared memory");
+    static constexpr int kJoinCols = NR == 4 ? 32 : 64;             // channels per step of the workers' join
+    static constexpr int kJoinPitch = kJoinCols + 4;
+    static constexpr int kJoin = kGW * 8 * kJoinPitch * 4;
+    static constexpr int kStat = kGW * RT * 8 + RT * 8 + RT * 4;    // per warp and row (m, l); (m, 1 / l); query scale
+    static constexpr int kWorker = kQ + kJoin + kStat;
+    static constexpr int kPlan = (int(sizeof(AttShared)) + 15) / 16 * 16;
+    static constexpr int kMisc = 512;                               // barriers, wait state
+    static constexpr int kFixed = 2 * kWorker + kPlan + kMisc;
+    static constexpr int kFit = (227 * 1024 - kFixed) / (2 * kStage);
+    static constexpr int S = kFit > 8 ? 8 : kFit;                   // stages per worker
+    static constexpr size_t kSmem = size_t(2 * S) * kStage + kFixed;
+    static_assert(S >= 2 && kSmem <= 227 * 1024 && 4 * S * 8 + 64 <= kMisc, "shared memory");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -77,24 +93,41 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
                  : "r"(addr));
 }
 
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+__device__ __forceinline__ float lds_f32(uint32_t addr) { return __uint_as_float(lds32(addr)); }
+
+// A 16-byte piece of a value row with a channel that is not finite.
+template <bool Q8>
+__device__ __forceinline__ bool odd_values(const uint4 &x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    bool bad = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (Q8)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) bad = bad || ((w[e] >> (8 * b)) & 0x7Fu) == 0x7Fu;
+        else
+            bad = bad || (w[e] & 0x7F80u) == 0x7F80u || (w[e] & 0x7F800000u) == 0x7F800000u;
+    return bad;
+}
+
 template <bool F16>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     if (F16)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
                      "{%0,%1,%2,%3};"
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
                      "{%0,%1,%2,%3};"
                      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ float2 lds_f2(uint32_t addr) {
-    float2 r;
-    asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(r.x), "=f"(r.y) : "r"(addr));
-    return r;
 }
 
 __device__ __forceinline__ uint2 lds64(uint32_t addr) {
@@ -128,16 +161,15 @@ __device__ __forceinline__ uint32_t tile_at(uint32_t base, int key, int c) {
     return base + uint32_t((c >> 3) * kAttTile * 128 + key * 128 + (((c & 7) ^ (key & 7)) << 4));
 }
 
-// Channel of output register (t, c) of lane quad position q4: the bf16 tiles
-// are read with the plain order; an e4m3 lane reads 16 (or 8) neighbouring
-// channels of a value row at once, and channel number t of them serves
-// product step t.
+// Channel of row g8 (h = 0) or g8 + 8 (h = 1) of output block t (16 channels):
+// the bf16 tiles are read in plain order; an e4m3 lane reads 16 (or 8)
+// neighbouring channels of a value row at once, and numbers 2 t and 2 t + 1
+// of them serve block t.
 template <int D, bool Q8>
-__device__ __forceinline__ int out_channel(int t, int q4, int c) {
-    const int n = 2 * q4 + c;
-    if (!Q8) return 8 * t + n;
-    if (D == 128) return 16 * n + t;
-    return 16 * (n & 3) + 8 * (n >> 2) + t;
+__device__ __forceinline__ int out_channel(int t, int h, int g8) {
+    if (!Q8) return 16 * t + 8 * h + g8;
+    if (D == 128) return 16 * g8 + 2 * t + h;
+    return 16 * (g8 & 3) + 8 * (g8 >> 2) + 2 * t + h;
 }
 
 // Where channel d of a query row goes in the row's shared-memory copy, so
@@ -156,498 +188,592 @@ __device__ __forceinline__ uint32_t query_at(uint32_t base, int row, int c) {
     return base + uint32_t(row * D * 2 + ((c ^ (row & 7)) << 4));
 }
 
-template <int D, bool Q8, int MT>
-__global__ void __launch_bounds__(kAT, 1) attend_kernel(const __grid_constant__ AttendArgs a) {
-    using C = ACfg<D, Q8, MT>;
-    constexpr int S = C::S, RT = C::RT, NT = D / 8, KS = D / 16;
+__device__ __forceinline__ void worker_sync(int worker) {
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + worker), "r"(kGT) : "memory");
+}
+
+template <int D, bool Q8, int NR>
+__global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_kernel(const __grid_constant__ AttendArgs a) {
+    using C = ACfg<D, Q8, NR>;
+    constexpr int S = C::S, RT = C::RT, KS = D / 16, MB = D / 16;  // product steps over channels, output blocks
+    constexpr int PPR = D / (Q8 ? 16 : 8);                        // 16-byte pieces of a cache row
+    constexpr bool kQRegs = NR <= 2;                              // query fragments stay in registers
     extern __shared__ __align__(1024) unsigned char smem[];
-    const uint32_t ring = smem_addr(smem);
-    unsigned char *fixed = smem + size_t(S) * C::kStage;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // this warp's worker: consumers 0-3 and 4-7; producers in the same order
+    const int me = warp < kCW ? warp / kGW : (warp - kCW) / (Q8 ? 4 : 2);
+    const uint32_t ring = smem_addr(smem) + uint32_t(me * S * C::kStage);
+    unsigned char *fixed = smem + size_t(2 * S) * C::kStage + me * C::kWorker;
     const uint32_t qs = smem_addr(fixed);
     float *join = reinterpret_cast<float *>(fixed + C::kQ);
-    float2 *rowstat = reinterpret_cast<float2 *>(fixed + C::kQ + C::kJoin);
-    AttShared &sh = *reinterpret_cast<AttShared *>(fixed + C::kQ + C::kJoin + C::kRowStat);
-    unsigned char *misc = fixed + C::kQ + C::kJoin + C::kRowStat + C::kLens;
-    misc = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(misc) + 15) & ~uintptr_t(15));
-    uint64_t *full = reinterpret_cast<uint64_t *>(misc), *empty = full + S;
-    WaitCtl &ctl = *reinterpret_cast<WaitCtl *>(empty + S);
-    float *row_m = reinterpret_cast<float *>(misc + 512);  // [RT] the segment's maxima (RT <= 32)
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (ring & 1023u) {  // the swizzled boxes need a 1024-byte aligned ring
+    float2 *rowstat = reinterpret_cast<float2 *>(fixed + C::kQ + C::kJoin);  // [kGW][RT]
+    float2 *row_ml = rowstat + kGW * RT;                                     // [RT]
+    float *q_up = reinterpret_cast<float *>(row_ml + RT);                    // [RT]
+    AttShared &sh = *reinterpret_cast<AttShared *>(smem + size_t(2 * S) * C::kStage + 2 * C::kWorker);
+    unsigned char *misc = smem + size_t(2 * S) * C::kStage + 2 * C::kWorker + C::kPlan;
+    uint64_t *full = reinterpret_cast<uint64_t *>(misc) + me * 2 * S, *empty = full + S;
+    WaitCtl &ctl = *reinterpret_cast<WaitCtl *>(misc + 4 * S * 8);
+    int *s_last = reinterpret_cast<int *>(&ctl + 1);  // [2]
+    if (smem_addr(smem) & 1023u) {  // the swizzled boxes need 1024-byte aligned stages
         if (threadIdx.x == 0) record_error(a.err, W12_ERR_DEVICE);
         return;
     }
     if (threadIdx.x == 0) {
-        for (int s = 0; s < S; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], kCW / 2);
-        }
+        uint64_t *bar = reinterpret_cast<uint64_t *>(misc);
+        for (int s = 0; s < S; ++s)
+            for (int g = 0; g < 2; ++g) {
+                mbar_init(&bar[g * 2 * S + s], C::kProducers);
+                mbar_init(&bar[g * 2 * S + S + s], kGW);
+            }
         ctl.abort = 0;
         ctl.limit_ns = a.wait_ns ? a.wait_ns : kWaitLimitNs;
         mbar_fence_init();
     }
     pdl_launch_dependents();
     pdl_wait_previous();
-
-    const AttPlan plan = att_plan(a, sh, kAT);
-    const AttendLine &ln = a.line[a.self];
+    const AttPlan plan = att_plan(a, sh, 2, me);
+    const AttendLine &ln = a.line[kLineRest];
     const int t0 = plan.t0, t1 = plan.t1;
-    if (warp == kCW) {
-        att_producer<D, Q8, S>(a, plan, sh, ring, full, empty, &ctl);
+    if (warp >= kCW) {
+        // ------------------------------------------------------ producers
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsProducer));
+        const int part = (warp - kCW) % (Q8 ? 4 : 2);
+        if (part >= C::kProducers) return;
+        const int br = min(a.page, kAttTile);
+        int issued = 0;
+        att_producer<kAttTile>(
+            a, plan, sh, br,
+            [&](int i) {
+                const int s = i % S;
+                const bool go =
+                    i < S || (att_wait(&empty[s], uint32_t(i / S - 1) & 1u, &ctl, a.err) && !aborted(&ctl));
+                issued += go;
+                return __all_sync(0xFFFFFFFFu, go) != 0;
+            },
+            [&](int i, int chunks) {
+                mbar_expect_tx(&full[i % S], uint32_t(chunks * br) * uint32_t(part == 2 ? 8 : Q8 ? D : 2 * D));
+            },
+            [&](int i, int chunk, int row) {
+                const int s = i % S;
+                const uint32_t st = ring + uint32_t(s) * uint32_t(C::kStage), at = uint32_t(chunk * br);
+                if (part == 2) {
+                    const uint32_t sc = st + uint32_t(C::kScaleOff) + at * 4u;
+                    bulk_bytes(sc, a.ks + row, uint32_t(br) * 4u, &full[s]);
+                    bulk_bytes(sc + kAttTile * 4u, a.vs + row, uint32_t(br) * 4u, &full[s]);
+                } else {
+                    const CUtensorMap *map = part ? &a.mv : &a.mk;
+                    const uint32_t to = st + uint32_t(part ? C::kTileBytes : 0);
+                    if (Q8) {
+                        tma_box(to + at * uint32_t(D), map, 0, row, &full[s]);
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < D / 64; ++h)
+                            tma_box(to + uint32_t(h * kAttTile * 128) + at * 128u, map, 64 * h, row, &full[s]);
+                    }
+                }
+            });
+        // after a timeout: let the copies in flight land before the CTA ends
+        if (lane == 0 && aborted(&ctl))
+            for (int j = issued - 1; j >= 0 && j >= issued - S; --j)
+                mbar_drain(&full[j % S], uint32_t(j / S) & 1u, kAttDrainNs);
         return;
     }
 
     // ------------------------------------------------------------ consumers
-    const int grp = warp >> 2, kw = 16 * (warp & 3);  // this warp's keys of its group's tiles
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsConsumer));
+    const int tid = threadIdx.x & (kGT - 1), wg = warp & (kGW - 1);
+    const int kw = 16 * wg;                           // this warp's keys of a tile
     const int g8 = lane >> 2, q4 = lane & 3;
     const int r0 = lane & 7, mat = lane >> 3;         // ldmatrix: this lane's row and matrix
-    for (int t = t0; t < t1;) {
-        const AttSeg seg = att_locate(a, plan, sh, t);
-        const int n_tiles = min(seg.left, t1 - t);
-        // ---- query rows into shared memory (rows past the unit: zeros)
-        named_sync(kCT);  // the previous segment's copy is no longer read
-        for (int i = threadIdx.x; i < RT * (D / 8); i += kCT) {
-            const int row = i / (D / 8), c = i % (D / 8);
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (row < seg.nrows) {
-                const int rho = seg.row0 + row, tok = rho / a.G, hq = seg.head * a.G + rho - tok * a.G;
-                v = *reinterpret_cast<const uint4 *>(a.q + tok * a.q_stride + int64_t(hq) * D + 8 * c);
+    if (t0 >= t1) return;
+    AttSeg seg = sh.first[me];
+    // a thread's share of a segment's query rows: 16-byte pieces tid, tid + kGT ..
+    constexpr int kQP = RT * D / 8 / kGT ? RT * D / 8 / kGT : 1;
+    uint4 qn[kQP];
+    const auto load_q = [&](const AttSeg &s) {
+#pragma unroll
+        for (int x = 0; x < kQP; ++x) {
+            const int row = (tid + x * kGT) / (D / 8), c = (tid + x * kGT) % (D / 8);
+            qn[x] = make_uint4(0, 0, 0, 0);
+            if (row < s.nrows && row < RT) {
+                const int rho = s.row0 + row, tok = rho / a.G, hq = s.head * a.G + rho - tok * a.G;
+                qn[x] = *reinterpret_cast<const uint4 *>(a.q + tok * a.q_stride + int64_t(hq) * D + 8 * c);
             }
+        }
+    };
+    load_q(seg);
+#pragma unroll 1
+    for (int t = t0;;) {
+        const int n_tiles = min(seg.left, t1 - t);
+        // ---- query rows into shared memory (rows past the unit: zeros), and
+        // the next segment's on their way
+        worker_sync(me);  // the previous segment's copy is no longer read
+#pragma unroll
+        for (int x = 0; x < kQP; ++x) {
+            const int row = (tid + x * kGT) / (D / 8), c = (tid + x * kGT) % (D / 8);
+            const uint32_t w[4] = {qn[x].x, qn[x].y, qn[x].z, qn[x].w};
             if (!Q8) {
-                const uint32_t at = query_at<D>(qs, row, c);
-                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                             : "memory");
+                if (row < RT)
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(query_at<D>(qs, row, c)), "r"(w[0]),
+                                 "r"(w[1]), "r"(w[2]), "r"(w[3])
+                                 : "memory");
             } else {
                 // the row's largest magnitude (the D / 8 lanes of a row are neighbours)
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
                 uint32_t top = 0;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
-#pragma unroll
-                for (int o = 1; o < D / 8; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                top = __reduce_max_sync(D == 128 ? 0xFFFFu << (lane & 16) : 0xFFu << (lane & 24), top);
                 // 2^-e with e the exponent of the largest (kept in [-100, 126])
-                int e = int(top >> 7) - 127;
-                e = max(-100, min(126, e));
+                const int e = max(-100, min(126, int(top >> 7) - 127));
                 const float down = __uint_as_float(uint32_t(127 - e) << 23);
-                if (c == 0) rowstat[row].x = __uint_as_float(uint32_t(127 + e) << 23);
+                if (row < RT) {
+                    if (c == 0) q_up[row] = __uint_as_float(uint32_t(127 + e) << 23);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t p = pack_f16(bf16_bits_to_float(w[j] & 0xFFFFu) * down,
-                                                bf16_bits_to_float(w[j] >> 16) * down);
-                    const int col = query_column<Q8>(8 * c + 2 * j);
-                    const uint32_t at = query_at<D>(qs, row, col >> 3) + uint32_t(col & 7) * 2u;
-                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(p) : "memory");
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t p = pack_f16(bf16_bits_to_float(w[j] & 0xFFFFu) * down,
+                                                    bf16_bits_to_float(w[j] >> 16) * down);
+                        const int col = query_column<Q8>(8 * c + 2 * j);
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(query_at<D>(qs, row, col >> 3) + uint32_t(col & 7) * 2u),
+                                     "r"(p)
+                                     : "memory");
+                    }
                 }
             }
         }
-        named_sync(kCT);
-        float up[MT][2];  // per row: scale in log2 units (times the query row's power of two)
-        int pos[MT][2];
+        AttSeg next = seg;
+        const bool more = t + n_tiles < t1;
+        if (more) {
+            att_next(a, plan, sh, next);
+            load_q(next);
+        }
+        worker_sync(me);
+        // a lane has query rows 8 n + 2 q4 + c, n < NR, c < 2
+        float up[NR][2];  // scale in log2 units (times the query row's power of two)
+        int pos[NR][2];
         int min_pos = 0x7FFFFFFF;
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int n = 0; n < NR; ++n)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int row = 16 * m + 8 * h + g8;
-                up[m][h] = a.scale_log2 * (Q8 ? rowstat[row].x : 1.0f);
-                pos[m][h] = 0x7FFFFFFF;  // rows past the unit: their results are not kept
-                if (row < seg.nrows) {
-                    const int tok = (seg.row0 + row) / a.G, r = tok / a.T;
-                    pos[m][h] = sh.lens[r] - a.T + tok - r * a.T;
-                }
-                min_pos = min(min_pos, pos[m][h]);
+            for (int c = 0; c < 2; ++c) {
+                const int row = 8 * n + 2 * q4 + c;
+                up[n][c] = a.scale_log2 * (Q8 ? q_up[row] : 1.0f);
+                pos[n][c] = 0x7FFFFFFF;  // rows past the unit: their results are not kept
+                if (row < seg.nrows)  // (a unit's rows are of one request)
+                    pos[n][c] = seg.key_end - a.T + (seg.row0 + row) / a.G - seg.req * a.T;
+                min_pos = min(min_pos, pos[n][c]);
             }
         min_pos = __reduce_min_sync(0xFFFFFFFFu, min_pos);
-        if (Q8) named_sync(kCT);  // rowstat is read above and written again at the segment's end
-
-        float o[MT][NT][4];
-        float m_run[MT][2], l_run[MT][2];
+        uint32_t qf[kQRegs ? NR : 1][KS][2];
+        if (kQRegs) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            m_run[m][0] = m_run[m][1] = kNegInf;
-            l_run[m][0] = l_run[m][1] = 0.0f;
+            for (int n = 0; n < NR; ++n)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) o[m][n][0] = o[m][n][1] = o[m][n][2] = o[m][n][3] = 0.0f;
+                for (int ks = 0; ks < KS; ks += 2) {
+                    uint32_t x[4];
+                    ldsm4(x, query_at<D>(qs, 8 * n + r0, 2 * ks + mat));
+                    qf[kQRegs ? n : 0][ks][0] = x[0], qf[kQRegs ? n : 0][ks][1] = x[1];
+                    qf[kQRegs ? n : 0][ks + 1][0] = x[2], qf[kQRegs ? n : 0][ks + 1][1] = x[3];
+                }
         }
 
-        const int i0 = t - t0;
-        for (int k = ((i0 & 1) != grp); k < n_tiles; k += 2) {
-            const int i = i0 + k, s = i % S;
-            mbar_wait(&full[s], uint32_t(i / S) & 1u, &ctl, a.err);
-            const uint32_t kb = ring + uint32_t(s) * uint32_t(C::kStage), vb = kb + uint32_t(C::kTileBytes);
-            const int key0 = seg.key(k) + kw;  // this warp's first key
-            const bool whole = key0 >= seg.key_begin && key0 + 16 <= seg.key_end && key0 + 15 <= min_pos;
+        float o[MB][NR][4];
+        float m_run[NR][2], l_run[NR][2];
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            m_run[n][0] = m_run[n][1] = kNegInf;
+            l_run[n][0] = l_run[n][1] = 0.0f;
+#pragma unroll
+            for (int b = 0; b < MB; ++b) o[b][n][0] = o[b][n][1] = o[b][n][2] = o[b][n][3] = 0.0f;
+        }
 
-            // ---- scores of 16 keys
-            float sc[MT][2][4];
+#pragma unroll 1
+        for (int k = 0; k < n_tiles; ++k) {
+            const int i = t - t0 + k, s = i % S;
+            att_wait(&full[s], uint32_t(i / S) & 1u, &ctl, a.err);
+            const uint32_t kb = ring + uint32_t(s) * uint32_t(C::kStage), vb = kb + uint32_t(C::kTileBytes);
+            const int key0 = seg.key + k * kAttTile + kw;  // this warp's first key
+            const bool whole = key0 + 16 <= seg.key_end && key0 + 15 <= min_pos;
+
+            // ---- scores of 16 keys: sc[n][2 h + c], key g8 + 8 h; one block
+            // of rows: in two chains
+            float sc[NR][4], sc2[NR == 1 ? 1 : NR][4];
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int n = 0; n < NR; ++n)
 #pragma unroll
-                for (int n = 0; n < 2; ++n) sc[m][n][0] = sc[m][n][1] = sc[m][n][2] = sc[m][n][3] = 0.0f;
-            if (Q8) {
-                // a lane's pieces of keys g8 and g8 + 8: q4 and, for 128 channels, q4 + 4
-                uint4 kx[2][D / 64];
+                for (int x = 0; x < 4; ++x) sc[n][x] = sc2[n][x] = 0.0f;
+            uint4 kx[2][Q8 ? D / 64 : 1];  // e4m3: a lane's pieces q4 (and q4 + 4) of keys g8 and g8 + 8
+            if (Q8)
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int p = 0; p < D / 64; ++p) kx[n][p] = lds128(tile_at<D, Q8>(kb, kw + 8 * n + g8, q4 + 4 * p));
+                    for (int p = 0; p < D / 64; ++p)
+                        kx[h][Q8 ? p : 0] = lds128(tile_at<D, Q8>(kb, kw + 8 * h + g8, q4 + 4 * p));
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
+            for (int ks = 0; ks < KS; ++ks) {
+                uint32_t kf[4];
+                if (Q8) {
                     uint32_t w[2];
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const uint4 &x = kx[n][ks >> 2];
-                        w[n] = (ks & 3) == 0 ? x.x : (ks & 3) == 1 ? x.y : (ks & 3) == 2 ? x.z : x.w;
+                    for (int h = 0; h < 2; ++h) {
+                        const uint4 &x = kx[h][Q8 ? ks >> 2 : 0];
+                        w[h] = (ks & 3) == 0 ? x.x : (ks & 3) == 1 ? x.y : (ks & 3) == 2 ? x.z : x.w;
                     }
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        uint32_t qf[4];
-                        ldsm4(qf, query_at<D>(qs, 16 * m + r0 + 8 * (mat & 1), 2 * ks + (mat >> 1)));
-#pragma unroll
-                        for (int n = 0; n < 2; ++n)
-                            mma16816<true>(sc[m][n], qf, e4m3x2_lo_to_f16x2(w[n]), e4m3x2_hi_to_f16x2(w[n]));
-                    }
+                    kf[0] = e4m3x2_lo_to_f16x2(w[0]), kf[1] = e4m3x2_lo_to_f16x2(w[1]);
+                    kf[2] = e4m3x2_hi_to_f16x2(w[0]), kf[3] = e4m3x2_hi_to_f16x2(w[1]);
+                } else {
+                    ldsm4(kf, tile_at<D, Q8>(kb, kw + 8 * (mat & 1) + r0, 2 * ks + (mat >> 1)));
                 }
-            } else {
+                if (kQRegs) {
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    uint32_t kf[4];
-                    ldsm4(kf, tile_at<D, Q8>(kb, kw + 8 * (mat >> 1) + r0, 2 * ks + (mat & 1)));
+                    for (int n = 0; n < NR; ++n)
+                        mma16816<Q8>(NR == 1 && (ks & 1) ? sc2[0] : sc[n], kf, qf[kQRegs ? n : 0][ks][0],
+                                     qf[kQRegs ? n : 0][ks][1]);
+                } else {
 #pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        uint32_t qf[4];
-                        ldsm4(qf, query_at<D>(qs, 16 * m + r0 + 8 * (mat & 1), 2 * ks + (mat >> 1)));
-                        mma16816<false>(sc[m][0], qf, kf[0], kf[1]);
-                        mma16816<false>(sc[m][1], qf, kf[2], kf[3]);
+                    for (int n = 0; n < NR; n += 2) {
+                        uint32_t x[4];
+                        ldsm4(x, query_at<D>(qs, 8 * n + 8 * (mat >> 1) + r0, 2 * ks + (mat & 1)));
+                        mma16816<Q8>(sc[n], kf, x[0], x[1]);
+                        mma16816<Q8>(sc[n + 1], kf, x[2], x[3]);
                     }
                 }
             }
-            float2 kscale[2], vscale[2];
+            if (NR == 1)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) sc[0][x] += sc2[0][x];
+            // ---- values: on their way during the softmax, but for a tile
+            // whose value rows are changed below and for many rows (registers)
+            constexpr int W = Q8 ? (D == 128 ? 4 : 2) : 1;  // e4m3: words of a lane's piece of a value row
+            constexpr bool kEarlyV = NR <= 2;
+            uint32_t vx[4][W], vf[Q8 ? 1 : MB][4];
+            const auto load_v = [&] {
+                if (Q8) {
+                    const int ka = kw + 2 * q4;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int key = ka + (j & 1) + 8 * (j >> 1);
+                        if (D == 128) {
+                            const uint4 x = lds128(tile_at<D, Q8>(vb, key, g8));
+                            vx[j][0] = x.x, vx[j][W > 1 ? 1 : 0] = x.y, vx[j][W > 2 ? 2 : 0] = x.z, vx[j][W > 3 ? 3 : 0] = x.w;
+                        } else {
+                            const uint2 x = lds64(tile_at<D, Q8>(vb, key, g8 & 3) + 8u * uint32_t(g8 >> 2));
+                            vx[j][0] = x.x, vx[j][W > 1 ? 1 : 0] = x.y;
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int b = 0; b < MB; ++b)
+                        ldsm4t(vf[Q8 ? 0 : b], tile_at<D, Q8>(vb, kw + r0 + 8 * (mat >> 1), 2 * b + (mat & 1)));
+                }
+            };
+            if (kEarlyV && whole) load_v();
+            float kscale[2] = {1.0f, 1.0f}, vscale[2] = {1.0f, 1.0f};
             float lift = 0.0f;  // e4m3: e - 7 for value scales below 2^e
             if (Q8) {
-                const uint32_t sb = kb + uint32_t(C::kScaleOff) + uint32_t(kw + 2 * q4) * 4u;
-                float top = 0.0f;
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    kscale[n] = lds_f2(sb + 32u * uint32_t(n));
-                    vscale[n] = lds_f2(sb + kAttTile * 4u + 32u * uint32_t(n));
-                    // scales of rows that are not the unit's may be anything
-                    const int j = key0 + 8 * n + 2 * q4;
-                    if (j < seg.key_begin || j >= seg.key_end) kscale[n].x = vscale[n].x = 0.0f;
-                    if (j + 1 < seg.key_begin || j + 1 >= seg.key_end) kscale[n].y = vscale[n].y = 0.0f;
-                    top = fmaxf(top, fmaxf(vscale[n].x, vscale[n].y));
-                }
-                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-                lift = exp_above(top) - 7.0f;
-            }
-            // ---- mask, running maximum, weights
-            uint32_t pf[MT][4];
-            float pw[MT][2][4];
-            bool moved = false;
-            float alpha[MT][2];
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
+                const uint32_t sb = kb + uint32_t(C::kScaleOff) + uint32_t(kw + g8) * 4u;
+                uint32_t top = 0u;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float mx = kNegInf;
+                    kscale[h] = lds_f32(sb + 32u * uint32_t(h));
+                    vscale[h] = lds_f32(sb + kAttTile * 4u + 32u * uint32_t(h));
+                    // scales of rows that are not the unit's may be anything
+                    if (key0 + 8 * h + g8 >= seg.key_end) kscale[h] = vscale[h] = 0.0f;
+                    // (a NaN scale makes the rows that see the key NaN by itself)
+                    if (vscale[h] <= 3.0e38f) top = max(top, __float_as_uint(vscale[h]));
+                }
+                lift = exp_above(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, top))) - 7.0f;
+            }
+            // ---- mask, running maximum, weights
+            float pw[NR][4];
+            uint32_t pf[NR][2];
+            bool moved = false;
+            float alpha[NR][2];
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < NR; ++n) {
+                float x[2][2], mx[2];
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            float x = sc[m][n][2 * h + c] * up[m][h];
-                            if (Q8) x *= c ? kscale[n].y : kscale[n].x;
-                            const int j = key0 + 8 * n + 2 * q4 + c;
-                            if (!whole && (j < seg.key_begin || j >= seg.key_end || j > pos[m][h])) x = kNegInf;
-                            sc[m][n][2 * h + c] = x;
-                            mx = fmaxf(mx, x);
-                        }
-                    mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-                    const float mn = fmaxf(m_run[m][h], mx + lift);
-                    const float mu = mn == kNegInf ? 0.0f : mn;  // a row without keys so far
-                    alpha[m][h] = ex2(m_run[m][h] - mu);
-                    moved = moved || m_run[m][h] != mn;
-                    m_run[m][h] = mn;
-                    float sum = 0.0f;
+                for (int c = 0; c < 2; ++c) {
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const float p = ex2(sc[m][n][2 * h + c] - mu);
-                            sum += p;
-                            // a masked weight is zero whatever the key's scale holds
-                            pw[m][n][2 * h + c] =
-                                !Q8 ? p : p == 0.0f ? 0.0f : p * (c ? vscale[n].y : vscale[n].x);
-                        }
-                    l_run[m][h] = l_run[m][h] * alpha[m][h] + sum;
+                    for (int h = 0; h < 2; ++h) {
+                        x[c][h] = sc[n][2 * h + c] * up[n][c];
+                        if (Q8) x[c][h] *= kscale[h];
+                        const int j = key0 + 8 * h + g8;
+                        if (!whole && (j >= seg.key_end || j > pos[n][c])) x[c][h] = kNegInf;
+                    }
+                    mx[c] = fmaxf(x[c][0], x[c][1]);
                 }
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int off = 4; off <= 16; off <<= 1)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        pf[m][2 * n + h] = Q8 ? pack_f16(pw[m][n][2 * h], pw[m][n][2 * h + 1])
-                                              : pack_bf16(pw[m][n][2 * h], pw[m][n][2 * h + 1]);
+                    for (int c = 0; c < 2; ++c) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xFFFFFFFFu, mx[c], off));
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float mn = fmaxf(m_run[n][c], mx[c] + lift);
+                    const float mu = mn == kNegInf ? 0.0f : mn;  // a row without keys so far
+                    alpha[n][c] = ex2(m_run[n][c] - mu);
+                    moved = moved || m_run[n][c] != mn;
+                    m_run[n][c] = mn;
+                    const float p0 = ex2(x[c][0] - mu), p1 = ex2(x[c][1] - mu);
+                    l_run[n][c] = l_run[n][c] * alpha[n][c] + (p0 + p1);
+                    // a masked weight is zero whatever the key's scale holds
+                    pw[n][c] = !Q8 ? p0 : p0 == 0.0f ? 0.0f : p0 * vscale[0];
+                    pw[n][2 + c] = !Q8 ? p1 : p1 == 0.0f ? 0.0f : p1 * vscale[1];
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    pf[n][h] = transpose8x8(Q8 ? pack_f16(pw[n][2 * h], pw[n][2 * h + 1])
+                                               : pack_bf16(pw[n][2 * h], pw[n][2 * h + 1]));
             }
             if (__any_sync(0xFFFFFFFFu, moved)) {
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
+                for (int b = 0; b < MB; ++b)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                    for (int n = 0; n < NR; ++n)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) o[m][n][c] *= alpha[m][c >> 1];
+                        for (int x = 0; x < 4; ++x) o[b][n][x] *= alpha[n][x & 1];
             }
             // ---- value rows that some query row must not see
             if (!whole) {
-                bool touched = false;
-                // rows outside the unit's keys (another request's, or never
-                // written) are taken as zeros: 0 * NaN would reach the sum
-#pragma unroll 1
-                for (int x = lane; x < 16 * (D / (Q8 ? 16 : 8)); x += 32) {
-                    const int kr = x / (D / (Q8 ? 16 : 8)), c = x % (D / (Q8 ? 16 : 8)), j = key0 + kr;
-                    if (j >= seg.key_end || j < seg.key_begin) {
-                        sts_zero16(tile_at<D, Q8>(vb, kw + kr, c));
+                bool touched = false, bad = false;
+                // rows past the unit's keys (another request's, or never
+                // written) are taken as zeros: 0 * NaN would reach the sum;
+                // keys that only some rows see are looked at for channels
+                // that are not finite
+#pragma unroll 2
+                for (int x = lane; x < 16 * PPR; x += 32) {
+                    const int kr = x / PPR, c = x % PPR;
+                    const uint32_t at = tile_at<D, Q8>(vb, kw + kr, c);
+                    if (key0 + kr >= seg.key_end) {
+                        sts_zero16(at);
                         touched = true;
+                    } else if (key0 + kr > min_pos) {
+                        bad = bad || odd_values<Q8>(lds128(at));
                     }
                 }
-                // keys that only some rows see: a channel that is not finite
-                // is kept out of the matrix product and added to the rows
-                // that see it by itself
-                uint32_t odd = 0;
+                if (__any_sync(0xFFFFFFFFu, bad)) {
+                    // a row of values with such a channel is kept out of the
+                    // matrix product and added to the rows that see it by itself
 #pragma unroll 1
-                for (int kr = 0; kr < 16; ++kr) {
-                    const int j = key0 + kr;
-                    if (j < seg.key_begin || j >= seg.key_end || j <= min_pos) continue;
-                    bool bad = false;
-                    if (lane < D / (Q8 ? 16 : 8)) {
-                        const uint4 x = lds128(tile_at<D, Q8>(vb, kw + kr, lane));
-                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                    for (int kr = 0; kr < 16; ++kr) {
+                        const int j = key0 + kr;
+                        if (j >= seg.key_end || j <= min_pos) continue;
+                        if (!__any_sync(0xFFFFFFFFu, lane < PPR && odd_values<Q8>(lds128(tile_at<D, Q8>(vb, kw + kr, lane % PPR)))))
+                            continue;
+                        const int src = 4 * (kr & 7) + q4;  // the lane that has this key's weights of my rows
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (Q8)
+                        for (int n = 0; n < NR; ++n)
 #pragma unroll
-                                for (int b = 0; b < 4; ++b) bad = bad || ((w[e] >> (8 * b)) & 0x7Fu) == 0x7Fu;
-                            else
-                                bad = bad || (w[e] & 0x7F80u) == 0x7F80u || (w[e] & 0x7F800000u) == 0x7F800000u;
-                    }
-                    if (__any_sync(0xFFFFFFFFu, bad)) odd |= 1u << kr;
-                }
-                while (odd) {
-                    const int kr = __ffs(odd) - 1, j = key0 + kr;
-                    odd &= odd - 1u;
-                    const int src = (lane & ~3) | ((kr & 7) >> 1);
+                            for (int c = 0; c < 2; ++c) {
+                                const float p = __shfl_sync(0xFFFFFFFFu, kr >= 8 ? pw[n][2 + c] : pw[n][c], src);
+                                if (j <= pos[n][c]) {
 #pragma unroll
-                    for (int m = 0; m < MT; ++m)
+                                    for (int b = 0; b < MB; ++b)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const float w0 = __shfl_sync(0xFFFFFFFFu, kr >= 8 ? pw[m][1][2 * h] : pw[m][0][2 * h], src);
-                            const float w1 =
-                                __shfl_sync(0xFFFFFFFFu, kr >= 8 ? pw[m][1][2 * h + 1] : pw[m][0][2 * h + 1], src);
-                            if (j <= pos[m][h]) {
-                                const float p = (kr & 1) ? w1 : w0;
-#pragma unroll
-                                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                                    for (int c = 0; c < 2; ++c) {
-                                        const int d = out_channel<D, Q8>(n, q4, c);
-                                        float v;
-                                        if (Q8) {
-                                            const uint32_t b = lds_u8(tile_at<D, Q8>(vb, kw + kr, d >> 4) + uint32_t(d & 15));
-                                            float f[4];
-                                            e4m3x4_to_float(b, f);
-                                            v = f[0];
-                                        } else {
-                                            v = bf16_bits_to_float(
-                                                lds_u16(tile_at<D, Q8>(vb, kw + kr, d >> 3) + uint32_t(d & 7) * 2u));
+                                        for (int h = 0; h < 2; ++h) {
+                                            const int d = out_channel<D, Q8>(b, h, g8);
+                                            float v;
+                                            if (Q8) {
+                                                float f[4];
+                                                e4m3x4_to_float(
+                                                    lds_u8(tile_at<D, Q8>(vb, kw + kr, d >> 4) + uint32_t(d & 15)), f);
+                                                v = f[0];
+                                            } else {
+                                                v = bf16_bits_to_float(
+                                                    lds_u16(tile_at<D, Q8>(vb, kw + kr, d >> 3) + uint32_t(d & 7) * 2u));
+                                            }
+                                            o[b][n][2 * h + c] += p * v;
                                         }
-                                        o[m][n][2 * h + c] += p * v;
-                                    }
+                                }
                             }
-                        }
-                    __syncwarp();
-                    if (lane < D / (Q8 ? 16 : 8)) sts_zero16(tile_at<D, Q8>(vb, kw + kr, lane));
-                    touched = true;
+                        __syncwarp();
+                        if (lane < PPR) sts_zero16(tile_at<D, Q8>(vb, kw + kr, lane));
+                        touched = true;
+                        __syncwarp();
+                    }
                 }
                 if (touched) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the next box lands here
                 __syncwarp();
             }
+            if (!kEarlyV || !whole) load_v();
             // ---- weights times values
             if (Q8) {
-                const int ka = kw + 2 * q4;
-                constexpr int W = D == 128 ? 4 : 2;  // words of a lane's piece of a value row
-                uint32_t vx[4][W];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int key = ka + (j & 1) + 8 * (j >> 1);
-                    if (D == 128) {
-                        const uint4 x = lds128(tile_at<D, Q8>(vb, key, g8));
-                        vx[j][0] = x.x, vx[j][1] = x.y, vx[j][W - 2] = x.z, vx[j][W - 1] = x.w;
-                    } else {
-                        const uint2 x = lds64(tile_at<D, Q8>(vb, key, g8 & 3) + 8u * uint32_t(g8 >> 2));
-                        vx[j][0] = x.x, vx[j][1] = x.y;
+                for (int w = 0; w < W; ++w)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        // channels 4 w + 2 e and the next, of keys (2 q4, 2 q4 + 1) and 8 later
+                        const uint32_t sel = e ? 0x7362u : 0x5140u;
+                        const uint32_t x = prmt2(vx[0][w], vx[1][w], sel), y = prmt2(vx[2][w], vx[3][w], sel);
+                        const uint32_t f[4] = {e4m3x2_lo_to_f16x2(x), e4m3x2_hi_to_f16x2(x), e4m3x2_lo_to_f16x2(y),
+                                               e4m3x2_hi_to_f16x2(y)};
+#pragma unroll
+                        for (int n = 0; n < NR; ++n) mma16816<true>(o[2 * w + e][n], f, pf[n][0], pf[n][1]);
                     }
-                }
-#pragma unroll
-                for (int w = 0; w < W; ++w) {
-                    const uint32_t x0 = prmt2(vx[0][w], vx[1][w], 0x5140u), x1 = prmt2(vx[0][w], vx[1][w], 0x7362u);
-                    const uint32_t y0 = prmt2(vx[2][w], vx[3][w], 0x5140u), y1 = prmt2(vx[2][w], vx[3][w], 0x7362u);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t b0 = (e & 1) ? e4m3x2_hi_to_f16x2(e & 2 ? x1 : x0) : e4m3x2_lo_to_f16x2(e & 2 ? x1 : x0);
-                        const uint32_t b1 = (e & 1) ? e4m3x2_hi_to_f16x2(e & 2 ? y1 : y0) : e4m3x2_lo_to_f16x2(e & 2 ? y1 : y0);
-#pragma unroll
-                        for (int m = 0; m < MT; ++m) mma16816<true>(o[m][4 * w + e], pf[m], b0, b1);
-                    }
-                }
             } else {
 #pragma unroll
-                for (int n = 0; n < NT; n += 2) {
-                    uint32_t vf[4];
-                    ldsm4t(vf, tile_at<D, Q8>(vb, kw + r0 + 8 * (mat & 1), n + (mat >> 1)));
+                for (int b = 0; b < MB; ++b)
 #pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        mma16816<false>(o[m][n], pf[m], vf[0], vf[1]);
-                        mma16816<false>(o[m][n + 1], pf[m], vf[2], vf[3]);
-                    }
-                }
+                    for (int n = 0; n < NR; ++n) mma16816<false>(o[b][n], vf[Q8 ? 0 : b], pf[n][0], pf[n][1]);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);
         }
 
-        // ---- the segment's end: add up the 8 warps' (m, l, O) in warp order
-        const int slot = seg.unit + int(blockIdx.x);
+        // ---- the segment's end: add up the worker's four (m, l, O) in warp order
+        int first = 0, n_seg = 2;  // the unit's segments: the first worker, how many (join: not needed)
+        if (!a.join) {
+            const int n = sh.cum[seg.req + 1] - sh.cum[seg.req], total = plan.per_head * a.heads;
+            const int b = seg.head * plan.per_head + ln.su * sh.cum[seg.req] + seg.block * n;
+            first = att_owner(total, ln.grid, b);
+            n_seg = att_owner(total, ln.grid, b + n - 1) - first + 1;
+        }
+        const bool alone = n_seg == 1;  // the only result of its rows
+        const int64_t entry = int64_t(seg.unit) + 2 * int(blockIdx.x) + me;
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int n = 0; n < NR; ++n)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float l = l_run[m][h];
-                l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
-                l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
-                if (q4 == 0) rowstat[warp * RT + 16 * m + 8 * h + g8] = make_float2(m_run[m][h], l);
+            for (int c = 0; c < 2; ++c) {
+                float l = l_run[n][c];
+                l += __shfl_xor_sync(0xFFFFFFFFu, l, 4);
+                l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
+                l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
+                if (g8 == 0) rowstat[wg * RT + 8 * n + 2 * q4 + c] = make_float2(m_run[n][c], l);
             }
-        named_sync(kCT);
-        if (threadIdx.x < RT) {
-            const int row = threadIdx.x;
+        worker_sync(me);
+        if (tid < RT) {
+            const int row = tid;
             float m = kNegInf;
 #pragma unroll
-            for (int w = 0; w < kCW; ++w) m = fmaxf(m, rowstat[w * RT + row].x);
+            for (int w = 0; w < kGW; ++w) m = fmaxf(m, rowstat[w * RT + row].x);
             const float mu = m == kNegInf ? 0.0f : m;
             float l = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kCW; ++w) l += rowstat[w * RT + row].y * ex2(rowstat[w * RT + row].x - mu);
-            row_m[row] = mu;
-            if (row < seg.nrows) ln.part_ml[size_t(slot) * RT + row] = make_float2(m, l);
-        }
-        named_sync(kCT);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            float f[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                f[h] = ex2(m_run[m][h] - row_m[16 * m + 8 * h + g8]);
-#pragma unroll
-            for (int c0 = 0; c0 < NT / 4; ++c0) {
-                // 32 channels of 16 rows per step: this warp's registers (n, c)
-                // of the step, at column 8 (n % 4) + 2 q4 + c
-#pragma unroll
-                for (int n = 0; n < 4; ++n)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        *reinterpret_cast<float2 *>(&join[(warp * 16 + 8 * h + g8) * kJoinPitch + 8 * n + 2 * q4]) =
-                            make_float2(o[m][4 * c0 + n][2 * h] * f[h], o[m][4 * c0 + n][2 * h + 1] * f[h]);
-                named_sync(kCT);
-                for (int i = threadIdx.x; i < 16 * kJoinCols; i += kCT) {
-                    const int row = i / kJoinCols, col = i % kJoinCols;
-                    float x = 0.0f;
-#pragma unroll
-                    for (int w = 0; w < kCW; ++w) x += join[(w * 16 + row) * kJoinPitch + col];
-                    const int d = out_channel<D, Q8>(4 * c0 + (col >> 3), (col >> 1) & 3, col & 1);
-                    if (16 * m + row < seg.nrows) ln.part_o[(size_t(slot) * RT + 16 * m + row) * D + d] = x;
-                }
-                named_sync(kCT);
+            for (int w = 0; w < kGW; ++w) l += rowstat[w * RT + row].y * ex2(rowstat[w * RT + row].x - mu);
+            row_ml[row] = make_float2(mu, l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l));  // no key: zeros
+            if (row < seg.nrows) {
+                if (alone)
+                    att_store_lse(a, seg.head, seg.row0 + row, mu, l);
+                else
+                    ln.part_ml[entry * RT + row] = make_float2(m, l);
             }
         }
+        worker_sync(me);
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            float f[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) f[c] = ex2(m_run[n][c] - row_ml[8 * n + 2 * q4 + c].x);
+#pragma unroll
+            for (int b0 = 0; b0 < MB; b0 += C::kJoinCols / 16) {
+                // kJoinCols channels of 8 rows per step; column 16 b + 8 h + g8
+                // is out_channel(b0 + b, h, g8)
+#pragma unroll
+                for (int b = 0; b < C::kJoinCols / 16; ++b)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        join[(wg * 8 + 2 * q4 + (x & 1)) * C::kJoinPitch + 16 * b + 8 * (x >> 1) + g8] =
+                            o[b0 + b][n][x] * f[x & 1];
+                worker_sync(me);
+                // a thread: two neighbouring channels d, d + 1 of a row
+#pragma unroll
+                for (int y = tid; y < 4 * C::kJoinCols; y += kGT) {
+                    const int jr = y & 7, pi = y >> 3, row = 8 * n + jr;
+                    const int c0 = Q8 ? 16 * (pi >> 3) + (pi & 7) : 2 * pi, c1 = c0 + (Q8 ? 8 : 1);
+                    const int d = Q8 ? out_channel<D, Q8>(b0 + (pi >> 3), 0, pi & 7) : 16 * b0 + c0;
+                    float x0 = 0.0f, x1 = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < kGW; ++w) {
+                        x0 += join[(w * 8 + jr) * C::kJoinPitch + c0];
+                        x1 += join[(w * 8 + jr) * C::kJoinPitch + c1];
+                    }
+                    if (row < seg.nrows) {
+                        if (alone) {
+                            const float inv = row_ml[row].y;
+                            *reinterpret_cast<uint32_t *>(att_out<D>(a, seg.head, seg.row0 + row) + d) =
+                                pack_bf16(x0 * inv, x1 * inv);
+                        } else {
+                            ln.part_o[(entry * D + d) * RT + row] = x0;
+                            ln.part_o[(entry * D + d + 1) * RT + row] = x1;
+                        }
+                    }
+                }
+                worker_sync(me);
+            }
+        }
+        if (!alone && !a.join) {
+            // the worker that is done with the unit's last segment adds them up
+            if (tid == 0) {  // (the step above ended with a barrier)
+                uint32_t before;
+                asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;"
+                             : "=r"(before)
+                             : "l"(&a.arrived[seg.unit])
+                             : "memory");
+                s_last[me] = before == uint32_t(n_seg - 1);
+                if (s_last[me]) a.arrived[seg.unit] = 0u;
+            }
+            worker_sync(me);
+            if (s_last[me]) {
+                constexpr int CH = RT * D / kGT, U = CH <= 4 ? 8 : CH <= 8 ? 4 : 1;
+                const int row = tid % RT, d0 = tid / RT * CH;
+                if (row < seg.nrows) {
+                    float m = kNegInf, l = 0.0f, acc[CH] = {};
+                    att_add<D, CH, U>(ln, int64_t(seg.unit) + first, n_seg, row, d0, m, l, acc);
+                    const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+                    uint32_t *dst = reinterpret_cast<uint32_t *>(att_out<D>(a, seg.head, seg.row0 + row) + d0);
+#pragma unroll
+                    for (int c = 0; c < CH; c += 2) dst[c / 2] = pack_bf16(acc[c] * inv, acc[c + 1] * inv);
+                    if (d0 == 0) att_store_lse(a, seg.head, seg.row0 + row, m == kNegInf ? 0.0f : m, l);
+                }
+            }
+        }
+        if (!more) break;
         t += n_tiles;
+        seg = next;
     }
 }
 
-// One warp per output row: the results of its segments in every line, under
-// the prefix and of its request, each from the first CTA to the last.
+// The join of the lines' results.  A warp has 32 query rows of a head (a lane
+// each) and kJC channels.
+constexpr int kJC = 4;
+
 template <int D>
 __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ AttendArgs a) {
-    constexpr int V = D / 32;
     const int lane = threadIdx.x & 31;
+    const int groups = (a.rows + 31) / 32;
+    const int w = int(blockIdx.x) * 8 + int(threadIdx.x >> 5), slices = D / kJC;
     pdl_launch_dependents();
     pdl_wait_previous();
-    const int64_t i = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (i >= int64_t(a.rows) * a.heads) return;
-    const int tok = int(i / (a.G * a.heads)), hq = int(i - int64_t(tok) * (a.G * a.heads));
-    const int head = hq / a.G, rho = tok * a.G + (hq - head * a.G), r = tok / a.T, in_req = rho - r * a.T * a.G;
-    // running maximum of the references, sum and output so far
-    float m = kNegInf, l = 0.0f, acc[V] = {};
-    const auto add = [&](const AttendLine &ln, int first, int n, int row) {
-        // entries (slot, half) first .. : reference and sum of up to 32 at once, a lane each
-        for (int k0 = 0; k0 < n * ln.halves; k0 += 32) {
-            const int left = min(32, n * ln.halves - k0);
-            const size_t e0 = size_t(first) * ln.halves + k0;
-            float2 ml = make_float2(kNegInf, 0.0f);
-            if (lane < left) ml = ln.part_ml[(e0 + lane) * ln.rt + row];
-            float top = ml.x;
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-            const float mn = fmaxf(m, top), mu = mn == kNegInf ? 0.0f : mn;
-            const float down = ex2(m - mu);
-            l *= down;
-#pragma unroll
-            for (int v = 0; v < V; ++v) acc[v] *= down;
-            m = mn;
-            const float f = ex2(ml.x - mu), lf = ml.y * f;
-#pragma unroll 8
-            for (int k = 0; k < left; ++k) {
-                const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
-                const float lk = __shfl_sync(0xFFFFFFFFu, lf, k);
-                l += lk;
-                // (an entry without keys may hold anything)
-                if (fk == 0.0f && lk == 0.0f) continue;
-                const float *src = ln.part_o + ((e0 + k) * ln.rt + row) * D + V * lane;
-                if (V == 4) {
-                    const float4 x = *reinterpret_cast<const float4 *>(src);
-                    acc[0] += x.x * fk, acc[1] += x.y * fk, acc[V - 2] += x.z * fk, acc[V - 1] += x.w * fk;
-                } else {
-                    const float2 x = *reinterpret_cast<const float2 *>(src);
-                    acc[0] += x.x * fk, acc[1] += x.y * fk;
-                }
-            }
-        }
-    };
-    for (int q = 0; q < kLines; ++q) {
-        const AttendLine &ln = a.line[q];
-        if (!ln.grid) continue;
-        const int np = ln.plan[0], c_r = ln.plan[1 + r], n_r = ln.plan[2 + r] - c_r;
-        const int per_head = ln.pu * np + ln.su * ln.plan[1 + a.R], total = per_head * a.heads;
-        const int units = ln.pu + a.R * ln.su;
-        if (ln.pu && np) {
-            const int p = rho / ln.rt, b = head * per_head + p * np, c = att_owner(total, ln.grid, b);
-            add(ln, head * units + p + c, att_owner(total, ln.grid, b + np - 1) - c + 1, rho - p * ln.rt);
-        }
-        if (ln.su && n_r) {
-            const int s = in_req / ln.rt, b = head * per_head + ln.pu * np + ln.su * c_r + s * n_r;
-            const int c = att_owner(total, ln.grid, b);
-            add(ln, head * units + ln.pu + r * ln.su + s + c, att_owner(total, ln.grid, b + n_r - 1) - c + 1,
-                in_req - s * ln.rt);
-        }
+    const int d0 = w % slices * kJC, head = w / slices / groups;
+    const int rho = w / slices % groups * 32 + lane;
+    if (head >= a.heads || rho >= a.rows) return;
+    const int r = rho / (a.T * a.G), in_req = rho - r * a.T * a.G;
+    const AttendLine &lp = a.line[kLinePrefix], &lq = a.line[kLineRequests], &lr = a.line[kLineRest];
+    const int32_t *cq = a.plan + 1, *cr = a.plan + a.R + 2;
+    const int np = a.plan[0], q0 = cq[r], q1 = cq[r + 1], qa = cq[a.R], r0 = cr[r], r1 = cr[r + 1], ra = cr[a.R];
+    float m = kNegInf, l = 0.0f, acc[kJC] = {};
+    if (lp.grid && np) {
+        const int p = rho / lp.rt, u = head * lp.pu + p, b = u * np, total = a.heads * lp.pu * np;
+        const int c = att_owner(total, lp.grid, b);
+        att_add<D, kJC, 4>(lp, int64_t(u + c) * lp.halves, (att_owner(total, lp.grid, b + np - 1) - c + 1) * lp.halves,
+                           rho - p * lp.rt, d0, m, l, acc);
+    }
+    if (lq.grid && q1 > q0) {
+        const int s = in_req / lq.rt, b = head * lq.su * qa + lq.su * q0 + s * (q1 - q0), total = a.heads * lq.su * qa;
+        const int c = att_owner(total, lq.grid, b);
+        att_add<D, kJC, 4>(lq, int64_t((head * a.R + r) * lq.su + s + c) * lq.halves,
+                           (att_owner(total, lq.grid, b + q1 - q0 - 1) - c + 1) * lq.halves, in_req - s * lq.rt, d0, m,
+                           l, acc);
+    }
+    {
+        const int s = in_req / lr.rt, b = head * lr.su * ra + lr.su * r0 + s * (r1 - r0), total = a.heads * lr.su * ra;
+        const int c = att_owner(total, lr.grid, b);
+        att_add<D, kJC, 2>(lr, int64_t((head * a.R + r) * lr.su + s) + c, att_owner(total, lr.grid, b + r1 - r0 - 1) - c + 1,
+                           in_req - s * lr.rt, d0, m, l, acc);
     }
     const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);  // no key: zeros
-    uint16_t *dst = a.out + int64_t(tok) * a.out_stride + int64_t(hq) * D + V * lane;
-    if (V == 4)
-        *reinterpret_cast<uint2 *>(dst) =
-            make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[V - 2] * inv, acc[V - 1] * inv));
-    else
-        *reinterpret_cast<uint32_t *>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
-    if (a.lse && lane == 0)
-        a.lse[int64_t(tok) * (a.G * a.heads) + hq] =
-            l == 0.0f ? kNegInf : ((m == kNegInf ? 0.0f : m) + log2f(l)) * 0.6931471805599453f;
+    *reinterpret_cast<uint2 *>(att_out<D>(a, head, rho) + d0) =
+        make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+    if (d0 == 0) att_store_lse(a, head, rho, m == kNegInf ? 0.0f : m, l);
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -682,20 +808,20 @@ int cache_map(CUtensorMap *m, void *base, int64_t rows, int dim, bool q8, int bo
 }
 
 // The dynamic shared-memory limit is raised once per device and variant.
-template <int D, bool Q8, int MT>
+template <int D, bool Q8, int NR>
 int run(const AttendArgs &a, void *stream) {
-    using C = ACfg<D, Q8, MT>;
+    using C = ACfg<D, Q8, NR>;
     static std::atomic<uint64_t> ready[4];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 256) return W12_ERR_CUDA;
     const uint64_t bit = uint64_t(1) << (dev & 63);
     if (!(ready[dev >> 6].load(std::memory_order_relaxed) & bit)) {
-        if (cudaFuncSetAttribute(attend_kernel<D, Q8, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(attend_kernel<D, Q8, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  int(C::kSmem)) != cudaSuccess)
             return W12_ERR_CUDA;
         ready[dev >> 6].fetch_or(bit, std::memory_order_relaxed);
     }
-    return launch_step(attend_kernel<D, Q8, MT>, a.line[a.self].grid, kAT, C::kSmem, 1, stream, a);
+    return launch_step(attend_kernel<D, Q8, NR>, a.line[kLineRest].grid / 2, C::kThreads, C::kSmem, 1, stream, a);
 }
 
 }  // namespace
@@ -709,17 +835,21 @@ int attend_make_maps(AttendArgs &a, const w12_kv *kv) {
     return st != W12_OK ? st : cache_map(&a.mv, kv->v, rows, kv->head_dim, q8, br);
 }
 
+template <int D, bool Q8>
+int run_rows(const AttendArgs &a, void *stream) {
+    const int rt = a.line[kLineRest].rt;
+    return rt == 8 ? run<D, Q8, 1>(a, stream) : rt == 16 ? run<D, Q8, 2>(a, stream) : run<D, Q8, 4>(a, stream);
+}
+
 int launch_attend_rest(const AttendArgs &a, int dim, int kv, void *stream) {
-    const bool q8 = kv == W12_KV_E4M3, two = a.line[kLineRest].rt > 16;
-    if (dim == 128)
-        return q8 ? (two ? run<128, true, 2>(a, stream) : run<128, true, 1>(a, stream))
-                  : (two ? run<128, false, 2>(a, stream) : run<128, false, 1>(a, stream));
-    return q8 ? (two ? run<64, true, 2>(a, stream) : run<64, true, 1>(a, stream))
-              : (two ? run<64, false, 2>(a, stream) : run<64, false, 1>(a, stream));
+    const bool q8 = kv == W12_KV_E4M3;
+    if (dim == 128) return q8 ? run_rows<128, true>(a, stream) : run_rows<128, false>(a, stream);
+    return q8 ? run_rows<64, true>(a, stream) : run_rows<64, false>(a, stream);
 }
 
 int launch_attend_join(const AttendArgs &a, int dim, void *stream) {
-    const int blocks = int((int64_t(a.rows) * a.heads + 7) / 8);
+    const int64_t warps = int64_t((a.rows + 31) / 32) * a.heads * (dim / kJC);
+    const int blocks = int((warps + 7) / 8);
     return dim == 128 ? launch_step(attend_join_kernel<128>, blocks, 256, 0, 1, stream, a)
                       : launch_step(attend_join_kernel<64>, blocks, 256, 0, 1, stream, a);
 }

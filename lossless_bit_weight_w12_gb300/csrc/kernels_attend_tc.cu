@@ -4,22 +4,24 @@
 // every key of these tiles is seen by every row, so there are no masks.
 //
 // A CTA has two slots, each a block of 128 query rows with its own region of
-// tensor memory -- scores S (64 columns; the weights P take their place),
-// output O (head_dim columns) and queries Q -- and its own four softmax
-// warps (thread = row = tensor-memory lane) and issuing thread.  Units of
-// 256 rows: slot s has rows 128 s .., both use every tile.  Units of 128
-// rows: the slots take alternate tiles, and their results are added up by
-// the join.  Per tile and slot:
-//   S = Q K^T      4 or 8 products, A = Q from tensor memory, B = keys as
-//                  they lie in the ring (K-major, 128-byte swizzle)
+// tensor memory -- scores S (128 columns; the weights P take their place) and
+// output O (head_dim columns) -- and its own four softmax warps (thread = row =
+// tensor-memory lane).  Units of 256 rows: slot s has rows
+// 128 s .., both use every tile.  Units of 128 rows: the slots take alternate
+// tiles, and their results are added up at the end.  Per tile of 128 keys
+// and slot:
+//   S = Q K^T      A = the queries in shared memory, B = the keys as they lie
+//                  in the ring (K-major, 128-byte swizzle)
 //   softmax        S to registers, maximum, exponentials, P back
-//   O += P V       4 products, A = P from tensor memory, B = values as they
-//                  lie in the ring (the channels contiguous)
-// While one slot's warps work on S the tensor cores work for the other.  Q
-// and P come from tensor memory so that shared memory only feeds B: a tile's
-// keys and values are read once per slot, 256 cycles of 512 that the
-// products take.  The issuing thread orders the products of its slot: S of
-// tile i + 1 overwrites P of tile i after the product that reads it.
+//   O += P V       A = P from tensor memory, B = the values as they lie in
+//                  the ring (the channels contiguous)
+// While one slot's warps work on S the tensor cores work for the other.  128
+// keys a tile, because a product of N = 64 takes nearly as long as one of N =
+// 128 (about 45 and 64 cycles), and because every hand-over between the warps
+// and the tensor cores costs some 200 cycles.  The issuing thread orders the
+// products of its slot: S of tile i + 1 overwrites P of tile i after the
+// product that reads it.  Keys and values are separate stages of the ring:
+// the keys' is free as soon as S is there.
 //
 // O stays in tensor memory.  It is rescaled only when the maximum has grown
 // by more than 2^8 since the last time (the exponentials are then at most
@@ -42,29 +44,52 @@ namespace w12 {
 namespace {
 
 constexpr float kNegInf = -INFINITY;
-constexpr int kProdWarp = 8;   // copies
-constexpr int kIssueWarp = 9;  // 9, 10: products of slot 0, 1
+constexpr int kProdWarp = 8;   // 8, 11: copies of keys, values
+constexpr int kIssueWarp = 9;  // 9, 10: products of slot 0, 1 (9 owns the tensor memory)
 constexpr int kConvWarp = 12;  // 12 .. 15: e4m3 to fp16
-constexpr uint32_t kTmem = 512, kSlotCols = 256, kOCol = 64, kQCol = 192;
+constexpr uint32_t kTmem = 512, kSlotCols = 256, kOCol = 128;
+constexpr int kKT = kAttTcTile;
 
 template <int D, bool Q8, bool TWO>
 struct TC {
     static constexpr int kThreads = Q8 ? 512 : 384;
-    static constexpr int kOpTile = kAttTile * D * 2;    // keys or values of a tile as operands
-    static constexpr int kOp = 2 * kOpTile;
-    static constexpr int kIn = AttStage<D, Q8>::kBytes;
-    static constexpr int kScales = (2 * kAttTile + 4) * 4;  // e4m3: per operand stage, scales and their bound
-    static constexpr int kFixed = int(sizeof(AttShared)) + 1024 + (Q8 ? 8 * kScales : 0);
-    // bf16: one ring, copies land as operands.  Units of 128 rows use stages
-    // alternately by slot: an even number keeps a stage with one slot.
-    static constexpr int SO = Q8 ? 4 : ((227 * 1024 - kFixed) / kOp > 8 ? 8 : ((227 * 1024 - kFixed) / kOp) & ~1);
-    static constexpr int kInFit = (227 * 1024 - kFixed - SO * kOp) / kIn;
+    // The softmax warps need the registers that the others do not: shares of
+    // the launch's 12 x 168 or 16 x 128 per lane.
+    static constexpr int kRegsSoftmax = Q8 ? 184 : 216, kRegsOther = 72;
+    static constexpr int kLaunchRegs = Q8 ? 16 * 128 : 12 * 168;
+    static_assert(8 * kRegsSoftmax + (kThreads / 32 - 8) * kRegsOther <= kLaunchRegs, "register shares");
+    static constexpr int kHalf = kKT * D * 2;           // keys, or values, of a tile as operands
+    static constexpr int kQ = (TWO ? 256 : 128) * D * 2;
+    static constexpr int kInScale = kKT * D;            // e4m3 input stage: codes, then 128 scales
+    static constexpr int kIn = Q8 ? kKT * D + 1024 : kHalf;
+    static constexpr int kScales = kKT + 4;             // floats per half tile: scales, and (values) their bound
+    // The keys' stage is free before the softmax has read their scales; a
+    // half tile's scales are written over 8 halves later, which the
+    // converters reach only after this tile's values were released.
+    static constexpr int kScaleRing = 8;
+    static constexpr int kFixed = (int(sizeof(AttShared)) + 15) / 16 * 16 + 1024 + (Q8 ? kScaleRing * kScales * 4 + 1024 : 0);
+    static constexpr int kRoom = 227 * 1024 - kFixed - kQ;
+    // Operand stages.  With units of 128 rows a stage has to stay with one
+    // slot (tile i: stages 2 i, 2 i + 1, slot i & 1): a multiple of 4.
+    // e4m3 leaves room for the input ring.
+    static constexpr int kOpFit = (Q8 ? kRoom - 3 * kIn : kRoom) / kHalf;
+    static constexpr int SO = TWO ? (kOpFit > 4 && Q8 ? 4 : kOpFit > 8 ? 8 : kOpFit) : kOpFit >= 8 && !Q8 ? 8 : 4;
+    static constexpr int kInFit = (kRoom - SO * kHalf) / kIn;
     static constexpr int SI = Q8 ? (kInFit > 8 ? 8 : kInFit) : SO;
-    static constexpr int kRing = Q8 ? SI * kIn + SO * kOp : SO * kOp;
-    static constexpr size_t kSmem = size_t(kRing) + kFixed;
-    static_assert(SO >= 2 && SI >= 2 && kSmem <= 227 * 1024, "shared memory");
-    static_assert((5 * 8 + 20) * 8 <= 1000, "barriers");
+    static constexpr int kRing = Q8 ? SI * kIn + SO * kHalf : SO * kHalf;
+    static constexpr size_t kSmem = size_t(kQ) + kRing + kFixed;
+    static_assert(SO >= 3 && SI >= 3 && SO <= 8 && (!Q8 || SO + 1 < kScaleRing) && (TWO || SO % 4 == 0) && kSmem <= 227 * 1024, "shared memory");
+    static_assert((4 * 8 + 12) * 8 + 32 <= 1008, "barriers");
 };
+
+template <int N>
+__device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
@@ -75,7 +100,7 @@ template <int D>
 __device__ __forceinline__ void convert_piece(uint32_t src, uint32_t dst, int key, int c) {
     const uint4 x = lds128(D == 128 ? src + uint32_t(key * 128 + ((c ^ (key & 7)) << 4))
                                     : src + uint32_t(key * 64 + ((c ^ ((key >> 1) & 3)) << 4)));
-    const uint32_t row = dst + uint32_t((c >> 2) * kAttTile * 128 + key * 128);
+    const uint32_t row = dst + uint32_t((c >> 2) * kKT * 128 + key * 128);
     const int p = 2 * (c & 3);
     sts128(row + uint32_t((p ^ (key & 7)) << 4), e4m3x2_lo_to_f16x2(x.x), e4m3x2_hi_to_f16x2(x.x),
            e4m3x2_lo_to_f16x2(x.y), e4m3x2_hi_to_f16x2(x.y));
@@ -89,23 +114,26 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
     constexpr int SO = C::SO, SI = C::SI, KS = D / 16;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t base = smem_addr(smem);
-    const uint32_t ops = base + uint32_t(Q8 ? SI * C::kIn : 0);  // the operand ring
-    AttShared &sh = *reinterpret_cast<AttShared *>(smem + C::kRing);
-    unsigned char *misc = smem + C::kRing + ((sizeof(AttShared) + 15) & ~size_t(15));
+    const uint32_t ring = base + uint32_t(C::kQ);                    // input ring (e4m3), operand ring
+    const uint32_t ops = ring + uint32_t(Q8 ? SI * C::kIn : 0);
+    unsigned char *fixed = smem + C::kQ + C::kRing;
+    AttShared &sh = *reinterpret_cast<AttShared *>(fixed);
+    unsigned char *misc = fixed + (sizeof(AttShared) + 15) / 16 * 16;
     uint64_t *in_full = reinterpret_cast<uint64_t *>(misc), *in_empty = in_full + SI;
     uint64_t *op_full = Q8 ? in_empty + SI : in_full, *op_empty = Q8 ? op_full + SO : in_empty;
     uint64_t *s_full = (Q8 ? op_empty + SO : in_empty + SI), *p_full = s_full + 2, *q_full = s_full + 4,
-             *o_done = s_full + 6, *fin = s_full + 8;
-    WaitCtl &ctl = *reinterpret_cast<WaitCtl *>(s_full + 10);
+             *o_done = s_full + 6, *fin = s_full + 8, *token = s_full + 10;
+    WaitCtl &ctl = *reinterpret_cast<WaitCtl *>(s_full + 12);
     uint32_t &s_tmem = *reinterpret_cast<uint32_t *>(reinterpret_cast<unsigned char *>(&ctl) + sizeof(WaitCtl));
-    float *scales = reinterpret_cast<float *>(misc + 1008 - 16);  // [SO][2 * 64 + 4], 16-byte aligned
+    float *scales = reinterpret_cast<float *>(misc + 1024);          // [kScaleRing][128 scales, their bound]
+    float *q_up = scales + (Q8 ? C::kScaleRing * C::kScales : 0);    // e4m3: [256] powers of two of the query rows
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (base & 1023u) {  // the swizzled boxes and operands need a 1024-byte aligned ring
+    if (base & 1023u) {  // the swizzled boxes and operands need 1024-byte aligned stages
         if (threadIdx.x == 0) record_error(a.err, W12_ERR_DEVICE);
         return;
     }
     if (threadIdx.x == 0) {
-        constexpr uint32_t kUsers = TWO ? 2 : 1;  // issuing threads that use a stage
+        constexpr uint32_t kUsers = TWO ? 2 : 1;  // slots that use a stage
         for (int s = 0; s < SI; ++s) {
             mbar_init(&in_full[s], 1);
             mbar_init(&in_empty[s], Q8 ? 4 : kUsers);
@@ -121,6 +149,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
             mbar_init(&q_full[s], 4);
             mbar_init(&o_done[s], 1);
             mbar_init(&fin[s], 1);
+            mbar_init(&token[s], 1);
         }
         ctl.abort = 0;
         ctl.limit_ns = a.wait_ns ? a.wait_ns : kWaitLimitNs;
@@ -134,7 +163,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
     }
     pdl_launch_dependents();
     pdl_wait_previous();
-    const AttPlan plan = att_plan(a, sh, C::kThreads);
+    const AttPlan plan = att_plan(a, sh, 1, 0);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
@@ -146,149 +175,85 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
     const auto first_tile = [](int i0, int slot) { return TWO ? 0 : (i0 & 1) != slot ? 1 : 0; };
     constexpr int kStep = TWO ? 1 : 2;
 
-    if (warp == kProdWarp) {
-        att_producer<D, Q8, SI>(a, plan, sh, base, in_full, in_empty, &ctl);
-    } else if (warp == kIssueWarp || warp == kIssueWarp + 1) {
-        // ------------------------------------------------------ products
-        const int slot = warp - kIssueWarp;
-        if (lane == 0) {
-            const uint32_t ts = tmem + uint32_t(slot) * kSlotCols, to = ts + kOCol, tq = ts + kQCol;
-            const uint32_t iqk = umma_idesc(Q8, kAttTile, false), ipv = umma_idesc(Q8, D, true);
-            uint32_t n_seg = 0, n_p = 0;
-            const auto scores = [&](int i) {
-                const int s = i % SO;
-                mbar_wait(&op_full[s], uint32_t(i / SO) & 1u, &ctl, a.err);
-                tmem_fence_after();
-                const uint64_t d = umma_desc_k(ops + uint32_t(s) * uint32_t(C::kOp));
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks)
-                    umma_tmem_a(ts, tq + 8u * uint32_t(ks),
-                                d + uint64_t(((ks >> 2) * kAttTile * 128 + 32 * (ks & 3)) >> 4), iqk, ks ? 1u : 0u);
-                umma_arrive(&s_full[slot]);
-            };
-            for (int t = t0; t < t1;) {
-                const AttSeg seg = att_locate(a, plan, sh, t);
-                const int n = min(seg.left, t1 - t), i0 = t - t0, k0 = first_tile(i0, slot);
-                t += n;
-                if (k0 >= n) continue;
-                mbar_wait(&q_full[slot], n_seg++ & 1u, &ctl, a.err);
-                tmem_fence_after();
-                scores(i0 + k0);
-                for (int k = k0; k < n; k += kStep) {
-                    const int i = i0 + k, s = i % SO;
-                    mbar_wait(&p_full[slot], n_p++ & 1u, &ctl, a.err);
-                    tmem_fence_after();
-                    const uint64_t d = umma_desc_mn(ops + uint32_t(s) * uint32_t(C::kOp) + uint32_t(C::kOpTile),
-                                                    kAttTile * 128);
-#pragma unroll
-                    for (int ks = 0; ks < kAttTile / 16; ++ks)
-                        umma_tmem_a(to, ts + 8u * uint32_t(ks), d + uint64_t((ks * 2048) >> 4), ipv,
-                                    (k > k0 || ks) ? 1u : 0u);
-                    umma_arrive(&op_empty[s]);
-                    if (k + kStep < n)
-                        scores(i + kStep);
-                    else
-                        umma_arrive(&o_done[slot]);
-                }
-            }
-            // every product issued has completed before the tensor memory is freed
-            umma_arrive(&fin[slot]);
-            mbar_drain(&fin[slot], 0u, ctl.limit_ns);
-        }
-        __syncwarp();
-    } else if (Q8 && warp >= kConvWarp) {
-        // ---------------------------------------------------- converters
-        const int cw = warp - kConvWarp;
-        // a quarter-warp's 8 lanes read the pieces 0-3 of an even key and 4-7
-        // of the next (128 channels), then the others: neither the reads nor
-        // the writes of the fp16 pieces share a bank
-        const int odd = (lane >> 2) & 1;
-        for (int t = t0; t < t1; ++t) {
-            const int i = t - t0, si = i % SI, so = i % SO;
-            mbar_wait(&in_full[si], uint32_t(i / SI) & 1u, &ctl, a.err);
-            if (i >= SO) mbar_wait(&op_empty[so], uint32_t(i / SO - 1) & 1u, &ctl, a.err);
-            const uint32_t src = base + uint32_t(si) * uint32_t(C::kIn);
-            const uint32_t dst = ops + uint32_t(so) * uint32_t(C::kOp);
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int key = 32 * h + 8 * cw + 2 * (lane >> 3) + odd;
-#pragma unroll
-                    for (int p = 0; p < D / 64; ++p)
-                        convert_piece<D>(src + uint32_t(kv * AttStage<D, Q8>::kTile), dst + uint32_t(kv * C::kOpTile),
-                                         key, (lane & 3) + (D == 128 ? 4 * (p ^ odd) : 0));
-                }
-            float *sc = scales + so * (2 * kAttTile + 4);
-            const uint32_t ss = src + uint32_t(AttStage<D, Q8>::kScale);
-            sc[32 * cw + lane] = __uint_as_float(lds32(ss + uint32_t(32 * cw + lane) * 4u));
-            if (cw == 0) {  // the bound of the tile's value scales
-                float top = fmaxf(__uint_as_float(lds32(ss + uint32_t(kAttTile + lane) * 4u)),
-                                  __uint_as_float(lds32(ss + uint32_t(kAttTile + 32 + lane) * 4u)));
-#pragma unroll
-                for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-                if (lane == 0) sc[2 * kAttTile] = exp_above(top) - 7.0f;
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&op_full[so]);
-                mbar_arrive(&in_empty[si]);
-            }
-        }
-    } else if (warp < kProdWarp) {
+    // tile i's keys (kv = 0) or values (1) are in operand stage (2 i + kv) % SO
+    const auto stage = [](int i, int kv) { return (2 * i + kv) % SO; };
+    const auto phase = [](int i, int kv) { return uint32_t((2 * i + kv) / SO) & 1u; };
+    // the roles, by warpgroup (a warpgroup changes its registers as one)
+    if (warp < kProdWarp) {
         // ------------------------------------------------------- softmax
+        regs_up<C::kRegsSoftmax>();
         const int slot = warp >> 2;
         const int row = 32 * (warp & 3) + lane;
         const uint32_t ts = tmem + uint32_t(slot) * kSlotCols + (uint32_t(32 * (warp & 3)) << 16);
-        const uint32_t to = ts + kOCol, tq = ts + kQCol;
+        const uint32_t to = ts + kOCol;
         uint32_t n_s = 0, n_seg = 0;
-        for (int t = t0; t < t1;) {
-            const AttSeg seg = att_locate(a, plan, sh, t);
-            const int n = min(seg.left, t1 - t), i0 = t - t0, k0 = first_tile(i0, slot);
-            t += n;
+        AttSeg seg = sh.first[0];
+#pragma unroll 1
+        for (int t = t0, n; t < t1; t += n) {
+            if (t > t0) att_next(a, plan, sh, seg);
+            const int i0 = t - t0, k0 = first_tile(i0, slot);
+            n = min(seg.left, t1 - t);
             const size_t entry = size_t(seg.unit + int(blockIdx.x)) * size_t(ln.halves) + (TWO ? 0 : slot);
             const int in_unit = (TWO ? 128 * slot : 0) + row;
             const bool valid = in_unit < seg.nrows;
             const bool warp_valid = __any_sync(0xFFFFFFFFu, valid);
             const size_t at = entry * size_t(ln.rt) + in_unit;
+            // ---- queries to shared memory, D / 8 lanes a row.  Units of 128
+            // rows have one copy for both slots: their warps wait for one
+            // another's products on the last one, then each copies half.
+            float sc = fabsf(a.scale_log2);
+            if (!TWO) named_sync(256);
+            {
+                constexpr int L = D / 8, RPW = 32 / L;            // lanes per row, rows per step of a warp
+                constexpr int kRows = TWO ? 32 : 16;              // rows of this warp
+                const int c = lane % L;
+                const uint32_t qb = base + uint32_t(TWO ? slot : 0) * uint32_t(128 * D * 2);
+                const uint32_t sign = a.scale_log2 < 0.0f ? 0x80008000u : 0u;  // scores grow with S
+                const int first = TWO ? 32 * (warp & 3) : 16 * warp;
+                constexpr int B = 8;                              // loads in flight
+#pragma unroll 1
+                for (int x0 = 0; x0 < kRows; x0 += B * RPW) {
+                    uint4 q[B];
+#pragma unroll
+                    for (int x = 0; x < B; ++x) {
+                        const int in_u = (TWO ? 128 * slot : 0) + first + x0 + x * RPW + lane / L;
+                        q[x] = make_uint4(0, 0, 0, 0);
+                        if (in_u < seg.nrows) {
+                            const int rho = seg.row0 + in_u, tok = rho / a.G, hq = seg.head * a.G + rho - tok * a.G;
+                            q[x] = *reinterpret_cast<const uint4 *>(a.q + tok * a.q_stride + int64_t(hq) * D + 8 * c);
+                        }
+                    }
+#pragma unroll
+                    for (int x = 0; x < B; ++x) {
+                        const int rq = first + x0 + x * RPW + lane / L;
+                        uint32_t w[4] = {q[x].x, q[x].y, q[x].z, q[x].w};
+                        if (Q8) {  // fp16, the row scaled by a power of two to below 2
+                            uint32_t top = 0;
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) top = max(top, max(w[y] & 0x7FFFu, (w[y] >> 16) & 0x7FFFu));
+                            top = __reduce_max_sync((L == 16 ? 0xFFFFu : 0xFFu) << (lane / L * L), top);
+                            const int e = max(-100, min(126, int(top >> 7) - 127));
+                            const float down = __uint_as_float(uint32_t(127 - e) << 23);
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                w[y] = pack_f16(bf16_bits_to_float(w[y] & 0xFFFFu) * down,
+                                                bf16_bits_to_float(w[y] >> 16) * down);
+                            if (c == 0) q_up[(TWO ? 128 * slot : 0) + rq] = __uint_as_float(uint32_t(127 + e) << 23);
+                        }
+                        sts128(qb + uint32_t((c >> 3) * 128 * 128 + rq * 128) + uint32_t(((c & 7) ^ (rq & 7)) << 4),
+                               w[0] ^ sign, w[1] ^ sign, w[2] ^ sign, w[3] ^ sign);
+                    }
+                }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            if (TWO)
+                __syncwarp();
+            else
+                named_sync(256);
+            if (Q8) sc *= q_up[in_unit];
             if (k0 >= n) {  // no tile of the segment is this slot's
                 if (valid) ln.part_ml[at] = make_float2(kNegInf, 0.0f);
                 continue;
-            }
-            // ---- queries to tensor memory
-            float sc = fabsf(a.scale_log2);
-            if (warp_valid) {
-                uint32_t q[D / 2];
-#pragma unroll
-                for (int j = 0; j < D / 2; ++j) q[j] = 0u;
-                if (valid) {
-                    const int rho = seg.row0 + in_unit, tok = rho / a.G, hq = seg.head * a.G + rho - tok * a.G;
-                    const uint16_t *src = a.q + tok * a.q_stride + int64_t(hq) * D;
-#pragma unroll
-                    for (int j = 0; j < D / 8; ++j) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(src + 8 * j);
-                        q[4 * j] = x.x, q[4 * j + 1] = x.y, q[4 * j + 2] = x.z, q[4 * j + 3] = x.w;
-                    }
-                }
-                const uint32_t sign = a.scale_log2 < 0.0f ? 0x80008000u : 0u;  // scores grow with S
-                if (Q8) {
-                    uint32_t top = 0;
-#pragma unroll
-                    for (int j = 0; j < D / 2; ++j) top = max(top, max(q[j] & 0x7FFFu, (q[j] >> 16) & 0x7FFFu));
-                    int e = int(top >> 7) - 127;
-                    e = max(-100, min(126, e));
-                    const float down = __uint_as_float(uint32_t(127 - e) << 23);
-                    sc *= __uint_as_float(uint32_t(127 + e) << 23);
-#pragma unroll
-                    for (int j = 0; j < D / 2; ++j)
-                        q[j] = pack_f16(bf16_bits_to_float(q[j] & 0xFFFFu) * down, bf16_bits_to_float(q[j] >> 16) * down);
-                }
-#pragma unroll
-                for (int j = 0; j < D / 2; ++j) q[j] ^= sign;
-#pragma unroll
-                for (int j = 0; j < D / 2; j += 32) tmem_store32(tq + uint32_t(j), q + j);
-                tmem_wait_st();
             }
             tmem_fence_before();
             __syncwarp();
@@ -296,25 +261,26 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
 
             float m = kNegInf, l = 0.0f;
             for (int k = k0; k < n; k += kStep) {
-                const int i = i0 + k, so = i % SO;
-                mbar_wait(&s_full[slot], n_s++ & 1u, &ctl, a.err);
+                const int i = i0 + k;
+                att_wait(&s_full[slot], n_s++ & 1u, &ctl, a.err);
                 tmem_fence_after();
                 if (warp_valid) {
-                    float2 x[32];
-                    tmem_load32(ts, reinterpret_cast<uint32_t *>(x));
-                    tmem_load32(ts + 32u, reinterpret_cast<uint32_t *>(x + 16));
-                    const float4 *tab = nullptr;
+                    float2 x[kKT / 2];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_load32(ts + 32u * uint32_t(c), reinterpret_cast<uint32_t *>(x + 16 * c));
+                    const float *vsc = nullptr;
                     float lift = 0.0f;
                     if (Q8) {
-                        // (the scores are there, so the tile is: this does not wait)
-                        mbar_wait(&op_full[so], uint32_t(i / SO) & 1u, &ctl, a.err);
-                        tab = reinterpret_cast<const float4 *>(scales + so * (2 * kAttTile + 4));
-                        lift = scales[so * (2 * kAttTile + 4) + 2 * kAttTile];
+                        // (the keys are there, their product is)
+                        vsc = scales + (2 * i + 1) % C::kScaleRing * C::kScales;
+                        att_wait(&op_full[stage(i, 1)], phase(i, 1), &ctl, a.err);
+                        lift = vsc[kKT];
                     }
                     tmem_wait_ld();
                     if (Q8) {
+                        const float4 *tab = reinterpret_cast<const float4 *>(scales + 2 * i % C::kScaleRing * C::kScales);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
+                        for (int j = 0; j < kKT / 4; ++j) {
                             const float4 s4 = tab[j];
                             x[2 * j] = __fmul2_rn(x[2 * j], make_float2(s4.x, s4.y));
                             x[2 * j + 1] = __fmul2_rn(x[2 * j + 1], make_float2(s4.z, s4.w));
@@ -322,7 +288,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
                     }
                     float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], fmaxf(x[j].x, x[j].y));
+                    for (int j = 0; j < kKT / 2; ++j) mx[j & 3] = fmaxf(mx[j & 3], fmaxf(x[j].x, x[j].y));
                     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc + lift;
                     if (k == k0) {
                         m = top;
@@ -347,21 +313,21 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
                     const float mu = m == kNegInf ? 0.0f : m;
                     const float2 sc2 = make_float2(sc, sc), mu2 = make_float2(-mu, -mu);
                     float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-                    uint32_t p[32];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        float2 e = __ffma2_rn(x[j], sc2, mu2);
-                        e.x = ex2(e.x), e.y = ex2(e.y);
-                        sum[j & 1] = __fadd2_rn(sum[j & 1], e);
-                        if (Q8) {
-                            const float2 v = reinterpret_cast<const float2 *>(tab)[kAttTile / 2 + j];
-                            e = __fmul2_rn(e, v);
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t p[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            float2 e = __ffma2_rn(x[32 * c + j], sc2, mu2);
+                            e.x = ex2(e.x), e.y = ex2(e.y);
+                            sum[j & 1] = __fadd2_rn(sum[j & 1], e);
+                            if (Q8) e = __fmul2_rn(e, reinterpret_cast<const float2 *>(vsc)[32 * c + j]);
+                            p[j] = Q8 ? pack_f16(e.x, e.y) : pack_bf16(e.x, e.y);
                         }
-                        p[j] = Q8 ? pack_f16(e.x, e.y) : pack_bf16(e.x, e.y);
+                        tmem_store32(ts + 32u * uint32_t(c), p);
                     }
                     sum[0] = __fadd2_rn(sum[0], sum[1]);
                     l += sum[0].x + sum[0].y;
-                    tmem_store32(ts, p);
                     tmem_wait_st();
                 }
                 tmem_fence_before();
@@ -370,22 +336,172 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
             }
 
             // ---- the segment's result
-            mbar_wait(&o_done[slot], n_seg++ & 1u, &ctl, a.err);
+            att_wait(&o_done[slot], n_seg++ & 1u, &ctl, a.err);
             tmem_fence_after();
             if (warp_valid) {
                 if (valid) ln.part_ml[at] = make_float2(m, l);
-                float *dst = ln.part_o + at * D;
-#pragma unroll
+                // [channel][row]: a warp's rows are neighbours
+                float *dst = ln.part_o + entry * size_t(ln.rt) * D + in_unit;
+#pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
                     tmem_load32(to + uint32_t(c), o);
                     tmem_wait_ld();
                     if (valid)
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4)
-                            *reinterpret_cast<uint4 *>(dst + c + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                        for (int j = 0; j < 32; ++j) dst[size_t(c + j) * (TWO ? 256 : 128)] = __uint_as_float(o[j]);
                 }
             }
+        }
+    } else if (Q8 && warp >= kConvWarp) {
+        // ---------------------------------------------------- converters
+        regs_down<C::kRegsOther>();
+        const int cw = warp - kConvWarp;
+        // a quarter-warp's 8 lanes read the pieces 0-3 of an even key and 4-7
+        // of the next (128 channels), then the others: neither the reads nor
+        // the writes of the fp16 pieces share a bank
+        const int odd = (lane >> 2) & 1;
+        for (int h = 0; h < 2 * (t1 - t0); ++h) {  // keys and values in turn
+            const int si = h % SI, so = h % SO;
+            att_wait(&in_full[si], uint32_t(h / SI) & 1u, &ctl, a.err);
+            if (h >= SO) att_wait(&op_empty[so], uint32_t(h / SO - 1) & 1u, &ctl, a.err);
+            const uint32_t src = ring + uint32_t(si) * uint32_t(C::kIn);
+            const uint32_t dst = ops + uint32_t(so) * uint32_t(C::kHalf);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int key = 32 * q + 8 * cw + 2 * (lane >> 3) + odd;
+#pragma unroll
+                for (int p = 0; p < D / 64; ++p)
+                    convert_piece<D>(src, dst, key, (lane & 3) + (D == 128 ? 4 * (p ^ odd) : 0));
+            }
+            float *sc = scales + (h % C::kScaleRing) * C::kScales;
+            const uint32_t ss = src + uint32_t(C::kInScale);
+            sc[32 * cw + lane] = __uint_as_float(lds32(ss + uint32_t(32 * cw + lane) * 4u));
+            if (cw == 0 && (h & 1)) {  // the bound of the tile's value scales
+                uint32_t top = 0u;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float x = __uint_as_float(lds32(ss + uint32_t(32 * q + lane) * 4u));
+                    if (x <= 3.0e38f) top = max(top, __float_as_uint(x));
+                }
+                top = __reduce_max_sync(0xFFFFFFFFu, top);
+                if (lane == 0) sc[kKT] = exp_above(__uint_as_float(top)) - 7.0f;
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&op_full[so]);
+                mbar_arrive(&in_empty[si]);
+            }
+        }
+    } else {
+        regs_down<C::kRegsOther>();
+        if (warp == kProdWarp || warp == kProdWarp + 3) {
+            // -------------------------------------------------------- copies
+            // one warp for the keys, one for the values
+            const int kv = warp == kProdWarp ? 0 : 1, br = min(a.page, 64);
+            int issued = 0;
+            att_producer<kKT>(
+                a, plan, sh, br,
+                [&](int i) {
+                    const int h = 2 * i + kv, s = h % SI;
+                    const bool go =
+                        h < SI || (att_wait(&in_empty[s], uint32_t(h / SI - 1) & 1u, &ctl, a.err) && !aborted(&ctl));
+                    issued += go;
+                    return __all_sync(0xFFFFFFFFu, go) != 0;
+                },
+                [&](int i, int chunks) {
+                    mbar_expect_tx(&in_full[(2 * i + kv) % SI], uint32_t(chunks * br) * uint32_t(Q8 ? D + 4 : 2 * D));
+                },
+                [&](int i, int chunk, int row) {
+                    const int s = (2 * i + kv) % SI;
+                    const uint32_t st = ring + uint32_t(s) * uint32_t(C::kIn), at = uint32_t(chunk * br);
+                    const CUtensorMap *map = kv ? &a.mv : &a.mk;
+                    if (Q8) {
+                        tma_box(st + at * uint32_t(D), map, 0, row, &in_full[s]);
+                        bulk_bytes(st + uint32_t(C::kInScale) + at * 4u, (kv ? a.vs : a.ks) + row, uint32_t(br) * 4u,
+                                   &in_full[s]);
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < D / 64; ++x)
+                            tma_box(st + uint32_t(x * kKT * 128) + at * 128u, map, 64 * x, row, &in_full[s]);
+                    }
+                });
+            // after a timeout: let the copies in flight land before the CTA ends
+            if (lane == 0 && aborted(&ctl))
+                for (int j = issued - 1; j >= 0 && j >= issued - SI; --j) {
+                    const int h = 2 * j + kv;
+                    mbar_drain(&in_full[h % SI], uint32_t(h / SI) & 1u, kAttDrainNs);
+                }
+        } else if (warp == kIssueWarp || warp == kIssueWarp + 1) {
+            // -------------------------------------------------- products
+            // A thread per slot.  A burst is P V of a tile and Q K^T of the
+            // slot's next; the two threads take turns by a token, so that the
+            // tensor cores finish one slot's scores while the other's warps
+            // work on theirs (bursts that interleave end at the same time, and
+            // both slots wait at the same time), and each thread's waits --
+            // some 250 cycles even on a barrier that is complete, while
+            // products are in flight -- pass under the other's burst.
+            const int slot = warp - kIssueWarp;
+            if (lane == 0) {
+                const uint32_t iqk = umma_idesc(Q8, kKT, false), ipv = umma_idesc(Q8, D, true);
+                const uint32_t ts = tmem + uint32_t(slot) * kSlotCols;
+                const uint64_t dq = umma_desc_k(base + uint32_t((TWO ? slot : 0) * (128 * D * 2)));
+                uint32_t n_seg = 0, n_p = 0;
+                const auto scores = [&](int i, bool pass) {
+                    const int s = stage(i, 0);
+                    const uint64_t d = umma_desc_k(ops + uint32_t(s) * uint32_t(C::kHalf));
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) {
+                        const uint32_t in_half = 32u * uint32_t(ks & 3);  // 16 channels inside the swizzle atom
+                        umma_smem(ts, dq + uint64_t(((ks >> 2) * 128 * 128 + in_half) >> 4),
+                                  d + uint64_t(((ks >> 2) * kKT * 128 + in_half) >> 4), iqk, ks ? 1u : 0u);
+                        // (the other thread takes its time to see it)
+                        if (ks == KS / 2 - 1 && pass) mbar_arrive(&token[slot ^ 1]);
+                    }
+                    umma_arrive(&s_full[slot]);
+                    umma_arrive(&op_empty[s]);
+                };
+                AttSeg seg = sh.first[0];
+#pragma unroll 1
+                for (int t = t0, n; t < t1; t += n) {
+                    if (t > t0) att_next(a, plan, sh, seg);
+                    const int i0 = t - t0, k0 = first_tile(i0, slot);
+                    n = min(seg.left, t1 - t);
+                    if (k0 >= n) continue;
+                    att_wait(&q_full[slot], n_seg++ & 1u, &ctl, a.err);
+                    att_wait(&op_full[stage(i0 + k0, 0)], phase(i0 + k0, 0), &ctl, a.err);
+                    tmem_fence_after();
+                    scores(i0 + k0, false);
+#pragma unroll 1
+                    for (int k = k0; k < n; k += kStep) {
+                        const int i = i0 + k, s = stage(i, 1);
+                        const bool more = k + kStep < n;
+                        const int burst = TWO ? 2 * i + slot : i;  // of the CTA; odd ones are slot 1's
+                        att_wait(&op_full[s], phase(i, 1), &ctl, a.err);
+                        if (more) att_wait(&op_full[stage(i + kStep, 0)], phase(i + kStep, 0), &ctl, a.err);
+                        att_wait(&p_full[slot], n_p++ & 1u, &ctl, a.err);
+                        if (burst > 0) att_wait(&token[slot], uint32_t((burst - 1) / 2) & 1u, &ctl, a.err);
+                        tmem_fence_after();
+                        const uint64_t d = umma_desc_mn(ops + uint32_t(s) * uint32_t(C::kHalf), kKT * 128);
+#pragma unroll
+                        for (int ks = 0; ks < kKT / 16; ++ks) {
+                            umma_tmem_a(ts + kOCol, ts + 8u * uint32_t(ks), d + uint64_t((ks * 2048) >> 4), ipv,
+                                        (k > k0 || ks) ? 1u : 0u);
+                            if (ks == kKT / 32 - 1 && !more) mbar_arrive(&token[slot ^ 1]);
+                        }
+                        umma_arrive(&op_empty[s]);
+                        if (more)
+                            scores(i + kStep, true);
+                        else
+                            umma_arrive(&o_done[slot]);
+                    }
+                }
+                // every product issued has completed before the tensor memory is freed
+                umma_arrive(&fin[slot]);
+                mbar_drain(&fin[slot], 0u, ctl.limit_ns);
+            }
+            __syncwarp();
         }
     }
     tmem_fence_before();

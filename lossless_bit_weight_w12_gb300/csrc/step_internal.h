@@ -66,7 +66,8 @@ int launch_read(const ReadArgs &a, int head_dim, int kv_dtype, void *stream);
 
 // Attention (kernels_attend.cu, kernels_attend_tc.cu); the work split is
 // described in attend_device.cuh.
-constexpr int kAttTile = 64;  // keys per tile
+constexpr int kAttTile = 64;     // keys per tile of the register kernel
+constexpr int kAttTcTile = 128;  // of the tensor-memory kernel
 
 // One launch's share of the work: units, their tiles on a line, the CTAs
 // that cut it, and where the segments' results go.
@@ -74,18 +75,17 @@ struct AttendLine {
     int32_t pu, su;   // units per head: row blocks of all requests under the prefix, row blocks per request
     int32_t rt;       // query rows per unit
     int32_t halves;   // results per segment (2: its tiles in two alternating halves)
-    int32_t grid;     // CTAs; 0: the line is not used
-    int32_t *plan;    // tiles of a prefix unit, then the R + 1 cumulative tile counts of the requests
-    float *part_o;    // [slots][halves][rt][head_dim]
+    int32_t grid;     // workers that cut it (CTAs, or halves of CTAs); 0: the line is not used
+    float *part_o;    // [slots][halves][head_dim][rt]
     float2 *part_ml;  // [slots][halves][rt]: reference exponent (log2 units) and sum
 };
 
-// Lines: the tensor-memory kernel on the prefix's whole tiles, the same on
-// the requests' whole tiles, the register kernel on the rest.
+// Lines: the tensor-memory kernel on the prefix, the same on the requests'
+// whole tiles, the register kernel on the rest.
 enum { kLinePrefix = 0, kLineRequests = 1, kLineRest = 2, kLines = 3 };
 
 struct AttendArgs {
-    CUtensorMap mk, mv;  // the cache as rows of head_dim channels
+    CUtensorMap mk, mv;  // the cache as rows of head_dim channels; boxes of min(page, 64) rows
     const uint16_t *q;
     uint16_t *out;
     float *lse;
@@ -99,6 +99,9 @@ struct AttendArgs {
     int32_t self;      // the line of this launch
     float scale_log2;  // scale * log2(e)
     int *err;
+    uint32_t *arrived;  // [rest units] segments that are done; zero between calls
+    int32_t *plan;      // for the join: W, then the R + 1 cumulative tiles of kLineRequests and of kLineRest
+    int32_t join;       // 1: a join kernel adds up the results (other lines have some)
     uint64_t wait_ns;
     AttendLine line[kLines];
 };
