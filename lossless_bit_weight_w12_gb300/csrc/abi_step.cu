@@ -91,6 +91,12 @@ int plan_attend(const w12_kv *kv, int64_t R, int64_t T, int q_heads, int64_t max
     }
     l[kLineRest].rt = tg <= 8 ? 8 : tg <= 16 ? 16 : 32;
     l[kLineRest].su = blocks(tg, l[kLineRest].rt);
+    const int64_t own = max_len / kAttTile + 1;  // at most these many tiles of a request
+    for (int i = 0; i < kLines; ++i) {           // 32-bit tile numbers
+        if (own > kLim31 / (R * std::max(l[i].su, 1)) || shared > kLim31 / std::max(l[i].pu, 1) ||
+            own * R * l[i].su + shared * l[i].pu >= kLim31 / kv->heads)
+            return W12_ERR_SHAPE;
+    }
     int sms = 0;
     if (current_sms(&sms) != W12_OK) return W12_ERR_CUDA;
     size_t off = kWsHeader;
@@ -103,10 +109,7 @@ int plan_attend(const w12_kv *kv, int64_t R, int64_t T, int q_heads, int64_t max
         auto &n = l[i];
         if (n.pu + n.su == 0) continue;
         n.halves = i != kLineRest && n.rt == 128 ? 2 : 1;
-        const int64_t own = max_len / kAttTile + 1;  // at most these many tiles of a request
-        if (own > kLim31 / (R * std::max(n.su, 1)) || shared > kLim31 / std::max(n.pu, 1)) return W12_ERR_SHAPE;
         const int64_t tiles = own * R * n.su + shared * n.pu;
-        if (tiles >= kLim31 / kv->heads) return W12_ERR_SHAPE;
         // (the register kernel has two workers per CTA)
         const int64_t per = i == kLineRest ? 2 : 1;
         n.grid = int(per * std::max<int64_t>(1, std::min<int64_t>(sms, (tiles * kv->heads + per - 1) / per)));

@@ -95,19 +95,6 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, ui
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-// One 16-byte piece of an e4m3 row (16 channels) as two pieces of its fp16 row.
-template <int D>
-__device__ __forceinline__ void convert_piece(uint32_t src, uint32_t dst, int key, int c) {
-    const uint4 x = lds128(D == 128 ? src + uint32_t(key * 128 + ((c ^ (key & 7)) << 4))
-                                    : src + uint32_t(key * 64 + ((c ^ ((key >> 1) & 3)) << 4)));
-    const uint32_t row = dst + uint32_t((c >> 2) * kKT * 128 + key * 128);
-    const int p = 2 * (c & 3);
-    sts128(row + uint32_t((p ^ (key & 7)) << 4), e4m3x2_lo_to_f16x2(x.x), e4m3x2_hi_to_f16x2(x.x),
-           e4m3x2_lo_to_f16x2(x.y), e4m3x2_hi_to_f16x2(x.y));
-    sts128(row + uint32_t(((p + 1) ^ (key & 7)) << 4), e4m3x2_lo_to_f16x2(x.z), e4m3x2_hi_to_f16x2(x.z),
-           e4m3x2_lo_to_f16x2(x.w), e4m3x2_hi_to_f16x2(x.w));
-}
-
 template <int D, bool Q8, bool TWO>
 __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __grid_constant__ AttendArgs a) {
     using C = TC<D, Q8, TWO>;
@@ -360,20 +347,44 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
         // a quarter-warp's 8 lanes read the pieces 0-3 of an even key and 4-7
         // of the next (128 channels), then the others: neither the reads nor
         // the writes of the fp16 pieces share a bank
-        const int odd = (lane >> 2) & 1;
+        const int odd = (lane >> 2) & 1, key = 8 * cw + 2 * (lane >> 3) + odd;  // and + 32, 64, 96
+        uint32_t src_at[D / 64], dst_at[D / 64][2];
+#pragma unroll
+        for (int p = 0; p < D / 64; ++p) {
+            const int c = (lane & 3) + (D == 128 ? 4 * (p ^ odd) : 0);
+            src_at[p] = D == 128 ? uint32_t(key * 128 + ((c ^ (key & 7)) << 4))
+                                 : uint32_t(key * 64 + ((c ^ ((key >> 1) & 3)) << 4));
+            const uint32_t row = uint32_t((c >> 2) * kKT * 128 + key * 128);
+            const int w = 2 * (c & 3);
+            dst_at[p][0] = row + uint32_t((w ^ (key & 7)) << 4);
+            dst_at[p][1] = row + uint32_t(((w + 1) ^ (key & 7)) << 4);
+        }
+#pragma unroll 1
         for (int h = 0; h < 2 * (t1 - t0); ++h) {  // keys and values in turn
             const int si = h % SI, so = h % SO;
             att_wait(&in_full[si], uint32_t(h / SI) & 1u, &ctl, a.err);
             if (h >= SO) att_wait(&op_empty[so], uint32_t(h / SO - 1) & 1u, &ctl, a.err);
             const uint32_t src = ring + uint32_t(si) * uint32_t(C::kIn);
             const uint32_t dst = ops + uint32_t(so) * uint32_t(C::kHalf);
+            // 16-byte pieces of e4m3 rows (16 channels), each to two pieces of
+            // the fp16 row; all reads first.  (key & 7) and so the swizzles
+            // are the same for every q.
+            uint4 x[4 * (D / 64)];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int key = 32 * q + 8 * cw + 2 * (lane >> 3) + odd;
+            for (int q = 0; q < 4; ++q)
 #pragma unroll
-                for (int p = 0; p < D / 64; ++p)
-                    convert_piece<D>(src, dst, key, (lane & 3) + (D == 128 ? 4 * (p ^ odd) : 0));
-            }
+                for (int p = 0; p < D / 64; ++p) x[q * (D / 64) + p] = lds128(src + src_at[p] + uint32_t(32 * q * D));
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int p = 0; p < D / 64; ++p) {
+                    const uint4 &y = x[q * (D / 64) + p];
+                    const uint32_t to = dst + uint32_t(32 * q * 128);
+                    sts128(to + dst_at[p][0], e4m3x2_lo_to_f16x2(y.x), e4m3x2_hi_to_f16x2(y.x), e4m3x2_lo_to_f16x2(y.y),
+                           e4m3x2_hi_to_f16x2(y.y));
+                    sts128(to + dst_at[p][1], e4m3x2_lo_to_f16x2(y.z), e4m3x2_hi_to_f16x2(y.z), e4m3x2_lo_to_f16x2(y.w),
+                           e4m3x2_hi_to_f16x2(y.w));
+                }
             float *sc = scales + (h % C::kScaleRing) * C::kScales;
             const uint32_t ss = src + uint32_t(C::kInScale);
             sc[32 * cw + lane] = __uint_as_float(lds32(ss + uint32_t(32 * cw + lane) * 4u));

@@ -189,6 +189,23 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+_raw_stream = None
+
+
+def _stream_of(t, stream):
+    """The stream handle for a call on tensor t's device (the decode-step
+    calls take microseconds: the current stream is asked for without a
+    torch.cuda.Stream object where torch can)."""
+    global _raw_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda device: torch.cuda.current_stream(device).cuda_stream)
+    return _raw_stream(t.get_device())
+
+
 def _kn(w, layout):
     return (w.shape[0], w.shape[1]) if layout == LAYOUT_KN else (w.shape[1], w.shape[0])
 
@@ -405,22 +422,36 @@ class KVCache:
         return KVCache(*kv, *(torch.empty(shape[:3], device=device) for _ in range(2)))
 
 
-def _heads_ptr(t, heads: int, dim: int):
-    """Device pointer of [tokens, heads, dim] rows with contiguous heads (any token stride)."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"expected [tokens, {heads}, {dim}], got {tuple(t.shape)}")
+def _ptr(t):
+    """Address of a contiguous CUDA tensor (None: NULL)."""
+    if t is None:
+        return None
     if not t.is_cuda:
         raise ValueError("expected a CUDA tensor")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
-        raise ValueError("expected contiguous heads")
+    if not t.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
     return t.data_ptr()
 
 
-def _int32(t, what: str):
-    import torch
-    if t.dtype != torch.int32:
-        raise ValueError(f"{what}: expected int32")
-    return _dptr(t)
+def _heads_ptr(t, n: int, heads: int, dim: int, dtype):
+    """(address, token stride) of [n, heads, dim] rows of a type with contiguous heads."""
+    if t.shape != (n, heads, dim) or t.dtype is not dtype:
+        raise ValueError(f"expected {dtype} [{n}, {heads}, {dim}], got {t.dtype} {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    token, head, one = t.stride()
+    if one != 1 or (heads > 1 and head != dim):
+        raise ValueError("expected contiguous heads")
+    return t.data_ptr(), token
+
+
+def _typed_ptr(t, dtype, n: int, what: str):
+    """Address of a contiguous CUDA tensor of n elements of a type (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() != n:
+        raise ValueError(f"{what}: expected {n} elements of {dtype}")
+    return _ptr(t)
 
 
 def rope_table(positions: int, rot: int, base: float = 10000.0, mode: int = ROPE_SCALE_NONE, factor: float = 1.0,
@@ -441,36 +472,39 @@ def kv_append(kv: KVCache, q, k, v, block_table, kv_len, T: int, q_out, table=No
     table: the rotary table on the device (None: no rotation)."""
     import torch
     n, hq, dim = q.shape
-    R = kv_len.numel()
-    if n != R * T or block_table.shape[0] != R or not (q.dtype == k.dtype == v.dtype):
-        raise ValueError("q, k, v: R * T tokens of one type; block_table: R rows")
-    if q.dtype not in (torch.float32, torch.bfloat16) or q_out.dtype != torch.bfloat16:
-        raise ValueError("q, k, v: float32 or bfloat16; q_out: bfloat16")
-    if k.shape[0] != n or v.shape[0] != n or q_out.shape[0] != n:
-        raise ValueError("q, k, v, q_out: R * T tokens each")
+    R, blocks = block_table.shape
+    x = q.dtype
+    if n != R * T or dim != kv.head_dim or (x is not torch.float32 and x is not torch.bfloat16):
+        raise ValueError("q: R * T tokens of head_dim channels, float32 or bfloat16")
+    qp, qs = _heads_ptr(q, n, hq, dim, x)
+    kp, ks = _heads_ptr(k, n, kv.heads, dim, x)
+    vp, vs = _heads_ptr(v, n, kv.heads, dim, x)
+    op, os_ = _heads_ptr(q_out, n, hq, dim, torch.bfloat16)
     positions, rot = (0, 0) if table is None else table.shape
-    if table is not None and table.dtype != torch.float32:
-        raise ValueError("table: expected float32")
-    _check(lib().w12_kv_append(
-        kv.ref, _heads_ptr(q, hq, kv.head_dim), q.stride(0), _heads_ptr(k, kv.heads, kv.head_dim), k.stride(0),
-        _heads_ptr(v, kv.heads, kv.head_dim), v.stride(0), F32 if q.dtype == torch.float32 else BF16, R, T, hq,
-        _int32(block_table, "block_table"), block_table.shape[1], _int32(kv_len, "kv_len"), _dptr(table),
-        positions, rot, layout, _heads_ptr(q_out, hq, kv.head_dim), q_out.stride(0), _dptr(err_dev),
-        _stream(stream)), "w12_kv_append")
+    st = lib().w12_kv_append(kv.ref, qp, qs, kp, ks, vp, vs, F32 if x is torch.float32 else BF16, R, T, hq,
+                             _typed_ptr(block_table, torch.int32, R * blocks, "block_table"), blocks,
+                             _typed_ptr(kv_len, torch.int32, R, "kv_len"),
+                             _typed_ptr(table, torch.float32, positions * rot, "table"), positions, rot, layout, op,
+                             os_, _ptr(err_dev), _stream_of(q, stream))
+    if st:
+        raise W12Error(st, "w12_kv_append")
 
 
 def kv_read(kv: KVCache, block_table, cu_len, k_out, v_out, err_dev=None, stream=None):
     """Read rows 0 .. cu_len[r+1] - cu_len[r] - 1 of every request back, packed
     into k_out and v_out [tokens, heads, head_dim] bfloat16."""
     import torch
-    R = cu_len.numel() - 1
-    if block_table.shape[0] != R or k_out.dtype != torch.bfloat16 or v_out.dtype != torch.bfloat16:
-        raise ValueError("block_table: one row per request; outputs: bfloat16")
-    if k_out.shape != v_out.shape or k_out.shape[1:] != (kv.heads, kv.head_dim):
-        raise ValueError("outputs: [tokens, heads, head_dim]")
-    _check(lib().w12_kv_read(kv.ref, _int32(block_table, "block_table"), block_table.shape[1],
-                             _int32(cu_len, "cu_len"), R, k_out.shape[0], _dptr(k_out), _dptr(v_out),
-                             _dptr(err_dev), _stream(stream)), "w12_kv_read")
+    R, blocks = block_table.shape
+    n = k_out.shape[0]
+    kp, _ = _heads_ptr(k_out, n, kv.heads, kv.head_dim, torch.bfloat16)
+    vp, _ = _heads_ptr(v_out, n, kv.heads, kv.head_dim, torch.bfloat16)
+    if not (k_out.is_contiguous() and v_out.is_contiguous()):
+        raise ValueError("outputs: contiguous")
+    st = lib().w12_kv_read(kv.ref, _typed_ptr(block_table, torch.int32, R * blocks, "block_table"), blocks,
+                           _typed_ptr(cu_len, torch.int32, R + 1, "cu_len"), R, n, kp, vp, _ptr(err_dev),
+                           _stream_of(k_out, stream))
+    if st:
+        raise W12Error(st, "w12_kv_read")
 
 
 def attend_workspace_size(kv: KVCache, R: int, T: int, q_heads: int, max_len: int, prefix_len: int = 0) -> int:
@@ -485,18 +519,18 @@ def attend(kv: KVCache, q, block_table, kv_len, T: int, max_len: int, out, ws_de
     requests; lse_dev: float32 [R*T, q_heads] or None."""
     import torch
     n, hq, dim = q.shape
-    R = kv_len.numel()
-    if n != R * T or out.shape != q.shape or block_table.shape[0] != R:
-        raise ValueError("q and out: R * T tokens; block_table: R rows")
-    if q.dtype != torch.bfloat16 or out.dtype != torch.bfloat16:
-        raise ValueError("q and out: bfloat16")
-    if lse_dev is not None and (lse_dev.dtype != torch.float32 or lse_dev.numel() != n * hq):
-        raise ValueError("lse: float32 [R * T, q_heads]")
-    _check(lib().w12_attend(kv.ref, _heads_ptr(q, hq, kv.head_dim), q.stride(0), R, T, hq,
-                            _int32(block_table, "block_table"), block_table.shape[1], _int32(kv_len, "kv_len"),
-                            max_len, prefix_len, dim ** -0.5 if scale is None else scale,
-                            _heads_ptr(out, hq, kv.head_dim), out.stride(0), _dptr(lse_dev), _dptr(ws_dev),
-                            ws_dev.numel() * ws_dev.element_size(), _stream(stream)), "w12_attend")
+    R, blocks = block_table.shape
+    if n != R * T or dim != kv.head_dim:
+        raise ValueError("q: R * T tokens of head_dim channels")
+    qp, qs = _heads_ptr(q, n, hq, dim, torch.bfloat16)
+    op, os_ = _heads_ptr(out, n, hq, dim, torch.bfloat16)
+    st = lib().w12_attend(kv.ref, qp, qs, R, T, hq, _typed_ptr(block_table, torch.int32, R * blocks, "block_table"),
+                          blocks, _typed_ptr(kv_len, torch.int32, R, "kv_len"), max_len, prefix_len,
+                          dim ** -0.5 if scale is None else scale, op, os_,
+                          _typed_ptr(lse_dev, torch.float32, n * hq, "lse"), _ptr(ws_dev), ws_dev.nbytes,
+                          _stream_of(q, stream))
+    if st:
+        raise W12Error(st, "w12_attend")
 
 
 # ---------------------------------------------------- decode step: sampling
@@ -512,19 +546,20 @@ def sample(logits, R: int, T: int, u, tokens_dev, ws_dev, temperature=None, top_
     (float32) and top_k (int32): [R] or None; with accept_dev and next_dev the
     drafts are accepted against the sampled tokens."""
     import torch
-    if logits.dtype not in (torch.float32, torch.bfloat16) or logits.numel() != R * T * logits.shape[-1]:
-        raise ValueError("logits: float32 or bfloat16 [R * T, V]")
-    for t, n in ((temperature, R), (top_p, R), (min_p, R), (u, R * T), (prob_dev, R * T)):
-        if t is not None and (t.dtype != torch.float32 or t.numel() != n):
-            raise ValueError("temperature, top_p, min_p [R], u, prob [R * T]: float32")
-    for t, n in ((top_k, R), (tokens_dev, R * T), (draft_dev, R * (T - 1)), (accept_dev, R), (next_dev, R)):
-        if t is not None and (t.dtype != torch.int32 or t.numel() != n):
-            raise ValueError("top_k, accept, next [R], tokens [R * T], draft [R, T - 1]: int32")
-    _check(lib().w12_sample(_dptr(logits), F32 if logits.dtype == torch.float32 else BF16, R, T, logits.shape[-1],
-                            _dptr(temperature), _dptr(top_k), _dptr(top_p), _dptr(min_p), _dptr(u),
-                            _dptr(tokens_dev), _dptr(prob_dev), _dptr(draft_dev), _dptr(accept_dev),
-                            _dptr(next_dev), _dptr(ws_dev), ws_dev.numel() * ws_dev.element_size(),
-                            _stream(stream)), "w12_sample")
+    x, f32, i32 = logits.dtype, torch.float32, torch.int32
+    V = logits.shape[-1]
+    n = R * T
+    if x is not f32 and x is not torch.bfloat16:
+        raise ValueError("logits: float32 or bfloat16")
+    st = lib().w12_sample(_typed_ptr(logits, x, n * V, "logits"), F32 if x is f32 else BF16, R, T, V,
+                          _typed_ptr(temperature, f32, R, "temperature"), _typed_ptr(top_k, i32, R, "top_k"),
+                          _typed_ptr(top_p, f32, R, "top_p"), _typed_ptr(min_p, f32, R, "min_p"),
+                          _typed_ptr(u, f32, n, "u"), _typed_ptr(tokens_dev, i32, n, "tokens"),
+                          _typed_ptr(prob_dev, f32, n, "prob"), _typed_ptr(draft_dev, i32, R * (T - 1), "draft"),
+                          _typed_ptr(accept_dev, i32, R, "accept"), _typed_ptr(next_dev, i32, R, "next"),
+                          _ptr(ws_dev), ws_dev.nbytes, _stream_of(logits, stream))
+    if st:
+        raise W12Error(st, "w12_sample")
 
 
 # --------------------------------------------------------------- helpers

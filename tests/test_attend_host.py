@@ -42,10 +42,13 @@ def test_workspace_size_refusals(w12):  # noqa: F811
 
 def test_binding_refusals(w12):  # noqa: F811
     import torch
-    with pytest.raises(ValueError):
-        w12._heads_ptr(torch.zeros(2, 4, 64), 4, 64)  # not on a GPU
-    with pytest.raises(ValueError):
-        w12._heads_ptr(torch.zeros(2, 4, 32), 4, 64)
-    with pytest.raises(ValueError):
-        w12._int32(torch.zeros(2), "kv_len")
+    x = torch.zeros(2, 4, 64)
+    for bad in (lambda: w12._heads_ptr(x, 2, 4, 64, torch.float32),        # not on a GPU
+                lambda: w12._heads_ptr(x, 2, 4, 32, torch.float32),        # another shape
+                lambda: w12._heads_ptr(x, 2, 4, 64, torch.bfloat16),       # another type
+                lambda: w12._typed_ptr(torch.zeros(2), torch.int32, 2, "kv_len"),
+                lambda: w12._typed_ptr(torch.zeros(2), torch.float32, 3, "u")):
+        with pytest.raises(ValueError):
+            bad()
+    assert w12._typed_ptr(None, torch.float32, 3, "lse") is None
     assert ctypes.sizeof(w12._CKV) == 56
