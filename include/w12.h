@@ -508,8 +508,9 @@ int w12_rope_table(int64_t positions, int rot, double base, const w12_rope_scali
  *   rope_dev: fp32 [rope_positions][rot] (w12_rope_table), 16-byte aligned;
  *     NULL with rot = 0: no rotation.  rot is a multiple of 8, at most
  *     head_dim; the channels from rot on are left as they are.
- *   q_out_dev: bf16, token stride q_out_stride (a multiple of 4), 8-byte
- *     aligned.  Padding tokens write nothing, here and in the cache.
+ *   q_out_dev: bf16, token stride q_out_stride (a multiple of 8), 16-byte
+ *     aligned, not overlapping the inputs.  Padding tokens write nothing, here
+ *     and in the cache.
  * W12_KV_E4M3: a row's scale is amax / 448 and its codes are
  * round(x * (448 / amax)) (nearest even); a row whose amax is at most 1e-30
  * is stored as zeros; one that holds a NaN or an infinity reads back as NaN.

@@ -145,11 +145,11 @@ extern "C" int w12_kv_append(const w12_kv *kv, const void *q, int64_t q_stride, 
     if (R * T >= kLim31) return W12_ERR_SHAPE;
     if (R == 0) return W12_OK;
     if (!q || !k || !v || !table || !kv_len || !q_out || (rot > 0 && !rope)) return W12_ERR_ARG;
-    const uintptr_t xa = x_dtype == W12_F32 ? 16 : 8;
-    if (!aligned(q, xa) || !aligned(k, xa) || !aligned(v, xa) || !aligned(q_out, 8) || !aligned(table, 4) ||
+    const uintptr_t xa = x_dtype == W12_F32 ? 16 : 8;  // four channels at a time
+    if (!aligned(q, xa) || !aligned(k, xa) || !aligned(v, xa) || !aligned(q_out, 16) || !aligned(table, 4) ||
         !aligned(kv_len, 4) || (rot > 0 && !aligned(rope, 16)) || (err && !aligned(err, 4)))
         return W12_ERR_ALIGN;
-    if ((q_stride | k_stride | v_stride | q_out_stride) & 3) return W12_ERR_ALIGN;
+    if (((q_stride | k_stride | v_stride) & 3) || (q_out_stride & 7)) return W12_ERR_ALIGN;
     int sms = 0;
     if (current_sms(&sms) != W12_OK) return W12_ERR_CUDA;
     AppendArgs a = {};
@@ -177,13 +177,15 @@ extern "C" int w12_kv_read(const w12_kv *kv, const int32_t *table, int64_t block
     if (!aligned(table, 4) || !aligned(cu_len, 4) || !aligned(k_out, 16) || !aligned(v_out, 16) ||
         (err && !aligned(err, 4)))
         return W12_ERR_ALIGN;
+    int sms = 0;
+    if (current_sms(&sms) != W12_OK) return W12_ERR_CUDA;
     ReadArgs a = {};
     a.kc = kv->k, a.vc = kv->v, a.ks = kv->k_scale, a.vs = kv->v_scale;
     a.table = table, a.cu_len = cu_len, a.k_out = k_out, a.v_out = v_out;
     a.R = R, a.tokens = tokens, a.table_cols = blocks, a.n_pages = kv->n_pages;
     a.heads = kv->heads, a.page = kv->page, a.page_log2 = log2_of(kv->page);
     a.err = err;
-    return launch_read(a, kv->head_dim, kv->dtype, stream);
+    return launch_read(a, kv->head_dim, kv->dtype, sms, stream);
 }
 
 extern "C" size_t w12_attend_workspace_size(const w12_kv *kv, int64_t R, int64_t T, int q_heads, int64_t max_len,

@@ -1,5 +1,5 @@
 // step_device.cuh -- small device helpers of the decode-step kernels:
-// dependent-launch control, bf16 and e4m3 conversions, the rotary turn.
+// dependent-launch control, bf16, fp16 and e4m3 conversions.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -47,15 +47,6 @@ __device__ __forceinline__ void e4m3x4_to_float(uint32_t w, float (&f)[4]) {
     const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&a));
     const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&b));
     f[0] = x.x, f[1] = x.y, f[2] = y.x, f[3] = y.y;
-}
-
-// The pair (x, y) turned by an angle with cosine c and sine s; each product
-// and the sum rounded by itself.
-__device__ __forceinline__ float turn_a(float x, float y, float c, float s) {
-    return __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
-}
-__device__ __forceinline__ float turn_b(float x, float y, float c, float s) {
-    return __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
 }
 
 }  // namespace w12

@@ -49,6 +49,7 @@ struct AppendArgs {
     const float *rope;
     int64_t rope_positions, tokens, table_cols, n_pages;
     int32_t T, q_heads, heads, page, page_log2, rot, interleaved;
+    int32_t parts;  // groups of lanes per token
     int *err;
 };
 int launch_append(const AppendArgs &a, int x_dtype, int head_dim, int kv_dtype, int sms, void *stream);
@@ -62,7 +63,7 @@ struct ReadArgs {
     int32_t heads, page, page_log2;
     int *err;
 };
-int launch_read(const ReadArgs &a, int head_dim, int kv_dtype, void *stream);
+int launch_read(const ReadArgs &a, int head_dim, int kv_dtype, int sms, void *stream);
 
 // Attention (kernels_attend.cu, kernels_attend_tc.cu); the work split is
 // described in attend_device.cuh.
@@ -120,6 +121,7 @@ struct SampleArgs {
     int64_t V, rows, R, T;
     int32_t chunk;      // logits per CTA of a row's cluster
     int32_t resident;   // the chunk fits in shared memory
+    int32_t keep_w;     // and so do its weights
     int32_t vec;        // 16-byte loads: every chunk starts on a 16-byte boundary
 };
 int launch_sample(SampleArgs &a, int dtype, int sms, void *stream);

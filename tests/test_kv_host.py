@@ -124,7 +124,7 @@ def test_append_refusals(w12):
                      (dict(k=None), E.ERR_ARG), (dict(v=None), E.ERR_ARG), (dict(table=None), E.ERR_ARG),
                      (dict(lens=None), E.ERR_ARG), (dict(out=None), E.ERR_ARG), (dict(rope=None), E.ERR_ARG),
                      (dict(q=DEV + 4), E.ERR_ALIGN), (dict(dt=E.F32, k=DEV + 8), E.ERR_ALIGN),
-                     (dict(out=DEV + 4), E.ERR_ALIGN), (dict(rope=DEV + 8), E.ERR_ALIGN),
+                     (dict(out=DEV + 4), E.ERR_ALIGN), (dict(out=DEV + 8), E.ERR_ALIGN), (dict(rope=DEV + 8), E.ERR_ALIGN),
                      (dict(qs=514), E.ERR_ALIGN), (dict(os=257), E.ERR_ALIGN), (dict(err=DEV + 2), E.ERR_ALIGN)]:
         assert _append(w12, **kw) == want, kw
     for kw, want in KV_REFUSALS:
