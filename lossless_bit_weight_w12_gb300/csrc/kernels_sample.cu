@@ -11,14 +11,26 @@
 // below the largest logit) can neither be drawn nor change a sum.
 //
 // A row is read once: a cluster of up to 8 CTAs keeps it in distributed
-// shared memory (151936 fp32 logits: 74 KB a CTA).  Passes over the resident
-// row: maximum (with the load); for top-k and top-p each a histogram of
-// counts or weights over 2048 bins linear in (max - x) / t, merged over the
-// cluster (each CTA adds up its share of the bins of all), then the one bin
-// that holds the threshold is gathered and ranked in one CTA, after further
-// histograms over its composite range while it is too full (many equal
-// logits); last the weights by warp in index order, and the draw inside one
-// warp's part.
+// shared memory (151936 fp32 logits: 74 KB a CTA).  The work on it:
+//  - maximum, with the load;
+//  - top_k up to 1024: the k-th largest of the threads' own maxima bounds the
+//    k-th largest logit from below, so one histogram entry per thread gives a
+//    bin (linear in (max - x) / t) above which all of the first k lie; they
+//    are gathered in one CTA, which ranks them, cuts by top_p and min_p and
+//    draws, alone;
+//  - top_p over a whole row: the weights, kept in the logits' place (bf16:
+//    beside them), and their sum; a sample of them -- the first eight of every
+//    thread -- tells about where top_p of the sum is reached.  The tokens
+//    around it, about 2500, are gathered in one CTA, which finds the boundary
+//    from the exact sum of those above;
+//  - where they are more than fit or do not hold it after all, and for larger
+//    top_k: a histogram (64 bins per octave of weight) over the cluster of the
+//    tokens that can matter -- a weight below (1 - top_p) of the mean cannot
+//    hold the boundary -- the one bin that holds the boundary gathered and
+//    ranked in one CTA, after further histograms over its composite range
+//    while it is too full (many equal logits);
+//  - the draw: a thread has consecutive tokens, so the sums of the threads
+//    give the one that holds the token, and its warp looks at them again.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -39,28 +51,59 @@ using u64 = unsigned long long;
 constexpr int kST = 512;               // threads per CTA
 constexpr int kSW = kST / 32;
 constexpr int kBins = 2048;
-constexpr int kCap = 1024;             // members of the threshold bin that are ranked directly
+constexpr int kCap = 1024;             // tokens that are ranked directly, one against all
+constexpr int kWide = 4096;            // tokens that can be gathered for a nucleus' boundary
+constexpr int kOwn = 2048;             // of them from one CTA
+constexpr int kAround = 1250;          // tokens to either side of where the sample sees the boundary
+constexpr int kTaken = 8;              // sampled tokens per thread
 constexpr int kMaxCluster = 8;
 constexpr float kOne31 = 2147483648.0f;
 constexpr float kSpan = 22.25f;        // e^-22.25 rounds to weight 0
 
-struct SampleShared {
-    // counts; weights in two 16-bit halves (a bin's sums stay below 2^32 for
-    // the 65536 logits a CTA can have at most)
-    uint32_t cnt[kBins], lo[kBins], hi[kBins];
-    u64 list[kCap];                             // composites of the threshold bin (CTA 0 of the cluster)
-    uint32_t list_w[kCap];
-    u64 slice[2][kMaxCluster];                  // per CTA of the cluster: what it sent (two buffers)
+struct SampleSmall {
+    u64 slice[2][kMaxCluster];         // per CTA of the cluster: what it sent
     u64 slice2[kMaxCluster];
     u64 warp_sum[kSW];
     u64 found_above;
     u64 thr;
+    float top[kMaxCluster];
+    float warp_top[kSW];
     int found_bin;
     uint32_t list_n;
+    uint32_t mine_n;                   // tokens in this CTA's own list
+    u64 mass;                     // what weighs more than the window
+    uint32_t win_lo, win_end;          // window of weights
     int last;
 };
 
+// Only for top_k and top_p.
+struct SampleCut {
+    // counts; weights in two 16-bit halves (a bin's sums stay below 2^32 for
+    // the 65536 logits a CTA can have at most)
+    uint32_t cnt[kBins], lo[kBins], hi[kBins];
+    u64 list[kWide];                   // composites that were gathered (CTA 0 of the cluster)
+    uint32_t list_w[kWide];
+    uint32_t rank[kCap];
+    uint32_t own[kOwn];                // positions in this CTA's chunk, before they go there
+};
+
+constexpr size_t kSmallBytes = (sizeof(SampleSmall) + 15) & ~size_t(15), kCutBytes = (sizeof(SampleCut) + 15) & ~size_t(15);
+
+// Where the weights are kept: fp32 logits are overwritten by theirs, bf16 ones
+// (chunk: a multiple of 8) followed by them.
+template <int DT>
+__host__ __device__ constexpr size_t weights_at(int64_t chunk) {
+    return DT == W12_F32 ? 0 : size_t(chunk) * 2;
+}
+
 __device__ __forceinline__ u64 umax64(u64 a, u64 b) { return a > b ? a : b; }
+
+// acc + w, in one instruction
+__device__ __forceinline__ u64 add_wide(u64 acc, uint32_t w) {
+    u64 r;
+    asm("mad.wide.u32 %0, %1, 1, %2;" : "=l"(r) : "r"(w), "l"(acc));
+    return r;
+}
 
 __device__ __forceinline__ u64 warp_sum64(u64 x) {
 #pragma unroll
@@ -72,170 +115,230 @@ __device__ __forceinline__ u64 warp_max64(u64 x) {
     for (int o = 16; o >= 1; o >>= 1) x = umax64(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
     return x;
 }
-
-template <int DT>
-struct Row {
-    const void *x;  // this CTA's chunk (shared or global memory)
-    int n;          // logits in it
-    uint32_t first; // index of its first
-    float mx, inv_t;
-
-    __device__ __forceinline__ float at(int i) const {
-        const float v = DT == W12_F32 ? static_cast<const float *>(x)[i]
-                                      : bf16_bits_to_float(static_cast<const uint16_t *>(x)[i]);
-        return v != v ? -INFINITY : v;  // NaN is never sampled
+__device__ __forceinline__ u64 warp_scan64(u64 x, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 z = __shfl_up_sync(0xFFFFFFFFu, x, o);
+        if (lane >= o) x += z;
     }
-    __device__ __forceinline__ u64 comp(float v, int i) const { return pack_key(v, first + uint32_t(i)); }
-    // (max - x) / t as the exponent's argument, <= 0
-    __device__ __forceinline__ float arg(float v) const { return __fmul_rn(v == mx ? 0.0f : __fsub_rn(v, mx), inv_t); }
-    __device__ __forceinline__ uint32_t weight(float v) const {
-        const float d = arg(v);
-        if (!(d > -kSpan) || v == -INFINITY) return 0u;
-        return __float2uint_rn(expf(d) * kOne31);
-    }
-};
-
-// Which elements a histogram is over: composite >= thr, weight > 0, and, from
-// the second level on, lo <= composite <= hi.
-struct Range {
-    u64 thr, lo, hi;
-    int shift;   // bins of the composite range: (hi - composite) >> shift; -1: bins linear in the argument
-    int bin;     // after a level: the bin that holds the threshold
-};
+    return x;
+}
 
 __device__ __forceinline__ int arg_bin(float d) {
     const int b = int(-d * (float(kBins) / kSpan));
     return b < kBins ? b : kBins - 1;
 }
 
+// Bins of weights, largest first: 64 per octave of [1, 2^31].
+__device__ __forceinline__ int weight_bin(uint32_t w) {
+    return int(((158u << 23) - __float_as_uint(__uint2float_rz(w))) >> 17);
+}
+static_assert((31 << 6) < kBins, "octaves of weights");
+
 template <int DT>
-__device__ __forceinline__ bool in_bin(const Row<DT> &row, const Range &g, float v, u64 c) {
-    if (c < g.thr) return false;
-    if (g.shift < 0) return arg_bin(row.arg(v)) == g.bin;
-    return c >= g.lo && c <= g.hi && int((g.hi - c) >> g.shift) == g.bin;
+struct Row {
+    const void *x;      // this CTA's chunk (shared or global memory)
+    const uint32_t *w;  // its weights, once they are kept (shared memory), or NULL
+    int n;              // logits in it
+    int i0, i1;         // this thread's
+    bool vec;           // four at a time: the chunk starts on a 16- (bf16: 8-) byte boundary
+    bool inf;           // the largest is +infinity: such logits count as 0, the others as -infinity
+    uint32_t first;     // index of its first
+    float mx, inv_t;
+
+    __device__ __forceinline__ float clean(float v) const {
+        if (inf) return v == INFINITY ? 0.0f : -INFINITY;
+        return fmaxf(v, -INFINITY);  // NaN is never sampled
+    }
+    __device__ __forceinline__ float at(int i) const {
+        return clean(DT == W12_F32 ? static_cast<const float *>(x)[i]
+                                   : bf16_bits_to_float(static_cast<const uint16_t *>(x)[i]));
+    }
+    // logits i .. i + 3 (-infinity past the chunk); i is a multiple of 4
+    __device__ __forceinline__ void at4(int i, float (&v)[4]) const {
+        if (vec && i + 4 <= n) {
+            if (DT == W12_F32) {
+                const float4 f = reinterpret_cast<const float4 *>(x)[i >> 2];
+                v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+            } else {
+                const uint2 f = reinterpret_cast<const uint2 *>(x)[i >> 2];
+                v[0] = bf16_bits_to_float(f.x & 0xFFFFu), v[1] = bf16_bits_to_float(f.x >> 16);
+                v[2] = bf16_bits_to_float(f.y & 0xFFFFu), v[3] = bf16_bits_to_float(f.y >> 16);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = clean(v[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = i + j < n ? at(i + j) : -INFINITY;
+        }
+    }
+    __device__ __forceinline__ u64 comp(float v, int i) const { return pack_key(v, first + uint32_t(i)); }
+    // (max - x) / t as the exponent's argument, <= 0
+    __device__ __forceinline__ float arg(float v) const { return __fmul_rn(__fsub_rn(v, mx), inv_t); }
+    // (an argument of -infinity, or NaN -- an infinity times 0 -- gives 0)
+    __device__ __forceinline__ uint32_t weight(float v) const { return __float2uint_rn(expf(arg(v)) * kOne31); }
+    __device__ __forceinline__ uint32_t weight_at(int i) const { return w ? w[i] : weight(at(i)); }
+    __device__ __forceinline__ void weight4(int i, uint32_t (&y)[4]) const {
+        if (w) {  // (kept up to a multiple of 4)
+            const uint4 f = reinterpret_cast<const uint4 *>(w)[i >> 2];
+            y[0] = f.x, y[1] = f.y, y[2] = f.z, y[3] = f.w;
+        } else {
+            float v[4];
+            at4(i, v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = weight(v[j]);
+        }
+    }
+};
+
+// Which elements a histogram is over, from the second level on: lo <=
+// composite <= hi, in bins of 2^shift composites; shift -1: bins of weights.
+struct Range {
+    u64 lo, hi;
+    int shift;
+    int bin;     // after a level: the bin that holds the boundary
+};
+
+// Adds up this CTA's share of the bins over the cluster (v: a thread's up to
+// 4 bins from tid * pt on), and finds the boundary: the bin in which the sum
+// from bin 0 on (`above` before it) reaches `need`.  Returns the whole sum.
+// The bins may be written again when it returns.
+template <bool BYMASS>
+__device__ __forceinline__ void find_bin(cg::cluster_group &cl, SampleSmall &sh, SampleCut &cut, u64 above, u64 need,
+                                         int *bin, u64 *before_bin) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int cs = int(cl.num_blocks()), me = int(cl.block_rank());
+    const int per = kBins / cs, pt = (per + kST - 1) / kST;  // bins per CTA and per thread (1 .. 4)
+    cl.sync();
+    u64 v[4], mine = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        v[j] = 0;
+        const int b = tid * pt + j;
+        if (j < pt && b < per)
+            for (int c = 0; c < cs; ++c) {
+                const SampleCut *o = cl.map_shared_rank(&cut, c);
+                v[j] += BYMASS ? u64(o->lo[me * per + b]) + (u64(o->hi[me * per + b]) << 16)
+                               : u64(o->cnt[me * per + b]);
+            }
+        mine += v[j];
+    }
+    const u64 incl = warp_scan64(mine, lane);
+    if (lane == 31) sh.warp_sum[warp] = incl;
+    __syncthreads();
+    u64 before = incl - mine + above, total = 0;
+    for (int w = 0; w < kSW; ++w) {
+        if (w < warp) before += sh.warp_sum[w];
+        total += sh.warp_sum[w];
+    }
+    if (tid < cs) cl.map_shared_rank(&sh, tid)->slice2[me] = total;
+    if (tid == 0) sh.found_bin = -1;
+    cl.sync();
+    for (int c = 0; c < me; ++c) before += sh.slice2[c];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (v[j] && before < need && need <= before + v[j])  // one thread of the cluster
+            for (int c = 0; c < cs; ++c) {
+                SampleSmall *o = cl.map_shared_rank(&sh, c);
+                o->found_bin = me * per + tid * pt + j;
+                o->found_above = before;
+            }
+        before += v[j];
+    }
+    if (tid == 0 && me == 0) sh.list_n = 0u;
+    cl.sync();
+    *bin = sh.found_bin;
+    *before_bin = sh.found_above;
+}
+
+// The cluster's counts (cut.cnt added up) in every CTA's cut.lo; the caller's
+// next write to cut.cnt comes after another cluster barrier.
+__device__ __forceinline__ void add_counts(cg::cluster_group &cl, SampleCut &cut) {
+    const int cs = int(cl.num_blocks()), me = int(cl.block_rank()), g = kBins / 4 / cs;
+    cl.sync();
+    if (int(threadIdx.x) < g) {
+        const int at = me * g + threadIdx.x;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        for (int c = 0; c < cs; ++c) {
+            const uint4 x = reinterpret_cast<const uint4 *>(cl.map_shared_rank(&cut, c)->cnt)[at];
+            v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+        }
+        for (int c = 0; c < cs; ++c) reinterpret_cast<uint4 *>(cl.map_shared_rank(&cut, c)->lo)[at] = v;
+    }
+    cl.sync();
+}
+
+__device__ __forceinline__ void gather(cg::cluster_group &cl, SampleSmall &sh, SampleCut &cut, u64 c, uint32_t w) {
+    const uint32_t at = atomicAdd(&cl.map_shared_rank(&sh, 0)->list_n, 1u);
+    if (at < uint32_t(kCap)) {
+        SampleCut *root = cl.map_shared_rank(&cut, 0);
+        root->list[at] = c;
+        root->list_w[at] = w;
+    }
 }
 
 // The threshold composite of the tokens that are kept: by count (BYMASS
-// false: the first `need`) or by weight (those before which less than
-// ceil(p total) lies, at least one).  thr0: what an earlier cut has kept.
-// Every thread of the cluster calls it and gets the result.
+// false: the first `need`) or by weight (those before which less than `need`
+// lies), of those from thr0 on whose weight is at least w_min (the others
+// cannot hold the boundary).  Every thread of the cluster calls it and gets
+// the result.
 template <int DT, bool BYMASS>
-__device__ u64 select(cg::cluster_group &cl, SampleShared &sh, const Row<DT> &row, u64 thr0, u64 need, uint64_t p_fix) {
+__device__ __noinline__ u64 select(cg::cluster_group &cl, SampleSmall &sh, SampleCut &cut, const Row<DT> &row_, u64 thr0,
+                                   u64 need, uint32_t w_min) {
+    const Row<DT> row = row_;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cs = int(cl.num_blocks()), me = int(cl.block_rank());
-    Range g{thr0, 0ull, ~0ull, -1, 0};
+    Range g{0ull, ~0ull, -1, 0};
     u64 above = 0;  // count or weight above the range
+    // calls f(composite, weight, bin) for the elements of the level
+    const auto members = [&](auto f) {
+#pragma unroll 1
+        for (int i0 = row.i0; i0 < row.i1; i0 += 4) {
+            uint32_t w[4];
+            row.weight4(i0, w);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (w[j] < w_min || i0 + j >= row.i1) continue;
+                const u64 c = thr0 || g.shift >= 0 ? row.comp(row.at(i0 + j), i0 + j) : ~0ull;
+                if (c < thr0 || (g.shift >= 0 && (c < g.lo || c > g.hi))) continue;
+                f(i0 + j, w[j], g.shift < 0 ? weight_bin(w[j]) : int((g.hi - c) >> g.shift));
+            }
+        }
+    };
+#pragma unroll 1
     for (int level = 0; level < 8; ++level) {
-        for (int i = tid; i < kBins; i += kST) sh.cnt[i] = sh.lo[i] = sh.hi[i] = 0u;
+        for (int i = tid; i < kBins; i += kST) cut.cnt[i] = cut.lo[i] = cut.hi[i] = 0u;
         __syncthreads();
-        for (int i = tid; i < row.n; i += kST) {
-            const float v = row.at(i);
-            const u64 c = row.comp(v, i);
-            if (c < thr0) continue;
-            const uint32_t w = row.weight(v);
-            if (w == 0u) continue;
-            int b;
-            if (g.shift < 0) {
-                b = arg_bin(row.arg(v));
-            } else {
-                if (c < g.lo || c > g.hi) continue;
-                b = int((g.hi - c) >> g.shift);
-            }
+        members([&](int, uint32_t w, int b) {
             if (BYMASS) {
-                atomicAdd(&sh.lo[b], w & 0xFFFFu);
-                atomicAdd(&sh.hi[b], w >> 16);
+                atomicAdd(&cut.lo[b], w & 0xFFFFu);
+                if (w >> 16) atomicAdd(&cut.hi[b], w >> 16);
             } else {
-                atomicAdd(&sh.cnt[b], 1u);
+                atomicAdd(&cut.cnt[b], 1u);
             }
-        }
-        cl.sync();
-        // this CTA's share of the bins, added up over the cluster; a thread
-        // takes consecutive bins
-        const int per = kBins / cs, pt = (per + kST - 1) / kST;  // bins per CTA and per thread (1 .. 4)
-        u64 v[4], mine = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[j] = 0;
-            const int b = tid * pt + j;
-            if (j < pt && b < per)
-                for (int c = 0; c < cs; ++c) {
-                    const SampleShared *o = cl.map_shared_rank(&sh, c);
-                    v[j] += BYMASS ? u64(o->lo[me * per + b]) + (u64(o->hi[me * per + b]) << 16)
-                                   : u64(o->cnt[me * per + b]);
-                }
-            mine += v[j];
-        }
-        u64 incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const u64 z = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-            if (lane >= o) incl += z;
-        }
-        if (lane == 31) sh.warp_sum[warp] = incl;
-        __syncthreads();
-        u64 before = incl - mine, total = 0;
-        for (int w = 0; w < kSW; ++w) {
-            if (w < warp) before += sh.warp_sum[w];
-            total += sh.warp_sum[w];
-        }
-        if (tid < cs) cl.map_shared_rank(&sh, tid)->slice2[me] = total;
-        cl.sync();
-        u64 all = 0;
-        for (int c = 0; c < cs; ++c) {
-            if (c < me) before += sh.slice2[c];
-            all += sh.slice2[c];
-        }
-        if (level == 0) {
-            if (BYMASS) {
-                need = p_fix * (all >> 24) + ((p_fix * (all & 0xFFFFFFull) + 0xFFFFFFull) >> 24);
-                need = need < 1 ? 1 : need;
-            }
-            if (need >= all) return thr0;  // nothing is cut (uniform over the cluster)
-        }
-        before += above;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (v[j] && before < need && need <= before + v[j]) {  // one thread of the cluster
-                for (int c = 0; c < cs; ++c) {
-                    SampleShared *o = cl.map_shared_rank(&sh, c);
-                    o->found_bin = me * per + tid * pt + j;
-                    o->found_above = before;
-                }
-            }
-            before += v[j];
-        }
-        if (tid == 0 && me == 0) sh.list_n = 0u;
-        cl.sync();
-        g.bin = sh.found_bin;
-        above = sh.found_above;
+        });
+        find_bin<BYMASS>(cl, sh, cut, above, need, &g.bin, &above);
+        if (g.bin < 0) return thr0;  // fewer than `need` of them: nothing is cut
         // gather the bin's members in CTA 0
-        SampleShared *root = cl.map_shared_rank(&sh, 0);
         u64 top = 0, bottom = ~0ull;
-        for (int i = tid; i < row.n; i += kST) {
-            const float x = row.at(i);
-            const u64 c = row.comp(x, i);
-            if (!in_bin(row, g, x, c)) continue;
-            const uint32_t w = row.weight(x);
-            if (w == 0u) continue;
+        members([&](int i, uint32_t w, int b) {
+            if (b != g.bin) return;
+            const u64 c = row.comp(row.at(i), i);
             top = umax64(top, c);
             bottom = bottom < c ? bottom : c;
-            const uint32_t at = atomicAdd(&root->list_n, 1u);
-            if (at < kCap) {
-                root->list[at] = c;
-                root->list_w[at] = w;
-            }
-        }
+            gather(cl, sh, cut, c, w);
+        });
         cl.sync();
-        const uint32_t n = root->list_n;
-        if (n <= kCap) {
+        const uint32_t n = cl.map_shared_rank(&sh, 0)->list_n;
+        if (n <= uint32_t(kCap)) {
             if (me == 0) {
                 if (tid == 0) sh.thr = ~0ull;
                 __syncthreads();
                 for (uint32_t i = tid; i < n; i += kST) {
-                    const u64 c = sh.list[i];
+                    const u64 c = cut.list[i];
                     u64 b = above;
                     for (uint32_t j = 0; j < n; ++j)
-                        if (sh.list[j] > c) b += BYMASS ? u64(sh.list_w[j]) : 1ull;
+                        if (cut.list[j] > c) b += BYMASS ? u64(cut.list_w[j]) : 1ull;
                     if (b < need) atomicMin(&sh.thr, c);
                 }
                 __syncthreads();
@@ -273,12 +376,250 @@ __device__ u64 select(cg::cluster_group &cl, SampleShared &sh, const Row<DT> &ro
     return thr0;  // not reached: a level divides the 64-bit range by 2048
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kST) sample_kernel(const __grid_constant__ SampleArgs a) {
+// floor(u total / 2^24) with u in [0, 2^24)
+__device__ __forceinline__ u64 scaled(uint64_t u, u64 total) { return (__umul64hi(u, total) << 40) | ((u * total) >> 24); }
+
+__device__ __forceinline__ uint64_t fixed_u(float u) {
+    const float f = u * 16777216.0f;
+    return f >= 16777215.0f ? 16777215ull : f > 0.0f ? uint64_t(f) : 0ull;
+}
+
+// ceil(p total), at least 1: what lies before a token that stays
+__device__ __forceinline__ u64 nucleus(uint64_t p, u64 total) {
+    const u64 lim = p * (total >> 24) + ((p * (total & 0xFFFFFFull) + 0xFFFFFFull) >> 24);
+    return lim < 1 ? 1 : lim;
+}
+
+// The cut and the draw among n <= kCap gathered tokens, by one CTA (all
+// threads): the first k by rank, of those the nucleus p (2^24: all), of those
+// the weights from floor_w on.
+__device__ __forceinline__ void draw_from_list(SampleSmall &sh, SampleCut &cut, uint32_t n, uint32_t k, uint64_t p,
+                                               u64 floor_w, uint64_t u, int32_t *token, float *prob, bool *writer) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // a token's rank and the weight before it
+    u64 before[2];
+    uint32_t rank[2];
+    u64 mine = 0;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const uint32_t i = tid + q * kST;
+        before[q] = 0, rank[q] = ~0u;
+        if (i >= n) continue;
+        const u64 c = cut.list[i];
+        rank[q] = 0;
+        for (uint32_t j = 0; j < n; ++j)
+            if (cut.list[j] > c) {
+                before[q] += cut.list_w[j];
+                ++rank[q];
+            }
+        if (rank[q] < k) mine += cut.list_w[i];
+    }
+    mine = warp_sum64(mine);
+    __syncthreads();
+    if (lane == 0) sh.warp_sum[warp] = mine;
+    __syncthreads();
+    u64 total = 0;
+    for (int w = 0; w < kSW; ++w) total += sh.warp_sum[w];
+    const u64 lim = p >= (1ull << 24) ? ~0ull : nucleus(p, total);
+    // the weights that stay, in place of the others' zeros
+    u64 kept = 0;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const uint32_t i = tid + q * kST;
+        if (i >= n) continue;
+        const uint32_t w = cut.list_w[i];
+        cut.rank[i] = rank[q] < k && before[q] < lim && w >= floor_w ? w : 0u;
+        kept += cut.rank[i];
+    }
+    kept = warp_sum64(kept);
+    __syncthreads();
+    if (lane == 0) sh.warp_sum[warp] = kept;
+    __syncthreads();
+    total = 0;
+    for (int w = 0; w < kSW; ++w) total += sh.warp_sum[w];
+    if (total == 0) return;
+    *writer = false;
+    const u64 target = scaled(u, total);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const uint32_t i = tid + q * kST;
+        if (i >= n || cut.rank[i] == 0u) continue;
+        // the weight before it in index order (a composite's low half is ~index)
+        const uint32_t key = uint32_t(cut.list[i]);
+        u64 b = 0;
+        for (uint32_t j = 0; j < n; ++j)
+            if (uint32_t(cut.list[j]) > key) b += cut.rank[j];
+        if (b <= target && target < b + cut.rank[i]) {  // one thread
+            *token = int32_t(key_index(cut.list[i]));
+            *prob = __fdiv_rn(__uint2float_rn(cut.rank[i]), __ull2float_rn(total));
+            *writer = true;
+        }
+    }
+}
+
+// The bin of cut.lo (counts) in which the sum from bin 0 on reaches `need`, -1:
+// it does not.
+__device__ __forceinline__ int find_count(SampleSmall &sh, const SampleCut &cut, uint32_t need) {
+    static_assert(kBins == 4 * kST, "four bins a thread");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint4 v = reinterpret_cast<const uint4 *>(cut.lo)[tid];
+    const uint32_t c[4] = {v.x, v.y, v.z, v.w}, mine = v.x + v.y + v.z + v.w;
+    uint32_t before = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t z = __shfl_up_sync(0xFFFFFFFFu, before, o);
+        if (lane >= o) before += z;
+    }
+    if (lane == 31) sh.warp_sum[warp] = before;
+    if (tid == 0) sh.found_bin = -1;
+    __syncthreads();
+    before -= mine;
+    for (int w = 0; w < warp; ++w) before += uint32_t(sh.warp_sum[w]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (before < need && need <= before + c[j]) sh.found_bin = tid * 4 + j;
+        before += c[j];
+    }
+    __syncthreads();
+    return sh.found_bin;
+}
+
+// The smallest weight in the bins up to b (a bin's end is a float).
+__device__ __forceinline__ uint32_t bin_end(int b) {
+    return max(1u, __float2uint_ru(__uint_as_float((158u << 23) - (uint32_t(b + 1) << 17) + 1u)));
+}
+
+// From the sample's counts (cut.lo, by weight_bin) and what the nucleus leaves
+// out: the window of weights, from bin_end to bin_end, around its boundary.
+// `each`: logits per thread, of which kTaken were sampled.
+__device__ __forceinline__ void set_window(SampleSmall &sh, const SampleCut &cut, u64 room, int each) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const float part = each > kTaken ? float(kTaken) / float(each) : 1.0f;
+    const float want = __ull2float_rn(room) * part;
+    // the lightest first: the sums of what lies below are what counts
+    const int b0 = kBins - 4 - 4 * tid;
+    const uint4 v = *reinterpret_cast<const uint4 *>(&cut.lo[b0]);
+    const uint32_t c[4] = {v.w, v.z, v.y, v.x};
+    float w[4], mine = 0.0f;
+    uint32_t mine_n = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        // (a bin's middle; the exact sum is taken later)
+        w[j] = float(c[j]) * __uint_as_float((158u << 23) - (uint32_t(b0 + 3 - j) << 17) - (1u << 16));
+        mine += w[j];
+        mine_n += c[j];
+    }
+    float below = mine;
+    uint32_t below_n = mine_n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float x = __shfl_up_sync(0xFFFFFFFFu, below, o);
+        const uint32_t z = __shfl_up_sync(0xFFFFFFFFu, below_n, o);
+        if (lane >= o) below += x, below_n += z;
+    }
+    if (lane == 31) sh.warp_top[warp] = below, sh.warp_sum[warp] = below_n;
+    if (tid == 0) sh.found_above = ~0ull, sh.win_lo = 1u, sh.win_end = ~0u;
+    __syncthreads();
+    float all = 0.0f;
+    uint32_t all_n = 0;
+    for (int q = 0; q < kSW; ++q) {
+        if (q < warp) below += sh.warp_top[q], below_n += uint32_t(sh.warp_sum[q]);
+        all += sh.warp_top[q], all_n += uint32_t(sh.warp_sum[q]);
+    }
+    below -= mine, below_n -= mine_n;
+    {
+        // sampled tokens below the boundary: all, where even they weigh less
+        float x = below;
+        uint32_t n = below_n;
+        bool hit = false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (!hit && x + w[j] >= want) atomicMin(&sh.found_above, u64(n)), hit = true;
+            x += w[j], n += c[j];
+        }
+    }
+    __syncthreads();
+    const uint32_t n = sh.found_above == ~0ull ? all_n : uint32_t(sh.found_above);
+    const uint32_t d = uint32_t(float(kAround) * part) + 1u;
+    const uint32_t from = n > d ? n - d : 0u, to = n + d;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int b = b0 + 3 - j;
+        if (c[j] && below_n <= from && from < below_n + c[j] && from > 0u) sh.win_lo = bin_end(b);
+        if (c[j] && below_n <= to && to < below_n + c[j]) sh.win_end = b > 0 ? bin_end(b - 1) : ~0u;
+        below_n += c[j];
+    }
+    __syncthreads();
+}
+
+// In one CTA: the threshold composite among the n gathered tokens, which are
+// those of the window: the last before which, together with the window's
+// mass above, less than lim lies.  0: they do not hold it, or too many share
+// its bin.
+__device__ __forceinline__ u64 window_threshold(SampleSmall &sh, SampleCut &cut, uint32_t n, u64 lim) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    for (int i = tid; i < kBins; i += kST) cut.cnt[i] = cut.lo[i] = cut.hi[i] = 0u;
+    // bins over the floats between the window's ends
+    const uint32_t top = __float_as_uint(__uint2float_rz(min(sh.win_end, 0x80000000u)));
+    const uint32_t span = top - __float_as_uint(__uint2float_rz(sh.win_lo));
+    int shift = 0;
+    while (span >> shift >= uint32_t(kBins)) ++shift;
+    const auto bin_of = [&](uint32_t w) { return int((top - __float_as_uint(__uint2float_rz(w))) >> shift); };
+    if (tid == 0) sh.found_bin = -1, sh.list_n = 0u, sh.thr = ~0ull;
+    __syncthreads();
+    for (uint32_t i = tid; i < n; i += kST) {
+        const uint32_t w = cut.list_w[i];
+        const int b = bin_of(w);
+        atomicAdd(&cut.lo[b], w & 0xFFFFu);
+        if (w >> 16) atomicAdd(&cut.hi[b], w >> 16);
+    }
+    __syncthreads();
+    u64 v[4], mine = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        v[j] = u64(cut.lo[tid * 4 + j]) + (u64(cut.hi[tid * 4 + j]) << 16);
+        mine += v[j];
+    }
+    const u64 incl = warp_scan64(mine, lane);
+    if (lane == 31) sh.warp_sum[warp] = incl;
+    __syncthreads();
+    u64 before = sh.mass + incl - mine;
+    for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (v[j] && before < lim && lim <= before + v[j]) sh.found_bin = tid * 4 + j, sh.found_above = before;
+        before += v[j];
+    }
+    __syncthreads();
+    const int bin = sh.found_bin;
+    if (bin < 0) return 0;
+    for (uint32_t i = tid; i < n; i += kST)
+        if (bin_of(cut.list_w[i]) == bin) {
+            const uint32_t at = atomicAdd(&sh.list_n, 1u);
+            if (at < uint32_t(kCap)) cut.rank[at] = i;
+        }
+    __syncthreads();
+    const uint32_t m = sh.list_n;
+    if (m > uint32_t(kCap)) return 0;
+    for (uint32_t i = tid; i < m; i += kST) {
+        const u64 c = cut.list[cut.rank[i]];
+        u64 b = sh.found_above;
+        for (uint32_t j = 0; j < m; ++j)
+            if (cut.list[cut.rank[j]] > c) b += cut.list_w[cut.rank[j]];
+        if (b < lim) atomicMin(&sh.thr, c);
+    }
+    __syncthreads();
+    return sh.thr;
+}
+
+// CUT: top_k or top_p may be asked for.
+template <int DT, bool CUT>
+__global__ void __launch_bounds__(kST, CUT ? 1 : 2) sample_kernel(const __grid_constant__ SampleArgs a) {
     cg::cluster_group cl = cg::this_cluster();
     extern __shared__ __align__(16) unsigned char smem[];
-    SampleShared &sh = *reinterpret_cast<SampleShared *>(smem);
-    unsigned char *buf = smem + ((sizeof(SampleShared) + 15) & ~size_t(15));
+    SampleSmall &sh = *reinterpret_cast<SampleSmall *>(smem);
+    SampleCut &cut = *reinterpret_cast<SampleCut *>(smem + kSmallBytes);
+    unsigned char *buf = smem + kSmallBytes + (CUT ? kCutBytes : 0);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cs = int(cl.num_blocks()), me = int(cl.block_rank());
     const int64_t r = int64_t(blockIdx.x) / cs;
@@ -292,32 +633,41 @@ __global__ void __launch_bounds__(kST) sample_kernel(const __grid_constant__ Sam
     row.n = int(a.V - c0 > a.chunk ? a.chunk : a.V - c0 > 0 ? a.V - c0 : 0);
     const unsigned char *src = static_cast<const unsigned char *>(a.logits) + (r * a.V + row.first) * ES;
     row.x = a.resident ? static_cast<const void *>(buf) : static_cast<const void *>(src);
+    row.w = nullptr;
+    row.vec = a.resident || a.vec;
+    row.inf = false;
     row.mx = 0.0f, row.inv_t = 1.0f;
+    // consecutive logits per thread, an odd number of fours: neither fp32 nor
+    // bf16 fours of a warp share a bank (the same number in every CTA)
+    const int each = (((a.chunk + kST - 1) / kST + 3) / 4 | 1) * 4;
+    row.i0 = min(tid * each, row.n), row.i1 = min(row.i0 + each, row.n);
+    const int64_t req = r / a.T;
+    const float t = a.temperature ? a.temperature[req] : 1.0f;
+    const int32_t top_k = CUT && a.top_k ? a.top_k[req] : 0;
+    const bool few = CUT && top_k > 0 && top_k < a.V && top_k <= kCap && t > 0.0f;  // the first top_k in one CTA
+    if (CUT)
+        for (int i = tid; i < kBins; i += kST) cut.cnt[i] = 0u;
 
-    // ---- load, maximum
-    u64 best = 0;
+    // ---- load, maximum (fmaxf drops a NaN)
+    float best = -INFINITY;
     const int nv = a.vec ? row.n / VE : 0;
-    for (int i0 = tid; i0 < nv; i0 += 4 * kST) {
-        uint4 x[4];
+    for (int i0 = tid; i0 < nv; i0 += 8 * kST) {
+        uint4 x[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 8; ++k)
             if (i0 + k * kST < nv) x[k] = ldg_stream(src + size_t(i0 + k * kST) * 16);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 8; ++k) {
             const int i = i0 + k * kST;
             if (i >= nv) continue;
             if (a.resident) reinterpret_cast<uint4 *>(buf)[i] = x[k];
             const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                if (DT == W12_F32) {
-                    const float v = __uint_as_float(w[q]);
-                    if (v == v) best = umax64(best, row.comp(v, 4 * i + q));
-                } else {
-                    const float v0 = bf16_bits_to_float(w[q] & 0xFFFFu), v1 = bf16_bits_to_float(w[q] >> 16);
-                    if (v0 == v0) best = umax64(best, row.comp(v0, 8 * i + 2 * q));
-                    if (v1 == v1) best = umax64(best, row.comp(v1, 8 * i + 2 * q + 1));
-                }
+                if (DT == W12_F32)
+                    best = fmaxf(best, __uint_as_float(w[q]));
+                else
+                    best = fmaxf(best, fmaxf(bf16_bits_to_float(w[q] & 0xFFFFu), bf16_bits_to_float(w[q] >> 16)));
             }
         }
     }
@@ -331,100 +681,255 @@ __global__ void __launch_bounds__(kST) sample_kernel(const __grid_constant__ Sam
             if (a.resident) reinterpret_cast<uint16_t *>(buf)[i] = b;
             v = bf16_bits_to_float(b);
         }
-        if (v == v) best = umax64(best, row.comp(v, i));
+        best = fmaxf(best, v);
     }
-    best = warp_max64(best);
-    if (lane == 0) sh.warp_sum[warp] = best;
-    __syncthreads();
-    if (tid < cs) {
-        for (int w = 0; w < kSW; ++w) best = umax64(best, sh.warp_sum[w]);
-        cl.map_shared_rank(&sh, tid)->slice[0][me] = best;
-    }
-    cl.sync();
-    best = 0;
-    for (int c = 0; c < cs; ++c) best = umax64(best, sh.slice[0][c]);
-    {   // the logit back from its key
-        const uint32_t k = uint32_t(best >> 32);
-        row.mx = best ? __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k) : -INFINITY;
+    {
+        float m = best;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        if (lane == 0) sh.warp_top[warp] = m;
+        __syncthreads();
+        if (tid < cs) {
+            for (int w = 0; w < kSW; ++w) m = fmaxf(m, sh.warp_top[w]);
+            cl.map_shared_rank(&sh, tid)->top[me] = m;
+        }
+        cl.sync();
+        m = -INFINITY;
+        for (int c = 0; c < cs; ++c) m = fmaxf(m, sh.top[c]);
+        row.inf = m == INFINITY;
+        row.mx = row.inf ? 0.0f : m;
+        best = row.clean(best);
     }
 
-    const int64_t req = r / a.T;
-    const float t = a.temperature ? a.temperature[req] : 1.0f;
     int32_t token = -1;
     float prob = 0.0f;
     bool writer = me == 0 && tid == 0;
+    u64 floor_w = 1;
+    if (a.min_p) {
+        const float m = a.min_p[req];
+        if (m > 0.0f) floor_w = umax64(1ull, u64(ceilf(fminf(m, 2.0f) * kOne31)));
+    }
+    uint64_t p_fix = 1ull << 24;
+    if (CUT && a.top_p) {
+        const float p = rintf(a.top_p[req] * 16777216.0f);
+        if (!(p >= 16777216.0f)) p_fix = p > 0.0f ? uint64_t(p) : 0ull;
+    }
     if (row.mx == -INFINITY) {
         // nothing can be sampled
     } else if (!(t > 0.0f)) {
-        token = int32_t(key_index(best));
-        prob = 1.0f;
-    } else {
-        row.inv_t = __fdiv_rn(1.0f, t);
-        u64 thr = 0;
-        const int32_t k = a.top_k ? a.top_k[req] : 0;
-        if (k > 0 && k < a.V) thr = select<DT, false>(cl, sh, row, thr, u64(k), 0ull);
-        if (a.top_p) {
-            const float p = rintf(a.top_p[req] * 16777216.0f);
-            if (!(p >= 16777216.0f))
-                thr = select<DT, true>(cl, sh, row, thr, 0ull, p > 0.0f ? uint64_t(p) : 0ull);
+        // the lowest index of the largest (a composite's low half is ~index)
+        u64 first = 0;
+#pragma unroll 1
+        for (int i0 = row.i0; i0 < row.i1; i0 += 4) {
+            float v[4];
+            row.at4(i0, v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (v[j] == row.mx && i0 + j < row.i1) first = umax64(first, row.comp(v[j], i0 + j));
         }
-        u64 floor_w = 1;
-        if (a.min_p) {
-            const float m = a.min_p[req];
-            if (m > 0.0f) floor_w = umax64(1ull, u64(ceilf(fminf(m, 2.0f) * kOne31)));
-        }
-        // ---- weights by warp, in index order (each warp a contiguous part)
-        const int part = ((row.n + kSW - 1) / kSW + 31) & ~31;
-        const int p0 = min(warp * part, row.n), p1 = min(p0 + part, row.n);
-        const auto kept = [&](int i) -> uint32_t {
-            const float v = row.at(i);
-            if (row.comp(v, i) < thr) return 0u;
-            const uint32_t w = row.weight(v);
-            return w >= floor_w ? w : 0u;
-        };
-        u64 sum = 0;
-        for (int i = p0 + lane; i < p1; i += 32) sum += kept(i);
-        sum = warp_sum64(sum);
+        first = warp_max64(first);
+        if (lane == 0) sh.warp_sum[warp] = first;
         __syncthreads();
-        if (lane == 0) sh.warp_sum[warp] = sum;
-        __syncthreads();
-        if (tid < cs) {
-            u64 s = 0;
-            for (int w = 0; w < kSW; ++w) s += sh.warp_sum[w];
-            cl.map_shared_rank(&sh, tid)->slice[1][me] = s;
+        if (tid == 0) {
+            for (int w = 1; w < kSW; ++w) first = umax64(first, sh.warp_sum[w]);
+            cl.map_shared_rank(&sh, 0)->slice[0][me] = first;
         }
         cl.sync();
-        u64 before = 0, total = 0;
-        for (int c = 0; c < cs; ++c) {
-            if (c < me) before += sh.slice[1][c];
-            total += sh.slice[1][c];
+        if (writer) {
+            for (int c = 0; c < cs; ++c) first = umax64(first, sh.slice[0][c]);
+            token = int32_t(key_index(first));
+            prob = 1.0f;
         }
-        if (total > 0) {
-            const float uf = a.u[r] * 16777216.0f;
-            const uint64_t u = uf >= 16777215.0f ? 16777215ull : uf > 0.0f ? uint64_t(uf) : 0ull;
-            const u64 target = (__umul64hi(u, total) << 40) | ((u * total) >> 24);
-            for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
-            writer = false;
-            if (before <= target && target < before + sum) {  // one warp of the cluster
-                for (int i0 = p0; i0 < p1; i0 += 32) {
-                    const uint32_t w = i0 + lane < p1 ? kept(i0 + lane) : 0u;
-                    u64 incl = w;
+    } else {
+        row.inv_t = __fdiv_rn(1.0f, t);
+        bool done = false;
+        u64 thr = 0;
+        if (CUT && few) {
+            const float d = row.arg(best);
+            if (d > -kSpan) atomicAdd(&cut.cnt[arg_bin(d)], 1u);
+            if (tid == 0) sh.list_n = 0u;
+            add_counts(cl, cut);
+            const int bin = find_count(sh, cut, uint32_t(top_k));
+            // all logits down to the bin's end (fewer threads than top_k have
+            // a weight: everything that has one)
+            const float end = bin < 0 ? -kSpan : -(float(bin) + 1.01f) * (kSpan / float(kBins));
+#pragma unroll 2
+            for (int i0 = row.i0; i0 < row.i1; i0 += 4) {
+                float v[4];
+                row.at4(i0, v);
+                bool any = false;
 #pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const u64 z = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-                        if (lane >= o) incl += z;
+                for (int j = 0; j < 4; ++j) any = any || row.arg(v[j]) >= end;
+                if (!any) continue;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (!(row.arg(v[j]) >= end) || i0 + j >= row.i1) continue;
+                    const uint32_t w = row.weight(v[j]);
+                    if (w) gather(cl, sh, cut, row.comp(v[j], i0 + j), w);
+                }
+            }
+            cl.sync();
+            const uint32_t n = cl.map_shared_rank(&sh, 0)->list_n;
+            done = n <= uint32_t(kCap);
+            if (done) {
+                if (me == 0)
+                    draw_from_list(sh, cut, n, uint32_t(top_k), p_fix, floor_w, fixed_u(a.u[r]), &token, &prob, &writer);
+            } else {
+                cl.sync();  // all have read the count
+            }
+        }
+        if (!done) {
+            // ---- weights, and their sums in index order
+            uint32_t w_thr = 0;  // the threshold's weight
+            const auto set_thr = [&](u64 c) {
+                if (c == thr) return;
+                thr = c;
+                const uint32_t k = uint32_t(c >> 32);
+                w_thr = row.weight(__uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k));
+            };
+            const auto kept = [&](int i, uint32_t w) -> uint32_t {
+                if (CUT && (w < w_thr || (w == w_thr && w && thr && row.comp(row.at(i), i) < thr))) return 0u;
+                return w >= floor_w ? w : 0u;
+            };
+            u64 mine = 0, before, total;  // this thread's sum, what lies before it
+            const auto add_up = [&](int slot) {
+                const u64 incl = warp_scan64(mine, lane);
+                __syncthreads();
+                if (lane == 31) sh.warp_sum[warp] = incl;
+                __syncthreads();
+                if (tid < cs) {
+                    u64 s = 0;
+                    for (int w = 0; w < kSW; ++w) s += sh.warp_sum[w];
+                    cl.map_shared_rank(&sh, tid)->slice[slot][me] = s;
+                }
+                before = incl - mine;
+                for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
+                cl.sync();
+                total = 0;
+                for (int c = 0; c < cs; ++c) {
+                    if (c < me) before += sh.slice[slot][c];
+                    total += sh.slice[slot][c];
+                }
+            };
+            const bool cuts = CUT && ((top_k > 0 && top_k < a.V) || p_fix < (1ull << 24));
+            uint32_t *keep = cuts && a.keep_w ? reinterpret_cast<uint32_t *>(buf + weights_at<DT>(a.chunk)) : nullptr;
+            const bool wide = cuts && !(top_k > 0 && top_k < a.V);  // top_p over the whole row
+            if (CUT && wide && tid == 0) sh.mine_n = sh.list_n = 0u, sh.mass = 0;
+#pragma unroll 2
+            for (int i = row.i0; i < row.i1; i += 4) {
+                uint32_t w[4];
+                row.weight4(i, w);
+                if (keep) reinterpret_cast<uint4 *>(keep)[i >> 2] = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mine = add_wide(mine, cuts || w[j] >= floor_w ? w[j] : 0u);
+                if (CUT && wide && i < row.i0 + kTaken)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (w[j]) atomicAdd(&cut.cnt[weight_bin(w[j])], 1u);
+            }
+            if (keep) {
+                row.w = keep;
+                if (DT == W12_F32) row.x = src;  // (the few logits that are looked at again)
+                __syncthreads();
+            }
+            add_up(0);
+            if (CUT && wide) {
+                const u64 lim = nucleus(p_fix, total);
+                if (lim < total) {
+                    add_counts(cl, cut);
+                    set_window(sh, cut, total - lim, each);
+                    const uint32_t lo = sh.win_lo, end = sh.win_end;
+                    u64 more = 0;
+#pragma unroll 2
+                    for (int i = row.i0; i < row.i1; i += 4) {
+                        uint32_t w[4];
+                        row.weight4(i, w);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) more = add_wide(more, w[j] >= end ? w[j] : 0u);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (w[j] >= lo && w[j] < end && i + j < row.i1) {
+                                const uint32_t at = atomicAdd(&sh.mine_n, 1u);
+                                if (at < uint32_t(kOwn)) cut.own[at] = uint32_t(i + j);
+                            }
                     }
-                    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, before + incl > target);
-                    if (hit) {
-                        const int at = __ffs(hit) - 1;
-                        if (lane == at) {
-                            token = int32_t(row.first) + i0 + lane;
-                            prob = __fdiv_rn(__uint2float_rn(w), __ull2float_rn(total));
-                            writer = true;
+                    more = warp_sum64(more);
+                    SampleSmall *root = cl.map_shared_rank(&sh, 0);
+                    SampleCut *to = cl.map_shared_rank(&cut, 0);
+                    if (lane == 0 && more) atomicAdd(&root->mass, more);
+                    __syncthreads();
+                    const uint32_t n = sh.mine_n;
+                    // (a CTA with too many spoils the count)
+                    if (tid == 0) sh.found_bin = int(atomicAdd(&root->list_n, n <= uint32_t(kOwn) ? n : uint32_t(kWide) + 1u));
+                    __syncthreads();
+                    const uint32_t base = uint32_t(sh.found_bin);
+                    if (n <= uint32_t(kOwn))
+                        for (uint32_t q = tid; q < n && base + q < uint32_t(kWide); q += kST) {
+                            const int i = int(cut.own[q]);
+                            to->list[base + q] = row.comp(row.at(i), i);
+                            to->list_w[base + q] = row.weight_at(i);
                         }
-                        break;
+                    cl.sync();
+                    if (me == 0) {
+                        const uint32_t all = sh.list_n;
+                        __syncthreads();
+                        const u64 c = all <= uint32_t(kWide) ? window_threshold(sh, cut, all, lim) : 0ull;
+                        if (tid < cs) cl.map_shared_rank(&sh, tid)->slice2[0] = c;
                     }
-                    before += __shfl_sync(0xFFFFFFFFu, incl, 31);
+                    cl.sync();
+                    set_thr(sh.slice2[0]);
+                }
+            }
+            if (CUT && cuts) {
+                if (top_k > 0 && top_k < a.V) {
+                    set_thr(select<DT, false>(cl, sh, cut, row, thr, u64(top_k), 1u));
+                    mine = 0;
+                    for (int i = row.i0; i < row.i1; ++i) {
+                        const uint32_t w = row.weight_at(i);
+                        if (w > w_thr || (w && w == w_thr && row.comp(row.at(i), i) >= thr)) mine += w;
+                    }
+                    add_up(1);
+                }
+                if (p_fix < (1ull << 24) && !(wide && thr)) {
+                    const u64 lim = nucleus(p_fix, total);
+                    // weights below it add up to at most total - lim
+                    const u64 small = (total - lim) / u64(a.V);
+                    if (lim < total)
+                        set_thr(select<DT, true>(cl, sh, cut, row, thr, lim, uint32_t(small > 1 ? small : 1)));
+                }
+                mine = 0;
+#pragma unroll 2
+                for (int i = row.i0; i < row.i1; i += 4) {
+                    uint32_t w[4];
+                    row.weight4(i, w);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (w[j] >= w_thr && w[j]) mine += kept(i + j, w[j]);
+                }
+                add_up(wide ? 1 : 0);  // (not the slot of the sum before it)
+            }
+            if (total > 0) {
+                const u64 target = scaled(fixed_u(a.u[r]), total);
+                writer = false;
+                const uint32_t hit = __ballot_sync(0xFFFFFFFFu, before <= target && target < before + mine);
+                if (hit) {  // one warp of the cluster: the thread's logits again, a lane each
+                    const int src_lane = __ffs(hit) - 1;
+                    u64 b = __shfl_sync(0xFFFFFFFFu, before, src_lane);
+                    const int j1 = __shfl_sync(0xFFFFFFFFu, row.i1, src_lane);
+                    for (int j0 = __shfl_sync(0xFFFFFFFFu, row.i0, src_lane); j0 < j1; j0 += 32) {
+                        const uint32_t w = j0 + lane < j1 ? kept(j0 + lane, row.weight_at(j0 + lane)) : 0u;
+                        const u64 incl = warp_scan64(u64(w), lane);
+                        const uint32_t at = __ballot_sync(0xFFFFFFFFu, b + incl > target);
+                        if (at) {
+                            if (lane == __ffs(at) - 1) {
+                                token = int32_t(row.first) + j0 + lane;
+                                prob = __fdiv_rn(__uint2float_rn(w), __ull2float_rn(total));
+                                writer = true;
+                            }
+                            break;
+                        }
+                        b += __shfl_sync(0xFFFFFFFFu, incl, 31);
+                    }
                 }
             }
         }
@@ -456,23 +961,29 @@ __global__ void __launch_bounds__(kST) sample_kernel(const __grid_constant__ Sam
     if (tid == 0) *a.counter = 0u;
 }
 
-constexpr size_t kSharedFixed = (sizeof(SampleShared) + 15) & ~size_t(15);
 constexpr size_t kMostShared = 227 * 1024;
 
-template <int DT>
-int run(const SampleArgs &a, int cs, void *stream) {
+template <int DT, bool CUT>
+int run_t(const SampleArgs &a, int cs, void *stream) {
     static std::atomic<uint64_t> ready[4];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 256) return W12_ERR_CUDA;
     const uint64_t bit = uint64_t(1) << (dev & 63);
     if (!(ready[dev >> 6].load(std::memory_order_relaxed) & bit)) {
-        if (cudaFuncSetAttribute(sample_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMostShared)) !=
+        if (cudaFuncSetAttribute(sample_kernel<DT, CUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMostShared)) !=
             cudaSuccess)
             return W12_ERR_CUDA;
         ready[dev >> 6].fetch_or(bit, std::memory_order_relaxed);
     }
-    const size_t smem = kSharedFixed + (a.resident ? (size_t(a.chunk) * (DT == W12_F32 ? 4 : 2) + 15) / 16 * 16 : 0);
-    return launch_step(sample_kernel<DT>, int(a.rows * cs), kST, smem, cs, stream, a);
+    const size_t smem = kSmallBytes + (CUT ? kCutBytes : 0) +
+                        (a.keep_w ? weights_at<DT>(a.chunk) + size_t(a.chunk) * 4
+                                  : a.resident ? (size_t(a.chunk) * (DT == W12_F32 ? 4 : 2) + 15) / 16 * 16 : 0);
+    return launch_step(sample_kernel<DT, CUT>, int(a.rows * cs), kST, smem, cs, stream, a);
+}
+
+template <int DT>
+int run(const SampleArgs &a, int cs, void *stream) {
+    return a.top_k || a.top_p ? run_t<DT, true>(a, cs, stream) : run_t<DT, false>(a, cs, stream);
 }
 
 }  // namespace
@@ -487,7 +998,9 @@ int launch_sample(SampleArgs &a, int dtype, int sms, void *stream) {
     const int64_t chunk = ((a.V + cs - 1) / cs + 7) / 8 * 8;
     static_assert(W12_SAMPLE_MAX_V <= kMaxCluster * 65536, "16-bit halves of the weights");
     a.chunk = int32_t(chunk);
-    a.resident = kSharedFixed + size_t(chunk) * es + 16 <= kMostShared;
+    a.resident = kSmallBytes + kCutBytes + size_t(chunk) * es + 16 <= kMostShared;
+    const size_t at = dtype == W12_F32 ? weights_at<W12_F32>(chunk) : weights_at<W12_BF16>(chunk);
+    a.keep_w = (a.top_k || a.top_p) && kSmallBytes + kCutBytes + at + size_t(chunk) * 4 + 16 <= kMostShared;
     a.vec = (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0 && (a.V * es) % 16 == 0;
     return dtype == W12_F32 ? run<W12_F32>(a, cs, stream) : run<W12_BF16>(a, cs, stream);
 }
