@@ -19,9 +19,9 @@
 //    are gathered in one CTA, which ranks them, cuts by top_p and min_p and
 //    draws, alone;
 //  - top_p over a whole row: the weights, kept in the logits' place (bf16:
-//    beside them), and their sum; a sample of them -- the first eight of every
-//    thread -- tells about where top_p of the sum is reached.  The tokens
-//    around it, about 2500, are gathered in one CTA, which finds the boundary
+//    beside them), and their sum; a sample of them -- the first sixteen of
+//    every thread -- tells about where top_p of the sum is reached.  The tokens
+//    around it, about 2000, are gathered in one CTA, which finds the boundary
 //    from the exact sum of those above;
 //  - where they are more than fit or do not hold it after all, and for larger
 //    top_k: a histogram (64 bins per octave of weight) over the cluster of the
@@ -52,10 +52,9 @@ constexpr int kST = 512;               // threads per CTA
 constexpr int kSW = kST / 32;
 constexpr int kBins = 2048;
 constexpr int kCap = 1024;             // tokens that are ranked directly, one against all
-constexpr int kWide = 4096;            // tokens that can be gathered for a nucleus' boundary
-constexpr int kOwn = 2048;             // of them from one CTA
-constexpr int kAround = 1250;          // tokens to either side of where the sample sees the boundary
-constexpr int kTaken = 8;              // sampled tokens per thread
+constexpr int kWide = 2304;            // tokens that can be gathered for a nucleus' boundary
+constexpr int kAround = 800;           // tokens to either side of where the sample sees the boundary
+constexpr int kTaken = 16;             // sampled tokens per thread
 constexpr int kMaxCluster = 8;
 constexpr float kOne31 = 2147483648.0f;
 constexpr float kSpan = 22.25f;        // e^-22.25 rounds to weight 0
@@ -70,21 +69,26 @@ struct SampleSmall {
     float warp_top[kSW];
     int found_bin;
     uint32_t list_n;
-    uint32_t mine_n;                   // tokens in this CTA's own list
     u64 mass;                     // what weighs more than the window
     uint32_t win_lo, win_end;          // window of weights
     int last;
 };
 
-// Only for top_k and top_p.
+// Only for top_k and top_p.  With 74 KB of logits just small enough for two
+// CTAs on an SM, so that 16 rows of 8 CTAs run at once (36 clusters fit; with
+// one CTA on an SM 15 would).
 struct SampleCut {
-    // counts; weights in two 16-bit halves (a bin's sums stay below 2^32 for
-    // the 65536 logits a CTA can have at most)
-    uint32_t cnt[kBins], lo[kBins], hi[kBins];
-    u64 list[kWide];                   // composites that were gathered (CTA 0 of the cluster)
-    uint32_t list_w[kWide];
+    // counts and their sums over the cluster; or weights in two 16-bit halves
+    // (a bin's sums stay below 2^32 for the 65536 logits a CTA can have)
+    uint32_t lo[kBins], hi[kBins];
+    union {                            // tokens that were gathered (CTA 0 of the cluster)
+        struct {
+            u64 list[kCap];            // their composites
+            uint32_t list_w[kCap];     // and weights
+        };
+        u64 win[kWide];                // weight << 32 | index
+    };
     uint32_t rank[kCap];
-    uint32_t own[kOwn];                // positions in this CTA's chunk, before they go there
 };
 
 constexpr size_t kSmallBytes = (sizeof(SampleSmall) + 15) & ~size_t(15), kCutBytes = (sizeof(SampleCut) + 15) & ~size_t(15);
@@ -219,7 +223,7 @@ __device__ __forceinline__ void find_bin(cg::cluster_group &cl, SampleSmall &sh,
             for (int c = 0; c < cs; ++c) {
                 const SampleCut *o = cl.map_shared_rank(&cut, c);
                 v[j] += BYMASS ? u64(o->lo[me * per + b]) + (u64(o->hi[me * per + b]) << 16)
-                               : u64(o->cnt[me * per + b]);
+                               : u64(o->lo[me * per + b]);
             }
         mine += v[j];
     }
@@ -251,8 +255,8 @@ __device__ __forceinline__ void find_bin(cg::cluster_group &cl, SampleSmall &sh,
     *before_bin = sh.found_above;
 }
 
-// The cluster's counts (cut.cnt added up) in every CTA's cut.lo; the caller's
-// next write to cut.cnt comes after another cluster barrier.
+// The cluster's counts (cut.lo added up) in every CTA's cut.hi; the caller's
+// next write to cut.lo comes after another cluster barrier.
 __device__ __forceinline__ void add_counts(cg::cluster_group &cl, SampleCut &cut) {
     const int cs = int(cl.num_blocks()), me = int(cl.block_rank()), g = kBins / 4 / cs;
     cl.sync();
@@ -260,12 +264,40 @@ __device__ __forceinline__ void add_counts(cg::cluster_group &cl, SampleCut &cut
         const int at = me * g + threadIdx.x;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         for (int c = 0; c < cs; ++c) {
-            const uint4 x = reinterpret_cast<const uint4 *>(cl.map_shared_rank(&cut, c)->cnt)[at];
+            const uint4 x = reinterpret_cast<const uint4 *>(cl.map_shared_rank(&cut, c)->lo)[at];
             v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
         }
-        for (int c = 0; c < cs; ++c) reinterpret_cast<uint4 *>(cl.map_shared_rank(&cut, c)->lo)[at] = v;
+        for (int c = 0; c < cs; ++c) reinterpret_cast<uint4 *>(cl.map_shared_rank(&cut, c)->hi)[at] = v;
     }
     cl.sync();
+}
+
+// Calls put(place, i) for every logit i of the row's chunk that marks(i0)
+// has a bit for (bit j: i0 + j), with places from the count in CTA 0 on, which
+// a warp raises once for 64 logits a lane.
+template <int DT, class M, class P>
+__device__ __forceinline__ void collect(cg::cluster_group &cl, SampleSmall &sh, const Row<DT> &row, int each, M marks,
+                                        P put) {
+    const int lane = threadIdx.x & 31;
+    uint32_t *count = &cl.map_shared_rank(&sh, 0)->list_n;
+#pragma unroll 1
+    for (int q0 = 0; q0 < each; q0 += 64) {
+        u64 mask = 0;
+        const int from = row.i0 + q0, to = min(row.i1, from + 64);
+#pragma unroll 2
+        for (int i = from; i < to; i += 4) mask |= u64(marks(i)) << (i - from);
+        const uint32_t n = __popcll(mask);
+        uint32_t at = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t z = __shfl_up_sync(0xFFFFFFFFu, at, o);
+            if (lane >= o) at += z;
+        }
+        uint32_t base = 0;
+        if (lane == 31 && at) base = atomicAdd(count, at);
+        at += __shfl_sync(0xFFFFFFFFu, base, 31) - n;
+        for (; mask; mask &= mask - 1) put(at++, from + __ffsll(mask) - 1);
+    }
 }
 
 __device__ __forceinline__ void gather(cg::cluster_group &cl, SampleSmall &sh, SampleCut &cut, u64 c, uint32_t w) {
@@ -307,14 +339,14 @@ __device__ __noinline__ u64 select(cg::cluster_group &cl, SampleSmall &sh, Sampl
     };
 #pragma unroll 1
     for (int level = 0; level < 8; ++level) {
-        for (int i = tid; i < kBins; i += kST) cut.cnt[i] = cut.lo[i] = cut.hi[i] = 0u;
+        for (int i = tid; i < kBins; i += kST) cut.lo[i] = cut.hi[i] = 0u;
         __syncthreads();
         members([&](int, uint32_t w, int b) {
             if (BYMASS) {
                 atomicAdd(&cut.lo[b], w & 0xFFFFu);
                 if (w >> 16) atomicAdd(&cut.hi[b], w >> 16);
             } else {
-                atomicAdd(&cut.cnt[b], 1u);
+                atomicAdd(&cut.lo[b], 1u);
             }
         });
         find_bin<BYMASS>(cl, sh, cut, above, need, &g.bin, &above);
@@ -396,23 +428,31 @@ __device__ __forceinline__ u64 nucleus(uint64_t p, u64 total) {
 __device__ __forceinline__ void draw_from_list(SampleSmall &sh, SampleCut &cut, uint32_t n, uint32_t k, uint64_t p,
                                                u64 floor_w, uint64_t u, int32_t *token, float *prob, bool *writer) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // lanes per token (the whole CTA has work at any n), tokens at a time
+    int lanes = 1;
+    while (lanes < 32 && n * 2 * lanes <= uint32_t(kST)) lanes *= 2;
+    const uint32_t sub = tid & (lanes - 1), team = tid / lanes, teams = kST / lanes;
     // a token's rank and the weight before it
     u64 before[2];
     uint32_t rank[2];
     u64 mine = 0;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-        const uint32_t i = tid + q * kST;
-        before[q] = 0, rank[q] = ~0u;
-        if (i >= n) continue;
-        const u64 c = cut.list[i];
-        rank[q] = 0;
-        for (uint32_t j = 0; j < n; ++j)
-            if (cut.list[j] > c) {
-                before[q] += cut.list_w[j];
-                ++rank[q];
-            }
-        if (rank[q] < k) mine += cut.list_w[i];
+        const uint32_t i = team + q * teams;
+        before[q] = 0, rank[q] = 0;
+        if (i < n) {
+            const u64 c = cut.list[i];
+            for (uint32_t j = sub; j < n; j += lanes)
+                if (cut.list[j] > c) {
+                    before[q] += cut.list_w[j];
+                    ++rank[q];
+                }
+        }
+        for (int o = 1; o < lanes; o <<= 1) {
+            before[q] += __shfl_xor_sync(0xFFFFFFFFu, before[q], o);
+            rank[q] += __shfl_xor_sync(0xFFFFFFFFu, rank[q], o);
+        }
+        if (i < n && sub == 0 && rank[q] < k) mine += cut.list_w[i];
     }
     mine = warp_sum64(mine);
     __syncthreads();
@@ -425,8 +465,8 @@ __device__ __forceinline__ void draw_from_list(SampleSmall &sh, SampleCut &cut, 
     u64 kept = 0;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-        const uint32_t i = tid + q * kST;
-        if (i >= n) continue;
+        const uint32_t i = team + q * teams;
+        if (i >= n || sub) continue;
         const uint32_t w = cut.list_w[i];
         cut.rank[i] = rank[q] < k && before[q] < lim && w >= floor_w ? w : 0u;
         kept += cut.rank[i];
@@ -442,13 +482,16 @@ __device__ __forceinline__ void draw_from_list(SampleSmall &sh, SampleCut &cut, 
     const u64 target = scaled(u, total);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-        const uint32_t i = tid + q * kST;
-        if (i >= n || cut.rank[i] == 0u) continue;
+        const uint32_t i = team + q * teams;
         // the weight before it in index order (a composite's low half is ~index)
-        const uint32_t key = uint32_t(cut.list[i]);
         u64 b = 0;
-        for (uint32_t j = 0; j < n; ++j)
-            if (uint32_t(cut.list[j]) > key) b += cut.rank[j];
+        if (i < n) {
+            const uint32_t key = uint32_t(cut.list[i]);
+            for (uint32_t j = sub; j < n; j += lanes)
+                if (uint32_t(cut.list[j]) > key) b += cut.rank[j];
+        }
+        for (int o = 1; o < lanes; o <<= 1) b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+        if (i >= n || sub) continue;
         if (b <= target && target < b + cut.rank[i]) {  // one thread
             *token = int32_t(key_index(cut.list[i]));
             *prob = __fdiv_rn(__uint2float_rn(cut.rank[i]), __ull2float_rn(total));
@@ -457,12 +500,12 @@ __device__ __forceinline__ void draw_from_list(SampleSmall &sh, SampleCut &cut, 
     }
 }
 
-// The bin of cut.lo (counts) in which the sum from bin 0 on reaches `need`, -1:
+// The bin of cut.hi (counts) in which the sum from bin 0 on reaches `need`, -1:
 // it does not.
 __device__ __forceinline__ int find_count(SampleSmall &sh, const SampleCut &cut, uint32_t need) {
     static_assert(kBins == 4 * kST, "four bins a thread");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint4 v = reinterpret_cast<const uint4 *>(cut.lo)[tid];
+    const uint4 v = reinterpret_cast<const uint4 *>(cut.hi)[tid];
     const uint32_t c[4] = {v.x, v.y, v.z, v.w}, mine = v.x + v.y + v.z + v.w;
     uint32_t before = mine;
 #pragma unroll
@@ -489,7 +532,7 @@ __device__ __forceinline__ uint32_t bin_end(int b) {
     return max(1u, __float2uint_ru(__uint_as_float((158u << 23) - (uint32_t(b + 1) << 17) + 1u)));
 }
 
-// From the sample's counts (cut.lo, by weight_bin) and what the nucleus leaves
+// From the sample's counts (cut.hi, by weight_bin) and what the nucleus leaves
 // out: the window of weights, from bin_end to bin_end, around its boundary.
 // `each`: logits per thread, of which kTaken were sampled.
 __device__ __forceinline__ void set_window(SampleSmall &sh, const SampleCut &cut, u64 room, int each) {
@@ -498,7 +541,7 @@ __device__ __forceinline__ void set_window(SampleSmall &sh, const SampleCut &cut
     const float want = __ull2float_rn(room) * part;
     // the lightest first: the sums of what lies below are what counts
     const int b0 = kBins - 4 - 4 * tid;
-    const uint4 v = *reinterpret_cast<const uint4 *>(&cut.lo[b0]);
+    const uint4 v = *reinterpret_cast<const uint4 *>(&cut.hi[b0]);
     const uint32_t c[4] = {v.w, v.z, v.y, v.x};
     float w[4], mine = 0.0f;
     uint32_t mine_n = 0;
@@ -552,13 +595,13 @@ __device__ __forceinline__ void set_window(SampleSmall &sh, const SampleCut &cut
     __syncthreads();
 }
 
-// In one CTA: the threshold composite among the n gathered tokens, which are
-// those of the window: the last before which, together with the window's
-// mass above, less than lim lies.  0: they do not hold it, or too many share
-// its bin.
-__device__ __forceinline__ u64 window_threshold(SampleSmall &sh, SampleCut &cut, uint32_t n, u64 lim) {
+// In one CTA, with cut.lo and cut.hi all 0: the threshold composite among the n
+// gathered tokens, which are those of the window: the last before which,
+// together with the window's mass above, less than lim lies.  0: they do not
+// hold it, or too many share its bin.  logit(index): of the row.
+template <class L>
+__device__ __forceinline__ u64 window_threshold(SampleSmall &sh, SampleCut &cut, uint32_t n, u64 lim, L logit) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    for (int i = tid; i < kBins; i += kST) cut.cnt[i] = cut.lo[i] = cut.hi[i] = 0u;
     // bins over the floats between the window's ends
     const uint32_t top = __float_as_uint(__uint2float_rz(min(sh.win_end, 0x80000000u)));
     const uint32_t span = top - __float_as_uint(__uint2float_rz(sh.win_lo));
@@ -566,9 +609,8 @@ __device__ __forceinline__ u64 window_threshold(SampleSmall &sh, SampleCut &cut,
     while (span >> shift >= uint32_t(kBins)) ++shift;
     const auto bin_of = [&](uint32_t w) { return int((top - __float_as_uint(__uint2float_rz(w))) >> shift); };
     if (tid == 0) sh.found_bin = -1, sh.list_n = 0u, sh.thr = ~0ull;
-    __syncthreads();
     for (uint32_t i = tid; i < n; i += kST) {
-        const uint32_t w = cut.list_w[i];
+        const uint32_t w = uint32_t(cut.win[i] >> 32);
         const int b = bin_of(w);
         atomicAdd(&cut.lo[b], w & 0xFFFFu);
         if (w >> 16) atomicAdd(&cut.hi[b], w >> 16);
@@ -594,7 +636,7 @@ __device__ __forceinline__ u64 window_threshold(SampleSmall &sh, SampleCut &cut,
     const int bin = sh.found_bin;
     if (bin < 0) return 0;
     for (uint32_t i = tid; i < n; i += kST)
-        if (bin_of(cut.list_w[i]) == bin) {
+        if (bin_of(uint32_t(cut.win[i] >> 32)) == bin) {
             const uint32_t at = atomicAdd(&sh.list_n, 1u);
             if (at < uint32_t(kCap)) cut.rank[at] = i;
         }
@@ -602,10 +644,15 @@ __device__ __forceinline__ u64 window_threshold(SampleSmall &sh, SampleCut &cut,
     const uint32_t m = sh.list_n;
     if (m > uint32_t(kCap)) return 0;
     for (uint32_t i = tid; i < m; i += kST) {
-        const u64 c = cut.list[cut.rank[i]];
+        const u64 x = cut.win[cut.rank[i]];
+        const u64 c = pack_key(logit(uint32_t(x)), uint32_t(x));
         u64 b = sh.found_above;
-        for (uint32_t j = 0; j < m; ++j)
-            if (cut.list[cut.rank[j]] > c) b += cut.list_w[cut.rank[j]];
+        for (uint32_t j = 0; j < m; ++j) {
+            const u64 y = cut.win[cut.rank[j]];
+            if (y >> 32 < x >> 32 || y == x) continue;
+            // (different logits can have the same weight)
+            if (y >> 32 > x >> 32 || pack_key(logit(uint32_t(y)), uint32_t(y)) > c) b += y >> 32;
+        }
         if (b < lim) atomicMin(&sh.thr, c);
     }
     __syncthreads();
@@ -614,7 +661,7 @@ __device__ __forceinline__ u64 window_threshold(SampleSmall &sh, SampleCut &cut,
 
 // CUT: top_k or top_p may be asked for.
 template <int DT, bool CUT>
-__global__ void __launch_bounds__(kST, CUT ? 1 : 2) sample_kernel(const __grid_constant__ SampleArgs a) {
+__global__ void __launch_bounds__(kST, 2) sample_kernel(const __grid_constant__ SampleArgs a) {
     cg::cluster_group cl = cg::this_cluster();
     extern __shared__ __align__(16) unsigned char smem[];
     SampleSmall &sh = *reinterpret_cast<SampleSmall *>(smem);
@@ -646,7 +693,7 @@ __global__ void __launch_bounds__(kST, CUT ? 1 : 2) sample_kernel(const __grid_c
     const int32_t top_k = CUT && a.top_k ? a.top_k[req] : 0;
     const bool few = CUT && top_k > 0 && top_k < a.V && top_k <= kCap && t > 0.0f;  // the first top_k in one CTA
     if (CUT)
-        for (int i = tid; i < kBins; i += kST) cut.cnt[i] = 0u;
+        for (int i = tid; i < kBins; i += kST) cut.lo[i] = 0u;
 
     // ---- load, maximum (fmaxf drops a NaN)
     float best = -INFINITY;
@@ -746,28 +793,27 @@ __global__ void __launch_bounds__(kST, CUT ? 1 : 2) sample_kernel(const __grid_c
         u64 thr = 0;
         if (CUT && few) {
             const float d = row.arg(best);
-            if (d > -kSpan) atomicAdd(&cut.cnt[arg_bin(d)], 1u);
+            if (d > -kSpan) atomicAdd(&cut.lo[arg_bin(d)], 1u);
             if (tid == 0) sh.list_n = 0u;
             add_counts(cl, cut);
             const int bin = find_count(sh, cut, uint32_t(top_k));
             // all logits down to the bin's end (fewer threads than top_k have
             // a weight: everything that has one)
             const float end = bin < 0 ? -kSpan : -(float(bin) + 1.01f) * (kSpan / float(kBins));
-#pragma unroll 2
-            for (int i0 = row.i0; i0 < row.i1; i0 += 4) {
+            SampleCut *root = cl.map_shared_rank(&cut, 0);
+            collect(cl, sh, row, each, [&](int i) {
                 float v[4];
-                row.at4(i0, v);
-                bool any = false;
+                row.at4(i, v);
+                uint32_t bits = 0;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) any = any || row.arg(v[j]) >= end;
-                if (!any) continue;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (!(row.arg(v[j]) >= end) || i0 + j >= row.i1) continue;
-                    const uint32_t w = row.weight(v[j]);
-                    if (w) gather(cl, sh, cut, row.comp(v[j], i0 + j), w);
-                }
-            }
+                for (int j = 0; j < 4; ++j) bits |= uint32_t(row.arg(v[j]) >= end) << j;
+                return bits;
+            }, [&](uint32_t at, int i) {
+                if (at >= uint32_t(kCap)) return;
+                const float v = row.at(i);
+                root->list[at] = row.comp(v, i);
+                root->list_w[at] = row.weight(v);
+            });
             cl.sync();
             const uint32_t n = cl.map_shared_rank(&sh, 0)->list_n;
             done = n <= uint32_t(kCap);
@@ -814,7 +860,7 @@ __global__ void __launch_bounds__(kST, CUT ? 1 : 2) sample_kernel(const __grid_c
             const bool cuts = CUT && ((top_k > 0 && top_k < a.V) || p_fix < (1ull << 24));
             uint32_t *keep = cuts && a.keep_w ? reinterpret_cast<uint32_t *>(buf + weights_at<DT>(a.chunk)) : nullptr;
             const bool wide = cuts && !(top_k > 0 && top_k < a.V);  // top_p over the whole row
-            if (CUT && wide && tid == 0) sh.mine_n = sh.list_n = 0u, sh.mass = 0;
+            if (CUT && wide && tid == 0) sh.list_n = 0u, sh.mass = 0;
 #pragma unroll 2
             for (int i = row.i0; i < row.i1; i += 4) {
                 uint32_t w[4];
@@ -825,7 +871,7 @@ __global__ void __launch_bounds__(kST, CUT ? 1 : 2) sample_kernel(const __grid_c
                 if (CUT && wide && i < row.i0 + kTaken)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        if (w[j]) atomicAdd(&cut.cnt[weight_bin(w[j])], 1u);
+                        if (w[j]) atomicAdd(&cut.lo[weight_bin(w[j])], 1u);
             }
             if (keep) {
                 row.w = keep;
@@ -839,41 +885,34 @@ __global__ void __launch_bounds__(kST, CUT ? 1 : 2) sample_kernel(const __grid_c
                     add_counts(cl, cut);
                     set_window(sh, cut, total - lim, each);
                     const uint32_t lo = sh.win_lo, end = sh.win_end;
+                    for (int i = tid; i < kBins; i += kST) cut.lo[i] = cut.hi[i] = 0u;
                     u64 more = 0;
-#pragma unroll 2
-                    for (int i = row.i0; i < row.i1; i += 4) {
-                        uint32_t w[4];
+                    SampleCut *root = cl.map_shared_rank(&cut, 0);
+                    collect(cl, sh, row, each, [&](int i) {
+                        uint32_t w[4], bits = 0;
                         row.weight4(i, w);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) more = add_wide(more, w[j] >= end ? w[j] : 0u);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (w[j] >= lo && w[j] < end && i + j < row.i1) {
-                                const uint32_t at = atomicAdd(&sh.mine_n, 1u);
-                                if (at < uint32_t(kOwn)) cut.own[at] = uint32_t(i + j);
-                            }
-                    }
-                    more = warp_sum64(more);
-                    SampleSmall *root = cl.map_shared_rank(&sh, 0);
-                    SampleCut *to = cl.map_shared_rank(&cut, 0);
-                    if (lane == 0 && more) atomicAdd(&root->mass, more);
-                    __syncthreads();
-                    const uint32_t n = sh.mine_n;
-                    // (a CTA with too many spoils the count)
-                    if (tid == 0) sh.found_bin = int(atomicAdd(&root->list_n, n <= uint32_t(kOwn) ? n : uint32_t(kWide) + 1u));
-                    __syncthreads();
-                    const uint32_t base = uint32_t(sh.found_bin);
-                    if (n <= uint32_t(kOwn))
-                        for (uint32_t q = tid; q < n && base + q < uint32_t(kWide); q += kST) {
-                            const int i = int(cut.own[q]);
-                            to->list[base + q] = row.comp(row.at(i), i);
-                            to->list_w[base + q] = row.weight_at(i);
+                        for (int j = 0; j < 4; ++j) {
+                            more = add_wide(more, w[j] >= end ? w[j] : 0u);
+                            bits |= uint32_t(w[j] - lo < end - lo) << j;
                         }
+                        return bits;
+                    }, [&](uint32_t at, int i) {
+                        if (at < uint32_t(kWide)) root->win[at] = u64(row.weight_at(i)) << 32 | (row.first + uint32_t(i));
+                    });
+                    more = warp_sum64(more);
+                    if (lane == 0 && more) atomicAdd(&cl.map_shared_rank(&sh, 0)->mass, more);
                     cl.sync();
                     if (me == 0) {
-                        const uint32_t all = sh.list_n;
+                        const uint32_t n = sh.list_n;
                         __syncthreads();
-                        const u64 c = all <= uint32_t(kWide) ? window_threshold(sh, cut, all, lim) : 0ull;
+                        u64 c = 0;
+                        if (n <= uint32_t(kWide))
+                            c = window_threshold(sh, cut, n, lim, [&](uint32_t i) {
+                                return row.clean(DT == W12_F32
+                                                     ? static_cast<const float *>(a.logits)[r * a.V + i]
+                                                     : bf16_bits_to_float(static_cast<const uint16_t *>(a.logits)[r * a.V + i]));
+                            });
                         if (tid < cs) cl.map_shared_rank(&sh, tid)->slice2[0] = c;
                     }
                     cl.sync();
@@ -902,9 +941,16 @@ __global__ void __launch_bounds__(kST, CUT ? 1 : 2) sample_kernel(const __grid_c
                 for (int i = row.i0; i < row.i1; i += 4) {
                     uint32_t w[4];
                     row.weight4(i, w);
+                    bool same = false;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (w[j] >= w_thr && w[j]) mine += kept(i + j, w[j]);
+                    for (int j = 0; j < 4; ++j) {
+                        mine = add_wide(mine, w[j] > w_thr && w[j] >= floor_w ? w[j] : 0u);
+                        same = same || w[j] == w_thr;
+                    }
+                    if (same)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (w[j] == w_thr) mine += kept(i + j, w[j]);
                 }
                 add_up(wide ? 1 : 0);  // (not the slot of the sum before it)
             }
@@ -962,6 +1008,7 @@ __global__ void __launch_bounds__(kST, CUT ? 1 : 2) sample_kernel(const __grid_c
 }
 
 constexpr size_t kMostShared = 227 * 1024;
+constexpr size_t kTwoShared = 113 * 1024;  // two CTAs on an SM
 
 template <int DT, bool CUT>
 int run_t(const SampleArgs &a, int cs, void *stream) {
@@ -1000,7 +1047,7 @@ int launch_sample(SampleArgs &a, int dtype, int sms, void *stream) {
     a.chunk = int32_t(chunk);
     a.resident = kSmallBytes + kCutBytes + size_t(chunk) * es + 16 <= kMostShared;
     const size_t at = dtype == W12_F32 ? weights_at<W12_F32>(chunk) : weights_at<W12_BF16>(chunk);
-    a.keep_w = (a.top_k || a.top_p) && kSmallBytes + kCutBytes + at + size_t(chunk) * 4 + 16 <= kMostShared;
+    a.keep_w = (a.top_k || a.top_p) && kSmallBytes + kCutBytes + at + size_t(chunk) * 4 + 16 <= kTwoShared;
     a.vec = (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0 && (a.V * es) % 16 == 0;
     return dtype == W12_F32 ? run<W12_F32>(a, cs, stream) : run<W12_BF16>(a, cs, stream);
 }
