@@ -60,10 +60,10 @@ struct AttendPlan {
     bool join;
 };
 
-// Rows per key head and request from which the tensor-memory kernel takes a
-// request's whole tiles: its tile has 128 rows whatever their number, the
-// register kernel streams the keys once per 32 rows.  (The prefix of two or
-// more requests always goes there: it is what reads it once.)
+// Rows per key head and request from which the tensor-memory kernel takes
+// the requests: its tile has 128 rows whatever their number, the register
+// kernel streams the keys once per 32 rows.  (The prefix of two or more
+// requests always goes there: it is what reads it once.)
 constexpr int64_t kTcRows = 33;
 
 // Work split and workspace layout of an attention call.
@@ -73,7 +73,8 @@ int plan_attend(const w12_kv *kv, int64_t R, int64_t T, int q_heads, int64_t max
     if (R < 1 || R > W12_ATTEND_MAX_R || T < 1 || T >= kLim31 || q_heads < 1 || q_heads > (1 << 20) ||
         q_heads % kv->heads != 0)
         return W12_ERR_SHAPE;
-    if (max_len < 0 || max_len >= kLim31 || prefix < 0 || prefix >= kLim31) return W12_ERR_SHAPE;
+    // (the end of a tile is a 32-bit number, too)
+    if (max_len < 0 || max_len > kLim31 - 256 || prefix < 0 || prefix >= kLim31) return W12_ERR_SHAPE;
     const int64_t tg = T * (q_heads / kv->heads), rows = R * tg;
     if (rows >= kLim31 / 2) return W12_ERR_SHAPE;
     p->rows = int32_t(rows);
@@ -85,12 +86,13 @@ int plan_attend(const w12_kv *kv, int64_t R, int64_t T, int q_heads, int64_t max
         l[kLinePrefix].rt = rows <= 128 ? 128 : 256;
         l[kLinePrefix].pu = blocks(rows, l[kLinePrefix].rt);
     }
-    if (tg >= kTcRows && max_len - T + 1 >= kAttTcTile) {
+    if (tg >= kTcRows) {
         l[kLineRequests].rt = tg <= 128 ? 128 : 256;
         l[kLineRequests].su = blocks(tg, l[kLineRequests].rt);
+    } else {
+        l[kLineRest].rt = tg <= 8 ? 8 : tg <= 16 ? 16 : 32;
+        l[kLineRest].su = 1;
     }
-    l[kLineRest].rt = tg <= 8 ? 8 : tg <= 16 ? 16 : 32;
-    l[kLineRest].su = blocks(tg, l[kLineRest].rt);
     const int64_t own = max_len / kAttTile + 1;  // at most these many tiles of a request
     for (int i = 0; i < kLines; ++i) {           // 32-bit tile numbers
         if (own > kLim31 / (R * std::max(l[i].su, 1)) || shared > kLim31 / std::max(l[i].pu, 1) ||
@@ -101,9 +103,9 @@ int plan_attend(const w12_kv *kv, int64_t R, int64_t T, int q_heads, int64_t max
     if (current_sms(&sms) != W12_OK) return W12_ERR_CUDA;
     size_t off = kWsHeader;
     p->off_arrived = off;
-    off += round256(uint64_t(kv->heads) * R * l[kLineRest].su * 4u);
+    off += round256(uint64_t(kv->heads) * R * 4u);
     p->off_plan = off;
-    off += round256(uint64_t(2 * R + 3) * 4u);
+    off += round256(uint64_t(R + 2) * 4u);
     p->join = l[kLinePrefix].pu + l[kLineRequests].su > 0;
     for (int i = 0; i < kLines; ++i) {
         auto &n = l[i];

@@ -8,13 +8,12 @@
 //    keys of the prefix, read once through request 0's table;
 //  - request unit (r, s), s < su: rows s rt .. of request r against its own
 //    keys.
-// Up to three launches ("lines") share the keys.  Tiles of 128 keys that
-// every row of a part sees go to the tensor-memory kernel, which needs no
-// masks: the prefix's first W tiles, and, for requests with many rows, their
-// tiles from W to the last that their first new token sees whole.  The rest
-// -- what follows, and requests with few rows from W on -- goes to the
-// register kernel in tiles of 64 keys.  (The part of the prefix past W * 128
-// keys is thus read by each request through its own table.)
+// Up to two launches ("lines") share the keys: the prefix's first W tiles of
+// 128 keys, for all requests at once, and what follows, request by request
+// (so the part of the prefix past 128 W keys is read by each request through
+// its own table).  The prefix and requests with many rows go to the
+// tensor-memory kernel, requests with few rows to the register kernel in
+// tiles of 64 keys.
 // Within a line, units of a head are ordered by p, or by r and s; heads in
 // order.  All tiles of all units form one row, cut into equal pieces, one per
 // worker (a CTA; in the register kernel each half of a CTA): every worker
@@ -63,16 +62,12 @@ __device__ __forceinline__ int att_len(const AttendArgs &a, int n) {
 __device__ __forceinline__ int att_prefix_whole(const AttendArgs &a, int shortest) {
     return a.line[kLinePrefix].grid ? min(a.prefix, max(shortest - a.T + 1, 0)) / kAttTcTile : 0;
 }
-// The end of a request's tiles of 128 keys that the tensor-memory kernel takes.
-__device__ __forceinline__ int att_req_whole(const AttendArgs &a, int w, int len) {
-    return a.line[kLineRequests].grid ? max(w, max(len - a.T + 1, 0) / kAttTcTile) : w;
-}
-// This line's tiles of a request of len keys.
+// This line's tiles of a request of len keys (at least one, so that every
+// request has a result).
 __device__ __forceinline__ int att_req_tiles(const AttendArgs &a, int w, int len) {
     if (a.self == kLinePrefix) return 0;
-    const int c1 = att_req_whole(a, w, len);
-    if (a.self == kLineRequests) return c1 - w;
-    return max((len + kAttTile - 1) / kAttTile - c1 * (kAttTcTile / kAttTile), 1);
+    const int kt = a.self == kLineRequests ? kAttTcTile : kAttTile;
+    return max((len + kt - 1) / kt - w * (kAttTcTile / kt), 1);
 }
 
 // Worker c's tiles begin at att_begin(total, grid, c); the worker that has
@@ -111,7 +106,12 @@ __device__ __forceinline__ void att_unit_at(const AttendArgs &a, const AttPlan &
     s.nrows = min(ln.rt, tg - s.block * ln.rt);
     s.left = sh.cum[s.req + 1] - sh.cum[s.req] - k;
     s.key_end = sh.lens[s.req];
-    s.key = a.self == kLineRest ? att_req_whole(a, p.w, s.key_end) * kAttTcTile + k * kAttTile : (p.w + k) * kAttTcTile;
+    s.key = p.w * kAttTcTile + k * (a.self == kLineRequests ? kAttTcTile : kAttTile);
+}
+
+// The last key that every row of the segment's unit sees.
+__device__ __forceinline__ int att_seen_by_all(const AttendArgs &a, const AttSeg &s) {
+    return a.self == kLinePrefix ? 0x7FFFFFFF : s.key_end - a.T + s.row0 / a.G - s.req * a.T;
 }
 
 // The position of tile t of the line.
@@ -167,7 +167,8 @@ __device__ __forceinline__ AttPlan att_plan(const AttendArgs &a, AttShared &sh, 
         shortest = __reduce_min_sync(0xFFFFFFFFu, shortest);
         const int w = att_prefix_whole(a, shortest);
         __syncwarp();
-        int sum = 0, sum_q = 0;
+        int sum = 0;
+        const bool tell = a.join && a.self != kLinePrefix && blockIdx.x == 0;  // for the join kernel
         for (int r0 = 0; r0 < a.R; r0 += 32) {
             const int r = r0 + lane;
             const int n = r < a.R ? sh.lens[r] : 0;
@@ -180,29 +181,12 @@ __device__ __forceinline__ AttPlan att_plan(const AttendArgs &a, AttShared &sh, 
             }
             if (r < a.R) sh.cum[r] = sum + x - y;
             sum += __shfl_sync(0xFFFFFFFFu, x, 31);
-            if (a.join && a.self == kLineRest && blockIdx.x == 0) {  // for the join kernel
-                int q = r < a.R ? att_req_whole(a, w, n) - w : 0;
-                const int p = q;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int z = __shfl_up_sync(0xFFFFFFFFu, q, o);
-                    if (lane >= o) q += z;
-                }
-                if (r < a.R) {
-                    a.plan[1 + r] = sum_q + q - p;
-                    a.plan[a.R + 2 + r] = sh.cum[r];
-                }
-                sum_q += __shfl_sync(0xFFFFFFFFu, q, 31);
-            }
+            if (r < a.R && tell) a.plan[1 + r] = sh.cum[r];
         }
         if (lane == 0) {
             sh.cum[a.R] = sum;
             sh.w = w;
-            if (a.join && a.self == kLineRest && blockIdx.x == 0) {
-                a.plan[0] = w;
-                a.plan[1 + a.R] = sum_q;
-                a.plan[2 * a.R + 2] = sum;
-            }
+            if (tell) a.plan[0] = w, a.plan[1 + a.R] = sum;
         }
     }
     __syncthreads();

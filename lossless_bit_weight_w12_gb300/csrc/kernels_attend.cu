@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_kernel(const __grid_
                 mbar_init(&bar[g * 2 * S + S + s], kGW);
             }
         ctl.abort = 0;
-        ctl.limit_ns = a.wait_ns ? a.wait_ns : kWaitLimitNs;
+        ctl.limit_ns = kWaitLimitNs;
         mbar_fence_init();
     }
     pdl_launch_dependents();
@@ -747,9 +747,9 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     const int rho = w / slices % groups * 32 + lane;
     if (head >= a.heads || rho >= a.rows) return;
     const int r = rho / (a.T * a.G), in_req = rho - r * a.T * a.G;
-    const AttendLine &lp = a.line[kLinePrefix], &lq = a.line[kLineRequests], &lr = a.line[kLineRest];
-    const int32_t *cq = a.plan + 1, *cr = a.plan + a.R + 2;
-    const int np = a.plan[0], q0 = cq[r], q1 = cq[r + 1], qa = cq[a.R], r0 = cr[r], r1 = cr[r + 1], ra = cr[a.R];
+    const AttendLine &lp = a.line[kLinePrefix], &lq = a.line[a.line[kLineRequests].grid ? kLineRequests : kLineRest];
+    const int32_t *cum = a.plan + 1;
+    const int np = a.plan[0], q0 = cum[r], q1 = cum[r + 1], qa = cum[a.R];
     float m = kNegInf, l = 0.0f, acc[kJC] = {};
     if (lp.grid && np) {
         const int p = rho / lp.rt, u = head * lp.pu + p, b = u * np, total = a.heads * lp.pu * np;
@@ -757,18 +757,12 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
         att_add<D, kJC, 4>(lp, int64_t(u + c) * lp.halves, (att_owner(total, lp.grid, b + np - 1) - c + 1) * lp.halves,
                            rho - p * lp.rt, d0, m, l, acc);
     }
-    if (lq.grid && q1 > q0) {
+    {
         const int s = in_req / lq.rt, b = head * lq.su * qa + lq.su * q0 + s * (q1 - q0), total = a.heads * lq.su * qa;
         const int c = att_owner(total, lq.grid, b);
         att_add<D, kJC, 4>(lq, int64_t((head * a.R + r) * lq.su + s + c) * lq.halves,
                            (att_owner(total, lq.grid, b + q1 - q0 - 1) - c + 1) * lq.halves, in_req - s * lq.rt, d0, m,
                            l, acc);
-    }
-    {
-        const int s = in_req / lr.rt, b = head * lr.su * ra + lr.su * r0 + s * (r1 - r0), total = a.heads * lr.su * ra;
-        const int c = att_owner(total, lr.grid, b);
-        att_add<D, kJC, 2>(lr, int64_t((head * a.R + r) * lr.su + s) + c, att_owner(total, lr.grid, b + r1 - r0 - 1) - c + 1,
-                           in_req - s * lr.rt, d0, m, l, acc);
     }
     const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);  // no key: zeros
     *reinterpret_cast<uint2 *>(att_out<D>(a, head, rho) + d0) =

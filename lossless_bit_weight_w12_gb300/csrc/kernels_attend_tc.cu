@@ -1,7 +1,6 @@
-// kernels_attend_tc.cu -- attention over whole key tiles on the tensor cores
-// (tcgen05), for parts with many query rows per key head: the prefix that
-// all requests share, draft blocks.  The mathematics is kernels_attend.cu's;
-// every key of these tiles is seen by every row, so there are no masks.
+// kernels_attend_tc.cu -- attention on the tensor cores (tcgen05), for parts
+// with many query rows per key head: the prefix that all requests share,
+// draft blocks.  The mathematics is kernels_attend.cu's.
 //
 // A CTA has two slots, each a block of 128 query rows with its own region of
 // tensor memory -- scores S (128 columns; the weights P take their place) and
@@ -30,6 +29,12 @@
 //
 // e4m3 tiles pass four converter warps, which write them as fp16 tiles in
 // the same layout into a second ring.
+//
+// Tiles with keys that some row must not see (a draft block's own tokens, the
+// end of the keys) have their scores masked in the registers.  A weight of 0
+// does not keep out a value that is not finite, so value rows past the end
+// are set to zero before the product, and channels that are not finite in
+// rows that only some query rows see are taken out and added by hand.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -95,6 +100,96 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, ui
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
+__device__ __forceinline__ void tmem_load1(uint32_t taddr, uint32_t &r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
+}
+__device__ __forceinline__ void tmem_store1(uint32_t taddr, uint32_t r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(r) : "memory");
+}
+
+// Barriers of a part of the softmax warps; any of them: x.
+__device__ __forceinline__ bool bar_any(int id, int threads, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, %3, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(uint32_t(x)), "r"(id), "r"(threads)
+        : "memory");
+    return r != 0u;
+}
+
+// 16-byte piece c of row `key` of a tile's values in an operand stage.
+__device__ __forceinline__ uint32_t value_at(uint32_t stage, int key, int c) {
+    return stage + uint32_t((c >> 3) * kKT * 128 + key * 128 + (((c & 7) ^ (key & 7)) << 4));
+}
+
+// Bits of the exponent of fp16, bf16: all ones where a number is not finite.
+template <bool Q8>
+__device__ __forceinline__ bool odd16(uint32_t x) {
+    constexpr uint32_t e = Q8 ? 0x7C00u : 0x7F80u;
+    return (x & e) == e;
+}
+template <bool Q8>
+__device__ __forceinline__ bool odd_piece(const uint4 &x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    bool odd = false;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) odd = odd || odd16<Q8>(w[j]) || odd16<Q8>(w[j] >> 16);
+    return odd;
+}
+
+// Adds the channels that are not finite in the values' rows from..to - 1 to
+// the outputs of the rows that see them (row r of the tile: r <= seen), with
+// the weights as they are in tensor memory.
+template <int D, bool Q8>
+__device__ __noinline__ void add_odd(uint32_t stage, int from, int to, int seen, uint32_t t_p, uint32_t t_o) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int r = from; r < to; ++r) {
+        uint32_t pieces = __ballot_sync(0xFFFFFFFFu, lane < D / 8 && odd_piece<Q8>(lds128(value_at(stage, r, lane % (D / 8)))));
+        if (!pieces) continue;
+        uint32_t pp;
+        tmem_load1(t_p + uint32_t(r >> 1), pp);
+        tmem_wait_ld();
+        const uint16_t ph = uint16_t(r & 1 ? pp >> 16 : pp);
+        const float w = Q8 ? __half2float(__ushort_as_half(ph)) : bf16_bits_to_float(ph);
+#pragma unroll 1
+        for (; pieces; pieces &= pieces - 1) {
+            const int c = __ffs(pieces) - 1;
+            const uint4 x = lds128(value_at(stage, r, c));
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint16_t h = uint16_t(e & 1 ? xs[e >> 1] >> 16 : xs[e >> 1]);
+                if (!odd16<Q8>(h)) continue;  // (the same for all lanes)
+                const float v = Q8 ? __half2float(__ushort_as_half(h)) : bf16_bits_to_float(h);
+                uint32_t o;
+                tmem_load1(t_o + uint32_t(8 * c + e), o);
+                tmem_wait_ld();
+                if (r <= seen) o = __float_as_uint(__uint_as_float(o) + w * v);
+                tmem_store1(t_o + uint32_t(8 * c + e), o);
+                tmem_wait_st();
+            }
+        }
+    }
+}
+
+// Zeros in their place; part `me` of n of the work.
+template <int D, bool Q8>
+__device__ __noinline__ void clear_odd(uint32_t stage, int from, int to, int me, int n) {
+    for (int x = me; x < (to - from) * (D / 8); x += n) {
+        const uint32_t at = value_at(stage, from + x / (D / 8), x % (D / 8));
+        const uint4 y = lds128(at);
+        if (!odd_piece<Q8>(y)) continue;
+        uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[j] &= (odd16<Q8>(w[j]) ? 0xFFFF0000u : ~0u) & (odd16<Q8>(w[j] >> 16) ? 0xFFFFu : ~0u);
+        sts128(at, w[0], w[1], w[2], w[3]);
+    }
+}
+
 template <int D, bool Q8, bool TWO>
 __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __grid_constant__ AttendArgs a) {
     using C = TC<D, Q8, TWO>;
@@ -139,7 +234,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
             mbar_init(&token[s], 1);
         }
         ctl.abort = 0;
-        ctl.limit_ns = a.wait_ns ? a.wait_ns : kWaitLimitNs;
+        ctl.limit_ns = kWaitLimitNs;
         mbar_fence_init();
     }
     if (warp == kIssueWarp) {
@@ -238,9 +333,18 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
             else
                 named_sync(256);
             if (Q8) sc *= q_up[in_unit];
+            sc = fmaxf(sc, 1e-37f);  // (a mask's -infinity times 0 would be NaN)
+            const int all_see = att_seen_by_all(a, seg);
+            const int pos = valid && a.self != kLinePrefix ? seg.key_end - a.T + (seg.row0 + in_unit) / a.G - seg.req * a.T
+                                                           : seg.key_end - 1;
             if (k0 >= n) {  // no tile of the segment is this slot's
                 if (valid) ln.part_ml[at] = make_float2(kNegInf, 0.0f);
                 continue;
+            }
+            if (seg.key + (k0 + 1) * kKT - 1 > all_see) {  // add_odd() may come before the first product
+                const uint32_t zero[32] = {};
+                for (int c = 0; c < D; c += 32) tmem_store32(to + uint32_t(c), zero);
+                tmem_wait_st();
             }
             tmem_fence_before();
             __syncwarp();
@@ -249,6 +353,25 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
             float m = kNegInf, l = 0.0f;
             for (int k = k0; k < n; k += kStep) {
                 const int i = i0 + k;
+                const int key0 = seg.key + k * kKT;
+                const bool masked = key0 + kKT - 1 > all_see;
+                // rows of the values that not every query row sees: from .. to - 1, then rows past the end
+                const int from = masked ? max(all_see - key0 + 1, 0) : 0, until = max(min(seg.key_end - key0, kKT), from);
+                const uint32_t vb = ops + uint32_t(stage(i, 1)) * uint32_t(C::kHalf);
+                bool odd = false;
+                if (masked) {
+                    att_wait(&op_full[stage(i, 1)], phase(i, 1), &ctl, a.err);
+                    for (int x = TWO ? int(threadIdx.x) : row; x < (kKT - from) * (D / 8); x += TWO ? 256 : 128) {
+                        const int r = from + x / (D / 8);
+                        const uint32_t at = value_at(vb, r, x % (D / 8));
+                        if (r < until)
+                            odd = odd || odd_piece<Q8>(lds128(at));
+                        else if (!Q8)  // (the converters have done it)
+                            sts128(at, 0u, 0u, 0u, 0u);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    odd = bar_any(TWO ? 1 : 2 + slot, TWO ? 256 : 128, odd);
+                }
                 att_wait(&s_full[slot], n_s++ & 1u, &ctl, a.err);
                 tmem_fence_after();
                 if (warp_valid) {
@@ -271,6 +394,14 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
                             const float4 s4 = tab[j];
                             x[2 * j] = __fmul2_rn(x[2 * j], make_float2(s4.x, s4.y));
                             x[2 * j + 1] = __fmul2_rn(x[2 * j + 1], make_float2(s4.z, s4.w));
+                        }
+                    }
+                    if (masked) {
+                        const int seen = pos - key0;
+#pragma unroll
+                        for (int j = 0; j < kKT / 2; ++j) {
+                            x[j].x = 2 * j <= seen ? x[j].x : kNegInf;
+                            x[j].y = 2 * j + 1 <= seen ? x[j].y : kNegInf;
                         }
                     }
                     float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
@@ -308,7 +439,12 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
                             float2 e = __ffma2_rn(x[32 * c + j], sc2, mu2);
                             e.x = ex2(e.x), e.y = ex2(e.y);
                             sum[j & 1] = __fadd2_rn(sum[j & 1], e);
-                            if (Q8) e = __fmul2_rn(e, reinterpret_cast<const float2 *>(vsc)[32 * c + j]);
+                            if (Q8) {
+                                const float2 z = reinterpret_cast<const float2 *>(vsc)[32 * c + j];
+                                const float2 y = __fmul2_rn(e, z);
+                                // a masked weight is zero whatever the value's scale holds
+                                e = masked ? make_float2(e.x == 0.0f ? 0.0f : y.x, e.y == 0.0f ? 0.0f : y.y) : y;
+                            }
                             p[j] = Q8 ? pack_f16(e.x, e.y) : pack_bf16(e.x, e.y);
                         }
                         tmem_store32(ts + 32u * uint32_t(c), p);
@@ -316,6 +452,13 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
                     sum[0] = __fadd2_rn(sum[0], sum[1]);
                     l += sum[0].x + sum[0].y;
                     tmem_wait_st();
+                }
+                if (odd) {
+                    if (warp_valid) add_odd<D, Q8>(vb, from, until, pos - key0, ts, to);
+                    bar_any(TWO ? 1 : 2 + slot, TWO ? 256 : 128, false);
+                    clear_odd<D, Q8>(vb, from, until, TWO ? int(threadIdx.x) : row, TWO ? 256 : 128);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    bar_any(TWO ? 1 : 2 + slot, TWO ? 256 : 128, false);
                 }
                 tmem_fence_before();
                 __syncwarp();
@@ -359,8 +502,17 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
             dst_at[p][0] = row + uint32_t((w ^ (key & 7)) << 4);
             dst_at[p][1] = row + uint32_t(((w + 1) ^ (key & 7)) << 4);
         }
+        AttSeg seg = sh.first[0];
+        int left = seg.left, key0 = seg.key;  // of the segment; the tile's first key
 #pragma unroll 1
         for (int h = 0; h < 2 * (t1 - t0); ++h) {  // keys and values in turn
+            if (h && !(h & 1)) {
+                key0 += kKT;
+                if (--left == 0) {
+                    att_next(a, plan, sh, seg);
+                    left = seg.left, key0 = seg.key;
+                }
+            }
             const int si = h % SI, so = h % SO;
             att_wait(&in_full[si], uint32_t(h / SI) & 1u, &ctl, a.err);
             if (h >= SO) att_wait(&op_empty[so], uint32_t(h / SO - 1) & 1u, &ctl, a.err);
@@ -374,6 +526,12 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
             for (int q = 0; q < 4; ++q)
 #pragma unroll
                 for (int p = 0; p < D / 64; ++p) x[q * (D / 64) + p] = lds128(src + src_at[p] + uint32_t(32 * q * D));
+            if (seg.key_end - key0 < kKT)  // rows past the end may hold anything
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (key0 + key + 32 * q >= seg.key_end)
+#pragma unroll
+                        for (int p = 0; p < D / 64; ++p) x[q * (D / 64) + p] = make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -385,15 +543,16 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
                     sts128(to + dst_at[p][1], e4m3x2_lo_to_f16x2(y.z), e4m3x2_hi_to_f16x2(y.z), e4m3x2_lo_to_f16x2(y.w),
                            e4m3x2_hi_to_f16x2(y.w));
                 }
+            const int n_keys = seg.key_end - key0;  // of the tile (or more)
             float *sc = scales + (h % C::kScaleRing) * C::kScales;
             const uint32_t ss = src + uint32_t(C::kInScale);
-            sc[32 * cw + lane] = __uint_as_float(lds32(ss + uint32_t(32 * cw + lane) * 4u));
+            sc[32 * cw + lane] = 32 * cw + lane < n_keys ? __uint_as_float(lds32(ss + uint32_t(32 * cw + lane) * 4u)) : 0.0f;
             if (cw == 0 && (h & 1)) {  // the bound of the tile's value scales
                 uint32_t top = 0u;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const float x = __uint_as_float(lds32(ss + uint32_t(32 * q + lane) * 4u));
-                    if (x <= 3.0e38f) top = max(top, __float_as_uint(x));
+                    if (x <= 3.0e38f && 32 * q + lane < n_keys) top = max(top, __float_as_uint(x));
                 }
                 top = __reduce_max_sync(0xFFFFFFFFu, top);
                 if (lane == 0) sc[kKT] = exp_above(__uint_as_float(top)) - 7.0f;
@@ -480,6 +639,8 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
                     const int i0 = t - t0, k0 = first_tile(i0, slot);
                     n = min(seg.left, t1 - t);
                     if (k0 >= n) continue;
+                    // (zeros were written to the output, see the softmax warps)
+                    const bool zeroed = seg.key + (k0 + 1) * kKT - 1 > att_seen_by_all(a, seg);
                     att_wait(&q_full[slot], n_seg++ & 1u, &ctl, a.err);
                     att_wait(&op_full[stage(i0 + k0, 0)], phase(i0 + k0, 0), &ctl, a.err);
                     tmem_fence_after();
@@ -490,7 +651,9 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
                         const bool more = k + kStep < n;
                         const int burst = TWO ? 2 * i + slot : i;  // of the CTA; odd ones are slot 1's
                         att_wait(&op_full[s], phase(i, 1), &ctl, a.err);
-                        if (more) att_wait(&op_full[stage(i + kStep, 0)], phase(i + kStep, 0), &ctl, a.err);
+                        // e4m3: the next keys may be converted only after the
+                        // values' stage of a tile before was released
+                        if (!Q8 && more) att_wait(&op_full[stage(i + kStep, 0)], phase(i + kStep, 0), &ctl, a.err);
                         att_wait(&p_full[slot], n_p++ & 1u, &ctl, a.err);
                         if (burst > 0) att_wait(&token[slot], uint32_t((burst - 1) / 2) & 1u, &ctl, a.err);
                         tmem_fence_after();
@@ -498,14 +661,19 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
 #pragma unroll
                         for (int ks = 0; ks < kKT / 16; ++ks) {
                             umma_tmem_a(ts + kOCol, ts + 8u * uint32_t(ks), d + uint64_t((ks * 2048) >> 4), ipv,
-                                        (k > k0 || ks) ? 1u : 0u);
+                                        (k > k0 || ks || zeroed) ? 1u : 0u);
                             if (ks == kKT / 32 - 1 && !more) mbar_arrive(&token[slot ^ 1]);
                         }
                         umma_arrive(&op_empty[s]);
-                        if (more)
+                        if (more) {
+                            if (Q8) {
+                                att_wait(&op_full[stage(i + kStep, 0)], phase(i + kStep, 0), &ctl, a.err);
+                                tmem_fence_after();
+                            }
                             scores(i + kStep, true);
-                        else
+                        } else {
                             umma_arrive(&o_done[slot]);
+                        }
                     }
                 }
                 // every product issued has completed before the tensor memory is freed

@@ -81,8 +81,8 @@ struct AttendLine {
     float2 *part_ml;  // [slots][halves][rt]: reference exponent (log2 units) and sum
 };
 
-// Lines: the tensor-memory kernel on the prefix, the same on the requests'
-// whole tiles, the register kernel on the rest.
+// Lines: the tensor-memory kernel on the prefix; what follows, request by
+// request, in the tensor-memory kernel or in the register kernel.
 enum { kLinePrefix = 0, kLineRequests = 1, kLineRest = 2, kLines = 3 };
 
 struct AttendArgs {
@@ -101,9 +101,8 @@ struct AttendArgs {
     float scale_log2;  // scale * log2(e)
     int *err;
     uint32_t *arrived;  // [rest units] segments that are done; zero between calls
-    int32_t *plan;      // for the join: W, then the R + 1 cumulative tiles of kLineRequests and of kLineRest
-    int32_t join;       // 1: a join kernel adds up the results (other lines have some)
-    uint64_t wait_ns;
+    int32_t *plan;      // for the join: W, then the R + 1 cumulative tiles of the requests
+    int32_t join;       // 1: a join kernel adds up the results (the tensor-memory kernel has some)
     AttendLine line[kLines];
 };
 int attend_make_maps(AttendArgs &a, const w12_kv *kv);

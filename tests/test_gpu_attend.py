@@ -80,7 +80,7 @@ class Problem:
         assert bool((out_all[:, 0] == 5.0).all()) and bool((out_all[:, -1] == 5.0).all())
         return out, z
 
-    def check(self, out, lse, rows=None):
+    def check(self, out, lse, rows=None, floor=0.0):
         q = self.q.float().cpu().numpy().astype(np.float64)
         out = out.float().cpu().numpy().astype(np.float64)
         lse = None if lse is None else lse.cpu().numpy().astype(np.float64)
@@ -108,7 +108,7 @@ class Problem:
                     want = p @ v[:stop, h] / l
                     amount = p @ np.abs(v[:stop, h]) / l
                     w = 2.0 ** -11 if e4m3 else u
-                    tol = (w + 2.0 ** -16 * (1 + size[:, None])) * amount + u * np.abs(want) + 1e-30
+                    tol = (w + 2.0 ** -16 * (1 + size[:, None])) * amount + u * np.abs(want) + 1e-30 + floor * stop * np.abs(v[:stop, h]).max()
                     err = np.abs(out[tok, at] - want)
                     assert np.all(err <= tol * (1 + u)), (tok, h, float((err / tol).max()))
                     if lse is not None:
@@ -151,6 +151,28 @@ def test_attend(dev, w12mod, case, e4m3):
     assert torch.equal(out, again) and torch.equal(lse, z)
     third, _ = p.run(lse=False, max_len=max(p.lens) + 1000)
     assert third is not None and bool((third.float() - out.float()).abs().max() <= 2.0 ** -6 * out.float().abs().max() + 1e-30)
+
+
+BLOCKS = [
+    (3, 50, 6, 1, 64, 16, [0, 49, 640], 0),         # 300 rows: none, some and all with keys
+    (4, 12, 6, 2, 128, 64, [128, 139, 140, 1035], 0),  # the new tokens before, across and after a tile's end
+    (5, 7, 12, 2, 128, 32, [700, 520, 519, 640, 1000], 512),  # 42 rows after a prefix
+]
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("case", BLOCKS, ids=[str(i) for i in range(len(BLOCKS))])
+def test_blocks_at_tile_ends(dev, w12mod, case, e4m3):
+    """fp16 weights have a floor: spacing 2^-24, where the largest weight times
+    its scale is 2^7 (2^e the bound of a tile's scales, m = max - 7 + e).  A
+    weight is thus off by up to 2^-25 2^(e - 7) <= 2^-31 max(scale) of the
+    row's largest, and an output by 2^-31 max(scale) max(code) per key, whose
+    product is at most 2^9 max |v| here (scales and codes apart by no more)."""
+    p = Problem(w12mod, dev, *case[:6], e4m3, case[6], case[7])
+    p.poison()
+    out, lse = p.run()
+    assert w12mod.get_device_error(p.ws) == 0
+    p.check(out, lse, floor=2.0 ** -22 if e4m3 else 0.0)
 
 
 def test_prefix_and_plain_agree(dev, w12mod):
@@ -199,6 +221,34 @@ def test_later_tokens_do_not_leak(dev, w12mod, e4m3):
             out, _ = p.run()
             assert torch.equal(out[:T - 3], clean[:T - 3]) and bool(torch.isnan(out[T - 3:]).all())
             s.copy_(keep)
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("T,hq,n", [(4, 6, 90), (4, 6, 1000), (40, 6, 300), (40, 6, 128), (130, 1, 131)])
+def test_odd_values_of_any_block(dev, w12mod, T, hq, n, e4m3):
+    """As above for few rows, several tiles, more than 128 rows; values that are
+    not finite in several channels, in the first new token and in the last."""
+    import torch
+    p = Problem(w12mod, dev, 1, T, hq, 1, 128, 32, e4m3, [n])
+    clean, _ = p.run()
+    spots = [(n - T + 1, 3), (n - T + 1, 4), (n - T // 2, 127), (n - 1, 64)]  # position, channel
+    t = p.kv.v
+    for at, ch in spots:
+        if e4m3:
+            t.view(torch.uint8)[int(p.table[0, at // 32]), 0, at % 32, ch] = 0x7F
+        else:
+            t[int(p.table[0, at // 32]), 0, at % 32, ch] = float("-inf")
+    out, lse = p.run()
+    again, _ = p.run()
+    assert torch.equal(torch.isfinite(out), torch.isfinite(again))
+    hit = torch.zeros(T, 128, dtype=torch.bool)
+    for at, ch in spots:
+        hit[at - (n - T):, ch] = True
+    hit = hit[:, None, :].expand(-1, hq, -1)
+    got = out.float().cpu()
+    assert not bool(torch.isfinite(got[hit]).any()) and bool(torch.isfinite(got[~hit]).all())
+    assert bool(((got - clean.float().cpu())[~hit].abs() <= 2.0 ** -6).all())
+    assert bool(torch.isfinite(lse).all())
 
 
 @pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
