@@ -34,7 +34,8 @@
 // end of the keys) have their scores masked in the registers.  A weight of 0
 // does not keep out a value that is not finite, so value rows past the end
 // are set to zero before the product, and channels that are not finite in
-// rows that only some query rows see are taken out and added by hand.
+// rows that only some query rows see are taken out and added by hand.  (The
+// same for weights whose value scale is not finite.)
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -68,23 +69,27 @@ struct TC {
     static constexpr int kInScale = kKT * D;            // e4m3 input stage: codes, then 128 scales
     static constexpr int kIn = Q8 ? kKT * D + 1024 : kHalf;
     static constexpr int kScales = kKT + 4;             // floats per half tile: scales, and (values) their bound
-    // The keys' stage is free before the softmax has read their scales; a
-    // half tile's scales are written over 8 halves later, which the
-    // converters reach only after this tile's values were released.
+    // The keys' stage is free before the softmax has read their scales, and
+    // the values' scales are given out before their stage; a half tile's
+    // scales are written over 8 halves (4 tiles) later, which the converters
+    // reach only after a product that follows this tile's softmax.
     static constexpr int kScaleRing = 8;
     static constexpr int kFixed = (int(sizeof(AttShared)) + 15) / 16 * 16 + 1024 + (Q8 ? kScaleRing * kScales * 4 + 1024 : 0);
     static constexpr int kRoom = 227 * 1024 - kFixed - kQ;
-    // Operand stages.  With units of 128 rows a stage has to stay with one
-    // slot (tile i: stages 2 i, 2 i + 1, slot i & 1): a multiple of 4.
-    // e4m3 leaves room for the input ring.
+    // Operand stages.  With units of 128 rows the values' stages (bf16: the
+    // keys', too) have to stay with one slot: a multiple of 4 in turn, or,
+    // e4m3, one for the keys and one per slot for the values.  e4m3 leaves
+    // room for the input ring, whose stages each belong to the keys or to the
+    // values (an even number) where these have converters of their own.
+    static constexpr bool kOwn = Q8 && !TWO;
     static constexpr int kOpFit = (Q8 ? kRoom - 3 * kIn : kRoom) / kHalf;
-    static constexpr int SO = TWO ? (kOpFit > 4 && Q8 ? 4 : kOpFit > 8 ? 8 : kOpFit) : kOpFit >= 8 && !Q8 ? 8 : 4;
+    static constexpr int SO = kOwn ? 3 : TWO ? (kOpFit > 4 && Q8 ? 4 : kOpFit > 8 ? 8 : kOpFit) : kOpFit >= 8 ? 8 : 4;
     static constexpr int kInFit = (kRoom - SO * kHalf) / kIn;
-    static constexpr int SI = Q8 ? (kInFit > 8 ? 8 : kInFit) : SO;
+    static constexpr int SI = Q8 ? (kInFit > 8 ? 8 : kOwn ? kInFit / 2 * 2 : kInFit) : SO;
     static constexpr int kRing = Q8 ? SI * kIn + SO * kHalf : SO * kHalf;
     static constexpr size_t kSmem = size_t(kQ) + kRing + kFixed;
-    static_assert(SO >= 3 && SI >= 3 && SO <= 8 && (!Q8 || SO + 1 < kScaleRing) && (TWO || SO % 4 == 0) && kSmem <= 227 * 1024, "shared memory");
-    static_assert((4 * 8 + 12) * 8 + 32 <= 1008, "barriers");
+    static_assert(SO >= 3 && SI >= 3 && SO <= 8 && (!Q8 || SO + 1 < kScaleRing) && (TWO || kOwn || SO % 4 == 0) && (!kOwn || SI % 2 == 0) && kSmem <= 227 * 1024, "shared memory");
+    static_assert((4 * 8 + 13 + kScaleRing / 2) * 8 + 32 <= 1008, "barriers");
 };
 
 template <int N>
@@ -101,10 +106,48 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, ui
 }
 
 __device__ __forceinline__ void tmem_load1(uint32_t taddr, uint32_t &r) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r)
+                 : "r"(taddr)
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_store1(uint32_t taddr, uint32_t r) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(r) : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+__device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t *v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+// f(c, columns 32 c .. of this lane's row) for c < 4, the next columns on their way.
+template <typename F>
+__device__ __forceinline__ void by_columns(uint32_t ts, F f) {
+    float2 x[16], y[16];
+    tmem_load32(ts, reinterpret_cast<uint32_t *>(x));
+    tmem_wait_ld();
+    tmem_landed32(reinterpret_cast<uint32_t *>(x));
+#pragma unroll 1
+    for (int c = 0; c < 4; c += 2) {
+        tmem_load32(ts + 32u * uint32_t(c + 1), reinterpret_cast<uint32_t *>(y));
+        f(c, x);
+        tmem_wait_ld();
+        tmem_landed32(reinterpret_cast<uint32_t *>(y));
+        if (c == 0) tmem_load32(ts + 64u, reinterpret_cast<uint32_t *>(x));
+        f(c + 1, y);
+        tmem_wait_ld();
+        tmem_landed32(reinterpret_cast<uint32_t *>(x));
+    }
 }
 
 // Barriers of a part of the softmax warps; any of them: x.
@@ -151,7 +194,6 @@ __device__ __noinline__ void add_odd(uint32_t stage, int from, int to, int seen,
         if (!pieces) continue;
         uint32_t pp;
         tmem_load1(t_p + uint32_t(r >> 1), pp);
-        tmem_wait_ld();
         const uint16_t ph = uint16_t(r & 1 ? pp >> 16 : pp);
         const float w = Q8 ? __half2float(__ushort_as_half(ph)) : bf16_bits_to_float(ph);
 #pragma unroll 1
@@ -166,12 +208,25 @@ __device__ __noinline__ void add_odd(uint32_t stage, int from, int to, int seen,
                 const float v = Q8 ? __half2float(__ushort_as_half(h)) : bf16_bits_to_float(h);
                 uint32_t o;
                 tmem_load1(t_o + uint32_t(8 * c + e), o);
-                tmem_wait_ld();
                 if (r <= seen) o = __float_as_uint(__uint_as_float(o) + w * v);
                 tmem_store1(t_o + uint32_t(8 * c + e), o);
                 tmem_wait_st();
             }
         }
+    }
+}
+
+// e4m3: a key's weight is zero for the rows that must not see it, whatever
+// its value's scale holds (0 times a scale that is not finite is NaN).
+__device__ __noinline__ void clear_weights(const float *vsc, int from, int to, int seen, uint32_t t_p) {
+#pragma unroll 1
+    for (int r = from; r < to; ++r) {
+        if (fabsf(vsc[r]) <= 3.0e38f) continue;
+        uint32_t w;
+        tmem_load1(t_p + uint32_t(r >> 1), w);
+        if (r > seen) w &= r & 1 ? 0xFFFFu : 0xFFFF0000u;
+        tmem_store1(t_p + uint32_t(r >> 1), w);
+        tmem_wait_st();
     }
 }
 
@@ -202,10 +257,10 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
     AttShared &sh = *reinterpret_cast<AttShared *>(fixed);
     unsigned char *misc = fixed + (sizeof(AttShared) + 15) / 16 * 16;
     uint64_t *in_full = reinterpret_cast<uint64_t *>(misc), *in_empty = in_full + SI;
-    uint64_t *op_full = Q8 ? in_empty + SI : in_full, *op_empty = Q8 ? op_full + SO : in_empty;
+    uint64_t *op_full = Q8 ? in_empty + SI : in_full, *op_empty = Q8 ? op_full + SO + 1 : in_empty;
     uint64_t *s_full = (Q8 ? op_empty + SO : in_empty + SI), *p_full = s_full + 2, *q_full = s_full + 4,
-             *o_done = s_full + 6, *fin = s_full + 8, *token = s_full + 10;
-    WaitCtl &ctl = *reinterpret_cast<WaitCtl *>(s_full + 12);
+             *o_done = s_full + 6, *fin = s_full + 8, *token = s_full + 10, *vs_full = s_full + 12;
+    WaitCtl &ctl = *reinterpret_cast<WaitCtl *>(s_full + 12 + C::kScaleRing / 2);
     uint32_t &s_tmem = *reinterpret_cast<uint32_t *>(reinterpret_cast<unsigned char *>(&ctl) + sizeof(WaitCtl));
     float *scales = reinterpret_cast<float *>(misc + 1024);          // [kScaleRing][128 scales, their bound]
     float *q_up = scales + (Q8 ? C::kScaleRing * C::kScales : 0);    // e4m3: [256] powers of two of the query rows
@@ -215,16 +270,18 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
         return;
     }
     if (threadIdx.x == 0) {
-        constexpr uint32_t kUsers = TWO ? 2 : 1;  // slots that use a stage
+        constexpr uint32_t kUsers = TWO ? 2 : 1;       // slots that use a stage
+        constexpr uint32_t kConverters = TWO ? 4 : 2;  // warps that write an operand stage
         for (int s = 0; s < SI; ++s) {
             mbar_init(&in_full[s], 1);
-            mbar_init(&in_empty[s], Q8 ? 4 : kUsers);
+            mbar_init(&in_empty[s], Q8 ? kConverters : kUsers);
         }
         if (Q8)
             for (int s = 0; s < SO; ++s) {
-                mbar_init(&op_full[s], 4);
+                mbar_init(&op_full[s], kConverters);
                 mbar_init(&op_empty[s], kUsers);
             }
+        if (C::kOwn) mbar_init(&op_full[3], kConverters);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&s_full[s], 1);
             mbar_init(&p_full[s], 4);
@@ -233,6 +290,8 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
             mbar_init(&fin[s], 1);
             mbar_init(&token[s], 1);
         }
+        if (Q8)
+            for (int s = 0; s < C::kScaleRing / 2; ++s) mbar_init(&vs_full[s], kConverters);
         ctl.abort = 0;
         ctl.limit_ns = kWaitLimitNs;
         mbar_fence_init();
@@ -257,9 +316,19 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
     const auto first_tile = [](int i0, int slot) { return TWO ? 0 : (i0 & 1) != slot ? 1 : 0; };
     constexpr int kStep = TWO ? 1 : 2;
 
-    // tile i's keys (kv = 0) or values (1) are in operand stage (2 i + kv) % SO
-    const auto stage = [](int i, int kv) { return (2 * i + kv) % SO; };
-    const auto phase = [](int i, int kv) { return uint32_t((2 * i + kv) / SO) & 1u; };
+    // tile i's keys (kv = 0) or values (1): their operand stage, how often it
+    // was used before
+    const auto stage = [](int i, int kv) { return C::kOwn ? kv ? 1 + (i & 1) : 0 : (2 * i + kv) % SO; };
+    const auto used = [](int i, int kv) { return C::kOwn ? kv ? i >> 1 : i : (2 * i + kv) / SO; };
+    // Waits until it is filled.  One stage for all keys has a barrier per slot:
+    // the slots wait for alternate tiles, and a slot that had not waited for
+    // the tile before could take its phase for the next.
+    const auto wait_operand = [&](int i, int kv) {
+        if (C::kOwn)
+            att_wait(&op_full[kv ? 1 + (i & 1) : 3 * (i & 1)], uint32_t(i >> 1) & 1u, &ctl, a.err);
+        else
+            att_wait(&op_full[stage(i, kv)], uint32_t(used(i, kv)) & 1u, &ctl, a.err);
+    };
     // the roles, by warpgroup (a warpgroup changes its registers as one)
     if (warp < kProdWarp) {
         // ------------------------------------------------------- softmax
@@ -360,54 +429,74 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
                 const uint32_t vb = ops + uint32_t(stage(i, 1)) * uint32_t(C::kHalf);
                 bool odd = false;
                 if (masked) {
-                    att_wait(&op_full[stage(i, 1)], phase(i, 1), &ctl, a.err);
-                    for (int x = TWO ? int(threadIdx.x) : row; x < (kKT - from) * (D / 8); x += TWO ? 256 : 128) {
-                        const int r = from + x / (D / 8);
-                        const uint32_t at = value_at(vb, r, x % (D / 8));
-                        if (r < until)
-                            odd = odd || odd_piece<Q8>(lds128(at));
-                        else if (!Q8)  // (the converters have done it)
-                            sts128(at, 0u, 0u, 0u, 0u);
-                    }
+                    wait_operand(i, 1);
+                    const int x0 = TWO ? int(threadIdx.x) : row;
+                    for (int x = from * (D / 8) + x0; x < until * (D / 8); x += TWO ? 256 : 128)
+                        odd = odd || odd_piece<Q8>(lds128(value_at(vb, x / (D / 8), x % (D / 8))));
+                    if (!Q8)  // (e4m3: the converters have done it)
+                        for (int x = until * (D / 8) + x0; x < kKT * (D / 8); x += TWO ? 256 : 128)
+                            sts128(value_at(vb, x / (D / 8), x % (D / 8)), 0u, 0u, 0u, 0u);
+                    if (Q8 && row >= from && row < until)
+                        odd = odd || !(fabsf(scales[(2 * i + 1) % C::kScaleRing * C::kScales + row]) <= 3.0e38f);
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     odd = bar_any(TWO ? 1 : 2 + slot, TWO ? 256 : 128, odd);
                 }
                 att_wait(&s_full[slot], n_s++ & 1u, &ctl, a.err);
                 tmem_fence_after();
                 if (warp_valid) {
-                    float2 x[kKT / 2];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_load32(ts + 32u * uint32_t(c), reinterpret_cast<uint32_t *>(x + 16 * c));
-                    const float *vsc = nullptr;
                     float lift = 0.0f;
+                    const uint32_t tk = smem_addr(scales + 2 * i % C::kScaleRing * C::kScales);
+                    const uint32_t tv = tk + uint32_t(C::kScales) * 4u;  // (2 i + 1 is in the ring's same turn)
+                    const int seen = pos - key0;
+                    float top;
+                    float2 xs[Q8 ? 1 : kKT / 2];
                     if (Q8) {
-                        // (the keys are there, their product is)
-                        vsc = scales + (2 * i + 1) % C::kScaleRing * C::kScales;
-                        att_wait(&op_full[stage(i, 1)], phase(i, 1), &ctl, a.err);
-                        lift = vsc[kKT];
-                    }
-                    tmem_wait_ld();
-                    if (Q8) {
-                        const float4 *tab = reinterpret_cast<const float4 *>(scales + 2 * i % C::kScaleRing * C::kScales);
+                        // Two passes over 32 columns at a time, by small loops
+                        // (unrolled, the multiplications by the scales make
+                        // the code miss the instruction cache): the scaled
+                        // scores go back to tensor memory.
+                        float mx[2] = {kNegInf, kNegInf};
+                        by_columns(ts, [&](int c, float2 (&x)[16]) {
 #pragma unroll
-                        for (int j = 0; j < kKT / 4; ++j) {
-                            const float4 s4 = tab[j];
-                            x[2 * j] = __fmul2_rn(x[2 * j], make_float2(s4.x, s4.y));
-                            x[2 * j + 1] = __fmul2_rn(x[2 * j + 1], make_float2(s4.z, s4.w));
+                            for (int j = 0; j < 8; ++j) {
+                                const uint4 z = lds128(tk + uint32_t(128 * c + 16 * j));
+                                x[2 * j] = __fmul2_rn(x[2 * j], make_float2(__uint_as_float(z.x), __uint_as_float(z.y)));
+                                x[2 * j + 1] =
+                                    __fmul2_rn(x[2 * j + 1], make_float2(__uint_as_float(z.z), __uint_as_float(z.w)));
+                            }
+                            if (masked) {
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) {
+                                    x[j].x = 32 * c + 2 * j <= seen ? x[j].x : kNegInf;
+                                    x[j].y = 32 * c + 2 * j + 1 <= seen ? x[j].y : kNegInf;
+                                }
+                            }
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) mx[j & 1] = max3(mx[j & 1], x[j].x, x[j].y);
+                            tmem_store32(ts + 32u * uint32_t(c), reinterpret_cast<const uint32_t *>(x));
+                        });
+                        att_wait(&vs_full[i % (C::kScaleRing / 2)], uint32_t(i / (C::kScaleRing / 2)) & 1u, &ctl, a.err);
+                        lift = __uint_as_float(lds32(tv + uint32_t(kKT) * 4u));
+                        top = fmaxf(mx[0], mx[1]) * sc + lift;
+                        tmem_wait_st();
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) tmem_load32(ts + 32u * uint32_t(c), reinterpret_cast<uint32_t *>(xs + 16 * c));
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) tmem_landed32(reinterpret_cast<uint32_t *>(xs + 16 * c));
+                        if (masked) {
+#pragma unroll
+                            for (int j = 0; j < kKT / 2; ++j) {
+                                xs[j].x = 2 * j <= seen ? xs[j].x : kNegInf;
+                                xs[j].y = 2 * j + 1 <= seen ? xs[j].y : kNegInf;
+                            }
                         }
-                    }
-                    if (masked) {
-                        const int seen = pos - key0;
+                        float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
-                        for (int j = 0; j < kKT / 2; ++j) {
-                            x[j].x = 2 * j <= seen ? x[j].x : kNegInf;
-                            x[j].y = 2 * j + 1 <= seen ? x[j].y : kNegInf;
-                        }
+                        for (int j = 0; j < kKT / 2; ++j) mx[j & 3] = max3(mx[j & 3], xs[j].x, xs[j].y);
+                        top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
                     }
-                    float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-#pragma unroll
-                    for (int j = 0; j < kKT / 2; ++j) mx[j & 3] = fmaxf(mx[j & 3], fmaxf(x[j].x, x[j].y));
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc + lift;
                     if (k == k0) {
                         m = top;
                     } else {
@@ -421,6 +510,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
                                 uint32_t o[32];
                                 tmem_load32(to + uint32_t(c), o);
                                 tmem_wait_ld();
+                                tmem_landed32(o);
 #pragma unroll
                                 for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
                                 tmem_store32(to + uint32_t(c), o);
@@ -431,30 +521,46 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
                     const float mu = m == kNegInf ? 0.0f : m;
                     const float2 sc2 = make_float2(sc, sc), mu2 = make_float2(-mu, -mu);
                     float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                    if (Q8) {
+                        by_columns(ts, [&](int c, float2 (&x)[16]) {
+                            uint32_t p[16];
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t p[32];
+                            for (int j = 0; j < 8; ++j) {
+                                const uint4 z = lds128(tv + uint32_t(128 * c + 16 * j));
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            float2 e = __ffma2_rn(x[32 * c + j], sc2, mu2);
-                            e.x = ex2(e.x), e.y = ex2(e.y);
-                            sum[j & 1] = __fadd2_rn(sum[j & 1], e);
-                            if (Q8) {
-                                const float2 z = reinterpret_cast<const float2 *>(vsc)[32 * c + j];
-                                const float2 y = __fmul2_rn(e, z);
-                                // a masked weight is zero whatever the value's scale holds
-                                e = masked ? make_float2(e.x == 0.0f ? 0.0f : y.x, e.y == 0.0f ? 0.0f : y.y) : y;
+                                for (int h = 0; h < 2; ++h) {
+                                    float2 e = __ffma2_rn(x[2 * j + h], sc2, mu2);
+                                    e.x = ex2(e.x), e.y = ex2(e.y);
+                                    sum[h] = __fadd2_rn(sum[h], e);
+                                    e = __fmul2_rn(e, make_float2(__uint_as_float(h ? z.z : z.x), __uint_as_float(h ? z.w : z.y)));
+                                    p[2 * j + h] = pack_f16(e.x, e.y);
+                                }
                             }
-                            p[j] = Q8 ? pack_f16(e.x, e.y) : pack_bf16(e.x, e.y);
+                            tmem_store16(ts + 16u * uint32_t(c), p);  // (columns that have been read)
+                        });
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t p[32];
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                float2 e = __ffma2_rn(xs[32 * c + j], sc2, mu2);
+                                e.x = ex2(e.x), e.y = ex2(e.y);
+                                sum[j & 1] = __fadd2_rn(sum[j & 1], e);
+                                p[j] = pack_bf16(e.x, e.y);
+                            }
+                            tmem_store32(ts + 32u * uint32_t(c), p);
                         }
-                        tmem_store32(ts + 32u * uint32_t(c), p);
                     }
                     sum[0] = __fadd2_rn(sum[0], sum[1]);
                     l += sum[0].x + sum[0].y;
                     tmem_wait_st();
                 }
                 if (odd) {
-                    if (warp_valid) add_odd<D, Q8>(vb, from, until, pos - key0, ts, to);
+                    if (warp_valid) {
+                        if (Q8) clear_weights(scales + (2 * i + 1) % C::kScaleRing * C::kScales, from, until, pos - key0, ts);
+                        add_odd<D, Q8>(vb, from, until, pos - key0, ts, to);
+                    }
                     bar_any(TWO ? 1 : 2 + slot, TWO ? 256 : 128, false);
                     clear_odd<D, Q8>(vb, from, until, TWO ? int(threadIdx.x) : row, TWO ? 256 : 128);
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -477,6 +583,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
                     uint32_t o[32];
                     tmem_load32(to + uint32_t(c), o);
                     tmem_wait_ld();
+                    tmem_landed32(o);
                     if (valid)
 #pragma unroll
                         for (int j = 0; j < 32; ++j) dst[size_t(c + j) * (TWO ? 256 : 128)] = __uint_as_float(o[j]);
@@ -486,11 +593,14 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
     } else if (Q8 && warp >= kConvWarp) {
         // ---------------------------------------------------- converters
         regs_down<C::kRegsOther>();
-        const int cw = warp - kConvWarp;
+        // Units of 128 rows: two warps for the keys, two for the values, so
+        // that the next keys do not wait until a values' stage is free.
+        constexpr int W = TWO ? 4 : 2;                    // warps per half tile
+        const int cw = (warp - kConvWarp) % W;
         // a quarter-warp's 8 lanes read the pieces 0-3 of an even key and 4-7
         // of the next (128 channels), then the others: neither the reads nor
         // the writes of the fp16 pieces share a bank
-        const int odd = (lane >> 2) & 1, key = 8 * cw + 2 * (lane >> 3) + odd;  // and + 32, 64, 96
+        const int odd = (lane >> 2) & 1, key = 8 * cw + 2 * (lane >> 3) + odd;  // and 8 W, 16 W .. further
         uint32_t src_at[D / 64], dst_at[D / 64][2];
 #pragma unroll
         for (int p = 0; p < D / 64; ++p) {
@@ -505,62 +615,76 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
         AttSeg seg = sh.first[0];
         int left = seg.left, key0 = seg.key;  // of the segment; the tile's first key
 #pragma unroll 1
-        for (int h = 0; h < 2 * (t1 - t0); ++h) {  // keys and values in turn
-            if (h && !(h & 1)) {
+        for (int h = TWO ? 0 : (warp - kConvWarp) / W; h < 2 * (t1 - t0); h += TWO ? 1 : 2) {  // 2 i + (1 for values)
+            if (TWO ? h && !(h & 1) : h > 1) {
                 key0 += kKT;
                 if (--left == 0) {
                     att_next(a, plan, sh, seg);
                     left = seg.left, key0 = seg.key;
                 }
             }
-            const int si = h % SI, so = h % SO;
-            att_wait(&in_full[si], uint32_t(h / SI) & 1u, &ctl, a.err);
-            if (h >= SO) att_wait(&op_empty[so], uint32_t(h / SO - 1) & 1u, &ctl, a.err);
-            const uint32_t src = ring + uint32_t(si) * uint32_t(C::kIn);
+            const int si = h % SI, so = stage(h >> 1, h & 1), turn = used(h >> 1, h & 1), n_keys = seg.key_end - key0;  // keys of the tile (or more)
+            const uint32_t src = ring + uint32_t(si) * uint32_t(C::kIn), ss = src + uint32_t(C::kInScale);
             const uint32_t dst = ops + uint32_t(so) * uint32_t(C::kHalf);
+            float *sc = scales + (h % C::kScaleRing) * C::kScales;
+            const auto put_scales = [&] {
+#pragma unroll
+                for (int q = 0; q < 4 / W; ++q) {
+                    const int k = 32 * (cw + W * q) + lane;
+                    sc[k] = k < n_keys ? __uint_as_float(lds32(ss + uint32_t(k) * 4u)) : 0.0f;
+                }
+            };
+            att_wait(&in_full[si], uint32_t(h / SI) & 1u, &ctl, a.err);
+            if (h & 1) {  // the softmax takes the values' scales before their product is near
+                put_scales();
+                if (cw == 0) {  // and their bound
+                    uint32_t top = 0u;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float x = __uint_as_float(lds32(ss + uint32_t(32 * q + lane) * 4u));
+                        if (x <= 3.0e38f && 32 * q + lane < n_keys) top = max(top, __float_as_uint(x));
+                    }
+                    top = __reduce_max_sync(0xFFFFFFFFu, top);
+                    if (lane == 0) sc[kKT] = exp_above(__uint_as_float(top)) - 7.0f;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&vs_full[(h >> 1) % (C::kScaleRing / 2)]);
+            }
+            if (turn > 0) att_wait(&op_empty[so], uint32_t(turn - 1) & 1u, &ctl, a.err);
+            if (!(h & 1)) put_scales();
             // 16-byte pieces of e4m3 rows (16 channels), each to two pieces of
-            // the fp16 row; all reads first.  (key & 7) and so the swizzles
-            // are the same for every q.
-            uint4 x[4 * (D / 64)];
+            // the fp16 row; a batch's reads first.  (key & 7) and so the
+            // swizzles are the same for every q.
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-                for (int p = 0; p < D / 64; ++p) x[q * (D / 64) + p] = lds128(src + src_at[p] + uint32_t(32 * q * D));
-            if (seg.key_end - key0 < kKT)  // rows past the end may hold anything
+            for (int q0 = 0; q0 < 16 / W; q0 += 4) {
+                uint4 x[4 * (D / 64)];
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    if (key0 + key + 32 * q >= seg.key_end)
 #pragma unroll
-                        for (int p = 0; p < D / 64; ++p) x[q * (D / 64) + p] = make_uint4(0, 0, 0, 0);
+                    for (int p = 0; p < D / 64; ++p)
+                        x[q * (D / 64) + p] = lds128(src + src_at[p] + uint32_t(8 * W * (q0 + q) * D));
+                if (n_keys < kKT)  // rows past the end may hold anything
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+                    for (int q = 0; q < 4; ++q)
+                        if (key + 8 * W * (q0 + q) >= n_keys)
 #pragma unroll
-                for (int p = 0; p < D / 64; ++p) {
-                    const uint4 &y = x[q * (D / 64) + p];
-                    const uint32_t to = dst + uint32_t(32 * q * 128);
-                    sts128(to + dst_at[p][0], e4m3x2_lo_to_f16x2(y.x), e4m3x2_hi_to_f16x2(y.x), e4m3x2_lo_to_f16x2(y.y),
-                           e4m3x2_hi_to_f16x2(y.y));
-                    sts128(to + dst_at[p][1], e4m3x2_lo_to_f16x2(y.z), e4m3x2_hi_to_f16x2(y.z), e4m3x2_lo_to_f16x2(y.w),
-                           e4m3x2_hi_to_f16x2(y.w));
-                }
-            const int n_keys = seg.key_end - key0;  // of the tile (or more)
-            float *sc = scales + (h % C::kScaleRing) * C::kScales;
-            const uint32_t ss = src + uint32_t(C::kInScale);
-            sc[32 * cw + lane] = 32 * cw + lane < n_keys ? __uint_as_float(lds32(ss + uint32_t(32 * cw + lane) * 4u)) : 0.0f;
-            if (cw == 0 && (h & 1)) {  // the bound of the tile's value scales
-                uint32_t top = 0u;
+                            for (int p = 0; p < D / 64; ++p) x[q * (D / 64) + p] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float x = __uint_as_float(lds32(ss + uint32_t(32 * q + lane) * 4u));
-                    if (x <= 3.0e38f && 32 * q + lane < n_keys) top = max(top, __float_as_uint(x));
-                }
-                top = __reduce_max_sync(0xFFFFFFFFu, top);
-                if (lane == 0) sc[kKT] = exp_above(__uint_as_float(top)) - 7.0f;
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int p = 0; p < D / 64; ++p) {
+                        const uint4 &y = x[q * (D / 64) + p];
+                        const uint32_t to = dst + uint32_t(8 * W * (q0 + q) * 128);
+                        sts128(to + dst_at[p][0], e4m3x2_lo_to_f16x2(y.x), e4m3x2_hi_to_f16x2(y.x),
+                               e4m3x2_lo_to_f16x2(y.y), e4m3x2_hi_to_f16x2(y.y));
+                        sts128(to + dst_at[p][1], e4m3x2_lo_to_f16x2(y.z), e4m3x2_hi_to_f16x2(y.z),
+                               e4m3x2_lo_to_f16x2(y.w), e4m3x2_hi_to_f16x2(y.w));
+                    }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&op_full[so]);
+                mbar_arrive(&op_full[C::kOwn && (h & 3) == 2 ? 3 : so]);
                 mbar_arrive(&in_empty[si]);
             }
         }
@@ -642,7 +766,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
                     // (zeros were written to the output, see the softmax warps)
                     const bool zeroed = seg.key + (k0 + 1) * kKT - 1 > att_seen_by_all(a, seg);
                     att_wait(&q_full[slot], n_seg++ & 1u, &ctl, a.err);
-                    att_wait(&op_full[stage(i0 + k0, 0)], phase(i0 + k0, 0), &ctl, a.err);
+                    wait_operand(i0 + k0, 0);
                     tmem_fence_after();
                     scores(i0 + k0, false);
 #pragma unroll 1
@@ -650,10 +774,10 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
                         const int i = i0 + k, s = stage(i, 1);
                         const bool more = k + kStep < n;
                         const int burst = TWO ? 2 * i + slot : i;  // of the CTA; odd ones are slot 1's
-                        att_wait(&op_full[s], phase(i, 1), &ctl, a.err);
+                        wait_operand(i, 1);
                         // e4m3: the next keys may be converted only after the
                         // values' stage of a tile before was released
-                        if (!Q8 && more) att_wait(&op_full[stage(i + kStep, 0)], phase(i + kStep, 0), &ctl, a.err);
+                        if (!Q8 && more) wait_operand(i + kStep, 0);
                         att_wait(&p_full[slot], n_p++ & 1u, &ctl, a.err);
                         if (burst > 0) att_wait(&token[slot], uint32_t((burst - 1) / 2) & 1u, &ctl, a.err);
                         tmem_fence_after();
@@ -667,7 +791,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
                         umma_arrive(&op_empty[s]);
                         if (more) {
                             if (Q8) {
-                                att_wait(&op_full[stage(i + kStep, 0)], phase(i + kStep, 0), &ctl, a.err);
+                                wait_operand(i + kStep, 0);
                                 tmem_fence_after();
                             }
                             scores(i + kStep, true);

@@ -83,4 +83,13 @@ __device__ __forceinline__ void tmem_load32(uint32_t taddr, uint32_t *r) {
         : "r"(taddr));
 }
 
+// After tmem_wait_ld(): the loaded registers are used from here on (the wait
+// itself names none of them).
+__device__ __forceinline__ void tmem_landed32(uint32_t *r) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+        asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                     "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+
 }  // namespace w12
