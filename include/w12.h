@@ -540,7 +540,8 @@ int w12_kv_read(const w12_kv *kv, const int32_t *block_table_dev, int64_t blocks
 #define W12_ATTEND_MAX_R 512
 
 /* Bytes of workspace w12_attend needs (0 on invalid arguments; max_len and
- * prefix_len as in the call). */
+ * prefix_len as in the call).  A workspace serves calls of all sizes that
+ * need no more than it has. */
 size_t w12_attend_workspace_size(const w12_kv *kv, int64_t R, int64_t T, int q_heads, int64_t max_len,
                                  int64_t prefix_len);
 

@@ -50,6 +50,8 @@ int check_kv(const w12_kv *kv) {
 
 constexpr int64_t kLim31 = int64_t(1) << 31;
 
+constexpr size_t kWsCounters = 4096;
+
 struct AttendPlan {
     int32_t rows;
     struct Line {
@@ -103,7 +105,8 @@ int plan_attend(const w12_kv *kv, int64_t R, int64_t T, int q_heads, int64_t max
     if (current_sms(&sms) != W12_OK) return W12_ERR_CUDA;
     size_t off = kWsHeader;
     p->off_arrived = off;
-    off += round256(uint64_t(kv->heads) * R * 4u);
+    off += kWsCounters;  // (the same for all sizes: one workspace serves them all)
+    if (uint64_t(2 * sms) * 4u > kWsCounters) return W12_ERR_CUDA;
     p->off_plan = off;
     off += round256(uint64_t(R + 2) * 4u);
     p->join = l[kLinePrefix].pu + l[kLineRequests].su > 0;
@@ -228,6 +231,7 @@ extern "C" int w12_attend(const w12_kv *kv, const uint16_t *q, int64_t q_stride,
     a.arrived = reinterpret_cast<uint32_t *>(w + p.off_arrived);
     a.plan = reinterpret_cast<int32_t *>(w + p.off_plan);
     a.join = p.join;
+    a.per_g = ~uint64_t(0) / uint64_t(a.G) + 1;
     for (int i = 0; i < kLines; ++i) {
         const auto &n = p.line[i];
         a.line[i] = {n.pu, n.su, n.rt, n.halves, n.grid, reinterpret_cast<float *>(w + n.off_o),

@@ -21,10 +21,12 @@
 // share of a unit is a segment; it leaves its (m, l, O) -- reference exponent,
 // sum and unnormalised output -- in slot (unit + worker), which no other
 // segment has: from one segment to the next either the unit or the worker
-// goes up, never down.  Where only the rest line has results, the worker that
-// finishes a unit's last segment adds them up (a unit of one segment is
-// written at once); else a join kernel does.  Both in a fixed order, so the
-// outputs do not depend on timing.
+// goes up, never down.  Where the register kernel has all the results, the
+// worker that finishes a unit's last segment adds them up.  With results of
+// the tensor-memory kernel a join kernel does: 40 KB and more per unit, which
+// one worker takes three times as long to fetch as a whole kernel (128
+// requests under a prefix: 42 us against 13).  All sums have a fixed order: the outputs do not
+// depend on timing.
 #pragma once
 
 #include "async_common.cuh"
@@ -34,6 +36,12 @@
 namespace w12 {
 
 constexpr int kAttMaxR = W12_ATTEND_MAX_R;
+
+// rho / G, by the reciprocal: rho * (2^64 / G, rounded up) is too large by less
+// than rho * G < 2^64 / G for rows and heads in range, so the floor is exact.
+__device__ __forceinline__ int att_token(const AttendArgs &a, int rho) {
+    return a.G == 1 ? rho : int(__umul64hi(uint64_t(uint32_t(rho)), a.per_g));
+}
 
 // A position on the line: a unit, its first key from here on, its tiles left.
 struct AttSeg {
@@ -111,7 +119,7 @@ __device__ __forceinline__ void att_unit_at(const AttendArgs &a, const AttPlan &
 
 // The last key that every row of the segment's unit sees.
 __device__ __forceinline__ int att_seen_by_all(const AttendArgs &a, const AttSeg &s) {
-    return a.self == kLinePrefix ? 0x7FFFFFFF : s.key_end - a.T + s.row0 / a.G - s.req * a.T;
+    return a.self == kLinePrefix ? 0x7FFFFFFF : s.key_end - a.T + att_token(a, s.row0) - s.req * a.T;
 }
 
 // The position of tile t of the line.
@@ -155,38 +163,41 @@ __device__ __forceinline__ void att_next(const AttendArgs &a, const AttPlan &p, 
 __device__ __forceinline__ AttPlan att_plan(const AttendArgs &a, AttShared &sh, int workers, int worker) {
     const int lane = threadIdx.x & 31;
     const AttendLine &ln = a.line[a.self];
+    for (int r = threadIdx.x; r < a.R; r += int(blockDim.x)) {
+        const int n0 = a.kv_len[r], n = att_len(a, n0);
+        if (n0 > n && blockIdx.x == 0) atomicCAS(a.err, 0, W12_ERR_DEVICE);
+        sh.lens[r] = n;
+    }
+    __syncthreads();
     if (threadIdx.x < 32) {
-        int longest = 0, shortest = 0x7FFFFFFF;
-        for (int r = lane; r < a.R; r += 32) {
-            const int n0 = a.kv_len[r], n = att_len(a, n0);
-            if (n0 > n && blockIdx.x == 0) atomicCAS(a.err, 0, W12_ERR_DEVICE);
-            sh.lens[r] = n;
-            longest = max(longest, n);
-            shortest = min(shortest, n);
+        int w = 0;
+        if (a.line[kLinePrefix].grid) {
+            int shortest = 0x7FFFFFFF;
+            for (int r = lane; r < a.R; r += 32) shortest = min(shortest, sh.lens[r]);
+            w = att_prefix_whole(a, __reduce_min_sync(0xFFFFFFFFu, shortest));
         }
-        shortest = __reduce_min_sync(0xFFFFFFFFu, shortest);
-        const int w = att_prefix_whole(a, shortest);
-        __syncwarp();
+        // a lane's requests are neighbours
+        const int per = (a.R + 31) / 32, r0 = lane * per, r1 = min(r0 + per, a.R);
         int sum = 0;
-        const bool tell = a.join && a.self != kLinePrefix && blockIdx.x == 0;  // for the join kernel
-        for (int r0 = 0; r0 < a.R; r0 += 32) {
-            const int r = r0 + lane;
-            const int n = r < a.R ? sh.lens[r] : 0;
-            int x = r < a.R ? att_req_tiles(a, w, n) : 0;
-            const int y = x;
+        for (int r = r0; r < r1; ++r) sum += att_req_tiles(a, w, sh.lens[r]);
+        int x = sum;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int z = __shfl_up_sync(0xFFFFFFFFu, x, o);
-                if (lane >= o) x += z;
-            }
-            if (r < a.R) sh.cum[r] = sum + x - y;
-            sum += __shfl_sync(0xFFFFFFFFu, x, 31);
-            if (r < a.R && tell) a.plan[1 + r] = sh.cum[r];
+        for (int o = 1; o < 32; o <<= 1) {
+            const int z = __shfl_up_sync(0xFFFFFFFFu, x, o);
+            if (lane >= o) x += z;
+        }
+        if (lane == 31) sh.cum[a.R] = x;
+        x -= sum;
+        const bool tell = a.join && a.self != kLinePrefix && blockIdx.x == 0;  // the join kernel
+        if (lane == 31 && tell) a.plan[1 + a.R] = x + sum;
+        for (int r = r0; r < r1; ++r) {
+            sh.cum[r] = x;
+            if (tell) a.plan[1 + r] = x;
+            x += att_req_tiles(a, w, sh.lens[r]);
         }
         if (lane == 0) {
-            sh.cum[a.R] = sum;
             sh.w = w;
-            if (tell) a.plan[0] = w, a.plan[1 + a.R] = sum;
+            if (tell) a.plan[0] = w;
         }
     }
     __syncthreads();
@@ -196,12 +207,25 @@ __device__ __forceinline__ AttPlan att_plan(const AttendArgs &a, AttShared &sh, 
     p.per_head = ln.pu * p.np + ln.su * sh.cum[a.R];
     const int total = p.per_head * a.heads;
     // the CTA's `workers` workers; this thread's is number `worker` of them
-    const int c = int(blockIdx.x) * workers + worker;
-    p.t0 = att_begin(total, ln.grid, c);
-    p.t1 = att_begin(total, ln.grid, c + 1);
-    if (int(threadIdx.x) < workers) {
-        const int t = att_begin(total, ln.grid, int(blockIdx.x) * workers + int(threadIdx.x));
-        if (t < total) sh.first[threadIdx.x] = att_locate(a, p, sh, t);
+    const int c0 = int(blockIdx.x) * workers;
+    p.t0 = att_begin(total, ln.grid, c0 + worker);
+    p.t1 = att_begin(total, ln.grid, c0 + worker + 1);
+    const int q = int(threadIdx.x >> 5);  // a warp finds a worker's first tile
+    if (q < workers) {
+        const int t = att_begin(total, ln.grid, c0 + q);
+        if (t < total && a.self == kLinePrefix) {
+            if (lane == 0) sh.first[q] = att_locate(a, p, sh, t);
+        } else if (t < total) {
+            const int head = t / p.per_head, at = t - head * p.per_head, x = at / ln.su;
+            for (int r = lane; r < a.R; r += 32)
+                if (sh.cum[r] <= x && x < sh.cum[r + 1]) {  // one lane's request
+                    const int n = sh.cum[r + 1] - sh.cum[r], in_req = at - sh.cum[r] * ln.su;
+                    AttSeg s;
+                    s.head = head, s.req = r, s.block = in_req / n;
+                    att_unit_at(a, p, sh, s, in_req - s.block * n);
+                    sh.first[q] = s;
+                }
+        }
     }
     __syncthreads();
     return p;
@@ -356,13 +380,42 @@ __device__ __forceinline__ void att_add(const AttendLine &ln, int64_t first, int
 // The output row of query row rho of a head, and its lse.
 template <int D>
 __device__ __forceinline__ uint16_t *att_out(const AttendArgs &a, int head, int rho) {
-    const int tok = rho / a.G, hq = head * a.G + rho - tok * a.G;
+    const int tok = att_token(a, rho), hq = head * a.G + rho - tok * a.G;
     return a.out + int64_t(tok) * a.out_stride + int64_t(hq) * D;
 }
 __device__ __forceinline__ void att_store_lse(const AttendArgs &a, int head, int rho, float mu, float l) {
     if (!a.lse) return;
-    const int tok = rho / a.G, hq = head * a.G + rho - tok * a.G;
+    const int tok = att_token(a, rho), hq = head * a.G + rho - tok * a.G;
     a.lse[int64_t(tok) * (a.G * a.heads) + hq] = l == 0.0f ? -INFINITY : (mu + log2f(l)) * 0.6931471805599453f;
+}
+
+// Where a unit of n tiles from b on of a line of `total` lies: its first
+// worker, its segments.
+__device__ __forceinline__ void att_segments(const AttendLine &ln, int total, int b, int n, int &first, int &segments) {
+    first = att_owner(total, ln.grid, b);
+    segments = att_owner(total, ln.grid, b + n - 1) - first + 1;
+}
+__device__ __forceinline__ void att_unit_segments(const AttendArgs &a, const AttPlan &p, const AttShared &sh,
+                                                  const AttSeg &s, int &first, int &segments) {
+    const AttendLine &ln = a.line[a.self];
+    const int n = sh.cum[s.req + 1] - sh.cum[s.req];
+    att_segments(ln, p.per_head * a.heads, s.head * p.per_head + ln.su * sh.cum[s.req] + s.block * n, n, first, segments);
+}
+
+// True in the worker that is the last of a unit's `segments` to get here (one
+// thread; the others' results are behind a barrier that it has passed).  A
+// worker is the first of at most one unit with several segments, so it names
+// the counter.
+__device__ __forceinline__ bool att_last(const AttendArgs &a, int first, int segments) {
+    if (segments == 1) return true;
+    uint32_t before;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;"
+                 : "=r"(before)
+                 : "l"(&a.arrived[first])
+                 : "memory");
+    const bool last = before == uint32_t(segments - 1);
+    if (last) a.arrived[first] = 0u;
+    return last;
 }
 
 }  // namespace w12

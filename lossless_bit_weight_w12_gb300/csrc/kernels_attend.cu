@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_kernel(const __grid_
             const int row = (tid + x * kGT) / (D / 8), c = (tid + x * kGT) % (D / 8);
             qn[x] = make_uint4(0, 0, 0, 0);
             if (row < s.nrows && row < RT) {
-                const int rho = s.row0 + row, tok = rho / a.G, hq = s.head * a.G + rho - tok * a.G;
+                const int rho = s.row0 + row, tok = att_token(a, rho), hq = s.head * a.G + rho - tok * a.G;
                 qn[x] = *reinterpret_cast<const uint4 *>(a.q + tok * a.q_stride + int64_t(hq) * D + 8 * c);
             }
         }
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_kernel(const __grid_
                 up[n][c] = a.scale_log2 * (Q8 ? q_up[row] : 1.0f);
                 pos[n][c] = 0x7FFFFFFF;  // rows past the unit: their results are not kept
                 if (row < seg.nrows)  // (a unit's rows are of one request)
-                    pos[n][c] = seg.key_end - a.T + (seg.row0 + row) / a.G - seg.req * a.T;
+                    pos[n][c] = seg.key_end - a.T + att_token(a, seg.row0 + row) - seg.req * a.T;
                 min_pos = min(min_pos, pos[n][c]);
             }
         min_pos = __reduce_min_sync(0xFFFFFFFFu, min_pos);
@@ -620,14 +620,9 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_kernel(const __grid_
         }
 
         // ---- the segment's end: add up the worker's four (m, l, O) in warp order
-        int first = 0, n_seg = 2;  // the unit's segments: the first worker, how many (join: not needed)
-        if (!a.join) {
-            const int n = sh.cum[seg.req + 1] - sh.cum[seg.req], total = plan.per_head * a.heads;
-            const int b = seg.head * plan.per_head + ln.su * sh.cum[seg.req] + seg.block * n;
-            first = att_owner(total, ln.grid, b);
-            n_seg = att_owner(total, ln.grid, b + n - 1) - first + 1;
-        }
-        const bool alone = n_seg == 1;  // the only result of its rows
+        int first, n_seg;
+        att_unit_segments(a, plan, sh, seg, first, n_seg);
+        const bool alone = n_seg == 1 && !a.join;  // the only result of its rows
         const int64_t entry = int64_t(seg.unit) + 2 * int(blockIdx.x) + me;
 #pragma unroll
         for (int n = 0; n < NR; ++n)
@@ -702,15 +697,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_kernel(const __grid_
         }
         if (!alone && !a.join) {
             // the worker that is done with the unit's last segment adds them up
-            if (tid == 0) {  // (the step above ended with a barrier)
-                uint32_t before;
-                asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;"
-                             : "=r"(before)
-                             : "l"(&a.arrived[seg.unit])
-                             : "memory");
-                s_last[me] = before == uint32_t(n_seg - 1);
-                if (s_last[me]) a.arrived[seg.unit] = 0u;
-            }
+            if (tid == 0) s_last[me] = att_last(a, first, n_seg);  // (the step above ended with a barrier)
             worker_sync(me);
             if (s_last[me]) {
                 constexpr int CH = RT * D / kGT, U = CH <= 4 ? 8 : CH <= 8 ? 4 : 1;
@@ -751,18 +738,15 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     const int32_t *cum = a.plan + 1;
     const int np = a.plan[0], q0 = cum[r], q1 = cum[r + 1], qa = cum[a.R];
     float m = kNegInf, l = 0.0f, acc[kJC] = {};
-    if (lp.grid && np) {
-        const int p = rho / lp.rt, u = head * lp.pu + p, b = u * np, total = a.heads * lp.pu * np;
-        const int c = att_owner(total, lp.grid, b);
-        att_add<D, kJC, 4>(lp, int64_t(u + c) * lp.halves, (att_owner(total, lp.grid, b + np - 1) - c + 1) * lp.halves,
-                           rho - p * lp.rt, d0, m, l, acc);
-    }
-    {
-        const int s = in_req / lq.rt, b = head * lq.su * qa + lq.su * q0 + s * (q1 - q0), total = a.heads * lq.su * qa;
-        const int c = att_owner(total, lq.grid, b);
-        att_add<D, kJC, 4>(lq, int64_t((head * a.R + r) * lq.su + s + c) * lq.halves,
-                           (att_owner(total, lq.grid, b + q1 - q0 - 1) - c + 1) * lq.halves, in_req - s * lq.rt, d0, m,
-                           l, acc);
+    int c, n;
+    const int s = in_req / lq.rt;
+    att_segments(lq, a.heads * lq.su * qa, head * lq.su * qa + lq.su * q0 + s * (q1 - q0), q1 - q0, c, n);
+    const int u = (head * a.R + r) * lq.su + s;
+    att_add<D, kJC, 4>(lq, int64_t(u + c) * lq.halves, n * lq.halves, in_req - s * lq.rt, d0, m, l, acc);
+    if (np > 0) {
+        const int b = rho / lp.rt, up = head * lp.pu + b;
+        att_segments(lp, a.heads * lp.pu * np, up * np, np, c, n);
+        att_add<D, kJC, 4>(lp, int64_t(up + c) * lp.halves, n * lp.halves, rho - b * lp.rt, d0, m, l, acc);
     }
     const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);  // no key: zeros
     *reinterpret_cast<uint2 *>(att_out<D>(a, head, rho) + d0) =

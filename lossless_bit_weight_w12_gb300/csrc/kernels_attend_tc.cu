@@ -361,7 +361,8 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
                 const uint32_t qb = base + uint32_t(TWO ? slot : 0) * uint32_t(128 * D * 2);
                 const uint32_t sign = a.scale_log2 < 0.0f ? 0x80008000u : 0u;  // scores grow with S
                 const int first = TWO ? 32 * (warp & 3) : 16 * warp;
-                constexpr int B = 8;                              // loads in flight
+                constexpr int B = kRows / RPW < 8 ? kRows / RPW : 8;  // loads in flight
+                static_assert(kRows % (B * RPW) == 0, "rows of a warp");
 #pragma unroll 1
                 for (int x0 = 0; x0 < kRows; x0 += B * RPW) {
                     uint4 q[B];
@@ -370,7 +371,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
                         const int in_u = (TWO ? 128 * slot : 0) + first + x0 + x * RPW + lane / L;
                         q[x] = make_uint4(0, 0, 0, 0);
                         if (in_u < seg.nrows) {
-                            const int rho = seg.row0 + in_u, tok = rho / a.G, hq = seg.head * a.G + rho - tok * a.G;
+                            const int rho = seg.row0 + in_u, tok = att_token(a, rho), hq = seg.head * a.G + rho - tok * a.G;
                             q[x] = *reinterpret_cast<const uint4 *>(a.q + tok * a.q_stride + int64_t(hq) * D + 8 * c);
                         }
                     }
@@ -404,7 +405,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
             if (Q8) sc *= q_up[in_unit];
             sc = fmaxf(sc, 1e-37f);  // (a mask's -infinity times 0 would be NaN)
             const int all_see = att_seen_by_all(a, seg);
-            const int pos = valid && a.self != kLinePrefix ? seg.key_end - a.T + (seg.row0 + in_unit) / a.G - seg.req * a.T
+            const int pos = valid && a.self != kLinePrefix ? seg.key_end - a.T + att_token(a, seg.row0 + in_unit) - seg.req * a.T
                                                            : seg.key_end - 1;
             if (k0 >= n) {  // no tile of the segment is this slot's
                 if (valid) ln.part_ml[at] = make_float2(kNegInf, 0.0f);

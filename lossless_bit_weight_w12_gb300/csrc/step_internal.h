@@ -100,9 +100,10 @@ struct AttendArgs {
     int32_t self;      // the line of this launch
     float scale_log2;  // scale * log2(e)
     int *err;
-    uint32_t *arrived;  // [rest units] segments that are done; zero between calls
+    uint64_t per_g;     // 2^64 / G, rounded up (G = 1: not used)
+    uint32_t *arrived;  // [workers] segments of a unit that are done; zero between calls
     int32_t *plan;      // for the join: W, then the R + 1 cumulative tiles of the requests
-    int32_t join;       // 1: a join kernel adds up the results (the tensor-memory kernel has some)
+    int32_t join;       // 1: a join kernel adds up the results
     AttendLine line[kLines];
 };
 int attend_make_maps(AttendArgs &a, const w12_kv *kv);

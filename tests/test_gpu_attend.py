@@ -297,6 +297,20 @@ def test_long_context_offsets(dev, w12mod):
     assert bool(((lse[0].double() - torch.logsumexp(sc, -1).reshape(-1)).abs() <= 2.0 ** -15).all())
 
 
+def test_one_workspace_for_all_sizes(dev, w12mod):
+    """A workspace used for one size serves any other that fits, back and forth."""
+    shapes = [(4, 1, 48, 8, 128, 64, [1, 300, 2500, 777], 0), (2, 16, 12, 2, 128, 64, [16, 517], 0),
+              (1, 130, 2, 1, 128, 32, [2000], 0), (7, 1, 12, 2, 128, 32, [333, 400, 334, 1000, 350, 360, 500], 333),
+              (1, 1, 6, 1, 128, 64, [9000], 0)]
+    probs = [Problem(w12mod, dev, *c[:6], e4m3, c[6], c[7]) for c in shapes for e4m3 in (False, True)]
+    need = max(w12mod.attend_workspace_size(p.kv, p.R, p.T, p.hq, max(p.lens), p.prefix) for p in probs)
+    ws = w12mod.workspace(need, dev)
+    for p in probs + probs[::-1]:
+        out, lse = p.run(ws=ws)
+        p.check(out, lse)
+    assert w12mod.get_device_error(ws) == 0
+
+
 def test_device_errors(dev, w12mod):
     """Lengths above max_len or the table, and pages outside the cache: told in
     the workspace's error word, which get_device_error clears."""
