@@ -321,12 +321,6 @@ __device__ __forceinline__ bool att_wait(uint64_t *bar, uint32_t parity, WaitCtl
     return mbar_wait(bar, parity, ctl, err);
 }
 
-// Adds up n entries from `first` on of row r and channels d0 .. d0 + C - 1 in a
-// line's results; U entries are in flight.
-template <int D, int C, int U>
-__device__ __forceinline__ void att_add(const AttendLine &ln, int64_t first, int n, int r, int d0, float &m, float &l,
-                                        float (&acc)[C]);
-
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -338,12 +332,17 @@ __device__ __forceinline__ float exp_above(float x) {
     return float(int(__float_as_uint(fmaxf(x, 1e-30f)) >> 23) - 126);
 }
 
-template <int D, int C, int U>
+// Adds up n entries from `first` on of row r and channels d0 .. d0 + C - 1 in a
+// line's results; U entries are in flight.  ROWS: the register kernel's order
+// of them (a short loop of wide loads: one worker runs it, on code that its SM
+// has not met before; with a load per channel the last worker took 9 us for 9
+// entries).
+template <int D, bool ROWS, int C, int U>
 __device__ __forceinline__ void att_add(const AttendLine &ln, int64_t first, int n, int r, int d0, float &m, float &l,
                                         float (&acc)[C]) {
     const int rt = ln.rt;
     const float2 *pm = ln.part_ml + first * rt + r;
-    const float *po = ln.part_o + (first * D + d0) * rt + r;
+    const float *po = ln.part_o + (ROWS ? (first * rt + r) * D + d0 : (first * D + d0) * rt + r);
 #pragma unroll 1
     for (int k0 = 0; k0 < n; k0 += U) {
         // (past the last entry: the last one again, with weight 0)
@@ -354,8 +353,16 @@ __device__ __forceinline__ void att_add(const AttendLine &ln, int64_t first, int
             const int e = min(k0 + k, n - 1);
             ml[k] = __ldcg(pm + int64_t(e) * rt);
             const float *src = po + int64_t(e) * (D * rt);
+            if (ROWS) {
 #pragma unroll
-            for (int c = 0; c < C; ++c) x[k][c] = __ldcg(src + c * rt);
+                for (int c = 0; c < C; c += 4) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + c));
+                    x[k][c] = v.x, x[k][c + 1] = v.y, x[k][c + 2] = v.z, x[k][c + 3] = v.w;
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < C; ++c) x[k][c] = __ldcg(src + c * rt);
+            }
         }
         float mn = m;
 #pragma unroll

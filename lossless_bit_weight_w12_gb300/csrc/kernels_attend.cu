@@ -687,8 +687,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_kernel(const __grid_
                             *reinterpret_cast<uint32_t *>(att_out<D>(a, seg.head, seg.row0 + row) + d) =
                                 pack_bf16(x0 * inv, x1 * inv);
                         } else {
-                            ln.part_o[(entry * D + d) * RT + row] = x0;
-                            ln.part_o[(entry * D + d + 1) * RT + row] = x1;
+                            *reinterpret_cast<float2 *>(&ln.part_o[(entry * RT + row) * D + d]) = make_float2(x0, x1);
                         }
                     }
                 }
@@ -700,15 +699,18 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_kernel(const __grid_
             if (tid == 0) s_last[me] = att_last(a, first, n_seg);  // (the step above ended with a barrier)
             worker_sync(me);
             if (s_last[me]) {
-                constexpr int CH = RT * D / kGT, U = CH <= 4 ? 8 : CH <= 8 ? 4 : 1;
-                const int row = tid % RT, d0 = tid / RT * CH;
-                if (row < seg.nrows) {
-                    float m = kNegInf, l = 0.0f, acc[CH] = {};
-                    att_add<D, CH, U>(ln, int64_t(seg.unit) + first, n_seg, row, d0, m, l, acc);
+                constexpr int L = D / 8;  // lanes per row, 8 channels each
+                const int d0 = tid % L * 8;
+#pragma unroll 1
+                for (int row = tid / L; row < seg.nrows; row += kGT / L) {
+                    float m = kNegInf, l = 0.0f, acc[8] = {};
+                    att_add<D, true, 8, 8>(ln, int64_t(seg.unit) + first, n_seg, row, d0, m, l, acc);
                     const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
-                    uint32_t *dst = reinterpret_cast<uint32_t *>(att_out<D>(a, seg.head, seg.row0 + row) + d0);
+                    uint2 *dst = reinterpret_cast<uint2 *>(att_out<D>(a, seg.head, seg.row0 + row) + d0);
 #pragma unroll
-                    for (int c = 0; c < CH; c += 2) dst[c / 2] = pack_bf16(acc[c] * inv, acc[c + 1] * inv);
+                    for (int c = 0; c < 8; c += 4)
+                        dst[c / 4] = make_uint2(pack_bf16(acc[c] * inv, acc[c + 1] * inv),
+                                                pack_bf16(acc[c + 2] * inv, acc[c + 3] * inv));
                     if (d0 == 0) att_store_lse(a, seg.head, seg.row0 + row, m == kNegInf ? 0.0f : m, l);
                 }
             }
@@ -742,11 +744,14 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     const int s = in_req / lq.rt;
     att_segments(lq, a.heads * lq.su * qa, head * lq.su * qa + lq.su * q0 + s * (q1 - q0), q1 - q0, c, n);
     const int u = (head * a.R + r) * lq.su + s;
-    att_add<D, kJC, 4>(lq, int64_t(u + c) * lq.halves, n * lq.halves, in_req - s * lq.rt, d0, m, l, acc);
+    if (a.line[kLineRequests].grid)
+        att_add<D, false, kJC, 4>(lq, int64_t(u + c) * lq.halves, n * lq.halves, in_req - s * lq.rt, d0, m, l, acc);
+    else
+        att_add<D, true, kJC, 2>(lq, int64_t(u + c), n, in_req - s * lq.rt, d0, m, l, acc);
     if (np > 0) {
         const int b = rho / lp.rt, up = head * lp.pu + b;
         att_segments(lp, a.heads * lp.pu * np, up * np, np, c, n);
-        att_add<D, kJC, 4>(lp, int64_t(up + c) * lp.halves, n * lp.halves, rho - b * lp.rt, d0, m, l, acc);
+        att_add<D, false, kJC, 4>(lp, int64_t(up + c) * lp.halves, n * lp.halves, rho - b * lp.rt, d0, m, l, acc);
     }
     const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);  // no key: zeros
     *reinterpret_cast<uint2 *>(att_out<D>(a, head, rho) + d0) =

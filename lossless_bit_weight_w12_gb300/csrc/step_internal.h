@@ -77,7 +77,7 @@ struct AttendLine {
     int32_t rt;       // query rows per unit
     int32_t halves;   // results per segment (2: its tiles in two alternating halves)
     int32_t grid;     // workers that cut it (CTAs, or halves of CTAs); 0: the line is not used
-    float *part_o;    // [slots][halves][head_dim][rt]
+    float *part_o;    // [slots][halves][head_dim][rt]; the register kernel's: [slots][rt][head_dim]
     float2 *part_ml;  // [slots][halves][rt]: reference exponent (log2 units) and sum
 };
 
