@@ -332,17 +332,12 @@ __device__ __forceinline__ float exp_above(float x) {
     return float(int(__float_as_uint(fmaxf(x, 1e-30f)) >> 23) - 126);
 }
 
-// Adds up n entries from `first` on of row r and channels d0 .. d0 + C - 1 in a
-// line's results; U entries are in flight.  ROWS: the register kernel's order
-// of them (a short loop of wide loads: one worker runs it, on code that its SM
-// has not met before; with a load per channel the last worker took 9 us for 9
-// entries).
+// Adds up n entries of a row: from pm (reference and sum) and po (channels),
+// `rt` rows from entry to entry; U are in flight.  ROWS: the register kernel's
+// order of the channels.
 template <int D, bool ROWS, int C, int U>
-__device__ __forceinline__ void att_add(const AttendLine &ln, int64_t first, int n, int r, int d0, float &m, float &l,
+__device__ __forceinline__ void att_add(const float2 *pm, const float *po, int rt, int n, float &m, float &l,
                                         float (&acc)[C]) {
-    const int rt = ln.rt;
-    const float2 *pm = ln.part_ml + first * rt + r;
-    const float *po = ln.part_o + (ROWS ? (first * rt + r) * D + d0 : (first * D + d0) * rt + r);
 #pragma unroll 1
     for (int k0 = 0; k0 < n; k0 += U) {
         // (past the last entry: the last one again, with weight 0)
@@ -351,8 +346,8 @@ __device__ __forceinline__ void att_add(const AttendLine &ln, int64_t first, int
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             const int e = min(k0 + k, n - 1);
-            ml[k] = __ldcg(pm + int64_t(e) * rt);
-            const float *src = po + int64_t(e) * (D * rt);
+            ml[k] = __ldcg(pm + size_t(uint32_t(e * rt)));
+            const float *src = po + size_t(uint32_t(e * rt)) * D;
             if (ROWS) {
 #pragma unroll
                 for (int c = 0; c < C; c += 4) {
@@ -374,12 +369,12 @@ __device__ __forceinline__ void att_add(const AttendLine &ln, int64_t first, int
         for (int c = 0; c < C; ++c) acc[c] *= down;
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-            // (an entry without keys may hold anything)
-            const bool none = k0 + k >= n || (ml[k].x == -INFINITY && ml[k].y == 0.0f);
-            const float f = ex2(ml[k].x - mu);
-            l += none ? 0.0f : ml[k].y * f;
+            // (a row without keys: the register kernel has zeros, the other anything)
+            const bool none = k0 + k >= n || (!ROWS && ml[k].x == -INFINITY && ml[k].y == 0.0f);
+            const float f = none ? 0.0f : ex2(ml[k].x - mu);
+            l += ml[k].y * f;
 #pragma unroll
-            for (int c = 0; c < C; ++c) acc[c] += none ? 0.0f : x[k][c] * f;
+            for (int c = 0; c < C; ++c) acc[c] += !ROWS && none ? 0.0f : x[k][c] * f;
         }
     }
 }

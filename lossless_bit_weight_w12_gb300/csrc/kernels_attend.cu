@@ -699,12 +699,16 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_kernel(const __grid_
             if (tid == 0) s_last[me] = att_last(a, first, n_seg);  // (the step above ended with a barrier)
             worker_sync(me);
             if (s_last[me]) {
+                // (short code: the worker runs it once, and its SM has not
+                // met it before; with a load per channel and entry, or in
+                // 300 instructions, this took 9 or 6 us for 9 entries)
                 constexpr int L = D / 8;  // lanes per row, 8 channels each
                 const int d0 = tid % L * 8;
 #pragma unroll 1
                 for (int row = tid / L; row < seg.nrows; row += kGT / L) {
                     float m = kNegInf, l = 0.0f, acc[8] = {};
-                    att_add<D, true, 8, 8>(ln, int64_t(seg.unit) + first, n_seg, row, d0, m, l, acc);
+                    const size_t at = (size_t(seg.unit) + first) * RT + row;
+                    att_add<D, true, 8, 8>(ln.part_ml + at, ln.part_o + at * D + d0, RT, n_seg, m, l, acc);
                     const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
                     uint2 *dst = reinterpret_cast<uint2 *>(att_out<D>(a, seg.head, seg.row0 + row) + d0);
 #pragma unroll
@@ -744,14 +748,18 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     const int s = in_req / lq.rt;
     att_segments(lq, a.heads * lq.su * qa, head * lq.su * qa + lq.su * q0 + s * (q1 - q0), q1 - q0, c, n);
     const int u = (head * a.R + r) * lq.su + s;
-    if (a.line[kLineRequests].grid)
-        att_add<D, false, kJC, 4>(lq, int64_t(u + c) * lq.halves, n * lq.halves, in_req - s * lq.rt, d0, m, l, acc);
-    else
-        att_add<D, true, kJC, 2>(lq, int64_t(u + c), n, in_req - s * lq.rt, d0, m, l, acc);
+    if (a.line[kLineRequests].grid) {
+        const size_t at = size_t(u + c) * lq.halves * lq.rt, r0 = in_req - s * lq.rt;
+        att_add<D, false, kJC, 4>(lq.part_ml + at + r0, lq.part_o + at * D + d0 * lq.rt + r0, lq.rt, n * lq.halves, m, l, acc);
+    } else {
+        const size_t at = size_t(u + c) * lq.rt + in_req;
+        att_add<D, true, kJC, 2>(lq.part_ml + at, lq.part_o + at * D + d0, lq.rt, n, m, l, acc);
+    }
     if (np > 0) {
         const int b = rho / lp.rt, up = head * lp.pu + b;
         att_segments(lp, a.heads * lp.pu * np, up * np, np, c, n);
-        att_add<D, false, kJC, 4>(lp, int64_t(up + c) * lp.halves, n * lp.halves, rho - b * lp.rt, d0, m, l, acc);
+        const size_t at = size_t(up + c) * lp.halves * lp.rt, r0 = rho - b * lp.rt;
+        att_add<D, false, kJC, 4>(lp.part_ml + at + r0, lp.part_o + at * D + d0 * lp.rt + r0, lp.rt, n * lp.halves, m, l, acc);
     }
     const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);  // no key: zeros
     *reinterpret_cast<uint2 *>(att_out<D>(a, head, rho) + d0) =
