@@ -53,7 +53,7 @@ constexpr int64_t kLim31 = int64_t(1) << 31;
 constexpr size_t kWsCounters = 4096;
 
 struct AttendPlan {
-    int32_t rows;
+    int32_t rows, sms;
     struct Line {
         int32_t pu, su, rt, halves, grid;
         size_t off_ml, off_o;
@@ -107,8 +107,9 @@ int plan_attend(const w12_kv *kv, int64_t R, int64_t T, int q_heads, int64_t max
     p->off_arrived = off;
     off += kWsCounters;  // (the same for all sizes: one workspace serves them all)
     if (uint64_t(2 * sms) * 4u > kWsCounters) return W12_ERR_CUDA;
+    p->sms = sms;
     p->off_plan = off;
-    off += round256(uint64_t(R + 2) * 4u);
+    off += round256(uint64_t(R + 4) * 4u);
     p->join = l[kLinePrefix].pu + l[kLineRequests].su > 0;
     for (int i = 0; i < kLines; ++i) {
         auto &n = l[i];
@@ -231,6 +232,7 @@ extern "C" int w12_attend(const w12_kv *kv, const uint16_t *q, int64_t q_stride,
     a.arrived = reinterpret_cast<uint32_t *>(w + p.off_arrived);
     a.plan = reinterpret_cast<int32_t *>(w + p.off_plan);
     a.join = p.join;
+    a.sms = p.sms;
     a.per_g = ~uint64_t(0) / uint64_t(a.G) + 1;
     for (int i = 0; i < kLines; ++i) {
         const auto &n = p.line[i];

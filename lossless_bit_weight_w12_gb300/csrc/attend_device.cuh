@@ -13,7 +13,7 @@
 // (so the part of the prefix past 128 W keys is read by each request through
 // its own table).  The prefix and requests with many rows go to the
 // tensor-memory kernel, requests with few rows to the register kernel in
-// tiles of 64 keys.
+// tiles of 64 keys.  The two run side by side, each on its share of the SMs.
 // Within a line, units of a head are ordered by p, or by r and s; heads in
 // order.  All tiles of all units form one row, cut into equal pieces, one per
 // worker (a CTA; in the register kernel each half of a CTA): every worker
@@ -56,7 +56,7 @@ struct AttSeg {
 struct AttShared {
     int lens[kAttMaxR];
     int cum[kAttMaxR + 1];  // tiles of the requests before r, one row block each
-    int w;
+    int w, grid;
     AttSeg first[2];        // the CTA's workers' first positions
 };
 
@@ -70,11 +70,10 @@ __device__ __forceinline__ int att_len(const AttendArgs &a, int n) {
 __device__ __forceinline__ int att_prefix_whole(const AttendArgs &a, int shortest) {
     return a.line[kLinePrefix].grid ? min(a.prefix, max(shortest - a.T + 1, 0)) / kAttTcTile : 0;
 }
-// This line's tiles of a request of len keys (at least one, so that every
-// request has a result).
+// The requests' tiles of one of len keys (at least one, so that every request
+// has a result).
 __device__ __forceinline__ int att_req_tiles(const AttendArgs &a, int w, int len) {
-    if (a.self == kLinePrefix) return 0;
-    const int kt = a.self == kLineRequests ? kAttTcTile : kAttTile;
+    const int kt = a.line[kLineRequests].grid ? kAttTcTile : kAttTile;
     return max((len + kt - 1) / kt - w * (kAttTcTile / kt), 1);
 }
 
@@ -91,10 +90,33 @@ __device__ __forceinline__ int att_owner(int total, int grid, int t) {
 
 struct AttPlan {
     int w;         // the prefix's shared tiles
+    int grid;      // workers of this line
     int np;        // tiles of a prefix unit of this line
     int per_head;  // tiles of a head
     int t0, t1;    // this worker's tiles
 };
+
+// SMs that take the prefix while the others take the requests (of both more
+// than the GPU has).  The prefix's kernel is bound by its chain of products
+// and exponentials, the requests' by the cache stream, so side by side they
+// take less than one after the other (128 requests, 16000 + 460 keys: 51 + 54
+// us apart).  An SM's time, measured, in units of 100 cycles: a prefix tile of
+// 256 rows 33 (128 rows: 18) and 250 a CTA; of the requests a tile of 64 keys
+// 5 in the register kernel, of 128 keys 18 or 33 in the other, a unit 30.
+__device__ __forceinline__ int att_prefix_sms(const AttendArgs &a, int w, int sum) {
+    const AttendLine &lp = a.line[kLinePrefix];
+    const bool tc = a.line[kLineRequests].grid != 0;
+    const AttendLine &lq = a.line[tc ? kLineRequests : kLineRest];
+    const int sms_q = tc ? lq.grid : lq.grid / 2;
+    if (lp.grid + sms_q <= a.sms) return lp.grid;
+    const float tp = float(a.heads) * float(lp.pu) * float(w) * (lp.rt == 256 ? 33.0f : 18.0f);
+    const float tq = float(a.heads) * (float(lq.su) * float(sum) * (tc ? lq.rt == 256 ? 33.0f : 18.0f : 5.0f) +
+                                       float(a.R) * float(lq.su) * 30.0f);
+    // tp / x + 250 = tq / (sms - x), by a few steps from the ratio
+    float x = float(a.sms) * tp / (tp + tq);
+    for (int k = 0; k < 4; ++k) x = float(a.sms) * (tp + 250.0f * x) / (tp + 250.0f * x + tq);
+    return max(a.sms - sms_q, max(1, min(min(lp.grid, a.sms - 1), int(x + 0.5f))));
+}
 
 // Fills in what follows from (head, req, block) for the unit's tile k.
 __device__ __forceinline__ void att_unit_at(const AttendArgs &a, const AttPlan &p, const AttShared &sh, AttSeg &s, int k) {
@@ -180,6 +202,7 @@ __device__ __forceinline__ AttPlan att_plan(const AttendArgs &a, AttShared &sh, 
         const int per = (a.R + 31) / 32, r0 = lane * per, r1 = min(r0 + per, a.R);
         int sum = 0;
         for (int r = r0; r < r1; ++r) sum += att_req_tiles(a, w, sh.lens[r]);
+        // (the prefix's launch needs it, too, for its share of the SMs)
         int x = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -189,30 +212,40 @@ __device__ __forceinline__ AttPlan att_plan(const AttendArgs &a, AttShared &sh, 
         if (lane == 31) sh.cum[a.R] = x;
         x -= sum;
         const bool tell = a.join && a.self != kLinePrefix && blockIdx.x == 0;  // the join kernel
-        if (lane == 31 && tell) a.plan[1 + a.R] = x + sum;
+        if (lane == 31 && tell) a.plan[3 + a.R] = x + sum;
         for (int r = r0; r < r1; ++r) {
             sh.cum[r] = x;
-            if (tell) a.plan[1 + r] = x;
+            if (tell) a.plan[3 + r] = x;
             x += att_req_tiles(a, w, sh.lens[r]);
         }
+        const int all = __shfl_sync(0xFFFFFFFFu, sh.cum[a.R], 31);
         if (lane == 0) {
+            int g = ln.grid;
+            if (w > 0) {
+                const int gp = att_prefix_sms(a, w, all);
+                const int gq = a.line[kLineRequests].grid ? min(ln.grid, a.sms - gp) : min(ln.grid, 2 * (a.sms - gp));
+                g = a.self == kLinePrefix ? gp : gq;
+                if (tell) a.plan[1] = gp;
+            }
             sh.w = w;
-            if (tell) a.plan[0] = w;
+            sh.grid = g;
+            if (tell) a.plan[0] = w, a.plan[2] = g;
         }
     }
     __syncthreads();
     AttPlan p;
     p.w = sh.w;
+    p.grid = sh.grid;
     p.np = a.self == kLinePrefix ? p.w : 0;
-    p.per_head = ln.pu * p.np + ln.su * sh.cum[a.R];
+    p.per_head = a.self == kLinePrefix ? ln.pu * p.np : ln.su * sh.cum[a.R];
     const int total = p.per_head * a.heads;
     // the CTA's `workers` workers; this thread's is number `worker` of them
     const int c0 = int(blockIdx.x) * workers;
-    p.t0 = att_begin(total, ln.grid, c0 + worker);
-    p.t1 = att_begin(total, ln.grid, c0 + worker + 1);
+    p.t0 = att_begin(total, p.grid, min(c0 + worker, p.grid));
+    p.t1 = att_begin(total, p.grid, min(c0 + worker + 1, p.grid));
     const int q = int(threadIdx.x >> 5);  // a warp finds a worker's first tile
     if (q < workers) {
-        const int t = att_begin(total, ln.grid, c0 + q);
+        const int t = att_begin(total, p.grid, min(c0 + q, p.grid));
         if (t < total && a.self == kLinePrefix) {
             if (lane == 0) sh.first[q] = att_locate(a, p, sh, t);
         } else if (t < total) {
@@ -393,15 +426,31 @@ __device__ __forceinline__ void att_store_lse(const AttendArgs &a, int head, int
 
 // Where a unit of n tiles from b on of a line of `total` lies: its first
 // worker, its segments.
-__device__ __forceinline__ void att_segments(const AttendLine &ln, int total, int b, int n, int &first, int &segments) {
-    first = att_owner(total, ln.grid, b);
-    segments = att_owner(total, ln.grid, b + n - 1) - first + 1;
+__device__ __forceinline__ void att_segments(int grid, int total, int b, int n, int &first, int &segments) {
+    first = att_owner(total, grid, b);
+    segments = att_owner(total, grid, b + n - 1) - first + 1;
 }
 __device__ __forceinline__ void att_unit_segments(const AttendArgs &a, const AttPlan &p, const AttShared &sh,
                                                   const AttSeg &s, int &first, int &segments) {
     const AttendLine &ln = a.line[a.self];
     const int n = sh.cum[s.req + 1] - sh.cum[s.req];
-    att_segments(ln, p.per_head * a.heads, s.head * p.per_head + ln.su * sh.cum[s.req] + s.block * n, n, first, segments);
+    att_segments(p.grid, p.per_head * a.heads, s.head * p.per_head + ln.su * sh.cum[s.req] + s.block * n, n, first, segments);
+}
+
+// The kernels of a call with a prefix run side by side: the prefix's waits for
+// what the stream did before and then lets the requests' start, which does not
+// wait -- all that it reads was there when every CTA of the prefix's kernel had
+// passed its wait -- but ends only after the prefix's kernel has ended, so that
+// the join, which waits for the requests' kernel, has both's results.
+__device__ __forceinline__ bool att_side_by_side(const AttendArgs &a) {
+    return a.line[kLinePrefix].grid && a.self != kLinePrefix;
+}
+__device__ __forceinline__ void att_start(const AttendArgs &a) {
+    if (!att_side_by_side(a)) pdl_wait_previous();
+    pdl_launch_dependents();
+}
+__device__ __forceinline__ void att_end(const AttendArgs &a) {
+    if (att_side_by_side(a)) pdl_wait_previous();
 }
 
 // True in the worker that is the last of a unit's `segments` to get here (one

@@ -229,8 +229,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_kernel(const __grid_
         ctl.limit_ns = kWaitLimitNs;
         mbar_fence_init();
     }
-    pdl_launch_dependents();
-    pdl_wait_previous();
+    att_start(a);
     const AttPlan plan = att_plan(a, sh, 2, me);
     const AttendLine &ln = a.line[kLineRest];
     const int t0 = plan.t0, t1 = plan.t1;
@@ -285,7 +284,10 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_kernel(const __grid_
     const int kw = 16 * wg;                           // this warp's keys of a tile
     const int g8 = lane >> 2, q4 = lane & 3;
     const int r0 = lane & 7, mat = lane >> 3;         // ldmatrix: this lane's row and matrix
-    if (t0 >= t1) return;
+    if (t0 >= t1) {
+        att_end(a);
+        return;
+    }
     AttSeg seg = sh.first[me];
     // a thread's share of a segment's query rows: 16-byte pieces tid, tid + kGT ..
     constexpr int kQP = RT * D / 8 / kGT ? RT * D / 8 / kGT : 1;
@@ -723,6 +725,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_kernel(const __grid_
         t += n_tiles;
         seg = next;
     }
+    att_end(a);
 }
 
 // The join of the lines' results.  A warp has 32 query rows of a head (a lane
@@ -741,12 +744,12 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     if (head >= a.heads || rho >= a.rows) return;
     const int r = rho / (a.T * a.G), in_req = rho - r * a.T * a.G;
     const AttendLine &lp = a.line[kLinePrefix], &lq = a.line[a.line[kLineRequests].grid ? kLineRequests : kLineRest];
-    const int32_t *cum = a.plan + 1;
-    const int np = a.plan[0], q0 = cum[r], q1 = cum[r + 1], qa = cum[a.R];
+    const int32_t *cum = a.plan + 3;
+    const int np = a.plan[0], gp = a.plan[1], gq = a.plan[2], q0 = cum[r], q1 = cum[r + 1], qa = cum[a.R];
     float m = kNegInf, l = 0.0f, acc[kJC] = {};
     int c, n;
     const int s = in_req / lq.rt;
-    att_segments(lq, a.heads * lq.su * qa, head * lq.su * qa + lq.su * q0 + s * (q1 - q0), q1 - q0, c, n);
+    att_segments(gq, a.heads * lq.su * qa, head * lq.su * qa + lq.su * q0 + s * (q1 - q0), q1 - q0, c, n);
     const int u = (head * a.R + r) * lq.su + s;
     if (a.line[kLineRequests].grid) {
         const size_t at = size_t(u + c) * lq.halves * lq.rt, r0 = in_req - s * lq.rt;
@@ -757,7 +760,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     }
     if (np > 0) {
         const int b = rho / lp.rt, up = head * lp.pu + b;
-        att_segments(lp, a.heads * lp.pu * np, up * np, np, c, n);
+        att_segments(gp, a.heads * lp.pu * np, up * np, np, c, n);
         const size_t at = size_t(up + c) * lp.halves * lp.rt, r0 = rho - b * lp.rt;
         att_add<D, false, kJC, 4>(lp.part_ml + at + r0, lp.part_o + at * D + d0 * lp.rt + r0, lp.rt, n * lp.halves, m, l, acc);
     }

@@ -302,8 +302,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    pdl_launch_dependents();
-    pdl_wait_previous();
+    att_start(a);
     const AttPlan plan = att_plan(a, sh, 1, 0);
     tmem_fence_before();
     __syncthreads();
@@ -810,6 +809,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
     }
     tmem_fence_before();
     __syncthreads();
+    att_end(a);
     if (warp == kIssueWarp) {
         tmem_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");

@@ -76,7 +76,7 @@ struct AttendLine {
     int32_t pu, su;   // units per head: row blocks of all requests under the prefix, row blocks per request
     int32_t rt;       // query rows per unit
     int32_t halves;   // results per segment (2: its tiles in two alternating halves)
-    int32_t grid;     // workers that cut it (CTAs, or halves of CTAs); 0: the line is not used
+    int32_t grid;     // its workers (CTAs, or halves of CTAs) at most; 0: the line is not used
     float *part_o;    // [slots][halves][head_dim][rt]; the register kernel's: [slots][rt][head_dim]
     float2 *part_ml;  // [slots][halves][rt]: reference exponent (log2 units) and sum
 };
@@ -98,11 +98,12 @@ struct AttendArgs {
     int32_t rows;      // R * T * G query rows per key head
     int32_t prefix, max_len;
     int32_t self;      // the line of this launch
+    int32_t sms;
     float scale_log2;  // scale * log2(e)
     int *err;
     uint64_t per_g;     // 2^64 / G, rounded up (G = 1: not used)
     uint32_t *arrived;  // [workers] segments of a unit that are done; zero between calls
-    int32_t *plan;      // for the join: W, then the R + 1 cumulative tiles of the requests
+    int32_t *plan;      // for the join: W, both lines' workers, the R + 1 cumulative tiles of the requests
     int32_t join;       // 1: a join kernel adds up the results
     AttendLine line[kLines];
 };
