@@ -102,7 +102,7 @@ struct AttPlan {
 // take less than one after the other (128 requests, 16000 + 460 keys: 51 + 54
 // us apart).  An SM's time, measured, in units of 100 cycles: a prefix tile of
 // 256 rows 33 (128 rows: 18) and 250 a CTA; of the requests a tile of 64 keys
-// 5 in the register kernel, of 128 keys 18 or 33 in the other, a unit 30.
+// 7 in the register kernel, of 128 keys 18 or 33 in the other, a unit 40.
 __device__ __forceinline__ int att_prefix_sms(const AttendArgs &a, int w, int sum) {
     const AttendLine &lp = a.line[kLinePrefix];
     const bool tc = a.line[kLineRequests].grid != 0;
@@ -110,8 +110,8 @@ __device__ __forceinline__ int att_prefix_sms(const AttendArgs &a, int w, int su
     const int sms_q = tc ? lq.grid : lq.grid / 2;
     if (lp.grid + sms_q <= a.sms) return lp.grid;
     const float tp = float(a.heads) * float(lp.pu) * float(w) * (lp.rt == 256 ? 33.0f : 18.0f);
-    const float tq = float(a.heads) * (float(lq.su) * float(sum) * (tc ? lq.rt == 256 ? 33.0f : 18.0f : 5.0f) +
-                                       float(a.R) * float(lq.su) * 30.0f);
+    const float tq = float(a.heads) * (float(lq.su) * float(sum) * (tc ? lq.rt == 256 ? 33.0f : 18.0f : 7.0f) +
+                                       float(a.R) * float(lq.su) * 40.0f);
     // tp / x + 250 = tq / (sms - x), by a few steps from the ratio
     float x = float(a.sms) * tp / (tp + tq);
     for (int k = 0; k < 4; ++k) x = float(a.sms) * (tp + 250.0f * x) / (tp + 250.0f * x + tq);
