@@ -36,6 +36,7 @@
 
 #include <atomic>
 
+#include "async_common.cuh"
 #include "device_common.cuh"
 #include "step_device.cuh"
 #include "step_internal.h"
@@ -426,7 +427,7 @@ __device__ __forceinline__ u64 nucleus(uint64_t p, u64 total) {
 // threads): the first k by rank, of those the nucleus p (2^24: all), of those
 // the weights from floor_w on.
 __device__ __forceinline__ void draw_from_list(SampleSmall &sh, SampleCut &cut, uint32_t n, uint32_t k, uint64_t p,
-                                               u64 floor_w, uint64_t u, int32_t *token, float *prob, bool *writer) {
+                                               uint32_t floor_w, uint64_t u, int32_t *token, float *prob, bool *writer) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // lanes per token (the whole CTA has work at any n), tokens at a time
     int lanes = 1;
@@ -751,10 +752,10 @@ __global__ void __launch_bounds__(kST, 2) sample_kernel(const __grid_constant__ 
     int32_t token = -1;
     float prob = 0.0f;
     bool writer = me == 0 && tid == 0;
-    u64 floor_w = 1;
+    uint32_t floor_w = 1;  // (above 2^31: no token stays)
     if (a.min_p) {
         const float m = a.min_p[req];
-        if (m > 0.0f) floor_w = umax64(1ull, u64(ceilf(fminf(m, 2.0f) * kOne31)));
+        if (m > 0.0f) floor_w = max(1u, min(0x80000001u, __float2uint_ru(fminf(m, 1.5f) * kOne31)));
     }
     uint64_t p_fix = 1ull << 24;
     if (CUT && a.top_p) {
@@ -861,17 +862,42 @@ __global__ void __launch_bounds__(kST, 2) sample_kernel(const __grid_constant__ 
             uint32_t *keep = cuts && a.keep_w ? reinterpret_cast<uint32_t *>(buf + weights_at<DT>(a.chunk)) : nullptr;
             const bool wide = cuts && !(top_k > 0 && top_k < a.V);  // top_p over the whole row
             if (CUT && wide && tid == 0) sh.list_n = 0u, sh.mass = 0;
-#pragma unroll 2
-            for (int i = row.i0; i < row.i1; i += 4) {
-                uint32_t w[4];
-                row.weight4(i, w);
-                if (keep) reinterpret_cast<uint4 *>(keep)[i >> 2] = make_uint4(w[0], w[1], w[2], w[3]);
+            const auto take = [&](int i, const uint32_t (&w)[4]) {
+                if (CUT && keep) reinterpret_cast<uint4 *>(keep)[i >> 2] = make_uint4(w[0], w[1], w[2], w[3]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) mine = add_wide(mine, cuts || w[j] >= floor_w ? w[j] : 0u);
+                for (int j = 0; j < 4; ++j) mine = add_wide(mine, (CUT && cuts) || w[j] >= floor_w ? w[j] : 0u);
                 if (CUT && wide && i < row.i0 + kTaken)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         if (w[j]) atomicAdd(&cut.lo[weight_bin(w[j])], 1u);
+            };
+            int i = row.i0;
+            if (a.resident && !row.inf) {  // whole fours in shared memory, without the general case's questions
+                const uint32_t from = smem_addr(buf);
+                const int full = row.i0 + (row.i1 - row.i0) / 4 * 4;
+#pragma unroll 2
+                for (; i < full; i += 4) {
+                    float v[4];
+                    if (DT == W12_F32) {
+                        const uint4 f = lds128(from + uint32_t(i) * 4u);
+                        v[0] = __uint_as_float(f.x), v[1] = __uint_as_float(f.y);
+                        v[2] = __uint_as_float(f.z), v[3] = __uint_as_float(f.w);
+                    } else {
+                        const uint32_t x = lds32(from + uint32_t(i) * 2u), y = lds32(from + uint32_t(i) * 2u + 4u);
+                        v[0] = bf16_bits_to_float(x & 0xFFFFu), v[1] = bf16_bits_to_float(x >> 16);
+                        v[2] = bf16_bits_to_float(y & 0xFFFFu), v[3] = bf16_bits_to_float(y >> 16);
+                    }
+                    uint32_t w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[j] = row.weight(fmaxf(v[j], -INFINITY));
+                    take(i, w);
+                }
+            }
+#pragma unroll 1
+            for (; i < row.i1; i += 4) {
+                uint32_t w[4];
+                row.weight4(i, w);
+                take(i, w);
             }
             if (keep) {
                 row.w = keep;
