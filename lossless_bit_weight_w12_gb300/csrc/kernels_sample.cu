@@ -101,6 +101,21 @@ __host__ __device__ constexpr size_t weights_at(int64_t chunk) {
     return DT == W12_F32 ? 0 : size_t(chunk) * 2;
 }
 
+// A cluster barrier at which only warp 0 has written for other CTAs (the
+// others need not wait until their own writes have gone out).
+__device__ __forceinline__ void sync_sums() {
+    if (threadIdx.x < 32)
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    else
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// One at which nothing was written for others.
+__device__ __forceinline__ void sync_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 __device__ __forceinline__ u64 umax64(u64 a, u64 b) { return a > b ? a : b; }
 
 // acc + w, in one instruction
@@ -741,7 +756,7 @@ __global__ void __launch_bounds__(kST, 2) sample_kernel(const __grid_constant__ 
             for (int w = 0; w < kSW; ++w) m = fmaxf(m, sh.warp_top[w]);
             cl.map_shared_rank(&sh, tid)->top[me] = m;
         }
-        cl.sync();
+        sync_sums();
         m = -INFINITY;
         for (int c = 0; c < cs; ++c) m = fmaxf(m, sh.top[c]);
         row.inf = m == INFINITY;
@@ -851,7 +866,7 @@ __global__ void __launch_bounds__(kST, 2) sample_kernel(const __grid_constant__ 
                 }
                 before = incl - mine;
                 for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
-                cl.sync();
+                sync_sums();
                 total = 0;
                 for (int c = 0; c < cs; ++c) {
                     if (c < me) before += sh.slice[slot][c];
@@ -1010,7 +1025,7 @@ __global__ void __launch_bounds__(kST, 2) sample_kernel(const __grid_constant__ 
         a.tokens[r] = token;
         if (a.prob) a.prob[r] = prob;
     }
-    cl.sync();  // no CTA leaves while another may read its shared memory
+    sync_relaxed();  // no CTA leaves while another may read its shared memory
     if (!a.accept_len || me != 0) return;
     // ---- the last row's cluster applies the acceptance rule
     if (tid == 0) {
