@@ -64,9 +64,13 @@ struct AttendPlan {
 
 // Rows per key head and request from which the tensor-memory kernel takes
 // the requests: its tile has 128 rows whatever their number, the register
-// kernel streams the keys once per 32 rows.  (The prefix of two or more
-// requests always goes there: it is what reads it once.)
-constexpr int64_t kTcRows = 33;
+// kernel's work grows with them.  8 requests of 700 .. 9000 keys, 8 key heads
+// (us, bf16 / e4m3), register kernel against the other: 12 rows 41 / 36
+// against 47 / 62, 18 rows 56 / 67 against 46 / 60, 30 rows 60 / 73 against
+// 45 / 56; of 200 .. 900 keys: 12 rows 17 / 17 against 20 / 27, 18 rows 22 /
+// 33 against 20 / 26.  (The prefix of two or more requests always goes there:
+// it is what reads it once.)
+constexpr int64_t kTcRows = 17;
 
 // Work split and workspace layout of an attention call.
 int plan_attend(const w12_kv *kv, int64_t R, int64_t T, int q_heads, int64_t max_len, int64_t prefix, AttendPlan *p) {
@@ -92,7 +96,7 @@ int plan_attend(const w12_kv *kv, int64_t R, int64_t T, int q_heads, int64_t max
         l[kLineRequests].rt = tg <= 128 ? 128 : 256;
         l[kLineRequests].su = blocks(tg, l[kLineRequests].rt);
     } else {
-        l[kLineRest].rt = tg <= 8 ? 8 : tg <= 16 ? 16 : 32;
+        l[kLineRest].rt = tg <= 8 ? 8 : 16;
         l[kLineRest].su = 1;
     }
     const int64_t own = max_len / kAttTile + 1;  // at most these many tiles of a request

@@ -68,7 +68,7 @@ struct ACfg {
     static constexpr int kStage = 2 * kTileBytes + (Q8 ? 1024 : 0);
     // per worker, after the rings: queries, the join's step, row statistics
     static constexpr int kQ = RT * D * 2;
-    static constexpr int kJoinCols = NR == 4 ? 32 : 64;             // channels per step of the workers' join
+    static constexpr int kJoinCols = 64;                            // channels per step of the workers' join
     static constexpr int kJoinPitch = kJoinCols + 4;
     static constexpr int kJoin = kGW * 8 * kJoinPitch * 4;
     static constexpr int kStat = kGW * RT * 8 + RT * 8 + RT * 4;    // per warp and row (m, l); (m, 1 / l); query scale
@@ -197,7 +197,6 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_kernel(const __grid_
     using C = ACfg<D, Q8, NR>;
     constexpr int S = C::S, RT = C::RT, KS = D / 16, MB = D / 16;  // product steps over channels, output blocks
     constexpr int PPR = D / (Q8 ? 16 : 8);                        // 16-byte pieces of a cache row
-    constexpr bool kQRegs = NR <= 2;                              // query fragments stay in registers
     extern __shared__ __align__(1024) unsigned char smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // this warp's worker: consumers 0-3 and 4-7; producers in the same order
@@ -365,18 +364,16 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_kernel(const __grid_
                 min_pos = min(min_pos, pos[n][c]);
             }
         min_pos = __reduce_min_sync(0xFFFFFFFFu, min_pos);
-        uint32_t qf[kQRegs ? NR : 1][KS][2];
-        if (kQRegs) {
+        uint32_t qf[NR][KS][2];
 #pragma unroll
-            for (int n = 0; n < NR; ++n)
+        for (int n = 0; n < NR; ++n)
 #pragma unroll
-                for (int ks = 0; ks < KS; ks += 2) {
-                    uint32_t x[4];
-                    ldsm4(x, query_at<D>(qs, 8 * n + r0, 2 * ks + mat));
-                    qf[kQRegs ? n : 0][ks][0] = x[0], qf[kQRegs ? n : 0][ks][1] = x[1];
-                    qf[kQRegs ? n : 0][ks + 1][0] = x[2], qf[kQRegs ? n : 0][ks + 1][1] = x[3];
-                }
-        }
+            for (int ks = 0; ks < KS; ks += 2) {
+                uint32_t x[4];
+                ldsm4(x, query_at<D>(qs, 8 * n + r0, 2 * ks + mat));
+                qf[n][ks][0] = x[0], qf[n][ks][1] = x[1];
+                qf[n][ks + 1][0] = x[2], qf[n][ks + 1][1] = x[3];
+            }
 
         float o[MB][NR][4];
         float m_run[NR][2], l_run[NR][2];
@@ -425,28 +422,16 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_kernel(const __grid_
                 } else {
                     ldsm4(kf, tile_at<D, Q8>(kb, kw + 8 * (mat & 1) + r0, 2 * ks + (mat >> 1)));
                 }
-                if (kQRegs) {
 #pragma unroll
-                    for (int n = 0; n < NR; ++n)
-                        mma16816<Q8>(NR == 1 && (ks & 1) ? sc2[0] : sc[n], kf, qf[kQRegs ? n : 0][ks][0],
-                                     qf[kQRegs ? n : 0][ks][1]);
-                } else {
-#pragma unroll
-                    for (int n = 0; n < NR; n += 2) {
-                        uint32_t x[4];
-                        ldsm4(x, query_at<D>(qs, 8 * n + 8 * (mat >> 1) + r0, 2 * ks + (mat & 1)));
-                        mma16816<Q8>(sc[n], kf, x[0], x[1]);
-                        mma16816<Q8>(sc[n + 1], kf, x[2], x[3]);
-                    }
-                }
+                for (int n = 0; n < NR; ++n)
+                    mma16816<Q8>(NR == 1 && (ks & 1) ? sc2[0] : sc[n], kf, qf[n][ks][0], qf[n][ks][1]);
             }
             if (NR == 1)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) sc[0][x] += sc2[0][x];
             // ---- values: on their way during the softmax, but for a tile
-            // whose value rows are changed below and for many rows (registers)
+            // whose value rows are changed below
             constexpr int W = Q8 ? (D == 128 ? 4 : 2) : 1;  // e4m3: words of a lane's piece of a value row
-            constexpr bool kEarlyV = NR <= 2;
             uint32_t vx[4][W], vf[Q8 ? 1 : MB][4];
             const auto load_v = [&] {
                 if (Q8) {
@@ -468,7 +453,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_kernel(const __grid_
                         ldsm4t(vf[Q8 ? 0 : b], tile_at<D, Q8>(vb, kw + r0 + 8 * (mat >> 1), 2 * b + (mat & 1)));
                 }
             };
-            if (kEarlyV && whole) load_v();
+            if (whole) load_v();
             float kscale[2] = {1.0f, 1.0f}, vscale[2] = {1.0f, 1.0f};
             float lift = 0.0f;  // e4m3: e - 7 for value scales below 2^e
             if (Q8) {
@@ -596,7 +581,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_kernel(const __grid_
                 if (touched) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the next box lands here
                 __syncwarp();
             }
-            if (!kEarlyV || !whole) load_v();
+            if (!whole) load_v();
             // ---- weights times values
             if (Q8) {
 #pragma unroll
@@ -832,7 +817,7 @@ int attend_make_maps(AttendArgs &a, const w12_kv *kv) {
 template <int D, bool Q8>
 int run_rows(const AttendArgs &a, void *stream) {
     const int rt = a.line[kLineRest].rt;
-    return rt == 8 ? run<D, Q8, 1>(a, stream) : rt == 16 ? run<D, Q8, 2>(a, stream) : run<D, Q8, 4>(a, stream);
+    return rt == 8 ? run<D, Q8, 1>(a, stream) : run<D, Q8, 2>(a, stream);
 }
 
 int launch_attend_rest(const AttendArgs &a, int dim, int kv, void *stream) {

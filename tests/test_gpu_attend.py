@@ -224,7 +224,7 @@ def test_later_tokens_do_not_leak(dev, w12mod, e4m3):
 
 
 @pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
-@pytest.mark.parametrize("T,hq,n", [(4, 6, 90), (4, 6, 1000), (40, 6, 300), (40, 6, 128), (130, 1, 131)])
+@pytest.mark.parametrize("T,hq,n", [(2, 6, 90), (2, 6, 1000), (4, 6, 90), (4, 6, 1000), (40, 6, 300), (40, 6, 128), (130, 1, 131)])
 def test_odd_values_of_any_block(dev, w12mod, T, hq, n, e4m3):
     """As above for few rows, several tiles, more than 128 rows; values that are
     not finite in several channels, in the first new token and in the last."""
