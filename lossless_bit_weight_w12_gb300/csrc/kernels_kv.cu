@@ -52,25 +52,61 @@ struct AppendLane {
     uint32_t group;  // lanes of the row
 };
 
-// One row: KIND 0 a query, 1 a key, 2 a value head.
-template <int DIM, int XT, int KV, bool IL, int KIND>
-__device__ __forceinline__ void append_row(const AppendArgs &a, const AppendLane &ln, const void *src, int64_t at,
-                                           uint16_t *q_out, int64_t slot) {
+// Eight channels of a row as they lie in memory.
+template <int XT>
+struct Raw {
+    uint2 v[XT == W12_F32 ? 4 : 2];
+};
+template <int XT>
+__device__ __forceinline__ Raw<XT> load_raw(const unsigned char *p) {
+    Raw<XT> r;
+    if (XT == W12_F32) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint4 x = reinterpret_cast<const uint4 *>(p)[h];
+            r.v[2 * h] = make_uint2(x.x, x.y), r.v[2 * h + 1] = make_uint2(x.z, x.w);
+        }
+    } else {  // (only 8-byte alignment is asked for)
+        r.v[0] = reinterpret_cast<const uint2 *>(p)[0], r.v[1] = reinterpret_cast<const uint2 *>(p)[1];
+    }
+    return r;
+}
+template <int XT>
+__device__ __forceinline__ void unpack(const Raw<XT> &r, float (&x)[8]) {
+#pragma unroll
+    for (int j = 0; j < (XT == W12_F32 ? 4 : 2); ++j) {
+        if (XT == W12_F32) {
+            x[2 * j] = __uint_as_float(r.v[j].x), x[2 * j + 1] = __uint_as_float(r.v[j].y);
+        } else {
+            x[4 * j] = bf16_bits_to_float(r.v[j].x & 0xFFFFu), x[4 * j + 1] = bf16_bits_to_float(r.v[j].x >> 16);
+            x[4 * j + 2] = bf16_bits_to_float(r.v[j].y & 0xFFFFu), x[4 * j + 3] = bf16_bits_to_float(r.v[j].y >> 16);
+        }
+    }
+}
+
+// One row of head hd (query heads, key heads, value heads in order), src:
+// where its channel e is.
+template <int DIM, int XT, int KV, bool IL>
+__device__ __forceinline__ void append_row(const AppendArgs &a, const AppendLane &ln, const Raw<XT> &raw,
+                                           const unsigned char *src, int hd, uint16_t *q_out) {
+    constexpr int ES = XT == W12_F32 ? 4 : 2;
+    const bool query = hd < a.q_heads, value = hd >= a.q_heads + a.heads;
     float x[8], y[8], o[8];
-    load4<XT>(src, at, x);
-    load4<XT>(src, at + 4, x + 4);
-    if (KIND != 2 && !IL)
+    unpack<XT>(raw, x);
+    if (!IL)
 #pragma unroll
         for (int b = 0; b < 2; ++b)
-            if (ln.turned[b]) load4<XT>(src, at + 4 * b + ln.mate[b], o + 4 * b);
+            if (ln.turned[b] && !value) load4<XT>(src + 4 * b * ES, ln.mate[b], o + 4 * b);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         y[j] = x[j];
-        if (KIND != 2 && ln.turned[j / 4])
+        if (ln.turned[j / 4] && !value)
             y[j] = __fadd_rn(__fmul_rn(x[j], ln.cs[j]), __fmul_rn(IL ? x[j ^ 1] : o[j], ln.sn[j]));
     }
-    if (KIND == 0 || KV == W12_KV_BF16) {
-        uint16_t *to = KIND == 0 ? q_out : static_cast<uint16_t *>(KIND == 1 ? a.kc : a.vc) + slot * DIM;
+    const int kh = value ? hd - a.q_heads - a.heads : hd - a.q_heads;
+    const int64_t slot = ln.slot0 + (int64_t(kh) << a.page_log2);
+    if (KV == W12_KV_BF16 || query) {
+        uint16_t *to = query ? q_out + int64_t(hd) * DIM : static_cast<uint16_t *>(value ? a.vc : a.kc) + slot * DIM;
         *reinterpret_cast<uint4 *>(to + ln.e) =
             make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
         return;
@@ -89,21 +125,21 @@ __device__ __forceinline__ void append_row(const AppendArgs &a, const AppendLane
         w[j] = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(y[2 * j], inv), __fmul_rn(y[2 * j + 1], inv)), __NV_SATFINITE,
                                         __NV_E4M3);
     if (!some) w[0] = w[1] = w[2] = w[3] = 0u;  // (0 times an infinity)
-    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(KIND == 1 ? a.kc : a.vc) + slot * DIM + ln.e) =
+    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(value ? a.vc : a.kc) + slot * DIM + ln.e) =
         make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
     if (ln.e == 0)
-        (KIND == 1 ? a.ks : a.vs)[slot] = bad ? __int_as_float(0x7FC00000) : some ? __fdiv_rn(amax, kE4m3Max) : 0.0f;
+        (value ? a.vs : a.ks)[slot] = bad ? __int_as_float(0x7FC00000) : some ? __fdiv_rn(amax, kE4m3Max) : 0.0f;
 }
 
-// A group of DIM / 8 lanes has one token and every `parts`-th of its rows
-// (query heads, key heads, value heads in order), and reads the token's
-// rotary row and cache slot once.  rot is a multiple of 8, so a lane's block
-// of 4 channels lies in one half of the rotated ones: its pair partners are
-// the block rot / 2 further or back (read again, from L1) or, interleaved
+// A group of DIM / 8 lanes has one token and every `parts`-th of its rows,
+// and reads the token's rotary row and cache slot once -- behind the loads of
+// its first rows, which need neither.  rot is a multiple of 8, so a lane's
+// block of 4 channels lies in one half of the rotated ones: its pair partners
+// are the block rot / 2 further or back (read again, from L1) or, interleaved
 // (IL), its own neighbours.
-template <int DIM, int XT, int KV, bool IL>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a) {
-    constexpr int GL = DIM / 8;
+template <int DIM, int XT, int KV, bool IL, int kAhead>
+__global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_constant__ AppendArgs a) {
+    constexpr int GL = DIM / 8, ES = XT == W12_F32 ? 4 : 2;
     const uint32_t g = blockIdx.x * uint32_t(kThreads / GL) + threadIdx.x / GL;
     const uint32_t tok = g / uint32_t(a.parts), part = g - tok * uint32_t(a.parts);
     AppendLane ln;
@@ -112,6 +148,21 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     pdl_launch_dependents();
     pdl_wait_previous();
     if (tok >= uint32_t(a.tokens)) return;  // (whole groups leave; the reductions are the group's)
+    const int rows = a.q_heads + 2 * a.heads;
+    const unsigned char *q = static_cast<const unsigned char *>(a.q) + (int64_t(tok) * a.q_stride + ln.e) * ES;
+    const unsigned char *k = static_cast<const unsigned char *>(a.k) + (int64_t(tok) * a.k_stride + ln.e) * ES;
+    const unsigned char *v = static_cast<const unsigned char *>(a.v) + (int64_t(tok) * a.v_stride + ln.e) * ES;
+    const auto source = [&](int hd) {
+        const unsigned char *p = hd < a.q_heads ? q : hd < a.q_heads + a.heads ? k : v;
+        const int h = hd < a.q_heads ? hd : hd < a.q_heads + a.heads ? hd - a.q_heads : hd - a.q_heads - a.heads;
+        return p + int64_t(h) * (DIM * ES);
+    };
+    Raw<XT> raw[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+        const int hd = int(part) + i * a.parts;
+        if (hd < rows) raw[i] = load_raw<XT>(source(hd));
+    }
     const uint32_t r = tok / uint32_t(a.T);
     const int pos = a.kv_len[r] - a.T + int(tok - r * uint32_t(a.T));
     if (pos < 0) return;
@@ -143,23 +194,18 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
             s4[0] = low ? -s.x : s.x, s4[1] = low ? -s.y : s.y, s4[2] = low ? -s.z : s.z, s4[3] = low ? -s.w : s.w;
         }
     }
-    const int P = a.parts;
-    int hd = int(part);
-    const int64_t atq = int64_t(tok) * a.q_stride + ln.e;
     uint16_t *out = a.q_out + int64_t(tok) * a.out_stride;
-#pragma unroll 4
-    for (; hd < a.q_heads; hd += P)
-        append_row<DIM, XT, KV, IL, 0>(a, ln, a.q, atq + int64_t(hd) * DIM, out + int64_t(hd) * DIM, 0);
-    hd -= a.q_heads;
-    const int64_t atk = int64_t(tok) * a.k_stride + ln.e;
-#pragma unroll 2
-    for (; hd < a.heads; hd += P)
-        append_row<DIM, XT, KV, IL, 1>(a, ln, a.k, atk + int64_t(hd) * DIM, nullptr, ln.slot0 + (int64_t(hd) << a.page_log2));
-    hd -= a.heads;
-    const int64_t atv = int64_t(tok) * a.v_stride + ln.e;
-#pragma unroll 2
-    for (; hd < a.heads; hd += P)
-        append_row<DIM, XT, KV, IL, 2>(a, ln, a.v, atv + int64_t(hd) * DIM, nullptr, ln.slot0 + (int64_t(hd) << a.page_log2));
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+        const int hd = int(part) + i * a.parts;
+        if (hd >= rows) return;
+        append_row<DIM, XT, KV, IL>(a, ln, raw[i], source(hd), hd, out);
+    }
+#pragma unroll 1
+    for (int hd = int(part) + kAhead * a.parts; hd < rows; hd += a.parts) {
+        const unsigned char *src = source(hd);
+        append_row<DIM, XT, KV, IL>(a, ln, load_raw<XT>(src), src, hd, out);
+    }
 }
 
 template <int DIM, int XT, int KV>
@@ -168,12 +214,18 @@ int append_t(AppendArgs a, int sms, void *stream) {
     const int64_t nh = a.q_heads + 2 * a.heads;
     // A group per row while all blocks fit the GPU at once (8 blocks of 256
     // threads per SM); else 8 groups a token, which share its rotary row and
-    // look-up over nh / 8 rows.
+    // look-up over nh / 8 rows (8186 tokens of 48 rows of 64: 21.0 us; 4 or 16
+    // groups 23.6) and load their first rows ahead of the look-up (without
+    // 23.2; with 64 registers, which leaves 4 blocks on an SM).
     a.parts = int32_t(a.tokens * nh <= int64_t(sms) * 8 * GPB ? nh : nh < 8 ? nh : 8);
     if (a.tokens * a.parts >= int64_t(1) << 32) a.parts = 1;
     const int grid = int((a.tokens * a.parts + GPB - 1) / GPB);
-    return a.interleaved ? launch_step(append_kernel<DIM, XT, KV, true>, grid, kThreads, 0, 1, stream, a)
-                         : launch_step(append_kernel<DIM, XT, KV, false>, grid, kThreads, 0, 1, stream, a);
+    constexpr int kAhead = XT == W12_F32 ? 3 : 6;
+    if (a.parts == nh)
+        return a.interleaved ? launch_step(append_kernel<DIM, XT, KV, true, 1>, grid, kThreads, 0, 1, stream, a)
+                             : launch_step(append_kernel<DIM, XT, KV, false, 1>, grid, kThreads, 0, 1, stream, a);
+    return a.interleaved ? launch_step(append_kernel<DIM, XT, KV, true, kAhead>, grid, kThreads, 0, 1, stream, a)
+                         : launch_step(append_kernel<DIM, XT, KV, false, kAhead>, grid, kThreads, 0, 1, stream, a);
 }
 
 // TOK tokens per block: the first TOK threads find their token's request
