@@ -56,7 +56,7 @@ constexpr int kCap = 1024;             // tokens that are ranked directly, one a
 constexpr int kWide = 2304;            // tokens that can be gathered for a nucleus' boundary
 constexpr int kAround = 800;           // tokens to either side of where the sample sees the boundary
 constexpr int kTaken = 16;             // sampled tokens per thread
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;        // (8 where rows are many)
 constexpr float kOne31 = 2147483648.0f;
 constexpr float kSpan = 22.25f;        // e^-22.25 rounds to weight 0
 
@@ -70,7 +70,8 @@ struct SampleSmall {
     float warp_top[kSW];
     int found_bin;
     uint32_t list_n;
-    u64 mass;                     // what weighs more than the window
+    u64 lowest, highest;               // of the window's composites
+    u64 mass;                          // what weighs more than the window
     uint32_t win_lo, win_end;          // window of weights
     int last;
 };
@@ -89,7 +90,10 @@ struct SampleCut {
         };
         u64 win[kWide];                // weight << 32 | index
     };
-    uint32_t rank[kCap];
+    union {
+        uint32_t rank[kCap];
+        uint16_t member[2 * kCap];     // of the window: the tokens of one bin
+    };
 };
 
 constexpr size_t kSmallBytes = (sizeof(SampleSmall) + 15) & ~size_t(15), kCutBytes = (sizeof(SampleCut) + 15) & ~size_t(15);
@@ -577,7 +581,7 @@ __device__ __forceinline__ void set_window(SampleSmall &sh, const SampleCut &cut
         if (lane >= o) below += x, below_n += z;
     }
     if (lane == 31) sh.warp_top[warp] = below, sh.warp_sum[warp] = below_n;
-    if (tid == 0) sh.found_above = ~0ull, sh.win_lo = 1u, sh.win_end = ~0u;
+    if (tid == 0) sh.found_above = ~0ull;
     __syncthreads();
     float all = 0.0f;
     uint32_t all_n = 0;
@@ -599,39 +603,33 @@ __device__ __forceinline__ void set_window(SampleSmall &sh, const SampleCut &cut
     }
     __syncthreads();
     const uint32_t n = sh.found_above == ~0ull ? all_n : uint32_t(sh.found_above);
-    const uint32_t d = uint32_t(float(kAround) * part) + 1u;
-    const uint32_t from = n > d ? n - d : 0u, to = n + d;
+    // narrower, where the bins at its ends would make it too full (bf16: many
+    // equal logits)
+    for (int around = kAround; around >= kAround / 4; around /= 2) {
+        const uint32_t d = uint32_t(float(around) * part) + 1u;
+        const uint32_t from = n > d ? n - d : 0u, to = n + d;
+        __syncthreads();
+        if (tid == 0) sh.win_lo = 1u, sh.win_end = ~0u, sh.lowest = 0ull, sh.highest = all_n;
+        __syncthreads();
+        uint32_t at = below_n;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int b = b0 + 3 - j;
-        if (c[j] && below_n <= from && from < below_n + c[j] && from > 0u) sh.win_lo = bin_end(b);
-        if (c[j] && below_n <= to && to < below_n + c[j]) sh.win_end = b > 0 ? bin_end(b - 1) : ~0u;
-        below_n += c[j];
+        for (int j = 0; j < 4; ++j) {
+            const int b = b0 + 3 - j;
+            if (c[j] && at <= from && from < at + c[j] && from > 0u) sh.win_lo = bin_end(b), sh.lowest = at;
+            if (c[j] && at <= to && to < at + c[j]) sh.win_end = b > 0 ? bin_end(b - 1) : ~0u, sh.highest = at + c[j];
+            at += c[j];
+        }
+        __syncthreads();
+        if (float(sh.highest - sh.lowest) <= 0.85f * float(kWide) * part) break;
     }
-    __syncthreads();
 }
 
-// In one CTA, with cut.lo and cut.hi all 0: the threshold composite among the n
-// gathered tokens, which are those of the window: the last before which,
-// together with the window's mass above, less than lim lies.  0: they do not
-// hold it, or too many share its bin.  logit(index): of the row.
-template <class L>
-__device__ __forceinline__ u64 window_threshold(SampleSmall &sh, SampleCut &cut, uint32_t n, u64 lim, L logit) {
+// In one CTA: the bin of a histogram of weights (cut.lo, cut.hi) in which the
+// sum, `above` before bin 0, reaches lim (-1: none); sh.found_above: before it.
+__device__ __forceinline__ int boundary_bin(SampleSmall &sh, const SampleCut &cut, u64 above, u64 lim) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    // bins over the floats between the window's ends
-    const uint32_t top = __float_as_uint(__uint2float_rz(min(sh.win_end, 0x80000000u)));
-    const uint32_t span = top - __float_as_uint(__uint2float_rz(sh.win_lo));
-    int shift = 0;
-    while (span >> shift >= uint32_t(kBins)) ++shift;
-    const auto bin_of = [&](uint32_t w) { return int((top - __float_as_uint(__uint2float_rz(w))) >> shift); };
-    if (tid == 0) sh.found_bin = -1, sh.list_n = 0u, sh.thr = ~0ull;
-    for (uint32_t i = tid; i < n; i += kST) {
-        const uint32_t w = uint32_t(cut.win[i] >> 32);
-        const int b = bin_of(w);
-        atomicAdd(&cut.lo[b], w & 0xFFFFu);
-        if (w >> 16) atomicAdd(&cut.hi[b], w >> 16);
-    }
     __syncthreads();
+    if (tid == 0) sh.found_bin = -1;
     u64 v[4], mine = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -641,7 +639,7 @@ __device__ __forceinline__ u64 window_threshold(SampleSmall &sh, SampleCut &cut,
     const u64 incl = warp_scan64(mine, lane);
     if (lane == 31) sh.warp_sum[warp] = incl;
     __syncthreads();
-    u64 before = sh.mass + incl - mine;
+    u64 before = above + incl - mine;
     for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -649,22 +647,86 @@ __device__ __forceinline__ u64 window_threshold(SampleSmall &sh, SampleCut &cut,
         before += v[j];
     }
     __syncthreads();
-    const int bin = sh.found_bin;
+    return sh.found_bin;
+}
+
+// In one CTA, with cut.lo and cut.hi all 0: the threshold composite among the n
+// gathered tokens, which are those of the window: the last before which,
+// together with the window's mass above, less than lim lies.  0: they do not
+// hold it, or too many share its bin.  logit(index): of the row.
+template <class L>
+__device__ __forceinline__ u64 window_threshold(SampleSmall &sh, SampleCut &cut, uint32_t n, u64 lim, L logit) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    // bins over the floats between the window's ends
+    const uint32_t top = __float_as_uint(__uint2float_rz(min(sh.win_end, 0x80000000u)));
+    const uint32_t span = top - __float_as_uint(__uint2float_rz(sh.win_lo));
+    int shift = 0;
+    while (span >> shift >= uint32_t(kBins)) ++shift;
+    const auto bin_of = [&](uint32_t w) { return int((top - __float_as_uint(__uint2float_rz(w))) >> shift); };
+    if (tid == 0) sh.list_n = 0u, sh.thr = ~0ull;
+    for (uint32_t i = tid; i < n; i += kST) {
+        const uint32_t w = uint32_t(cut.win[i] >> 32);
+        const int b = bin_of(w);
+        atomicAdd(&cut.lo[b], w & 0xFFFFu);
+        if (w >> 16) atomicAdd(&cut.hi[b], w >> 16);
+    }
+    int bin = boundary_bin(sh, cut, sh.mass, lim);
     if (bin < 0) return 0;
     for (uint32_t i = tid; i < n; i += kST)
         if (bin_of(uint32_t(cut.win[i] >> 32)) == bin) {
             const uint32_t at = atomicAdd(&sh.list_n, 1u);
-            if (at < uint32_t(kCap)) cut.rank[at] = i;
+            if (at < 2u * kCap) cut.member[at] = uint16_t(i);
         }
     __syncthreads();
-    const uint32_t m = sh.list_n;
-    if (m > uint32_t(kCap)) return 0;
+    uint32_t m = sh.list_n;
+    if (m > 2u * kCap) return 0;
+    // many of one weight: bins over their composites
+#pragma unroll 1
+    while (m > 128u) {
+        u64 c[4], top = 0, bottom = ~0ull;
+        uint32_t id[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t i = tid + q * kST;
+            if (i >= m) continue;
+            id[q] = cut.member[i];
+            const uint32_t x = uint32_t(cut.win[id[q]]);
+            c[q] = pack_key(logit(x), x);
+            top = umax64(top, c[q]);
+            bottom = bottom < c[q] ? bottom : c[q];
+        }
+        const u64 above = sh.found_above;
+        for (int i = tid; i < kBins; i += kST) cut.lo[i] = cut.hi[i] = 0u;
+        if (tid == 0) sh.highest = 0ull, sh.lowest = ~0ull, sh.list_n = 0u;
+        __syncthreads();
+        top = warp_max64(top), bottom = ~warp_max64(~bottom);
+        if (lane == 0) atomicMax(&sh.highest, top), atomicMin(&sh.lowest, bottom);
+        __syncthreads();
+        const u64 hi = sh.highest, width = hi - sh.lowest;
+        int by = 0;
+        while (width >> by >= u64(kBins)) ++by;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (tid + q * kST < m) {
+                const uint32_t w = uint32_t(cut.win[id[q]] >> 32);
+                const int b = int((hi - c[q]) >> by);
+                atomicAdd(&cut.lo[b], w & 0xFFFFu);
+                if (w >> 16) atomicAdd(&cut.hi[b], w >> 16);
+            }
+        bin = boundary_bin(sh, cut, above, lim);
+        if (bin < 0) return 0;  // (not reached: the bin before held it)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (tid + q * kST < m && int((hi - c[q]) >> by) == bin) cut.member[atomicAdd(&sh.list_n, 1u)] = uint16_t(id[q]);
+        __syncthreads();
+        m = sh.list_n;
+    }
     for (uint32_t i = tid; i < m; i += kST) {
-        const u64 x = cut.win[cut.rank[i]];
+        const u64 x = cut.win[cut.member[i]];
         const u64 c = pack_key(logit(uint32_t(x)), uint32_t(x));
         u64 b = sh.found_above;
         for (uint32_t j = 0; j < m; ++j) {
-            const u64 y = cut.win[cut.rank[j]];
+            const u64 y = cut.win[cut.member[j]];
             if (y >> 32 < x >> 32 || y == x) continue;
             // (different logits can have the same weight)
             if (y >> 32 > x >> 32 || pack_key(logit(uint32_t(y)), uint32_t(y)) > c) b += y >> 32;
@@ -1059,7 +1121,8 @@ int run_t(const SampleArgs &a, int cs, void *stream) {
     const uint64_t bit = uint64_t(1) << (dev & 63);
     if (!(ready[dev >> 6].load(std::memory_order_relaxed) & bit)) {
         if (cudaFuncSetAttribute(sample_kernel<DT, CUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMostShared)) !=
-            cudaSuccess)
+                cudaSuccess ||
+            cudaFuncSetAttribute(sample_kernel<DT, CUT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
             return W12_ERR_CUDA;
         ready[dev >> 6].fetch_or(bit, std::memory_order_relaxed);
     }
@@ -1080,11 +1143,12 @@ int launch_sample(SampleArgs &a, int dtype, int sms, void *stream) {
     (void)sms;
     const int es = dtype == W12_F32 ? 4 : 2;
     // Enough CTAs per row that each holds a few thousand logits, and the row
-    // stays in shared memory.
+    // stays in shared memory.  16 for up to 14 rows, which run at once then
+    // (20 such clusters fit with the shared memory of 151936 logits)
     int cs = 1;
-    while (cs < kMaxCluster && a.V > int64_t(cs) * 4096) cs *= 2;
+    while (cs < (a.rows <= 14 ? kMaxCluster : 8) && a.V > int64_t(cs) * 4096) cs *= 2;
     const int64_t chunk = ((a.V + cs - 1) / cs + 7) / 8 * 8;
-    static_assert(W12_SAMPLE_MAX_V <= kMaxCluster * 65536, "16-bit halves of the weights");
+    static_assert(W12_SAMPLE_MAX_V <= 8 * 65536, "16-bit halves of the weights");
     a.chunk = int32_t(chunk);
     a.resident = kSmallBytes + kCutBytes + size_t(chunk) * es + 16 <= kMostShared;
     const size_t at = dtype == W12_F32 ? weights_at<W12_F32>(chunk) : weights_at<W12_BF16>(chunk);
