@@ -721,17 +721,20 @@ __device__ __forceinline__ u64 window_threshold(SampleSmall &sh, SampleCut &cut,
         __syncthreads();
         m = sh.list_n;
     }
-    for (uint32_t i = tid; i < m; i += kST) {
-        const u64 x = cut.win[cut.member[i]];
-        const u64 c = pack_key(logit(uint32_t(x)), uint32_t(x));
+    // the last ones against all
+    u64 *comp = reinterpret_cast<u64 *>(cut.lo);  // (the bins are done with)
+    __syncthreads();
+    u64 mine = 0;
+    if (tid < int(m)) {
+        const uint32_t x = uint32_t(cut.win[cut.member[tid]]);
+        comp[tid] = mine = pack_key(logit(x), x);
+    }
+    __syncthreads();
+    if (tid < int(m)) {
         u64 b = sh.found_above;
-        for (uint32_t j = 0; j < m; ++j) {
-            const u64 y = cut.win[cut.member[j]];
-            if (y >> 32 < x >> 32 || y == x) continue;
-            // (different logits can have the same weight)
-            if (y >> 32 > x >> 32 || pack_key(logit(uint32_t(y)), uint32_t(y)) > c) b += y >> 32;
-        }
-        if (b < lim) atomicMin(&sh.thr, c);
+        for (uint32_t j = 0; j < m; ++j)
+            if (comp[j] > mine) b += cut.win[cut.member[j]] >> 32;
+        if (b < lim) atomicMin(&sh.thr, mine);
     }
     __syncthreads();
     return sh.thr;
