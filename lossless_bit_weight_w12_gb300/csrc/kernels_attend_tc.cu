@@ -352,7 +352,6 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
             // rows have one copy for both slots: their warps wait for one
             // another's products on the last one, then each copies half.
             float sc = fabsf(a.scale_log2);
-            if (!TWO) named_sync(256);
             {
                 constexpr int L = D / 8, RPW = 32 / L;            // lanes per row, rows per step of a warp
                 constexpr int kRows = TWO ? 32 : 16;              // rows of this warp
@@ -360,29 +359,32 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
                 const uint32_t qb = base + uint32_t(TWO ? slot : 0) * uint32_t(128 * D * 2);
                 const uint32_t sign = a.scale_log2 < 0.0f ? 0x80008000u : 0u;  // scores grow with S
                 const int first = TWO ? 32 * (warp & 3) : 16 * warp;
-                constexpr int B = kRows / RPW < 8 ? kRows / RPW : 8;  // loads in flight
-                static_assert(kRows % (B * RPW) == 0, "rows of a warp");
-#pragma unroll 1
-                for (int x0 = 0; x0 < kRows; x0 += B * RPW) {
+                constexpr int B = kRows / RPW;                    // loads in flight: all of them
+                static_assert(kRows % RPW == 0, "rows of a warp");
+                {
                     uint4 q[B];
+                    int in_u = (TWO ? 128 * slot : 0) + first + lane / L;
+                    int tok = att_token(a, seg.row0 + in_u), g = seg.row0 + in_u - tok * a.G;
+                    const int step = att_token(a, RPW), step_g = RPW - step * a.G;
+                    const uint16_t *src = a.q + int64_t(seg.head * a.G) * D + 8 * c;
 #pragma unroll
                     for (int x = 0; x < B; ++x) {
-                        const int in_u = (TWO ? 128 * slot : 0) + first + x0 + x * RPW + lane / L;
                         q[x] = make_uint4(0, 0, 0, 0);
-                        if (in_u < seg.nrows) {
-                            const int rho = seg.row0 + in_u, tok = att_token(a, rho), hq = seg.head * a.G + rho - tok * a.G;
-                            q[x] = *reinterpret_cast<const uint4 *>(a.q + tok * a.q_stride + int64_t(hq) * D + 8 * c);
-                        }
+                        if (in_u < seg.nrows) q[x] = *reinterpret_cast<const uint4 *>(src + tok * a.q_stride + g * D);
+                        in_u += RPW, tok += step, g += step_g;
+                        if (g >= a.G) g -= a.G, ++tok;
                     }
+                    if (!TWO) named_sync(256);
 #pragma unroll
                     for (int x = 0; x < B; ++x) {
-                        const int rq = first + x0 + x * RPW + lane / L;
+                        const int rq = first + x * RPW + lane / L;
                         uint32_t w[4] = {q[x].x, q[x].y, q[x].z, q[x].w};
                         if (Q8) {  // fp16, the row scaled by a power of two to below 2
                             uint32_t top = 0;
 #pragma unroll
                             for (int y = 0; y < 4; ++y) top = max(top, max(w[y] & 0x7FFFu, (w[y] >> 16) & 0x7FFFu));
-                            top = __reduce_max_sync((L == 16 ? 0xFFFFu : 0xFFu) << (lane / L * L), top);
+#pragma unroll
+                            for (int o = L / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
                             const int e = max(-100, min(126, int(top >> 7) - 127));
                             const float down = __uint_as_float(uint32_t(127 - e) << 23);
 #pragma unroll
