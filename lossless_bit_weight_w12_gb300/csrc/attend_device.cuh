@@ -280,17 +280,22 @@ __device__ __forceinline__ void bulk_bytes(uint32_t dst, const void *src, uint32
                  : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // The tiles' copies by a producer warp: KT keys each, a lane per box ("chunk":
 // the keys of one page in one tile).  A batch of 32 chunks has its table
 // entries read at once, the next batch's behind the copies of this one's
-// first tile.  ready(i), by all lanes: waits until the CTA's tile i may be
+// first tile; the first batch stays in the worker's first segment, whose place
+// is known.  ready(i), by all lanes: waits until the CTA's tile i may be
 // written, false to stop; issue(i, chunks, chunk, row), on the lanes that have
 // a chunk of it (keys chunk * br ... of the tile, cache rows row ...): copies
 // it; chunks: of the tile, on its first, which arms the barrier before the
 // others' copies.
 template <int KT, typename Ready, typename Arm, typename Issue>
-__device__ __forceinline__ void att_producer(const AttendArgs &a, const AttPlan &plan, const AttShared &sh, int br,
-                                             Ready ready, Arm arm, Issue issue) {
+__device__ __forceinline__ void att_producer(const AttendArgs &a, const AttPlan &plan, const AttShared &sh,
+                                             const AttSeg &start, int br, Ready ready, Arm arm, Issue issue) {
     const int lane = threadIdx.x & 31;
     const int cpt = KT / br, tpb = 32 / cpt;
     const int my_tile = lane / cpt, my_chunk = lane % cpt;
@@ -298,46 +303,49 @@ __device__ __forceinline__ void att_producer(const AttendArgs &a, const AttPlan 
         int head, key, page, chunks;  // key < 0: nothing to load; chunks: of the tile, from this one on
     };
     // (what it loads is not looked at before the batch is issued)
-    const auto look = [&](int tb) {
-        const int t = tb + my_tile;
+    const auto chunk_of = [&](int head, int req, int tile_key, int key_end) {
         Chunk c{0, -1, 0, 0};
-        if (t >= plan.t1) return c;
-        const AttSeg g = att_locate(a, plan, sh, t);
-        const int key = g.key + my_chunk * br;
-        if (key >= g.key_end) return c;
-        c.head = g.head;
+        const int key = tile_key + my_chunk * br;
+        if (key >= key_end) return c;
+        c.head = head;
         c.key = key;
-        c.chunks = min(cpt - my_chunk, (g.key_end - key + br - 1) / br);
-        c.page = a.table[int64_t(g.req) * a.table_cols + (key >> a.page_log2)];
+        c.chunks = min(cpt - my_chunk, (key_end - key + br - 1) / br);
+        c.page = a.table[int64_t(req) * a.table_cols + (key >> a.page_log2)];
         return c;
     };
+    if (plan.t0 >= plan.t1) return;
     Chunk cur{0, -1, 0, 0}, nxt = cur;
-    int row = 0;
+    int tb = plan.t0, n = min(min(tpb, start.left), plan.t1 - tb);
+    if (my_tile < n) cur = chunk_of(start.head, start.req, start.key + my_tile * KT, start.key_end);
 #pragma unroll 1
-    for (int tb = plan.t0 - tpb, k = tpb - 1; tb < plan.t1;) {
-        // tile tb + k (first round: of a batch before the first, of which
-        // nothing is issued)
-        if (tb >= plan.t0) {
-            if (tb + k >= plan.t1) return;
+    for (;;) {
+        int pg = cur.page;
+        if (cur.key >= 0 && (pg < 0 || pg >= a.n_pages)) {
+            atomicCAS(a.err, 0, W12_ERR_DEVICE);
+            pg = 0;
+        }
+        const int row = ((pg * a.heads + cur.head) << a.page_log2) + (cur.key & (a.page - 1));
+#pragma unroll 1
+        for (int k = 0; k < n; ++k) {
             const int i = tb + k - plan.t0;
             if (!ready(i)) return;
             const bool mine = my_tile == k;
             if (mine && my_chunk == 0) arm(i, cur.chunks);
             if (cpt > 1) __syncwarp();
             if (mine && cur.key >= 0) issue(i, my_chunk, row);
-        }
-        if (k == 0 || tb < plan.t0) nxt = look(tb + tpb);
-        if (++k == tpb) {
-            k = 0;
-            tb += tpb;
-            cur = nxt;
-            int pg = cur.page;
-            if (cur.key >= 0 && (pg < 0 || pg >= a.n_pages)) {
-                atomicCAS(a.err, 0, W12_ERR_DEVICE);
-                pg = 0;
+            if (k == 0) {
+                const int t = tb + n + my_tile;
+                nxt = Chunk{0, -1, 0, 0};
+                if (t < plan.t1) {
+                    const AttSeg g = att_locate(a, plan, sh, t);
+                    nxt = chunk_of(g.head, g.req, g.key, g.key_end);
+                }
             }
-            row = ((pg * a.heads + cur.head) << a.page_log2) + (cur.key & (a.page - 1));
         }
+        tb += n;
+        if (tb >= plan.t1) return;
+        n = min(tpb, plan.t1 - tb);
+        cur = nxt;
     }
 }
 

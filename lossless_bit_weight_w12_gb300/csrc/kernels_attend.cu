@@ -228,6 +228,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_kernel(const __grid_
         ctl.limit_ns = kWaitLimitNs;
         mbar_fence_init();
     }
+    if (lane == 0 && warp >= kCW) prefetch_map(&a.mk), prefetch_map(&a.mv);
     att_start(a);
     const AttPlan plan = att_plan(a, sh, 2, me);
     const AttendLine &ln = a.line[kLineRest];
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_kernel(const __grid_
         const int br = min(a.page, kAttTile);
         int issued = 0;
         att_producer<kAttTile>(
-            a, plan, sh, br,
+            a, plan, sh, sh.first[me], br,
             [&](int i) {
                 const int s = i % S;
                 const bool go =

@@ -302,6 +302,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    if (lane == 0 && (warp == kProdWarp || warp == kProdWarp + 3)) prefetch_map(warp == kProdWarp ? &a.mk : &a.mv);
     att_start(a);
     const AttPlan plan = att_plan(a, sh, 1, 0);
     tmem_fence_before();
@@ -698,7 +699,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
             const int kv = warp == kProdWarp ? 0 : 1, br = min(a.page, 64);
             int issued = 0;
             att_producer<kKT>(
-                a, plan, sh, br,
+                a, plan, sh, sh.first[0], br,
                 [&](int i) {
                     const int h = 2 * i + kv, s = h % SI;
                     const bool go =
