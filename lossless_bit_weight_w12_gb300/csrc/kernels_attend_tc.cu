@@ -733,12 +733,15 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
         } else if (warp == kIssueWarp || warp == kIssueWarp + 1) {
             // -------------------------------------------------- products
             // A thread per slot.  A burst is P V of a tile and Q K^T of the
-            // slot's next; the two threads take turns by a token, so that the
-            // tensor cores finish one slot's scores while the other's warps
-            // work on theirs (bursts that interleave end at the same time, and
-            // both slots wait at the same time), and each thread's waits --
-            // some 250 cycles even on a barrier that is complete, while
-            // products are in flight -- pass under the other's burst.
+            // slot's next.  Units of 256 rows: the two threads take turns by a
+            // token, so that the tensor cores finish one slot's scores while
+            // the other's warps work on theirs (bursts that interleave end at
+            // the same time, and both slots wait at the same time: 110 us
+            // without it against 98, 128 requests under a prefix), and each
+            // thread's waits -- some 250 cycles even on a barrier that is
+            // complete, while products are in flight -- pass under the other's
+            // burst.  Units of 128 rows: the slots' tiles alternate anyway
+            // (8 x 16 tokens on e4m3: 54.6 us with it, 53.1 without).
             const int slot = warp - kIssueWarp;
             if (lane == 0) {
                 const uint32_t iqk = umma_idesc(Q8, kKT, false), ipv = umma_idesc(Q8, D, true);
@@ -754,7 +757,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
                         umma_smem(ts, dq + uint64_t(((ks >> 2) * 128 * 128 + in_half) >> 4),
                                   d + uint64_t(((ks >> 2) * kKT * 128 + in_half) >> 4), iqk, ks ? 1u : 0u);
                         // (the other thread takes its time to see it)
-                        if (ks == KS / 2 - 1 && pass) mbar_arrive(&token[slot ^ 1]);
+                        if (TWO && ks == KS / 2 - 1 && pass) mbar_arrive(&token[slot ^ 1]);
                     }
                     umma_arrive(&s_full[slot]);
                     umma_arrive(&op_empty[s]);
@@ -776,20 +779,20 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
                     for (int k = k0; k < n; k += kStep) {
                         const int i = i0 + k, s = stage(i, 1);
                         const bool more = k + kStep < n;
-                        const int burst = TWO ? 2 * i + slot : i;  // of the CTA; odd ones are slot 1's
                         wait_operand(i, 1);
                         // e4m3: the next keys may be converted only after the
                         // values' stage of a tile before was released
                         if (!Q8 && more) wait_operand(i + kStep, 0);
                         att_wait(&p_full[slot], n_p++ & 1u, &ctl, a.err);
-                        if (burst > 0) att_wait(&token[slot], uint32_t((burst - 1) / 2) & 1u, &ctl, a.err);
+                        if (TWO && (i > 0 || slot))  // burst 2 i + slot
+                            att_wait(&token[slot], uint32_t((2 * i + slot - 1) / 2) & 1u, &ctl, a.err);
                         tmem_fence_after();
                         const uint64_t d = umma_desc_mn(ops + uint32_t(s) * uint32_t(C::kHalf), kKT * 128);
 #pragma unroll
                         for (int ks = 0; ks < kKT / 16; ++ks) {
                             umma_tmem_a(ts + kOCol, ts + 8u * uint32_t(ks), d + uint64_t((ks * 2048) >> 4), ipv,
                                         (k > k0 || ks || zeroed) ? 1u : 0u);
-                            if (ks == kKT / 32 - 1 && !more) mbar_arrive(&token[slot ^ 1]);
+                            if (TWO && ks == kKT / 32 - 1 && !more) mbar_arrive(&token[slot ^ 1]);
                         }
                         umma_arrive(&op_empty[s]);
                         if (more) {
