@@ -121,32 +121,18 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-__device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t *v) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-            taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
-}
-
-// f(c, columns 32 c .. of this lane's row) for c < 4, the next columns on their way.
+// f(c, columns 64 c .. of this lane's row) for c < 2.
 template <typename F>
 __device__ __forceinline__ void by_columns(uint32_t ts, F f) {
-    float2 x[16], y[16];
-    tmem_load32(ts, reinterpret_cast<uint32_t *>(x));
-    tmem_wait_ld();
-    tmem_landed32(reinterpret_cast<uint32_t *>(x));
 #pragma unroll 1
-    for (int c = 0; c < 4; c += 2) {
-        tmem_load32(ts + 32u * uint32_t(c + 1), reinterpret_cast<uint32_t *>(y));
-        f(c, x);
-        tmem_wait_ld();
-        tmem_landed32(reinterpret_cast<uint32_t *>(y));
-        if (c == 0) tmem_load32(ts + 64u, reinterpret_cast<uint32_t *>(x));
-        f(c + 1, y);
+    for (int c = 0; c < 2; ++c) {
+        float2 x[32];
+        tmem_load32(ts + 64u * uint32_t(c), reinterpret_cast<uint32_t *>(x));
+        tmem_load32(ts + 64u * uint32_t(c) + 32u, reinterpret_cast<uint32_t *>(x + 16));
         tmem_wait_ld();
         tmem_landed32(reinterpret_cast<uint32_t *>(x));
+        tmem_landed32(reinterpret_cast<uint32_t *>(x + 16));
+        f(c, x);
     }
 }
 
@@ -454,33 +440,35 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
                     float top;
                     float2 xs[Q8 ? 1 : kKT / 2];
                     if (Q8) {
-                        // Two passes over 32 columns at a time, by small loops
+                        // Two passes over 64 columns at a time, by small loops
                         // (unrolled, the multiplications by the scales make
-                        // the code miss the instruction cache): the scaled
-                        // scores go back to tensor memory.
-                        float mx[2] = {kNegInf, kNegInf};
-                        by_columns(ts, [&](int c, float2 (&x)[16]) {
+                        // the code miss the instruction cache: 73 us against 57
+                        // for 8 x 16 tokens): the scaled scores go back to
+                        // tensor memory.
+                        float mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+                        by_columns(ts, [&](int c, float2 (&x)[32]) {
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const uint4 z = lds128(tk + uint32_t(128 * c + 16 * j));
+                            for (int j = 0; j < 16; ++j) {
+                                const uint4 z = lds128(tk + uint32_t(256 * c + 16 * j));
                                 x[2 * j] = __fmul2_rn(x[2 * j], make_float2(__uint_as_float(z.x), __uint_as_float(z.y)));
                                 x[2 * j + 1] =
                                     __fmul2_rn(x[2 * j + 1], make_float2(__uint_as_float(z.z), __uint_as_float(z.w)));
                             }
                             if (masked) {
 #pragma unroll
-                                for (int j = 0; j < 16; ++j) {
-                                    x[j].x = 32 * c + 2 * j <= seen ? x[j].x : kNegInf;
-                                    x[j].y = 32 * c + 2 * j + 1 <= seen ? x[j].y : kNegInf;
+                                for (int j = 0; j < 32; ++j) {
+                                    x[j].x = 64 * c + 2 * j <= seen ? x[j].x : kNegInf;
+                                    x[j].y = 64 * c + 2 * j + 1 <= seen ? x[j].y : kNegInf;
                                 }
                             }
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) mx[j & 1] = max3(mx[j & 1], x[j].x, x[j].y);
-                            tmem_store32(ts + 32u * uint32_t(c), reinterpret_cast<const uint32_t *>(x));
+                            for (int j = 0; j < 32; ++j) mx[j & 3] = max3(mx[j & 3], x[j].x, x[j].y);
+                            tmem_store32(ts + 64u * uint32_t(c), reinterpret_cast<const uint32_t *>(x));
+                            tmem_store32(ts + 64u * uint32_t(c) + 32u, reinterpret_cast<const uint32_t *>(x + 16));
                         });
                         att_wait(&vs_full[i % (C::kScaleRing / 2)], uint32_t(i / (C::kScaleRing / 2)) & 1u, &ctl, a.err);
                         lift = __uint_as_float(lds32(tv + uint32_t(kKT) * 4u));
-                        top = fmaxf(mx[0], mx[1]) * sc + lift;
+                        top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc + lift;
                         tmem_wait_st();
                     } else {
 #pragma unroll
@@ -525,11 +513,11 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
                     const float2 sc2 = make_float2(sc, sc), mu2 = make_float2(-mu, -mu);
                     float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                     if (Q8) {
-                        by_columns(ts, [&](int c, float2 (&x)[16]) {
-                            uint32_t p[16];
+                        by_columns(ts, [&](int c, float2 (&x)[32]) {
+                            uint32_t p[32];
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const uint4 z = lds128(tv + uint32_t(128 * c + 16 * j));
+                            for (int j = 0; j < 16; ++j) {
+                                const uint4 z = lds128(tv + uint32_t(256 * c + 16 * j));
 #pragma unroll
                                 for (int h = 0; h < 2; ++h) {
                                     float2 e = __ffma2_rn(x[2 * j + h], sc2, mu2);
@@ -539,7 +527,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
                                     p[2 * j + h] = pack_f16(e.x, e.y);
                                 }
                             }
-                            tmem_store16(ts + 16u * uint32_t(c), p);  // (columns that have been read)
+                            tmem_store32(ts + 32u * uint32_t(c), p);  // (columns that have been read)
                         });
                     } else {
 #pragma unroll
