@@ -232,3 +232,65 @@ def test_agrees_with_greedy_verify(dev, w12mod, oracle):
     c = Call(w12mod, dev, _dev(lg, dev), R, T, np.zeros(R * T), [0.0] * R, [7] * R, [0.5] * R, None, draft)
     assert c.accept.cpu().numpy().tolist() == want[0].tolist()
     assert c.next.cpu().numpy().tolist() == want[1].tolist()
+
+
+def test_side_stream_and_graph(dev, w12mod):
+    """On another stream than the tensors', and captured and replayed with new
+    numbers: the same tokens as by itself."""
+    import torch
+    R, T, V = 3, 4, 40000
+    g = torch.Generator(device=dev)
+    g.manual_seed(3)
+    x = 3 * torch.randn(R * T, V, generator=g, device=dev)
+    u = torch.rand(R * T, generator=g, device=dev)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device=dev)  # noqa: E731
+    temp, top_p = torch.full((R,), 0.8, device=dev), torch.full((R,), 0.9, device=dev)
+    draft, ws = i32(R, T - 1), w12mod.workspace(w12mod.sample_workspace_size(R, T, V), dev)
+    a, b = [i32(R * T), i32(R), i32(R)], [i32(R * T), i32(R), i32(R)]
+
+    def call(o, stream=None):
+        w12mod.sample(x, R, T, u, o[0], ws, temp, None, top_p, draft_dev=draft, accept_dev=o[1], next_dev=o[2],
+                      stream=stream)
+
+    call(a)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    call(b, side)
+    side.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        call(b)
+    for _ in range(3):
+        u.uniform_(generator=g)
+        draft.copy_(a[0].view(R, T)[:, :-1])
+        call(a)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_many_equal_logits_around_the_nucleus(dev, w12mod):
+    """Logits on a coarse grid: the nucleus ends among hundreds of equal ones, of
+    which the lowest indices stay (whole-number arithmetic on the weights)."""
+    import torch
+    V, n = 60000, 32
+    rng = np.random.default_rng(8)
+    x = np.round(rng.standard_normal(V) * 8).astype(np.float32) / 8
+    u = np.linspace(0, 1, n, endpoint=False).astype(np.float32)
+    # the library's weights (31-bit fixed point of the fp32 exponential, which torch's on the device is)
+    w = torch.exp((_dev(x, dev) - float(x.max())) * 1.0).double().cpu().numpy()
+    w = np.rint(w * 2.0 ** 31).astype(np.int64)
+    for p in (0.3, 0.7, 0.95):
+        order = np.lexsort((np.arange(V), -x))
+        pf = int(np.round(np.float32(p) * 2.0 ** 24))
+        lim = -(-pf * int(w.sum()) // (1 << 24))
+        before = np.cumsum(w[order]) - w[order]
+        kept = np.zeros(V, dtype=np.int64)
+        kept[order[before < lim]] = w[order[before < lim]]
+        cum = np.cumsum(kept)
+        want = [int(np.searchsorted(cum, int(np.float32(a) * 2.0 ** 24) * int(cum[-1]) >> 24, side="right")) for a in u]
+        for t in (torch.float32, torch.bfloat16):
+            c = Call(w12mod, dev, _dev(np.tile(x, (n, 1)), dev).to(t), n, 1, u, [1.0] * n, None, [p] * n)
+            assert c.tok.tolist() == want, (p, t)
