@@ -236,6 +236,14 @@ extern "C" int w12_attend(const w12_kv *kv, const uint16_t *q, int64_t q_stride,
     a.arrived = reinterpret_cast<uint32_t *>(w + p.off_arrived);
     a.plan = reinterpret_cast<int32_t *>(w + p.off_plan);
     a.join = p.join;
+    // The join's warps share entries where a row has many of them (about the
+    // workers per unit, and one at either end) and there are few rows: 76
+    // entries of 128 rows took 10 us in 128 warps.
+    int64_t entries = 0, warps = int64_t((p.rows + 31) / 32) * kv->heads * (kv->head_dim / 4);
+    for (const auto &n : p.line)
+        if (n.grid) entries += (n.grid / (int64_t(kv->heads) * (n.pu + R * n.su)) + 2) * n.halves;
+    a.split = 1;
+    while (a.split < 8 && entries > 12 * a.split && warps * a.split * 2 <= int64_t(p.sms) * 32) a.split *= 2;
     a.sms = p.sms;
     a.per_g = ~uint64_t(0) / uint64_t(a.G) + 1;
     for (int i = 0; i < kLines; ++i) {

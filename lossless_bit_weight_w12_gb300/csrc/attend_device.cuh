@@ -118,6 +118,15 @@ __device__ __forceinline__ int att_prefix_sms(const AttendArgs &a, int w, int su
     return max(a.sms - sms_q, max(1, min(min(lp.grid, a.sms - 1), int(x + 0.5f))));
 }
 
+// Workers of the tensor-memory kernel: each has a few tiles (4 of 128 rows, 2
+// of 256), as a segment costs about as much as two and leaves 64 KB of
+// results, but no unit waits for another (4 requests x 8 tokens under one key
+// head, 7500 keys: 42 us with a worker per tile, 18 so).
+__device__ __forceinline__ int att_tc_grid(int grid, int rt, int units, int tiles) {
+    const int few = rt == 256 ? 2 : 4;
+    return min(grid, max(units, (tiles + few - 1) / few));
+}
+
 // Fills in what follows from (head, req, block) for the unit's tile k.
 __device__ __forceinline__ void att_unit_at(const AttendArgs &a, const AttPlan &p, const AttShared &sh, AttSeg &s, int k) {
     const AttendLine &ln = a.line[a.self];
@@ -222,11 +231,12 @@ __device__ __forceinline__ AttPlan att_plan(const AttendArgs &a, AttShared &sh, 
         if (lane == 0) {
             int g = ln.grid;
             if (w > 0) {
-                const int gp = att_prefix_sms(a, w, all);
-                const int gq = a.line[kLineRequests].grid ? min(ln.grid, a.sms - gp) : min(ln.grid, 2 * (a.sms - gp));
-                g = a.self == kLinePrefix ? gp : gq;
+                const int gp = att_tc_grid(att_prefix_sms(a, w, all), a.line[kLinePrefix].rt,
+                                           a.heads * a.line[kLinePrefix].pu, a.heads * a.line[kLinePrefix].pu * w);
+                g = a.self == kLinePrefix ? gp : min(g, (a.sms - gp) * (a.line[kLineRequests].grid ? 1 : 2));
                 if (tell) a.plan[1] = gp;
             }
+            if (a.self == kLineRequests) g = att_tc_grid(g, ln.rt, a.heads * a.R * ln.su, a.heads * ln.su * all);
             sh.w = w;
             sh.grid = g;
             if (tell) a.plan[0] = w, a.plan[2] = g;

@@ -714,42 +714,74 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_kernel(const __grid_
     att_end(a);
 }
 
-// The join of the lines' results.  A warp has 32 query rows of a head (a lane
-// each) and kJC channels.
+// The join of the lines' results.  `split` warps of a block share 32 query
+// rows of a head (a lane each) and kJC channels: they take parts of the
+// entries, which are then added up in their order.
 constexpr int kJC = 4;
 
-template <int D>
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ AttendArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int groups = (a.rows + 31) / 32;
-    const int w = int(blockIdx.x) * 8 + int(threadIdx.x >> 5), slices = D / kJC;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int groups = (a.rows + 31) / 32, slices = D / kJC, sp = SPLIT ? a.split : 1, mine = SPLIT ? warp % sp : 0;
+    const int w = (int(blockIdx.x) * 8 + warp) / sp;
     pdl_launch_dependents();
     pdl_wait_previous();
     const int d0 = w % slices * kJC, head = w / slices / groups;
     const int rho = w / slices % groups * 32 + lane;
-    if (head >= a.heads || rho >= a.rows) return;
-    const int r = rho / (a.T * a.G), in_req = rho - r * a.T * a.G;
-    const AttendLine &lp = a.line[kLinePrefix], &lq = a.line[a.line[kLineRequests].grid ? kLineRequests : kLineRest];
-    const int32_t *cum = a.plan + 3;
-    const int np = a.plan[0], gp = a.plan[1], gq = a.plan[2], q0 = cum[r], q1 = cum[r + 1], qa = cum[a.R];
+    const bool valid = head < a.heads && rho < a.rows;
     float m = kNegInf, l = 0.0f, acc[kJC] = {};
-    int c, n;
-    const int s = in_req / lq.rt;
-    att_segments(gq, a.heads * lq.su * qa, head * lq.su * qa + lq.su * q0 + s * (q1 - q0), q1 - q0, c, n);
-    const int u = (head * a.R + r) * lq.su + s;
-    if (a.line[kLineRequests].grid) {
-        const size_t at = size_t(u + c) * lq.halves * lq.rt, r0 = in_req - s * lq.rt;
-        att_add<D, false, kJC, 4>(lq.part_ml + at + r0, lq.part_o + at * D + d0 * lq.rt + r0, lq.rt, n * lq.halves, m, l, acc);
-    } else {
-        const size_t at = size_t(u + c) * lq.rt + in_req;
-        att_add<D, true, kJC, 2>(lq.part_ml + at, lq.part_o + at * D + d0, lq.rt, n, m, l, acc);
+    if (valid) {
+        const int tg = a.T * a.G, r = rho / tg, in_req = rho - r * tg;
+        const AttendLine &lp = a.line[kLinePrefix], &lq = a.line[a.line[kLineRequests].grid ? kLineRequests : kLineRest];
+        const int32_t *cum = a.plan + 3;
+        const int np = a.plan[0], gp = a.plan[1], gq = a.plan[2], q0 = cum[r], q1 = cum[r + 1], qa = cum[a.R];
+        int c, n;
+        const int s = in_req / lq.rt;
+        att_segments(gq, a.heads * lq.su * qa, head * lq.su * qa + lq.su * q0 + s * (q1 - q0), q1 - q0, c, n);
+        const int u = (head * a.R + r) * lq.su + s;
+        n *= lq.halves;
+        int e0 = n * mine / sp, e1 = n * (mine + 1) / sp;
+        if (a.line[kLineRequests].grid) {
+            const size_t at = (size_t(u + c) * lq.halves + e0) * lq.rt, r0 = in_req - s * lq.rt;
+            att_add<D, false, kJC, 4>(lq.part_ml + at + r0, lq.part_o + at * D + d0 * lq.rt + r0, lq.rt, e1 - e0, m, l, acc);
+        } else {
+            const size_t at = size_t(u + c + e0) * lq.rt + in_req;
+            att_add<D, true, kJC, 2>(lq.part_ml + at, lq.part_o + at * D + d0, lq.rt, e1 - e0, m, l, acc);
+        }
+        if (np > 0) {
+            const int b = rho / lp.rt, up = head * lp.pu + b;
+            att_segments(gp, a.heads * lp.pu * np, up * np, np, c, n);
+            n *= lp.halves;
+            e0 = n * mine / sp, e1 = n * (mine + 1) / sp;
+            const size_t at = (size_t(up + c) * lp.halves + e0) * lp.rt, r0 = rho - b * lp.rt;
+            att_add<D, false, kJC, 4>(lp.part_ml + at + r0, lp.part_o + at * D + d0 * lp.rt + r0, lp.rt, e1 - e0, m, l, acc);
+        }
     }
-    if (np > 0) {
-        const int b = rho / lp.rt, up = head * lp.pu + b;
-        att_segments(gp, a.heads * lp.pu * np, up * np, np, c, n);
-        const size_t at = size_t(up + c) * lp.halves * lp.rt, r0 = rho - b * lp.rt;
-        att_add<D, false, kJC, 4>(lp.part_ml + at + r0, lp.part_o + at * D + d0 * lp.rt + r0, lp.rt, n * lp.halves, m, l, acc);
+    if (SPLIT) {
+        __shared__ float part[8][32][kJC + 2];
+        float *o = part[warp][lane];
+        o[0] = m, o[1] = l;
+#pragma unroll
+        for (int c = 0; c < kJC; ++c) o[2 + c] = acc[c];
+        __syncthreads();
+        if (mine) return;
+        float top = m;
+        for (int k = 1; k < sp; ++k) top = fmaxf(top, part[warp + k][lane][0]);
+        const float mu = top == kNegInf ? 0.0f : top;
+        float f = ex2(m - mu);
+        l *= f;
+#pragma unroll
+        for (int c = 0; c < kJC; ++c) acc[c] *= f;
+        for (int k = 1; k < sp; ++k) {
+            const float *y = part[warp + k][lane];
+            f = ex2(y[0] - mu);
+            l += y[1] * f;
+#pragma unroll
+            for (int c = 0; c < kJC; ++c) acc[c] += y[2 + c] * f;
+        }
+        m = top;
     }
+    if (!valid) return;
     const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);  // no key: zeros
     *reinterpret_cast<uint2 *>(att_out<D>(a, head, rho) + d0) =
         make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
@@ -828,10 +860,13 @@ int launch_attend_rest(const AttendArgs &a, int dim, int kv, void *stream) {
 }
 
 int launch_attend_join(const AttendArgs &a, int dim, void *stream) {
-    const int64_t warps = int64_t((a.rows + 31) / 32) * a.heads * (dim / kJC);
+    const int64_t warps = int64_t((a.rows + 31) / 32) * a.heads * (dim / kJC) * a.split;
     const int blocks = int((warps + 7) / 8);
-    return dim == 128 ? launch_step(attend_join_kernel<128>, blocks, 256, 0, 1, stream, a)
-                      : launch_step(attend_join_kernel<64>, blocks, 256, 0, 1, stream, a);
+    if (a.split > 1)
+        return dim == 128 ? launch_step(attend_join_kernel<128, true>, blocks, 256, 0, 1, stream, a)
+                          : launch_step(attend_join_kernel<64, true>, blocks, 256, 0, 1, stream, a);
+    return dim == 128 ? launch_step(attend_join_kernel<128, false>, blocks, 256, 0, 1, stream, a)
+                      : launch_step(attend_join_kernel<64, false>, blocks, 256, 0, 1, stream, a);
 }
 
 }  // namespace w12

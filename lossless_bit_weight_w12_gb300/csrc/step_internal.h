@@ -105,6 +105,7 @@ struct AttendArgs {
     uint32_t *arrived;  // [workers] segments of a unit that are done; zero between calls
     int32_t *plan;      // for the join: W, both lines' workers, the R + 1 cumulative tiles of the requests
     int32_t join;       // 1: a join kernel adds up the results
+    int32_t split;      // its warps per row group and channels: 1, 2, 4 or 8
     AttendLine line[kLines];
 };
 int attend_make_maps(AttendArgs &a, const w12_kv *kv);
