@@ -284,13 +284,11 @@ extern "C" int w12_sample(const void *logits, int dtype, int64_t R, int64_t T, i
     if (!aligned(logits, dtype == W12_F32 ? 4 : 2)) return W12_ERR_ALIGN;
     if (!ws || ws_bytes < need) return W12_ERR_WORKSPACE;
     if (!aligned(ws, 256)) return W12_ERR_ALIGN;
-    int sms = 0;
-    if (current_sms(&sms) != W12_OK) return W12_ERR_CUDA;
     SampleArgs a = {};
     a.logits = logits;
     a.temperature = temperature, a.top_k = top_k, a.top_p = top_p, a.min_p = min_p, a.u = u;
     a.tokens = tokens, a.prob = prob, a.draft = draft, a.accept_len = accept_len, a.next_tok = next_tok;
     a.counter = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(ws) + kWsHeader);
     a.V = V, a.rows = R * T, a.R = R, a.T = T;
-    return launch_sample(a, dtype, sms, stream);
+    return launch_sample(a, dtype, stream);
 }

@@ -464,19 +464,19 @@ __device__ __forceinline__ bool att_side_by_side(const AttendArgs &a) {
     return a.line[kLinePrefix].grid && a.self != kLinePrefix;
 }
 __device__ __forceinline__ void att_start(const AttendArgs &a) {
-    if (!att_side_by_side(a)) pdl_wait_previous();
+    if (a.self == kLinePrefix) pdl_wait_previous();
     pdl_launch_dependents();
+    if (a.self != kLinePrefix && !att_side_by_side(a)) pdl_wait_previous();
 }
 __device__ __forceinline__ void att_end(const AttendArgs &a) {
     if (att_side_by_side(a)) pdl_wait_previous();
 }
 
-// True in the worker that is the last of a unit's `segments` to get here (one
-// thread; the others' results are behind a barrier that it has passed).  A
-// worker is the first of at most one unit with several segments, so it names
-// the counter.
+// True in the worker that is the last of a unit's (two or more) segments to
+// get here (one thread; the others' results are behind a barrier that it has
+// passed).  A worker is the first of at most one unit with several segments,
+// so it names the counter.
 __device__ __forceinline__ bool att_last(const AttendArgs &a, int first, int segments) {
-    if (segments == 1) return true;
     uint32_t before;
     asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;"
                  : "=r"(before)

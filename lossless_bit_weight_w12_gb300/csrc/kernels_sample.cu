@@ -10,8 +10,8 @@
 // top-p keep is always "composite >= threshold".  A token of weight 0 (22 t
 // below the largest logit) can neither be drawn nor change a sum.
 //
-// A row is read once: a cluster of up to 8 CTAs keeps it in distributed
-// shared memory (151936 fp32 logits: 74 KB a CTA).  The work on it:
+// A row is read once: a cluster of 8 CTAs (16 where rows are few) keeps it in
+// distributed shared memory (151936 fp32 logits: 74 KB a CTA).  The work on it:
 //  - maximum, with the load;
 //  - top_k up to 1024: the k-th largest of the threads' own maxima bounds the
 //    k-th largest logit from below, so one histogram entry per thread gives a
@@ -1142,12 +1142,12 @@ int run(const SampleArgs &a, int cs, void *stream) {
 
 }  // namespace
 
-int launch_sample(SampleArgs &a, int dtype, int sms, void *stream) {
-    (void)sms;
+int launch_sample(SampleArgs &a, int dtype, void *stream) {
     const int es = dtype == W12_F32 ? 4 : 2;
     // Enough CTAs per row that each holds a few thousand logits, and the row
-    // stays in shared memory.  16 for up to 14 rows, which run at once then
-    // (20 such clusters fit with the shared memory of 151936 logits)
+    // stays in shared memory.  16 for up to 14 rows: so many such clusters run
+    // at once (151936 logits, top-p: 8 rows 24 us with 16 CTAs, 30 with 8; 16
+    // rows 41 and 31).
     int cs = 1;
     while (cs < (a.rows <= 14 ? kMaxCluster : 8) && a.V > int64_t(cs) * 4096) cs *= 2;
     const int64_t chunk = ((a.V + cs - 1) / cs + 7) / 8 * 8;

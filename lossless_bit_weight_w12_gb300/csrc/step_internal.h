@@ -126,6 +126,6 @@ struct SampleArgs {
     int32_t keep_w;     // and so do its weights
     int32_t vec;        // 16-byte loads: every chunk starts on a 16-byte boundary
 };
-int launch_sample(SampleArgs &a, int dtype, int sms, void *stream);
+int launch_sample(SampleArgs &a, int dtype, void *stream);
 
 }  // namespace w12
