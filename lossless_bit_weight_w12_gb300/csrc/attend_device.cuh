@@ -25,8 +25,8 @@
 // worker that finishes a unit's last segment adds them up.  With results of
 // the tensor-memory kernel a join kernel does: 40 KB and more per unit, which
 // one worker takes three times as long to fetch as a whole kernel (128
-// requests under a prefix: 42 us against 13).  All sums have a fixed order: the outputs do not
-// depend on timing.
+// requests under a prefix: 42 us against 13).  All sums have a fixed order:
+// the outputs do not depend on timing.
 #pragma once
 
 #include "async_common.cuh"

@@ -23,6 +23,12 @@
 // query rows is 8 wide and not 16 (48 query heads over 8 key heads make 6
 // rows a token); P^T is turned between the two by movmatrix.
 //
+// What bounds it: the cache stream for long contexts -- one request of 131000
+// keys, 8 key heads, e4m3 (277 MB): 55 us, of which 44 stream at 6.3 TB/s --
+// and for short ones the fixed parts: plan, first tile, the four warps' sums,
+// the add-up of partial results, 2 - 3 us each (4 requests of 300 .. 2500
+// keys, bf16: 13.6 us for 23 MB).
+//
 // e4m3 tiles stay 8 bits wide up to the registers: codes are exact in fp16,
 // so both products run in fp16; the query row is scaled by a power of two to
 // below 2 (its bf16 values then lose nothing that matters: what is 2^-14 of

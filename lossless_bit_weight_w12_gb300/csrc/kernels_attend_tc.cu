@@ -17,7 +17,9 @@
 // While one slot's warps work on S the tensor cores work for the other.  128
 // keys a tile, because a product of N = 64 takes nearly as long as one of N =
 // 128 (about 45 and 64 cycles), and because every hand-over between the warps
-// and the tensor cores costs some 200 cycles.  The issuing thread orders the
+// and the tensor cores costs some 300 cycles (in halves of 64 keys, a slot's
+// next scores ready during its softmax: 77 us against 54 for 8 requests x 16
+// tokens, 105 against 98 under a prefix).  The issuing thread orders the
 // products of its slot: S of tile i + 1 overwrites P of tile i after the
 // product that reads it.  Keys and values are separate stages of the ring:
 // the keys' is free as soon as S is there.
@@ -36,6 +38,12 @@
 // are set to zero before the product, and channels that are not finite in
 // rows that only some query rows see are taken out and added by hand.  (The
 // same for weights whose value scale is not finite.)
+//
+// What bounds it: a slot's chain of scores, softmax and product, about 6500
+// cycles for two tiles on e4m3 (the multiplications by the scales) and 3300 on
+// bf16, where the products alone take 2048.  8 requests x 16 tokens of 700 ..
+// 9000 keys, 8 key heads, e4m3: 47 us and 9 for the join, 82 MB; the prefix of
+// 16000 for 128 requests of 48 heads: 78 us on 90 SMs, 50 GFLOP.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
