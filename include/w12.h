@@ -555,7 +555,7 @@ size_t w12_attend_workspace_size(const w12_kv *kv, int64_t R, int64_t T, int q_h
  *   out_dev: bf16, token stride out_stride (a multiple of 4), 8-byte aligned.
  *   lse_dev: NULL, or fp32 [R * T][q_heads]: log(sum_j exp(scale q . k_j)).
  *   max_len: no kv_len is above it (a longer one records W12_ERR_DEVICE and
- *     is cut there); it only bounds the work.
+ *     is cut there); it only bounds the work.  At most 2^31 - 256.
  *   prefix_len: 0, or the number of leading keys that ALL requests share
  *     (the same rows of the cache, or copies): as far as they fill tiles of
  *     128 keys that every token sees, they are read once for the whole
