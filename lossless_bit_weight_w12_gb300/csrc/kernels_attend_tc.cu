@@ -425,6 +425,15 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
                 const int from = masked ? max(all_see - key0 + 1, 0) : 0, until = max(min(seg.key_end - key0, kKT), from);
                 const uint32_t vb = ops + uint32_t(stage(i, 1)) * uint32_t(C::kHalf);
                 bool odd = false;
+                // The scores come first, for every warp: their product was
+                // issued after that of the slot's tile before, whose values it
+                // had waited for, so the phase before of a values' stage (or
+                // of its scales) is over and the parity below tells this one.
+                // A warp that had not waited for those values would else take
+                // their phase for this tile's, and touch a stage that is being
+                // filled.
+                att_wait(&s_full[slot], n_s++ & 1u, &ctl, a.err);
+                tmem_fence_after();
                 if (masked) {
                     wait_operand(i, 1);
                     const int x0 = TWO ? int(threadIdx.x) : row;
@@ -438,8 +447,6 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     odd = bar_any(TWO ? 1 : 2 + slot, TWO ? 256 : 128, odd);
                 }
-                att_wait(&s_full[slot], n_s++ & 1u, &ctl, a.err);
-                tmem_fence_after();
                 if (warp_valid) {
                     float lift = 0.0f;
                     const uint32_t tk = smem_addr(scales + 2 * i % C::kScaleRing * C::kScales);
