@@ -111,20 +111,18 @@ __host__ __device__ constexpr size_t weights_at(int64_t chunk) {
     return DT == W12_F32 ? 0 : size_t(chunk) * 2;
 }
 
-// A cluster barrier at which only warp 0 has written for other CTAs (the
-// others need not wait until their own writes have gone out).
-__device__ __forceinline__ void sync_sums() {
-    if (threadIdx.x < 32)
+// A cluster barrier at which only the warps with `wrote` (the same in a warp)
+// have written for other CTAs: the others need not wait until their own writes
+// have gone out.
+__device__ __forceinline__ void sync_written(bool wrote) {
+    if (wrote)
         asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     else
         asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// One at which nothing was written for others.
-__device__ __forceinline__ void sync_relaxed() {
-    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+// One at which only warp 0 has.
+__device__ __forceinline__ void sync_sums() { sync_written(threadIdx.x < 32); }
 
 __device__ __forceinline__ u64 umax64(u64 a, u64 b) { return a > b ? a : b; }
 
@@ -1096,7 +1094,9 @@ __global__ void __launch_bounds__(kST, 2) sample_kernel(const __grid_constant__ 
         a.tokens[r] = token;
         if (a.prob) a.prob[r] = prob;
     }
-    sync_relaxed();  // no CTA leaves while another may read its shared memory
+    // No CTA leaves while another may read its shared memory; and CTA 0 counts
+    // the row below for the warp that stored its token, whichever CTA's it is.
+    sync_written(__any_sync(0xFFFFFFFFu, writer));
     if (!a.accept_len || me != 0) return;
     // ---- the last row's cluster applies the acceptance rule
     if (tid == 0) {

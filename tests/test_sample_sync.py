@@ -1,0 +1,43 @@
+"""Hand-overs inside the sampling kernel, read from its source: what one thread
+writes for another is behind a barrier that orders it.  (None of them can be
+provoked reliably on a GPU.)
+"""
+import os
+import re
+
+SOURCE = os.path.join(os.path.dirname(os.path.abspath(__file__)), "..", "lossless_bit_weight_w12_gb300", "csrc",
+                      "kernels_sample.cu")
+
+
+def text():
+    return re.sub(r"//[^\n]*", "", open(SOURCE).read())
+
+
+def body(name):
+    """The body of the function `name`."""
+    s = text()
+    at = s.index("{", re.search(r"\b%s\([^;{]*\{" % name, s).start())
+    depth = 0
+    for i in range(at, len(s)):
+        depth += {"{": 1, "}": -1}.get(s[i], 0)
+        if depth == 0:
+            return s[at:i + 1]
+    raise AssertionError(name)
+
+
+def test_a_drawn_token_is_released_before_the_row_is_counted():
+    """Any thread of the cluster may store the token; CTA 0 then counts the row
+    for the acceptance on that thread's behalf.  The barrier between the two
+    has to release what the storing warp wrote (a fence in CTA 0 orders only
+    what CTA 0 has seen)."""
+    kernel = body("sample_kernel")
+    between = kernel[kernel.index("a.tokens[r] = token"):kernel.index("atomicAdd(a.counter")]
+    call = re.search(r"\b(sync_\w+)\((.*)\);", between)
+    if not call:
+        assert "cl.sync()" in between
+        return
+    arrive = body(call.group(1))
+    assert "barrier.cluster.arrive.release" in arrive and "barrier.cluster.wait.acquire" in arrive
+    if "barrier.cluster.arrive.relaxed" in arrive:  # only for warps without the storing thread
+        assert re.search(r"if \(wrote\)\s*asm volatile\(\"barrier\.cluster\.arrive\.release", arrive)
+        assert "__any_sync" in call.group(2) and "writer" in call.group(2)
