@@ -687,6 +687,7 @@ __device__ __forceinline__ u64 window_threshold(SampleSmall &sh, SampleCut &cut,
     // many of one weight: bins over their composites
 #pragma unroll 1
     while (m > 128u) {
+        __syncthreads();  // all have read the count that is reset below
         u64 c[4], top = 0, bottom = ~0ull;
         uint32_t id[4];
 #pragma unroll

@@ -41,3 +41,32 @@ def test_a_drawn_token_is_released_before_the_row_is_counted():
     if "barrier.cluster.arrive.relaxed" in arrive:  # only for warps without the storing thread
         assert re.search(r"if \(wrote\)\s*asm volatile\(\"barrier\.cluster\.arrive\.release", arrive)
         assert "__any_sync" in call.group(2) and "writer" in call.group(2)
+
+
+def test_the_count_of_gathered_tokens_is_read_before_its_reset():
+    """In window_threshold all threads read list_n and branch on it, and thread
+    0 resets it for the next turn: a warp that read late would see 0, leave the
+    loop and meet other barriers than its CTA.  Walks the function's statements
+    in their order, the loop's twice: between a read and the next write of
+    list_n there is a barrier."""
+    b = body("window_threshold")
+    loop = b.index("while (m > 128u)")
+    start = b.index("{", loop)
+    depth, end = 0, start
+    for end in range(start, len(b)):
+        depth += {"{": 1, "}": -1}.get(b[end], 0)
+        if depth == 0:
+            break
+    run = b[:end] + b[start:end] + b[end:]
+    events = re.findall(r"__syncthreads\(\)|boundary_bin\(|m = sh\.list_n|sh\.list_n = 0u|atomicAdd\(&sh\.list_n", run)
+    assert events.count("m = sh.list_n") == 3 and events.count("sh.list_n = 0u") == 3
+    read = False
+    for e in events:
+        if e in ("__syncthreads()", "boundary_bin("):  # (boundary_bin begins and ends with one)
+            read = False
+        elif e == "m = sh.list_n":
+            read = True
+        else:
+            assert not read, e
+    bin_body = body("boundary_bin")
+    assert bin_body.lstrip("{ \n").split(";")[1].strip() == "__syncthreads()"
