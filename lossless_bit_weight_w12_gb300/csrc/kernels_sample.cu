@@ -123,6 +123,10 @@ __device__ __forceinline__ void sync_written(bool wrote) {
 }
 // One at which only warp 0 has.
 __device__ __forceinline__ void sync_sums() { sync_written(threadIdx.x < 32); }
+// One in two halves, for the cluster's start: another CTA's shared memory may be
+// touched only once that CTA runs.
+__device__ __forceinline__ void cluster_here() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_started() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ u64 umax64(u64 a, u64 b) { return a > b ? a : b; }
 
@@ -757,6 +761,7 @@ __global__ void __launch_bounds__(kST, 2) sample_kernel(const __grid_constant__ 
     const int cs = int(cl.num_blocks()), me = int(cl.block_rank());
     const int64_t r = int64_t(blockIdx.x) / cs;
     constexpr int ES = DT == W12_F32 ? 4 : 2, VE = 16 / ES;
+    cluster_here();  // (its wait is behind the row's loads)
     pdl_launch_dependents();
     pdl_wait_previous();
 
@@ -822,6 +827,7 @@ __global__ void __launch_bounds__(kST, 2) sample_kernel(const __grid_constant__ 
         for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
         if (lane == 0) sh.warp_top[warp] = m;
         __syncthreads();
+        cluster_started();
         if (tid < cs) {
             for (int w = 0; w < kSW; ++w) m = fmaxf(m, sh.warp_top[w]);
             cl.map_shared_rank(&sh, tid)->top[me] = m;

@@ -70,3 +70,15 @@ def test_the_count_of_gathered_tokens_is_read_before_its_reset():
             assert not read, e
     bin_body = body("boundary_bin")
     assert bin_body.lstrip("{ \n").split(";")[1].strip() == "__syncthreads()"
+
+
+def test_all_ctas_have_started_before_the_first_remote_access():
+    """Another CTA's shared memory may be touched only once that CTA has
+    started: behind a barrier of the whole cluster."""
+    kernel = body("sample_kernel")
+    first = kernel.index("map_shared_rank")
+    barriers = [kernel.find(x) for x in ("cl.sync()", "sync_sums()", "sync_written(", "cluster_started()")]
+    barriers = [x for x in barriers if x >= 0]
+    assert barriers and min(barriers) < first
+    assert kernel.index("cluster_here()") < kernel.index("cluster_started()") < first
+    assert "barrier.cluster.arrive" in body("cluster_here") and "barrier.cluster.wait" in body("cluster_started")
