@@ -221,7 +221,11 @@ __device__ __forceinline__ AttPlan att_plan(const AttendArgs &a, AttShared &sh, 
         }
         if (lane == 31) sh.cum[a.R] = x;
         x -= sum;
-        const bool tell = a.join && a.self != kLinePrefix && blockIdx.x == 0;  // the join kernel
+        // For the join kernel: by one CTA, the requests' part by their kernel,
+        // the prefix's workers by its own (the share is float arithmetic, which
+        // another compilation may round differently).
+        const bool tells = a.join && blockIdx.x == 0, tell = tells && a.self != kLinePrefix;
+        const bool tell_prefix = tells && a.self == kLinePrefix;
         if (lane == 31 && tell) a.plan[3 + a.R] = x + sum;
         for (int r = r0; r < r1; ++r) {
             sh.cum[r] = x;
@@ -235,7 +239,7 @@ __device__ __forceinline__ AttPlan att_plan(const AttendArgs &a, AttShared &sh, 
                 const int gp = att_tc_grid(att_prefix_sms(a, w, all), a.line[kLinePrefix].rt,
                                            a.heads * a.line[kLinePrefix].pu, a.heads * a.line[kLinePrefix].pu * w);
                 g = a.self == kLinePrefix ? gp : min(g, (a.sms - gp) * (a.line[kLineRequests].grid ? 1 : 2));
-                if (tell) a.plan[1] = gp;
+                if (tell_prefix) a.plan[1] = gp;
             }
             if (a.self == kLineRequests) g = att_tc_grid(g, ln.rt, a.heads * a.R * ln.su, a.heads * ln.su * all);
             sh.w = w;
