@@ -556,12 +556,13 @@ size_t w12_attend_workspace_size(const w12_kv *kv, int64_t R, int64_t T, int q_h
  *   lse_dev: NULL, or fp32 [R * T][q_heads]: log(sum_j exp(scale q . k_j)).
  *   max_len: no kv_len is above it (a longer one records W12_ERR_DEVICE and
  *     is cut there); it only bounds the work.  At most 2^31 - 256.
- *   prefix_len: 0, or the number of leading keys that ALL requests share
- *     (the same rows of the cache, or copies): as far as they fill tiles of
- *     128 keys that every token sees, they are read once for the whole
- *     batch, through request 0's table.  Every request's row of the table
- *     names all of its pages, the prefix's among them.  Not tied to page
- *     boundaries.
+ *   prefix_len: 0, or the number of leading keys that all requests with keys
+ *     share (the same rows of the cache, or copies): as far as they fill tiles
+ *     of 128 keys that every token of these requests sees, they are read once
+ *     for the whole batch, through the first such request's row of the table.
+ *     Each such request's row names all of its pages, the prefix's among
+ *     them.  Not tied to page boundaries.  A request with kv_len <= 0 (an
+ *     idle slot) takes no part: its row and its queries may hold anything.
  * A token that sees no key (a padding token, kv_len = 0) gives zeros and
  * lse = -infinity.  Keys past a token's position, rows past kv_len and pages
  * not named by the table never reach a result, whatever they hold.  Scores,

@@ -5,7 +5,8 @@
 // i, G = query heads per key head; a request's rows are consecutive.  A unit
 // is a block of rt query rows of one head against one stretch of keys:
 //  - prefix unit p < pu: rows [p rt, (p + 1) rt) of ALL requests against the
-//    keys of the prefix, read once through request 0's table;
+//    keys of the prefix, read once through the table of the first request that
+//    has keys (rows of requests without any are computed and left out later);
 //  - request unit (r, s), s < su: rows s rt .. of request r against its own
 //    keys.
 // Up to two launches ("lines") share the keys: the prefix's first W tiles of
@@ -56,7 +57,7 @@ struct AttSeg {
 struct AttShared {
     int lens[kAttMaxR];
     int cum[kAttMaxR + 1];  // tiles of the requests before r, one row block each
-    int w, grid;
+    int w, grid, source;
     AttSeg first[2];        // the CTA's workers' first positions
 };
 
@@ -66,7 +67,9 @@ __device__ __forceinline__ int att_len(const AttendArgs &a, int n) {
     return n < 0 ? 0 : n > cap ? cap : n;
 }
 
-// W: the prefix's tiles of 128 keys that are read once for all requests.
+// W: the prefix's tiles of 128 keys that are read once for all requests;
+// shortest: of the lengths above 0 (a request without keys, such as an idle
+// slot of a fixed batch, does not part the prefix), or 0.
 __device__ __forceinline__ int att_prefix_whole(const AttendArgs &a, int shortest) {
     return a.line[kLinePrefix].grid ? min(a.prefix, max(shortest - a.T + 1, 0)) / kAttTcTile : 0;
 }
@@ -90,6 +93,7 @@ __device__ __forceinline__ int att_owner(int total, int grid, int t) {
 
 struct AttPlan {
     int w;         // the prefix's shared tiles
+    int source;    // the request whose table they are read through
     int grid;      // workers of this line
     int np;        // tiles of a prefix unit of this line
     int per_head;  // tiles of a head
@@ -128,10 +132,12 @@ __device__ __forceinline__ int att_tc_grid(int grid, int rt, int units, int tile
     return min(grid, max(units, (tiles + few - 1) / few));
 }
 
-// Fills in what follows from (head, req, block) for the unit's tile k.
+// Fills in what follows from (head, req, block) -- under the prefix from (head,
+// block) -- for the unit's tile k.
 __device__ __forceinline__ void att_unit_at(const AttendArgs &a, const AttPlan &p, const AttShared &sh, AttSeg &s, int k) {
     const AttendLine &ln = a.line[a.self];
     if (a.self == kLinePrefix) {
+        s.req = p.source;
         s.unit = s.head * ln.pu + s.block;
         s.row0 = s.block * ln.rt;
         s.nrows = min(ln.rt, a.rows - s.row0);
@@ -160,7 +166,6 @@ __device__ __forceinline__ AttSeg att_locate(const AttendArgs &a, const AttPlan 
     AttSeg s;
     s.head = t / p.per_head;
     int w = t - s.head * p.per_head, n = p.np;
-    s.req = 0;
     if (a.self != kLinePrefix) {
         int lo = 0, hi = a.R;  // the last request with cum <= w / su
         const int x = w / ln.su;
@@ -204,9 +209,12 @@ __device__ __forceinline__ AttPlan att_plan(const AttendArgs &a, AttShared &sh, 
     if (threadIdx.x < 32) {
         int w = 0;
         if (a.line[kLinePrefix].grid) {
-            int shortest = 0x7FFFFFFF;
-            for (int r = lane; r < a.R; r += 32) shortest = min(shortest, sh.lens[r]);
-            w = att_prefix_whole(a, __reduce_min_sync(0xFFFFFFFFu, shortest));
+            int shortest = 0x7FFFFFFF, source = 0x7FFFFFFF;
+            for (int r = lane; r < a.R; r += 32)
+                if (sh.lens[r] > 0) shortest = min(shortest, sh.lens[r]), source = min(source, r);
+            shortest = __reduce_min_sync(0xFFFFFFFFu, shortest), source = __reduce_min_sync(0xFFFFFFFFu, source);
+            w = att_prefix_whole(a, source < a.R ? shortest : 0);
+            if (lane == 0) sh.source = source;
         }
         // a lane's requests are neighbours
         const int per = (a.R + 31) / 32, r0 = lane * per, r1 = min(r0 + per, a.R);
@@ -250,6 +258,7 @@ __device__ __forceinline__ AttPlan att_plan(const AttendArgs &a, AttShared &sh, 
     __syncthreads();
     AttPlan p;
     p.w = sh.w;
+    p.source = sh.source;  // (only looked at under a prefix)
     p.grid = sh.grid;
     p.np = a.self == kLinePrefix ? p.w : 0;
     p.per_head = a.self == kLinePrefix ? ln.pu * p.np : ln.su * sh.cum[a.R];

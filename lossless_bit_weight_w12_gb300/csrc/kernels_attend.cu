@@ -754,7 +754,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
             const size_t at = size_t(u + c + e0) * lq.rt + in_req;
             att_add<D, true, kJC, 2>(lq.part_ml + at, lq.part_o + at * D + d0, lq.rt, e1 - e0, m, l, acc);
         }
-        if (np > 0) {
+        if (np > 0 && att_len(a, a.kv_len[r]) > 0) {  // (a request without keys has no prefix either)
             const int b = rho / lp.rt, up = head * lp.pu + b;
             att_segments(gp, a.heads * lp.pu * np, up * np, np, c, n);
             n *= lp.halves;
