@@ -120,8 +120,9 @@ __device__ __forceinline__ void append_row(const AppendArgs &a, const AppendLane
     uint32_t top = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(y[j]) & 0x7FFFFFFFu);
-    const float amax = __uint_as_float(__reduce_max_sync(ln.group, top));
-    const bool bad = !(amax <= 3.0e38f), some = amax > kTinyRow && !bad;
+    top = __reduce_max_sync(ln.group, top);
+    const float amax = __uint_as_float(top);
+    const bool bad = top >= 0x7F800000u, some = amax > kTinyRow && !bad;
     const float inv = some ? __fdiv_rn(kE4m3Max, amax) : 0.0f;
     uint32_t w[4];
 #pragma unroll
