@@ -169,7 +169,8 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
         if (hd < rows) raw[i] = load_raw<XT>(source(hd));
     }
     const uint32_t r = tok / uint32_t(a.T);
-    const int pos = a.kv_len[r] - a.T + int(tok - r * uint32_t(a.T));
+    // (a negative length counts as 0: all its tokens are padding)
+    const int pos = max(a.kv_len[r], 0) - a.T + int(tok - r * uint32_t(a.T));
     if (pos < 0) return;
     const int64_t col = int64_t(pos) >> a.page_log2;
     const int32_t pg = col < a.table_cols ? a.table[r * a.table_cols + col] : -1;

@@ -39,3 +39,24 @@ def test_largest_finite_rows_e4m3(dev, w12mod, bf16):
         assert fine.tolist() == [True] * 5 + [False] * 2
         assert np.all(np.abs(got[fine] - want[fine]) <= (2.0 ** -8 + 2.0 ** -20) * np.abs(want[fine]))
         assert np.all(np.isnan(got[~fine]))
+
+
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+def test_any_negative_length_is_padding(dev, w12mod, e4m3):
+    """A request whose length is far below 0 has only padding tokens."""
+    import torch
+    T, dim = 3, 64
+    lens = np.array([-1, -(1 << 31), 3 - (1 << 31), 0, 3], dtype=np.int32)
+    n = len(lens) * T
+    kv = w12mod.KVCache.alloc(8, 1, dim, 16, w12mod.KV_E4M3 if e4m3 else w12mod.KV_BF16, dev)
+    for t in (kv.k, kv.v):
+        t.view(torch.uint8).fill_(0)
+    x = torch.ones((n, 3, dim), dtype=torch.bfloat16, device=dev)
+    q = torch.full((n, 1, dim), -3.0, dtype=torch.bfloat16, device=dev)
+    table = _dev(np.arange(len(lens), dtype=np.int32)[:, None].copy(), dev)
+    rope = _dev(w12mod.rope_table(64, 8), dev)
+    err = torch.zeros(1, dtype=torch.int32, device=dev)
+    w12mod.kv_append(kv, x[:, :1], x[:, 1:2], x[:, 2:], table, _dev(lens, dev), T, q, rope, err_dev=err)
+    assert int(err.item()) == 0
+    assert bool((q[:-T] == -3.0).all()) and bool((q[-T:, 0, 63] == 1.0).all())
+    assert int((kv.v.view(torch.uint8).flatten(1) != 0).any(-1).sum()) == 1
