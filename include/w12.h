@@ -605,6 +605,7 @@ size_t w12_sample_workspace_size(int64_t R, int64_t T, int64_t V);
  *   tokens_dev[row] = the first index, in index order, at which the sum of the
  *     staying weights W passes u W; prob_dev[row] (may be NULL) = its w / W.
  *   t <= 0 (or NaN): the lowest index of the largest logit, probability 1.
+ *   (0 < t < 2^-128, where 1 / t is no fp32 number, counts as 2^-128.)
  *   A row without a logit above -infinity, or whose tokens min_p > 1 all
  *   removes: token -1, probability 0.
  * The sums are whole numbers, so a result does not depend on how a row is

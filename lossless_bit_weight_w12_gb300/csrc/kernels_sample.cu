@@ -880,7 +880,9 @@ __global__ void __launch_bounds__(kST, 2) sample_kernel(const __grid_constant__ 
             prob = 1.0f;
         }
     } else {
-        row.inv_t = __fdiv_rn(1.0f, t);
+        // finite for the smallest t, too: 0 (the largest logit's distance) times
+        // infinity would be NaN
+        row.inv_t = fminf(__fdiv_rn(1.0f, t), 3.402823466e38f);
         bool done = false;
         u64 thr = 0;
         if (CUT && few) {
