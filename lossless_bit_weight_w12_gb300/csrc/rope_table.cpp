@@ -2,13 +2,13 @@
 // precision: a model makes it once, and the angle p * f keeps its low bits at
 // any position (an fp32 product is off by 2^-24 of a large angle).
 #include <cmath>
-#include <vector>
 
 #include "../../include/w12.h"
 
 namespace {
 
 constexpr double kPi = 3.14159265358979323846;
+constexpr int kPairs = 512;  // channel pairs at a time: their frequencies are on the stack
 
 double clamp01(double x) { return x < 0.0 ? 0.0 : x > 1.0 ? 1.0 : x; }
 
@@ -29,8 +29,7 @@ extern "C" int w12_rope_table(int64_t positions, int rot, double base, const w12
     if (!table) return W12_ERR_ARG;
 
     const int half = rot / 2;
-    std::vector<double> f(half);
-    double amp = 1.0, b = base, j0 = 0.0, j1 = 0.0;
+    double f[kPairs], amp = 1.0, b = base, j0 = 0.0, j1 = 0.0;
     if (mode == W12_ROPE_SCALE_BASE) b = base * std::pow(sc->factor, double(rot) / double(rot - 2));
     if (mode == W12_ROPE_SCALE_YARN) {
         // channel pair that makes t turns over the original length
@@ -42,23 +41,27 @@ extern "C" int w12_rope_table(int64_t positions, int rot, double base, const w12
         if (j1 <= j0) j1 = j0 + 0.001;
         amp = sc->attention > 0.0 ? sc->attention : 0.1 * std::log(sc->factor) + 1.0;
     }
-    for (int j = 0; j < half; ++j) {
-        double v = std::pow(b, -2.0 * j / rot);
-        if (mode == W12_ROPE_SCALE_LINEAR) v /= sc->factor;
-        if (bands) {
-            const double g = mode == W12_ROPE_SCALE_BANDS
-                                 ? clamp01((sc->original * v / (2.0 * kPi) - sc->low) / (sc->high - sc->low))
-                                 : 1.0 - clamp01((j - j0) / (j1 - j0));
-            v = v * g + v / sc->factor * (1.0 - g);
+    for (int first = 0; first < half; first += kPairs) {
+        const int n = half - first < kPairs ? half - first : kPairs;
+        for (int i = 0; i < n; ++i) {
+            const int j = first + i;
+            double v = std::pow(b, -2.0 * j / rot);
+            if (mode == W12_ROPE_SCALE_LINEAR) v /= sc->factor;
+            if (bands) {
+                const double g = mode == W12_ROPE_SCALE_BANDS
+                                     ? clamp01((sc->original * v / (2.0 * kPi) - sc->low) / (sc->high - sc->low))
+                                     : 1.0 - clamp01((j - j0) / (j1 - j0));
+                v = v * g + v / sc->factor * (1.0 - g);
+            }
+            f[i] = v;
         }
-        f[j] = v;
-    }
 #pragma omp parallel for schedule(static)
-    for (int64_t p = 0; p < positions; ++p) {
-        float *t = table + p * rot;
-        for (int j = 0; j < half; ++j) {
-            t[j] = float(std::cos(double(p) * f[j]) * amp);
-            t[half + j] = float(std::sin(double(p) * f[j]) * amp);
+        for (int64_t p = 0; p < positions; ++p) {
+            float *t = table + p * rot + first;
+            for (int i = 0; i < n; ++i) {
+                t[i] = float(std::cos(double(p) * f[i]) * amp);
+                t[half + i] = float(std::sin(double(p) * f[i]) * amp);
+            }
         }
     }
     return W12_OK;
