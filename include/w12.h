@@ -567,10 +567,12 @@ size_t w12_attend_workspace_size(const w12_kv *kv, int64_t R, int64_t T, int q_h
  * lse = -infinity.  Keys past a token's position, rows past kv_len and pages
  * not named by the table never reach a result, whatever they hold.  Scores,
  * the running maximum and sums are fp32; the weights of the second product
- * are rounded to bf16 (bf16 cache) or fp16 (e4m3 cache).  The order of every
- * sum is fixed by the arguments, the lengths and the GPU's SM count, so
- * repeated calls give identical bits.  head_dim 64 or 128; 1 <= R <=
- * W12_ATTEND_MAX_R; q_heads a multiple of kv->heads.
+ * are rounded to bf16 (bf16 cache) or, times their value's scale, to fp16
+ * (e4m3 cache; fp16 ends at 2^-24, so a weight times its scale is kept down to
+ * 2^-31 of the row's largest weight times the largest value scale it sees).
+ * The order of every sum is fixed by the arguments, the lengths and the GPU's
+ * SM count, so repeated calls give identical bits.  head_dim 64 or 128; 1 <= R
+ * <= W12_ATTEND_MAX_R; q_heads a multiple of kv->heads.
  * Errors: W12_ERR_ARG, W12_ERR_SHAPE, W12_ERR_ALIGN, W12_ERR_WORKSPACE,
  * W12_ERR_CUDA.  Device errors in word 0 of ws: W12_ERR_DEVICE (a length
  * above max_len or the table, a page outside the cache, which reads as page

@@ -460,9 +460,10 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_kernel(const __grid_
                         ldsm4t(vf[Q8 ? 0 : b], tile_at<D, Q8>(vb, kw + r0 + 8 * (mat >> 1), 2 * b + (mat & 1)));
                 }
             };
-            if (whole) load_v();
             float kscale[2] = {1.0f, 1.0f}, vscale[2] = {1.0f, 1.0f};
-            float lift = 0.0f;  // e4m3: e - 7 for value scales below 2^e
+            float lift[NR][2];  // e4m3: e - 7 for value scales below 2^e
+#pragma unroll
+            for (int n = 0; n < NR; ++n) lift[n][0] = lift[n][1] = 0.0f;
             if (Q8) {
                 const uint32_t sb = kb + uint32_t(C::kScaleOff) + uint32_t(kw + g8) * 4u;
                 uint32_t top = 0u;
@@ -475,7 +476,33 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_kernel(const __grid_
                     // (a NaN scale makes the rows that see the key NaN by itself)
                     if (vscale[h] <= 3.0e38f) top = max(top, __float_as_uint(vscale[h]));
                 }
-                lift = exp_above(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, top))) - 7.0f;
+                const float all = exp_above(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, top))) - 7.0f;
+#pragma unroll
+                for (int n = 0; n < NR; ++n) lift[n][0] = lift[n][1] = all;
+            }
+            if (whole) {
+                load_v();
+            } else if (Q8 && min(key0 + 15, seg.key_end - 1) > min_pos) {
+                // keys that some row does not see: each row's bound is of the
+                // scales that it sees (the same, as a rule, for all rows)
+                float common = 0.0f, top[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    top[h] = vscale[h] <= 3.0e38f ? vscale[h] : 0.0f;
+                    if (key0 + 8 * h + g8 <= min_pos) common = fmaxf(common, top[h]);
+                }
+                common = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(common)));
+                if (exp_above(common) - 7.0f != lift[0][0]) {
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            float x = fmaxf(key0 + g8 <= pos[n][c] ? top[0] : 0.0f, key0 + 8 + g8 <= pos[n][c] ? top[1] : 0.0f);
+#pragma unroll
+                            for (int off = 4; off <= 16; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, off));
+                            lift[n][c] = exp_above(x) - 7.0f;
+                        }
+                }
             }
             // ---- mask, running maximum, weights
             float pw[NR][4];
@@ -502,7 +529,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_kernel(const __grid_
                     for (int c = 0; c < 2; ++c) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xFFFFFFFFu, mx[c], off));
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const float mn = fmaxf(m_run[n][c], mx[c] + lift);
+                    const float mn = fmaxf(m_run[n][c], mx[c] + lift[n][c]);
                     const float mu = mn == kNegInf ? 0.0f : mn;  // a row without keys so far
                     alpha[n][c] = ex2(m_run[n][c] - mu);
                     moved = moved || m_run[n][c] != mn;

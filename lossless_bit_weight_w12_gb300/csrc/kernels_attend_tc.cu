@@ -224,6 +224,26 @@ __device__ __noinline__ void clear_weights(const float *vsc, int from, int to, i
     }
 }
 
+// e4m3: as `lift`, which the converters make of all value scales of a tile, but
+// of those that the lane's row sees (r <= seen; before `from`: all rows), so
+// that a later token's do not reach it.  It is the same, as a rule, for all rows.
+// vsc: where the scales are.
+__device__ __noinline__ float seen_lift(uint32_t vsc, float lift, int from, int until, int seen) {
+    const auto bits = [](uint32_t x) { return __uint_as_float(x) <= 3.0e38f ? x : 0u; };
+    const int mine = 4 * int(threadIdx.x & 31);
+    const uint4 y = lds128(vsc + 4u * uint32_t(mine));
+    uint32_t top = max(max(mine < from ? bits(y.x) : 0u, mine + 1 < from ? bits(y.y) : 0u),
+                       max(mine + 2 < from ? bits(y.z) : 0u, mine + 3 < from ? bits(y.w) : 0u));
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if (exp_above(__uint_as_float(top)) - 7.0f == lift) return lift;
+#pragma unroll 1
+    for (int r = from; r < until; ++r) {
+        const uint32_t x = bits(lds32(vsc + 4u * uint32_t(r)));
+        if (r <= seen) top = max(top, x);
+    }
+    return exp_above(__uint_as_float(top)) - 7.0f;
+}
+
 // Zeros in their place; part `me` of n of the work.
 template <int D, bool Q8>
 __device__ __noinline__ void clear_odd(uint32_t stage, int from, int to, int me, int n) {
@@ -483,6 +503,9 @@ __global__ void __launch_bounds__(Q8 ? 512 : 384, 1) attend_tc_kernel(const __gr
                         });
                         att_wait(&vs_full[i % (C::kScaleRing / 2)], uint32_t(i / (C::kScaleRing / 2)) & 1u, &ctl, a.err);
                         lift = __uint_as_float(lds32(tv + uint32_t(kKT) * 4u));
+                        // keys that only some rows see (out of line: the loop
+                        // has to stay in the instruction cache)
+                        if (__builtin_expect(masked && from < until, 0)) lift = seen_lift(tv, lift, from, until, seen);
                         top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc + lift;
                         tmem_wait_st();
                     } else {
