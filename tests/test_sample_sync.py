@@ -25,22 +25,27 @@ def body(name):
     raise AssertionError(name)
 
 
-def test_a_drawn_token_is_released_before_the_row_is_counted():
-    """Any thread of the cluster may store the token; CTA 0 then counts the row
-    for the acceptance on that thread's behalf.  The barrier between the two
-    has to release what the storing warp wrote (a fence in CTA 0 orders only
-    what CTA 0 has seen)."""
+def test_a_drawn_token_is_stored_before_the_row_is_counted():
+    """Any thread of the cluster may store the token.  Counting the row for the
+    acceptance has to be ordered after that store: by the storing thread itself,
+    with a fence, or behind a barrier that releases what its warp wrote (a fence
+    in CTA 0 orders only what CTA 0 has seen)."""
     kernel = body("sample_kernel")
     between = kernel[kernel.index("a.tokens[r] = token"):kernel.index("atomicAdd(a.counter")]
+    by_itself = re.search(r"if \(writer\) \{\s*__threadfence\(\);\s*sh\.last = $", between)
     call = re.search(r"\b(sync_\w+)\((.*)\);", between)
-    if not call:
-        assert "cl.sync()" in between
-        return
-    arrive = body(call.group(1))
-    assert "barrier.cluster.arrive.release" in arrive and "barrier.cluster.wait.acquire" in arrive
-    if "barrier.cluster.arrive.relaxed" in arrive:  # only for warps without the storing thread
-        assert re.search(r"if \(wrote\)\s*asm volatile\(\"barrier\.cluster\.arrive\.release", arrive)
-        assert "__any_sync" in call.group(2) and "writer" in call.group(2)
+    released = "cl.sync()" in between
+    if call and not by_itself:
+        arrive = body(call.group(1))
+        released = "arrive.release" in arrive and (
+            "arrive.relaxed" not in arrive or "writer" in call.group(2) and "__any_sync" in call.group(2))
+    assert by_itself or released
+    # the CTA of the storing thread goes on: its flag is reset in every CTA, and read behind a barrier
+    if by_itself:
+        assert kernel.index("if (tid == 0) sh.last = 0;") < kernel.index("cluster_started()")
+        rest = kernel[kernel.index("atomicAdd(a.counter"):]
+        assert rest.index("__syncthreads()") < rest.index("if (!sh.last) return;") < rest.index("__threadfence()")
+        assert "me != 0" not in rest[:rest.index("a.accept_len[q]")] and "me != 0" not in between
 
 
 def test_the_count_of_gathered_tokens_is_read_before_its_reset():
