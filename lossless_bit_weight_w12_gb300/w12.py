@@ -454,6 +454,16 @@ def _typed_ptr(t, dtype, n: int, what: str):
     return _ptr(t)
 
 
+def _err_ptr(t):
+    """Address of an error word, the first element of an int32 CUDA tensor (None: NULL)."""
+    if t is None:
+        return None
+    import torch
+    if t.dtype is not torch.int32 or t.numel() < 1:
+        raise ValueError("err_dev: expected an int32 tensor")
+    return _ptr(t)
+
+
 def rope_table(positions: int, rot: int, base: float = 10000.0, mode: int = ROPE_SCALE_NONE, factor: float = 1.0,
                original: float = 0.0, low: float = 1.0, high: float = 32.0, attention: float = 0.0) -> np.ndarray:
     """w12_rope_table: float32 [positions, rot], cosines then sines (host)."""
@@ -485,7 +495,7 @@ def kv_append(kv: KVCache, q, k, v, block_table, kv_len, T: int, q_out, table=No
                              _typed_ptr(block_table, torch.int32, R * blocks, "block_table"), blocks,
                              _typed_ptr(kv_len, torch.int32, R, "kv_len"),
                              _typed_ptr(table, torch.float32, positions * rot, "table"), positions, rot, layout, op,
-                             os_, _ptr(err_dev), _stream_of(q, stream))
+                             os_, _err_ptr(err_dev), _stream_of(q, stream))
     if st:
         raise W12Error(st, "w12_kv_append")
 
@@ -501,7 +511,7 @@ def kv_read(kv: KVCache, block_table, cu_len, k_out, v_out, err_dev=None, stream
     if not (k_out.is_contiguous() and v_out.is_contiguous()):
         raise ValueError("outputs: contiguous")
     st = lib().w12_kv_read(kv.ref, _typed_ptr(block_table, torch.int32, R * blocks, "block_table"), blocks,
-                           _typed_ptr(cu_len, torch.int32, R + 1, "cu_len"), R, n, kp, vp, _ptr(err_dev),
+                           _typed_ptr(cu_len, torch.int32, R + 1, "cu_len"), R, n, kp, vp, _err_ptr(err_dev),
                            _stream_of(k_out, stream))
     if st:
         raise W12Error(st, "w12_kv_read")
