@@ -38,8 +38,9 @@ namespace w12 {
 
 constexpr int kAttMaxR = W12_ATTEND_MAX_R;
 
-// rho / G, by the reciprocal: rho * (2^64 / G, rounded up) is too large by less
-// than rho * G < 2^64 / G for rows and heads in range, so the floor is exact.
+// rho / G, by the reciprocal: 2^64 / G rounded up is too large by less than 1,
+// the product over 2^64 by less than rho / 2^64.  The floor is exact where that
+// is below 1 / G, the least distance to the next whole number: rho * G < 2^64.
 __device__ __forceinline__ int att_token(const AttendArgs &a, int rho) {
     return a.G == 1 ? rho : int(__umul64hi(uint64_t(uint32_t(rho)), a.per_g));
 }

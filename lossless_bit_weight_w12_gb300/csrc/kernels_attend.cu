@@ -9,8 +9,8 @@
 // second product rounded to bf16 (bf16 cache) or fp16 (e4m3 cache), as
 // tensor cores take them; l sums the unrounded ones.
 //
-// The register kernel, for few query rows per key head (the cache stream
-// bounds it) and for every tile that needs a mask.  One CTA per SM with two
+// The register kernel, for requests with few query rows per key head (the cache
+// stream bounds it).  One CTA per SM with two
 // workers, each four warps with a ring of key/value tiles of its own and its
 // own piece of the work: while one finishes a segment the other streams.  A
 // warp owns 16 of a tile's 64 keys for all query rows; no warp waits for
@@ -34,9 +34,9 @@
 // below 2 (its bf16 values then lose nothing that matters: what is 2^-14 of
 // the row's largest keeps fewer bits), the key's scale multiplies the score
 // and the value's scale the weight.  m only has to keep the exponentials in
-// range: with value scales below 2^e it is max - 7 + e, so that weights times
-// scales stay below 2^7 and the fp16 they are rounded to is far from both of
-// its ends.
+// range: with the value scales that a row sees below 2^e it is max - 7 + e, so
+// that weights times scales stay below 2^7 and the fp16 they are rounded to is
+// far from both of its ends.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -42,8 +42,9 @@
 // What bounds it: a slot's chain of scores, softmax and product, about 6500
 // cycles for two tiles on e4m3 (the multiplications by the scales) and 3300 on
 // bf16, where the products alone take 2048.  8 requests x 16 tokens of 700 ..
-// 9000 keys, 8 key heads, e4m3: 47 us and 9 for the join, 82 MB; the prefix of
-// 16000 for 128 requests of 48 heads: 78 us on 90 SMs, 50 GFLOP.
+// 9000 keys, 8 key heads: e4m3 (82 MB) 51 us and bf16 (160 MB) 49, each with 9
+// for the join; the prefix of 16000 for 128 requests of 48 heads: 79 us on 90
+// SMs, 50 GFLOP.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

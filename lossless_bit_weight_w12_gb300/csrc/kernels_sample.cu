@@ -34,7 +34,7 @@
 //
 // What bounds it: the steps that wait for one another -- load, weights,
 // counts, window, threshold, draw, each some 2000 cycles of work and a cluster
-// barrier (16 rows of 151936, top-p: 31 us; one row, top-k: 10 us) -- and for
+// barrier (16 rows of 151936, top-p: 30 us; one row, top-k: 10 us) -- and for
 // many rows the instructions of the exact exponential and the 64-bit sums (128
 // rows: 39 us for 78 MB).
 #include <cooperative_groups.h>

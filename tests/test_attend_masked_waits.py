@@ -1,5 +1,5 @@
-"""The waits of the tcgen05 attention kernel's units of 128 rows, with tiles that
-need a mask, on the CPU, for both caches.
+"""The waits of the tcgen05 attention kernel with tiles that need a mask, on the
+CPU, for both caches.
 
 As in test_attend_pipeline_protocol the kernel's roles and the tensor cores run
 as coroutines in random order and waits are by parity.  Here a tile that needs
@@ -7,9 +7,14 @@ a mask has its values looked at by all softmax warps of its slot, those without
 valid rows among them (they skip the softmax, so they run ahead), and on bf16
 the rows past the end are set to zero in the stage the product reads.
 
-Operand stages: bf16, head_dim 128: four in turn, keys 0 and 2, values 1 and 3,
-filled by the copy engine.  e4m3: one for the keys with a full barrier per slot,
-one per slot for the values, filled by converters from an input ring.
+Units of 128 rows: the two slots take alternate tiles.  Operand stages: bf16,
+head_dim 128: four in turn, keys 0 and 2, values 1 and 3, filled by the copy
+engine.  e4m3: one for the keys with a full barrier per slot, one per slot for
+the values, filled by converters from an input ring.
+
+Units of 256 rows: both slots use every tile, and their issuing threads take
+turns.  Operand stages in turn, four (bf16) or three (e4m3, with an input ring
+of three), keys and values alike.
 
 The order that is checked is the kernel's: whether the wait for a tile's scores
 comes before the wait for its values is read from its source.
@@ -250,10 +255,161 @@ class Blocks:
             if next(r, self) is self:
                 roles.remove(r)
         assert not roles, "no progress"
-        assert sorted(self.result) == list(range(self.tiles))
+        assert sorted(self.result) == self.results()
+
+    def results(self):
+        return list(range(self.tiles))
 
 
-def problem(seed, e4m3, scores_first):
+class Wide(Blocks):
+    """Units of 256 rows."""
+
+    def __init__(self, segments, masked, e4m3, scores_first, seed):
+        super().__init__(segments, masked, e4m3, scores_first, seed)
+        bars = lambda n, arrivals=1: [Bar(arrivals) for _ in range(n)]  # noqa: E731
+        self.operands, self.stages = (3 if e4m3 else 4), 3
+        writers = 2 if e4m3 else 1  # converter warps, each in the order of the tiles
+        self.op_full, self.op_empty = bars(self.operands, writers), bars(self.operands, 2)
+        self.in_empty = bars(self.stages, writers)
+        self.scales_full, self.token = bars(4, writers), bars(2)
+        self.half = [[] for _ in range(self.operands)]
+
+    def stage(self, i, kv):
+        return (2 * i + kv) % self.operands
+
+    def full(self, i, kv):
+        return self.op_full[self.stage(i, kv)], (2 * i + kv) // self.operands
+
+    def turn(self, i, kv):
+        return (2 * i + kv) // self.operands
+
+    def convert(self, warp):
+        if not self.e4m3:
+            return
+        for h in range(2 * self.tiles):
+            i, kv, s = h // 2, h % 2, h % self.stages
+            yield from wait(self.in_full[s], h // self.stages)
+            assert self.ring[s] == (i, kv)
+            if kv:
+                self.value_scales[i % 4] = i
+                self.scales_full[i % 4].arrive()
+            to, turn = self.stage(i, kv), self.turn(i, kv)
+            if turn:
+                yield from wait(self.op_empty[to], turn - 1)
+            if not kv:
+                self.key_scales[i % 4] = i
+            if self.op[to] != ("half", i, kv):
+                self.op[to], self.half[to], self.cleared[to] = ("half", i, kv), [], []
+            yield
+            assert self.ring[s] == (i, kv) and self.op[to] == ("half", i, kv)
+            self.half[to].append(warp)
+            if len(self.half[to]) == 2:
+                self.op[to] = (i, kv)
+            self.op_full[to].arrive()
+            self.in_empty[s].arrive()
+            yield
+
+    def parts(self, slot):
+        t = 0
+        for n in self.segments:
+            yield (t, t + n)
+            t += n
+
+    def softmax(self, slot, valid):
+        tiles = 0
+        for segs, part in enumerate(self.parts(slot)):
+            yield from self.meet(("queries", segs, slot), WARPS)
+            if valid:
+                self.output[slot] = []
+            self.q_full[slot].arrive()
+            for i in range(*part):
+                if self.scores_first:
+                    yield from wait(self.s_full[slot], tiles)
+                if i in self.masked:
+                    bar, phase = self.full(i, 1)
+                    yield from wait(bar, phase)
+                    s = self.stage(i, 1)
+                    assert self.op[s] == (i, 1)
+                    yield
+                    assert self.op[s] == (i, 1)
+                    if self.e4m3:
+                        assert self.value_scales[i % 4] == i
+                    else:
+                        self.cleared[s].append(i)
+                    yield from self.meet(("masked", i), 2 * WARPS)
+                if not self.scores_first:
+                    yield from wait(self.s_full[slot], tiles)
+                tiles += 1
+                if valid:
+                    assert self.scores[slot] == i
+                    yield
+                    if self.e4m3:
+                        assert self.key_scales[i % 4] == i
+                        yield from wait(self.scales_full[i % 4], i // 4)
+                        assert self.value_scales[i % 4] == i
+                        yield
+                        assert self.value_scales[i % 4] == i and self.key_scales[i % 4] == i
+                    self.weights[slot] = i
+                self.p_full[slot].arrive()
+                yield
+            yield from wait(self.o_done[slot], segs)
+            if valid:
+                self.result.extend(self.output[slot])
+            yield
+
+    def issue(self, slot):
+        def scores(i, hand_on):
+            def run():
+                assert self.op[self.stage(i, 0)] == (i, 0)
+                self.scores[slot] = i
+                self.s_full[slot].arrive()
+                self.op_empty[self.stage(i, 0)].arrive()
+            self.products.append(run)
+            if hand_on:
+                self.token[slot ^ 1].arrive()
+
+        def outputs(i):
+            def run():
+                s = self.stage(i, 1)
+                assert self.op[s] == (i, 1) and self.weights[slot] == i
+                if not self.e4m3:
+                    assert self.cleared[s] == ([i] * 2 * WARPS if i in self.masked else [])
+                self.output[slot].append(i)
+                self.op_empty[s].arrive()
+            self.products.append(run)
+
+        tiles = 0
+        for segs, part in enumerate(self.parts(slot)):
+            yield from wait(self.q_full[slot], segs)
+            yield from wait(*self.full(part[0], 0))
+            scores(part[0], False)
+            yield
+            for i in range(*part):
+                more = i + 1 < part[1]
+                yield from wait(*self.full(i, 1))
+                if more and not self.e4m3:
+                    yield from wait(*self.full(i + 1, 0))
+                yield from wait(self.p_full[slot], tiles)
+                tiles += 1
+                if i or slot:
+                    yield from wait(self.token[slot], (2 * i + slot - 1) // 2)
+                outputs(i)
+                if not more:
+                    self.token[slot ^ 1].arrive()
+                yield
+                if more:
+                    if self.e4m3:
+                        yield from wait(*self.full(i + 1, 0))
+                    scores(i + 1, True)
+                else:
+                    self.products.append(self.o_done[slot].arrive)
+                yield
+
+    def results(self):
+        return sorted(list(range(self.tiles)) * 2)
+
+
+def problem(kind, seed, e4m3, scores_first):
     """Segments of a CTA; the last tiles of some of them (a request's newest keys) are masked."""
     r = random.Random(seed)
     segments = [r.choice([1, 1, 2, 3, 4, 5, 9, 16]) for _ in range(r.randrange(1, 6))]
@@ -261,13 +417,14 @@ def problem(seed, e4m3, scores_first):
     for n in segments:
         t += n
         masked |= set(range(t - min(n, r.choice([0, 1, 1, 2])), t))
-    return Blocks(segments, masked, e4m3, scores_first, seed)
+    return kind(segments, masked, e4m3, scores_first, seed)
 
 
 @pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
-def test_masked_tiles_in_the_kernels_order(e4m3):
+@pytest.mark.parametrize("kind", [Blocks, Wide], ids=["128", "256"])
+def test_masked_tiles_in_the_kernels_order(kind, e4m3):
     for seed in range(300):
-        problem(seed, e4m3, kernel_waits_for_scores_first()).run()
+        problem(kind, seed, e4m3, kernel_waits_for_scores_first()).run()
 
 
 @pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
@@ -277,7 +434,7 @@ def test_waiting_for_the_values_first_is_not_safe(e4m3):
     wrong = 0
     for seed in range(300):
         try:
-            problem(seed, e4m3, False).run()
+            problem(Blocks, seed, e4m3, False).run()
         except AssertionError:
             wrong += 1
     assert wrong > 10
