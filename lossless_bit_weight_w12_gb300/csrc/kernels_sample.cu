@@ -854,7 +854,7 @@ __global__ void __launch_bounds__(kST, 2) sample_kernel(const __grid_constant__ 
     uint64_t p_fix = 1ull << 24;
     if (CUT && a.top_p) {
         const float p = rintf(a.top_p[req] * 16777216.0f);
-        if (!(p >= 16777216.0f)) p_fix = p > 0.0f ? uint64_t(p) : 0ull;
+        if (p < 16777216.0f) p_fix = p > 0.0f ? uint64_t(p) : 0ull;  // (a NaN is no cut)
     }
     if (row.mx == -INFINITY) {
         // nothing can be sampled

@@ -45,3 +45,20 @@ def test_infinite_temperature(dev, w12mod):
     c = Call(w12mod, dev, _dev(x, dev), 3, 1, u, [np.inf] * 3)
     assert c.tok.tolist() == [int(live[int(np.floor(float(a) * 2.0 ** 24)) * len(live) >> 24]) for a in u]
     assert np.all(np.abs(c.pr * len(live) - 1.0) <= 2.0 ** -22)
+
+
+@pytest.mark.parametrize("V", [7, 151936])
+def test_parameters_that_are_nan(dev, w12mod, V):
+    """A top_p or min_p that is NaN is no cut (only top_p < 1 and min_p > 0 are
+    one); a temperature that is NaN is the greedy choice."""
+    rng = np.random.default_rng(V)
+    x = _dev(rng.standard_normal((4, V)).astype(np.float32), dev)
+    u = rng.random(4).astype(np.float32)
+    nan = [float("nan")] * 4
+    plain = Call(w12mod, dev, x, 4, 1, u, [1.0] * 4)
+    assert plain.tok.tolist() != np.argmax(x.cpu().numpy(), -1).tolist()
+    for kw in (dict(top_p=nan), dict(min_p=nan), dict(top_p=nan, min_p=nan, top_k=[0] * 4)):
+        c = Call(w12mod, dev, x, 4, 1, u, [1.0] * 4, **kw)
+        assert c.tok.tolist() == plain.tok.tolist() and c.pr.tolist() == plain.pr.tolist(), kw
+    c = Call(w12mod, dev, x, 4, 1, u, nan)
+    assert c.tok.tolist() == np.argmax(x.cpu().numpy(), -1).tolist() and c.pr.tolist() == [1.0] * 4
