@@ -552,7 +552,8 @@ size_t w12_attend_workspace_size(const w12_kv *kv, int64_t R, int64_t T, int q_h
  *   G = q_heads / kv->heads, over the keys j <= position of token n.
  *   q_dev: bf16, token n's heads at q_dev + n * q_stride; 16-byte aligned,
  *     q_stride a multiple of 8.
- *   out_dev: bf16, token stride out_stride (a multiple of 4), 8-byte aligned.
+ *   out_dev: bf16, token stride out_stride (a multiple of 4), 8-byte aligned,
+ *     not overlapping the inputs.
  *   lse_dev: NULL, or fp32 [R * T][q_heads]: log(sum_j exp(scale q . k_j)).
  *   max_len: no kv_len is above it (a longer one records W12_ERR_DEVICE and
  *     is cut there); it only bounds the work.  At most 2^31 - 256.
