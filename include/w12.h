@@ -70,9 +70,10 @@ extern "C" {
 #define W12_LAYOUT_KN 0 /* w[k*N + n]: row-major [K][N]                         */
 #define W12_LAYOUT_NK 1 /* w[n*K + k]: row-major [N][K] (a linear layer's weight) */
 
-/* Element types of y and of logits. */
+/* Element types of y and of logits (and, where a call says so, of x). */
 #define W12_F32 0
 #define W12_BF16 1
+#define W12_E4M3 2 /* 8-bit codes with one fp32 scale per row: value = code * scale */
 
 /* GEMM paths (w12_gemm_ex, w12_gemm_batched_ex).  All three stream the
  * weights' unit blocks with bulk copies (TMA) through a shared-memory ring,
@@ -626,6 +627,51 @@ int w12_sample(const void *logits_dev, int dtype, int64_t R, int64_t T, int64_t 
                const int32_t *top_k_dev, const float *top_p_dev, const float *min_p_dev, const float *u_dev,
                int32_t *tokens_dev, float *prob_dev, const int32_t *draft_dev, int32_t *accept_len_dev,
                int32_t *next_tok_dev, void *ws_dev, size_t ws_bytes, void *stream);
+
+/* --------------------------------------------------------------------- */
+/* Around a draft model                                                  */
+/* --------------------------------------------------------------------- */
+
+/*
+ * The calls from here on serve the other half of speculative decoding, the
+ * draft model: the addition and norm between two products of either model,
+ * products with 4-bit weights (a drafter's weights may lose bits, the
+ * target's verification makes up for them), and the verification of sampled
+ * drafts.  The SpecPilot pages describe none of them; they are this
+ * library's own.  They use programmatic dependent launch as the decode-step
+ * calls do.
+ */
+
+/* Largest row of w12_add_norm. */
+#define W12_NORM_MAX_DIM 32768
+
+/*
+ * Residual addition and root-mean-square norm of `rows` rows of `dim`:
+ *   h = x + delta,  y = h (weight + offset) / sqrt(mean(h^2) + eps).
+ *   x_dev: x_dtype W12_F32 or W12_BF16; delta_dev (NULL: none): delta_dtype
+ *     the same two; row r at x_dev + r * x_stride (elements; any stride).
+ *   weight_dev: [dim] W12_F32 or W12_BF16, NULL: ones.  offset: 0, or 1 for
+ *     models that store weight - 1.
+ *   residual_dev (may be NULL): h in x's type, rounded once; the norm is of
+ *     the unrounded h.  It may be x_dev itself with x's stride, or, where the
+ *     types agree, delta_dev with delta's.
+ *   out_dev: out_dtype W12_BF16, or W12_E4M3 with scale_dev [rows] fp32 (for
+ *     W12_BF16 NULL): scale = amax / 448 of the row's y, codes round(y * (448
+ *     / amax)) (nearest even); a row whose amax is at most 1e-30 is stored as
+ *     zeros with scale 0, one that holds a NaN or an infinity as zeros with
+ *     scale NaN.  Rows of out_dev and residual_dev at their strides, at least
+ *     dim apart.
+ * Pointers are aligned to their elements; rows that start on 16-byte
+ * boundaries with dim a multiple of 8 are read faster.  Other than named,
+ * outputs overlap nothing.  Sums are fp32, in a fixed order; |h (weight +
+ * offset)| is to stay below 3.4e38 for a row to be finite.
+ * 1 <= dim <= W12_NORM_MAX_DIM, 0 <= rows < 2^31, eps >= 0 and finite.
+ * Errors: W12_ERR_ARG, W12_ERR_SHAPE, W12_ERR_ALIGN, W12_ERR_CUDA.
+ */
+int w12_add_norm(const void *x_dev, int64_t x_stride, int x_dtype, const void *delta_dev, int64_t delta_stride,
+                 int delta_dtype, const void *weight_dev, int weight_dtype, float offset, float eps, int64_t rows,
+                 int64_t dim, void *residual_dev, int64_t residual_stride, void *out_dev, int64_t out_stride,
+                 int out_dtype, float *scale_dev, void *stream);
 
 /*
  * Read (and clear) the sticky device error word of a workspace: waits for

@@ -21,12 +21,13 @@ OK = 0
 ERR_ARG, ERR_SHAPE, ERR_ALIGN, ERR_WORKSPACE, ERR_BLOB = 1, 2, 3, 4, 5
 ERR_TOO_MANY_ESCAPES, ERR_CUDA, ERR_TIMEOUT, ERR_DEVICE = 6, 7, 8, 9
 LAYOUT_KN, LAYOUT_NK = 0, 1
-F32, BF16 = 0, 1
+F32, BF16, E4M3 = 0, 1, 2
 PATH_AUTO, PATH_GEMV, PATH_MMA, PATH_TC = 0, 1, 2, 3
 OPT_EARLY_WEIGHTS = 0x100  # OR into a path: weight copies start under the previous kernel's tail
 MAX_M = 128
 ATTEND_MAX_R = 512
 SAMPLE_MAX_V = 524288
+NORM_MAX_DIM = 32768
 KV_BF16, KV_E4M3 = 0, 1
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 ROPE_SCALE_NONE, ROPE_SCALE_LINEAR, ROPE_SCALE_BASE, ROPE_SCALE_BANDS, ROPE_SCALE_YARN = 0, 1, 2, 3, 4
@@ -41,6 +42,7 @@ EXPORTS = (
     "w12_encode_device_workspace_size", "w12_encode_plan_device", "w12_encode_device",
     "w12_gemm_batched_debug", "w12_rope_table", "w12_kv_append", "w12_kv_read",
     "w12_attend_workspace_size", "w12_attend", "w12_sample_workspace_size", "w12_sample",
+    "w12_add_norm",
 )
 
 
@@ -151,6 +153,8 @@ def lib():
         L.w12_sample_workspace_size.restype = SZ
         L.w12_sample_workspace_size.argtypes = [I64, I64, I64]
         L.w12_sample.argtypes = [P, I, I64, I64, I64, P, P, P, P, P, P, P, P, P, P, P, SZ, P]
+        F = ctypes.c_float
+        L.w12_add_norm.argtypes = [P, I64, I, P, I64, I, P, I, F, F, I64, I64, P, I64, P, I64, I, P, P]
         _lib = L
     return _lib
 
@@ -570,6 +574,55 @@ def sample(logits, R: int, T: int, u, tokens_dev, ws_dev, temperature=None, top_
                           _ptr(ws_dev), ws_dev.nbytes, _stream_of(logits, stream))
     if st:
         raise W12Error(st, "w12_sample")
+
+
+# --------------------------------------------- draft model: add and norm
+
+def _dtype_of(t):
+    """F32 or BF16 of a tensor (E4M3: float8_e4m3fn)."""
+    import torch
+    d = t.dtype
+    k = F32 if d is torch.float32 else BF16 if d is torch.bfloat16 else E4M3 if d is torch.float8_e4m3fn else -1
+    if k < 0:
+        raise ValueError(f"expected float32, bfloat16 or float8_e4m3fn, got {d}")
+    return k
+
+
+def _rows_ptr(t, n: int, dim: int, what: str):
+    """(address, row stride) of [n, dim] rows with contiguous elements (None: NULL)."""
+    if t is None:
+        return None, 0
+    if t.shape != (n, dim):
+        raise ValueError(f"{what}: expected [{n}, {dim}], got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    row, one = t.stride()
+    if one != 1 and dim > 1:
+        raise ValueError(f"{what}: expected contiguous rows")
+    return t.data_ptr(), row
+
+
+def add_norm(x, weight, out, delta=None, residual_out=None, eps: float = 1e-6, offset: float = 0.0, scale_out=None,
+             stream=None):
+    """out = rms_norm(x + delta) * (weight + offset), row by row.  x, delta
+    [n, dim] float32 or bfloat16; residual_out (x's type, may be x): x + delta;
+    out bfloat16, or float8_e4m3fn with scale_out float32 [n]; any row strides;
+    weight [dim] float32, bfloat16 or None."""
+    import torch
+    n, dim = x.shape
+    xp, xs = _rows_ptr(x, n, dim, "x")
+    dp, ds = _rows_ptr(delta, n, dim, "delta")
+    rp, rs = _rows_ptr(residual_out, n, dim, "residual_out")
+    op, os_ = _rows_ptr(out, n, dim, "out")
+    if residual_out is not None and residual_out.dtype is not x.dtype:
+        raise ValueError("residual_out: x's type")
+    if weight is not None and weight.numel() != dim:
+        raise ValueError(f"weight: expected {dim} elements")
+    st = lib().w12_add_norm(xp, xs, _dtype_of(x), dp, ds, 0 if delta is None else _dtype_of(delta), _ptr(weight),
+                            0 if weight is None else _dtype_of(weight), offset, eps, n, dim, rp, rs, op, os_,
+                            _dtype_of(out), _typed_ptr(scale_out, torch.float32, n, "scale_out"), _stream_of(x, stream))
+    if st:
+        raise W12Error(st, "w12_add_norm")
 
 
 # --------------------------------------------------------------- helpers
