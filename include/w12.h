@@ -674,6 +674,84 @@ int w12_add_norm(const void *x_dev, int64_t x_stride, int x_dtype, const void *d
                  int out_dtype, float *scale_dev, void *stream);
 
 /*
+ * 4-bit weights.  A K x N matrix (a linear layer's [N][K]) of e2m1 codes with
+ * an e4m3 scale for 16 consecutive k of a column and one fp32 number:
+ *   W[k, n] = code[n, k] scales[n, k / 16] scale,
+ * codes 0, 0.5, 1, 1.5, 2, 3, 4, 6 (bits 2-0) with bit 3 as the sign.  The
+ * plain form has codes [N][K / 2] bytes, the even k in a byte's low four bits,
+ * and scales [N][K / 16] bytes.  The products read a blob: for tile t of 128
+ * columns and group kg of 128 k, unit t * K / 128 + kg is a block of
+ * W12_FP4_UNIT_BYTES:
+ *   [0, 8192)     codes: column c's 64 bytes at 64 c, four 16-byte chunks of
+ *                 four 32-bit words; chunk j at j ^ ((c >> 1) & 3), its word q
+ *                 holds k = 64 (q >> 1) + 16 j + 8 (q & 1) .. + 7: the even k in
+ *                 the low half, the odd ones in the high half; of a half's
+ *                 codes 0 .. 3 the magnitudes at bits 8-6, 5-3, 2-0, 11-9, the
+ *                 signs at 15, 12, 14, 13
+ *   [8192, 9216)  scales: column c's 8 at 8192 + 8 c, that of k / 16 = g at
+ *                 2 (g & 3) + (g >> 2): 5 exponent bits (bias 9), 3 mantissa
+ *                 bits, no sign (a negative scale turns the codes' signs); a zero
+ *                 scale is 0 with zero codes, NaN is 0xAF
+ * Columns past N are zeros.  K is a multiple of 128.
+ */
+#define W12_FP4_UNIT_BYTES 9216
+typedef struct w12_fp4 {
+    const void *blob; /* w12_fp4_bytes(K, N) bytes on the device, 256-byte aligned */
+    int64_t K, N;
+    float scale;      /* in [2^-100, 2^100] */
+    int32_t reserved; /* 0 */
+} w12_fp4;
+
+/* Bytes of a blob (0 for a shape that is not served). */
+size_t w12_fp4_bytes(int64_t K, int64_t N);
+
+/* The blob of a matrix in the plain form (codes_dev 16-byte, scales_dev
+ * 8-byte aligned).  Errors: W12_ERR_ARG, W12_ERR_SHAPE, W12_ERR_ALIGN,
+ * W12_ERR_CUDA. */
+int w12_fp4_pack(const uint8_t *codes_dev, const uint8_t *scales_dev, int64_t K, int64_t N, void *blob_dev, void *stream);
+
+/*
+ * The blob of a bf16 matrix w_dev [N][K] (16-byte aligned) for a given scale
+ * (usually the largest |w| / 2688, which uses the whole range): per 16 k the
+ * e4m3 number nearest to max |w| / (6 scale), at least 2^-9 where a weight is not
+ * 0, and the codes nearest to w / (that scale), ties to even.  Weights past the
+ * range take the largest code; a NaN turns its 16 weights into NaN.
+ * Errors: W12_ERR_ARG, W12_ERR_SHAPE, W12_ERR_ALIGN, W12_ERR_CUDA.
+ */
+int w12_fp4_encode(const uint16_t *w_dev, int64_t K, int64_t N, float scale, void *blob_dev, void *stream);
+
+/* The weights back as fp32 [N][K] (16-byte aligned).  Errors as above. */
+int w12_fp4_decode(const w12_fp4 *w, float *out_dev, void *stream);
+
+/* Bytes of workspace w12_fp4_gemm (count 1) and w12_fp4_gemm_batched need for
+ * these matrices and M (0 on invalid arguments); blob and scale are not read.  A
+ * workspace serves calls of all sizes that need no more than it has. */
+size_t w12_fp4_gemm_workspace_size(const w12_fp4 *w, int count, int64_t M);
+
+/*
+ * y[m, n] = sum_k x[m, k] W[k, n], 1 <= M <= W12_MAX_M.
+ *   x_dev: [M][K] x_dtype W12_BF16 or W12_E4M3, 16-byte aligned; for W12_E4M3
+ *     x_scale_dev [M] fp32 (w12_add_norm writes both), else NULL.
+ *   y_dev: [M][N] y_dtype W12_F32 or W12_BF16, not overlapping the inputs.
+ *   options: 0 or W12_OPT_EARLY_WEIGHTS (as in w12_gemm_ex: the blob was not
+ *     written by the kernel launched just before).
+ * code times the group's scale is exact in the products' type; sums are fp32,
+ * in an order fixed by the shapes, M and the GPU's SM count, so repeated
+ * calls give identical bits.
+ * Errors: W12_ERR_ARG, W12_ERR_SHAPE, W12_ERR_ALIGN, W12_ERR_WORKSPACE,
+ * W12_ERR_CUDA.  Device errors in word 0 of ws: W12_ERR_TIMEOUT.
+ */
+int w12_fp4_gemm(const w12_fp4 *w, const void *x_dev, int x_dtype, const float *x_scale_dev, int64_t M, void *y_dev,
+                 int y_dtype, void *ws_dev, size_t ws_bytes, int options, void *stream);
+
+/* count independent products (1 <= count <= W12_MAX_BATCH) of one M in one
+ * launch, as w12_gemm_batched: host arrays of count matrices and device
+ * pointers (x_scale_dev NULL for W12_BF16). */
+int w12_fp4_gemm_batched(const w12_fp4 *w, const void *const *x_dev, int x_dtype, const float *const *x_scale_dev, int64_t M,
+                         void *const *y_dev, int y_dtype, int count, void *ws_dev, size_t ws_bytes, int options,
+                         void *stream);
+
+/*
  * Read (and clear) the sticky device error word of a workspace: waits for
  * `stream`, copies word 0 to *err_host, then zeroes it.  Returns W12_OK or
  * W12_ERR_CUDA.  *err_host is W12_OK or the first error recorded since the

@@ -3,6 +3,9 @@
 // argument checks and dispatch.  Host code only.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <atomic>
+
 #include "draft_internal.h"
 
 namespace w12 {
@@ -16,6 +19,63 @@ constexpr int64_t kLim31 = int64_t(1) << 31;
 size_t size_of(int dtype) { return dtype == W12_F32 ? 4 : dtype == W12_BF16 ? 2 : 1; }
 
 bool float_type(int dtype) { return dtype == W12_F32 || dtype == W12_BF16; }
+
+// SM count and CTAs per SM of a product variant on the current device, asked
+// once per device and variant.
+constexpr int kMaxDevices = 256;
+std::atomic<uint64_t> g_fp4[kMaxDevices][kFp4Variants];
+
+int fp4_device(int variant, int *sms, int *blocks) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return W12_ERR_CUDA;
+    uint64_t v = g_fp4[dev][variant].load(std::memory_order_acquire);
+    if (v == 0) {
+        int s = 0, b = 0;
+        if (device_sm_count(&s) != W12_OK || fp4_occupancy(variant, &b) != W12_OK || b < 1) return W12_ERR_CUDA;
+        v = uint64_t(s) << 32 | uint64_t(b);
+        g_fp4[dev][variant].store(v, std::memory_order_release);
+    }
+    *sms = int(v >> 32), *blocks = int(v & 0xFFFFFFFFu);
+    return W12_OK;
+}
+
+int check_fp4_shape(int64_t K, int64_t N) {
+    if (K < kGroup || N < 1 || K % kGroup != 0 || K >= kLim31 || N >= kLim31) return W12_ERR_SHAPE;
+    // units (and the threads that write them, one a column) in 32 bits
+    return (N + kTileCols - 1) / kTileCols < (int64_t(1) << 31) / (K / kGroup) / 2 ? W12_OK : W12_ERR_SHAPE;
+}
+
+uint64_t fp4_units(int64_t K, int64_t N) { return uint64_t((N + kTileCols - 1) / kTileCols) * uint64_t(K / kGroup); }
+
+bool usable_scale(float s) { return s >= 0x1p-100f && s <= 0x1p100f; }
+
+constexpr size_t kFp4Counters = 4096;  // (the same for all sizes: one workspace serves them all)
+
+struct Fp4Plan {
+    int64_t U, ubase[kMaxBatch];
+    size_t partial, total;
+    int grid;
+};
+
+int plan_fp4(const w12_fp4 *w, int count, int64_t M, Fp4Plan *p) {
+    if (!w) return W12_ERR_ARG;
+    if (count < 1 || count > kMaxBatch || M < 1 || M > W12_MAX_M) return W12_ERR_SHAPE;
+    p->U = 0;
+    for (int i = 0; i < count; ++i) {
+        const int st = check_fp4_shape(w[i].K, w[i].N);
+        if (st != W12_OK) return st;
+        p->ubase[i] = p->U;
+        p->U += int64_t(fp4_units(w[i].K, w[i].N));
+    }
+    if (p->U >= kLim31) return W12_ERR_SHAPE;
+    int sms = 0, blocks = 0;
+    if (fp4_device(fp4_variant(M), &sms, &blocks) != W12_OK) return W12_ERR_CUDA;
+    p->grid = int(std::min<int64_t>(int64_t(sms) * blocks, p->U));
+    if (size_t(p->grid) * 4u > kFp4Counters) return W12_ERR_CUDA;
+    p->partial = kWsHeader + kFp4Counters;
+    p->total = p->partial + round256(uint64_t(p->grid) * 2u * uint64_t(M) * kTileCols * 4u);
+    return W12_OK;
+}
 
 }  // namespace
 
@@ -53,4 +113,84 @@ extern "C" int w12_add_norm(const void *x, int64_t x_stride, int x_dtype, const 
                      rows_at(residual, residual_stride, size_of(x_dtype), 16) &&
                      rows_at(out, out_stride, size_of(out_dtype), out_dtype == W12_E4M3 ? 8 : 16);
     return launch_norm(a, x_dtype, delta ? delta_dtype : -1, out_dtype, vec, stream);
+}
+
+extern "C" size_t w12_fp4_bytes(int64_t K, int64_t N) {
+    return check_fp4_shape(K, N) == W12_OK ? size_t(fp4_units(K, N)) * kFp4Unit : 0;
+}
+
+extern "C" int w12_fp4_pack(const uint8_t *codes, const uint8_t *scales, int64_t K, int64_t N, void *blob, void *stream) {
+    const int st = check_fp4_shape(K, N);
+    if (st != W12_OK) return st;
+    if (!codes || !scales || !blob) return W12_ERR_ARG;
+    if (!aligned(codes, 16) || !aligned(scales, 8) || !aligned(blob, 256)) return W12_ERR_ALIGN;
+    return launch_fp4_pack(codes, scales, K, N, blob, stream);
+}
+
+extern "C" int w12_fp4_encode(const uint16_t *w, int64_t K, int64_t N, float scale, void *blob, void *stream) {
+    const int st = check_fp4_shape(K, N);
+    if (st != W12_OK) return st;
+    if (!w || !blob || !usable_scale(scale)) return W12_ERR_ARG;
+    if (!aligned(w, 16) || !aligned(blob, 256)) return W12_ERR_ALIGN;
+    return launch_fp4_encode(w, K, N, scale, blob, stream);
+}
+
+extern "C" int w12_fp4_decode(const w12_fp4 *w, float *out, void *stream) {
+    if (!w) return W12_ERR_ARG;
+    const int st = check_fp4_shape(w->K, w->N);
+    if (st != W12_OK) return st;
+    if (!w->blob || !out || !usable_scale(w->scale)) return W12_ERR_ARG;
+    if (!aligned(w->blob, 256) || !aligned(out, 16)) return W12_ERR_ALIGN;
+    return launch_fp4_decode(w->blob, w->K, w->N, w->scale, out, stream);
+}
+
+extern "C" size_t w12_fp4_gemm_workspace_size(const w12_fp4 *w, int count, int64_t M) {
+    Fp4Plan p;
+    return plan_fp4(w, count, M, &p) == W12_OK ? p.total : 0;
+}
+
+extern "C" int w12_fp4_gemm_batched(const w12_fp4 *w, const void *const *x, int x_dtype, const float *const *x_scale, int64_t M,
+                                    void *const *y, int y_dtype, int count, void *ws, size_t ws_bytes, int options,
+                                    void *stream) {
+    if ((x_dtype != W12_BF16 && x_dtype != W12_E4M3) || !float_type(y_dtype) || (options & ~W12_OPT_EARLY_WEIGHTS))
+        return W12_ERR_ARG;
+    const bool e4m3 = x_dtype == W12_E4M3;
+    if (!w || !x || !y || e4m3 != (x_scale != nullptr)) return W12_ERR_ARG;
+    if (count < 1 || count > kMaxBatch || M < 1 || M > W12_MAX_M) return W12_ERR_SHAPE;
+    for (int i = 0; i < count; ++i) {
+        const int st = check_fp4_shape(w[i].K, w[i].N);
+        if (st != W12_OK) return st;
+        if (!w[i].blob || !x[i] || !y[i] || (e4m3 && !x_scale[i]) || !usable_scale(w[i].scale)) return W12_ERR_ARG;
+        if (!aligned(w[i].blob, 256) || !aligned(x[i], 16) || !aligned(y[i], size_of(y_dtype)) ||
+            (e4m3 && !aligned(x_scale[i], 4)))
+            return W12_ERR_ALIGN;
+    }
+    if (!ws) return W12_ERR_WORKSPACE;
+    if (!aligned(ws, 256)) return W12_ERR_ALIGN;
+    Fp4Plan p;
+    const int st = plan_fp4(w, count, M, &p);
+    if (st != W12_OK) return st;
+    if (ws_bytes < p.total) return W12_ERR_WORKSPACE;
+    uint8_t *at = static_cast<uint8_t *>(ws);
+    Fp4Batch b = {};
+    for (int i = 0; i < count; ++i) {
+        Fp4One &g = b.g[i];
+        g.units = static_cast<const uint8_t *>(w[i].blob);
+        g.x = x[i], g.x_scale = e4m3 ? x_scale[i] : nullptr, g.y = y[i];
+        g.scale = w[i].scale;
+        g.K = int32_t(w[i].K), g.N = int32_t(w[i].N), g.KG = int32_t(w[i].K / kGroup);
+        g.NB = int32_t((w[i].N + kTileCols - 1) / kTileCols);
+        g.ubase = int32_t(p.ubase[i]);
+    }
+    b.partial = reinterpret_cast<float *>(at + p.partial);
+    b.counters = reinterpret_cast<uint32_t *>(at + kWsHeader);
+    b.err = reinterpret_cast<int *>(at);
+    b.count = count, b.M = int(M), b.y_dtype = y_dtype, b.U = int32_t(p.U);
+    b.early_weights = (options & W12_OPT_EARLY_WEIGHTS) != 0;
+    return launch_fp4(b, e4m3, p.grid, stream);
+}
+
+extern "C" int w12_fp4_gemm(const w12_fp4 *w, const void *x, int x_dtype, const float *x_scale, int64_t M, void *y, int y_dtype,
+                            void *ws, size_t ws_bytes, int options, void *stream) {
+    return w12_fp4_gemm_batched(w, &x, x_dtype, x_scale ? &x_scale : nullptr, M, &y, y_dtype, 1, ws, ws_bytes, options, stream);
 }

@@ -24,4 +24,39 @@ struct NormArgs {
 // 16-byte boundary and dim is a multiple of 8.
 int launch_norm(const NormArgs &a, int x_dtype, int delta_dtype, int out_dtype, bool vec, void *stream);
 
+// 4-bit weights.  Unit blocks as of the W12 format: unit t * KG + kg holds
+// the codes and scales of 128 columns x 128 k (include/w12.h).
+constexpr int kFp4Unit = W12_FP4_UNIT_BYTES;
+constexpr int kFp4Scales = 8192;  // the scales' place in a unit block
+
+struct Fp4One {
+    const uint8_t *units;
+    const void *x;         // [M][K] bf16, or e4m3 with
+    const float *x_scale;  // [M]
+    void *y;               // [M][N]
+    float scale;
+    int32_t K, N, KG, NB;
+    int32_t ubase;         // first unit of this product
+};
+
+struct Fp4Batch {
+    Fp4One g[kMaxBatch];
+    float *partial;      // [grid][2][M][128] partial sums of split tiles
+    uint32_t *counters;  // [grid] arrivals of a split tile, by the CTA that has its first unit (zero between calls)
+    int *err;
+    int count, M, y_dtype;
+    int32_t U;
+    int early_weights;  // the first weight copies do not wait for the kernel before
+};
+
+int launch_fp4_pack(const uint8_t *codes, const uint8_t *scales, int64_t K, int64_t N, void *blob, void *stream);
+int launch_fp4_encode(const uint16_t *w, int64_t K, int64_t N, float scale, void *blob, void *stream);
+int launch_fp4_decode(const void *blob, int64_t K, int64_t N, float scale, float *out, void *stream);
+// The product kernel's variant for M tokens, and its CTAs per SM (the call also
+// raises the variant's shared-memory limit on the current device).
+constexpr int kFp4Variants = 5;
+int fp4_variant(int64_t M);
+int fp4_occupancy(int variant, int *blocks);
+int launch_fp4(const Fp4Batch &b, bool e4m3, int grid, void *stream);
+
 }  // namespace w12

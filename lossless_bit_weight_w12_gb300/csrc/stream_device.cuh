@@ -57,7 +57,9 @@ struct SCur {
     int gi, nb, kg;
 };
 
-__device__ __forceinline__ SCur s_at(const StreamBatch &b, int u) {
+// (A batch's products by first unit: of W12 weights, or of 4-bit ones.)
+template <class Batch>
+__device__ __forceinline__ SCur s_at(const Batch &b, int u) {
     SCur c{0, 0, 0};
     while (c.gi + 1 < b.count && u >= b.g[c.gi + 1].ubase) ++c.gi;
     const int local = u - b.g[c.gi].ubase;
@@ -66,7 +68,8 @@ __device__ __forceinline__ SCur s_at(const StreamBatch &b, int u) {
     return c;
 }
 
-__device__ __forceinline__ void s_next_tile(const StreamBatch &b, SCur &c) {
+template <class Batch>
+__device__ __forceinline__ void s_next_tile(const Batch &b, SCur &c) {
     c.kg = 0;
     if (++c.nb == b.g[c.gi].NB) {
         c.nb = 0;
@@ -74,7 +77,8 @@ __device__ __forceinline__ void s_next_tile(const StreamBatch &b, SCur &c) {
     }
 }
 
-__device__ __forceinline__ void s_next(const StreamBatch &b, SCur &c) {
+template <class Batch>
+__device__ __forceinline__ void s_next(const Batch &b, SCur &c) {
     if (++c.kg == b.g[c.gi].KG) s_next_tile(b, c);
 }
 
@@ -82,16 +86,18 @@ __device__ __forceinline__ void s_next(const StreamBatch &b, SCur &c) {
 // [first, first + KG); CTA c's piece of it is stored in partial slot
 // (c, 0) if the piece starts at c's first unit, else (c, 1) (only a CTA's
 // first and last pieces can be split).  Each piece adds its unit count to
-// counters[nb]; the CTA that completes the count sums the pieces' slots in
+// the tile's counter; the CTA that completes the count sums the pieces' slots in
 // CTA order (the same bits on every call), writes y and resets the counter.
-template <bool FUSED>
-__device__ __forceinline__ void stream_fixup(const StreamBatch &b, const StreamOne &g, int first, int nb,
+__device__ __forceinline__ uint32_t *arrivals(const StreamBatch &, const StreamOne &g, int, int nb) { return &g.counters[nb]; }
+
+template <bool FUSED, class Batch, class One>
+__device__ __forceinline__ void stream_fixup(const Batch &b, const One &g, int first, int nb,
                                              int count, int *s_last, int tid, int nthreads,
                                              unsigned long long *s_best) {
     __threadfence();
     named_sync(nthreads);
     if (tid == 0) {
-        const uint32_t old = atomicAdd(&g.counters[nb], uint32_t(count));
+        const uint32_t old = atomicAdd(arrivals(b, g, first, nb), uint32_t(count));
         *s_last = (int(old) + count == g.KG);
     }
     named_sync(nthreads);
@@ -149,7 +155,7 @@ __device__ __forceinline__ void stream_fixup(const StreamBatch &b, const StreamO
                 if (FUSED && best != 0ull) atomicMax(&s_best[m], best);
             }
         }
-        if (tid == 0) g.counters[nb] = 0u;
+        if (tid == 0) *arrivals(b, g, first, nb) = 0u;
     }
     named_sync(nthreads);  // s_last is reused by the next piece
 }

@@ -42,7 +42,8 @@ EXPORTS = (
     "w12_encode_device_workspace_size", "w12_encode_plan_device", "w12_encode_device",
     "w12_gemm_batched_debug", "w12_rope_table", "w12_kv_append", "w12_kv_read",
     "w12_attend_workspace_size", "w12_attend", "w12_sample_workspace_size", "w12_sample",
-    "w12_add_norm",
+    "w12_add_norm", "w12_fp4_bytes", "w12_fp4_pack", "w12_fp4_encode", "w12_fp4_decode",
+    "w12_fp4_gemm_workspace_size", "w12_fp4_gemm", "w12_fp4_gemm_batched",
 )
 
 
@@ -75,6 +76,11 @@ class _CRopeScaling(ctypes.Structure):
     _fields_ = [("mode", ctypes.c_int32), ("reserved", ctypes.c_int32), ("factor", ctypes.c_double),
                 ("original", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double),
                 ("attention", ctypes.c_double)]
+
+
+class _CFP4(ctypes.Structure):
+    _fields_ = [("blob", ctypes.c_void_p), ("K", ctypes.c_int64), ("N", ctypes.c_int64), ("scale", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
 
 
 @dataclass(frozen=True)
@@ -155,6 +161,16 @@ def lib():
         L.w12_sample.argtypes = [P, I, I64, I64, I64, P, P, P, P, P, P, P, P, P, P, P, SZ, P]
         F = ctypes.c_float
         L.w12_add_norm.argtypes = [P, I64, I, P, I64, I, P, I, F, F, I64, I64, P, I64, P, I64, I, P, P]
+        Q = ctypes.POINTER(_CFP4)
+        L.w12_fp4_bytes.restype = SZ
+        L.w12_fp4_bytes.argtypes = [I64, I64]
+        L.w12_fp4_pack.argtypes = [P, P, I64, I64, P, P]
+        L.w12_fp4_encode.argtypes = [P, I64, I64, F, P, P]
+        L.w12_fp4_decode.argtypes = [Q, P, P]
+        L.w12_fp4_gemm_workspace_size.restype = SZ
+        L.w12_fp4_gemm_workspace_size.argtypes = [Q, I, I64]
+        L.w12_fp4_gemm.argtypes = [Q, P, I, P, I64, P, I, P, SZ, I, P]
+        L.w12_fp4_gemm_batched.argtypes = [Q, P, I, P, I64, P, I, I, P, SZ, I, P]
         _lib = L
     return _lib
 
@@ -623,6 +639,100 @@ def add_norm(x, weight, out, delta=None, residual_out=None, eps: float = 1e-6, o
                             _dtype_of(out), _typed_ptr(scale_out, torch.float32, n, "scale_out"), _stream_of(x, stream))
     if st:
         raise W12Error(st, "w12_add_norm")
+
+
+# ----------------------------------------------- draft model: 4-bit weights
+
+class FP4Weight:
+    """A matrix of 4-bit weights on the device (w12_fp4): holds the blob and
+    the marshalled descriptor.  Made by pack() or encode()."""
+
+    def __init__(self, blob, K: int, N: int, scale: float):
+        self.blob, self.K, self.N, self.scale = blob, K, N, float(scale)
+        self.c = _CFP4(blob.data_ptr(), K, N, self.scale, 0)
+
+    @staticmethod
+    def _blob(K: int, N: int, device):
+        import torch
+        n = int(lib().w12_fp4_bytes(K, N))
+        if n == 0:
+            raise W12Error(ERR_SHAPE, "w12_fp4_bytes")
+        t = torch.empty(n + 256, dtype=torch.uint8, device=device)
+        off = (-t.data_ptr()) % 256
+        return t[off:off + n]
+
+    @staticmethod
+    def pack(codes, scales, scale: float = 1.0, stream=None) -> "FP4Weight":
+        """From codes uint8 [N, K / 2] and scales float8_e4m3fn [N, K / 16]."""
+        import torch
+        N, K = codes.shape[0], 2 * codes.shape[1]
+        blob = FP4Weight._blob(K, N, codes.device)
+        _check(lib().w12_fp4_pack(_typed_ptr(codes, torch.uint8, N * K // 2, "codes"),
+                                  _typed_ptr(scales, torch.float8_e4m3fn, N * K // 16, "scales"), K, N, _ptr(blob),
+                                  _stream_of(codes, stream)), "w12_fp4_pack")
+        return FP4Weight(blob, K, N, scale)
+
+    @staticmethod
+    def encode(w, scale: float | None = None, stream=None) -> "FP4Weight":
+        """From bfloat16 weights [N, K]; scale: the largest |w| / 2688 by default."""
+        import torch
+        N, K = w.shape
+        if scale is None:
+            top = float(w.abs().max())
+            scale = top / 2688.0 if 0.0 < top < float("inf") else 1.0
+        blob = FP4Weight._blob(K, N, w.device)
+        _check(lib().w12_fp4_encode(_typed_ptr(w, torch.bfloat16, N * K, "w"), K, N, scale, _ptr(blob), _stream_of(w, stream)),
+               "w12_fp4_encode")
+        return FP4Weight(blob, K, N, scale)
+
+    def decode(self, stream=None):
+        """float32 [N, K]."""
+        import torch
+        out = torch.empty(self.N, self.K, dtype=torch.float32, device=self.blob.device)
+        _check(lib().w12_fp4_decode(ctypes.byref(self.c), _ptr(out), _stream_of(self.blob, stream)), "w12_fp4_decode")
+        return out
+
+
+def _fp4_array(weights):
+    return (_CFP4 * len(weights))(*[w.c for w in weights])
+
+
+def fp4_gemm_workspace_size(weights, M: int) -> int:
+    return int(lib().w12_fp4_gemm_workspace_size(_fp4_array(weights), len(weights), M))
+
+
+class FP4Batch:
+    """Marshalled arguments of one w12_fp4_gemm_batched call (built once, reused:
+    the pointer arrays stay valid while the tensors live)."""
+
+    def __init__(self, weights, xs, ys, ws, x_scales=None, options: int = 0):
+        import torch
+        n = len(weights)
+        if n < 1 or len(xs) != n or len(ys) != n or (x_scales is not None and len(x_scales) != n):
+            raise ValueError("one x, y and scale per matrix")
+        self.M, self.x_dtype, self.y_dtype, self.options = xs[0].shape[0], _dtype_of(xs[0]), _dtype_of(ys[0]), options
+        for w, x, y in zip(weights, xs, ys):
+            if x.shape != (self.M, w.K) or y.shape != (self.M, w.N) or x.dtype is not xs[0].dtype or y.dtype is not ys[0].dtype:
+                raise ValueError("x [M, K] and y [M, N] of one type each")
+        self.w = _fp4_array(weights)
+        ptrs = lambda ts: (ctypes.c_void_p * n)(*[_ptr(t) for t in ts])  # noqa: E731
+        self.xs, self.ys = ptrs(xs), ptrs(ys)
+        self.x_scales = None if x_scales is None else (ctypes.c_void_p * n)(
+            *[_typed_ptr(t, torch.float32, self.M, "x_scale") for t in x_scales])
+        self.count, self.ws, self.ws_ptr, self.ws_bytes = n, ws, _ptr(ws), ws.nbytes
+        self._keep = (list(weights), list(xs), list(ys), None if x_scales is None else list(x_scales))
+
+    def __call__(self, stream=None):
+        st = lib().w12_fp4_gemm_batched(self.w, self.xs, self.x_dtype, self.x_scales, self.M, self.ys, self.y_dtype,
+                                        self.count, self.ws_ptr, self.ws_bytes, self.options, _stream_of(self.ws, stream))
+        if st:
+            raise W12Error(st, "w12_fp4_gemm_batched")
+
+
+def fp4_gemm(weight: FP4Weight, x, y, ws_dev, x_scale=None, options: int = 0, stream=None):
+    """y [M, N] (float32 or bfloat16) = x [M, K] @ W; x bfloat16, or
+    float8_e4m3fn with x_scale float32 [M]."""
+    FP4Batch([weight], [x], [y], ws_dev, None if x_scale is None else [x_scale], options)(stream)
 
 
 # --------------------------------------------------------------- helpers

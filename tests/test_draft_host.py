@@ -29,3 +29,37 @@ def test_add_norm_checks(w12):
     assert call(x=DEV + 2) == call(d=DEV + 1) == call(w=DEV + 1) == call(res=DEV + 2) == call(out=DEV + 1) == w12.ERR_ALIGN
     assert call(ot=2, scale=DEV + 2) == w12.ERR_ALIGN
     assert call(rows=0, x=None, out=None) == w12.OK
+
+
+def test_fp4_checks(w12):
+    import ctypes
+    L = w12.lib()
+    F = w12._CFP4
+
+    def gemm(blob=DEV, K=256, N=100, scale=1.0, x=DEV, xt=1, xs=None, M=4, y=DEV, yt=0, count=1, ws=DEV, wsb=1 << 24, opt=0, no_w=False):
+        arr = (F * 1)(F(blob, K, N, scale, 0))
+        one = lambda p: (ctypes.c_void_p * 1)(p)  # noqa: E731
+        return L.w12_fp4_gemm_batched(None if no_w else arr, one(x), xt, None if xs is None else one(xs), M, one(y), yt, count, ws,
+                                      wsb, opt, None)
+
+    assert gemm(xt=0) == gemm(xt=3) == gemm(yt=2) == gemm(opt=1) == gemm(opt=0x101) == gemm(no_w=True) == w12.ERR_ARG
+    assert gemm(xs=DEV) == gemm(xt=2) == w12.ERR_ARG
+    assert gemm(M=0) == gemm(M=129) == gemm(count=0) == gemm(count=9) == w12.ERR_SHAPE
+    assert gemm(K=0) == gemm(K=100) == gemm(K=-128) == gemm(N=0) == gemm(N=1 << 31) == gemm(K=1 << 31) == w12.ERR_SHAPE
+    assert gemm(K=1 << 24, N=1 << 24) == w12.ERR_SHAPE
+    assert gemm(blob=None) == gemm(x=None) == gemm(y=None) == gemm(scale=0.0) == gemm(scale=-1.0) == w12.ERR_ARG
+    assert gemm(scale=float("nan")) == gemm(scale=float("inf")) == w12.ERR_ARG
+    assert gemm(blob=DEV + 128) == gemm(x=DEV + 8) == gemm(y=DEV + 2) == gemm(y=DEV + 1, yt=1) == w12.ERR_ALIGN
+    assert gemm(xt=2, xs=DEV + 2) == w12.ERR_ALIGN
+    assert gemm(ws=None) == w12.ERR_WORKSPACE
+    assert gemm(ws=DEV + 128) == w12.ERR_ALIGN
+    assert L.w12_fp4_bytes(256, 129) == 4 * 9216 and L.w12_fp4_bytes(100, 1) == L.w12_fp4_bytes(0, 1) == L.w12_fp4_bytes(128, 0) == 0
+    assert L.w12_fp4_pack(None, DEV, 128, 1, DEV, None) == w12.ERR_ARG
+    assert L.w12_fp4_pack(DEV, DEV, 130, 1, DEV, None) == w12.ERR_SHAPE
+    assert L.w12_fp4_pack(DEV + 8, DEV, 128, 1, DEV, None) == L.w12_fp4_pack(DEV, DEV + 4, 128, 1, DEV, None) == w12.ERR_ALIGN
+    assert L.w12_fp4_encode(DEV, 128, 1, 0.0, DEV, None) == L.w12_fp4_encode(None, 128, 1, 1.0, DEV, None) == w12.ERR_ARG
+    assert L.w12_fp4_encode(DEV + 2, 128, 1, 1.0, DEV, None) == L.w12_fp4_encode(DEV, 128, 1, 1.0, DEV + 16, None) == w12.ERR_ALIGN
+    one = F(DEV, 128, 1, 1.0, 0)
+    assert L.w12_fp4_decode(ctypes.byref(one), None, None) == w12.ERR_ARG
+    assert L.w12_fp4_decode(ctypes.byref(one), DEV + 4, None) == w12.ERR_ALIGN
+    assert L.w12_fp4_decode(None, DEV, None) == w12.ERR_ARG
