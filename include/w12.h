@@ -751,6 +751,56 @@ int w12_fp4_gemm_batched(const w12_fp4 *w, const void *const *x_dev, int x_dtype
                          void *const *y_dev, int y_dtype, int count, void *ws_dev, size_t ws_bytes, int options,
                          void *stream);
 
+/* Cuts of a distribution per request, as in w12_sample: [R] each, or NULL
+ * (temperature 1; no cut). */
+typedef struct w12_cut {
+    const float *temperature;
+    const int32_t *top_k;
+    const float *top_p, *min_p;
+} w12_cut;
+
+/* Bytes of workspace w12_verify_sampled needs (0 on invalid arguments).  A
+ * workspace serves calls of all sizes that need no more than it has. */
+size_t w12_verify_sampled_workspace_size(int64_t R, int64_t T, int64_t V);
+
+/*
+ * Verify R sampled draft blocks against the target's probabilities, from given
+ * random numbers (the greedy rule is w12_verify_greedy; w12_sample accepts
+ * drafts that equal the target's own samples, this accepts more of them when
+ * they were sampled from a distribution near the target's).
+ *   logits_dev: [R*T][V] of the target, dtype W12_F32 or W12_BF16: row i of a
+ *     block is its prediction after [last token, d0 .. d(i-1)].
+ *   draft_logits_dev: [R*(T-1)][V] of the drafter, draft_dtype: row i is what
+ *     draft token i was drawn from.  Both aligned to their elements; 16-byte
+ *     aligned rows are read faster.
+ *   draft_dev: [R][T-1] int32; a token outside [0, V) is none: the block ends
+ *     there.  (These three may be NULL when T == 1.)
+ *   target_cut, draft_cut (may be NULL): what p and q are the distributions of
+ *     -- w / W of the tokens that stay, with w12_sample's weights and rules
+ *     (temperature <= 0: its one token); draft_cut is the one the drafts were
+ *     drawn with.
+ *   u_dev: [R][T] fp32 in [0, 1): u[r, i < T-1] for draft i, u[r, T-1] for the
+ *     next token.
+ * With p and q in fp32 (a weight times the rounded 1 / W):
+ *   accept_len_dev[r] = first i < T-1 without u[r, i] q_i(d_i) < p_i(d_i), else
+ *     T-1 =: n;
+ *   next_tok_dev[r] = the first index at which the sum of the weights passes
+ *     u[r, T-1] times their whole sum: for n < T-1 (with a draft there) the
+ *     weights round(2^44 max(p_n - q_n, 0)), where they are not all 0, else the
+ *     target's own (the token that w12_sample draws).  -1: no token of the row
+ *     stays.
+ *   ratio_dev (may be NULL): [R][T-1] fp32, min(1, p / q) of every draft (0
+ *     where p is 0 or there is no draft).
+ * R >= 1, T >= 1, R * T < 2^26, 1 <= V <= W12_SAMPLE_MAX_V.  Sums are whole
+ * numbers: repeated calls give identical results.
+ * Errors: W12_ERR_ARG, W12_ERR_SHAPE, W12_ERR_ALIGN, W12_ERR_WORKSPACE,
+ * W12_ERR_CUDA.
+ */
+int w12_verify_sampled(const void *logits_dev, int dtype, const void *draft_logits_dev, int draft_dtype, int64_t R,
+                       int64_t T, int64_t V, const int32_t *draft_dev, const w12_cut *target_cut,
+                       const w12_cut *draft_cut, const float *u_dev, float *ratio_dev, int32_t *accept_len_dev,
+                       int32_t *next_tok_dev, void *ws_dev, size_t ws_bytes, void *stream);
+
 /*
  * Read (and clear) the sticky device error word of a workspace: waits for
  * `stream`, copies word 0 to *err_host, then zeroes it.  Returns W12_OK or

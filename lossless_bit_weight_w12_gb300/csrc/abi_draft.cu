@@ -194,3 +194,52 @@ extern "C" int w12_fp4_gemm(const w12_fp4 *w, const void *x, int x_dtype, const 
                             void *ws, size_t ws_bytes, int options, void *stream) {
     return w12_fp4_gemm_batched(w, &x, x_dtype, x_scale ? &x_scale : nullptr, M, &y, y_dtype, 1, ws, ws_bytes, options, stream);
 }
+
+namespace {
+
+bool cut_aligned(const w12_cut *c) {
+    return !c || (aligned(c->temperature, 4) && aligned(c->top_k, 4) && aligned(c->top_p, 4) && aligned(c->min_p, 4));
+}
+
+int cut_rows(const void *logits, int dtype, int64_t R, int64_t T, int64_t V, const w12_cut *cut, RowCut *out, void *stream) {
+    SampleArgs a = {};
+    a.logits = logits;
+    if (cut) a.temperature = cut->temperature, a.top_k = cut->top_k, a.top_p = cut->top_p, a.min_p = cut->min_p;
+    a.cut_out = out;
+    a.V = V, a.rows = R * T, a.R = R, a.T = T;
+    return launch_cut(a, dtype, stream);
+}
+
+}  // namespace
+
+extern "C" size_t w12_verify_sampled_workspace_size(int64_t R, int64_t T, int64_t V) {
+    if (R < 1 || T < 1 || V < 1 || V > W12_SAMPLE_MAX_V || R >= kLim31 || T >= kLim31 || R * T >= (int64_t(1) << 26))
+        return 0;
+    return kWsHeader + round256(uint64_t(R) * uint64_t(2 * T - 1) * sizeof(RowCut));
+}
+
+extern "C" int w12_verify_sampled(const void *logits, int dtype, const void *draft_logits, int draft_dtype, int64_t R, int64_t T,
+                                  int64_t V, const int32_t *draft, const w12_cut *target_cut, const w12_cut *draft_cut,
+                                  const float *u, float *ratio, int32_t *accept_len, int32_t *next_tok, void *ws,
+                                  size_t ws_bytes, void *stream) {
+    if (!float_type(dtype) || (T > 1 && !float_type(draft_dtype))) return W12_ERR_ARG;
+    const size_t need = w12_verify_sampled_workspace_size(R, T, V);
+    if (need == 0) return W12_ERR_SHAPE;
+    if (!logits || !u || !accept_len || !next_tok || (T > 1 && (!draft_logits || !draft))) return W12_ERR_ARG;
+    if (!aligned(logits, size_of(dtype)) || (T > 1 && !aligned(draft_logits, size_of(draft_dtype))) || !aligned(u, 4) ||
+        !aligned(ratio, 4) || !aligned(draft, 4) || !aligned(accept_len, 4) || !aligned(next_tok, 4) || !cut_aligned(target_cut) ||
+        !cut_aligned(draft_cut))
+        return W12_ERR_ALIGN;
+    if (!ws || ws_bytes < need) return W12_ERR_WORKSPACE;
+    if (!aligned(ws, 256)) return W12_ERR_ALIGN;
+    AcceptArgs a = {};
+    a.logits = logits, a.draft_logits = draft_logits;
+    a.f32 = dtype == W12_F32, a.draft_f32 = draft_dtype == W12_F32;
+    RowCut *cuts = reinterpret_cast<RowCut *>(static_cast<uint8_t *>(ws) + kWsHeader);
+    a.cuts = cuts, a.draft_cuts = cuts + R * T;
+    a.draft = draft, a.u = u, a.ratio = ratio, a.accept_len = accept_len, a.next_tok = next_tok;
+    a.R = R, a.T = T, a.V = V;
+    int st = cut_rows(logits, dtype, R, T, V, target_cut, cuts, stream);
+    if (st == W12_OK && T > 1) st = cut_rows(draft_logits, draft_dtype, R, T - 1, V, draft_cut, cuts + R * T, stream);
+    return st == W12_OK ? launch_accept(a, stream) : st;
+}

@@ -59,4 +59,16 @@ int fp4_variant(int64_t M);
 int fp4_occupancy(int variant, int *blocks);
 int launch_fp4(const Fp4Batch &b, bool e4m3, int grid, void *stream);
 
+struct AcceptArgs {
+    const void *logits, *draft_logits;  // [R T][V], [R (T - 1)][V]
+    int32_t f32, draft_f32;
+    const RowCut *cuts, *draft_cuts;    // of their rows
+    const int32_t *draft;
+    const float *u;
+    float *ratio;
+    int32_t *accept_len, *next_tok;
+    int64_t R, T, V;
+};
+int launch_accept(const AcceptArgs &a, void *stream);
+
 }  // namespace w12

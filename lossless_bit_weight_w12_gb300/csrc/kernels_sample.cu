@@ -44,6 +44,7 @@
 
 #include "async_common.cuh"
 #include "device_common.cuh"
+#include "sample_device.cuh"
 #include "step_device.cuh"
 #include "step_internal.h"
 
@@ -53,8 +54,6 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-using u64 = unsigned long long;
-
 constexpr int kST = 512;               // threads per CTA
 constexpr int kSW = kST / 32;
 constexpr int kBins = 2048;
@@ -63,7 +62,6 @@ constexpr int kWide = 2304;            // tokens that can be gathered for a nucl
 constexpr int kAround = 800;           // tokens to either side of where the sample sees the boundary
 constexpr int kTaken = 16;             // sampled tokens per thread
 constexpr int kMaxCluster = 16;        // (8 where rows are many)
-constexpr float kOne31 = 2147483648.0f;
 constexpr float kSpan = 22.25f;        // e^-22.25 rounds to weight 0
 
 struct SampleSmall {
@@ -130,34 +128,6 @@ __device__ __forceinline__ void sync_relaxed() {
 __device__ __forceinline__ void cluster_here() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_started() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ u64 umax64(u64 a, u64 b) { return a > b ? a : b; }
-
-// acc + w, in one instruction
-__device__ __forceinline__ u64 add_wide(u64 acc, uint32_t w) {
-    u64 r;
-    asm("mad.wide.u32 %0, %1, 1, %2;" : "=l"(r) : "r"(w), "l"(acc));
-    return r;
-}
-
-__device__ __forceinline__ u64 warp_sum64(u64 x) {
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-    return x;
-}
-__device__ __forceinline__ u64 warp_max64(u64 x) {
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) x = umax64(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
-    return x;
-}
-__device__ __forceinline__ u64 warp_scan64(u64 x, int lane) {
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const u64 z = __shfl_up_sync(0xFFFFFFFFu, x, o);
-        if (lane >= o) x += z;
-    }
-    return x;
-}
-
 __device__ __forceinline__ int arg_bin(float d) {
     const int b = int(-d * (float(kBins) / kSpan));
     return b < kBins ? b : kBins - 1;
@@ -168,62 +138,6 @@ __device__ __forceinline__ int weight_bin(uint32_t w) {
     return int(((158u << 23) - __float_as_uint(__uint2float_rz(w))) >> 17);
 }
 static_assert((31 << 6) < kBins, "octaves of weights");
-
-template <int DT>
-struct Row {
-    const void *x;      // this CTA's chunk (shared or global memory)
-    const uint32_t *w;  // its weights, once they are kept (shared memory), or NULL
-    int n;              // logits in it
-    int i0, i1;         // this thread's
-    bool vec;           // four at a time: the chunk starts on a 16- (bf16: 8-) byte boundary
-    bool inf;           // the largest is +infinity: such logits count as 0, the others as -infinity
-    uint32_t first;     // index of its first
-    float mx, inv_t;
-
-    __device__ __forceinline__ float clean(float v) const {
-        if (inf) return v == INFINITY ? 0.0f : -INFINITY;
-        return fmaxf(v, -INFINITY);  // NaN is never sampled
-    }
-    __device__ __forceinline__ float at(int i) const {
-        return clean(DT == W12_F32 ? static_cast<const float *>(x)[i]
-                                   : bf16_bits_to_float(static_cast<const uint16_t *>(x)[i]));
-    }
-    // logits i .. i + 3 (-infinity past the chunk); i is a multiple of 4
-    __device__ __forceinline__ void at4(int i, float (&v)[4]) const {
-        if (vec && i + 4 <= n) {
-            if (DT == W12_F32) {
-                const float4 f = reinterpret_cast<const float4 *>(x)[i >> 2];
-                v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
-            } else {
-                const uint2 f = reinterpret_cast<const uint2 *>(x)[i >> 2];
-                v[0] = bf16_bits_to_float(f.x & 0xFFFFu), v[1] = bf16_bits_to_float(f.x >> 16);
-                v[2] = bf16_bits_to_float(f.y & 0xFFFFu), v[3] = bf16_bits_to_float(f.y >> 16);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = clean(v[j]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = i + j < n ? at(i + j) : -INFINITY;
-        }
-    }
-    __device__ __forceinline__ u64 comp(float v, int i) const { return pack_key(v, first + uint32_t(i)); }
-    // (max - x) / t as the exponent's argument, <= 0
-    __device__ __forceinline__ float arg(float v) const { return __fmul_rn(__fsub_rn(v, mx), inv_t); }
-    // (an argument of -infinity, or NaN -- an infinity times 0 -- gives 0)
-    __device__ __forceinline__ uint32_t weight(float v) const { return __float2uint_rn(expf(arg(v)) * kOne31); }
-    __device__ __forceinline__ uint32_t weight_at(int i) const { return w ? w[i] : weight(at(i)); }
-    __device__ __forceinline__ void weight4(int i, uint32_t (&y)[4]) const {
-        if (w) {  // (kept up to a multiple of 4)
-            const uint4 f = reinterpret_cast<const uint4 *>(w)[i >> 2];
-            y[0] = f.x, y[1] = f.y, y[2] = f.z, y[3] = f.w;
-        } else {
-            float v[4];
-            at4(i, v);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) y[j] = weight(v[j]);
-        }
-    }
-};
 
 // Which elements a histogram is over, from the second level on: lo <=
 // composite <= hi, in bins of 2^shift composites; shift -1: bins of weights.
@@ -436,20 +350,6 @@ __device__ __noinline__ u64 select(cg::cluster_group &cl, SampleSmall &sh, Sampl
         cl.sync();  // the slices are read before the next level writes them
     }
     return thr0;  // not reached: a level divides the 64-bit range by 2048
-}
-
-// floor(u total / 2^24) with u in [0, 2^24)
-__device__ __forceinline__ u64 scaled(uint64_t u, u64 total) { return (__umul64hi(u, total) << 40) | ((u * total) >> 24); }
-
-__device__ __forceinline__ uint64_t fixed_u(float u) {
-    const float f = u * 16777216.0f;
-    return f >= 16777215.0f ? 16777215ull : f > 0.0f ? uint64_t(f) : 0ull;
-}
-
-// ceil(p total), at least 1: what lies before a token that stays
-__device__ __forceinline__ u64 nucleus(uint64_t p, u64 total) {
-    const u64 lim = p * (total >> 24) + ((p * (total & 0xFFFFFFull) + 0xFFFFFFull) >> 24);
-    return lim < 1 ? 1 : lim;
 }
 
 // The cut and the draw among n <= kCap gathered tokens, by one CTA (all
@@ -751,8 +651,9 @@ __device__ __forceinline__ u64 window_threshold(SampleSmall &sh, SampleCut &cut,
     return sh.thr;
 }
 
-// CUT: top_k or top_p may be asked for.
-template <int DT, bool CUT>
+// CUT: top_k or top_p may be asked for.  STAT: what the cuts leave is written
+// (a.cut_out) and nothing is drawn.
+template <int DT, bool CUT, bool STAT>
 __global__ void __launch_bounds__(kST, 2) sample_kernel(const __grid_constant__ SampleArgs a) {
     cg::cluster_group cl = cg::this_cluster();
     extern __shared__ __align__(16) unsigned char smem[];
@@ -784,7 +685,7 @@ __global__ void __launch_bounds__(kST, 2) sample_kernel(const __grid_constant__ 
     const int64_t req = r / a.T;
     const float t = a.temperature ? a.temperature[req] : 1.0f;
     const int32_t top_k = CUT && a.top_k ? a.top_k[req] : 0;
-    const bool few = CUT && top_k > 0 && top_k < a.V && top_k <= kCap && t > 0.0f;  // the first top_k in one CTA
+    const bool few = CUT && !STAT && top_k > 0 && top_k < a.V && top_k <= kCap && t > 0.0f;  // the first top_k in one CTA
     if (tid == 0) sh.last = 0;
     if (CUT)
         for (int i = tid; i < kBins; i += kST) cut.lo[i] = 0u;
@@ -1076,7 +977,9 @@ __global__ void __launch_bounds__(kST, 2) sample_kernel(const __grid_constant__ 
                 }
                 add_up(wide ? 1 : 0);  // (not the slot of the sum before it)
             }
-            if (total > 0) {
+            if (STAT) {
+                if (writer) a.cut_out[r] = {thr, total, row.mx, row.inv_t, w_thr, floor_w, -1, row.inf};
+            } else if (total > 0) {
                 const u64 target = scaled(fixed_u(a.u[r]), total);
                 writer = false;
                 const uint32_t hit = __ballot_sync(0xFFFFFFFFu, before <= target && target < before + mine);
@@ -1102,12 +1005,14 @@ __global__ void __launch_bounds__(kST, 2) sample_kernel(const __grid_constant__ 
             }
         }
     }
-    if (writer) {  // one thread of the cluster
+    if (STAT && writer && (row.mx == -INFINITY || !(t > 0.0f)))
+        a.cut_out[r] = {0ull, token >= 0 ? 1ull << 31 : 0ull, row.mx, 1.0f, 0u, 1u, token, row.inf};
+    if (!STAT && writer) {  // one thread of the cluster
         a.tokens[r] = token;
         if (a.prob) a.prob[r] = prob;
     }
     sync_relaxed();  // no CTA leaves while another may read its shared memory
-    if (!a.accept_len) return;
+    if (STAT || !a.accept_len) return;
     // ---- the CTA that has the last row's token applies the acceptance rule:
     // the thread that stored a token counts its row, as only it can order the
     // two (a release by the barrier above in its place: 16 rows 32.4 us, so 30.3)
@@ -1134,33 +1039,32 @@ __global__ void __launch_bounds__(kST, 2) sample_kernel(const __grid_constant__ 
 constexpr size_t kMostShared = 227 * 1024;
 constexpr size_t kTwoShared = 113 * 1024;  // two CTAs on an SM
 
-template <int DT, bool CUT>
+template <int DT, bool CUT, bool STAT>
 int run_t(const SampleArgs &a, int cs, void *stream) {
     static std::atomic<uint64_t> ready[4];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 256) return W12_ERR_CUDA;
     const uint64_t bit = uint64_t(1) << (dev & 63);
     if (!(ready[dev >> 6].load(std::memory_order_relaxed) & bit)) {
-        if (cudaFuncSetAttribute(sample_kernel<DT, CUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMostShared)) !=
+        if (cudaFuncSetAttribute(sample_kernel<DT, CUT, STAT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMostShared)) !=
                 cudaSuccess ||
-            cudaFuncSetAttribute(sample_kernel<DT, CUT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+            cudaFuncSetAttribute(sample_kernel<DT, CUT, STAT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
             return W12_ERR_CUDA;
         ready[dev >> 6].fetch_or(bit, std::memory_order_relaxed);
     }
     const size_t smem = kSmallBytes + (CUT ? kCutBytes : 0) +
                         (a.keep_w ? weights_at<DT>(a.chunk) + size_t(a.chunk) * 4
                                   : a.resident ? (size_t(a.chunk) * (DT == W12_F32 ? 4 : 2) + 15) / 16 * 16 : 0);
-    return launch_step(sample_kernel<DT, CUT>, int(a.rows * cs), kST, smem, cs, stream, a);
+    return launch_step(sample_kernel<DT, CUT, STAT>, int(a.rows * cs), kST, smem, cs, stream, a);
 }
 
-template <int DT>
+template <int DT, bool STAT>
 int run(const SampleArgs &a, int cs, void *stream) {
-    return a.top_k || a.top_p ? run_t<DT, true>(a, cs, stream) : run_t<DT, false>(a, cs, stream);
+    return a.top_k || a.top_p ? run_t<DT, true, STAT>(a, cs, stream) : run_t<DT, false, STAT>(a, cs, stream);
 }
 
-}  // namespace
-
-int launch_sample(SampleArgs &a, int dtype, void *stream) {
+template <bool STAT>
+int plan_and_run(SampleArgs &a, int dtype, void *stream) {
     const int es = dtype == W12_F32 ? 4 : 2;
     // Enough CTAs per row that each holds a few thousand logits, and the row
     // stays in shared memory.  16 for up to 14 rows: so many such clusters run
@@ -1175,7 +1079,13 @@ int launch_sample(SampleArgs &a, int dtype, void *stream) {
     const size_t at = dtype == W12_F32 ? weights_at<W12_F32>(chunk) : weights_at<W12_BF16>(chunk);
     a.keep_w = (a.top_k || a.top_p) && kSmallBytes + kCutBytes + at + size_t(chunk) * 4 + 16 <= kTwoShared;
     a.vec = (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0 && (a.V * es) % 16 == 0;
-    return dtype == W12_F32 ? run<W12_F32>(a, cs, stream) : run<W12_BF16>(a, cs, stream);
+    return dtype == W12_F32 ? run<W12_F32, STAT>(a, cs, stream) : run<W12_BF16, STAT>(a, cs, stream);
 }
+
+}  // namespace
+
+int launch_sample(SampleArgs &a, int dtype, void *stream) { return plan_and_run<false>(a, dtype, stream); }
+
+int launch_cut(SampleArgs &a, int dtype, void *stream) { return plan_and_run<true>(a, dtype, stream); }
 
 }  // namespace w12

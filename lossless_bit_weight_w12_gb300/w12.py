@@ -44,6 +44,7 @@ EXPORTS = (
     "w12_attend_workspace_size", "w12_attend", "w12_sample_workspace_size", "w12_sample",
     "w12_add_norm", "w12_fp4_bytes", "w12_fp4_pack", "w12_fp4_encode", "w12_fp4_decode",
     "w12_fp4_gemm_workspace_size", "w12_fp4_gemm", "w12_fp4_gemm_batched",
+    "w12_verify_sampled_workspace_size", "w12_verify_sampled",
 )
 
 
@@ -81,6 +82,11 @@ class _CRopeScaling(ctypes.Structure):
 class _CFP4(ctypes.Structure):
     _fields_ = [("blob", ctypes.c_void_p), ("K", ctypes.c_int64), ("N", ctypes.c_int64), ("scale", ctypes.c_float),
                 ("reserved", ctypes.c_int32)]
+
+
+class _CCut(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p),
+                ("min_p", ctypes.c_void_p)]
 
 
 @dataclass(frozen=True)
@@ -171,6 +177,10 @@ def lib():
         L.w12_fp4_gemm_workspace_size.argtypes = [Q, I, I64]
         L.w12_fp4_gemm.argtypes = [Q, P, I, P, I64, P, I, P, SZ, I, P]
         L.w12_fp4_gemm_batched.argtypes = [Q, P, I, P, I64, P, I, I, P, SZ, I, P]
+        CUT = ctypes.POINTER(_CCut)
+        L.w12_verify_sampled_workspace_size.restype = SZ
+        L.w12_verify_sampled_workspace_size.argtypes = [I64, I64, I64]
+        L.w12_verify_sampled.argtypes = [P, I, P, I, I64, I64, I64, P, CUT, CUT, P, P, P, P, P, SZ, P]
         _lib = L
     return _lib
 
@@ -733,6 +743,58 @@ def fp4_gemm(weight: FP4Weight, x, y, ws_dev, x_scale=None, options: int = 0, st
     """y [M, N] (float32 or bfloat16) = x [M, K] @ W; x bfloat16, or
     float8_e4m3fn with x_scale float32 [M]."""
     FP4Batch([weight], [x], [y], ws_dev, None if x_scale is None else [x_scale], options)(stream)
+
+
+# ------------------------------------- draft model: sampled verification
+
+class Cut:
+    """Cuts of a distribution per request (w12_cut), as sample()'s: temperature,
+    top_p, min_p float32 [R] and top_k int32 [R], or None.  Holds the tensors
+    and the marshalled struct."""
+
+    def __init__(self, temperature=None, top_k=None, top_p=None, min_p=None):
+        import torch
+        given = [t for t in (temperature, top_k, top_p, min_p) if t is not None]
+        self.R = given[0].numel() if given else None
+        self._keep = given
+        ptr = lambda t, d, n: _typed_ptr(t, d, self.R or 0, n)  # noqa: E731
+        self.c = _CCut(ptr(temperature, torch.float32, "temperature"), ptr(top_k, torch.int32, "top_k"),
+                       ptr(top_p, torch.float32, "top_p"), ptr(min_p, torch.float32, "min_p"))
+        self.ref = ctypes.byref(self.c)
+
+
+def verify_sampled_workspace_size(R: int, T: int, V: int) -> int:
+    return int(lib().w12_verify_sampled_workspace_size(R, T, V))
+
+
+def verify_sampled(logits, draft_logits, R: int, T: int, draft, u, accept_dev, next_dev, ws_dev,
+                   target_cut: Cut | None = None, draft_cut: Cut | None = None, ratio_dev=None, stream=None):
+    """Accept drafts [R, T - 1] int32 against the target's probabilities (logits
+    [R*T, V], draft_logits [R*(T-1), V], float32 or bfloat16) with the random
+    numbers u [R, T] float32, and draw the next token of each request."""
+    import torch
+    f32, i32 = torch.float32, torch.int32
+    V = logits.shape[-1]
+    n = R * (T - 1)
+    for c in (target_cut, draft_cut):
+        if c is not None and c.R is not None and c.R != R:
+            raise ValueError(f"cuts: expected {R} elements")
+    if logits.dtype is not f32 and logits.dtype is not torch.bfloat16:
+        raise ValueError("logits: float32 or bfloat16")
+    if T > 1 and (draft_logits is None or draft is None or draft_logits.shape[-1] != V or
+                  (draft_logits.dtype is not f32 and draft_logits.dtype is not torch.bfloat16)):
+        raise ValueError("draft_logits: float32 or bfloat16 [R * (T - 1), V]")
+    many = T > 1
+    st = lib().w12_verify_sampled(_typed_ptr(logits, logits.dtype, R * T * V, "logits"), F32 if logits.dtype is f32 else BF16,
+                                  _typed_ptr(draft_logits, draft_logits.dtype, n * V, "draft_logits") if many else None,
+                                  F32 if not many or draft_logits.dtype is f32 else BF16, R, T, V,
+                                  _typed_ptr(draft, i32, n, "draft") if many else None,
+                                  None if target_cut is None else target_cut.ref, None if draft_cut is None else draft_cut.ref,
+                                  _typed_ptr(u, f32, R * T, "u"), _typed_ptr(ratio_dev, f32, n, "ratio") if many else None,
+                                  _typed_ptr(accept_dev, i32, R, "accept"), _typed_ptr(next_dev, i32, R, "next"),
+                                  _ptr(ws_dev), ws_dev.nbytes, _stream_of(logits, stream))
+    if st:
+        raise W12Error(st, "w12_verify_sampled")
 
 
 # --------------------------------------------------------------- helpers

@@ -63,3 +63,24 @@ def test_fp4_checks(w12):
     assert L.w12_fp4_decode(ctypes.byref(one), None, None) == w12.ERR_ARG
     assert L.w12_fp4_decode(ctypes.byref(one), DEV + 4, None) == w12.ERR_ALIGN
     assert L.w12_fp4_decode(None, DEV, None) == w12.ERR_ARG
+
+
+def test_verify_sampled_checks(w12):
+    import ctypes
+    L = w12.lib()
+    C = w12._CCut
+
+    def call(x=DEV, xt=0, q=DEV, qt=1, R=2, T=3, V=100, d=DEV, tc=None, dc=None, u=DEV, ratio=None, acc=DEV, nxt=DEV, ws=DEV, wsb=1 << 20):
+        ref = lambda c: None if c is None else ctypes.byref(C(*c))  # noqa: E731
+        return L.w12_verify_sampled(x, xt, q, qt, R, T, V, d, ref(tc), ref(dc), u, ratio, acc, nxt, ws, wsb, None)
+
+    assert call(xt=2) == call(qt=2) == call(xt=-1) == w12.ERR_ARG
+    assert call(R=0) == call(T=0) == call(V=0) == call(V=w12.SAMPLE_MAX_V + 1) == call(R=1 << 25, T=2) == w12.ERR_SHAPE
+    assert call(x=None) == call(q=None) == call(d=None) == call(u=None) == call(acc=None) == call(nxt=None) == w12.ERR_ARG
+    assert call(x=DEV + 2) == call(q=DEV + 1) == call(u=DEV + 2) == call(d=DEV + 2) == call(ratio=DEV + 1) == w12.ERR_ALIGN
+    assert call(acc=DEV + 1) == call(nxt=DEV + 2) == w12.ERR_ALIGN
+    assert call(tc=(DEV + 2, None, None, None)) == call(dc=(None, DEV + 1, None, None)) == w12.ERR_ALIGN
+    assert call(tc=(None, None, DEV + 2, None)) == call(dc=(None, None, None, DEV + 2)) == w12.ERR_ALIGN
+    assert call(ws=None) == call(wsb=256) == w12.ERR_WORKSPACE
+    assert call(ws=DEV + 128) == w12.ERR_ALIGN
+    assert w12.verify_sampled_workspace_size(2, 3, 100) == 256 + 512
