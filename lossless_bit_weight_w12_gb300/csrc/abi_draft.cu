@@ -201,21 +201,41 @@ bool cut_aligned(const w12_cut *c) {
     return !c || (aligned(c->temperature, 4) && aligned(c->top_k, 4) && aligned(c->top_p, 4) && aligned(c->min_p, 4));
 }
 
-int cut_rows(const void *logits, int dtype, int64_t R, int64_t T, int64_t V, const w12_cut *cut, RowCut *out, void *stream) {
-    SampleArgs a = {};
-    a.logits = logits;
-    if (cut) a.temperature = cut->temperature, a.top_k = cut->top_k, a.top_p = cut->top_p, a.min_p = cut->min_p;
-    a.cut_out = out;
-    a.V = V, a.rows = R * T, a.R = R, a.T = T;
-    return launch_cut(a, dtype, stream);
+CutSide cut_side(const void *logits, int dtype, int64_t R, int64_t T, int64_t V, const w12_cut *cut, RowCut *out) {
+    CutSide s = {};
+    s.x = logits, s.f32 = dtype == W12_F32;
+    s.vec = aligned(logits, 16) && uint64_t(V) * size_of(dtype) % 16 == 0;
+    s.rows = R * T, s.T = T;
+    if (cut) s.temperature = cut->temperature, s.top_k = cut->top_k, s.top_p = cut->top_p, s.min_p = cut->min_p;
+    s.out = out;
+    return s;
+}
+
+}  // namespace
+
+namespace {
+
+struct VerifyPlan {
+    size_t cuts, arrived, parts, total;
+    int32_t each, pieces;
+};
+
+int plan_verify(int64_t R, int64_t T, int64_t V, VerifyPlan *p) {
+    if (R < 1 || T < 1 || V < 1 || V > W12_SAMPLE_MAX_V || R >= kLim31 || T >= kLim31 || R * T >= (int64_t(1) << 26))
+        return W12_ERR_SHAPE;
+    accept_pieces(R, V, &p->each, &p->pieces);
+    p->cuts = kWsHeader;
+    p->arrived = p->cuts + round256(uint64_t(R) * uint64_t(2 * T - 1) * sizeof(RowCut));
+    p->parts = p->arrived + round256(uint64_t(R) * 4u);
+    p->total = p->parts + round256(uint64_t(R) * uint64_t(p->pieces) * 16u);
+    return W12_OK;
 }
 
 }  // namespace
 
 extern "C" size_t w12_verify_sampled_workspace_size(int64_t R, int64_t T, int64_t V) {
-    if (R < 1 || T < 1 || V < 1 || V > W12_SAMPLE_MAX_V || R >= kLim31 || T >= kLim31 || R * T >= (int64_t(1) << 26))
-        return 0;
-    return kWsHeader + round256(uint64_t(R) * uint64_t(2 * T - 1) * sizeof(RowCut));
+    VerifyPlan p;
+    return plan_verify(R, T, V, &p) == W12_OK ? p.total : 0;
 }
 
 extern "C" int w12_verify_sampled(const void *logits, int dtype, const void *draft_logits, int draft_dtype, int64_t R, int64_t T,
@@ -223,23 +243,32 @@ extern "C" int w12_verify_sampled(const void *logits, int dtype, const void *dra
                                   const float *u, float *ratio, int32_t *accept_len, int32_t *next_tok, void *ws,
                                   size_t ws_bytes, void *stream) {
     if (!float_type(dtype) || (T > 1 && !float_type(draft_dtype))) return W12_ERR_ARG;
-    const size_t need = w12_verify_sampled_workspace_size(R, T, V);
-    if (need == 0) return W12_ERR_SHAPE;
+    VerifyPlan p;
+    const int st = plan_verify(R, T, V, &p);
+    if (st != W12_OK) return st;
     if (!logits || !u || !accept_len || !next_tok || (T > 1 && (!draft_logits || !draft))) return W12_ERR_ARG;
     if (!aligned(logits, size_of(dtype)) || (T > 1 && !aligned(draft_logits, size_of(draft_dtype))) || !aligned(u, 4) ||
         !aligned(ratio, 4) || !aligned(draft, 4) || !aligned(accept_len, 4) || !aligned(next_tok, 4) || !cut_aligned(target_cut) ||
         !cut_aligned(draft_cut))
         return W12_ERR_ALIGN;
-    if (!ws || ws_bytes < need) return W12_ERR_WORKSPACE;
+    if (!ws || ws_bytes < p.total) return W12_ERR_WORKSPACE;
     if (!aligned(ws, 256)) return W12_ERR_ALIGN;
     AcceptArgs a = {};
     a.logits = logits, a.draft_logits = draft_logits;
     a.f32 = dtype == W12_F32, a.draft_f32 = draft_dtype == W12_F32;
-    RowCut *cuts = reinterpret_cast<RowCut *>(static_cast<uint8_t *>(ws) + kWsHeader);
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    RowCut *cuts = reinterpret_cast<RowCut *>(w + p.cuts);
     a.cuts = cuts, a.draft_cuts = cuts + R * T;
     a.draft = draft, a.u = u, a.ratio = ratio, a.accept_len = accept_len, a.next_tok = next_tok;
     a.R = R, a.T = T, a.V = V;
-    int st = cut_rows(logits, dtype, R, T, V, target_cut, cuts, stream);
-    if (st == W12_OK && T > 1) st = cut_rows(draft_logits, draft_dtype, R, T - 1, V, draft_cut, cuts + R * T, stream);
-    return st == W12_OK ? launch_accept(a, stream) : st;
+    a.arrived = reinterpret_cast<uint32_t *>(w + p.arrived);
+    a.parts = reinterpret_cast<unsigned long long *>(w + p.parts);
+    a.each = p.each, a.pieces = p.pieces;
+    CutArgs c = {};
+    c.side[0] = cut_side(logits, dtype, R, T, V, target_cut, cuts);
+    if (T > 1) c.side[1] = cut_side(draft_logits, draft_dtype, R, T - 1, V, draft_cut, cuts + R * T);
+    c.V = V, c.err = reinterpret_cast<int *>(w), c.arrived = a.arrived;
+    c.cuts = c.side[0].top_k || c.side[0].top_p || c.side[1].top_k || c.side[1].top_p;
+    const int done = launch_cut(c, stream);
+    return done == W12_OK ? launch_accept(a, stream) : done;
 }

@@ -59,6 +59,38 @@ int fp4_variant(int64_t M);
 int fp4_occupancy(int variant, int *blocks);
 int launch_fp4(const Fp4Batch &b, bool e4m3, int grid, void *stream);
 
+// What the cuts leave of a row: a token stays if its weight (sample_device.cuh,
+// with mx and inv_t) is above w_thr, or equal with a composite of thr at least,
+// and not below floor_w.  one >= 0: that token alone.  total: the weight that
+// stays; 0: no token does.
+struct RowCut {
+    uint64_t thr, total;
+    float mx, inv_t;
+    uint32_t w_thr, floor_w;
+    int32_t one, inf;
+};
+
+// The cuts of the rows of two tensors of logits (the target's, the drafter's).
+struct CutSide {
+    const void *x;
+    int32_t f32;
+    int32_t vec;         // rows on 16-byte boundaries, whole 16-byte pieces
+    int64_t rows, T;     // T rows per request
+    const float *temperature, *top_p, *min_p;
+    const int32_t *top_k;
+    RowCut *out;
+};
+
+struct CutArgs {
+    CutSide side[2];
+    int64_t V;
+    int32_t chunk;       // logits per CTA of a row's cluster
+    int32_t cuts;        // a top_k or top_p is given
+    int *err;
+    uint32_t *arrived;   // [requests] set to zero, for launch_accept
+};
+int launch_cut(CutArgs &a, void *stream);
+
 struct AcceptArgs {
     const void *logits, *draft_logits;  // [R T][V], [R (T - 1)][V]
     int32_t f32, draft_f32;
@@ -68,7 +100,11 @@ struct AcceptArgs {
     float *ratio;
     int32_t *accept_len, *next_tok;
     int64_t R, T, V;
+    uint32_t *arrived;      // [R], zeros
+    unsigned long long *parts;  // [R][pieces][2]
+    int32_t each, pieces;   // tokens a piece, pieces a row
 };
+void accept_pieces(int64_t R, int64_t V, int32_t *each, int32_t *pieces);
 int launch_accept(const AcceptArgs &a, void *stream);
 
 }  // namespace w12

@@ -133,10 +133,6 @@ __device__ __forceinline__ int arg_bin(float d) {
     return b < kBins ? b : kBins - 1;
 }
 
-// Bins of weights, largest first: 64 per octave of [1, 2^31].
-__device__ __forceinline__ int weight_bin(uint32_t w) {
-    return int(((158u << 23) - __float_as_uint(__uint2float_rz(w))) >> 17);
-}
 static_assert((31 << 6) < kBins, "octaves of weights");
 
 // Which elements a histogram is over, from the second level on: lo <=
@@ -651,9 +647,8 @@ __device__ __forceinline__ u64 window_threshold(SampleSmall &sh, SampleCut &cut,
     return sh.thr;
 }
 
-// CUT: top_k or top_p may be asked for.  STAT: what the cuts leave is written
-// (a.cut_out) and nothing is drawn.
-template <int DT, bool CUT, bool STAT>
+// CUT: top_k or top_p may be asked for.
+template <int DT, bool CUT>
 __global__ void __launch_bounds__(kST, 2) sample_kernel(const __grid_constant__ SampleArgs a) {
     cg::cluster_group cl = cg::this_cluster();
     extern __shared__ __align__(16) unsigned char smem[];
@@ -685,7 +680,7 @@ __global__ void __launch_bounds__(kST, 2) sample_kernel(const __grid_constant__ 
     const int64_t req = r / a.T;
     const float t = a.temperature ? a.temperature[req] : 1.0f;
     const int32_t top_k = CUT && a.top_k ? a.top_k[req] : 0;
-    const bool few = CUT && !STAT && top_k > 0 && top_k < a.V && top_k <= kCap && t > 0.0f;  // the first top_k in one CTA
+    const bool few = CUT && top_k > 0 && top_k < a.V && top_k <= kCap && t > 0.0f;  // the first top_k in one CTA
     if (tid == 0) sh.last = 0;
     if (CUT)
         for (int i = tid; i < kBins; i += kST) cut.lo[i] = 0u;
@@ -977,9 +972,7 @@ __global__ void __launch_bounds__(kST, 2) sample_kernel(const __grid_constant__ 
                 }
                 add_up(wide ? 1 : 0);  // (not the slot of the sum before it)
             }
-            if (STAT) {
-                if (writer) a.cut_out[r] = {thr, total, row.mx, row.inv_t, w_thr, floor_w, -1, row.inf};
-            } else if (total > 0) {
+            if (total > 0) {
                 const u64 target = scaled(fixed_u(a.u[r]), total);
                 writer = false;
                 const uint32_t hit = __ballot_sync(0xFFFFFFFFu, before <= target && target < before + mine);
@@ -1005,14 +998,12 @@ __global__ void __launch_bounds__(kST, 2) sample_kernel(const __grid_constant__ 
             }
         }
     }
-    if (STAT && writer && (row.mx == -INFINITY || !(t > 0.0f)))
-        a.cut_out[r] = {0ull, token >= 0 ? 1ull << 31 : 0ull, row.mx, 1.0f, 0u, 1u, token, row.inf};
-    if (!STAT && writer) {  // one thread of the cluster
+    if (writer) {  // one thread of the cluster
         a.tokens[r] = token;
         if (a.prob) a.prob[r] = prob;
     }
     sync_relaxed();  // no CTA leaves while another may read its shared memory
-    if (STAT || !a.accept_len) return;
+    if (!a.accept_len) return;
     // ---- the CTA that has the last row's token applies the acceptance rule:
     // the thread that stored a token counts its row, as only it can order the
     // two (a release by the barrier above in its place: 16 rows 32.4 us, so 30.3)
@@ -1039,32 +1030,33 @@ __global__ void __launch_bounds__(kST, 2) sample_kernel(const __grid_constant__ 
 constexpr size_t kMostShared = 227 * 1024;
 constexpr size_t kTwoShared = 113 * 1024;  // two CTAs on an SM
 
-template <int DT, bool CUT, bool STAT>
+template <int DT, bool CUT>
 int run_t(const SampleArgs &a, int cs, void *stream) {
     static std::atomic<uint64_t> ready[4];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 256) return W12_ERR_CUDA;
     const uint64_t bit = uint64_t(1) << (dev & 63);
     if (!(ready[dev >> 6].load(std::memory_order_relaxed) & bit)) {
-        if (cudaFuncSetAttribute(sample_kernel<DT, CUT, STAT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMostShared)) !=
+        if (cudaFuncSetAttribute(sample_kernel<DT, CUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMostShared)) !=
                 cudaSuccess ||
-            cudaFuncSetAttribute(sample_kernel<DT, CUT, STAT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+            cudaFuncSetAttribute(sample_kernel<DT, CUT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
             return W12_ERR_CUDA;
         ready[dev >> 6].fetch_or(bit, std::memory_order_relaxed);
     }
     const size_t smem = kSmallBytes + (CUT ? kCutBytes : 0) +
                         (a.keep_w ? weights_at<DT>(a.chunk) + size_t(a.chunk) * 4
                                   : a.resident ? (size_t(a.chunk) * (DT == W12_F32 ? 4 : 2) + 15) / 16 * 16 : 0);
-    return launch_step(sample_kernel<DT, CUT, STAT>, int(a.rows * cs), kST, smem, cs, stream, a);
+    return launch_step(sample_kernel<DT, CUT>, int(a.rows * cs), kST, smem, cs, stream, a);
 }
 
-template <int DT, bool STAT>
+template <int DT>
 int run(const SampleArgs &a, int cs, void *stream) {
-    return a.top_k || a.top_p ? run_t<DT, true, STAT>(a, cs, stream) : run_t<DT, false, STAT>(a, cs, stream);
+    return a.top_k || a.top_p ? run_t<DT, true>(a, cs, stream) : run_t<DT, false>(a, cs, stream);
 }
 
-template <bool STAT>
-int plan_and_run(SampleArgs &a, int dtype, void *stream) {
+}  // namespace
+
+int launch_sample(SampleArgs &a, int dtype, void *stream) {
     const int es = dtype == W12_F32 ? 4 : 2;
     // Enough CTAs per row that each holds a few thousand logits, and the row
     // stays in shared memory.  16 for up to 14 rows: so many such clusters run
@@ -1079,13 +1071,7 @@ int plan_and_run(SampleArgs &a, int dtype, void *stream) {
     const size_t at = dtype == W12_F32 ? weights_at<W12_F32>(chunk) : weights_at<W12_BF16>(chunk);
     a.keep_w = (a.top_k || a.top_p) && kSmallBytes + kCutBytes + at + size_t(chunk) * 4 + 16 <= kTwoShared;
     a.vec = (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0 && (a.V * es) % 16 == 0;
-    return dtype == W12_F32 ? run<W12_F32, STAT>(a, cs, stream) : run<W12_BF16, STAT>(a, cs, stream);
+    return dtype == W12_F32 ? run<W12_F32>(a, cs, stream) : run<W12_BF16>(a, cs, stream);
 }
-
-}  // namespace
-
-int launch_sample(SampleArgs &a, int dtype, void *stream) { return plan_and_run<false>(a, dtype, stream); }
-
-int launch_cut(SampleArgs &a, int dtype, void *stream) { return plan_and_run<true>(a, dtype, stream); }
 
 }  // namespace w12

@@ -41,6 +41,11 @@ __device__ __forceinline__ u64 warp_scan64(u64 x, int lane) {
     return x;
 }
 
+// Bins of weights, largest first: 64 per octave of [1, 2^31].
+__device__ __forceinline__ int weight_bin(uint32_t w) {
+    return int(((158u << 23) - __float_as_uint(__uint2float_rz(w))) >> 17);
+}
+
 template <int DT>
 struct Row {
     const void *x;      // this CTA's chunk (shared or global memory)

@@ -113,17 +113,6 @@ int launch_attend_rest(const AttendArgs &a, int head_dim, int kv_dtype, void *st
 int launch_attend_tc(const AttendArgs &a, int head_dim, int kv_dtype, void *stream);
 int launch_attend_join(const AttendArgs &a, int head_dim, void *stream);
 
-// What the cuts leave of a row: a token stays if its weight (sample_device.cuh,
-// with mx and inv_t) is above w_thr, or equal with a composite of thr at least,
-// and not below floor_w.  one >= 0: that token alone.  total: the weight that
-// stays; 0: no token does.
-struct RowCut {
-    uint64_t thr, total;
-    float mx, inv_t;
-    uint32_t w_thr, floor_w;
-    int32_t one, inf;
-};
-
 struct SampleArgs {
     const void *logits;
     const float *temperature, *top_p, *min_p, *u;
@@ -136,10 +125,7 @@ struct SampleArgs {
     int32_t resident;   // the chunk fits in shared memory
     int32_t keep_w;     // and so do its weights
     int32_t vec;        // 16-byte loads: every chunk starts on a 16-byte boundary
-    RowCut *cut_out;    // of launch_cut
 };
 int launch_sample(SampleArgs &a, int dtype, void *stream);
-// The cuts of every row (a.cut_out) in place of draws.
-int launch_cut(SampleArgs &a, int dtype, void *stream);
 
 }  // namespace w12

@@ -83,4 +83,4 @@ def test_verify_sampled_checks(w12):
     assert call(tc=(None, None, DEV + 2, None)) == call(dc=(None, None, None, DEV + 2)) == w12.ERR_ALIGN
     assert call(ws=None) == call(wsb=256) == w12.ERR_WORKSPACE
     assert call(ws=DEV + 128) == w12.ERR_ALIGN
-    assert w12.verify_sampled_workspace_size(2, 3, 100) == 256 + 512
+    assert w12.verify_sampled_workspace_size(2, 3, 100) == 256 + 512 + 256 + 256
