@@ -39,13 +39,13 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kT = 256;             // threads per CTA
+constexpr int kT = 512, kPlainT = 256;  // threads per CTA, with cuts and without
 constexpr int kW = kT / 32;
 constexpr int kBins = 2048;
 constexpr int kPieces = 2;          // bulk copies of a CTA's part of the row
 constexpr int kMostCluster = 16;
 constexpr int kCap = 680;           // tokens that are gathered
-constexpr int kFew = 128;           // tokens that are ranked one against all
+constexpr int kFew = 256;           // tokens that are ranked one against all
 constexpr int kFine = 256;          // bins of the gathered tokens
 constexpr float kSpan = 22.25f;     // e^-22.25 rounds to weight 0
 
@@ -133,14 +133,15 @@ __device__ __forceinline__ void add_if(uint32_t addr, uint32_t v, uint32_t w, ui
 }
 
 // A block's sums of a and b (both in every thread of warp 0 when it returns).
+template <int W>
 __device__ __forceinline__ void block_sum2(Small &sh, u64 &a, u64 &b) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     a = warp_sum64(a), b = warp_sum64(b);
     if (lane == 0) sh.warp_a[warp] = a, sh.warp_b[warp] = b;
     __syncthreads();
     if (warp == 0) {
-        a = warp_sum64(lane < kW ? sh.warp_a[lane] : 0ull);
-        b = warp_sum64(lane < kW ? sh.warp_b[lane] : 0ull);
+        a = warp_sum64(lane < W ? sh.warp_a[lane] : 0ull);
+        b = warp_sum64(lane < W ? sh.warp_b[lane] : 0ull);
     }
 }
 
@@ -247,7 +248,7 @@ static_assert(2 * kFew <= kT, "two threads a token");
 // CUTS: a top_k or top_p may be given.
 template <int DT, bool CUTS>
 __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a, const CutSide &s, int64_t r, unsigned char *smem) {
-    constexpr int ES = DT == W12_F32 ? 4 : 2;
+    constexpr int ES = DT == W12_F32 ? 4 : 2, kT = CUTS ? w12::kT : kPlainT, kW = kT / 32;
     Small &sh = *reinterpret_cast<Small *>(smem);
     CutMem &cut = *reinterpret_cast<CutMem *>(smem + kSmallBytes);
     unsigned char *buf = smem + kSmallBytes + (CUTS ? kCutBytes : 0);
@@ -262,6 +263,21 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
     const unsigned char *src = static_cast<const unsigned char *>(s.x) + (r * a.V + c0) * ES;
     const int64_t req = r / s.T;
     const int n8 = (row.n + 7) / 8 * 8;
+    // (the request's numbers are on their way while the row is)
+    const float t = s.temperature ? s.temperature[req] : 1.0f;
+    uint32_t floor_w = 1;  // (above 2^31: no token stays)
+    if (s.min_p) {
+        const float m = s.min_p[req];
+        if (m > 0.0f) floor_w = max(1u, min(0x80000001u, __float2uint_ru(fminf(m, 1.5f) * kOne31)));
+    }
+    const int32_t top_k = CUTS && s.top_k ? s.top_k[req] : 0;
+    const bool by_k = CUTS && top_k > 0 && top_k < a.V;
+    uint64_t p_fix = 1ull << 24;
+    if (CUTS && s.top_p) {
+        const float p = rintf(s.top_p[req] * 16777216.0f);
+        if (p < 16777216.0f) p_fix = p > 0.0f ? uint64_t(p) : 0ull;  // (a NaN is no cut)
+    }
+    const bool by_p = CUTS && p_fix < (1ull << 24);
     float best = -INFINITY;
     uint32_t best2 = 0xFF80FF80u;  // a pair of bf16 -infinities
 
@@ -339,12 +355,6 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
         row.inf = m == INFINITY;
         row.mx = row.inf ? 0.0f : m;
     }
-    const float t = s.temperature ? s.temperature[req] : 1.0f;
-    uint32_t floor_w = 1;  // (above 2^31: no token stays)
-    if (s.min_p) {
-        const float m = s.min_p[req];
-        if (m > 0.0f) floor_w = max(1u, min(0x80000001u, __float2uint_ru(fminf(m, 1.5f) * kOne31)));
-    }
     if (row.mx == -INFINITY) {  // nothing can be sampled
         if (me == 0 && tid == 0) s.out[r] = RowCut{0ull, 0ull, 0.0f, 1.0f, 0u, 1u, -1, 0};
         return;
@@ -375,14 +385,6 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
         return;
     }
     row.inv_t = fminf(__fdiv_rn(1.0f, t), 3.402823466e38f);
-    const int32_t top_k = CUTS && s.top_k ? s.top_k[req] : 0;
-    const bool by_k = CUTS && top_k > 0 && top_k < a.V;
-    uint64_t p_fix = 1ull << 24;
-    if (CUTS && s.top_p) {
-        const float p = rintf(s.top_p[req] * 16777216.0f);
-        if (p < 16777216.0f) p_fix = p > 0.0f ? uint64_t(p) : 0ull;  // (a NaN is no cut)
-    }
-    const bool by_p = CUTS && p_fix < (1ull << 24);
     Small *root = cl.map_shared_rank(&sh, 0);
     u64 thr = 0, kept = 0;  // (the first CTA's)
     uint32_t w_thr = 0;
@@ -393,6 +395,29 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
     float slope = float(kBins - 1) / kSpan;
     const auto linear_bin = [&](float d) {
         return min(int(__float_as_uint(fmaf(d, -slope, kMagic)) - __float_as_uint(kMagic)), kBins - 1);
+    };
+    // The logits from x0 to x1: first marked, 64 at a time, then taken one by one (a
+    // warp goes through f as often as one of its lanes has marks).
+    const auto between = [&](float x0, float x1, auto f) {
+#pragma unroll 1
+        for (int q = 4 * tid; q < n8; q += 64 * kT) {
+            u64 marks = 0;
+#pragma unroll 2
+            for (int k = 0; k < 16; ++k) {
+                const int i = q + 4 * k * kT;
+                if (i >= n8) break;
+                float v[4];
+                row.raw4(i, v);
+                uint32_t m = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) m |= uint32_t(v[j] >= x0 && v[j] <= x1) << j;
+                marks |= u64(m) << (4 * k);
+            }
+            for (; marks; marks &= marks - 1) {
+                const int b = __ffsll(marks) - 1, i = q + 4 * (b >> 2) * kT + (b & 3);
+                f(i, DT == W12_F32 ? reinterpret_cast<const float *>(buf)[i] : bf16_bits_to_float(reinterpret_cast<const uint16_t *>(buf)[i]));
+            }
+        }
     };
     const auto each = [&](auto f) {  // f(index, logit) of the part's logits, the padding too
 #pragma unroll 2
@@ -456,7 +481,7 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
         for (uint32_t i = tid; i < n; i += kT)
             if (cut.list[i] >= thr && cut.list_w[i] >= least) mine += cut.list_w[i];
         __syncthreads();
-        block_sum2(sh, mine, none);
+        block_sum2<kW>(sh, mine, none);
         if (tid == 0) sh.kept = mine;
         __syncthreads();
         return sh.kept;
@@ -485,8 +510,8 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
             if (g.bin < 0) break;
             const u64 from = sh.from;
             u64 hi = 0, lo = ~0ull;
-            each([&](int i, float v) {
-                if (g.shift < 0 && !(v >= g.x0 && v <= g.x1) && !row.inf) return;
+            const bool bounds = g.shift < 0 && !row.inf;
+            between(bounds ? g.x0 : -INFINITY, bounds ? g.x1 : INFINITY, [&](int i, float v) {
                 v = row.clean(v);
                 const float d = row.arg(v);
                 if (i >= row.n || (g.shift < 0 && (linear_bin(d) != g.bin || !(d > -kSpan)))) return;
@@ -563,8 +588,7 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
         cl.sync();
         const float end = sh.level.x0;
         const float x0 = row.inf ? 0.0f : row.mx + end * t * 1.000001f - 1e-6f * fabsf(row.mx);
-        each([&](int i, float v) {
-            if (!(v >= x0)) return;
+        between(x0, INFINITY, [&](int i, float v) {
             v = row.clean(v);
             if (i >= row.n || !(row.arg(v) >= end)) return;
             const uint32_t w = row.weight(v);
@@ -619,18 +643,39 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
                 u64 total = 0;
                 if (!row.inf && from == 0 && floor_w <= 1) {
                     const uint32_t at = smem_addr(cut.lo), large = max(light, 65536u);
+                    // (a NaN has weight 0 by itself)
                     const auto sum = [&](auto bins) {
-                        each([&](int i, float v) {  // (a NaN has weight 0 by itself)
-                            const float d = row.arg(v);
-                            const uint32_t w = __float2uint_rn(expf(d) * kOne31);
-                            total = add_wide(total, w);
-                            if (decltype(bins)::value) {
-                                const uint32_t b = __float_as_uint(fminf(fmaf(d, -slope, kMagic), kMagic + float(kBins - 1)));
-                                const uint32_t to = at + (b << 2) - (__float_as_uint(kMagic) << 2);
-                                add_if(to, w & 0xFFFFu, w, light);
-                                add_if(to + 4u * kBins, w >> 16, w, large);
+                        constexpr int N = decltype(bins)::value ? 8 : 4;
+#pragma unroll 1
+                        for (int i = 4 * tid; i < n8; i += N * kT) {
+                            float v[N];
+                            uint32_t w[N], to[N];
+#pragma unroll
+                            for (int k = 0; k < N; k += 4) {
+                                float(&q)[4] = *reinterpret_cast<float(*)[4]>(&v[k]);
+                                if (k == 0 || i + k * kT < n8)
+                                    row.raw4(i + k * kT, q);
+                                else
+                                    q[0] = q[1] = q[2] = q[3] = -INFINITY;
                             }
-                        });
+#pragma unroll
+                            for (int j = 0; j < N; ++j) {
+                                const float d = row.arg(v[j]);
+                                w[j] = __float2uint_rn(expf(d) * kOne31);
+                                if (decltype(bins)::value) {
+                                    const uint32_t b = __float_as_uint(fminf(fmaf(d, -slope, kMagic), kMagic + float(kBins - 1)));
+                                    to[j] = at + (b << 2) - (__float_as_uint(kMagic) << 2);
+                                }
+                            }
+#pragma unroll
+                            for (int j = 0; j < N; ++j) {
+                                total = add_wide(total, w[j]);
+                                if (decltype(bins)::value) {
+                                    add_if(to[j], w[j] & 0xFFFFu, w[j], light);
+                                    add_if(to[j] + 4u * kBins, w[j] >> 16, w[j], large);
+                                }
+                            }
+                        }
                     };
                     if (CUTS && by_p)
                         sum(std::true_type());
@@ -651,7 +696,7 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
                         }
                     }
                 }
-                block_sum2(sh, total, heavy);
+                block_sum2<kW>(sh, total, heavy);
                 if (tid == 0) root->sums[0][me] = total, root->sums[1][me] = heavy;
                 if (CUTS && by_p)
                     add_up();
@@ -678,10 +723,11 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
 }
 
 template <bool CUTS>
-__global__ void __launch_bounds__(kT, CUTS ? 3 : 5) cut_kernel(const __grid_constant__ CutArgs a) {
+__global__ void __launch_bounds__(CUTS ? kT : kPlainT, CUTS ? 2 : 5) cut_kernel(const __grid_constant__ CutArgs a) {
     cg::cluster_group cl = cg::this_cluster();
     extern __shared__ __align__(128) unsigned char smem[];
     Small &sh = *reinterpret_cast<Small *>(smem);
+    constexpr int threads = CUTS ? kT : kPlainT;
     const int cs = int(cl.num_blocks());
     cluster_here();  // (its wait is behind the row's loads)
     if (threadIdx.x == 0) {
@@ -693,7 +739,7 @@ __global__ void __launch_bounds__(kT, CUTS ? 3 : 5) cut_kernel(const __grid_cons
     }
     if (CUTS) {
         uint32_t *h = reinterpret_cast<uint32_t *>(smem + kSmallBytes);
-        for (int i = threadIdx.x; i < 2 * kBins; i += kT) h[i] = 0u;
+        for (int i = threadIdx.x; i < 2 * kBins; i += threads) h[i] = 0u;
     }
     pdl_launch_dependents();
     __syncthreads();
@@ -724,7 +770,7 @@ int run(const CutArgs &a, int cs, int es, void *stream) {
         ready[dev >> 6].fetch_or(bit, std::memory_order_relaxed);
     }
     const size_t smem = kSmallBytes + (CUTS ? kCutBytes : 0) + size_t(a.chunk) * es;
-    return launch_step(cut_kernel<CUTS>, int((a.side[0].rows + a.side[1].rows) * cs), kT, smem, cs, stream, a);
+    return launch_step(cut_kernel<CUTS>, int((a.side[0].rows + a.side[1].rows) * cs), CUTS ? kT : kPlainT, smem, cs, stream, a);
 }
 
 }  // namespace
@@ -733,13 +779,13 @@ int launch_cut(CutArgs &a, void *stream) {
     const int es = a.side[0].f32 || (a.side[1].rows && a.side[1].f32) ? 4 : 2;
     const size_t over = kSmallBytes + (a.cuts ? kCutBytes : 0);
     const int64_t rows = a.side[0].rows + a.side[1].rows;
-    // As few CTAs a row as five (with cuts: three) fit on an SM, so that some of them
-    // compute while others load or wait; more where there are few rows.
-    const size_t most = (a.cuts ? 75 : 45) * 1024;
+    // As few CTAs a row as five (with cuts: two, of twice the threads) fit on an SM, so
+    // that some of them compute while others load or wait; more where there are few rows.
+    const size_t most = (a.cuts ? 113 : 45) * 1024;
     const auto chunk = [&](int cs) { return ((a.V + cs - 1) / cs + 7) / 8 * 8; };
     int cs = 1;
     while (cs < kMostCluster && over + size_t(chunk(cs)) * es > most) cs *= 2;
-    while (cs < kMostCluster && chunk(cs) > 2048 && rows * cs * 2 <= 456) cs *= 2;
+    while (cs < kMostCluster && chunk(cs) > 2048 && rows * cs * 2 <= 304) cs *= 2;
     a.chunk = int32_t(chunk(cs));
     static_assert(kSmallBytes + kCutBytes + (W12_SAMPLE_MAX_V / kMostCluster) * 4 <= kMostShared, "the largest row");
     static_assert(W12_SAMPLE_MAX_V / kMostCluster <= 65536, "16-bit halves of the weights");
