@@ -679,22 +679,22 @@ int w12_add_norm(const void *x_dev, int64_t x_stride, int x_dtype, const void *d
  *   W[k, n] = code[n, k] scales[n, k / 16] scale,
  * codes 0, 0.5, 1, 1.5, 2, 3, 4, 6 (bits 2-0) with bit 3 as the sign.  The
  * plain form has codes [N][K / 2] bytes, the even k in a byte's low four bits,
- * and scales [N][K / 16] bytes.  The products read a blob: for tile t of 128
+ * and scales [N][K / 16] bytes.  The products read a blob: for tile t of 256
  * columns and group kg of 128 k, unit t * K / 128 + kg is a block of
  * W12_FP4_UNIT_BYTES:
- *   [0, 8192)     codes: column c's 64 bytes at 64 c, four 16-byte chunks of
- *                 four 32-bit words; chunk j at j ^ ((c >> 1) & 3), its word q
- *                 holds k = 64 (q >> 1) + 16 j + 8 (q & 1) .. + 7: the even k in
- *                 the low half, the odd ones in the high half; of a half's
- *                 codes 0 .. 3 the magnitudes at bits 8-6, 5-3, 2-0, 11-9, the
- *                 signs at 15, 12, 14, 13
- *   [8192, 9216)  scales: column c's 8 at 8192 + 8 c, that of k / 16 = g at
- *                 2 (g & 3) + (g >> 2): 5 exponent bits (bias 9), 3 mantissa
- *                 bits, no sign (a negative scale turns the codes' signs); a zero
- *                 scale is 0 with zero codes, NaN is 0xAF
+ *   [0, 16384)      codes: column c's 64 bytes at 64 c, four 16-byte chunks of
+ *                   four 32-bit words; chunk j at j ^ ((c >> 1) & 3), its word q
+ *                   holds k = 64 (q >> 1) + 16 j + 8 (q & 1) .. + 7: the even k in
+ *                   the low half, the odd ones in the high half; of a half's
+ *                   codes 0 .. 3 the magnitudes at bits 8-6, 5-3, 2-0, 11-9, the
+ *                   signs at 15, 12, 14, 13
+ *   [16384, 18432)  scales: column c's 8 at 16384 + 8 c, that of k / 16 = g at
+ *                   2 (g & 3) + (g >> 2): 5 exponent bits (bias 9), 3 mantissa
+ *                   bits, no sign (a negative scale turns the codes' signs); a
+ *                   zero scale is 0 with zero codes, NaN is 0xAF
  * Columns past N are zeros.  K is a multiple of 128.
  */
-#define W12_FP4_UNIT_BYTES 9216
+#define W12_FP4_UNIT_BYTES 18432
 typedef struct w12_fp4 {
     const void *blob; /* w12_fp4_bytes(K, N) bytes on the device, 256-byte aligned */
     int64_t K, N;

@@ -42,10 +42,10 @@ int fp4_device(int variant, int *sms, int *blocks) {
 int check_fp4_shape(int64_t K, int64_t N) {
     if (K < kGroup || N < 1 || K % kGroup != 0 || K >= kLim31 || N >= kLim31) return W12_ERR_SHAPE;
     // units (and the threads that write them, one a column) in 32 bits
-    return (N + kTileCols - 1) / kTileCols < (int64_t(1) << 31) / (K / kGroup) / 2 ? W12_OK : W12_ERR_SHAPE;
+    return (N + kFp4Tile - 1) / kFp4Tile < (int64_t(1) << 31) / (K / kGroup) / 2 ? W12_OK : W12_ERR_SHAPE;
 }
 
-uint64_t fp4_units(int64_t K, int64_t N) { return uint64_t((N + kTileCols - 1) / kTileCols) * uint64_t(K / kGroup); }
+uint64_t fp4_units(int64_t K, int64_t N) { return uint64_t((N + kFp4Tile - 1) / kFp4Tile) * uint64_t(K / kGroup); }
 
 bool usable_scale(float s) { return s >= 0x1p-100f && s <= 0x1p100f; }
 
@@ -53,7 +53,7 @@ constexpr size_t kFp4Counters = 4096;  // (the same for all sizes: one workspace
 
 struct Fp4Plan {
     int64_t U, ubase[kMaxBatch];
-    size_t partial, total;
+    size_t partial, x[kMaxBatch], total;
     int grid;
 };
 
@@ -73,7 +73,12 @@ int plan_fp4(const w12_fp4 *w, int count, int64_t M, Fp4Plan *p) {
     p->grid = int(std::min<int64_t>(int64_t(sms) * blocks, p->U));
     if (size_t(p->grid) * 4u > kFp4Counters) return W12_ERR_CUDA;
     p->partial = kWsHeader + kFp4Counters;
-    p->total = p->partial + round256(uint64_t(p->grid) * 2u * uint64_t(M) * kTileCols * 4u);
+    size_t off = p->partial + round256(uint64_t(p->grid) * 2u * uint64_t(M) * kFp4Tile * 4u);
+    for (int i = 0; i < count; ++i) {  // the tokens in bf16, where they come in e4m3
+        p->x[i] = off;
+        if (fp4_variant(M) >= kFp4TcVariant) off += round256(uint64_t(M) * uint64_t(w[i].K) * 2u);
+    }
+    p->total = off;
     return W12_OK;
 }
 
@@ -179,7 +184,7 @@ extern "C" int w12_fp4_gemm_batched(const w12_fp4 *w, const void *const *x, int 
         g.x = x[i], g.x_scale = e4m3 ? x_scale[i] : nullptr, g.y = y[i];
         g.scale = w[i].scale;
         g.K = int32_t(w[i].K), g.N = int32_t(w[i].N), g.KG = int32_t(w[i].K / kGroup);
-        g.NB = int32_t((w[i].N + kTileCols - 1) / kTileCols);
+        g.NB = int32_t((w[i].N + kFp4Tile - 1) / kFp4Tile);
         g.ubase = int32_t(p.ubase[i]);
     }
     b.partial = reinterpret_cast<float *>(at + p.partial);
@@ -187,7 +192,17 @@ extern "C" int w12_fp4_gemm_batched(const w12_fp4 *w, const void *const *x, int 
     b.err = reinterpret_cast<int *>(at);
     b.count = count, b.M = int(M), b.y_dtype = y_dtype, b.U = int32_t(p.U);
     b.early_weights = (options & W12_OPT_EARLY_WEIGHTS) != 0;
-    return launch_fp4(b, e4m3, p.grid, stream);
+    if (fp4_variant(M) < kFp4TcVariant) return launch_fp4(b, e4m3, p.grid, stream);
+    if (e4m3)
+        for (int i = 0; i < count; ++i) {
+            int again = 0;  // (products that share their tokens share the copy)
+            while (again < i && x[again] != x[i]) ++again;
+            b.g[i].x = at + p.x[again];
+            if (again < i) continue;
+            const int done = launch_fp4_widen(x[i], at + p.x[i], M * w[i].K, stream);
+            if (done != W12_OK) return done;
+        }
+    return launch_fp4_tc(b, p.grid, stream);
 }
 
 extern "C" int w12_fp4_gemm(const w12_fp4 *w, const void *x, int x_dtype, const float *x_scale, int64_t M, void *y, int y_dtype,

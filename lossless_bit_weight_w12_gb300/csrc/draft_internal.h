@@ -25,11 +25,13 @@ struct NormArgs {
 int launch_norm(const NormArgs &a, int x_dtype, int delta_dtype, int out_dtype, bool vec, void *stream);
 
 // 4-bit weights.  Unit blocks as of the W12 format: unit t * KG + kg holds
-// the codes and scales of 128 columns x 128 k (include/w12.h).
+// the codes and scales of 256 columns x 128 k (include/w12.h).
 constexpr int kFp4Unit = W12_FP4_UNIT_BYTES;
-constexpr int kFp4Scales = 8192;  // the scales' place in a unit block
+constexpr int kFp4Tile = 256;
+constexpr int kFp4Scales = kFp4Tile * 64;  // the scales' place in a unit block
 
 struct Fp4One {
+    CUtensorMap tx;        // of x in bf16, for the tcgen05 kernel: boxes of 64 k x MP tokens
     const uint8_t *units;
     const void *x;         // [M][K] bf16, or e4m3 with
     const float *x_scale;  // [M]
@@ -41,7 +43,7 @@ struct Fp4One {
 
 struct Fp4Batch {
     Fp4One g[kMaxBatch];
-    float *partial;      // [grid][2][M][128] partial sums of split tiles
+    float *partial;      // [grid][2][M][256] partial sums of split tiles
     uint32_t *counters;  // [grid] arrivals of a split tile, by the CTA that has its first unit (zero between calls)
     int *err;
     int count, M, y_dtype;
@@ -52,12 +54,18 @@ struct Fp4Batch {
 int launch_fp4_pack(const uint8_t *codes, const uint8_t *scales, int64_t K, int64_t N, void *blob, void *stream);
 int launch_fp4_encode(const uint16_t *w, int64_t K, int64_t N, float scale, void *blob, void *stream);
 int launch_fp4_decode(const void *blob, int64_t K, int64_t N, float scale, float *out, void *stream);
-// The product kernel's variant for M tokens, and its CTAs per SM (the call also
-// raises the variant's shared-memory limit on the current device).
-constexpr int kFp4Variants = 5;
-int fp4_variant(int64_t M);
+// The product kernels' variant for M tokens (from kFp4TcVariant on: tcgen05), and
+// its CTAs per SM (the call also raises the variant's shared-memory limit on the
+// current device).
+constexpr int kFp4Variants = 5, kFp4TcVariant = 2;
+inline int fp4_variant(int64_t M) { return M <= 8 ? 0 : M <= 16 ? 1 : M <= 32 ? 2 : M <= 64 ? 3 : 4; }
 int fp4_occupancy(int variant, int *blocks);
+int fp4_tc_occupancy(int variant, int *blocks);
 int launch_fp4(const Fp4Batch &b, bool e4m3, int grid, void *stream);
+// x of b.g[i] is bf16 here; its tensor maps are made by the call.
+int launch_fp4_tc(Fp4Batch &b, int grid, void *stream);
+// n e4m3 codes as bf16 (n a multiple of 16).
+int launch_fp4_widen(const void *codes, void *out, int64_t n, void *stream);
 
 // What the cuts leave of a row: a token stays if its weight (sample_device.cuh,
 // with mx and inv_t) is above w_thr, or equal with a composite of thr at least,

@@ -19,6 +19,8 @@
 #include <cstdint>
 
 #include "device_common.cuh"
+#include "draft_internal.h"
+#include "stream_device.cuh"
 
 namespace w12 {
 
@@ -63,6 +65,13 @@ __device__ __forceinline__ uint32_t fp4_word(uint32_t nibbles) {
         w |= ((v & 7u) << mag[i >> 1] | ((v >> 3) & 1u) << sign[i >> 1]) << (16 * (i & 1));
     }
     return w;
+}
+
+// A split tile starts in one CTA, as its last, so that CTA's number names the
+// counter: as many for any matrix, and one workspace serves them all.
+__device__ __forceinline__ uint32_t *arrivals(const Fp4Batch &b, const Fp4One &, int first, int) {
+    const int G = int(gridDim.x);
+    return &b.counters[sk_cta_of(first, b.U / G, b.U % G)];
 }
 
 }  // namespace w12

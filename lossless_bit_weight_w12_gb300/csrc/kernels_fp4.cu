@@ -1,17 +1,18 @@
 // kernels_fp4.cu -- products with 4-bit weights: y = x W^T, the weights e2m1
 // codes with an e4m3 scale for 16 consecutive k and one fp32 number for the
-// matrix; their packing into unit blocks, their encoding from bf16.
+// matrix; their packing into unit blocks, their encoding from bf16.  (More than 16
+// tokens: kernels_fp4_tc.cu.)
 //
 // A step of the product reads every weight once, 0.5625 bytes each, so the
-// kernel is a weight stream as the W12 one is: units of 128 columns x 128 k
-// (9216 contiguous bytes, one bulk copy), dealt out over the GPU as one line
+// kernel is a weight stream as the W12 one is: units of 256 columns x 128 k
+// (18432 contiguous bytes, one bulk copy), dealt out over the GPU as one line
 // (stream-K), a ring of shared-memory stages, split tiles finished by a fix-up
-// in CTA order (stream_device.cuh).  The tokens' part of a unit comes through
-// extra warps that read x, turn e4m3 codes into bf16 (exactly) and store it
-// beside the unit's weights.
+// in CTA order (stream_device.cuh).  The tokens' part of a unit comes through an
+// extra warp that reads x some units ahead, turns e4m3 codes into bf16 (exactly)
+// and stores it beside the unit's weights.
 //
 // Eight warps multiply (mma.m16n8k16, weights as operand A): warp w has columns
-// 16 w .. 16 w + 15, a lane 32 weights of two of them, expanded in registers
+// 32 w .. 32 w + 31, a lane 32 weights of four of them, expanded in registers
 // (fp4_device.cuh).  The tensor core's own sums run over one unit only; they are
 // added up in fp32 by the lanes, so their truncation does not pile up.
 #include <cuda_runtime.h>
@@ -23,32 +24,26 @@
 
 namespace w12 {
 
-// A split tile starts in one CTA, as its last, so that CTA's number names the
-// counter: as many for any matrix, and one workspace serves them all.
-__device__ __forceinline__ uint32_t *arrivals(const Fp4Batch &b, const Fp4One &, int first, int) {
-    const int G = int(gridDim.x);
-    return &b.counters[sk_cta_of(first, b.U / G, b.U % G)];
-}
-
 namespace {
 
 constexpr int kCW = 8;             // warps that multiply
 constexpr int kCT = kCW * 32;
 constexpr int kXRow = 256 + 16;    // a token's 128 activations: rows 16 bytes apart in the banks
 
-// NT tokens' tiles of 8.  One x warp for up to 16 tokens, four above.
+// NT tiles of 8 tokens.  kAhead: units that the x warp reads ahead of the one it
+// stores (a unit's x takes about a microsecond to arrive, the unit's share of the
+// weight stream half of one).
 template <int NT>
 struct FCfg {
     static constexpr int MP = 8 * NT;
-    static constexpr int XW = NT <= 2 ? 1 : 4;
-    static constexpr int kThreads = (kCW + 1 + XW) * 32;
-    static constexpr int MINB = NT <= 4 ? 2 : 1;
+    static constexpr int kThreads = (kCW + 2) * 32;
+    static constexpr int kPer = 4 * NT;     // 16-byte pieces of bf16 x per lane and unit, at most
+    static constexpr int kAhead = NT == 1 ? 3 : 2;
     static constexpr int kStage = kFp4Unit + MP * kXRow;
-    static constexpr int kBars = 1024;  // barriers and scalars, after the ring
-    static constexpr int kFit = ((227 * 1024) / MINB - 1024 - kBars) / kStage;
-    static constexpr int S = kFit > 12 ? 12 : kFit;
+    static constexpr int kBars = 1024;      // barriers and scalars, after the ring
+    static constexpr int S = (227 * 1024 / 2 - 1024 - kBars) / kStage;
     static constexpr size_t kSmem = size_t(S) * kStage + kBars;
-    static_assert(S >= 2 && (2 * S) * 8 + 64 <= kBars, "ring");
+    static_assert(S >= 3 && (2 * S) * 8 + 64 <= kBars, "ring");
 };
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -78,7 +73,7 @@ __device__ __forceinline__ uint2 e4m3x4_to_bf16(uint32_t w) {
 }
 
 template <int NT, bool E4M3>
-__global__ void __launch_bounds__(FCfg<NT>::kThreads, FCfg<NT>::MINB) fp4_kernel(const __grid_constant__ Fp4Batch b) {
+__global__ void __launch_bounds__(FCfg<NT>::kThreads, 2) fp4_kernel(const __grid_constant__ Fp4Batch b) {
     using C = FCfg<NT>;
     constexpr int S = C::S;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -98,7 +93,7 @@ __global__ void __launch_bounds__(FCfg<NT>::kThreads, FCfg<NT>::MINB) fp4_kernel
     }
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(&full[s], 1 + C::XW);  // the weights' copy (and its bytes), the x warps
+            mbar_init(&full[s], 2);  // the weights' copy (and its bytes), the x warp
             mbar_init(&empty[s], kCW);
         }
         ctl.abort = 0;
@@ -138,98 +133,127 @@ __global__ void __launch_bounds__(FCfg<NT>::kThreads, FCfg<NT>::MINB) fp4_kernel
 
     if (warp > kCW) {
         // -------------------------------------------------------- tokens
-        const int xt = threadIdx.x - (kCW + 1) * 32;  // of XW * 32
-        constexpr int kPer = E4M3 ? 8 : 16;           // 16-byte pieces of a token's part in global memory
-        SCur c = s_at(b, u0);
-        for (int u = u0, i = 0; u < u1; ++u, ++i) {
-            const int s = i % S;
-            const Fp4One &g = b.g[c.gi];
-            const uint8_t *x = static_cast<const uint8_t *>(g.x) + size_t(c.kg) * (E4M3 ? 128 : 256);
+        constexpr int kPer = E4M3 ? 8 : 16, P = E4M3 ? C::kPer / 2 : C::kPer;  // 16-byte pieces: of a token's part, of a lane's
+        uint4 v[C::kAhead][P];
+        SCur ahead = s_at(b, u0);
+        const auto read = [&](uint4(&to)[P]) {  // unit `ahead`, then the next one
+            const Fp4One &g = b.g[ahead.gi];
+            const uint8_t *x = static_cast<const uint8_t *>(g.x) + size_t(ahead.kg) * (E4M3 ? 128 : 256);
             const size_t row = size_t(g.K) * (E4M3 ? 1 : 2);
-            if (i >= S) mbar_wait(&empty[s], uint32_t(i / S - 1) & 1u, &ctl, b.err);
-            const uint32_t st = base + uint32_t(s) * C::kStage + kFp4Unit;
-            for (int p = xt; p < M * kPer; p += C::XW * 32) {
-                const uint4 v = ldg_v4(x + size_t(p / kPer) * row + 16 * (p % kPer));
-                const uint32_t at = st + uint32_t(p / kPer) * kXRow + uint32_t(p % kPer) * (E4M3 ? 32u : 16u);
-                if (E4M3) {
-                    const uint2 a = e4m3x4_to_bf16(v.x), d = e4m3x4_to_bf16(v.y), e = e4m3x4_to_bf16(v.z), f = e4m3x4_to_bf16(v.w);
-                    sts128(at, make_uint4(a.x, a.y, d.x, d.y));
-                    sts128(at + 16u, make_uint4(e.x, e.y, f.x, f.y));
-                } else {
-                    sts128(at, v);
-                }
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+                const int p = lane + 32 * q;
+                if (p < M * kPer) to[q] = ldg_v4(x + size_t(p / kPer) * row + 16 * (p % kPer));
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&full[s]);
-            s_next(b, c);
+            s_next(b, ahead);
+        };
+#pragma unroll
+        for (int d = 0; d < C::kAhead; ++d)
+            if (u0 + d < u1) read(v[d]);
+        for (int u = u0; u < u1; u += C::kAhead) {
+#pragma unroll
+            for (int d = 0; d < C::kAhead; ++d) {
+                if (u + d >= u1) break;
+                const int i = u + d - u0, s = i % S;
+                if (i >= S) mbar_wait(&empty[s], uint32_t(i / S - 1) & 1u, &ctl, b.err);
+                const uint32_t st = base + uint32_t(s) * C::kStage + kFp4Unit;
+#pragma unroll
+                for (int q = 0; q < P; ++q) {
+                    const int p = lane + 32 * q;
+                    if (p >= M * kPer) continue;
+                    const uint32_t at = st + uint32_t(p / kPer) * kXRow + uint32_t(p % kPer) * (E4M3 ? 32u : 16u);
+                    const uint4 &y = v[d][q];
+                    if (E4M3) {
+                        const uint2 a = e4m3x4_to_bf16(y.x), f = e4m3x4_to_bf16(y.y), e = e4m3x4_to_bf16(y.z), h = e4m3x4_to_bf16(y.w);
+                        sts128(at, make_uint4(a.x, a.y, f.x, f.y));
+                        sts128(at + 16u, make_uint4(e.x, e.y, h.x, h.y));
+                    } else {
+                        sts128(at, y);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[s]);
+                if (u + d + C::kAhead < u1) read(v[d]);
+            }
         }
         return;
     }
 
     // ------------------------------------------------------------ products
     const int g8 = lane >> 2, t = lane & 3;
-    const int ra = 16 * warp + g8;  // tile column of fragment row g8 (and ra + 8: the same chunk order)
-    const uint32_t pa = uint32_t(ra * 64 + 16 * fp4_chunk_at(ra, t)), pb = pa + 8u * 64u;
-    const uint32_t sa = uint32_t(kFp4Scales + ra * 8 + 2 * t), sb = sa + 64u;
+    const int ra = 32 * warp + g8;  // tile column of fragment row g8 (and ra + 8, 16, 24: the same chunk order)
+    const uint32_t pa = uint32_t(ra * 64 + 16 * fp4_chunk_at(ra, t));
+    const uint32_t sa = uint32_t(kFp4Scales + ra * 8 + 2 * t);
     const uint32_t xa = uint32_t(kFp4Unit + g8 * kXRow + 32 * t);  // k 16 t .. of token g8
     SCur c = s_at(b, u0);
-    int i = 0;
+    int s = 0;
+    uint32_t ph = 0;
     for (int u = u0; u < u1;) {
         const Fp4One &g = b.g[c.gi];
         const int nb = c.nb, first = g.ubase + nb * g.KG;
         const int ua = u, ub = min(u1, first + g.KG);
-        float acc[NT][4];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-        for (; u < ub; ++u, ++i) {
-            const int s = i % S;
-            mbar_wait(&full[s], uint32_t(i / S) & 1u, &ctl, b.err);
+        float acc[2][NT][4] = {};
+        for (; u < ub; ++u) {
+            mbar_wait(&full[s], ph, &ctl, b.err);
             const uint32_t st = base + uint32_t(s) * C::kStage;
-            const uint4 ca = lds128(st + pa), cb = lds128(st + pb);
-            const uint32_t fa = lds16(st + sa), fb = lds16(st + sb);
-            const uint32_t wa[4] = {ca.x, ca.y, ca.z, ca.w}, wb[4] = {cb.x, cb.y, cb.z, cb.w};
-            float part[NT][4];
+            uint32_t w[4][4], f[4];  // rows ra + 8 r: codes and scales
 #pragma unroll
-            for (int j = 0; j < NT; ++j) part[j][0] = part[j][1] = part[j][2] = part[j][3] = 0.f;
+            for (int r = 0; r < 4; ++r) {
+                const uint4 v = lds128(st + pa + uint32_t(r) * 512u);
+                w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
+                f[r] = lds16(st + sa + uint32_t(r) * 64u);
+            }
+            float part[2][NT][4] = {};
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                // words 0 and 1: the scale of k 16 t .., words 2 and 3: of k 64 + 16 t ..
-                const uint32_t da = fp4_scale2(prmt2(fa, 0u, q < 2 ? 0x4040u : 0x4141u));
-                const uint32_t db = fp4_scale2(prmt2(fb, 0u, q < 2 ? 0x4040u : 0x4141u));
-                uint32_t va[4], vb[4];
-                fp4_expand(wa[q], da, va);
-                fp4_expand(wb[q], db, vb);
+                uint4 bx[NT];
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    const uint4 bx = lds128(st + xa + uint32_t(j * 8 * kXRow + 128 * (q >> 1) + 16 * (q & 1)));
-                    mma_16816(part[j], va[0], vb[0], va[1], vb[1], bx.x, bx.y);
-                    mma_16816(part[j], va[2], vb[2], va[3], vb[3], bx.z, bx.w);
+                for (int j = 0; j < NT; ++j) bx[j] = lds128(st + xa + uint32_t(j * 8 * kXRow + 128 * (q >> 1) + 16 * (q & 1)));
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    // words 0 and 1: the scale of k 16 t .., words 2 and 3: of k 64 + 16 t ..
+                    const uint32_t da = fp4_scale2(prmt2(f[2 * h], 0u, q < 2 ? 0x4040u : 0x4141u));
+                    const uint32_t db = fp4_scale2(prmt2(f[2 * h + 1], 0u, q < 2 ? 0x4040u : 0x4141u));
+                    uint32_t va[4], vb[4];
+                    fp4_expand(w[2 * h][q], da, va);
+                    fp4_expand(w[2 * h + 1][q], db, vb);
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        mma_16816(part[h][j], va[0], vb[0], va[1], vb[1], bx[j].x, bx[j].y);
+                        mma_16816(part[h][j], va[2], vb[2], va[3], vb[3], bx[j].z, bx[j].w);
+                    }
                 }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);
+            if (++s == S) s = 0, ph ^= 1u;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[h][j][e] += part[h][j][e];
+        }
+        // acc[h][j][0..1]: column ra + 16 h, tokens 8 j + 2 t, + 1; [2..3]: column ra + 16 h + 8
+        const bool whole = ua == first && ub == first + g.KG;
+        float *P = b.partial + (size_t(blockIdx.x) * 2 + (ua == u0 ? 0 : 1)) * size_t(M) * kFp4Tile;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[j][e] += part[j][e];
-        }
-        // acc[j][0..1]: column ra, tokens 8 j + 2 t, + 1; [2..3]: column ra + 8
-        const bool whole = ua == first && ub == first + g.KG;
-        float *P = b.partial + (size_t(blockIdx.x) * 2 + (ua == u0 ? 0 : 1)) * size_t(M) * kTileN;
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int m = 8 * j + 2 * t + (e & 1), r = e < 2 ? ra : ra + 8, n = nb * kTileN + r;
-                if (m >= M) continue;
-                float v = acc[j][e] * (kFp4Back * g.scale);
-                if (E4M3) v *= __ldg(g.x_scale + m);
-                if (!whole)
-                    P[m * kTileN + r] = v;
-                else if (n < g.N)
-                    store_out(g.y, b.y_dtype, g.N, m, n, v);
-            }
-        if (!whole) stream_fixup<false>(b, g, first, nb, ub - ua, &s_last, threadIdx.x, kCT, static_cast<unsigned long long *>(nullptr));
+                for (int e = 0; e < 4; ++e) {
+                    const int m = 8 * j + 2 * t + (e & 1), r = ra + 16 * h + (e < 2 ? 0 : 8), n = nb * kFp4Tile + r;
+                    if (m >= M) continue;
+                    float v = acc[h][j][e] * (kFp4Back * g.scale);
+                    if (E4M3) v *= __ldg(g.x_scale + m);
+                    if (!whole)
+                        P[m * kFp4Tile + r] = v;
+                    else if (n < g.N)
+                        store_out(g.y, b.y_dtype, g.N, m, n, v);
+                }
+        if (!whole)
+            stream_fixup<false, kFp4Tile>(b, g, first, nb, ub - ua, &s_last, threadIdx.x, kCT, static_cast<unsigned long long *>(nullptr));
         s_next_tile(b, c);
     }
 }
@@ -261,7 +285,7 @@ int occ_nt(int *blocks) {
 
 // The unit block place of (column n, 128-k group kg).
 __device__ __forceinline__ uint8_t *unit_of(uint8_t *blob, int64_t n, int64_t kg, int64_t KG) {
-    return blob + ((n / kTileCols) * KG + kg) * kFp4Unit;
+    return blob + ((n / kFp4Tile) * KG + kg) * kFp4Unit;
 }
 
 // Writes column `col` of a unit block: its 16 words of codes (in k order, 8
@@ -317,7 +341,7 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const uint8_t *codes
         }
         s = *reinterpret_cast<const uint64_t *>(scales + (n * KG + kg) * 8);
     }
-    store_column(unit_of(blob, n, kg, KG), int(n % kTileCols), words, s);
+    store_column(unit_of(blob, n, kg, KG), int(n % kFp4Tile), words, s);
 }
 
 __device__ __forceinline__ float e4m3_value(uint32_t byte) {
@@ -374,7 +398,7 @@ __global__ void __launch_bounds__(kPackThreads) encode_kernel(const uint16_t *w,
             scales |= uint64_t(s) << (8 * gq);
         }
     }
-    store_column(unit_of(blob, n, kg, KG), int(n % kTileCols), words, scales);
+    store_column(unit_of(blob, n, kg, KG), int(n % kFp4Tile), words, scales);
 }
 
 // Back to fp32 [N][K]: code times scale (exact) times the matrix's number.
@@ -385,7 +409,7 @@ __global__ void __launch_bounds__(kPackThreads) decode_kernel(const uint8_t *blo
     const int64_t n = i / KG, kg = i % KG;
     if (n >= N) return;
     const uint8_t *unit = unit_of(const_cast<uint8_t *>(blob), n, kg, KG);
-    const int col = int(n % kTileCols);
+    const int col = int(n % kFp4Tile);
     float *o = out + (n * KG + kg) * 128;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -415,10 +439,32 @@ int pack_grid(int64_t columns, int64_t KG, unsigned *grid) {
 
 int launched() { return cudaGetLastError() == cudaSuccess ? W12_OK : W12_ERR_CUDA; }
 
+// n16 x 16 codes, 16 a thread.
+struct WidenArgs {
+    const uint4 *codes;
+    uint4 *out;
+    int64_t n16;
+};
+__global__ void __launch_bounds__(256) widen_kernel(const __grid_constant__ WidenArgs a) {
+    pdl_launch_dependents();
+    pdl_wait_previous();
+    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= a.n16) return;
+    const uint4 y = a.codes[i];
+    const uint2 p = e4m3x4_to_bf16(y.x), f = e4m3x4_to_bf16(y.y), e = e4m3x4_to_bf16(y.z), h = e4m3x4_to_bf16(y.w);
+    a.out[2 * i] = make_uint4(p.x, p.y, f.x, f.y);
+    a.out[2 * i + 1] = make_uint4(e.x, e.y, h.x, h.y);
+}
+
 }  // namespace
 
+int launch_fp4_widen(const void *codes, void *out, int64_t n, void *stream) {
+    const WidenArgs a{static_cast<const uint4 *>(codes), static_cast<uint4 *>(out), n / 16};
+    return launch_step(widen_kernel, int((a.n16 + 255) / 256), 256, 0, 1, stream, a);
+}
+
 int launch_fp4_pack(const uint8_t *codes, const uint8_t *scales, int64_t K, int64_t N, void *blob, void *stream) {
-    const int64_t NP = (N + kTileCols - 1) / kTileCols * kTileCols, KG = K / kGroup;
+    const int64_t NP = (N + kFp4Tile - 1) / kFp4Tile * kFp4Tile, KG = K / kGroup;
     unsigned grid;
     const int st = pack_grid(NP, KG, &grid);
     if (st != W12_OK) return st;
@@ -427,7 +473,7 @@ int launch_fp4_pack(const uint8_t *codes, const uint8_t *scales, int64_t K, int6
 }
 
 int launch_fp4_encode(const uint16_t *w, int64_t K, int64_t N, float scale, void *blob, void *stream) {
-    const int64_t NP = (N + kTileCols - 1) / kTileCols * kTileCols, KG = K / kGroup;
+    const int64_t NP = (N + kFp4Tile - 1) / kFp4Tile * kFp4Tile, KG = K / kGroup;
     unsigned grid;
     const int st = pack_grid(NP, KG, &grid);
     if (st != W12_OK) return st;
@@ -443,27 +489,16 @@ int launch_fp4_decode(const void *blob, int64_t K, int64_t N, float scale, float
     return launched();
 }
 
-int fp4_variant(int64_t M) { return M <= 8 ? 0 : M <= 16 ? 1 : M <= 32 ? 2 : M <= 64 ? 3 : 4; }
-
 int fp4_occupancy(int variant, int *blocks) {
     switch (variant) {
         case 0: return occ_nt<1>(blocks);
         case 1: return occ_nt<2>(blocks);
-        case 2: return occ_nt<4>(blocks);
-        case 3: return occ_nt<8>(blocks);
-        case 4: return occ_nt<16>(blocks);
     }
-    return W12_ERR_ARG;
+    return fp4_tc_occupancy(variant, blocks);
 }
 
 int launch_fp4(const Fp4Batch &b, bool e4m3, int grid, void *stream) {
-    switch (fp4_variant(b.M)) {
-        case 0: return launch_t<1>(b, e4m3, grid, stream);
-        case 1: return launch_t<2>(b, e4m3, grid, stream);
-        case 2: return launch_t<4>(b, e4m3, grid, stream);
-        case 3: return launch_t<8>(b, e4m3, grid, stream);
-    }
-    return launch_t<16>(b, e4m3, grid, stream);
+    return fp4_variant(b.M) == 0 ? launch_t<1>(b, e4m3, grid, stream) : launch_t<2>(b, e4m3, grid, stream);
 }
 
 }  // namespace w12

@@ -90,7 +90,7 @@ __device__ __forceinline__ void s_next(const Batch &b, SCur &c) {
 // CTA order (the same bits on every call), writes y and resets the counter.
 __device__ __forceinline__ uint32_t *arrivals(const StreamBatch &, const StreamOne &g, int, int nb) { return &g.counters[nb]; }
 
-template <bool FUSED, class Batch, class One>
+template <bool FUSED, int TILE = kTileN, class Batch, class One>
 __device__ __forceinline__ void stream_fixup(const Batch &b, const One &g, int first, int nb,
                                              int count, int *s_last, int tid, int nthreads,
                                              unsigned long long *s_best) {
@@ -106,8 +106,8 @@ __device__ __forceinline__ void stream_fixup(const Batch &b, const One &g, int f
         const int G = int(gridDim.x), per = b.U / G, rem = b.U % G;
         const int c_first = sk_cta_of(first, per, rem), c_last = sk_cta_of(first + g.KG - 1, per, rem);
         const int M = b.M;
-        const size_t slot_floats = size_t(M) * kTileN;
-        const int total = M * (kTileN / 4);
+        const size_t slot_floats = size_t(M) * TILE;
+        const int total = M * (TILE / 4);
         // four outputs per thread and round trip, summed in CTA order (the
         // same bits on every call)
         for (int o0 = tid; o0 < total; o0 += 4 * nthreads) {
@@ -139,8 +139,8 @@ __device__ __forceinline__ void stream_fixup(const Batch &b, const One &g, int f
             for (int k = 0; k < 4; ++k) {
                 const int o = o0 + k * nthreads;
                 if (o >= total) break;
-                const int m = o / (kTileN / 4), c4 = o % (kTileN / 4);
-                const int n0 = nb * kTileN + 4 * c4;
+                const int m = o / (TILE / 4), c4 = o % (TILE / 4);
+                const int n0 = nb * TILE + 4 * c4;
                 const float r[4] = {acc[k].x, acc[k].y, acc[k].z, acc[k].w};
                 unsigned long long best = 0ull;
 #pragma unroll
