@@ -48,6 +48,7 @@ struct Fp4Batch {
     int *err;
     int count, M, y_dtype;
     int32_t U;
+    int32_t grain;      // units that stay together in a CTA: 1, or a tile's (nothing is split)
     int early_weights;  // the first weight copies do not wait for the kernel before
 };
 

@@ -74,4 +74,11 @@ __device__ __forceinline__ uint32_t *arrivals(const Fp4Batch &b, const Fp4One &,
     return &b.counters[sk_cta_of(first, b.U / G, b.U % G)];
 }
 
+// The units of this CTA.
+__device__ __forceinline__ void fp4_units(const Fp4Batch &b, int &u0, int &u1) {
+    const int n = b.U / b.grain, G = int(gridDim.x), c = int(blockIdx.x), per = n / G, rem = n % G;
+    u0 = sk_unit_begin(c, per, rem) * b.grain;
+    u1 = u0 + (per + (c < rem ? 1 : 0)) * b.grain;
+}
+
 }  // namespace w12

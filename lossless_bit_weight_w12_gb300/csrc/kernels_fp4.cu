@@ -85,12 +85,7 @@ __global__ void __launch_bounds__(FCfg<NT>::kThreads, 2) fp4_kernel(const __grid
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int M = b.M;
     int u0, u1;
-    {
-        const int G = int(gridDim.x), c = int(blockIdx.x);
-        const int per = b.U / G, rem = b.U % G;
-        u0 = sk_unit_begin(c, per, rem);
-        u1 = u0 + per + (c < rem ? 1 : 0);
-    }
+    fp4_units(b, u0, u1);
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(&full[s], 2);  // the weights' copy (and its bytes), the x warp

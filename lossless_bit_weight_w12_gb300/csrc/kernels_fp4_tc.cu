@@ -105,12 +105,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_tc_kernel(const __grid_consta
     const uint32_t xbase = smem_addr(smem), wbase = xbase + uint32_t(SX * C::kX);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int u0, u1;
-    {
-        const int G = int(gridDim.x), c = int(blockIdx.x);
-        const int per = b.U / G, rem = b.U % G;
-        u0 = sk_unit_begin(c, per, rem);
-        u1 = u0 + per + (c < rem ? 1 : 0);
-    }
+    fp4_units(b, u0, u1);
     if (threadIdx.x == 0) {
         for (int s = 0; s < SW; ++s) mbar_init(&bar.full_w[s], 1), mbar_init(&bar.empty_w[s], kDW);
         for (int s = 0; s < SX; ++s) mbar_init(&bar.full_x[s], 1), mbar_init(&bar.empty_x[s], 2);
@@ -271,23 +266,41 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_tc_kernel(const __grid_consta
         const bool whole = ua == first && ub == first + g.KG;
         const int n = nb * kFp4Tile + col;
         float *P = b.partial + (size_t(blockIdx.x) * 2 + (ua == u0 ? 0 : 1)) * size_t(M) * kFp4Tile;
+        // (rolled: a piece of code that runs once costs an SM 250 cycles per 128 bytes of it)
         const float back = kFp4Back * g.scale;
-#pragma unroll
-        for (int q = 0; q < MP / 2; q += 16) {
+        const int m0 = h * (MP / 2), left = min(M - m0, MP / 2);
+        float *part = P + m0 * kFp4Tile + col;
+        const size_t at = size_t(m0) * g.N + n;
+        float *yf = static_cast<float *>(g.y) + at;
+        __nv_bfloat16 *yb = static_cast<__nv_bfloat16 *>(g.y) + at;
+#pragma unroll 1
+        for (int q = 0; q < left; q += 16) {
             uint32_t z[16];
-            tmem_load16(tmem + lanes + uint32_t(t * MP + h * (MP / 2) + q), z);
+            tmem_load16(tmem + lanes + uint32_t(t * MP + m0 + q), z);
             tmem_wait_ld();
             tmem_landed16(z);
+            float v[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int m = h * (MP / 2) + q + e;
-                if (m >= M) break;
-                float y = __uint_as_float(z[e]) * back;
-                if (g.x_scale) y *= __ldg(g.x_scale + m);
-                if (!whole)
-                    P[m * kFp4Tile + col] = y;
-                else if (n < g.N)
-                    store_out(g.y, b.y_dtype, g.N, m, n, y);
+            for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(z[e]) * back;
+            if (g.x_scale)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (q + e < left) v[e] *= __ldg(g.x_scale + m0 + q + e);
+            if (!whole) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (q + e < left) part[e * kFp4Tile] = v[e];
+                part += 16 * kFp4Tile;
+            } else if (n < g.N) {
+                if (b.y_dtype == W12_F32) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e, yf += g.N)
+                        if (q + e < left) *yf = v[e];
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e, yb += g.N)
+                        if (q + e < left) *yb = __float2bfloat16_rn(v[e]);
+                }
             }
         }
         tmem_fence_before();
