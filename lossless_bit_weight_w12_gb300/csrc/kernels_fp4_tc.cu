@@ -6,9 +6,11 @@
 // kernels_fp4.cu).  A unit is two tiles of 128 columns that share its tokens: at
 // 128 tokens a unit's tokens are 32 KB beside 18 KB of weights, and one tile alone
 // would read them twice.  Roles:
-//  - 16 warps expand: group t (8 warps) has tile t, thread (w, l) of it row 32 (w % 4)
-//    + l and half h = w / 4 of the 128 k: 64 weights, in registers, stored with
-//    tcgen05.st into one of the tile's two A buffers (column j: k = 2 j, 2 j + 1);
+//  - 16 warps expand, in two groups that take the units in turn (so that one group's
+//    waits lie under the other's work): thread (w, l) of a group has row 32 (w % 4) + l
+//    of both tiles and half h = w / 4 of the 128 k, 64 weights of each, expanded in
+//    registers and stored with tcgen05.st into the tile's A buffer of that group
+//    (column j: k = 2 j, 2 j + 1);
 //  - one warp copies the weights (one bulk copy a unit), one the tokens (two boxes of
 //    64 k x MP tokens, 128-byte swizzle);
 //  - two warps issue, one per tile: 8 UMMAs a unit (M = 128, N = MP, K = 16) into the
@@ -47,7 +49,7 @@ struct TCfg {
     static constexpr int SX = 3;
     static constexpr int kBars = 1024;
     static constexpr int kFit = (227 * 1024 - kBars - SX * kX) / kFp4Unit;
-    static constexpr int SW = kFit > 8 ? 8 : kFit;
+    static constexpr int SW = kFit > 8 ? 8 : kFit / 2 * 2;  // even: a stage's units are one group's
     static constexpr int kBarOff = SX * kX + SW * kFp4Unit;
     static constexpr size_t kSmem = size_t(kBarOff) + kBars;
     // sums of tile t at columns t MP, its A buffer a at kA + (2 t + a) 64
@@ -57,7 +59,7 @@ struct TCfg {
 };
 
 struct Bars {
-    uint64_t full_w[8], empty_w[8];  // the unit's weights; the 16 warps have read them
+    uint64_t full_w[8], empty_w[8];  // the unit's weights; its group's 8 warps have read them
     uint64_t full_x[3], empty_x[3];  // its tokens; both tiles' UMMAs have read them
     uint64_t a_full[2][2], a_empty[2][2];  // [tile][buffer]: expanded (8 warps); read by the UMMAs
     uint64_t sum_full[2], sum_empty[2];    // a piece's sums; read (8 warps)
@@ -107,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_tc_kernel(const __grid_consta
     int u0, u1;
     fp4_units(b, u0, u1);
     if (threadIdx.x == 0) {
-        for (int s = 0; s < SW; ++s) mbar_init(&bar.full_w[s], 1), mbar_init(&bar.empty_w[s], kDW);
+        for (int s = 0; s < SW; ++s) mbar_init(&bar.full_w[s], 1), mbar_init(&bar.empty_w[s], kDW / 2);
         for (int s = 0; s < SX; ++s) mbar_init(&bar.full_x[s], 1), mbar_init(&bar.empty_x[s], 2);
         for (int t = 0; t < 2; ++t) {
             for (int a = 0; a < 2; ++a) mbar_init(&bar.a_full[t][a], kDW / 2), mbar_init(&bar.a_empty[t][a], 1);
@@ -220,46 +222,54 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_tc_kernel(const __grid_consta
     }
 
     // ------------------------------------------------------------------ expansion
-    const int t = warp >> 3, h = (warp >> 2) & 1;
-    const int r = 32 * (warp & 3) + lane, col = 128 * t + r;  // row of the tile = lane of the tensor memory
+    const int grp = warp >> 3, h = (warp >> 2) & 1;
+    const int t = grp;                                        // the tile whose sums the warp reads
+    const int r = 32 * (warp & 3) + lane, col = 128 * t + r;  // row of a tile = lane of the tensor memory
     const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
-    const uint32_t p0 = uint32_t(col * 64 + 16 * fp4_chunk_at(col, 2 * h)), p1 = uint32_t(col * 64 + 16 * fp4_chunk_at(col, 2 * h + 1));
-    const uint32_t ps = uint32_t(kFp4Scales + 8 * col + 4 * h);  // (chunks 2 h and 2 h + 1: k 16 j .. and 64 + 16 j ..)
+    // of tile 0 (tile 1: 128 columns on, the same chunk order)
+    const uint32_t p0 = uint32_t(r * 64 + 16 * fp4_chunk_at(r, 2 * h)), p1 = uint32_t(r * 64 + 16 * fp4_chunk_at(r, 2 * h + 1));
+    const uint32_t ps = uint32_t(kFp4Scales + 8 * r + 4 * h);  // (chunks 2 h and 2 h + 1: k 16 j .. and 64 + 16 j ..)
     const int M = b.M;
     SCur c = s_at(b, u0);
     int i = 0, piece = 0;
     for (int u = u0; u < u1;) {
         const Fp4One &g = b.g[c.gi];
         const int nb = c.nb, first = g.ubase + nb * g.KG;
-        const int ua = u, ub = min(u1, first + g.KG);
-        for (; u < ub; ++u, ++i) {
-            const int s = i % SW, a = i & 1;
-            mbar_wait(&bar.full_w[s], uint32_t(i / SW) & 1u, ctl, b.err);
+        const int ua = u, ub = min(u1, first + g.KG), iend = i + ub - ua;
+        for (int iu = i + ((i & 1) != grp); iu < iend; iu += 2) {  // this group's units
+            const int s = iu % SW;
+            mbar_wait(&bar.full_w[s], uint32_t(iu / SW) & 1u, ctl, b.err);
             const uint32_t st = wbase + uint32_t(s) * kFp4Unit;
-            const uint4 c0 = lds128(st + p0), c1 = lds128(st + p1);
-            const uint32_t f = lds32(st + ps);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.empty_w[s]);
-            uint32_t v[32];
-            const uint32_t f0 = fp4_scale2(prmt2(f, 0u, 0x4040u)), f1 = fp4_scale2(prmt2(f, 0u, 0x4141u));
-            const uint32_t f2 = fp4_scale2(prmt2(f, 0u, 0x4242u)), f3 = fp4_scale2(prmt2(f, 0u, 0x4343u));
-            const auto expand = [&](uint32_t w, uint32_t scale, int at) {
-                uint32_t(&to)[4] = *reinterpret_cast<uint32_t(*)[4]>(&v[at]);
-                fp4_expand(w, scale, to);
-            };
-            // columns 16 h ..: k 32 h .. + 31; columns 32 + 16 h ..: k 64 + 32 h ..
-            expand(c0.x, f0, 0), expand(c0.y, f0, 4), expand(c1.x, f2, 8), expand(c1.y, f2, 12);
-            expand(c0.z, f1, 16), expand(c0.w, f1, 20), expand(c1.z, f3, 24), expand(c1.w, f3, 28);
-            if (i >= 2) mbar_wait(&bar.a_empty[t][a], uint32_t((i >> 1) - 1) & 1u, ctl, b.err);
-            tmem_fence_after();
-            const uint32_t ta = tmem + lanes + C::kA + uint32_t(2 * t + a) * 64u + 16u * uint32_t(h);
-            tmem_store16(ta, v);
-            tmem_store16(ta + 32u, v + 16);
-            tmem_wait_st();
-            tmem_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.a_full[t][a]);
+#pragma unroll
+            for (int tile = 0; tile < 2; ++tile) {
+                const uint4 c0 = lds128(st + p0 + uint32_t(tile * 128 * 64)), c1 = lds128(st + p1 + uint32_t(tile * 128 * 64));
+                const uint32_t f = lds32(st + ps + uint32_t(tile * 128 * 8));
+                if (tile == 1) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.empty_w[s]);
+                }
+                uint32_t v[32];
+                const uint32_t f0 = fp4_scale2(prmt2(f, 0u, 0x4040u)), f1 = fp4_scale2(prmt2(f, 0u, 0x4141u));
+                const uint32_t f2 = fp4_scale2(prmt2(f, 0u, 0x4242u)), f3 = fp4_scale2(prmt2(f, 0u, 0x4343u));
+                const auto expand = [&](uint32_t w, uint32_t scale, int at) {
+                    uint32_t(&to)[4] = *reinterpret_cast<uint32_t(*)[4]>(&v[at]);
+                    fp4_expand(w, scale, to);
+                };
+                // columns 16 h ..: k 32 h .. + 31; columns 32 + 16 h ..: k 64 + 32 h ..
+                expand(c0.x, f0, 0), expand(c0.y, f0, 4), expand(c1.x, f2, 8), expand(c1.y, f2, 12);
+                expand(c0.z, f1, 16), expand(c0.w, f1, 20), expand(c1.z, f3, 24), expand(c1.w, f3, 28);
+                if (iu >= 2) mbar_wait(&bar.a_empty[tile][grp], uint32_t((iu >> 1) - 1) & 1u, ctl, b.err);
+                tmem_fence_after();
+                const uint32_t ta = tmem + lanes + C::kA + uint32_t(2 * tile + grp) * 64u + 16u * uint32_t(h);
+                tmem_store16(ta, v);
+                tmem_store16(ta + 32u, v + 16);
+                tmem_wait_st();
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.a_full[tile][grp]);
+            }
         }
+        u = ub, i = iend;
         // ---- the piece's sums: row r, tokens h MP / 2 .. + MP / 2
         mbar_wait(&bar.sum_full[t], uint32_t(piece) & 1u, ctl, b.err);
         tmem_fence_after();
