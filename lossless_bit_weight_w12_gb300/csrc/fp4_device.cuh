@@ -67,18 +67,78 @@ __device__ __forceinline__ uint32_t fp4_word(uint32_t nibbles) {
     return w;
 }
 
-// A split tile starts in one CTA, as its last, so that CTA's number names the
-// counter: as many for any matrix, and one workspace serves them all.
-__device__ __forceinline__ uint32_t *arrivals(const Fp4Batch &b, const Fp4One &, int first, int) {
-    const int G = int(gridDim.x);
-    return &b.counters[sk_cta_of(first, b.U / G, b.U % G)];
-}
-
 // The units of this CTA.
 __device__ __forceinline__ void fp4_units(const Fp4Batch &b, int &u0, int &u1) {
     const int n = b.U / b.grain, G = int(gridDim.x), c = int(blockIdx.x), per = n / G, rem = n % G;
     u0 = sk_unit_begin(c, per, rem) * b.grain;
     u1 = u0 + (per + (c < rem ? 1 : 0)) * b.grain;
+}
+
+// Stream-K fix-up, as stream_fixup (stream_device.cuh), for tiles of 256 columns: up
+// to 8 pieces' parts are on their way at a time (16 pieces one after the other: 9 us).
+template <int O, int P>
+__device__ __forceinline__ void fp4_add_pieces(const Fp4Batch &b, const Fp4One &g, int first, int nb, int c0, int c1, int tid,
+                                               int nthreads) {
+    const int G = int(gridDim.x), per = b.U / G, rem = b.U % G, total = b.M * (kFp4Tile / 4);
+    const size_t slot = size_t(b.M) * kFp4Tile;
+#pragma unroll 1
+    for (int o0 = tid; o0 < total; o0 += O * nthreads) {
+        float4 sum[O];
+#pragma unroll
+        for (int k = 0; k < O; ++k) sum[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int c = c0; c <= c1; c += P) {
+            float4 v[P][O];
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                const int from = min(c + p, c1);
+                const float4 *part = reinterpret_cast<const float4 *>(
+                    b.partial + (size_t(from) * 2 + (sk_unit_begin(from, per, rem) >= first ? 0 : 1)) * slot);
+#pragma unroll
+                for (int k = 0; k < O; ++k) v[p][k] = __ldcg(part + min(o0 + k * nthreads, total - 1));
+            }
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+                if (c + p <= c1)
+#pragma unroll
+                    for (int k = 0; k < O; ++k)
+                        sum[k].x += v[p][k].x, sum[k].y += v[p][k].y, sum[k].z += v[p][k].z, sum[k].w += v[p][k].w;
+        }
+#pragma unroll
+        for (int k = 0; k < O; ++k) {
+            const int o = o0 + k * nthreads, m = o / (kFp4Tile / 4), n = nb * kFp4Tile + 4 * (o % (kFp4Tile / 4));
+            if (o >= total) break;
+            const float r[4] = {sum[k].x, sum[k].y, sum[k].z, sum[k].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (n + e < g.N) store_out(g.y, b.y_dtype, g.N, m, n + e, r[e]);
+        }
+    }
+}
+
+__device__ __forceinline__ void fp4_fixup(const Fp4Batch &b, const Fp4One &g, int first, int nb, int count, int *s_last, int tid,
+                                          int nthreads) {
+    const int G = int(gridDim.x), per = b.U / G, rem = b.U % G;
+    const int c0 = sk_cta_of(first, per, rem), c1 = sk_cta_of(first + g.KG - 1, per, rem);
+    __threadfence();
+    named_sync(nthreads);
+    if (tid == 0) {
+        // a split tile starts in one CTA, as its last: that CTA's number names the
+        // counter, as many for any matrix, and one workspace serves them all
+        uint32_t *arrived = &b.counters[c0];
+        const uint32_t old = atomicAdd(arrived, uint32_t(count));
+        *s_last = int(old) + count == g.KG;
+        if (*s_last) *arrived = 0u;
+    }
+    named_sync(nthreads);
+    if (*s_last) {
+        __threadfence();
+        if (c1 - c0 < 2)
+            fp4_add_pieces<4, 2>(b, g, first, nb, c0, c1, tid, nthreads);
+        else
+            fp4_add_pieces<1, 8>(b, g, first, nb, c0, c1, tid, nthreads);
+    }
+    named_sync(nthreads);  // s_last is reused by the next piece
 }
 
 }  // namespace w12

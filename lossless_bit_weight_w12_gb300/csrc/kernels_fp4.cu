@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(FCfg<NT>::kThreads, 2) fp4_kernel(const __grid
                         store_out(g.y, b.y_dtype, g.N, m, n, v);
                 }
         if (!whole)
-            stream_fixup<false, kFp4Tile>(b, g, first, nb, ub - ua, &s_last, threadIdx.x, kCT, static_cast<unsigned long long *>(nullptr));
+            fp4_fixup(b, g, first, nb, ub - ua, &s_last, threadIdx.x, kCT);
         s_next_tile(b, c);
     }
 }

@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_tc_kernel(const __grid_consta
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.sum_empty[t]);
         if (!whole)
-            stream_fixup<false, kFp4Tile>(b, g, first, nb, ub - ua, &bar.last, threadIdx.x, kDT, static_cast<unsigned long long *>(nullptr));
+            fp4_fixup(b, g, first, nb, ub - ua, &bar.last, threadIdx.x, kDT);
         ++piece;
         s_next_tile(b, c);
     }

@@ -86,18 +86,16 @@ __device__ __forceinline__ void s_next(const Batch &b, SCur &c) {
 // [first, first + KG); CTA c's piece of it is stored in partial slot
 // (c, 0) if the piece starts at c's first unit, else (c, 1) (only a CTA's
 // first and last pieces can be split).  Each piece adds its unit count to
-// the tile's counter; the CTA that completes the count sums the pieces' slots in
+// counters[nb]; the CTA that completes the count sums the pieces' slots in
 // CTA order (the same bits on every call), writes y and resets the counter.
-__device__ __forceinline__ uint32_t *arrivals(const StreamBatch &, const StreamOne &g, int, int nb) { return &g.counters[nb]; }
-
-template <bool FUSED, int TILE = kTileN, class Batch, class One>
-__device__ __forceinline__ void stream_fixup(const Batch &b, const One &g, int first, int nb,
+template <bool FUSED>
+__device__ __forceinline__ void stream_fixup(const StreamBatch &b, const StreamOne &g, int first, int nb,
                                              int count, int *s_last, int tid, int nthreads,
                                              unsigned long long *s_best) {
     __threadfence();
     named_sync(nthreads);
     if (tid == 0) {
-        const uint32_t old = atomicAdd(arrivals(b, g, first, nb), uint32_t(count));
+        const uint32_t old = atomicAdd(&g.counters[nb], uint32_t(count));
         *s_last = (int(old) + count == g.KG);
     }
     named_sync(nthreads);
@@ -106,8 +104,8 @@ __device__ __forceinline__ void stream_fixup(const Batch &b, const One &g, int f
         const int G = int(gridDim.x), per = b.U / G, rem = b.U % G;
         const int c_first = sk_cta_of(first, per, rem), c_last = sk_cta_of(first + g.KG - 1, per, rem);
         const int M = b.M;
-        const size_t slot_floats = size_t(M) * TILE;
-        const int total = M * (TILE / 4);
+        const size_t slot_floats = size_t(M) * kTileN;
+        const int total = M * (kTileN / 4);
         // four outputs per thread and round trip, summed in CTA order (the
         // same bits on every call)
         for (int o0 = tid; o0 < total; o0 += 4 * nthreads) {
@@ -139,8 +137,8 @@ __device__ __forceinline__ void stream_fixup(const Batch &b, const One &g, int f
             for (int k = 0; k < 4; ++k) {
                 const int o = o0 + k * nthreads;
                 if (o >= total) break;
-                const int m = o / (TILE / 4), c4 = o % (TILE / 4);
-                const int n0 = nb * TILE + 4 * c4;
+                const int m = o / (kTileN / 4), c4 = o % (kTileN / 4);
+                const int n0 = nb * kTileN + 4 * c4;
                 const float r[4] = {acc[k].x, acc[k].y, acc[k].z, acc[k].w};
                 unsigned long long best = 0ull;
 #pragma unroll
@@ -155,7 +153,7 @@ __device__ __forceinline__ void stream_fixup(const Batch &b, const One &g, int f
                 if (FUSED && best != 0ull) atomicMax(&s_best[m], best);
             }
         }
-        if (tid == 0) *arrivals(b, g, first, nb) = 0u;
+        if (tid == 0) g.counters[nb] = 0u;
     }
     named_sync(nthreads);  // s_last is reused by the next piece
 }
