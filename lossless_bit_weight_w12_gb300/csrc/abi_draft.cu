@@ -20,9 +20,24 @@ size_t size_of(int dtype) { return dtype == W12_F32 ? 4 : dtype == W12_BF16 ? 2 
 
 bool float_type(int dtype) { return dtype == W12_F32 || dtype == W12_BF16; }
 
+constexpr int kMaxDevices = 256;
+std::atomic<int> g_sms[kMaxDevices];
+
+// SM count of the current device, asked once per device.
+int current_sms(int *sms) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return W12_ERR_CUDA;
+    int v = g_sms[dev].load(std::memory_order_relaxed);
+    if (v == 0) {
+        if (device_sm_count(&v) != W12_OK) return W12_ERR_CUDA;
+        g_sms[dev].store(v, std::memory_order_relaxed);
+    }
+    *sms = v;
+    return W12_OK;
+}
+
 // SM count and CTAs per SM of a product variant on the current device, asked
 // once per device and variant.
-constexpr int kMaxDevices = 256;
 std::atomic<uint64_t> g_fp4[kMaxDevices][kFp4Variants];
 
 int fp4_device(int variant, int *sms, int *blocks) {
@@ -117,6 +132,9 @@ extern "C" int w12_add_norm(const void *x, int64_t x_stride, int x_dtype, const 
     a.x_stride = x_stride, a.delta_stride = delta_stride, a.residual_stride = residual_stride, a.out_stride = out_stride;
     a.rows = rows, a.dim = int32_t(dim), a.weight_f32 = weight && weight_dtype == W12_F32;
     a.eps = eps, a.offset = offset;
+    int sms = 0;
+    if (current_sms(&sms) != W12_OK) return W12_ERR_CUDA;
+    a.sms = sms;
     // rows on 16-byte boundaries (e4m3: 8), whole eights of elements
     const auto rows_at = [&](const void *p, int64_t stride, size_t size, size_t to) {
         return !p || (aligned(p, to) && (rows == 1 || uint64_t(stride) * size % to == 0));

@@ -18,6 +18,7 @@ struct NormArgs {
     int64_t rows;
     int32_t dim;
     int32_t weight_f32;
+    int32_t sms;
     float eps, offset;
 };
 // delta_dtype -1: no delta.  vec: every row of every tensor starts on a

@@ -3,7 +3,11 @@
 //
 //   h = x + delta,  r = 1 / sqrt(mean(h^2) + eps),  y = (h (weight + offset)) r
 //
-// One CTA per row, the row in registers: every tensor is read or written once.
+// A CTA takes a row at a time, in registers: every tensor is read or written once.
+// It asks for its next row before it reduces the one it has, so that the memory is
+// busy under the reductions; the weights stay in registers from row to row.  What
+// bounds it: from some hundred rows on the memory, below that the launch.
+//
 // The e4m3 scale needs the largest |y|; as r is one positive number for the
 // row and a rounded product does not decrease with its factor, it is the
 // rounded product of r and the largest |h (weight + offset)|, so one block
@@ -13,6 +17,8 @@
 // The sum of squares is fp32.  Where it overflows, the row is scaled by 2^-80
 // in its registers and reduced once more (eps is below every rounding there).
 #include <cuda_runtime.h>
+
+#include <algorithm>
 
 #include "device_common.cuh"
 #include "draft_internal.h"
@@ -37,24 +43,33 @@ __device__ __forceinline__ uint4 load16(const void *p) {  // (x may be written b
     return r;
 }
 
-// Elements i .. i + 7 of a row.
-template <bool F32>
-__device__ __forceinline__ void load8(const void *row, int i, float (&v)[8]) {
-    if (F32) {
-        const uint4 a = load16(static_cast<const float *>(row) + i), b = load16(static_cast<const float *>(row) + i + 4);
-        v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y), v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
-        v[4] = __uint_as_float(b.x), v[5] = __uint_as_float(b.y), v[6] = __uint_as_float(b.z), v[7] = __uint_as_float(b.w);
-    } else {
-        const uint4 a = load16(static_cast<const uint16_t *>(row) + i);
-        v[0] = bf_lo(a.x), v[1] = bf_hi(a.x), v[2] = bf_lo(a.y), v[3] = bf_hi(a.y);
-        v[4] = bf_lo(a.z), v[5] = bf_hi(a.z), v[6] = bf_lo(a.w), v[7] = bf_hi(a.w);
-    }
-}
+// Elements of a row as they lie in memory: eight consecutive ones, or one.
+template <bool VEC, bool F32>
+struct Raw {
+    uint4 v[VEC ? (F32 ? 2 : 1) : 1];  // (one element: in v[0].x)
 
-template <bool F32>
-__device__ __forceinline__ float load1(const void *row, int i) {
-    return F32 ? static_cast<const float *>(row)[i] : bf16_bits_to_float(static_cast<const uint16_t *>(row)[i]);
-}
+    __device__ __forceinline__ void load(const void *row, int i) {
+        if constexpr (VEC) {
+            const unsigned char *p = static_cast<const unsigned char *>(row) + size_t(i) * (F32 ? 4 : 2);
+            v[0] = load16(p);
+            if constexpr (F32) v[1] = load16(p + 16);
+        } else {
+            v[0].x = F32 ? __float_as_uint(static_cast<const volatile float *>(row)[i])
+                         : uint32_t(static_cast<const volatile uint16_t *>(row)[i]) << 16;
+        }
+    }
+    __device__ __forceinline__ void get(float (&f)[VEC ? 8 : 1]) const {
+        if constexpr (!VEC) {
+            f[0] = __uint_as_float(v[0].x);
+        } else if constexpr (F32) {
+            f[0] = __uint_as_float(v[0].x), f[1] = __uint_as_float(v[0].y), f[2] = __uint_as_float(v[0].z), f[3] = __uint_as_float(v[0].w);
+            f[4] = __uint_as_float(v[1].x), f[5] = __uint_as_float(v[1].y), f[6] = __uint_as_float(v[1].z), f[7] = __uint_as_float(v[1].w);
+        } else {
+            f[0] = bf_lo(v[0].x), f[1] = bf_hi(v[0].x), f[2] = bf_lo(v[0].y), f[3] = bf_hi(v[0].y);
+            f[4] = bf_lo(v[0].z), f[5] = bf_hi(v[0].z), f[6] = bf_lo(v[0].w), f[7] = bf_hi(v[0].w);
+        }
+    }
+};
 
 template <bool F32>
 __device__ __forceinline__ void store1(void *row, int i, float v) {
@@ -88,147 +103,177 @@ __device__ __forceinline__ void reduce(float &sum, uint32_t &top, float *s_sum, 
 // E: elements of a row per thread.  VEC: eight consecutive ones at a time
 // (chunk tid + q blockDim), else one (element tid + q blockDim).  XF, DF: x
 // and delta in fp32 (DF -1: no delta).
-template <int E, bool VEC, bool XF, int DF, bool E4M3>
-__global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ NormArgs a) {
-    __shared__ float s_sum[2][32];
-    __shared__ uint32_t s_top[2][32];
+// T: threads at most (768: two CTAs of them on an SM, with 40 registers a thread).
+template <int E, bool VEC, bool XF, int DF, bool E4M3, int T>
+__global__ void __launch_bounds__(T, 1536 / T) norm_kernel(const __grid_constant__ NormArgs a) {
+    __shared__ float s_sum[4][32];
+    __shared__ uint32_t s_top[4][32];
     const int tid = threadIdx.x, step = blockDim.x;
-    const int64_t r = blockIdx.x;
     constexpr int W = VEC ? 8 : 1, Q = E / W;
     pdl_launch_dependents();
     pdl_wait_previous();
     const auto at = [](const void *p, int64_t elements, bool f32) {
         return static_cast<const unsigned char *>(p) + elements * (f32 ? 4 : 2);
     };
-    const void *x = at(a.x, r * a.x_stride, XF);
-    const void *d = DF >= 0 ? at(a.delta, r * a.delta_stride, DF > 0) : nullptr;
-    float h[Q][W], w[Q][W];
+    constexpr bool kAhead = E == 8;  // (32 elements a thread leave no registers for a second row, or for weights)
     int i[Q];
+    Raw<VEC, XF> x[kAhead ? Q : 1];
+    Raw<VEC, (DF > 0)> d[kAhead ? Q : 1];
+    const auto ask = [&](int64_t r, int q, int to) {
+        if (i[q] >= a.dim) return;
+        x[to].load(at(a.x, r * a.x_stride, XF), i[q]);
+        if constexpr (DF >= 0) d[to].load(at(a.delta, r * a.delta_stride, DF > 0), i[q]);
+    };
+    const auto load_weights = [&](int q, float(&w)[W]) {
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-        i[q] = (tid + q * step) * W;
-        if (i[q] < a.dim) {
-            if constexpr (VEC) {
-                load8<XF>(x, i[q], h[q]);
-            } else {
-                h[q][0] = load1<XF>(x, i[q]);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < W; ++j) h[q][j] = 0.0f;
-        }
-    }
-    if constexpr (DF >= 0) {
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-            if (i[q] < a.dim) {
-                float y[W];
-                if constexpr (VEC) {
-                    load8<(DF > 0)>(d, i[q], y);
-                } else {
-                    y[0] = load1<(DF > 0)>(d, i[q]);
-                }
-#pragma unroll
-                for (int j = 0; j < W; ++j) h[q][j] += y[j];
-            }
-    }
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-#pragma unroll
-        for (int j = 0; j < W; ++j) w[q][j] = 1.0f;
+        for (int j = 0; j < W; ++j) w[j] = 1.0f;
         if (a.weight && i[q] < a.dim) {
-            if constexpr (VEC) {
-                if (a.weight_f32)
-                    load8<true>(a.weight, i[q], w[q]);
-                else
-                    load8<false>(a.weight, i[q], w[q]);
+            if (a.weight_f32) {
+                Raw<VEC, true> y;
+                y.load(a.weight, i[q]);
+                y.get(w);
             } else {
-                w[q][0] = a.weight_f32 ? load1<true>(a.weight, i[q]) : load1<false>(a.weight, i[q]);
+                Raw<VEC, false> y;
+                y.load(a.weight, i[q]);
+                y.get(w);
             }
         }
 #pragma unroll
-        for (int j = 0; j < W; ++j) w[q][j] += a.offset;
-    }
-    if (a.residual) {
-        void *o = static_cast<unsigned char *>(a.residual) + r * a.residual_stride * (XF ? 4 : 2);
+        for (int j = 0; j < W; ++j) w[j] += a.offset;
+    };
 #pragma unroll
-        for (int q = 0; q < Q; ++q)
-            if (i[q] < a.dim) {
-                if constexpr (VEC && XF) {
-                    float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(o) + i[q]);
-                    p[0] = make_float4(h[q][0], h[q][1], h[q][2], h[q][3]);
-                    p[1] = make_float4(h[q][4], h[q][5], h[q][6], h[q][7]);
-                } else if constexpr (VEC) {
-                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(o) + i[q]) =
-                        make_uint4(pack_bf16(h[q][0], h[q][1]), pack_bf16(h[q][2], h[q][3]), pack_bf16(h[q][4], h[q][5]),
-                                   pack_bf16(h[q][6], h[q][7]));
-                } else {
-                    store1<XF>(o, i[q], h[q][0]);
-                }
-            }
+    for (int q = 0; q < Q; ++q) i[q] = (tid + q * step) * W;
+    int64_t r = blockIdx.x;
+    float kept[kAhead ? Q : 1][W];
+    if constexpr (kAhead) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) ask(r, q, q);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) load_weights(q, kept[q]);
     }
-    float sum, eps = a.eps;
-    uint32_t top;
+    const auto weights = [&](int q, float(&w)[W]) {
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j] = kept[q][j];
+        } else {
+            load_weights(q, w);
+        }
+    };
+    int buffer = 0;  // (a buffer of the reduction is used again two rows later)
+    for (; r < a.rows; r += gridDim.x, buffer ^= 2) {
+        float h[Q][W];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            if constexpr (!kAhead) ask(r, q, 0);
+            if (i[q] < a.dim) {
+                x[kAhead ? q : 0].get(h[q]);
+                if constexpr (DF >= 0) {
+                    float y[W];
+                    d[kAhead ? q : 0].get(y);
+#pragma unroll
+                    for (int j = 0; j < W; ++j) h[q][j] += y[j];
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < W; ++j) h[q][j] = 0.0f;
+            }
+        }
+        if constexpr (kAhead)  // (the residual, written below, may be x: other rows of it)
+            if (r + gridDim.x < a.rows)
+#pragma unroll
+                for (int q = 0; q < Q; ++q) ask(r + gridDim.x, q, q);
+        if (a.residual) {
+            void *o = static_cast<unsigned char *>(a.residual) + r * a.residual_stride * (XF ? 4 : 2);
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+                if (i[q] < a.dim) {
+                    if constexpr (VEC && XF) {
+                        float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(o) + i[q]);
+                        p[0] = make_float4(h[q][0], h[q][1], h[q][2], h[q][3]);
+                        p[1] = make_float4(h[q][4], h[q][5], h[q][6], h[q][7]);
+                    } else if constexpr (VEC) {
+                        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(o) + i[q]) =
+                            make_uint4(pack_bf16(h[q][0], h[q][1]), pack_bf16(h[q][2], h[q][3]), pack_bf16(h[q][4], h[q][5]),
+                                       pack_bf16(h[q][6], h[q][7]));
+                    } else {
+                        store1<XF>(o, i[q], h[q][0]);
+                    }
+                }
+        }
+        float sum, eps = a.eps;
+        uint32_t top;
 #pragma unroll 1
-    for (int pass = 0;; ++pass) {
-        sum = 0.0f, top = 0u;
+        for (int pass = 0;; ++pass) {
+            sum = 0.0f, top = 0u;
 #pragma unroll
-        for (int q = 0; q < Q; ++q)
+            for (int q = 0; q < Q; ++q) {
+                float w[W];
+                if (E4M3) weights(q, w);
 #pragma unroll
-            for (int j = 0; j < W; ++j) {
-                sum = fmaf(h[q][j], h[q][j], sum);
-                if (E4M3) top = max(top, __float_as_uint(h[q][j] * w[q][j]) & 0x7FFFFFFFu);
-            }
-        reduce(sum, top, s_sum[pass], s_top[pass]);
-        if (pass == 1 || sum != INFINITY) break;
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-#pragma unroll
-            for (int j = 0; j < W; ++j) h[q][j] *= 0x1p-80f;
-        eps = 0.0f;
-    }
-    const float rs = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(sum, float(a.dim)) + eps));
-    if constexpr (E4M3) {
-        const float amax = __uint_as_float(top) * rs;
-        const bool bad = !(amax <= 3.402823466e38f), some = amax > kTinyRow;
-        const float inv = !bad && some ? __fdiv_rn(kE4m3Max, amax) : 0.0f;
-        if (tid == 0) a.scale[r] = bad ? __uint_as_float(0x7FC00000u) : some ? __fdiv_rn(amax, kE4m3Max) : 0.0f;
-        uint8_t *o = static_cast<uint8_t *>(a.out) + r * a.out_stride;
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-            if (i[q] < a.dim) {
-                float y[W];
-                // (inv 0: zeros, also where the row holds a NaN or an infinity)
-#pragma unroll
-                for (int j = 0; j < W; ++j) y[j] = inv > 0.0f ? h[q][j] * w[q][j] * rs * inv : 0.0f;
-                if constexpr (VEC) {
-                    *reinterpret_cast<uint2 *>(o + i[q]) = make_uint2(pack_e4m3(y[0], y[1]) | pack_e4m3(y[2], y[3]) << 16,
-                                                                      pack_e4m3(y[4], y[5]) | pack_e4m3(y[6], y[7]) << 16);
-                } else {
-                    o[i[q]] = uint8_t(pack_e4m3(y[0], 0.0f));
+                for (int j = 0; j < W; ++j) {
+                    sum = fmaf(h[q][j], h[q][j], sum);
+                    if (E4M3) top = max(top, __float_as_uint(h[q][j] * w[j]) & 0x7FFFFFFFu);
                 }
             }
-    } else {
-        uint16_t *o = static_cast<uint16_t *>(a.out) + r * a.out_stride;
+            reduce(sum, top, s_sum[buffer + pass], s_top[buffer + pass]);
+            if (pass == 1 || sum != INFINITY) break;
 #pragma unroll
-        for (int q = 0; q < Q; ++q)
-            if (i[q] < a.dim) {
-                float y[W];
+            for (int q = 0; q < Q; ++q)
 #pragma unroll
-                for (int j = 0; j < W; ++j) y[j] = h[q][j] * w[q][j] * rs;
-                if constexpr (VEC) {
-                    *reinterpret_cast<uint4 *>(o + i[q]) =
-                        make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
-                } else {
-                    store1<false>(o, i[q], y[0]);
+                for (int j = 0; j < W; ++j) h[q][j] *= 0x1p-80f;
+            eps = 0.0f;
+        }
+        const float rs = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(sum, float(a.dim)) + eps));
+        if constexpr (E4M3) {
+            const float amax = __uint_as_float(top) * rs;
+            const bool bad = !(amax <= 3.402823466e38f), some = amax > kTinyRow;
+            const float inv = !bad && some ? __fdiv_rn(kE4m3Max, amax) : 0.0f;
+            if (tid == 0) a.scale[r] = bad ? __uint_as_float(0x7FC00000u) : some ? __fdiv_rn(amax, kE4m3Max) : 0.0f;
+            uint8_t *o = static_cast<uint8_t *>(a.out) + r * a.out_stride;
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+                if (i[q] < a.dim) {
+                    float y[W], w[W];
+                    weights(q, w);
+                    // (inv 0: zeros, also where the row holds a NaN or an infinity)
+#pragma unroll
+                    for (int j = 0; j < W; ++j) y[j] = inv > 0.0f ? h[q][j] * w[j] * rs * inv : 0.0f;
+                    if constexpr (VEC) {
+                        *reinterpret_cast<uint2 *>(o + i[q]) = make_uint2(pack_e4m3(y[0], y[1]) | pack_e4m3(y[2], y[3]) << 16,
+                                                                          pack_e4m3(y[4], y[5]) | pack_e4m3(y[6], y[7]) << 16);
+                    } else {
+                        o[i[q]] = uint8_t(pack_e4m3(y[0], 0.0f));
+                    }
                 }
-            }
+        } else {
+            uint16_t *o = static_cast<uint16_t *>(a.out) + r * a.out_stride;
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+                if (i[q] < a.dim) {
+                    float y[W], w[W];
+                    weights(q, w);
+#pragma unroll
+                    for (int j = 0; j < W; ++j) y[j] = h[q][j] * w[j] * rs;
+                    if constexpr (VEC) {
+                        *reinterpret_cast<uint4 *>(o + i[q]) =
+                            make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+                    } else {
+                        store1<false>(o, i[q], y[0]);
+                    }
+                }
+        }
     }
 }
 
+// As many CTAs as fit on the GPU at a time (1536 threads an SM with 40 registers each,
+// for elements by eights, else 1024 with 64).
 template <int E, bool VEC, bool XF, int DF, bool E4M3>
 int run(const NormArgs &a, int threads, void *stream) {
-    return launch_step(norm_kernel<E, VEC, XF, DF, E4M3>, int(a.rows), threads, 0, 1, stream, a);
+    const auto grid = [&](int per_sm) { return int(std::min(a.rows, int64_t(a.sms) * std::max(1, per_sm / threads))); };
+    if constexpr (E == 8 && VEC)
+        if (threads <= 768)
+            return launch_step(norm_kernel<E, VEC, XF, DF, E4M3, 768>, grid(1536), threads, 0, 1, stream, a);
+    return launch_step(norm_kernel<E, VEC, XF, DF, E4M3, 1024>, grid(1024), threads, 0, 1, stream, a);
 }
 
 template <int E, bool VEC, bool XF, int DF>

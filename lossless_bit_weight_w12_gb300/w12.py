@@ -604,24 +604,29 @@ def sample(logits, R: int, T: int, u, tokens_dev, ws_dev, temperature=None, top_
 
 # --------------------------------------------- draft model: add and norm
 
-def _dtype_of(t):
-    """F32 or BF16 of a tensor (E4M3: float8_e4m3fn)."""
+_kinds = None
+
+
+def _dtype_kinds():
+    """{torch dtype: F32, BF16 or E4M3}."""
+    global _kinds
     import torch
-    d = t.dtype
-    k = F32 if d is torch.float32 else BF16 if d is torch.bfloat16 else E4M3 if d is torch.float8_e4m3fn else -1
+    _kinds = {torch.float32: F32, torch.bfloat16: BF16, torch.float8_e4m3fn: E4M3}
+    return _kinds
+
+
+def _dtype_of(t):
+    """F32, BF16 or E4M3 of a tensor."""
+    k = (_kinds or _dtype_kinds()).get(t.dtype, -1)
     if k < 0:
-        raise ValueError(f"expected float32, bfloat16 or float8_e4m3fn, got {d}")
+        raise ValueError(f"expected float32, bfloat16 or float8_e4m3fn, got {t.dtype}")
     return k
 
 
 def _rows_ptr(t, n: int, dim: int, what: str):
-    """(address, row stride) of [n, dim] rows with contiguous elements (None: NULL)."""
-    if t is None:
-        return None, 0
-    if t.shape != (n, dim):
-        raise ValueError(f"{what}: expected [{n}, {dim}], got {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError("expected a CUDA tensor")
+    """(address, row stride) of [n, dim] rows with contiguous elements."""
+    if not t.is_cuda or t.shape != (n, dim):
+        raise ValueError(f"{what}: expected a CUDA tensor [{n}, {dim}], got {tuple(t.shape)}")
     row, one = t.stride()
     if one != 1 and dim > 1:
         raise ValueError(f"{what}: expected contiguous rows")
@@ -634,19 +639,32 @@ def add_norm(x, weight, out, delta=None, residual_out=None, eps: float = 1e-6, o
     [n, dim] float32 or bfloat16; residual_out (x's type, may be x): x + delta;
     out bfloat16, or float8_e4m3fn with scale_out float32 [n]; any row strides;
     weight [dim] float32, bfloat16 or None."""
-    import torch
     n, dim = x.shape
+    kinds = _kinds or _dtype_kinds()
+    xt, ot = x.dtype, kinds.get(out.dtype, -1)
     xp, xs = _rows_ptr(x, n, dim, "x")
-    dp, ds = _rows_ptr(delta, n, dim, "delta")
-    rp, rs = _rows_ptr(residual_out, n, dim, "residual_out")
     op, os_ = _rows_ptr(out, n, dim, "out")
-    if residual_out is not None and residual_out.dtype is not x.dtype:
-        raise ValueError("residual_out: x's type")
-    if weight is not None and weight.numel() != dim:
-        raise ValueError(f"weight: expected {dim} elements")
-    st = lib().w12_add_norm(xp, xs, _dtype_of(x), dp, ds, 0 if delta is None else _dtype_of(delta), _ptr(weight),
-                            0 if weight is None else _dtype_of(weight), offset, eps, n, dim, rp, rs, op, os_,
-                            _dtype_of(out), _typed_ptr(scale_out, torch.float32, n, "scale_out"), _stream_of(x, stream))
+    dp = rp = wp = sp = None
+    ds = dt = rs = wt = 0
+    if delta is not None:
+        dp, ds = _rows_ptr(delta, n, dim, "delta")
+        dt = kinds.get(delta.dtype, -1)
+    if residual_out is not None:
+        rp, rs = _rows_ptr(residual_out, n, dim, "residual_out")
+        if residual_out.dtype is not xt:
+            raise ValueError("residual_out: x's type")
+    if weight is not None:
+        wp, wt = _ptr(weight), kinds.get(weight.dtype, -1)
+        if weight.numel() != dim:
+            raise ValueError(f"weight: expected {dim} elements")
+    if scale_out is not None:
+        import torch
+        sp = _typed_ptr(scale_out, torch.float32, n, "scale_out")
+    xt = kinds.get(xt, -1)
+    if min(xt, dt, wt, ot) < 0:
+        raise ValueError("float32 or bfloat16 tensors (out: bfloat16 or float8_e4m3fn)")
+    st = lib().w12_add_norm(xp, xs, xt, dp, ds, dt, wp, wt, offset, eps, n, dim, rp, rs, op, os_, ot, sp,
+                            _stream_of(x, stream))
     if st:
         raise W12Error(st, "w12_add_norm")
 
