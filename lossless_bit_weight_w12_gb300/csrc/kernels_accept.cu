@@ -41,7 +41,8 @@ constexpr float kOne44 = 17592186044416.0f;
 struct Dist {
     const void *x;
     int f32, vec;
-    int plain;    // nothing is cut
+    int easy;     // more than one token may stay, and the logits are finite
+    int last;     // the highest index that stays among the logits of `least`
     RowCut c;
     float inv;    // 1 / total (0: no token stays)
     float least;  // the tokens that stay have logits from it on
@@ -51,14 +52,16 @@ struct Dist {
         f32 = is_f32, vec = (reinterpret_cast<uintptr_t>(x) & (is_f32 ? 15 : 7)) == 0;
         c = cuts[row];
         inv = c.total ? __fdiv_rn(1.0f, __ull2float_rn(c.total)) : 0.0f;
-        plain = c.total != 0 && c.one < 0 && !c.inf && c.thr == 0 && c.floor_w <= 1;
+        easy = c.total != 0 && c.one < 0 && !c.inf;
+        last = c.thr ? int(key_index(c.thr)) : 0x7FFFFFFF;
         const uint32_t k = uint32_t(c.thr >> 32);
         const float at = __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
-        // (weights of e^-22.25 and less are 0)
-        least = c.total == 0 ? INFINITY
-                : c.one >= 0 ? -INFINITY
-                : c.inf      ? (c.thr ? 0.0f : -INFINITY)
-                             : fmaxf(c.thr ? at : -INFINITY, c.mx - 22.26f / c.inv_t * 1.00001f - fabsf(c.mx) * 1e-6f);
+        least = c.total == 0 ? INFINITY : c.one >= 0 || !c.thr ? -INFINITY : c.inf ? 0.0f : at;
+    }
+    // the weight of token i with logit v, of an easy row
+    __device__ __forceinline__ uint32_t easy_weight(float v, int i) const {
+        const uint32_t w = __float2uint_rn(expf(__fmul_rn(__fsub_rn(v, c.mx), c.inv_t)) * kOne31);
+        return (v > least || (v == least && i <= last)) && w >= c.floor_w ? w : 0u;
     }
     __device__ __forceinline__ float logit(int i) const {
         return f32 ? __ldg(static_cast<const float *>(x) + i)
@@ -111,17 +114,18 @@ struct Draw {
 // `stop`, *at is the token.
 __device__ __forceinline__ u64 quad(const Draw &d, bool rest, int i, float4 x, float4 y, u64 &whole, u64 stop, int *at) {
     u64 sum = 0;
-    const bool plain = d.p.plain && d.q.plain && d.rest;
-    const float mp = d.p.c.mx, tp = d.p.c.inv_t, ip = d.p.inv, mq = d.q.c.mx, tq = d.q.c.inv_t, iq = d.q.inv;
+    const bool easy = d.p.easy && (!d.rest || d.q.easy);
+    const float ip = d.p.inv, iq = d.q.inv, least = d.p.least;
 #pragma unroll 1
     for (int j = 0; j < 4; ++j) {
-        if (plain) {
-            const uint32_t w = __float2uint_rn(expf(__fmul_rn(__fsub_rn(x.x, mp), tp)) * kOne31);
-            const uint32_t z = __float2uint_rn(expf(__fmul_rn(__fsub_rn(y.x, mq), tq)) * kOne31);
+        if (!__any_sync(0xFFFFFFFFu, x.x >= least)) {
+            // (cut rows: most of them)
+        } else if (easy) {
+            const uint32_t w = d.p.easy_weight(x.x, i + j), z = d.rest ? d.q.easy_weight(y.x, i + j) : 0u;
             whole = add_wide(whole, w);
             const u64 a = above(__fmul_rn(__uint2float_rn(w), ip), __fmul_rn(__uint2float_rn(z), iq));
             sum += rest ? a : u64(w);
-        } else if (__any_sync(0xFFFFFFFFu, x.x >= d.p.least)) {
+        } else {
             const uint32_t w = d.p.weight(x.x, i + j);
             whole = add_wide(whole, w);
             if (!rest)

@@ -45,8 +45,8 @@ constexpr int kBins = 2048;
 constexpr int kPieces = 2;          // bulk copies of a CTA's part of the row
 constexpr int kMostCluster = 16;
 constexpr int kCap = 680;           // tokens that are gathered
-constexpr int kFew = 256;           // tokens that are ranked one against all
-constexpr int kFine = 256;          // bins of the gathered tokens
+constexpr int kFew = 64;            // tokens that are ranked one against all
+constexpr int kFine = 512;          // bins of the gathered tokens
 constexpr float kSpan = 22.25f;     // e^-22.25 rounds to weight 0
 
 // Which tokens a histogram is over: all (shift -1, bins linear in the exponent),
@@ -173,6 +173,12 @@ __device__ __forceinline__ void find(Small &sh, M mass, u64 above, u64 need) {
     __syncthreads();
 }
 
+// The smallest shift that brings x below N (a power of two).
+template <int N>
+__device__ __forceinline__ int bits_above(u64 x) {
+    return max(0, 64 - __clzll(static_cast<long long>(x)) - (31 - __clz(N)));
+}
+
 // In the first CTA: of its n gathered tokens, those from `from` on, the last one
 // before which, together with `above`, less than `need` lies (by count or mass):
 // sh.thr.
@@ -197,8 +203,7 @@ __device__ __noinline__ void resolve(Small &sh, CutMem &cut, uint32_t n, u64 fro
     uint32_t left = n;
 #pragma unroll 1
     while (left > uint32_t(kFew) && lo < hi) {
-        int shift = 0;
-        while (((hi - lo) >> shift) >= u64(kFine)) ++shift;
+        const int shift = bits_above<kFine>(hi - lo);
         if (tid < kFine) cut.fine_lo[tid] = cut.fine_hi[tid] = cut.fine_n[tid] = 0u;
         __syncthreads();
         for (uint32_t i = tid; i < n; i += kT) {
@@ -545,8 +550,7 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
             if (me == 0) {
                 g.hi = 0, g.lo = ~0ull;
                 for (int c = 0; c < cs; ++c) g.hi = umax64(g.hi, sh.ends[0][c]), g.lo = g.lo < sh.ends[1][c] ? g.lo : sh.ends[1][c];
-                g.shift = 0;
-                while (((g.hi - g.lo) >> g.shift) >= u64(kBins)) ++g.shift;
+                g.shift = bits_above<kBins>(g.hi - g.lo);
                 tell(g);
             }
             clear();
