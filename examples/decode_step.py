@@ -4,10 +4,10 @@ Requests share a prompt.  The prompt goes once through the block in pieces and
 into pages that every request's block table names; then each step runs a draft
 block of T tokens per request:
 
-    projections (w12_gemm_batched) -> rotary positions and cache (w12_kv_append)
-    -> attention, the prompt read once for all requests (w12_attend)
-    -> output projection, lm_head (w12_gemm) -> sampled tokens and how many of
-    the draft they accept (w12_sample)
+    norm (w12_add_norm) -> projections (w12_gemm_batched) -> rotary positions and
+    cache (w12_kv_append) -> attention, the prompt read once for all requests
+    (w12_attend) -> output projection (w12_gemm), addition and norm -> lm_head ->
+    sampled tokens and how many of the draft they accept (w12_sample)
 
 as one CUDA graph.  A rejected token's cache rows are simply written over: a
 request's length goes back to its last accepted token.
@@ -33,6 +33,7 @@ POSITIONS = 8192
 
 
 def norm(x):
+    """The norm in torch operations (Block.norm is the library's)."""
     x = x.float()
     return (x * torch.rsqrt(x.square().mean(-1, keepdim=True) + 1e-6)).to(torch.bfloat16)
 
@@ -62,26 +63,36 @@ class Block:
         b["q16"] = torch.empty(n, HEADS, DIM, dtype=torch.bfloat16, device=dev)
         b["a"] = torch.empty(n, HEADS, DIM, dtype=torch.bfloat16, device=dev)
         b["o"], b["logits"] = f32(n, HIDDEN), f32(n, VOCAB)
-        qkv = [self.w[m] for m in "qkv"]
-        b["ws"] = [w12.workspace(w12.gemm_batched_workspace_size([d for d, _ in qkv], n), dev),
+        b["h"] = torch.empty(n, HIDDEN, dtype=torch.bfloat16, device=dev)
+        b["ws"] = [w12.workspace(self.products_workspace("qkv", n), dev),
                    w12.workspace(w12.attend_workspace_size(kv, R, T, HEADS, max_len, prefix), dev),
-                   w12.workspace(max(w12.gemm_workspace_size(self.w[m][0], n) for m in ("o", "lm_head")), dev)]
+                   w12.workspace(max(self.products_workspace([m], n) for m in ("o", "lm_head")), dev)]
         return b
+
+    def products_workspace(self, names, n):
+        return w12.gemm_batched_workspace_size([self.w[m][0] for m in names], n)
+
+    def products(self, names, x, ys, ws):
+        """ys[i] = x @ the matrix names[i], in one launch."""
+        w12.gemm_batched([self.w[m][0] for m in names], [self.w[m][1] for m in names], [x] * len(names), ys, ws)
+
+    def norm(self, b, x, delta=None):
+        """The products' input b["h"]: x (+ delta), normalised."""
+        w12.add_norm(x, None, b["h"], delta=delta)
+        return b["h"]
 
     def forward(self, b, kv, ids, table, kv_len, T, max_len, prefix, logits=True):
         """ids [R * T] -> b["logits"]; the tokens enter the cache at kv_len - T .. kv_len - 1."""
         x = self.emb[ids]
-        h = norm(x)
-        w12.gemm_batched([self.w[m][0] for m in "qkv"], [self.w[m][1] for m in "qkv"], [h] * 3,
-                         [b["q"], b["k"], b["v"]], b["ws"][0])
+        self.products("qkv", self.norm(b, x), [b["q"], b["k"], b["v"]], b["ws"][0])
         n = len(ids)
         w12.kv_append(kv, b["q"].view(n, HEADS, DIM), b["k"].view(n, KV_HEADS, DIM), b["v"].view(n, KV_HEADS, DIM),
                       table, kv_len, T, b["q16"], self.rope)
         w12.attend(kv, b["q16"], table, kv_len, T, max_len, b["a"], b["ws"][1], prefix_len=prefix)
         if not logits:
             return
-        w12.gemm(*self.w["o"], b["a"].view(n, HEADS * DIM), b["o"], b["ws"][2])
-        w12.gemm(*self.w["lm_head"], norm(x.float() + b["o"]), b["logits"], b["ws"][2])
+        self.products(["o"], b["a"].view(n, HEADS * DIM), [b["o"]], b["ws"][2])
+        self.products(["lm_head"], self.norm(b, x, b["o"]), [b["logits"]], b["ws"][2])
 
 
 class Server:
