@@ -41,7 +41,7 @@ constexpr float kOne44 = 17592186044416.0f;
 struct Dist {
     const void *x;
     int f32, vec;
-    int easy;     // more than one token may stay, and the logits are finite
+    int easy;     // some token stays, and none is infinite
     int last;     // the highest index that stays among the logits of `least`
     RowCut c;
     float inv;    // 1 / total (0: no token stays)
@@ -52,13 +52,14 @@ struct Dist {
         f32 = is_f32, vec = (reinterpret_cast<uintptr_t>(x) & (is_f32 ? 15 : 7)) == 0;
         c = cuts[row];
         inv = c.total ? __fdiv_rn(1.0f, __ull2float_rn(c.total)) : 0.0f;
-        easy = c.total != 0 && c.one < 0 && !c.inf;
-        last = c.thr ? int(key_index(c.thr)) : 0x7FFFFFFF;
+        easy = c.total != 0 && !c.inf;
+        last = c.one >= 0 ? c.one : c.thr ? int(key_index(c.thr)) : 0x7FFFFFFF;
         const uint32_t k = uint32_t(c.thr >> 32);
         const float at = __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
-        least = c.total == 0 ? INFINITY : c.one >= 0 || !c.thr ? -INFINITY : c.inf ? 0.0f : at;
+        least = c.total == 0 ? INFINITY : c.inf ? 0.0f : c.one >= 0 ? c.mx : c.thr ? at : -INFINITY;
     }
-    // the weight of token i with logit v, of an easy row
+    // the weight of token i with logit v, of an easy row (a single token that stays is
+    // the first of the largest: mx, with 1 / t as 1)
     __device__ __forceinline__ uint32_t easy_weight(float v, int i) const {
         const uint32_t w = __float2uint_rn(expf(__fmul_rn(__fsub_rn(v, c.mx), c.inv_t)) * kOne31);
         return (v > least || (v == least && i <= last)) && w >= c.floor_w ? w : 0u;
@@ -199,7 +200,12 @@ __global__ void __launch_bounds__(kAT, 4) accept_kernel(const __grid_constant__ 
     const bool read_q = d.rest && d.q.c.one < 0;
     const float4 none = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
     const auto read_x = [&](int i, int end) { return i < end ? d.p.logits4(i, V) : none; };
-    const auto read_y = [&](int i, int end) { return read_q && i < end ? d.q.logits4(i, V) : none; };
+    const auto read_y = [&](int i, int end) {
+        if (read_q && i < end) return d.q.logits4(i, V);
+        const int k = d.rest ? d.q.c.one - i : -1;  // (the one token's logit need not be read)
+        const auto at = [&](int j) { return j == k ? d.q.c.mx : -INFINITY; };
+        return make_float4(at(0), at(1), at(2), at(3));
+    };
     u64 mine = 0, whole = 0, before;
     int at = 0;
     u64 *part = a.parts + (r * a.pieces) * 2;

@@ -132,7 +132,7 @@ __device__ __forceinline__ void add_if(uint32_t addr, uint32_t v, uint32_t w, ui
                  : "memory");
 }
 
-// A block's sums of a and b (both in every thread of warp 0 when it returns).
+// A block's sums of a and b (in warp 0's threads; the others keep their warp's).
 template <int W>
 __device__ __forceinline__ void block_sum2(Small &sh, u64 &a, u64 &b) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -390,6 +390,7 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
         return;
     }
     row.inv_t = fminf(__fdiv_rn(1.0f, t), 3.402823466e38f);
+    const float unit = fmaxf(t, 2.9387359e-39f);  // logits per unit of the exponent
     Small *root = cl.map_shared_rank(&sh, 0);
     u64 thr = 0, kept = 0;  // (the first CTA's)
     uint32_t w_thr = 0;
@@ -477,7 +478,6 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
                 Small *o = cl.map_shared_rank(&sh, c);
                 o->level = l, o->from = thr;
             }
-            sh.list_n = 0u;
         }
     };
     // The weight of the list's tokens from thr on.
@@ -506,9 +506,11 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
                     // (a bin's end is half a step off the integer; 0.1 more, and the roundings)
                     const float d0 = g.bin == kBins - 1 ? -INFINITY : -(float(g.bin) + 0.6f) / slope, d1 = -(float(g.bin) - 0.6f) / slope;
                     const float pad = 1e-6f * fabsf(row.mx);
-                    g.x0 = row.mx + d0 * t * 1.000001f - pad, g.x1 = row.mx + d1 * t + 1e-6f * fabsf(d1 * t) + pad;
+                    g.x0 = row.mx + d0 * unit * 1.000001f - pad, g.x1 = row.mx + d1 * unit * (d1 < 0.0f ? 0.999999f : 1.000001f) + pad;
                 }
                 tell(g);
+                // (a cluster barrier lies behind the others' last look at it)
+                if (tid == 0) sh.list_n = 0u;
             }
             cl.sync();
             g = sh.level;
@@ -591,7 +593,7 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
         }
         cl.sync();
         const float end = sh.level.x0;
-        const float x0 = row.inf ? 0.0f : row.mx + end * t * 1.000001f - 1e-6f * fabsf(row.mx);
+        const float x0 = row.inf ? 0.0f : row.mx + end * unit * 1.000001f - 1e-6f * fabsf(row.mx);
         between(x0, INFINITY, [&](int i, float v) {
             v = row.clean(v);
             if (i >= row.n || !(row.arg(v) >= end)) return;

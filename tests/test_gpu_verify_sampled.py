@@ -277,3 +277,97 @@ def test_refusals(dev, w12mod):
     with pytest.raises(w12mod.W12Error):
         call(ws=ws[:256])
     assert w12mod.verify_sampled_workspace_size(0, 1, 5) == w12mod.verify_sampled_workspace_size(1, 1, w12mod.SAMPLE_MAX_V + 1) == 0
+
+
+def _draws(w12mod, dev, x, cut, u):
+    """The tokens that w12_verify_sampled and w12_sample draw from a row with each of the numbers u."""
+    import torch
+    n, V = len(u), len(x)
+    rows = torch.from_numpy(np.broadcast_to(np.asarray(x, dtype=np.float32), (n, V)).copy()).to(dev)
+    f = {k: np.full(n, v) for k, v in cut.items()}
+    _, nxt, _ = _call(w12mod, dev, rows, None, n, 1, None, np.asarray(u)[:, None], f)
+    tokens = torch.empty(n, dtype=torch.int32, device=dev)
+    ws = w12mod.workspace(w12mod.sample_workspace_size(n, 1, V), dev)
+    d = {k: torch.from_numpy(v).to(dev, torch.int32 if k == "top_k" else torch.float32) for k, v in f.items()}
+    w12mod.sample(rows, n, 1, torch.from_numpy(np.asarray(u, dtype=np.float32)).to(dev), tokens, ws,
+                  d.get("temperature"), d.get("top_k"), d.get("top_p"), d.get("min_p"))
+    return nxt.tolist(), tokens.cpu().tolist()
+
+
+U = [0.0, 2.0 ** -24, 0.25, 0.5, 0.9, 1.0 - 2.0 ** -24]
+
+
+@pytest.mark.parametrize("V", [700, 20001, 151936])
+@pytest.mark.parametrize("cut", [dict(top_p=0.5), dict(top_p=2.0 ** -20), dict(top_k=300), dict(top_k=500), dict(top_k=500, top_p=0.5),
+                                 dict(top_k=300, top_p=0.5), dict(top_p=0.75, min_p=0.5), dict(top_p=0.75, min_p=1.25)],
+                         ids=lambda c: "_".join(f"{k}{v:.2g}" for k, v in c.items()))
+def test_equal_logits_under_cuts(dev, w12mod, V, cut):
+    """Equal weights: the first of them stay, min(k, V) and of these ceil(p n); the
+    draw is floor(u n) -- exactly, the weights being 2^31 each."""
+    n = min(cut.get("top_k", V), V)
+    n = int(np.ceil(cut.get("top_p", 1.0) * n))  # (p a multiple of 2^-24, so exact)
+    want = [-1 if cut.get("min_p", 0.0) > 1.0 else int(float(np.float32(u)) * n) for u in U]
+    got, other = _draws(w12mod, dev, np.full(V, -3.5), cut, U)
+    assert got == want and other == want
+    # a second, lighter kind of token among them (weight e^-1): all before it in the order
+    x = np.full(V, 1.0)
+    x[1::3] = 0.0
+    got, other = _draws(w12mod, dev, x, cut, U)
+    assert got == other
+
+
+@pytest.mark.parametrize("cut", [dict(top_p=0.9), dict(top_k=50), dict(top_k=1000, top_p=0.9), dict(min_p=0.25), dict(top_k=50, top_p=0.6, min_p=0.1)],
+                         ids=lambda c: "_".join(c))
+@pytest.mark.parametrize("row", ["large", "hot", "cold", "tiny", "inf", "nan", "zeros", "steps", "two"])
+def test_unusual_rows_under_cuts(dev, w12mod, row, cut):
+    """Rows and temperatures at the ends of what there is: the same tokens as w12_sample."""
+    rng = np.random.default_rng(7)
+    V = 30011
+    x = rng.standard_normal(V).astype(np.float32)
+    t = 1.0
+    if row == "large":
+        x, t = x * np.float32(8e37), 3e37
+    elif row == "hot":
+        t = 1e30
+    elif row == "cold":
+        t = 1e-30
+    elif row == "tiny":  # 1 / t is past the largest float
+        x, t = x * np.float32(1e-38), 1e-40
+    elif row == "inf":
+        x[rng.integers(0, V, 900)] = np.inf
+        x[5] = -np.inf
+    elif row == "nan":
+        x[rng.integers(0, V, 20000)] = np.nan
+        x[rng.integers(0, V, 20000)] = -np.inf
+    elif row == "zeros":  # both zeros are one logit
+        x = np.where(rng.random(V) < 0.5, 0.0, -0.0).astype(np.float32)
+    elif row == "steps":
+        x = np.floor(4 * x) / 4
+    elif row == "two":
+        x[:] = -np.inf
+        x[77], x[30010] = 0.0, -1.0
+    got, other = _draws(w12mod, dev, x, dict(cut, temperature=t), U)
+    assert got == other and min(got) >= 0
+
+
+@pytest.mark.parametrize("t", [0.0, 1.0])
+@pytest.mark.parametrize("qt", [0.0, 0.7])
+def test_greedy_rows(dev, w12mod, t, qt):
+    """Single tokens on either side, the largest more than once, or infinite."""
+    import torch
+    V, inf = 5000, float("inf")
+    x, q = torch.zeros(8, V, device=dev), torch.zeros(4, V, device=dev)
+    top = [3, 4999, 128, 2000]
+    for r in range(4):
+        x[2 * r, top[r]] = inf if r == 3 else 40.0
+        x[2 * r + 1, 11] = 40.0
+        q[r, top[r] if r else 9] = inf if r == 2 else 40.0
+    x[2, 4990], x[2, 4999], q[1, 4990] = 40.0, 40.0, 40.0
+    q[1, 4999] = 40.0
+    # request 0: the drafter's token is another; 1: one of two equal ones; 2, 3: the same
+    draft = [[9], [4990], [128], [2000]]
+    one = np.full(4, 1.0, dtype=np.float32)
+    acc, nxt, ratio = _call(w12mod, dev, x, q, 4, 2, draft, np.full((4, 2), 0.5), dict(temperature=t * one), dict(temperature=qt * one))
+    half = t > 0 and qt == 0  # request 1: half of the target's against all of the drafter's, and u q < p fails by equality
+    assert ratio[:, 0].tolist() == [0.0, 0.5 if half else 1.0, 1.0, 1.0]
+    assert acc.tolist() == [0, 0 if half else 1, 1, 1] and nxt.tolist() == [3, 4999 if half else 11, 11, 11]
