@@ -493,7 +493,8 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
     };
     // Finds the boundary: `need` by count or mass, of the bins that were added up.  The
     // tokens counted are those from `from` on with a weight of `light` at least.
-    const auto search = [&](u64 need, bool by_count, uint32_t light) {
+    // After the last search (`last`) the other CTAs are not needed: false for them.
+    const auto search = [&](u64 need, bool by_count, uint32_t light, bool last) {
         Level g{0ull, ~0ull, -1, 0, 0.0f, 0.0f};
         u64 above = 0;
 #pragma unroll 1
@@ -539,6 +540,7 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
             cl.sync();
             const uint32_t n = root->list_n;
             if (n <= uint32_t(kCap)) {
+                if (last && me != 0) return false;
                 if (me == 0) {
                     resolve(sh, cut, n, thr, above, need, by_count);
                     if (sh.thr != ~0ull) {
@@ -573,9 +575,11 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
         if (me == 0) {
             const uint32_t k = uint32_t(thr >> 32);
             w_thr = thr ? row.weight(__uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k)) : 0u;
-            tell(g);  // (the threshold)
         }
+        if (last) return me == 0;
+        if (me == 0) tell(g);  // (the threshold)
         cl.sync();
+        return true;
     };
 
     if (CUTS && by_k && top_k <= kCap / 2) {
@@ -604,7 +608,8 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
         const uint32_t n = root->list_n;
         done = n <= uint32_t(kCap);
         if (done) {
-            if (me == 0) {
+            if (me != 0) return;
+            {
                 u64 need = u64(top_k);
                 bool by_count = true, cut_it = n > uint32_t(top_k) || end > -kSpan;  // (else: every token that has a weight)
 #pragma unroll 1
@@ -715,7 +720,7 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
                 }
                 if (!CUTS || !by_p) break;
             }
-            search(need, stage == 0, light);
+            if (!search(need, stage == 0, light, stage == 1)) return;
             if (stage == 0) clear();
         }
         // min_p above the threshold: all from floor_w on, else what the cuts left
@@ -759,7 +764,9 @@ __global__ void __launch_bounds__(CUTS ? kT : kPlainT, CUTS ? 2 : 5) cut_kernel(
         cut_row<W12_F32, CUTS>(cl, a, s, r, smem);
     else
         cut_row<W12_BF16, CUTS>(cl, a, s, r, smem);
-    sync_relaxed();  // no CTA leaves while another may read its shared memory
+    // The first CTA, whose shared memory the others read last, leaves after them (a
+    // cluster barrier waits for the threads that have not left).
+    if (cl.block_rank() == 0) sync_relaxed();
 }
 
 constexpr size_t kMostShared = 227 * 1024;

@@ -320,8 +320,6 @@ constexpr int kPackThreads = 256;
 // A thread per (column, 128-k group); columns past N are zeros.
 __global__ void __launch_bounds__(kPackThreads) pack_kernel(const uint8_t *codes, const uint8_t *scales, int64_t KG, int64_t N,
                                                             int64_t NP, uint8_t *blob) {
-    pdl_launch_dependents();
-    pdl_wait_previous();
     const int64_t i = int64_t(blockIdx.x) * kPackThreads + threadIdx.x;
     const int64_t n = i / KG, kg = i % KG;
     if (n >= NP) return;
@@ -353,8 +351,6 @@ __device__ __forceinline__ uint32_t e2m1_code(float a) {
 // The same from bf16 weights [N][K].
 __global__ void __launch_bounds__(kPackThreads) encode_kernel(const uint16_t *w, int64_t KG, int64_t N, int64_t NP, float scale,
                                                               uint8_t *blob) {
-    pdl_launch_dependents();
-    pdl_wait_previous();
     const int64_t i = int64_t(blockIdx.x) * kPackThreads + threadIdx.x;
     const int64_t n = i / KG, kg = i % KG;
     if (n >= NP) return;
@@ -398,8 +394,6 @@ __global__ void __launch_bounds__(kPackThreads) encode_kernel(const uint16_t *w,
 
 // Back to fp32 [N][K]: code times scale (exact) times the matrix's number.
 __global__ void __launch_bounds__(kPackThreads) decode_kernel(const uint8_t *blob, int64_t KG, int64_t N, float scale, float *out) {
-    pdl_launch_dependents();
-    pdl_wait_previous();
     const int64_t i = int64_t(blockIdx.x) * kPackThreads + threadIdx.x;
     const int64_t n = i / KG, kg = i % KG;
     if (n >= N) return;
