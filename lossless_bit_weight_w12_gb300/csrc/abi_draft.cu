@@ -242,8 +242,10 @@ bool cut_aligned(const w12_cut *c) {
     return !c || (aligned(c->temperature, 4) && aligned(c->top_k, 4) && aligned(c->top_p, 4) && aligned(c->min_p, 4));
 }
 
-CutSide cut_side(const void *logits, int dtype, int64_t R, int64_t T, int64_t V, const w12_cut *cut, RowCut *out) {
+CutSide cut_side(const void *logits, int dtype, int64_t R, int64_t T, int64_t V, const w12_cut *cut, const int32_t *draft,
+                 int64_t drafts, RowCut *out) {
     CutSide s = {};
+    s.draft = draft, s.drafts = drafts;
     s.x = logits, s.f32 = dtype == W12_F32;
     s.vec = aligned(logits, 16) && uint64_t(V) * size_of(dtype) % 16 == 0;
     s.rows = R * T, s.T = T;
@@ -268,7 +270,7 @@ int plan_verify(int64_t R, int64_t T, int64_t V, VerifyPlan *p) {
     p->cuts = kWsHeader;
     p->arrived = p->cuts + round256(uint64_t(R) * uint64_t(2 * T - 1) * sizeof(RowCut));
     p->parts = p->arrived + round256(uint64_t(R) * 4u);
-    p->total = p->parts + round256(uint64_t(R) * uint64_t(p->pieces) * 16u);
+    p->total = p->parts + round256(uint64_t(R) * uint64_t(p->pieces) * uint64_t(kAcceptRuns) * 16u);
     return W12_OK;
 }
 
@@ -303,11 +305,11 @@ extern "C" int w12_verify_sampled(const void *logits, int dtype, const void *dra
     a.draft = draft, a.u = u, a.ratio = ratio, a.accept_len = accept_len, a.next_tok = next_tok;
     a.R = R, a.T = T, a.V = V;
     a.arrived = reinterpret_cast<uint32_t *>(w + p.arrived);
-    a.parts = reinterpret_cast<unsigned long long *>(w + p.parts);
+    a.parts = reinterpret_cast<ulonglong2 *>(w + p.parts);
     a.each = p.each, a.pieces = p.pieces;
     CutArgs c = {};
-    c.side[0] = cut_side(logits, dtype, R, T, V, target_cut, cuts);
-    if (T > 1) c.side[1] = cut_side(draft_logits, draft_dtype, R, T - 1, V, draft_cut, cuts + R * T);
+    c.side[0] = cut_side(logits, dtype, R, T, V, target_cut, draft, T - 1, cuts);
+    if (T > 1) c.side[1] = cut_side(draft_logits, draft_dtype, R, T - 1, V, draft_cut, draft, T - 1, cuts + R * T);
     c.V = V, c.err = reinterpret_cast<int *>(w), c.arrived = a.arrived;
     c.cuts = c.side[0].top_k || c.side[0].top_p || c.side[1].top_k || c.side[1].top_p;
     const int done = launch_cut(c, stream);

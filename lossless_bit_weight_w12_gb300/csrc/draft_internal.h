@@ -6,6 +6,8 @@
 #include <cstddef>
 #include <cstdint>
 
+#include <vector_types.h>
+
 #include "step_internal.h"
 
 namespace w12 {
@@ -69,15 +71,16 @@ int launch_fp4_tc(Fp4Batch &b, int grid, void *stream);
 // n e4m3 codes as bf16 (n a multiple of 16).
 int launch_fp4_widen(const void *codes, void *out, int64_t n, void *stream);
 
-// What the cuts leave of a row: a token stays if its weight (sample_device.cuh,
-// with mx and inv_t) is above w_thr, or equal with a composite of thr at least,
-// and not below floor_w.  one >= 0: that token alone.  total: the weight that
-// stays; 0: no token does.
+// What the cuts leave of a row: the tokens with a logit above `least`, or equal
+// with an index of `last` at most, whose weight (with mx and inv_t; cut_device.cuh)
+// is not below `floor`.  A row whose largest logit is infinite has least = infinity
+// and mx the largest float, one without any token last = -1 besides.
 struct RowCut {
-    uint64_t thr, total;
-    float mx, inv_t;
-    uint32_t w_thr, floor_w;
-    int32_t one, inf;
+    float mx, inv_t, least, floor;
+    int32_t last;
+    int32_t one;   // >= 0: that token alone stays (it is `last`)
+    float inv;     // 1 / the sum of the weights that stay; 0: none does
+    float share;   // of the row's drafted token (0: there is none)
 };
 
 // The cuts of the rows of two tensors of logits (the target's, the drafter's).
@@ -88,6 +91,8 @@ struct CutSide {
     int64_t rows, T;     // T rows per request
     const float *temperature, *top_p, *min_p;
     const int32_t *top_k;
+    const int32_t *draft;  // [requests][drafts]: of row r that of r % T, where it is below drafts
+    int64_t drafts;
     RowCut *out;
 };
 
@@ -111,9 +116,10 @@ struct AcceptArgs {
     int32_t *accept_len, *next_tok;
     int64_t R, T, V;
     uint32_t *arrived;      // [R], zeros
-    unsigned long long *parts;  // [R][pieces][2]
-    int32_t each, pieces;   // tokens a piece, pieces a row
+    ulonglong2 *parts;      // [R][pieces * kAcceptRuns]
+    int32_t each, pieces;   // tokens a CTA (a multiple of 1024), CTAs a row
 };
+constexpr int kAcceptRuns = 8;  // of a CTA's piece
 void accept_pieces(int64_t R, int64_t V, int32_t *each, int32_t *pieces);
 int launch_accept(const AcceptArgs &a, void *stream);
 

@@ -11,9 +11,10 @@
 // depend on how the row is cut.
 //
 // A request's row is cut into pieces of consecutive tokens, one per CTA.  Every CTA
-// finds the first draft that does not stay (a thread per position) and adds its
-// piece up; the last one to finish finds the piece that holds the drawn token and
-// goes through it again.
+// finds the first draft that does not stay (a thread per position; the drafts' shares
+// of p and q come with the cuts), and each of its warps adds a run of its piece up;
+// the last CTA to finish finds the run that holds the drawn token and goes through
+// that again.
 //
 // What bounds it: the instructions of two exact exponentials a token (some 50
 // where nothing is cut, so few requests are spread over all SMs), and the steps
@@ -24,8 +25,8 @@
 
 #include <algorithm>
 
+#include "cut_device.cuh"
 #include "draft_internal.h"
-#include "sample_device.cuh"
 #include "step_device.cuh"
 
 namespace w12 {
@@ -34,6 +35,7 @@ namespace {
 
 constexpr int kAT = 256;        // threads per CTA
 constexpr int kAW = kAT / 32;
+static_assert(kAW == kAcceptRuns, "a run a warp");
 constexpr int kStep = 4 * kAT;  // tokens of a CTA at a time
 constexpr float kOne44 = 17592186044416.0f;
 
@@ -41,55 +43,48 @@ constexpr float kOne44 = 17592186044416.0f;
 struct Dist {
     const void *x;
     int f32, vec;
-    int easy;     // some token stays, and none is infinite
-    int last;     // the highest index that stays among the logits of `least`
     RowCut c;
-    float inv;    // 1 / total (0: no token stays)
-    float least;  // the tokens that stay have logits from it on
 
     __device__ __forceinline__ void init(const void *logits, int is_f32, int64_t row, int64_t V, const RowCut *cuts) {
         x = static_cast<const unsigned char *>(logits) + row * V * (is_f32 ? 4 : 2);
         f32 = is_f32, vec = (reinterpret_cast<uintptr_t>(x) & (is_f32 ? 15 : 7)) == 0;
         c = cuts[row];
-        inv = c.total ? __fdiv_rn(1.0f, __ull2float_rn(c.total)) : 0.0f;
-        easy = c.total != 0 && !c.inf;
-        last = c.one >= 0 ? c.one : c.thr ? int(key_index(c.thr)) : 0x7FFFFFFF;
-        const uint32_t k = uint32_t(c.thr >> 32);
-        const float at = __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
-        least = c.total == 0 ? INFINITY : c.inf ? 0.0f : c.one >= 0 ? c.mx : c.thr ? at : -INFINITY;
     }
-    // the weight of token i with logit v, of an easy row (a single token that stays is
-    // the first of the largest: mx, with 1 / t as 1)
-    __device__ __forceinline__ uint32_t easy_weight(float v, int i) const {
-        const uint32_t w = __float2uint_rn(expf(__fmul_rn(__fsub_rn(v, c.mx), c.inv_t)) * kOne31);
-        return (v > least || (v == least && i <= last)) && w >= c.floor_w ? w : 0u;
+    __device__ __forceinline__ uint32_t bits(int i) const {
+        return f32 ? __float_as_uint(__ldg(static_cast<const float *>(x) + i)) : uint32_t(__ldg(static_cast<const uint16_t *>(x) + i));
     }
-    __device__ __forceinline__ float logit(int i) const {
-        return f32 ? __ldg(static_cast<const float *>(x) + i)
-                   : bf16_bits_to_float(__ldg(static_cast<const uint16_t *>(x) + i));
-    }
-    // logits i .. i + 3 (i a multiple of 4; past V: -infinity)
-    __device__ __forceinline__ float4 logits4(int i, int V) const {
-        if (i + 4 <= V && vec) {
-            if (f32) return __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(x) + i));
-            const uint2 y = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(x) + i));
-            return make_float4(bf16_bits_to_float(y.x & 0xFFFFu), __uint_as_float(y.x & 0xFFFF0000u),
-                               bf16_bits_to_float(y.y & 0xFFFFu), __uint_as_float(y.y & 0xFFFF0000u));
+    // Logits i .. i + 3 as they lie in memory (i a multiple of 4; from `end` on:
+    // -infinity), so that nothing waits for them before they are used.
+    __device__ __forceinline__ uint4 read(int i, int end) const {
+        uint4 r = make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
+        if (!f32) r.x = r.y = 0xFF80FF80u;
+        if (i + 4 <= end && vec) {
+            if (f32) {
+                r = __ldg(reinterpret_cast<const uint4 *>(static_cast<const float *>(x) + i));
+            } else {
+                const uint2 y = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(x) + i));
+                r.x = y.x, r.y = y.y;
+            }
+        } else if (i < end) {
+            const uint32_t none = f32 ? 0xFF800000u : 0xFF80u;
+            const uint32_t b0 = bits(i), b1 = i + 1 < end ? bits(i + 1) : none, b2 = i + 2 < end ? bits(i + 2) : none;
+            const uint32_t b3 = i + 3 < end ? bits(i + 3) : none;
+            r = f32 ? make_uint4(b0, b1, b2, b3) : make_uint4(b0 | b1 << 16, b2 | b3 << 16, 0u, 0u);
         }
-        const auto at = [&](int j) { return i + j < V ? logit(i + j) : -INFINITY; };
-        return make_float4(at(0), at(1), at(2), at(3));
+        return r;
     }
-    // the weight of token i with logit v among those that stay (v past V: -infinity)
-    __device__ __noinline__ uint32_t weight(float v, int i) const {
-        if (c.one >= 0) return i == c.one ? 0x80000000u : 0u;
-        if (!(v >= least)) return 0u;
-        if (c.inf) v = v == INFINITY ? 0.0f : -INFINITY;
-        const uint32_t w = __float2uint_rn(expf(__fmul_rn(__fsub_rn(v, c.mx), c.inv_t)) * kOne31);
-        if (w < c.w_thr || w < c.floor_w) return 0u;
-        if (w == c.w_thr && c.thr && pack_key(v, uint32_t(i)) < c.thr) return 0u;
-        return w;
+    // The same for a row of which one token stays: that one's logit need not be read.
+    __device__ __forceinline__ uint4 read_one(int i) const {
+        const uint32_t none = 0xFF800000u, top = __float_as_uint(c.least);
+        const int k = c.one - i;
+        const uint4 r = make_uint4(k == 0 ? top : none, k == 1 ? top : none, k == 2 ? top : none, k == 3 ? top : none);
+        return f32 ? r : make_uint4(r.x >> 16 | (r.y & 0xFFFF0000u), r.z >> 16 | (r.w & 0xFFFF0000u), 0u, 0u);
     }
-    __device__ __forceinline__ float share(float v, int i) const { return __fmul_rn(__uint2float_rn(weight(v, i)), inv); }
+    __device__ __forceinline__ float4 floats(const uint4 &r) const {
+        return f32 ? make_float4(__uint_as_float(r.x), __uint_as_float(r.y), __uint_as_float(r.z), __uint_as_float(r.w))
+                   : make_float4(bf16_bits_to_float(r.x & 0xFFFFu), __uint_as_float(r.x & 0xFFFF0000u),
+                                 bf16_bits_to_float(r.y & 0xFFFFu), __uint_as_float(r.y & 0xFFFF0000u));
+    }
 };
 
 // round(2^44 max(p - q, 0)): below 2^31 in one conversion, else 20 bits and the 24
@@ -104,43 +99,12 @@ __device__ __forceinline__ u64 above(float p, float q) {
     return (u64(hi) << 24) + u64(__float2uint_rn((z - __uint2float_rn(hi)) * 16777216.0f));
 }
 
-// What a request's CTAs share: the row that is drawn from.
+// What a request's CTAs share: the row that is drawn from, and, where a draft was
+// refused (rest), the drafter's.
 struct Draw {
     Dist p, q;
-    int rest;  // from p - q
+    int rest;
 };
-
-// The draw's weights of tokens i .. i + 3 (logits x and y): their sum, and in
-// whole the target's own.  Where the sum -- of the target's own if !rest -- passes
-// `stop`, *at is the token.
-__device__ __forceinline__ u64 quad(const Draw &d, bool rest, int i, float4 x, float4 y, u64 &whole, u64 stop, int *at) {
-    u64 sum = 0;
-    const bool easy = d.p.easy && (!d.rest || d.q.easy);
-    const float ip = d.p.inv, iq = d.q.inv, least = d.p.least;
-#pragma unroll 1
-    for (int j = 0; j < 4; ++j) {
-        if (!__any_sync(0xFFFFFFFFu, x.x >= least)) {
-            // (cut rows: most of them)
-        } else if (easy) {
-            const uint32_t w = d.p.easy_weight(x.x, i + j), z = d.rest ? d.q.easy_weight(y.x, i + j) : 0u;
-            whole = add_wide(whole, w);
-            const u64 a = above(__fmul_rn(__uint2float_rn(w), ip), __fmul_rn(__uint2float_rn(z), iq));
-            sum += rest ? a : u64(w);
-        } else {
-            const uint32_t w = d.p.weight(x.x, i + j);
-            whole = add_wide(whole, w);
-            if (!rest)
-                sum += w;
-            else if (w)
-                sum += above(__fmul_rn(__uint2float_rn(w), ip), d.q.share(y.x, i + j));
-        }
-        if (sum > stop) {
-            if (*at < 0) *at = i + j;
-        }
-        x = make_float4(x.y, x.z, x.w, 0.0f), y = make_float4(y.y, y.z, y.w, 0.0f);
-    }
-    return sum;
-}
 
 // The sum over the block, and what lies before this thread.
 __device__ __forceinline__ u64 block_scan(u64 *s_warp, u64 mine, u64 *before) {
@@ -163,9 +127,10 @@ __global__ void __launch_bounds__(kAT, 4) accept_kernel(const __grid_constant__ 
     __shared__ u64 s_warp[kAW];
     __shared__ long long s_first;
     __shared__ Draw d;
-    __shared__ int s_last, s_piece, s_token;
-    __shared__ u64 s_before;
-    const int tid = threadIdx.x;
+    __shared__ int s_last, s_run;
+    __shared__ u64 s_left;  // what is left of the drawn number at the run
+    __shared__ u64 s_each[4 * kAT];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t r = int64_t(blockIdx.x) / a.pieces, drafts = a.T - 1;
     const int me = int(blockIdx.x % a.pieces), V = int(a.V);
     if (tid == 0) s_first = drafts;
@@ -176,15 +141,9 @@ __global__ void __launch_bounds__(kAT, 4) accept_kernel(const __grid_constant__ 
     // ---- the first draft that does not stay
 #pragma unroll 1
     for (int64_t i = tid; i < drafts; i += kAT) {
-        const int64_t t = a.draft[r * drafts + i];
-        Dist x, y;
-        x.init(a.logits, a.f32, r * a.T + i, a.V, a.cuts);
-        y.init(a.draft_logits, a.draft_f32, r * drafts + i, a.V, a.draft_cuts);
-        const bool there = t >= 0 && t < a.V;
-        const float vx = there ? x.logit(int(t)) : 0.0f, vy = there ? y.logit(int(t)) : 0.0f;
-        const float p = there ? x.share(vx, int(t)) : 0.0f, q = there ? y.share(vy, int(t)) : 0.0f;
-        if (a.ratio && me == 0) a.ratio[r * drafts + i] = p >= q ? (p > 0.0f ? 1.0f : 0.0f) : __fdiv_rn(p, q);
+        const float p = a.cuts[r * a.T + i].share, q = a.draft_cuts[r * drafts + i].share;
         if (!(__fmul_rn(a.u[r * a.T + i], q) < p)) atomicMin(&s_first, static_cast<long long>(i));
+        if (a.ratio && me == 0) a.ratio[r * drafts + i] = p >= q ? (p > 0.0f ? 1.0f : 0.0f) : __fdiv_rn(p, q);
     }
     __syncthreads();
     const int64_t n = s_first;
@@ -196,96 +155,108 @@ __global__ void __launch_bounds__(kAT, 4) accept_kernel(const __grid_constant__ 
     }
     __syncthreads();
 
-    // ---- this piece's sums
-    const bool read_q = d.rest && d.q.c.one < 0;
-    const float4 none = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-    const auto read_x = [&](int i, int end) { return i < end ? d.p.logits4(i, V) : none; };
+    const int refused = d.rest;
     const auto read_y = [&](int i, int end) {
-        if (read_q && i < end) return d.q.logits4(i, V);
-        const int k = d.rest ? d.q.c.one - i : -1;  // (the one token's logit need not be read)
-        const auto at = [&](int j) { return j == k ? d.q.c.mx : -INFINITY; };
-        return make_float4(at(0), at(1), at(2), at(3));
+        return !refused ? make_uint4(0u, 0u, 0u, 0u) : d.q.c.one < 0 ? d.q.read(i, end) : d.q.read_one(i);
     };
-    u64 mine = 0, whole = 0, before;
-    int at = 0;
-    u64 *part = a.parts + (r * a.pieces) * 2;
-    {
-        const int end = min((me + 1) * a.each, V);
-        int i = me * a.each + 4 * tid;
-        float4 x = read_x(i, end), y = read_y(i, end);
+    // ---- pass 0: the sums of this warp's run of tokens; pass 1, in the last CTA: the
+    // run that holds the drawn token once more, all threads on it (one loop for both,
+    // so that its code is there when the second begins)
+    const int run = a.each / kAW, runs = a.pieces * kAW;
+    ulonglong2 *part = a.parts + r * runs;
+    const RowCut pc = d.p.c, qc = d.q.c;
+    int rest = refused, hop = 128, trips = run / 128;
+    int i = me * a.each + warp * run + 4 * lane, end = min(me * a.each + (warp + 1) * run, V);
+    u64 left = 0;
 #pragma unroll 1
-        for (int i0 = me * a.each; i0 < end; i0 += kStep, i += kStep) {  // (the next ones are on their way)
-            const float4 nx = read_x(i + kStep, end), ny = read_y(i + kStep, end);
-            mine += quad(d, d.rest, i, x, y, whole, ~0ull, &at);
-            x = nx, y = ny;
-        }
-    }
-    mine = block_scan(s_warp, mine, &before);
-    whole = block_scan(s_warp, whole, &before);
-    if (tid == 0) {
-        __stcg(&part[2 * me], mine);
-        __stcg(&part[2 * me + 1], whole);
-        __threadfence();
-        s_last = atomicAdd(&a.arrived[r], 1u) == uint32_t(a.pieces - 1);
-    }
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-
-    // ---- the last CTA: the piece, then the token
-    bool rest = d.rest;
-    u64 total = 0;
+    for (int pass = 0;; ++pass) {
+        u64 sum_rest = 0, sum_own = 0;
+        uint4 x0 = d.p.read(i, end), y0 = read_y(i, end), x1 = d.p.read(i + hop, end), y1 = read_y(i + hop, end);
 #pragma unroll 1
-    for (int pass = rest ? 0 : 1; pass < 2; ++pass) {  // where p - q leaves nothing: p
-        total = 0;
-        for (int c = tid; c < a.pieces; c += kAT) total += __ldcg(&part[2 * c + pass]);
-        total = block_scan(s_warp, total, &before);
-        rest = pass == 0;
-        if (total) break;
-    }
-    if (total == 0) {
-        if (tid == 0) a.accept_len[r] = int32_t(n), a.next_tok[r] = -1;
-        return;
-    }
-    const u64 target = scaled(fixed_u(a.u[r * a.T + drafts]), total);
-    u64 base = 0;
+        for (int k = 0; k < trips; ++k, i += hop) {
+            const uint4 x2 = d.p.read(i + 2 * hop, end), y2 = read_y(i + 2 * hop, end);
+            float4 x = d.p.floats(x0);
+            x0 = x1, x1 = x2;
+            u64 here = 0;
+            // (cut rows: most tokens are below)
+            int j = __any_sync(0xFFFFFFFFu, fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)) >= pc.least) || pass ? 0 : 4;
+            float4 y = d.q.floats(y0);
+            y0 = y1, y1 = y2;
 #pragma unroll 1
-    for (int c0 = 0; c0 < a.pieces; c0 += kAT) {  // (a whole number of rounds: all threads take part)
-        const int c = c0 + tid;
-        const u64 here = c < a.pieces ? __ldcg(&part[2 * c + (rest ? 0 : 1)]) : 0ull;
-        const u64 sum = block_scan(s_warp, here, &before);
-        if (base + before <= target && target < base + before + here) s_piece = c, s_before = base + before;
-        base += sum;
-    }
-    if (tid == 0) s_token = -1;
-    __syncthreads();
-    const int piece = s_piece;
-    base = s_before;
-    const int end = min((piece + 1) * a.each, V);
-#pragma unroll 1
-    for (int i0 = piece * a.each; i0 < end; i0 += kStep) {
-        const int i = i0 + 4 * tid;
-        const float4 x = read_x(i, end), y = read_y(i, end);
-        u64 here = 0, stop = ~0ull;
-#pragma unroll 1
-        for (int pass = 0; pass < 2; ++pass) {  // the sums, then the thread that holds the token
-            at = pass ? -1 : 0;
-            const u64 sum = quad(d, rest, i, x, y, whole, stop, &at);
-            if (pass == 0) {
-                here = sum;
-                const u64 all = block_scan(s_warp, here, &before);
-                before += base;
-                base += all;
-                if (target >= base) break;
-                stop = before <= target && target < before + here ? target - before : ~0ull;
-            } else if (stop != ~0ull) {
-                s_token = at;
+            for (; j < 4; ++j) {
+                const Weight w = cut_weight(pc, x.x, i + j);
+                u64 z = 0;
+                sum_own = add_wide(sum_own, w.whole);
+                if (refused) {
+                    z = above(__fmul_rn(w.f, pc.inv), __fmul_rn(cut_weight(qc, y.x, i + j).f, qc.inv));
+                    sum_rest += z;
+                }
+                if (pass) {
+                    if (!rest) z = w.whole;
+                    s_each[4 * tid + j] = z;
+                    here += z;
+                }
+                x = make_float4(x.y, x.z, x.w, 0.0f), y = make_float4(y.y, y.z, y.w, 0.0f);
             }
+            if (pass == 0) continue;
+            u64 before;
+            const u64 all = block_scan(s_warp, here, &before);
+            if (left < all) {
+                if (before <= left && left < before + here) {
+                    left -= before;
+                    int j = 0;
+#pragma unroll 1
+                    for (; j < 3 && left >= s_each[4 * tid + j]; ++j) left -= s_each[4 * tid + j];
+                    a.accept_len[r] = int32_t(n), a.next_tok[r] = i + j;
+                }
+                return;
+            }
+            left -= all;
         }
-        if (target < base) break;
+        if (pass) return;  // (not reached: the run holds it)
+        sum_rest = warp_sum64(sum_rest), sum_own = warp_sum64(sum_own);
+        if (lane == 0) __stcg(&part[me * kAW + warp], make_ulonglong2(sum_rest, sum_own));
+        __syncthreads();
+        if (tid == 0) {
+            __threadfence();
+            s_last = atomicAdd(&a.arrived[r], 1u) == uint32_t(a.pieces - 1);
+        }
+        __syncthreads();
+        if (!s_last) return;
+        __threadfence();
+        const int per = (runs + kAT - 1) / kAT, c0 = min(tid * per, runs), c1 = min(c0 + per, runs);
+        u64 total, mine, before;
+#pragma unroll 1
+        for (;; rest = 0) {  // (where p - q leaves nothing: p)
+            mine = 0;
+#pragma unroll 1
+            for (int c = c0; c < c1; ++c) {
+                const ulonglong2 z = __ldcg(&part[c]);
+                mine += rest ? z.x : z.y;
+            }
+            total = block_scan(s_warp, mine, &before);
+            if (total || !rest) break;
+        }
+        if (total == 0) {
+            if (tid == 0) a.accept_len[r] = int32_t(n), a.next_tok[r] = -1;
+            return;
+        }
+        const u64 target = scaled(fixed_u(a.u[r * a.T + drafts]), total);
+        if (before <= target && target < before + mine) {
+            left = target - before;
+            int c = c0;
+#pragma unroll 1
+            for (; c + 1 < c1; ++c) {
+                const ulonglong2 z = __ldcg(&part[c]);
+                if (left < (rest ? z.x : z.y)) break;
+                left -= rest ? z.x : z.y;
+            }
+            s_run = c, s_left = left;
+        }
+        __syncthreads();
+        left = s_left;
+        i = s_run * run + 4 * tid, end = min((s_run + 1) * run, V), hop = 4 * kAT, trips = (run + 4 * kAT - 1) / (4 * kAT);
     }
-    __syncthreads();
-    if (tid == 0) a.accept_len[r] = int32_t(n), a.next_tok[r] = s_token;
 }
 
 }  // namespace

@@ -29,6 +29,7 @@
 
 #include "async_common.cuh"
 #include "cluster_device.cuh"
+#include "cut_device.cuh"
 #include "draft_internal.h"
 #include "sample_device.cuh"
 #include "step_device.cuh"
@@ -117,6 +118,12 @@ struct Part {
     __device__ __forceinline__ uint32_t weight(float v) const { return __float2uint_rn(expf(arg(v)) * kOne31); }
     __device__ __forceinline__ u64 comp(float v, int i) const { return pack_key(v, first + uint32_t(i)); }
 };
+
+// The logit of a composite.
+__device__ __forceinline__ float key_logit(u64 c) {
+    const uint32_t k = uint32_t(c >> 32);
+    return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
+}
 
 // The larger of each half; a NaN loses against a number.
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
@@ -283,6 +290,21 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
         if (p < 16777216.0f) p_fix = p > 0.0f ? uint64_t(p) : 0ull;  // (a NaN is no cut)
     }
     const bool by_p = CUTS && p_fix < (1ull << 24);
+    int token = -1;  // the row's draft, for the first CTA
+    float drafted = 0.0f;
+    if (me == 0 && tid == 0 && r % s.T < s.drafts) {
+        token = s.draft[req * s.drafts + r % s.T];
+        if (token >= 0 && token < a.V) drafted = DT == W12_F32 ? static_cast<const float *>(s.x)[r * a.V + token]
+                                                               : bf16_bits_to_float(static_cast<const uint16_t *>(s.x)[r * a.V + token]);
+        if (token >= a.V) token = -1;
+    }
+    const auto put = [&](RowCut c, u64 total) {  // (one thread of the first CTA)
+        c.inv = total ? __fdiv_rn(1.0f, __ull2float_rn(total)) : 0.0f;
+        if (row.inf) c.mx = 3.402823466e38f, c.least = INFINITY;
+        if (!total) c.least = INFINITY, c.last = -1;
+        c.share = token >= 0 ? __fmul_rn(cut_weight(c, drafted, token).f, c.inv) : 0.0f;
+        s.out[r] = c;
+    };
     float best = -INFINITY;
     uint32_t best2 = 0xFF80FF80u;  // a pair of bf16 -infinities
 
@@ -361,7 +383,7 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
         row.mx = row.inf ? 0.0f : m;
     }
     if (row.mx == -INFINITY) {  // nothing can be sampled
-        if (me == 0 && tid == 0) s.out[r] = RowCut{0ull, 0ull, 0.0f, 1.0f, 0u, 1u, -1, 0};
+        if (me == 0 && tid == 0) put(RowCut{0.0f, 1.0f, INFINITY, 1.0f, -1, -1}, 0ull);
         return;
     }
     if (!(t > 0.0f)) {  // the lowest index of the largest
@@ -385,7 +407,8 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
         sync_sums();
         if (me == 0 && tid == 0) {
             for (int c = 0; c < cs; ++c) none = umax64(none, sh.first[c]);
-            s.out[r] = RowCut{0ull, 1ull << 31, row.mx, 1.0f, 0u, 1u, int32_t(key_index(none)), row.inf};
+            const int32_t one = int32_t(key_index(none));
+            put(RowCut{row.mx, 1.0f, row.mx, 1.0f, one, one}, 1ull << 31);
         }
         return;
     }
@@ -573,8 +596,7 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
             add_up();
         }
         if (me == 0) {
-            const uint32_t k = uint32_t(thr >> 32);
-            w_thr = thr ? row.weight(__uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k)) : 0u;
+            w_thr = thr ? row.weight(key_logit(thr)) : 0u;
         }
         if (last) return me == 0;
         if (me == 0) tell(g);  // (the threshold)
@@ -727,9 +749,7 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
         if (floor_w > 1u && floor_w > w_thr) kept = heavy;
     }
     if (me == 0 && tid == 0) {
-        const uint32_t k = uint32_t(thr >> 32);
-        w_thr = thr ? row.weight(__uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k)) : 0u;
-        s.out[r] = RowCut{thr, kept, row.mx, row.inv_t, w_thr, floor_w, -1, row.inf};
+        put(RowCut{row.mx, row.inv_t, thr ? key_logit(thr) : -INFINITY, float(floor_w), thr ? int32_t(key_index(thr)) : 0x7FFFFFFF, -1}, kept);
     }
 }
 
