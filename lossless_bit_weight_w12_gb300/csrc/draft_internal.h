@@ -100,6 +100,7 @@ struct CutArgs {
     CutSide side[2];
     int64_t V;
     int32_t chunk;       // logits per CTA of a row's cluster
+    int32_t ahead;       // rows that the GPU holds at a time
     int32_t cuts;        // a top_k or top_p is given
     int *err;
     uint32_t *arrived;   // [requests] set to zero, for launch_accept
