@@ -77,9 +77,10 @@ struct Small {
     uint32_t few_n;
 };
 
-// Behind it, for rows with cuts.  The bins are sums in two 16-bit halves (a bin's
-// stay below 2^32 for the 65536 logits a CTA can have), or counts; in the first CTA
-// the cluster's sums take their place, as 64-bit numbers in two halves.
+// Behind it, for rows with cuts.  The bins are sums modulo 2^32 and sums of the upper
+// 16-bit halves (with the 65536 logits a CTA can have, the lower halves' sums stay
+// below 2^32, so the two give the whole), or counts; in the first CTA the cluster's
+// sums take their place, as 64-bit numbers in two halves.
 struct CutMem {
     uint32_t lo[kBins], hi[kBins];
     u64 list[kCap];
@@ -132,10 +133,11 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
-// Adds v to a number in shared memory where w >= least.
+// Adds v to the number AT bytes behind addr in shared memory where w >= least.
+template <int AT>
 __device__ __forceinline__ void add_if(uint32_t addr, uint32_t v, uint32_t w, uint32_t least) {
-    asm volatile("{\n .reg .pred p;\n setp.ge.u32 p, %2, %3;\n @p red.shared.add.u32 [%0], %1;\n}\n" ::"r"(addr), "r"(v), "r"(w),
-                 "r"(least)
+    asm volatile("{\n .reg .pred p;\n setp.ge.u32 p, %2, %3;\n @p red.shared.add.u32 [%0+%4], %1;\n}\n" ::"r"(addr), "r"(v), "r"(w),
+                 "r"(least), "n"(AT)
                  : "memory");
 }
 
@@ -489,7 +491,7 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
                 }
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                    if (c0 + c < cs) m += u64(lo[c]) + (u64(hi[c]) << 16);
+                    if (c0 + c < cs) m += u64(lo[c] - (hi[c] << 16)) + (u64(hi[c]) << 16);
             }
             to->lo[b] = uint32_t(m), to->hi[b] = uint32_t(m >> 32);
         }
@@ -602,7 +604,7 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
                 const uint32_t w = row.weight(v);
                 if (w < light) return;
                 const int b = int((g.hi - c) >> g.shift);
-                atomicAdd(&cut.lo[b], by_count ? 1u : w & 0xFFFFu);
+                atomicAdd(&cut.lo[b], by_count ? 1u : w);
                 if (!by_count && w >> 16) atomicAdd(&cut.hi[b], w >> 16);
             });
             add_up();
@@ -716,8 +718,8 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
                             for (int j = 0; j < N; ++j) {
                                 total = add_wide(total, w[j]);
                                 if (decltype(bins)::value) {
-                                    add_if(to[j], w[j] & 0xFFFFu, w[j], light);
-                                    add_if(to[j] + 4u * kBins, w[j] >> 16, w[j], large);
+                                    add_if<0>(to[j], w[j], w[j], light);
+                                    add_if<4 * kBins>(to[j], w[j] >> 16, w[j], large);
                                 }
                             }
                         }
@@ -736,7 +738,7 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
                         total += w;
                         if (w >= floor_w) heavy += w;
                         if (CUTS && by_p && w >= light) {
-                            atomicAdd(&cut.lo[linear_bin(row.arg(v))], w & 0xFFFFu);
+                            atomicAdd(&cut.lo[linear_bin(row.arg(v))], w);
                             atomicAdd(&cut.hi[linear_bin(row.arg(v))], w >> 16);
                         }
                     }
