@@ -88,7 +88,10 @@ struct CutMem {
     u64 few[kFew];
     uint32_t few_w[kFew];
     uint32_t fine_lo[kFine], fine_hi[kFine], fine_n[kFine];
+
+    __device__ __forceinline__ float *tops() { return reinterpret_cast<float *>(fine_lo); }  // [kT], before those are used
 };
+static_assert(kFine >= kT, "the threads' maxima");
 constexpr size_t kSmallBytes = (sizeof(Small) + 127) / 128 * 128, kCutBytes = (sizeof(CutMem) + 127) / 128 * 128;
 
 // This CTA's part of a row in shared memory.
@@ -381,7 +384,35 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
             }
         }
     }
-    {
+    const bool quick = by_k && top_k <= kCap / 2 && t > 0.0f;
+    float near_top = -INFINITY;  // quick: one of kT threads' maxima, the same in every CTA
+    if (quick) {
+        // ---- of each warp the largest 32 / cs of its threads' maxima, for all CTAs
+        const int m = 32 / cs;
+        uint32_t key = order_key(best), top = key;
+        if (m < 32) {
+#pragma unroll 1
+            for (int j = 0; j < m; ++j) {
+                const uint32_t k = __reduce_max_sync(0xFFFFFFFFu, key);
+                if (lane == j) top = k;
+                if (lane == __ffs(__ballot_sync(0xFFFFFFFFu, key == k)) - 1) key = 0u;
+            }
+        }
+        const float v = key_logit(u64(top) << 32);
+        __syncthreads();
+        cluster_started();
+        if (lane < m)
+            for (int c = 0; c < cs; ++c) cl.map_shared_rank(&cut, c)->tops()[(me * kW + warp) * m + lane] = v;
+        cl.sync();
+        near_top = cut.tops()[tid];
+        const float w = key_logit(u64(__reduce_max_sync(0xFFFFFFFFu, order_key(near_top))) << 32);
+        if (lane == 0) sh.warp_top[warp] = w;
+        __syncthreads();
+        float mx = w;
+        for (int i = 0; i < kW; ++i) mx = fmaxf(mx, sh.warp_top[i]);
+        row.inf = mx == INFINITY;
+        row.mx = row.inf ? 0.0f : mx;
+    } else {
         float m = best;
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
@@ -404,8 +435,9 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
     }
     if (!(t > 0.0f)) {  // the lowest index of the largest
         u64 first = 0;
+        const float raw_mx = row.inf ? INFINITY : row.mx;
 #pragma unroll 1
-        for (int i = 4 * tid; i < n8; i += 4 * kT) {
+        for (int i = sh.top[me] == raw_mx ? 4 * tid : n8; i < n8; i += 4 * kT) {  // (most parts do not hold it)
             float v[4];
             row.raw4(i, v);
 #pragma unroll
@@ -618,21 +650,21 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
         return true;
     };
 
-    if (CUTS && by_k && top_k <= kCap / 2) {
-        // ---- at least top_k tokens are among the threads' own maxima
-        const float d = row.arg(row.clean(best));
-        if (d > -kSpan) atomicAdd(&cut.lo[linear_bin(d)], 1u);
-        add_up();
-        if (me == 0) {
-            find<kBins>(sh, mass, 0ull, u64(top_k));
-            Level l{0ull, ~0ull, -1, sh.bin, 0.0f, 0.0f};
-            // all logits down to the bin's end (fewer maxima than top_k have a weight:
-            // everything that has one)
-            l.x0 = sh.bin < 0 ? -kSpan : fmaxf(-kSpan, -(float(sh.bin) + 0.6f) / slope);
-            tell(l);
+    if (quick) {
+        // ---- at least top_k tokens are among the maxima: the top_k-th of them bounds the
+        // row's from below, to 22 / 2^14 of the exponent
+        const float d = row.arg(row.clean(near_top));
+        float end = -kSpan, above = 0.0f;  // (fewer of them than top_k have a weight: everything that has one)
+        if (__syncthreads_count(d > -kSpan) >= top_k) {
+#pragma unroll 1
+            for (int i = 0; i < 14; ++i) {
+                const float mid = 0.5f * (end + above);
+                if (__syncthreads_count(d >= mid) >= top_k)
+                    end = mid;
+                else
+                    above = mid;
+            }
         }
-        cl.sync();
-        const float end = sh.level.x0;
         const float x0 = row.inf ? 0.0f : row.mx + end * unit * 1.000001f - 1e-6f * fabsf(row.mx);
         between(x0, INFINITY, [&](int i, float v) {
             v = row.clean(v);
@@ -661,8 +693,6 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
                 }
                 kept = listed(n, floor_w);
             }
-        } else {
-            clear();
         }
     }
     const bool counted = CUTS && by_k && !done;
