@@ -639,7 +639,7 @@ int w12_sample(const void *logits_dev, int dtype, int64_t R, int64_t T, int64_t 
  * target's verification makes up for them), and the verification of sampled
  * drafts.  The SpecPilot pages describe none of them; they are this
  * library's own.  They use programmatic dependent launch as the decode-step
- * calls do.
+ * calls do (packing, encoding and decoding do not).
  */
 
 /* Largest row of w12_add_norm. */
@@ -737,7 +737,8 @@ size_t w12_fp4_gemm_workspace_size(const w12_fp4 *w, int count, int64_t M);
  *     written by the kernel launched just before).
  * code times the group's scale is exact in the products' type; sums are fp32,
  * in an order fixed by the shapes, M and the GPU's SM count, so repeated
- * calls give identical bits.
+ * calls give identical bits (from 17 tokens on the tensor core's own sums, whose
+ * additions are cut, not rounded).
  * Errors: W12_ERR_ARG, W12_ERR_SHAPE, W12_ERR_ALIGN, W12_ERR_WORKSPACE,
  * W12_ERR_CUDA.  Device errors in word 0 of ws: W12_ERR_TIMEOUT.
  */
@@ -794,7 +795,7 @@ size_t w12_verify_sampled_workspace_size(int64_t R, int64_t T, int64_t V);
  * R >= 1, T >= 1, R * T < 2^26, 1 <= V <= W12_SAMPLE_MAX_V.  Sums are whole
  * numbers: repeated calls give identical results.
  * Errors: W12_ERR_ARG, W12_ERR_SHAPE, W12_ERR_ALIGN, W12_ERR_WORKSPACE,
- * W12_ERR_CUDA.
+ * W12_ERR_CUDA.  Device errors in word 0 of ws: W12_ERR_TIMEOUT.
  */
 int w12_verify_sampled(const void *logits_dev, int dtype, const void *draft_logits_dev, int draft_dtype, int64_t R,
                        int64_t T, int64_t V, const int32_t *draft_dev, const w12_cut *target_cut,

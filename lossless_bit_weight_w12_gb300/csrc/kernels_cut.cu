@@ -1,26 +1,38 @@
 // kernels_cut.cu -- what temperature, top-k, top-p and min-p leave of rows of
-// logits: each row's largest logit, the threshold of the tokens that stay and
-// their whole weight (RowCut), by w12_sample's rules and with its whole-number
-// weights (sample_device.cuh).  Nothing is drawn: the sampled verification needs
-// single tokens' probabilities from most rows, and a draw from one per request.
+// logits: each row's largest logit, the lowest logit and index that stay, their whole
+// weight and the drafted token's share of it (RowCut), by w12_sample's rules and with
+// its whole-number weights (sample_device.cuh).  Nothing is drawn: the sampled
+// verification needs single tokens' probabilities from most rows, and a draw from one
+// per request.
 //
-// A row is read once: a cluster of CTAs (8 for 151936 logits) holds it in shared
-// memory, brought there by bulk copies.  The passes over it:
+// A row is read once: a cluster of CTAs holds it in shared memory, brought there by
+// bulk copies.  The passes over it:
 //  - the largest logit, as the pieces land;
-//  - top-k (up to kCap / 2): the k-th largest of the threads' own maxima bounds the
-//    k-th largest logit from below; what is not below it, little more than k
-//    tokens, is gathered in the first CTA, which ranks it and cuts it by top-p, too:
-//    no exponential of the others is needed;
+//  - top-k (up to kCap / 2): with the largest logit the CTAs exchange the largest of
+//    their warps' lanes' maxima, kT numbers a row; the k-th largest of these, found by
+//    bisection, bounds the k-th largest logit from below.  What is not below it, little
+//    more than k tokens, is gathered in the first CTA, which ranks it and cuts it by
+//    top-p, too: no exponential of the others is needed;
 //  - else the weights' sum, and for top-p a histogram of them: exact masses in 2048
 //    bins, linear in (max - x) / t, over the tokens that can hold the boundary (one
 //    lighter than (1 - top_p) 2^31 / V cannot: all such together weigh less than the
 //    nucleus leaves out);
 //  - the boundary: the first CTA finds the bin that holds it, its tokens are
-//    gathered there and ranked.  Where they are more than fit (many equal logits),
-//    histograms over their composites come first.  Larger top-k: the same with
-//    counts before the sum.
+//    gathered there and ranked, the other CTAs leave.  Where they are more than fit
+//    (many equal logits), histograms over their composites come first.  Larger top-k:
+//    the same with counts before the sum.
 // What stays weighs what lies above the bin and what stays of its tokens, so no
 // further pass over the row follows.
+//
+// What bounds it (rows of 151936): instructions and what waits between the cluster's
+// barriers.  Without cuts 29 instructions a token (an exact exponential, its rounding, a
+// 64-bit sum), 60 % of the issue slots: 240 fp32 rows 54 us, 21 for the bytes.  Top-p
+// 59 a token, 55 %: 248 bf16 rows 120 us, of a CTA's 54 kcycles 19 for the sum and the
+// bins (11 of them the two atomic additions a token), 8 for the gather, 6 for the
+// ranking, the rest at barriers and in code that it has not met.  160 fp32 rows with
+// top-k and 128 greedy ones 76 us.
+// As few CTAs a row as hold it: with cuts in clusters of 16 instead of 4 or 8 top-p
+// takes 164 us instead of 126, top-k 186 instead of 107.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -857,7 +869,9 @@ int launch_cut(CutArgs &a, void *stream) {
     const size_t over = kSmallBytes + (a.cuts ? kCutBytes : 0);
     const int64_t rows = a.side[0].rows + a.side[1].rows;
     // As few CTAs a row as five (with cuts: two, of twice the threads) fit on an SM, so
-    // that some of them compute while others load or wait; more where there are few rows.
+    // that some of them compute while others load or wait (without cuts, 240 rows of
+    // 151936 fp32 logits: 70 us in all; two an SM of 256 threads 77, of 512 threads 75,
+    // four of 384 80); more where there are few rows.
     const size_t most = (a.cuts ? 113 : 45) * 1024;
     const auto chunk = [&](int cs) { return ((a.V + cs - 1) / cs + 7) / 8 * 8; };
     int cs = 1;

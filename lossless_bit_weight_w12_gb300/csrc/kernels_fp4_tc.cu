@@ -19,7 +19,12 @@
 //    piece's place for the fix-up.
 // What bounds it: at 128 tokens the UMMAs (64 cycles each, 1024 a unit) and the
 // expansion (some 2900 warp-instructions a unit) beside one another, where the
-// weight stream would take 815; at fewer tokens the expansion alone.
+// weight stream would take 815; at fewer tokens the expansion alone.  5120 x 34816 at
+// 32 / 64 / 128 tokens: 31.5 / 32.8 / 36.5 us (14.8 for the bytes, 23.5 for 128 tokens'
+// products at the rate of a large matrix product); tensor pipe 47 %, issue 51 %.
+// The sums of a piece stay in tensor memory from its first unit to its last.  Its
+// additions are cut, not rounded: measured against 64 bits y is off by 2e-6 of its
+// norm at K = 5120 and 8e-6 at 17408, where a rounding to bf16 is up to 4e-3.
 //
 // Every wait is bounded; after a timeout every role runs to its end without waiting,
 // the producers let their copies land, and the issuers wait for their UMMAs before

@@ -6,7 +6,10 @@
 // A CTA takes a row at a time, in registers: every tensor is read or written once.
 // It asks for its next row before it reduces the one it has, so that the memory is
 // busy under the reductions; the weights stay in registers from row to row.  What
-// bounds it: from some hundred rows on the memory, below that the launch.
+// bounds it: from some hundred rows on the memory (8187 rows of 5120, bf16 with delta
+// and residual: 335 MB in 53 us, 94 % of the copy rate; asked for after the reductions
+// 62), below that the launch (one row 7.4 us with the host's call).  3001 odd rows of
+// 2883 fp32 elements go one element at a time: 23 us, 71 % of the copy rate.
 //
 // The e4m3 scale needs the largest |y|; as r is one positive number for the
 // row and a rounded product does not decrease with its factor, it is the

@@ -1,6 +1,6 @@
 // sample_device.cuh -- a row of logits as whole-number weights, shared by the
 // sampling kernel (kernels_sample.cu) and the sampled verification
-// (kernels_accept.cu).
+// (kernels_cut.cu, kernels_accept.cu).
 #pragma once
 
 #include <cstdint>
