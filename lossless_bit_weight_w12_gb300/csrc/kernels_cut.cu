@@ -776,7 +776,7 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
                         const float v = row.clean(DT == W12_F32 ? reinterpret_cast<const float *>(buf)[i]
                                                                 : bf16_bits_to_float(reinterpret_cast<const uint16_t *>(buf)[i]));
                         const uint32_t w = row.weight(v);
-                        if (row.comp(v, i) < from) continue;
+                        if (counted && row.comp(v, i) < from) continue;
                         total += w;
                         if (w >= floor_w) heavy += w;
                         if (CUTS && by_p && w >= light) {

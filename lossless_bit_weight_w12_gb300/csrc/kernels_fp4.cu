@@ -16,8 +16,8 @@
 // (fp4_device.cuh).  The tensor core's own sums run over one unit only; they are
 // added up in fp32 by the lanes, so their truncation does not pile up.
 //
-// What bounds it: the instructions of the expansion (3.1 a weight pair with the scale;
-// 67 % of the issue slots) beside the stream, and some 8 us that a call needs whatever
+// What bounds it: the instructions of the expansion (some 15 for 8 weights with the
+// scale; 67 % of the issue slots) beside the stream, and some 8 us that a call needs whatever
 // its size: the first units 1 to 3 us after the start, CTAs that end 3 us apart, the
 // fix-up 3.  A layer of 341 M weights (192 MB) at one token 40.5 us, 28.2 for the
 // bytes, 33.6 without the expansion, 31.6 without the products besides; 17408 x 5120
