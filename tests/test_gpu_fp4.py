@@ -230,3 +230,23 @@ def test_refusals(dev, w12mod):
         with pytest.raises(w12mod.W12Error):
             bad()
     assert w12mod.fp4_gemm_workspace_size([w], 0) == w12mod.fp4_gemm_workspace_size([w], 129) == 0
+
+
+@pytest.mark.parametrize("M,e4m3", [(3, True), (17, True), (33, False), (65, True), (128, True)])
+def test_eight_matrices(dev, w12mod, M, e4m3):
+    """As many matrices as a call takes, some on the same tokens, of one column to several tiles."""
+    import torch
+    rng = np.random.default_rng(M + 900)
+    shapes = [(128, 1), (128, 513), (256, 256), (256, 31), (1280, 700), (128, 512), (256, 300), (1280, 9)]
+    tokens = {K: _x(dev, rng, M, K, e4m3) for K in (128, 256, 1280)}
+    pairs = [_weight(w12mod, dev, rng, K, N, 0.02) for K, N in shapes]
+    xs = [tokens[K] for K, _ in shapes]
+    ws = w12mod.workspace(w12mod.fp4_gemm_workspace_size([w for w, _ in pairs], M), dev)
+    for options in (0, w12mod.OPT_EARLY_WEIGHTS):
+        ys = [torch.full((M, N), 5.0, device=dev) for _, N in shapes]
+        call = w12mod.FP4Batch([w for w, _ in pairs], [x for x, _, _ in xs], ys, ws, [s for _, s, _ in xs] if e4m3 else None, options)
+        call()
+        call()
+        for y, (_, w64), (_, _, x64), shape in zip(ys, pairs, xs, shapes):
+            _check(y, x64, w64, False, (M, shape))
+    assert w12mod.get_device_error(ws) == w12mod.OK

@@ -158,3 +158,21 @@ def test_refusals(dev, w12mod):
         with pytest.raises(w12mod.W12Error):
             bad()
     w12mod.add_norm(x[:0], w, out[:0])
+
+
+@pytest.mark.parametrize("n,dim", [(5000, 40), (1200, 2883), (700, 5120)])
+def test_more_rows_than_ctas_in_place(dev, w12mod, n, dim):
+    """A CTA's rows are asked for ahead of the writes of the rows before: in place of x, and of delta."""
+    import torch
+    rng = np.random.default_rng(dim)
+    x = torch.from_numpy(rng.standard_normal((n, dim)).astype(np.float32)).to(dev, torch.bfloat16)
+    d = torch.from_numpy(rng.standard_normal((n, dim)).astype(np.float32)).to(dev, torch.bfloat16)
+    h, y = dh.add_norm(dh.bits_f64(x), dh.bits_f64(d), None, 0.0, 1e-6)
+    for place in (0, 1):
+        a, b = x.clone(), d.clone()
+        out = torch.empty(n, dim, dtype=torch.bfloat16, device=dev)
+        w12mod.add_norm(a, None, out, delta=b, residual_out=(a, b)[place])
+        _check_out(torch, out, None, y, place)
+        err = np.abs(dh.bits_f64((a, b)[place]) - h)
+        assert np.all(err <= np.abs(h) * (2.0 ** -8 + 2.0 ** -24))
+        assert torch.equal((b, a)[place], (d, x)[place])

@@ -318,7 +318,7 @@ def test_equal_logits_under_cuts(dev, w12mod, V, cut):
 
 @pytest.mark.parametrize("cut", [dict(top_p=0.9), dict(top_k=50), dict(top_k=1000, top_p=0.9), dict(min_p=0.25), dict(top_k=50, top_p=0.6, min_p=0.1)],
                          ids=lambda c: "_".join(c))
-@pytest.mark.parametrize("row", ["large", "hot", "cold", "tiny", "inf", "nan", "zeros", "steps", "two"])
+@pytest.mark.parametrize("row", ["large", "hot", "flat", "cold", "tiny", "inf", "nan", "zeros", "steps", "two"])
 def test_unusual_rows_under_cuts(dev, w12mod, row, cut):
     """Rows and temperatures at the ends of what there is: the same tokens as w12_sample."""
     rng = np.random.default_rng(7)
@@ -329,6 +329,9 @@ def test_unusual_rows_under_cuts(dev, w12mod, row, cut):
         x, t = x * np.float32(8e37), 3e37
     elif row == "hot":
         t = 1e30
+    elif row == "flat":
+        t = np.inf
+        x[rng.integers(0, V, 900)] = -np.inf
     elif row == "cold":
         t = 1e-30
     elif row == "tiny":  # 1 / t is past the largest float
@@ -371,3 +374,73 @@ def test_greedy_rows(dev, w12mod, t, qt):
     half = t > 0 and qt == 0  # request 1: half of the target's against all of the drafter's, and u q < p fails by equality
     assert ratio[:, 0].tolist() == [0.0, 0.5 if half else 1.0, 1.0, 1.0]
     assert acc.tolist() == [0, 0 if half else 1, 1, 1] and nxt.tolist() == [3, 4999 if half else 11, 11, 11]
+
+
+@pytest.mark.parametrize("R,T,V", [(700, 2, 33), (2, 300, 40), (1300, 1, 5), (9, 3, 1), (3, 2, 1027)])
+@pytest.mark.parametrize("bf16", [False, True], ids=["f32", "bf16"])
+def test_many_requests_and_long_blocks(dev, w12mod, R, T, V, bf16):
+    """More requests than CTAs, more drafts than threads, rows of a few tokens on odd boundaries."""
+    import torch
+    rng = np.random.default_rng(R + T + V)
+    dtype = torch.bfloat16 if bf16 else torch.float32
+    x = torch.from_numpy(rng.standard_normal((R * T, V)).astype(np.float32)).to(dev, dtype)
+    q = torch.from_numpy(rng.standard_normal((R * (T - 1), V)).astype(np.float32)).to(dev, dtype)
+    draft = rng.integers(0, V, (R, T - 1))
+    row = lambda z, n: [_dist(v, 1.0, 0, 1.0, 0.0) for v in z.float().cpu().numpy().reshape(n, V)]  # noqa: E731
+    p, d = row(x, R * T), row(q, R * (T - 1))
+    u = rng.random((R, T)).astype(np.float32)
+    want, tol = np.zeros((R, T - 1)), np.zeros((R, T - 1))
+    for r in range(R):
+        stop = int(rng.integers(0, T))
+        for i in range(T - 1):
+            (pp, Wp, ep, _, _), (dd, Wd, eq, _, _) = p[r * T + i], d[r * (T - 1) + i]
+            a, b = pp[draft[r, i]], dd[draft[r, i]]
+            want[r, i] = ratio = min(1.0, a / b)
+            tol[r, i] = ratio * (2 * (ep + eq) + 2.0 ** -18 + 2.0 ** -32 / (a * Wp) + 2.0 ** -32 / (b * Wd))
+            u[r, i] = 0.5 * (1.0 + ratio) if i >= stop and ratio < 0.9 else 0.5 * ratio
+    acc, nxt, ratio = _call(w12mod, dev, x, q if T > 1 else None, R, T, draft, u)
+    assert np.all(np.abs(ratio - want) <= tol)
+    for r in range(R):
+        no = [i for i in range(T - 1) if u[r, i] > want[r, i]]
+        n = no[0] if no else T - 1
+        assert acc[r] == n
+        w, W, e, _, _ = p[r * T + n]
+        eps = 2 * e
+        if n < T - 1:
+            w = np.maximum(w - d[r * (T - 1) + n][0], 0.0)
+            eps = 2 * (e + d[r * (T - 1) + n][2]) + 2.0 ** -19 + V * 2.0 ** -45
+        cum = np.cumsum(w)
+        eps = (2 * eps + 2.0 ** -23) / cum[-1]  # (of the sum so far and of the whole; u to 2^-24)
+        at = np.float64(u[r, T - 1])
+        assert 0 <= nxt[r] < V and w[nxt[r]] > 0
+        assert (cum[nxt[r]] - w[nxt[r]]) / cum[-1] - eps <= at <= cum[nxt[r]] / cum[-1] + eps
+
+
+def test_graphs_on_one_workspace(dev, w12mod):
+    """Captured calls of other sizes on one workspace, replayed in turn, give what single calls give."""
+    import torch
+    g = torch.Generator(device=dev)
+    g.manual_seed(2)
+    sizes = [(2, 4, 5000), (40, 2, 301), (1, 6, 60001), (3, 1, 128)]
+    ws = w12mod.workspace(max(w12mod.verify_sampled_workspace_size(*s) for s in sizes), dev)
+    calls = []
+    for R, T, V in sizes:
+        x, q = torch.randn(R * T, V, generator=g, device=dev), torch.randn(R * (T - 1), V, generator=g, device=dev)
+        u, draft = torch.rand(R, T, generator=g, device=dev), torch.randint(0, V, (R, T - 1), generator=g, device=dev, dtype=torch.int32)
+        cut = w12mod.Cut(top_k=torch.full((R,), 20, dtype=torch.int32, device=dev), top_p=torch.full((R,), 0.9, device=dev))
+        out = [torch.full((R,), -7, dtype=torch.int32, device=dev) for _ in range(4)]
+        run = lambda a, n, w, x=x, q=q, R=R, T=T, draft=draft, u=u, cut=cut: w12mod.verify_sampled(  # noqa: E731
+            x, q if T > 1 else None, R, T, draft if T > 1 else None, u, a, n, w, cut, cut)
+        run(out[0], out[1], w12mod.workspace(w12mod.verify_sampled_workspace_size(R, T, V), dev))
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run(out[2], out[3], ws)
+        calls.append((graph, out, run))  # (run holds the tensors that the graph reads)
+    for _ in range(3):
+        for graph, out, _ in calls:
+            out[2].fill_(-8), out[3].fill_(-8)
+            graph.replay()
+        for _, out, _ in calls:
+            assert torch.equal(out[0], out[2]) and torch.equal(out[1], out[3])
+    assert w12mod.get_device_error(ws) == w12mod.OK
