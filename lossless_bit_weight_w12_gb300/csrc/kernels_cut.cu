@@ -30,9 +30,9 @@
 // 59 a token, 55 %: 248 bf16 rows 120 us, of a CTA's 54 kcycles 19 for the sum and the
 // bins (11 of them the two atomic additions a token), 8 for the gather, 6 for the
 // ranking, the rest at barriers and in code that it has not met.  160 fp32 rows with
-// top-k and 128 greedy ones 76 us.
+// top-k and 128 greedy ones 74 us.
 // As few CTAs a row as hold it: with cuts in clusters of 16 instead of 4 or 8 top-p
-// takes 164 us instead of 126, top-k 186 instead of 107.
+// takes 164 us instead of 126, top-k 186 instead of 107 (with the draw).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -73,6 +73,7 @@ struct Level {
 
 struct Small {
     uint64_t bar[kPieces];
+    uint64_t fin;                  // (first CTA) the CTAs' last words have come
     WaitCtl ctl;
     float top[kMostCluster];
     u64 sums[2][kMostCluster];     // (first CTA) weights, those from floor_w on
@@ -276,6 +277,19 @@ __device__ __noinline__ void resolve(Small &sh, CutMem &cut, uint32_t n, u64 fro
 }
 static_assert(2 * kFew <= kT, "two threads a token");
 
+// A CTA's last word to the first one: what this thread has written there before is
+// seen after all_in.  The CTA may leave then.
+__device__ __forceinline__ void hand_in(Small &sh) {
+    asm volatile(
+        "{\n .reg .b32 at;\n mapa.shared::cluster.u32 at, %0, 0;\n"
+        " mbarrier.arrive.release.cluster.shared::cluster.b64 _, [at];\n}\n" ::"r"(smem_addr(&sh.fin))
+        : "memory");
+}
+__device__ __forceinline__ void all_in(Small &sh, int *err) {
+    mbar_wait(&sh.fin, 0u, &sh.ctl, err);
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+}
+
 // CUTS: a top_k or top_p may be given.
 template <int DT, bool CUTS>
 __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a, const CutSide &s, int64_t r, unsigned char *smem) {
@@ -463,9 +477,10 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
         if (tid == 0) {
             for (int w = 1; w < kW; ++w) first = umax64(first, sh.warp_a[w]);
             cl.map_shared_rank(&sh, 0)->first[me] = first;
+            hand_in(sh);
         }
-        sync_sums();
         if (me == 0 && tid == 0) {
+            all_in(sh, a.err);
             for (int c = 0; c < cs; ++c) none = umax64(none, sh.first[c]);
             const int32_t one = int32_t(key_index(none));
             put(RowCut{row.mx, 1.0f, row.mx, 1.0f, one, one}, 1ull << 31);
@@ -786,11 +801,14 @@ __device__ __forceinline__ void cut_row(cg::cluster_group &cl, const CutArgs &a,
                     }
                 }
                 block_sum2<kW>(sh, total, heavy);
-                if (tid == 0) root->sums[0][me] = total, root->sums[1][me] = heavy;
+                if (tid == 0) {
+                    root->sums[0][me] = total, root->sums[1][me] = heavy;
+                    if (!CUTS || !by_p) hand_in(sh);
+                }
                 if (CUTS && by_p)
                     add_up();
-                else
-                    sync_sums();
+                else if (me == 0 && tid == 0)
+                    all_in(sh, a.err);
                 if (me == 0) {
                     kept = heavy = 0;
                     for (int c = 0; c < cs; ++c) kept += sh.sums[0][c], heavy += sh.sums[1][c];
@@ -819,6 +837,7 @@ __global__ void __launch_bounds__(CUTS ? kT : kPlainT, CUTS ? 2 : 5) cut_kernel(
     cluster_here();  // (its wait is behind the row's loads)
     if (threadIdx.x == 0) {
         for (int q = 0; q < kPieces; ++q) mbar_init(&sh.bar[q], 1);
+        mbar_init(&sh.fin, cs);
         sh.ctl.abort = 0;
         sh.ctl.limit_ns = kWaitLimitNs;
         sh.list_n = 0u;
@@ -869,14 +888,15 @@ int launch_cut(CutArgs &a, void *stream) {
     const size_t over = kSmallBytes + (a.cuts ? kCutBytes : 0);
     const int64_t rows = a.side[0].rows + a.side[1].rows;
     // As few CTAs a row as five (with cuts: two, of twice the threads) fit on an SM, so
-    // that some of them compute while others load or wait (without cuts, 240 rows of
-    // 151936 fp32 logits: 70 us in all; two an SM of 256 threads 77, of 512 threads 75,
-    // four of 384 80); more where there are few rows.
+    // that some of them compute while others load or wait; more where there are few rows.
+    // Without cuts, 240 rows of 151936 fp32 logits: 68 us in all with 14 a row, 70 with
+    // 16 (whole clusters fill the GPU's parts worse); two an SM of 256 threads 77, of
+    // 512 threads 75, four of 384 80.  (With cuts the CTAs share out powers of two.)
     const size_t most = (a.cuts ? 113 : 45) * 1024;
     const auto chunk = [&](int cs) { return ((a.V + cs - 1) / cs + 7) / 8 * 8; };
     int cs = 1;
-    while (cs < kMostCluster && over + size_t(chunk(cs)) * es > most) cs *= 2;
-    while (cs < kMostCluster && chunk(cs) > 2048 && rows * cs * 2 <= 304) cs *= 2;
+    while (cs < kMostCluster && over + size_t(chunk(cs)) * es > most) cs += a.cuts ? cs : 1;
+    while (cs < kMostCluster && chunk(cs) > 2048 && rows * cs * 2 <= 304) cs = cs * 2 < kMostCluster ? cs * 2 : kMostCluster;
     a.chunk = int32_t(chunk(cs));
     a.ahead = 304 / cs;
     static_assert(kSmallBytes + kCutBytes + (W12_SAMPLE_MAX_V / kMostCluster) * 4 <= kMostShared, "the largest row");
