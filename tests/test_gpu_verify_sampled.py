@@ -444,3 +444,25 @@ def test_graphs_on_one_workspace(dev, w12mod):
         for _, out, _ in calls:
             assert torch.equal(out[0], out[2]) and torch.equal(out[1], out[3])
     assert w12mod.get_device_error(ws) == w12mod.OK
+
+
+@pytest.mark.parametrize("V", [11000 * n for n in range(1, 17)] + [300001, 524288])
+def test_rows_over_more_and_more_ctas(dev, w12mod, V):
+    """Rows of every length that changes how many CTAs share them: the tokens that w12_sample draws."""
+    import torch
+    R = 40 if V > 176000 else 160
+    g = torch.Generator(device=dev)
+    g.manual_seed(V)
+    x = 3.0 * torch.randn(R, V, generator=g, device=dev)
+    u, tokens = torch.rand(R, generator=g, device=dev), torch.empty(R, dtype=torch.int32, device=dev)
+    t = torch.where(torch.arange(R, device=dev) % 5 == 4, 0.0, 0.9).float()
+    k = (torch.arange(R, device=dev) % 3 * 30).int()
+    p = torch.where(torch.arange(R, device=dev) % 2 == 1, 0.9, 1.0).float()
+    ws = w12mod.workspace(max(w12mod.sample_workspace_size(R, 1, V), w12mod.verify_sampled_workspace_size(R, 1, V)), dev)
+    acc, nxt = (torch.full((R,), -5, dtype=torch.int32, device=dev) for _ in range(2))
+    for cut in (dict(temperature=t), dict(temperature=t, top_k=k, top_p=p)):
+        w12mod.sample(x, R, 1, u, tokens, ws, cut["temperature"], cut.get("top_k"), cut.get("top_p"))
+        ws2 = w12mod.workspace(w12mod.verify_sampled_workspace_size(R, 1, V), dev)
+        w12mod.verify_sampled(x, None, R, 1, None, u.view(R, 1), acc, nxt, ws2, w12mod.Cut(**cut))
+        assert not bool(acc.any()) and torch.equal(nxt, tokens)
+        assert w12mod.get_device_error(ws2) == w12mod.OK
