@@ -19,10 +19,11 @@
 // What bounds it: the instructions of two exact exponentials a token (some 90 where
 // nothing is cut, so few requests are spread over all SMs; where tokens are cut, a
 // warp passes over fours without one that stays), and the steps that wait for one
-// another: 16 requests of 151936 tokens 18 us of 70, of which the sums 10, the end 5.
-// Loops are rolled on purpose: an SM that has not met a piece of code yet waits some
+// another: 16 requests of 151936 tokens 18 us of 65, of which the sums 9, the end 6.
+// Loops are short on purpose: an SM that has not met a piece of code yet waits some
 // 250 cycles per 128 bytes of it (sixteen tokens unrolled: 8 us of a single request's
-// 17), and both passes go through one loop for the same reason.
+// 17), and both passes go through one loop for the same reason.  Two tokens a turn: 16
+// x 8 rows 65 us in all; one 68, four 66.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -185,20 +186,22 @@ __global__ void __launch_bounds__(kAT, 4) accept_kernel(const __grid_constant__ 
             float4 y = d.q.floats(y0);
             y0 = y1, y1 = y2;
 #pragma unroll 1
-            for (; j < 4; ++j) {
-                const Weight w = cut_weight(pc, x.x, i + j);
-                u64 z = 0;
-                sum_own = add_wide(sum_own, w.whole);
-                if (refused) {
-                    z = above(__fmul_rn(w.f, pc.inv), __fmul_rn(cut_weight(qc, y.x, i + j).f, qc.inv));
-                    sum_rest += z;
+            for (; j < 4; j += 2, x.x = x.z, x.y = x.w, y.x = y.z, y.y = y.w) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const Weight w = cut_weight(pc, e ? x.y : x.x, i + j + e);
+                    u64 z = 0;
+                    sum_own = add_wide(sum_own, w.whole);
+                    if (refused) {
+                        z = above(__fmul_rn(w.f, pc.inv), __fmul_rn(cut_weight(qc, e ? y.y : y.x, i + j + e).f, qc.inv));
+                        sum_rest += z;
+                    }
+                    if (pass) {
+                        if (!rest) z = w.whole;
+                        s_each[4 * tid + j + e] = z;
+                        here += z;
+                    }
                 }
-                if (pass) {
-                    if (!rest) z = w.whole;
-                    s_each[4 * tid + j] = z;
-                    here += z;
-                }
-                x = make_float4(x.y, x.z, x.w, 0.0f), y = make_float4(y.y, y.z, y.w, 0.0f);
             }
             if (pass == 0) continue;
             u64 before;

@@ -889,9 +889,9 @@ int launch_cut(CutArgs &a, void *stream) {
     const int64_t rows = a.side[0].rows + a.side[1].rows;
     // As few CTAs a row as five (with cuts: two, of twice the threads) fit on an SM, so
     // that some of them compute while others load or wait; more where there are few rows.
-    // Without cuts, 240 rows of 151936 fp32 logits: 68 us in all with 14 a row, 70 with
-    // 16 (whole clusters fill the GPU's parts worse); two an SM of 256 threads 77, of
-    // 512 threads 75, four of 384 80.  (With cuts the CTAs share out powers of two.)
+    // Without cuts, 240 rows of 151936 fp32 logits: 68 us in all (the draw then took 3
+    // more) with 14 a row, 70 with 16 (whole clusters fill the GPU's parts worse); two an
+    // SM of 256 threads 77, of 512 threads 75, four of 384 80.  (With cuts the CTAs share out powers of two.)
     const size_t most = (a.cuts ? 113 : 45) * 1024;
     const auto chunk = [&](int cs) { return ((a.V + cs - 1) / cs + 7) / 8 * 8; };
     int cs = 1;
