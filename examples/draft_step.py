@@ -89,8 +89,8 @@ class Speculator:
         self.ratio = torch.empty(R, T - 1, device=dev)
         self.u = torch.empty(2, R, T, device=dev)  # for the drafts, for the verification
         full = lambda v: torch.full((R,), v, device=dev)  # noqa: E731
-        self.cut = w12.Cut(temperature=full(temperature), top_p=full(top_p))
-        self.temperature, self.top_p = self.cut._keep
+        self.temperature, self.top_p = full(temperature), full(top_p)
+        self.cut = w12.Cut(temperature=self.temperature, top_p=self.top_p)
         self.ws = [w12.workspace(w12.sample_workspace_size(R, 1, VOCAB), dev),
                    w12.workspace(w12.verify_sampled_workspace_size(R, T, VOCAB), dev)]
         self.rng = torch.Generator(device=dev)
