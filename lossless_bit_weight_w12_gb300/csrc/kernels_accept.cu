@@ -16,8 +16,8 @@
 // the last CTA to finish finds the run that holds the drawn token and goes through
 // that again.
 //
-// What bounds it: the instructions of two exact exponentials a token (some 90 where
-// nothing is cut, so few requests are spread over all SMs; where tokens are cut, a
+// What bounds it: the instructions of two exact exponentials a token (some 115 in all
+// where nothing is cut, so few requests are spread over all SMs; where tokens are cut, a
 // warp passes over fours without one that stays), and the steps that wait for one
 // another: 16 requests of 151936 tokens 18 us of 65, of which the sums 9, the end 6.
 // Loops are short on purpose: an SM that has not met a piece of code yet waits some

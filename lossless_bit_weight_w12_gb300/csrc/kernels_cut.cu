@@ -25,8 +25,8 @@
 // further pass over the row follows.
 //
 // What bounds it (rows of 151936): instructions and what waits between the cluster's
-// barriers.  Without cuts 29 instructions a token (an exact exponential, its rounding, a
-// 64-bit sum), 60 % of the issue slots: 240 fp32 rows 54 us, 21 for the bytes.  Top-p
+// barriers.  Without cuts 28 instructions a token (an exact exponential, its rounding, a
+// 64-bit sum), 62 % of the issue slots: 240 fp32 rows 52 us, 21 for the bytes.  Top-p
 // 59 a token, 55 %: 248 bf16 rows 120 us, of a CTA's 54 kcycles 19 for the sum and the
 // bins (11 of them the two atomic additions a token), 8 for the gather, 6 for the
 // ranking, the rest at barriers and in code that it has not met.  160 fp32 rows with
