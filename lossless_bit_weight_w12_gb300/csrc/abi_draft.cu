@@ -221,8 +221,8 @@ extern "C" int w12_fp4_gemm_batched(const w12_fp4 *w, const void *const *x, int 
     if (fp4_variant(M) < kFp4TcVariant) return launch_fp4(b, e4m3, p.grid, stream);
     if (e4m3)
         for (int i = 0; i < count; ++i) {
-            int again = 0;  // (products that share their tokens share the copy)
-            while (again < i && x[again] != x[i]) ++again;
+            int again = 0;  // (products that share their tokens, in rows of one length, share the copy)
+            while (again < i && (x[again] != x[i] || w[again].K != w[i].K)) ++again;
             b.g[i].x = at + p.x[again];
             if (again < i) continue;
             const int done = launch_fp4_widen(x[i], at + p.x[i], M * w[i].K, stream);
