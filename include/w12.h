@@ -663,8 +663,11 @@ int w12_sample(const void *logits_dev, int dtype, int64_t R, int64_t T, int64_t 
  *     dim apart.
  * Pointers are aligned to their elements; rows that start on 16-byte
  * boundaries with dim a multiple of 8 are read faster.  Other than named,
- * outputs overlap nothing.  Sums are fp32, in a fixed order; |h (weight +
- * offset)| is to stay below 3.4e38 for a row to be finite.
+ * outputs overlap nothing.  Sums are fp32, in a fixed order, of the row scaled
+ * by a power of two where its squares would pass fp32's ends; |h (weight +
+ * offset)| is to stay below 3.4e38 for a row to be finite, and |weight + offset|
+ * below 2^120 where the mean of h^2 is below 2^-100.  A row of zeros with eps 0
+ * gives zeros.
  * 1 <= dim <= W12_NORM_MAX_DIM, 0 <= rows < 2^31, eps >= 0 and finite.
  * Errors: W12_ERR_ARG, W12_ERR_SHAPE, W12_ERR_ALIGN, W12_ERR_CUDA.
  */

@@ -19,6 +19,10 @@
 //
 // The sum of squares is fp32.  Where it overflows, the row is scaled by 2^-80
 // in its registers and reduced once more (eps is below every rounding there).
+// Where it is so small that squares underflow and eps does not outweigh them, the
+// row is scaled by 2^50, up to three times (a row of fp32's smallest numbers ends
+// at 2^1); powers of two round nothing, and at 2^0 the largest scaled row leaves
+// the weights 2^120.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -33,6 +37,8 @@ namespace {
 
 constexpr float kE4m3Max = 448.0f;
 constexpr float kTinyRow = 1e-30f;
+constexpr float kTinySquare = 0x1p-100f;  // mean squares below it: the squares' own roundings (2^-150) count
+constexpr float kTinyEps = 0x1p-40f;      // from here on eps outweighs them
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -218,15 +224,20 @@ __global__ void __launch_bounds__(T, 1536 / T) norm_kernel(const __grid_constant
                     if (E4M3) top = max(top, __float_as_uint(h[q][j] * w[j]) & 0x7FFFFFFFu);
                 }
             }
-            reduce(sum, top, s_sum[buffer + pass], s_top[buffer + pass]);
-            if (pass == 1 || sum != INFINITY) break;
+            // (two buffers in turn: a barrier lies between a buffer's last read and its next write)
+            reduce(sum, top, s_sum[buffer + (pass & 1)], s_top[buffer + (pass & 1)]);
+            const bool large = pass == 0 && sum == INFINITY;
+            const bool small = pass < 3 && eps < kTinyEps && sum < kTinySquare * float(a.dim);
+            if (!large && !small) break;
+            const float by = large ? 0x1p-80f : 0x1p50f;
 #pragma unroll
             for (int q = 0; q < Q; ++q)
 #pragma unroll
-                for (int j = 0; j < W; ++j) h[q][j] *= 0x1p-80f;
-            eps = 0.0f;
+                for (int j = 0; j < W; ++j) h[q][j] *= by;
+            eps = large ? 0.0f : eps * by * by;
         }
-        const float rs = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(sum, float(a.dim)) + eps));
+        const float ms = __fdiv_rn(sum, float(a.dim)) + eps;
+        const float rs = ms == 0.0f ? 0.0f : __fdiv_rn(1.0f, __fsqrt_rn(ms));  // (0: a row of zeros, and eps 0)
         if constexpr (E4M3) {
             const float amax = __uint_as_float(top) * rs;
             const bool bad = !(amax <= 3.402823466e38f), some = amax > kTinyRow;
