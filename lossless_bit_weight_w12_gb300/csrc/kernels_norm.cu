@@ -17,8 +17,8 @@
 // reduction carries both the sum of squares and that maximum (as the bits of
 // |.|, which order like the numbers and put NaN above infinity).
 //
-// The sum of squares is fp32.  Where it overflows, the row is scaled by 2^-80
-// in its registers and reduced once more (eps is below every rounding there).
+// The sum of squares is fp32.  Where it (or with eps the mean) overflows, the row is
+// scaled by 2^-80 in its registers and reduced once more, with eps times 2^-160.
 // Where it is so small that squares underflow and eps does not outweigh them, the
 // row is scaled by 2^50, up to three times (a row of fp32's smallest numbers ends
 // at 2^1); powers of two round nothing, and at 2^0 the largest scaled row leaves
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(T, 1536 / T) norm_kernel(const __grid_constant
             }
             // (two buffers in turn: a barrier lies between a buffer's last read and its next write)
             reduce(sum, top, s_sum[buffer + (pass & 1)], s_top[buffer + (pass & 1)]);
-            const bool large = pass == 0 && sum == INFINITY;
+            const bool large = pass == 0 && (sum == INFINITY || (eps > 0x1p100f && sum > (0x1p127f - eps) * float(a.dim)));
             const bool small = pass < 3 && eps < kTinyEps && sum < kTinySquare * float(a.dim);
             if (!large && !small) break;
             const float by = large ? 0x1p-80f : 0x1p50f;
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(T, 1536 / T) norm_kernel(const __grid_constant
             for (int q = 0; q < Q; ++q)
 #pragma unroll
                 for (int j = 0; j < W; ++j) h[q][j] *= by;
-            eps = large ? 0.0f : eps * by * by;
+            eps = eps * by * by;
         }
         const float ms = __fdiv_rn(sum, float(a.dim)) + eps;
         const float rs = ms == 0.0f ? 0.0f : __fdiv_rn(1.0f, __fsqrt_rn(ms));  // (0: a row of zeros, and eps 0)
