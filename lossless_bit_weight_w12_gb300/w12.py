@@ -702,12 +702,16 @@ class FP4Weight:
 
     @staticmethod
     def encode(w, scale: float | None = None, stream=None) -> "FP4Weight":
-        """From bfloat16 weights [N, K]; scale: the largest |w| / 2688 by default."""
+        """From bfloat16 weights [N, K]; scale: the largest finite |w| / 2688 by
+        default (at least 2^-100, the smallest that is taken; 1 where no weight
+        is finite and not 0), read on the stream."""
         import torch
         N, K = w.shape
         if scale is None:
-            top = float(w.abs().max())
-            scale = top / 2688.0 if 0.0 < top < float("inf") else 1.0
+            with torch.cuda.stream(stream):
+                a = w.abs()
+                top = float(torch.where(a < float("inf"), a, 0.0).max())
+            scale = max(top / 2688.0, 2.0 ** -100) if top > 0.0 else 1.0
         blob = FP4Weight._blob(K, N, w.device)
         _check(lib().w12_fp4_encode(_typed_ptr(w, torch.bfloat16, N * K, "w"), K, N, scale, _ptr(blob), _stream_of(w, stream)),
                "w12_fp4_encode")
