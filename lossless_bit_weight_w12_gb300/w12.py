@@ -680,12 +680,14 @@ class FP4Weight:
         self.c = _CFP4(blob.data_ptr(), K, N, self.scale, 0)
 
     @staticmethod
-    def _blob(K: int, N: int, device):
+    def _blob(K: int, N: int, device, stream):
+        """A blob's memory, the stream's (where it is written)."""
         import torch
         n = int(lib().w12_fp4_bytes(K, N))
         if n == 0:
             raise W12Error(ERR_SHAPE, "w12_fp4_bytes")
-        t = torch.empty(n + 256, dtype=torch.uint8, device=device)
+        with torch.cuda.stream(stream):
+            t = torch.empty(n + 256, dtype=torch.uint8, device=device)
         off = (-t.data_ptr()) % 256
         return t[off:off + n]
 
@@ -694,7 +696,7 @@ class FP4Weight:
         """From codes uint8 [N, K / 2] and scales float8_e4m3fn [N, K / 16]."""
         import torch
         N, K = codes.shape[0], 2 * codes.shape[1]
-        blob = FP4Weight._blob(K, N, codes.device)
+        blob = FP4Weight._blob(K, N, codes.device, stream)
         _check(lib().w12_fp4_pack(_typed_ptr(codes, torch.uint8, N * K // 2, "codes"),
                                   _typed_ptr(scales, torch.float8_e4m3fn, N * K // 16, "scales"), K, N, _ptr(blob),
                                   _stream_of(codes, stream)), "w12_fp4_pack")
@@ -712,15 +714,16 @@ class FP4Weight:
                 a = w.abs()
                 top = float(torch.where(a < float("inf"), a, 0.0).max())
             scale = max(top / 2688.0, 2.0 ** -100) if top > 0.0 else 1.0
-        blob = FP4Weight._blob(K, N, w.device)
+        blob = FP4Weight._blob(K, N, w.device, stream)
         _check(lib().w12_fp4_encode(_typed_ptr(w, torch.bfloat16, N * K, "w"), K, N, scale, _ptr(blob), _stream_of(w, stream)),
                "w12_fp4_encode")
         return FP4Weight(blob, K, N, scale)
 
     def decode(self, stream=None):
-        """float32 [N, K]."""
+        """float32 [N, K], of the stream's memory."""
         import torch
-        out = torch.empty(self.N, self.K, dtype=torch.float32, device=self.blob.device)
+        with torch.cuda.stream(stream):
+            out = torch.empty(self.N, self.K, dtype=torch.float32, device=self.blob.device)
         _check(lib().w12_fp4_decode(ctypes.byref(self.c), _ptr(out), _stream_of(self.blob, stream)), "w12_fp4_decode")
         return out
 
