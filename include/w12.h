@@ -715,10 +715,12 @@ int w12_fp4_pack(const uint8_t *codes_dev, const uint8_t *scales_dev, int64_t K,
 
 /*
  * The blob of a bf16 matrix w_dev [N][K] (16-byte aligned) for a given scale
- * (usually the largest |w| / 2688, which uses the whole range): per 16 k the
- * e4m3 number nearest to max |w| / (6 scale), at least 2^-9 where a weight is not
- * 0, and the codes nearest to w / (that scale), ties to even.  Weights past the
- * range take the largest code; a NaN turns its 16 weights into NaN.
+ * (usually the largest |w| / 2688, which uses the whole range), in fp32: per 16 k
+ * s = the e4m3 number nearest to max |w| / (6 scale), at least 2^-9 where a weight
+ * is not 0, and the codes nearest to |w| (1 / (s scale)), ties to even (of the
+ * rounded product: where |w| lies within 2^-22 of the middle between two codes it
+ * may be either).  Weights past the range take the largest code; a NaN turns its
+ * 16 weights into NaN.
  * Errors: W12_ERR_ARG, W12_ERR_SHAPE, W12_ERR_ALIGN, W12_ERR_CUDA.
  */
 int w12_fp4_encode(const uint16_t *w_dev, int64_t K, int64_t N, float scale, void *blob_dev, void *stream);

@@ -355,7 +355,8 @@ __device__ __forceinline__ uint32_t e2m1_code(float a) {
     return (a > 0.25f) + (a >= 0.75f) + (a > 1.25f) + (a >= 1.75f) + (a > 2.5f) + (a >= 3.5f) + (a > 5.0f);
 }
 
-// The same from bf16 weights [N][K].
+// The same from bf16 weights [N][K].  A division per group, a product per weight: a
+// code's argument is off by three roundings.
 __global__ void __launch_bounds__(kPackThreads) encode_kernel(const uint16_t *w, int64_t KG, int64_t N, int64_t NP, float scale,
                                                               uint8_t *blob) {
     const int64_t i = int64_t(blockIdx.x) * kPackThreads + threadIdx.x;
