@@ -27,8 +27,8 @@
 // norm at K = 5120 and 8e-6 at 17408, where a rounding to bf16 is up to 4e-3.
 //
 // Every wait is bounded; after a timeout every role runs to its end without waiting,
-// the producers let their copies land, and the issuers wait for their UMMAs before
-// the tensor memory is freed.
+// the producers let their copies land, and the issuers wait for their UMMAs and for the
+// other warps' last use of the tensor memory before it is freed.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -69,6 +69,7 @@ struct Bars {
     uint64_t a_full[2][2], a_empty[2][2];  // [tile][buffer]: expanded (8 warps); read by the UMMAs
     uint64_t sum_full[2], sum_empty[2];    // a piece's sums; read (8 warps)
     uint64_t fin[2];
+    uint64_t out;                          // the warps that expand (16) have read their last sums
     uint32_t tmem;
     int last;
     WaitCtl ctl;
@@ -122,6 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_tc_kernel(const __grid_consta
             mbar_init(&bar.sum_empty[t], kDW / 2);
             mbar_init(&bar.fin[t], 1);
         }
+        mbar_init(&bar.out, kDW);
         bar.ctl.abort = 0;
         bar.ctl.limit_ns = kWaitLimitNs;
         mbar_fence_init();
@@ -211,10 +213,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_tc_kernel(const __grid_consta
                 ++piece;
                 s_next_tile(b, c);
             }
-            // every UMMA has completed, and the last sums have been read, before the memory is freed
+            // every UMMA has completed, and the other warps are done with the memory, before it is
+            // freed (also after a timeout, when they run on without waiting)
             umma_arrive(&bar.fin[t]);
             mbar_drain(&bar.fin[t], 0u, ctl->limit_ns);
-            if (piece > 0) mbar_wait(&bar.sum_empty[t], uint32_t(piece - 1) & 1u, ctl, b.err);
+            mbar_drain(&bar.out, 0u, ctl->limit_ns);
         }
         __syncwarp();
         // both issuers are done
@@ -320,7 +323,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_tc_kernel(const __grid_consta
         }
         tmem_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.sum_empty[t]);
+        if (lane == 0) {
+            mbar_arrive(&bar.sum_empty[t]);
+            if (u >= u1) mbar_arrive(&bar.out);
+        }
         if (!whole)
             fp4_fixup(b, g, first, nb, ub - ua, &bar.last, threadIdx.x, kDT);
         ++piece;
