@@ -51,8 +51,8 @@
 // Every mbarrier wait is bounded; after a timeout every role runs to its
 // end without waiting and the error word says W12_ERR_TIMEOUT.  The
 // producers stop issuing once the CTA has aborted and let their copies in
-// flight land, and each MMA thread waits (bounded) for its own UMMAs before
-// the tensor memory is freed.
+// flight land, and each MMA thread waits (bounded) for the UMMAs and for the
+// decoders' last use of the tensor memory before it is freed.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -303,6 +303,7 @@ __global__ void __launch_bounds__(kTT, 1) tc_kernel(const __grid_constant__ Stre
     uint32_t &s_tmem = *reinterpret_cast<uint32_t *>(a_full + 2 * SX + 3);
     WaitCtl &s_ctl = *reinterpret_cast<WaitCtl *>(a_full + 2 * SX + 4);
     int &s_last = *reinterpret_cast<int *>(a_full + 2 * SX + 6);
+    uint64_t &out = a_full[2 * SX + 7];  // the decoder warps have read their last sums
     unsigned long long *s_best = reinterpret_cast<unsigned long long *>(a_full + 2 * SX + 8);
     const uint32_t xbase = smem_addr(smem_dyn);  // token ring, then the weight ring
     const uint32_t wbase = xbase + uint32_t(C::kXRing);
@@ -323,6 +324,7 @@ __global__ void __launch_bounds__(kTT, 1) tc_kernel(const __grid_constant__ Stre
         mbar_init(&acc_full, 2);  // both issuers' commits after a piece's last unit
         mbar_init(&acc_empty, kDW);
         mbar_init(&fin, 2);
+        mbar_init(&out, kDW);
         wait_ctl_init(&s_ctl, b);
         mbar_fence_init();
     }
@@ -391,10 +393,11 @@ __global__ void __launch_bounds__(kTT, 1) tc_kernel(const __grid_constant__ Stre
                 ++piece;
                 s_next_tile(b, c);
             }
-            // every UMMA issued has completed before the memory is freed
+            // every UMMA issued has completed, and the decoders are done with the memory, before
+            // it is freed (also after a timeout, when they run on without waiting)
             umma_commit(&fin);
             mbar_drain(&fin, 0u, s_ctl.limit_ns);
-            if (piece > 0) mbar_wait(&acc_empty, uint32_t(piece - 1) & 1u, &s_ctl, b.err);
+            if (u0 < u1) mbar_drain(&out, 0u, s_ctl.limit_ns);
         }
         __syncwarp();
         if (warp == kMmaWarp) {
@@ -495,7 +498,10 @@ __global__ void __launch_bounds__(kTT, 1) tc_kernel(const __grid_constant__ Stre
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&acc_empty);
+        if (lane == 0) {
+            mbar_arrive(&acc_empty);
+            if (u >= u1) mbar_arrive(&out);
+        }
         if (ua == first && ub == first + g.KG) {
             if (valid && (!FUSED || g.y)) {
 #pragma unroll

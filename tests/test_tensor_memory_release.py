@@ -1,4 +1,5 @@
-"""When the tcgen05 product kernel gives its tensor memory back, on the CPU.
+"""When the tcgen05 product kernels (kernels_tc.cu, kernels_fp4_tc.cu) give their
+tensor memory back, on the CPU.
 
 After a wait that gave up every role runs to its end without waiting, so no wait
 that the abort flag cuts short can tell an issuer that the other warps are done:
@@ -6,7 +7,7 @@ a store to tensor memory that has been freed is an error of the whole context.
 The roles run as coroutines in random order -- producers reduced to their pace,
 warps that expand weights (they store A buffers and read sums), issuers -- and a
 random waiter gives up at a random time.  What an issuer waits for before it
-frees is read from the kernel's source.
+frees is read from the kernels' source.
 """
 import os
 import random
@@ -130,10 +131,10 @@ class Cta:
         assert self.freed
 
 
-@pytest.mark.parametrize("name", ["kernels_fp4_tc.cu"])
+@pytest.mark.parametrize("name", ["kernels_fp4_tc.cu", "kernels_tc.cu"])
 @pytest.mark.parametrize("give_up", [False, True], ids=["", "gives up"])
 def test_freed_after_the_last_use(name, give_up):
-    wait = last_wait(name, {"out", "sum_empty"})
+    wait = last_wait(name, {"out", "sum_empty", "acc_empty"})
     for seed in range(300):
         rnd = random.Random(seed)
         pieces = [rnd.choice([1, 2, 3, 8]) for _ in range(rnd.randint(1, 4))]
