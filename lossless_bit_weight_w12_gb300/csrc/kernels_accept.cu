@@ -42,7 +42,8 @@ static_assert(kAW == kAcceptRuns, "a run a warp");
 constexpr int kStep = 4 * kAT;  // tokens of a CTA at a time
 constexpr float kOne44 = 17592186044416.0f;
 
-// A row and what its cuts leave.
+// A row and what its cuts leave.  (The logits are read from L2, here as in the kernel
+// ahead: the read-only path is not for memory that was written after this kernel began.)
 struct Dist {
     const void *x;
     int f32, vec;
@@ -54,7 +55,7 @@ struct Dist {
         c = cuts[row];
     }
     __device__ __forceinline__ uint32_t bits(int i) const {
-        return f32 ? __float_as_uint(__ldg(static_cast<const float *>(x) + i)) : uint32_t(__ldg(static_cast<const uint16_t *>(x) + i));
+        return f32 ? __float_as_uint(__ldcg(static_cast<const float *>(x) + i)) : uint32_t(__ldcg(static_cast<const uint16_t *>(x) + i));
     }
     // Logits i .. i + 3 as they lie in memory (i a multiple of 4; from `end` on:
     // -infinity), so that nothing waits for them before they are used.
@@ -63,9 +64,9 @@ struct Dist {
         if (!f32) r.x = r.y = 0xFF80FF80u;
         if (i + 4 <= end && vec) {
             if (f32) {
-                r = __ldg(reinterpret_cast<const uint4 *>(static_cast<const float *>(x) + i));
+                r = __ldcg(reinterpret_cast<const uint4 *>(static_cast<const float *>(x) + i));
             } else {
-                const uint2 y = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(x) + i));
+                const uint2 y = __ldcg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(x) + i));
                 r.x = y.x, r.y = y.y;
             }
         } else if (i < end) {

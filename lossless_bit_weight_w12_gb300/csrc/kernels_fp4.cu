@@ -138,14 +138,15 @@ __global__ void __launch_bounds__(FCfg<NT>::kThreads, 2) fp4_kernel(const __grid
         constexpr int kPer = E4M3 ? 8 : 16, P = E4M3 ? C::kPer / 2 : C::kPer;  // 16-byte pieces: of a token's part, of a lane's
         uint4 v[C::kAhead][P];
         SCur ahead = s_at(b, u0);
-        const auto read = [&](uint4(&to)[P]) {  // unit `ahead`, then the next one
+        // unit `ahead`, then the next one (not by the read-only path: the kernel ahead writes x)
+        const auto read = [&](uint4(&to)[P]) {
             const Fp4One &g = b.g[ahead.gi];
             const uint8_t *x = static_cast<const uint8_t *>(g.x) + size_t(ahead.kg) * (E4M3 ? 128 : 256);
             const size_t row = size_t(g.K) * (E4M3 ? 1 : 2);
 #pragma unroll
             for (int q = 0; q < P; ++q) {
                 const int p = lane + 32 * q;
-                if (p < M * kPer) to[q] = ldg_v4(x + size_t(p / kPer) * row + 16 * (p % kPer));
+                if (p < M * kPer) to[q] = __ldcg(reinterpret_cast<const uint4 *>(x + size_t(p / kPer) * row + 16 * (p % kPer)));
             }
             s_next(b, ahead);
         };
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(FCfg<NT>::kThreads, 2) fp4_kernel(const __grid
                     const int m = 8 * j + 2 * t + (e & 1), r = ra + 16 * h + (e < 2 ? 0 : 8), n = nb * kFp4Tile + r;
                     if (m >= M) continue;
                     float v = acc[h][j][e] * (kFp4Back * g.scale);
-                    if (E4M3) v *= __ldg(g.x_scale + m);
+                    if (E4M3) v *= g.x_scale[m];
                     if (!whole)
                         P[m * kFp4Tile + r] = v;
                     else if (n < g.N)

@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_tc_kernel(const __grid_consta
             if (g.x_scale)
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                    if (q + e < left) v[e] *= __ldg(g.x_scale + m0 + q + e);
+                    if (q + e < left) v[e] *= g.x_scale[m0 + q + e];
             if (!whole) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
