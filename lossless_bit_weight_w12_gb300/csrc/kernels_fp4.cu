@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(FCfg<NT>::kThreads, 2) fp4_kernel(const __grid
     uint64_t *empty = full + S;
     WaitCtl &ctl = *reinterpret_cast<WaitCtl *>(empty + S);
     int &s_last = *reinterpret_cast<int *>(empty + S + 2);
+    volatile int &s_stored = *(reinterpret_cast<int *>(empty + S + 2) + 1);  // units whose tokens have come, once no more do, + 1
     const uint32_t base = smem_addr(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int M = b.M;
@@ -100,6 +101,7 @@ __global__ void __launch_bounds__(FCfg<NT>::kThreads, 2) fp4_kernel(const __grid
         }
         ctl.abort = 0;
         ctl.limit_ns = kWaitLimitNs;
+        s_stored = 0;
         mbar_fence_init();
     }
     // the rows past M stay zero
@@ -126,9 +128,15 @@ __global__ void __launch_bounds__(FCfg<NT>::kThreads, 2) fp4_kernel(const __grid
             bulk_copy(base + uint32_t(s) * C::kStage, g.units + (size_t(c.nb) * g.KG + c.kg) * kFp4Unit, kFp4Unit, &full[s], pol);
             s_next(b, c);
         }
-        // after a timeout: let the copies in flight land (bounded: the x warps may have stopped)
-        if (aborted(&ctl))
-            for (int k = issued > S ? issued - S : 0; k < issued; ++k) mbar_drain(&full[k % S], uint32_t(k / S) & 1u, ctl.limit_ns);
+        // after a timeout: let the copies in flight land, arriving for tokens that will not come
+        if (aborted(&ctl)) {
+            const uint64_t t0 = global_timer_ns();
+            while (!s_stored && global_timer_ns() - t0 < ctl.limit_ns) __nanosleep(1000);
+            const int from = issued > S ? issued - S : 0;
+            if (s_stored)
+                for (int k = max(from, s_stored - 1); k < issued; ++k) mbar_arrive(&full[k % S]);
+            for (int k = from; k < issued; ++k) mbar_drain(&full[k % S], uint32_t(k / S) & 1u, ctl.limit_ns);
+        }
         return;
     }
     pdl_wait();
@@ -153,12 +161,16 @@ __global__ void __launch_bounds__(FCfg<NT>::kThreads, 2) fp4_kernel(const __grid
 #pragma unroll
         for (int d = 0; d < C::kAhead; ++d)
             if (u0 + d < u1) read(v[d]);
-        for (int u = u0; u < u1; u += C::kAhead) {
+        // (a wait that gave up ends the stores: without waits a second arrival could meet a phase
+        // that only waits for its bytes)
+        int stored = 0;
+        for (int u = u0; u < u1 && stored == u - u0; u += C::kAhead) {
 #pragma unroll
             for (int d = 0; d < C::kAhead; ++d) {
                 if (u + d >= u1) break;
                 const int i = u + d - u0, s = i % S;
-                if (i >= S) mbar_wait(&empty[s], uint32_t(i / S - 1) & 1u, &ctl, b.err);
+                const bool stop = i >= S && (!mbar_wait(&empty[s], uint32_t(i / S - 1) & 1u, &ctl, b.err) || aborted(&ctl));
+                if (__any_sync(0xFFFFFFFFu, stop)) break;
                 const uint32_t st = base + uint32_t(s) * C::kStage + kFp4Unit;
 #pragma unroll
                 for (int q = 0; q < P; ++q) {
@@ -176,9 +188,11 @@ __global__ void __launch_bounds__(FCfg<NT>::kThreads, 2) fp4_kernel(const __grid
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&full[s]);
+                ++stored;
                 if (u + d + C::kAhead < u1) read(v[d]);
             }
         }
+        if (lane == 0) s_stored = stored + 1;
         return;
     }
 
