@@ -742,8 +742,9 @@ size_t w12_fp4_gemm_workspace_size(const w12_fp4 *w, int count, int64_t M);
  *     written by the kernel launched just before).
  * code times the group's scale is exact in the products' type; sums are fp32,
  * in an order fixed by the shapes, M and the GPU's SM count, so repeated
- * calls give identical bits (from 17 tokens on the tensor core's own sums, whose
- * additions are cut, not rounded).
+ * calls give identical bits.  From 17 tokens on they are the tensor core's own
+ * sums over up to 8192 k, whose additions are cut, not rounded: a sum of one
+ * sign comes out low by up to 7e-6 of itself, whatever K.
  * Errors: W12_ERR_ARG, W12_ERR_SHAPE, W12_ERR_ALIGN, W12_ERR_WORKSPACE,
  * W12_ERR_CUDA.  Device errors in word 0 of ws: W12_ERR_TIMEOUT.
  */

@@ -15,16 +15,20 @@
 //    64 k x MP tokens, 128-byte swizzle);
 //  - two warps issue, one per tile: 8 UMMAs a unit (M = 128, N = MP, K = 16) into the
 //    tile's sums, committed to the A buffer's and the token slot's barriers;
-//  - at the end of a tile's piece the group reads its sums and writes y, or the
-//    piece's place for the fix-up.
+//  - at the end of a part of a tile's piece the group adds its sums up, at the end of the
+//    piece it writes y, or the piece's place for the fix-up.
 // What bounds it: at 128 tokens the UMMAs (64 cycles each, 1024 a unit) and the
 // expansion (some 2900 warp-instructions a unit) beside one another, where the
 // weight stream would take 815; at fewer tokens the expansion alone.  5120 x 34816 at
 // 32 / 64 / 128 tokens: 31.5 / 32.8 / 36.5 us (14.8 for the bytes, 23.5 for 128 tokens'
 // products at the rate of a large matrix product); tensor pipe 47 %, issue 51 %.
-// The sums of a piece stay in tensor memory from its first unit to its last.  Its
-// additions are cut, not rounded: measured against 64 bits y is off by 2e-6 of its
-// norm at K = 5120 and 8e-6 at 17408, where a rounding to bf16 is up to 4e-3.
+// The tensor core cuts where it adds, so a sum of one sign drifts with its length.  After
+// kSpan units a part's sums are taken out of tensor memory and added up in fp32, in the
+// piece's place for the fix-up.  Sums of one sign, low by at most (of themselves): K = 5120
+// 4e-6, any longer K 7e-6 (kept in tensor memory throughout: 2.5e-5 at 17408, 5e-4 at
+// 131072, rising), where a rounding to bf16 is up to 4e-3; signs that differ: 2e-6 of y's
+// norm.  Spans of 32 / 16 units: 2e-6 / 6e-7, but a part's end lets the tensor core wait:
+// 5120 x 34816 at 32 / 128 tokens 33.8 / 42.5 and 35.3 / 47.3 us instead of 32.2 / 37.0.
 //
 // Every wait is bounded; after a timeout every role runs to its end without waiting,
 // the producers let their copies land, and the issuers wait for their UMMAs and for the
@@ -47,6 +51,7 @@ constexpr int kDT = kDW * 32;
 constexpr int kWeightWarp = kDW, kTokenWarp = kDW + 1, kIssueWarp = kDW + 2;  // two issuers
 constexpr int kThreads = (kDW + 4) * 32;
 constexpr uint32_t kTmemCols = 512;
+constexpr int kSpan = 64;  // units of a part (8192 k)
 
 template <int MP>
 struct TCfg {
@@ -97,6 +102,17 @@ __device__ __forceinline__ void tmem_landed16(uint32_t (&r)[16]) {
     for (int i = 0; i < 16; i += 8)
         asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]),
                      "+r"(r[i + 7]));
+}
+
+// *p += v, in L2 (no other thread's number: the order of a thread's additions is its own),
+// and the number back.
+__device__ __forceinline__ void add_to(float *p, float v) {
+    asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory");
+}
+__device__ __forceinline__ float load_back(const float *p) {
+    float v;
+    asm volatile("ld.relaxed.gpu.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+    return v;
 }
 
 template <int MP>
@@ -185,12 +201,12 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_tc_kernel(const __grid_consta
             const uint32_t idesc = umma_idesc(false, MP, false);
             const uint32_t sum = tmem + uint32_t(t * MP);
             SCur c = s_at(b, u0);
-            int i = 0, piece = 0;
-            for (int u = u0; u < u1;) {
+            int i = 0;
+            for (int u = u0, part = 0; u < u1; ++part) {
                 const Fp4One &g = b.g[c.gi];
-                const int ub = min(u1, g.ubase + (c.nb + 1) * g.KG);
-                // the sums of the piece before have been read
-                if (piece > 0) mbar_wait(&bar.sum_empty[t], uint32_t(piece - 1) & 1u, ctl, b.err);
+                const int end = min(u1, g.ubase + (c.nb + 1) * g.KG), ub = min(end, u + kSpan);
+                // the sums of the part before have been read
+                if (part > 0) mbar_wait(&bar.sum_empty[t], uint32_t(part - 1) & 1u, ctl, b.err);
                 tmem_fence_after();
                 for (bool fresh = true; u < ub; ++u, ++i) {
                     const int s = i % SX, a = i & 1;
@@ -210,8 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_tc_kernel(const __grid_consta
                     umma_arrive(&bar.empty_x[s]);
                 }
                 umma_arrive(&bar.sum_full[t]);
-                ++piece;
-                s_next_tile(b, c);
+                if (u == end) s_next_tile(b, c);
             }
             // every UMMA has completed, and the other warps are done with the memory, before it is
             // freed (also after a timeout, when they run on without waiting)
@@ -239,67 +254,101 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_tc_kernel(const __grid_consta
     const uint32_t ps = uint32_t(kFp4Scales + 8 * r + 4 * h);  // (chunks 2 h and 2 h + 1: k 16 j .. and 64 + 16 j ..)
     const int M = b.M;
     SCur c = s_at(b, u0);
-    int i = 0, piece = 0;
+    const int m0 = h * (MP / 2), left = min(M - m0, MP / 2);  // the tokens whose sums the warp reads
+    int i = 0, part = 0;
     for (int u = u0; u < u1;) {
         const Fp4One &g = b.g[c.gi];
         const int nb = c.nb, first = g.ubase + nb * g.KG;
         const int ua = u, ub = min(u1, first + g.KG), iend = i + ub - ua;
-        for (int iu = i + ((i & 1) != grp); iu < iend; iu += 2) {  // this group's units
-            const int s = iu % SW;
-            mbar_wait(&bar.full_w[s], uint32_t(iu / SW) & 1u, ctl, b.err);
-            const uint32_t st = wbase + uint32_t(s) * kFp4Unit;
+        // the piece's place for the fix-up; until its end, the sums of its parts so far
+        float *place = b.partial + (size_t(blockIdx.x) * 2 + (ua == u0 ? 0 : 1)) * size_t(M) * kFp4Tile + m0 * kFp4Tile + col;
+        bool fresh = true;
+        int iu = i + ((i & 1) != grp);  // this group's units
+#pragma unroll 1
+        for (int next = min(i + kSpan, iend);; next = min(next + kSpan, iend), fresh = false, ++part) {
+            for (; iu < next; iu += 2) {
+                const int s = iu % SW;
+                mbar_wait(&bar.full_w[s], uint32_t(iu / SW) & 1u, ctl, b.err);
+                const uint32_t st = wbase + uint32_t(s) * kFp4Unit;
 #pragma unroll
-            for (int tile = 0; tile < 2; ++tile) {
-                const uint4 c0 = lds128(st + p0 + uint32_t(tile * 128 * 64)), c1 = lds128(st + p1 + uint32_t(tile * 128 * 64));
-                const uint32_t f = lds32(st + ps + uint32_t(tile * 128 * 8));
-                if (tile == 1) {
+                for (int tile = 0; tile < 2; ++tile) {
+                    const uint4 c0 = lds128(st + p0 + uint32_t(tile * 128 * 64)), c1 = lds128(st + p1 + uint32_t(tile * 128 * 64));
+                    const uint32_t f = lds32(st + ps + uint32_t(tile * 128 * 8));
+                    if (tile == 1) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar.empty_w[s]);
+                    }
+                    uint32_t v[32];
+                    const uint32_t f0 = fp4_scale2(prmt2(f, 0u, 0x4040u)), f1 = fp4_scale2(prmt2(f, 0u, 0x4141u));
+                    const uint32_t f2 = fp4_scale2(prmt2(f, 0u, 0x4242u)), f3 = fp4_scale2(prmt2(f, 0u, 0x4343u));
+                    const auto expand = [&](uint32_t w, uint32_t scale, int at) {
+                        uint32_t(&to)[4] = *reinterpret_cast<uint32_t(*)[4]>(&v[at]);
+                        fp4_expand(w, scale, to);
+                    };
+                    // columns 16 h ..: k 32 h .. + 31; columns 32 + 16 h ..: k 64 + 32 h ..
+                    expand(c0.x, f0, 0), expand(c0.y, f0, 4), expand(c1.x, f2, 8), expand(c1.y, f2, 12);
+                    expand(c0.z, f1, 16), expand(c0.w, f1, 20), expand(c1.z, f3, 24), expand(c1.w, f3, 28);
+                    if (iu >= 2) mbar_wait(&bar.a_empty[tile][grp], uint32_t((iu >> 1) - 1) & 1u, ctl, b.err);
+                    tmem_fence_after();
+                    const uint32_t ta = tmem + lanes + C::kA + uint32_t(2 * tile + grp) * 64u + 16u * uint32_t(h);
+                    tmem_store16(ta, v);
+                    tmem_store16(ta + 32u, v + 16);
+                    tmem_wait_st();
+                    tmem_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.empty_w[s]);
+                    if (lane == 0) mbar_arrive(&bar.a_full[tile][grp]);
                 }
-                uint32_t v[32];
-                const uint32_t f0 = fp4_scale2(prmt2(f, 0u, 0x4040u)), f1 = fp4_scale2(prmt2(f, 0u, 0x4141u));
-                const uint32_t f2 = fp4_scale2(prmt2(f, 0u, 0x4242u)), f3 = fp4_scale2(prmt2(f, 0u, 0x4343u));
-                const auto expand = [&](uint32_t w, uint32_t scale, int at) {
-                    uint32_t(&to)[4] = *reinterpret_cast<uint32_t(*)[4]>(&v[at]);
-                    fp4_expand(w, scale, to);
-                };
-                // columns 16 h ..: k 32 h .. + 31; columns 32 + 16 h ..: k 64 + 32 h ..
-                expand(c0.x, f0, 0), expand(c0.y, f0, 4), expand(c1.x, f2, 8), expand(c1.y, f2, 12);
-                expand(c0.z, f1, 16), expand(c0.w, f1, 20), expand(c1.z, f3, 24), expand(c1.w, f3, 28);
-                if (iu >= 2) mbar_wait(&bar.a_empty[tile][grp], uint32_t((iu >> 1) - 1) & 1u, ctl, b.err);
-                tmem_fence_after();
-                const uint32_t ta = tmem + lanes + C::kA + uint32_t(2 * tile + grp) * 64u + 16u * uint32_t(h);
-                tmem_store16(ta, v);
-                tmem_store16(ta + 32u, v + 16);
-                tmem_wait_st();
-                tmem_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.a_full[tile][grp]);
             }
+            if (next == iend) break;
+            // ---- a part's sums, out of the way of the next one
+            mbar_wait(&bar.sum_full[t], uint32_t(part) & 1u, ctl, b.err);
+            tmem_fence_after();
+            float *to = place;
+#pragma unroll 1
+            for (int q = 0; q < left; q += 16, to += 16 * kFp4Tile) {
+                uint32_t z[16];
+                tmem_load16(tmem + lanes + uint32_t(t * MP + m0 + q), z);
+                tmem_wait_ld();
+                tmem_landed16(z);
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (q + e < left) {
+                        if (fresh)
+                            __stcg(to + e * kFp4Tile, __uint_as_float(z[e]));
+                        else
+                            add_to(to + e * kFp4Tile, __uint_as_float(z[e]));
+                    }
+            }
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.sum_empty[t]);
         }
         u = ub, i = iend;
         // ---- the piece's sums: row r, tokens h MP / 2 .. + MP / 2
-        mbar_wait(&bar.sum_full[t], uint32_t(piece) & 1u, ctl, b.err);
+        mbar_wait(&bar.sum_full[t], uint32_t(part) & 1u, ctl, b.err);
         tmem_fence_after();
         const bool whole = ua == first && ub == first + g.KG;
         const int n = nb * kFp4Tile + col;
-        float *P = b.partial + (size_t(blockIdx.x) * 2 + (ua == u0 ? 0 : 1)) * size_t(M) * kFp4Tile;
         // (rolled: a piece of code that runs once costs an SM 250 cycles per 128 bytes of it)
         const float back = kFp4Back * g.scale;
-        const int m0 = h * (MP / 2), left = min(M - m0, MP / 2);
-        float *part = P + m0 * kFp4Tile + col;
         const size_t at = size_t(m0) * g.N + n;
         float *yf = static_cast<float *>(g.y) + at;
         __nv_bfloat16 *yb = static_cast<__nv_bfloat16 *>(g.y) + at;
 #pragma unroll 1
-        for (int q = 0; q < left; q += 16) {
+        for (int q = 0; q < left; q += 16, place += 16 * kFp4Tile) {
             uint32_t z[16];
             tmem_load16(tmem + lanes + uint32_t(t * MP + m0 + q), z);
             tmem_wait_ld();
             tmem_landed16(z);
             float v[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(z[e]) * back;
+            for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(z[e]);
+            if (!fresh)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (q + e < left) v[e] += load_back(place + e * kFp4Tile);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] *= back;
             if (g.x_scale)
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
@@ -307,8 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_tc_kernel(const __grid_consta
             if (!whole) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                    if (q + e < left) part[e * kFp4Tile] = v[e];
-                part += 16 * kFp4Tile;
+                    if (q + e < left) place[e * kFp4Tile] = v[e];
             } else if (n < g.N) {
                 if (b.y_dtype == W12_F32) {
 #pragma unroll
@@ -329,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_tc_kernel(const __grid_consta
         }
         if (!whole)
             fp4_fixup(b, g, first, nb, ub - ua, &bar.last, threadIdx.x, kDT);
-        ++piece;
+        ++part;
         s_next_tile(b, c);
     }
 }
