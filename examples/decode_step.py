@@ -66,7 +66,7 @@ class Block:
         b["h"] = torch.empty(n, HIDDEN, dtype=torch.bfloat16, device=dev)
         b["ws"] = [w12.workspace(self.products_workspace("qkv", n), dev),
                    w12.workspace(w12.attend_workspace_size(kv, R, T, HEADS, max_len, prefix), dev),
-                   w12.workspace(max(self.products_workspace([m], n) for m in ("o", "lm_head")), dev)]
+                   *(w12.workspace(self.products_workspace([m], n), dev) for m in ("o", "lm_head"))]
         return b
 
     def products_workspace(self, names, n):
@@ -92,7 +92,7 @@ class Block:
         if not logits:
             return
         self.products(["o"], b["a"].view(n, HEADS * DIM), [b["o"]], b["ws"][2])
-        self.products(["lm_head"], self.norm(b, x, b["o"]), [b["logits"]], b["ws"][2])
+        self.products(["lm_head"], self.norm(b, x, b["o"]), [b["logits"]], b["ws"][3])
 
 
 class Server:
@@ -169,7 +169,7 @@ class Server:
         return acc.numpy(), nxt.numpy(), tokens.numpy().reshape(R, T)
 
     def check(self):
-        for ws in (self.b["ws"][0], self.b["ws"][1], self.b["ws"][2], self.ws):
+        for ws in (*self.b["ws"], self.ws):
             assert w12.get_device_error(ws) == w12.OK
 
 

@@ -38,7 +38,14 @@
  *  - Workspaces: a workspace of the size the matching *_workspace_size()
  *    call returns, 256-byte aligned, zero-filled by the caller before its
  *    first use.  Every kernel leaves its workspace counters at zero again, so
- *    a workspace is reused without clearing.  Word 0 of a workspace is a
+ *    the calls that a workspace belongs to reuse it without clearing:
+ *    w12_gemm, w12_gemm_ex, w12_gemm_batched and w12_gemm_batched_ex with the
+ *    same matrices (any M and path); w12_verify_greedy_lmhead with the same
+ *    matrix; w12_fp4_gemm and w12_fp4_gemm_batched; each other call by itself,
+ *    in any size that needs no more than it has.  Counters lie at different
+ *    places for different calls, and results on the way to the next kernel
+ *    stay where they are: a workspace that passes from one of these to another
+ *    has to be zero-filled in between.  Word 0 of a workspace is a
  *    sticky device error code (see w12_get_device_error).  Calls that share
  *    one workspace must be ordered (same stream, or events).
  */

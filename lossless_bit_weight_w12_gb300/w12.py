@@ -825,7 +825,9 @@ def verify_sampled(logits, draft_logits, R: int, T: int, draft, u, accept_dev, n
 # --------------------------------------------------------------- helpers
 
 def workspace(nbytes: int, device="cuda"):
-    """A zero-filled, 256-byte aligned device workspace of nbytes (torch uint8)."""
+    """A zero-filled, 256-byte aligned device workspace of nbytes (torch uint8).
+    It belongs to one call, or to one set of matrices of the gemm calls; only
+    calls of that kind share it (include/w12.h, conventions)."""
     import torch
     t = torch.zeros(max(int(nbytes), 256) + 256, dtype=torch.uint8, device=device)
     off = (-t.data_ptr()) % 256
