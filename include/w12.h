@@ -41,7 +41,7 @@
  *    the calls that a workspace belongs to reuse it without clearing:
  *    w12_gemm, w12_gemm_ex, w12_gemm_batched and w12_gemm_batched_ex with the
  *    same matrices (any M and path); w12_verify_greedy_lmhead with the same
- *    matrix; w12_fp4_gemm and w12_fp4_gemm_batched; each other call by itself,
+ *    matrix and R T; w12_fp4_gemm and w12_fp4_gemm_batched; each other call by itself,
  *    in any size that needs no more than it has.  Counters lie at different
  *    places for different calls, and results on the way to the next kernel
  *    stay where they are: a workspace that passes from one of these to another
