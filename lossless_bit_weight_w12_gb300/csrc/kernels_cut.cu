@@ -892,6 +892,7 @@ int launch_cut(CutArgs &a, void *stream) {
     // Without cuts, 240 rows of 151936 fp32 logits: 68 us in all (the draw then took 3
     // more) with 14 a row, 70 with 16 (whole clusters fill the GPU's parts worse); two an
     // SM of 256 threads 77, of 512 threads 75, four of 384 80.  (With cuts the CTAs share out powers of two.)
+    // (304: two CTAs on each of 152 SMs.)
     const size_t most = (a.cuts ? 113 : 45) * 1024;
     const auto chunk = [&](int cs) { return ((a.V + cs - 1) / cs + 7) / 8 * 8; };
     int cs = 1;

@@ -18,10 +18,12 @@
 //  - at the end of a part of a tile's piece the group adds its sums up, at the end of the
 //    piece it writes y, or the piece's place for the fix-up.
 // What bounds it: at 128 tokens the UMMAs (64 cycles each, 1024 a unit) and the
-// expansion (some 2900 warp-instructions a unit) beside one another, where the
-// weight stream would take 815; at fewer tokens the expansion alone.  5120 x 34816 at
-// 32 / 64 / 128 tokens: 31.5 / 32.8 / 36.5 us (14.8 for the bytes, 23.5 for 128 tokens'
-// products at the rate of a large matrix product); tensor pipe 47 %, issue 51 %.
+// expansion (some 2900 warp-instructions a unit, 725 cycles of the four schedulers)
+// beside one another, where the weight stream would take 815; tensor pipe 47 %, issue
+// 51 %.  At fewer tokens a unit takes some 1500 cycles, twice what the expansion issues:
+// its warps wait for one of two A buffers a tile.  5120 x 34816 at 32 / 64 / 128 tokens:
+// 32.2 / 32.9 / 37.0 us (14.8 for the bytes, 23.5 for 128 tokens' products at the rate of a
+// large matrix product).
 // The tensor core cuts where it adds, so a sum of one sign drifts with its length.  After
 // kSpan units a part's sums are taken out of tensor memory and added up in fp32, in the
 // piece's place for the fix-up.  Sums of one sign, low by at most (of themselves): K = 5120

@@ -7,9 +7,15 @@
 // It asks for its next row before it reduces the one it has, so that the memory is
 // busy under the reductions; the weights stay in registers from row to row.  What
 // bounds it: from some hundred rows on the memory (8187 rows of 5120, bf16 with delta
-// and residual: 335 MB in 53 us, 94 % of the copy rate; asked for after the reductions
-// 62), below that the launch (one row 7.4 us with the host's call).  3001 odd rows of
-// 2883 fp32 elements go one element at a time: 23 us, 71 % of the copy rate.
+// and residual: 335 MB in 53 us, 93 % of the copy rate; asked for after the reductions
+// 62), below that the launch (one row 7.4 us with the host's call).  Wider elements leave
+// fewer rows under way in 40 registers a thread, which nearly every form passes (-Xptxas
+// -v: bf16 4 bytes of spills, fp32 with fp32 delta to e4m3 some 130): 8187 x 5120 with
+// residual, fp32 and fp32 delta to bf16 96 us (86 for the bytes), to e4m3 114 (80), bf16
+// and fp32 delta to e4m3 81 (56).  Past 8192 elements a row has no next one under it and
+// the weights are read again: 4096 x 16384 bf16 111 us (79).  A call with any tensor off
+// 16-byte boundaries, or dim no multiple of 8, goes one element at a time throughout:
+// 3001 rows of 2883 fp32 elements 24 us, 70 % of the copy rate.
 //
 // The e4m3 scale needs the largest |y|; as r is one positive number for the
 // row and a rounded product does not decrease with its factor, it is the
